@@ -37,6 +37,7 @@ _lock = threading.Lock()
 # (name, restype, argtypes) for every entry point of include/fp8gemm.h
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 SIGNATURES = [
     ("fp8_quant_1x128", _I, [_P, _P, _P, _I, _I, _P]),
     ("fp8_quant_128x128", _I, [_P, _P, _P, _I, _I, _I, _P]),
@@ -57,6 +58,14 @@ SIGNATURES = [
     ("fp8gemm_grouped_contiguous", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     ("fp8gemm_grouped_masked", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     ("fp8gemm_dense_small_m_noalloc", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    ("fp8_rmsnorm_quant", _I,
+     [_P, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _I, _I, _I, _P]),
+    ("fp8_rmsnorm_backward", _I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _P]),
+    ("fp8_kv_append", _I,
+     [_P, _P, _L, _L, _P, _P, _P, _P, _P, _P, _P, *[_I] * 9, _P]),
+    ("fp8_kv_attention", _I,
+     [_P, _L, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, *[_I] * 10, _P]),
+    ("fp8_moe_few", _I, [*[_P] * 10, *[_I] * 6, _P]),
     ("fp8gemm_get_device_status", _I, [_P, ctypes.POINTER(ctypes.c_int)]),
     ("fp8gemm_strerror", ctypes.c_char_p, [_I]),
     ("fp8gemm_num_kernel_launches", ctypes.c_uint64, []),
@@ -567,6 +576,212 @@ def fp8gemm_dense_small_m_noalloc(A, sA, B, sB, D, stream=None):
         _ptr(A, "A"), _ptr(sA, "sA"), _ptr(B, "B"), _ptr(sB, "sB"), _ptr(D, "D"),
         M, N, K, _stream(stream)), "fp8gemm_dense_small_m_noalloc")
     return D
+
+
+def _type(t, name):
+    """FP8GEMM_TYPE_* of an activation tensor."""
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _like(t, name, X):
+    """A tensor of X's shape and type."""
+    if t.dtype != X.dtype:
+        raise TypeError(f"{name} must be {X.dtype} as the other activations, got {t.dtype}")
+    return _need(t, name, X.numel(), X.shape[-1])
+
+
+def _opt(t, name):
+    return None if t is None else _ptr(t, name)
+
+
+def fp8_rmsnorm_quant(X, gain, eps=1e-6, residual=None, fmt="e4m3", H=None, Q=None, sQ=None,
+                      rstd=None, stream=None):
+    """Residual addition, RMS norm and 1x128 FP8 output in one pass: X bf16 or
+    f32 [..., K], gain f32 [K] -> (Q u8 [..., K], sQ f32 [..., ceil(K/128)], H,
+    rstd f32 [...]).  H is X + residual in X's type (X itself without one);
+    H=residual updates the stream in place."""
+    torch = _torch()
+    kind = _type(X, "X")
+    K = X.shape[-1]
+    M = X.numel() // K if K else 0
+    _need(_f32(gain, "gain"), "gain", K)
+    if residual is not None:
+        _like(residual, "residual", X)
+        H = torch.empty_like(X) if H is None else _like(H, "H", X)
+    elif H is not None:
+        raise ValueError("H is the sum with the residual: give residual too")
+    if Q is None:
+        Q = torch.empty(X.shape, dtype=torch.uint8, device=X.device)
+    if sQ is None:
+        sQ = torch.empty((*X.shape[:-1], _cdiv(K, 128)), dtype=torch.float32, device=X.device)
+    if rstd is None:
+        rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
+    Qb = _need(_u8_fmt(Q, fmt, "Q"), "Q", M * K, K)
+    _need(_f32(sQ, "sQ"), "sQ", M * _cdiv(K, 128), _cdiv(K, 128))
+    _need(_f32(rstd, "rstd"), "rstd", M)
+    _check(lib().fp8_rmsnorm_quant(_ptr(X, "X"), _opt(residual, "residual"), kind,
+                                   _ptr(gain, "gain"), float(eps),
+                                   _opt(H, "H"), _ptr(Qb, "Q"), _ptr(sQ, "sQ"),
+                                   _ptr(rstd, "rstd"), M, K, FMT[fmt], _stream(stream)),
+           "fp8_rmsnorm_quant")
+    return Q, sQ, (X if residual is None else H), rstd
+
+
+def fp8_rmsnorm_backward(dY, H, rstd, gain, dH=None, dX=None, dgain=None, stream=None):
+    """Gradients of fp8_rmsnorm_quant's norm (straight through the quantiser):
+    dY and H bf16 or f32 [..., K], rstd f32 [...], gain f32 [K], dH (the
+    gradient that reaches H past the norm) as dY or None -> (dX, dgain f32 [K])."""
+    torch = _torch()
+    kind = _type(H, "H")
+    K = H.shape[-1]
+    M = H.numel() // K if K else 0
+    _like(dY, "dY", H)
+    if dH is not None:
+        _like(dH, "dH", H)
+    dX = torch.empty_like(H) if dX is None else _like(dX, "dX", H)
+    if dgain is None:
+        dgain = torch.empty(K, dtype=torch.float32, device=H.device)
+    _need(_f32(rstd, "rstd"), "rstd", M)
+    _need(_f32(gain, "gain"), "gain", K)
+    _need(_f32(dgain, "dgain"), "dgain", K)
+    _check(lib().fp8_rmsnorm_backward(_ptr(dY, "dY"), _ptr(H, "H"), kind, _ptr(rstd, "rstd"),
+                                      _ptr(gain, "gain"), _opt(dH, "dH"), _ptr(dX, "dX"),
+                                      _ptr(dgain, "dgain"), M, K, _stream(stream)),
+           "fp8_rmsnorm_backward")
+    return dX, dgain
+
+
+def _tokens(t, name, heads, dim):
+    """bf16 [T, heads, dim] whose tokens may lie apart (parts of the rows of a
+    fused projection's output): returns the token stride in elements."""
+    _bf16(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [T, {heads}, {dim}]")
+    ld, sh, sd = t.stride()
+    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
+        raise ValueError(f"{name} must hold each token's heads contiguously")
+    return ld if t.shape[0] > 1 else heads * dim
+
+
+def _cache(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T, fmt):
+    """Sizes of a paged cache and its index arrays: (codes k, codes v, blocks,
+    heads, block, dim, B, table width)."""
+    k, v = _u8_fmt(k_cache, fmt, "k_cache"), _u8_fmt(v_cache, fmt, "v_cache")
+    if k.dim() != 4 or v.shape != k.shape:
+        raise ValueError(f"k_cache {tuple(k.shape)} / v_cache {tuple(v.shape)}: the call needs"
+                         " [num_blocks, heads, block, dim] twice")
+    n, heads, block, dim = k.shape
+    _need(_f32(k_scale, "k_scale"), "k_scale", n * heads)
+    _need(_f32(v_scale, "v_scale"), "v_scale", n * heads)
+    if _i32(block_table, "block_table").dim() != 2:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}; the call needs"
+                         " [B, table_width]")
+    B, width = block_table.shape
+    _need(_i32(seq_lens, "seq_lens"), "seq_lens", B)
+    if cu is not None:
+        _need(_i32(cu, "the offsets"), "the offsets", B + 1)
+    elif B > 0 and T % B != 0:
+        raise ValueError(f"{T} tokens for {B} sequences: give the offsets")
+    return k, v, n, heads, block, dim, B, width
+
+
+def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_new=None,
+                  max_new=None, fmt="e4m3", stream=None):
+    """Write new keys and values (bf16 [T, heads, dim], tokens may lie apart)
+    into the paged FP8 cache (codes u8 [num_blocks, heads, block, dim], scales
+    f32 [num_blocks, heads]), at the end of each sequence: seq_lens i32 [B]
+    counts them already.  cu_new i32 [B + 1] are the offsets of each sequence's
+    tokens (None: T / B each); max_new bounds a sequence's (None: T)."""
+    T = K.shape[0]
+    kc, vc, n, heads, block, dim, B, width = _cache(k_cache, k_scale, v_cache, v_scale,
+                                                    block_table, seq_lens, cu_new, T, fmt)
+    ld_k, ld_v = _tokens(K, "K", heads, dim), _tokens(V, "V", heads, dim)
+    if V.shape[0] != T:
+        raise ValueError(f"K holds {T} tokens, V {V.shape[0]}")
+    if max_new is None:
+        max_new = T if cu_new is not None else _cdiv(T, max(B, 1))
+    _check(lib().fp8_kv_append(K.data_ptr(), V.data_ptr(), ld_k, ld_v,
+                               _ptr(kc, "k_cache"), _ptr(k_scale, "k_scale"),
+                               _ptr(vc, "v_cache"), _ptr(v_scale, "v_scale"),
+                               _ptr(block_table, "block_table"), _ptr(seq_lens, "seq_lens"),
+                               _opt(cu_new, "cu_new"), T, B, heads, dim, block, width, n,
+                               int(max_new), FMT[fmt], _stream(stream)), "fp8_kv_append")
+
+
+def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q=None,
+                     max_q=None, scale=None, fmt="e4m3", O=None, stream=None):
+    """Attention of the newest tokens (Q bf16 [T, heads * group, dim], tokens
+    may lie apart) over the paged FP8 cache that holds their keys and values
+    already -> O bf16 [T, heads * group, dim].  cu_q and max_q as
+    fp8_kv_append's; scale defaults to dim ** -0.5."""
+    torch = _torch()
+    T = Q.shape[0]
+    kc, vc, n, heads, block, dim, B, width = _cache(k_cache, k_scale, v_cache, v_scale,
+                                                    block_table, seq_lens, cu_q, T, fmt)
+    if Q.dim() != 3 or heads == 0 or Q.shape[1] % heads != 0:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}; the call needs [T, heads * group, dim]"
+                         f" with {heads} cached heads")
+    group = Q.shape[1] // heads
+    ld_q = _tokens(Q, "Q", heads * group, dim)
+    if O is None:
+        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
+    _need(_bf16(O, "O"), "O", T * heads * group * dim, dim)
+    if max_q is None:
+        max_q = T if cu_q is not None else _cdiv(T, max(B, 1))
+    if scale is None:
+        scale = dim ** -0.5
+    _check(lib().fp8_kv_attention(Q.data_ptr(), ld_q, _ptr(kc, "k_cache"),
+                                  _ptr(k_scale, "k_scale"), _ptr(vc, "v_cache"),
+                                  _ptr(v_scale, "v_scale"), _ptr(block_table, "block_table"),
+                                  _ptr(seq_lens, "seq_lens"), _opt(cu_q, "cu_q"), float(scale),
+                                  _ptr(O, "O"), T, B, heads, group, dim, block, width, n,
+                                  int(max_q), FMT[fmt], _stream(stream)), "fp8_kv_attention")
+    return O
+
+
+def fp8_moe_few(A, sA, logits, W1, s1, W2, s2, top_k, renormalise=True, D=None, ids=None,
+                weights=None, stream=None):
+    """A mixture-of-experts layer for at most 64 tokens: A u8 [T, H], sA f32
+    [T, ceil(H/128)], logits f32 [T, E], W1 u8 [E, 2 I, H] (gate rows, then up
+    rows), W2 u8 [E, H, I] with their 128x128 scales -> (D bf16 [T, H], ids i32
+    [T, top_k], weights f32 [T, top_k])."""
+    torch = _torch()
+    A, W1, W2 = _u8(A, "A"), _u8(W1, "W1"), _u8(W2, "W2")
+    if A.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
+        raise ValueError(f"A {tuple(A.shape)} / W1 {tuple(W1.shape)} / W2 {tuple(W2.shape)}: the"
+                         " call needs [T, H], [E, 2 I, H] and [E, H, I]")
+    T, H = A.shape
+    E, I2, _ = W1.shape
+    I = I2 // 2
+    if W1.shape != (E, 2 * I, H) or W2.shape != (E, H, I):
+        raise ValueError(f"W1 {tuple(W1.shape)} / W2 {tuple(W2.shape)}: the call needs"
+                         f" [E, 2 I, {H}] and [E, {H}, I]")
+    Hb, k = _cdiv(H, 128), int(top_k)
+    _need(_f32(sA, "sA"), "sA", T * Hb, Hb)
+    _need(_f32(logits, "logits"), "logits", T * E, E)
+    _need(_f32(s1, "s1"), "s1", E * _cdiv(2 * I, 128) * Hb, Hb)
+    _need(_f32(s2, "s2"), "s2", E * Hb * _cdiv(I, 128), _cdiv(I, 128))
+    if D is None:
+        D = torch.empty((T, H), dtype=torch.bfloat16, device=A.device)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=A.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=A.device)
+    _need(_bf16(D, "D"), "D", T * H, H)
+    _need(_i32(ids, "ids"), "ids", T * k, k)
+    _need(_f32(weights, "weights"), "weights", T * k, k)
+    _check(lib().fp8_moe_few(_ptr(A, "A"), _ptr(sA, "sA"), _ptr(logits, "logits"), _ptr(W1, "W1"),
+                             _ptr(s1, "s1"), _ptr(W2, "W2"), _ptr(s2, "s2"), _ptr(D, "D"),
+                             _ptr(ids, "ids"), _ptr(weights, "weights"), T, H, I, E, k,
+                             int(bool(renormalise)), _stream(stream)), "fp8_moe_few")
+    return D, ids, weights
 
 
 def fp8gemm_get_device_status(stream=None) -> int:

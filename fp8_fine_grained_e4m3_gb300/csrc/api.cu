@@ -11,6 +11,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "moe_few.cuh"
 
 namespace fp8gemm {
 
@@ -136,6 +137,7 @@ int device_info(DeviceInfo* out) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int finish(cudaError_t e, int nlaunch) {
   if (e != cudaSuccess) {
@@ -154,7 +156,10 @@ int finish(cudaError_t e, int nlaunch) {
 // Slot kWsTable: the stream-K partials and counters of the problem-table GEMM.
 // Slot kWsBatch: the tile counters of the batched dense GEMM.  Slot
 // kWsContig: the tile counters and tile order of the contiguous form.
-enum { kWsSplitK = 0, kWsQuantA = 1, kWsTable = 2, kWsBatch = 3, kWsContig = 4 };
+// Slot kWsNorm: partial gain gradients of the norm.  Slot kWsMoe: routing and
+// hidden activations of the few-token MoE layer.
+enum { kWsSplitK = 0, kWsQuantA = 1, kWsTable = 2, kWsBatch = 3, kWsContig = 4, kWsNorm = 5,
+       kWsMoe = 6 };
 
 int workspace_for(cudaStream_t s, size_t bytes, void** out, int slot = kWsSplitK) {
   int dev = 0;
@@ -507,6 +512,133 @@ int fp8gemm_grouped_masked(const uint8_t* A, const float* sA, const uint8_t* B, 
                            fp8gemm_stream_t stream) {
   return fp8gemm_grouped_masked_fmt(A, sA, FP8GEMM_FMT_E4M3, B, sB, FP8GEMM_FMT_E4M3, masked_m,
                                     D, E, M_max, N, K, stream);
+}
+
+int fp8_rmsnorm_quant(const void* X, const void* R, int x_type, const float* G, float eps, void* H,
+                      uint8_t* Q, float* sQ, float* rstd, int M, int K, int fmt,
+                      fp8gemm_stream_t stream) {
+  if (M < 0 || K <= 0 || K % kKAlign != 0 || K > kMaxNormK) return FP8GEMM_ERR_SHAPE;
+  if (!valid_fmt(fmt) || (x_type != FP8GEMM_TYPE_BF16 && x_type != FP8GEMM_TYPE_F32))
+    return FP8GEMM_ERR_FORMAT;
+  if (M == 0) return FP8GEMM_OK;
+  if (!X || !G || !Q || !sQ || (R == nullptr) != (H == nullptr)) return FP8GEMM_ERR_NULL;
+  if (!aligned16(X) || !aligned16(R) || !aligned16(G) || !aligned16(H) || !aligned16(Q) ||
+      !aligned16(sQ) || !aligned4(rstd))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const NormArgs a{X, R, G, eps, H, Q, sQ, rstd, M, K, x_type == FP8GEMM_TYPE_F32, fmt};
+  return finish(launch_rmsnorm_quant(c, a), 1);
+}
+
+int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float* rstd,
+                         const float* G, const void* dH, void* dX, float* dG, int M, int K,
+                         fp8gemm_stream_t stream) {
+  if (M < 0 || K <= 0 || K % kKAlign != 0 || K > kMaxNormK) return FP8GEMM_ERR_SHAPE;
+  if (x_type != FP8GEMM_TYPE_BF16 && x_type != FP8GEMM_TYPE_F32) return FP8GEMM_ERR_FORMAT;
+  if (!dG || !G) return FP8GEMM_ERR_NULL;
+  if (!aligned16(dG) || !aligned16(G)) return FP8GEMM_ERR_ALIGN;
+  if (M > 0 && (!dY || !H || !rstd || !dX)) return FP8GEMM_ERR_NULL;
+  if (!aligned16(dY) || !aligned16(H) || !aligned4(rstd) || !aligned16(dH) || !aligned16(dX))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  if (M == 0)  // a sum over no rows
+    return finish(cudaMemsetAsync(dG, 0, size_t(K) * 4, stream), 0);
+  void* ws = nullptr;
+  if (int r = workspace_for(stream, rmsnorm_backward_workspace_bytes(c, M, K), &ws, kWsNorm))
+    return r;
+  const NormGradArgs a{dY, H, rstd, G, dH, dX, dG, M, K, x_type == FP8GEMM_TYPE_F32};
+  return finish(launch_rmsnorm_backward(c, a, ws), 2);
+}
+
+// What the cache's two calls have in common.
+static int check_cache(int T, int B, int heads, int dim, int block, int width, int num_blocks,
+                       int most, const int32_t* cu, int fmt) {
+  if (T < 0 || B < 0 || heads < 0 || width < 0 || num_blocks < 0 || most < 0)
+    return FP8GEMM_ERR_SHAPE;
+  if ((dim != 64 && dim != 128) || (block != 16 && block != 32 && block != 64 && block != 128))
+    return FP8GEMM_ERR_SHAPE;
+  if (B > 32767 || heads > 65535) return FP8GEMM_ERR_SHAPE;
+  if (!cu && B > 0 && (T % B != 0 || most < T / B)) return FP8GEMM_ERR_SHAPE;
+  if (!valid_fmt(fmt)) return FP8GEMM_ERR_FORMAT;
+  return FP8GEMM_OK;
+}
+
+int fp8_kv_append(const void* K, const void* V, int64_t ld_k, int64_t ld_v, uint8_t* k_cache,
+                  float* k_scale, uint8_t* v_cache, float* v_scale, const int32_t* block_table,
+                  const int32_t* seq_lens, const int32_t* cu_new, int T, int B, int heads, int dim,
+                  int block, int table_width, int num_blocks, int max_new, int fmt,
+                  fp8gemm_stream_t stream) {
+  if (int r = check_cache(T, B, heads, dim, block, table_width, num_blocks, max_new, cu_new, fmt))
+    return r;
+  if (T == 0 || B == 0 || heads == 0 || max_new == 0) return FP8GEMM_OK;
+  const int64_t row = int64_t(heads) * dim;
+  if (ld_k < row || ld_v < row || ld_k % 8 != 0 || ld_v % 8 != 0) return FP8GEMM_ERR_SHAPE;
+  if (!K || !V || !k_cache || !k_scale || !v_cache || !v_scale || !block_table || !seq_lens)
+    return FP8GEMM_ERR_NULL;
+  if (!aligned16(K) || !aligned16(V) || !aligned16(k_cache) || !aligned4(k_scale) ||
+      !aligned16(v_cache) || !aligned4(v_scale) || !aligned4(block_table) ||
+      !aligned4(seq_lens) || !aligned4(cu_new))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const KvAppendArgs a{static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V),
+                       ld_k, ld_v, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
+                       cu_new, T, B, heads, dim, block, table_width, num_blocks, max_new, fmt};
+  return finish(launch_kv_append(c, a), 1);
+}
+
+int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
+                     const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
+                     const int32_t* seq_lens, const int32_t* cu_q, float scale, void* O, int T,
+                     int B, int heads, int group, int dim, int block, int table_width,
+                     int num_blocks, int max_q, int fmt, fp8gemm_stream_t stream) {
+  if (int r = check_cache(T, B, heads, dim, block, table_width, num_blocks, max_q, cu_q, fmt))
+    return r;
+  if (group < 0 || (long long)heads * group > 65535 || (long long)max_q * group > 0x7fffffffLL)
+    return FP8GEMM_ERR_SHAPE;
+  if (T == 0 || B == 0 || heads == 0 || group == 0 || max_q == 0) return FP8GEMM_OK;
+  if (ld_q < int64_t(heads) * group * dim || ld_q % 8 != 0) return FP8GEMM_ERR_SHAPE;
+  if (!Q || !k_cache || !k_scale || !v_cache || !v_scale || !block_table || !seq_lens || !O)
+    return FP8GEMM_ERR_NULL;
+  if (!aligned16(Q) || !aligned16(k_cache) || !aligned4(k_scale) || !aligned16(v_cache) ||
+      !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) ||
+      !aligned4(cu_q) || !aligned16(O))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const KvAttentionArgs a{static_cast<const __nv_bfloat16*>(Q), ld_q, k_cache, k_scale, v_cache,
+                          v_scale, block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O),
+                          scale, T, B, heads, group, dim, block, table_width, num_blocks, max_q,
+                          fmt};
+  return finish(launch_kv_attention(c, a), 1);
+}
+
+int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,
+                const float* s1, const uint8_t* W2, const float* s2, void* D, int32_t* ids,
+                float* weights, int T, int H, int I, int E, int top_k, int renormalise,
+                fp8gemm_stream_t stream) {
+  if (T < 0 || T > kMoeMaxTokens || H <= 0 || I <= 0 || H % kKAlign != 0 || I % kKAlign != 0)
+    return FP8GEMM_ERR_SHAPE;
+  if (E <= 0 || E > kMoeMaxExperts || top_k <= 0 || top_k > kMoeMaxTopK || top_k > E)
+    return FP8GEMM_ERR_SHAPE;
+  if ((long long)I * 2 > 0x7fffffffLL) return FP8GEMM_ERR_SHAPE;
+  if (T == 0) return FP8GEMM_OK;
+  if (!A || !sA || !logits || !W1 || !s1 || !W2 || !s2 || !D || !ids || !weights)
+    return FP8GEMM_ERR_NULL;
+  if (!aligned16(A) || !aligned16(sA) || !aligned4(logits) || !aligned16(W1) || !aligned16(s1) ||
+      !aligned16(W2) || !aligned16(s2) || !aligned16(D) || !aligned4(ids) || !aligned4(weights))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const MoeArgs a{A, sA, logits, W1, s1, W2, s2, static_cast<__nv_bfloat16*>(D), ids, weights,
+                  T, H, I, E, top_k, renormalise};
+  void* ws = nullptr;
+  if (int r = workspace_for(stream, moe_few_workspace_bytes(a), &ws, kWsMoe)) return r;
+  int launches = 0;
+  const cudaError_t e = launch_moe_few(c, a, ws, &launches);
+  return finish(e, launches);
 }
 
 int fp8gemm_get_device_status(fp8gemm_stream_t stream, int* out) {

@@ -108,6 +108,88 @@ size_t table_workspace_bytes(const LaunchCtx& c, int max_M);
 cudaError_t launch_gemm_table(const LaunchCtx& c, const fp8gemm_problem* tab, int P, int max_M,
                               void* ws, size_t ws_bytes);
 
+// The residual norm with FP8 output, and its gradient (norm.cu).
+constexpr int kMaxNormK = 16384;
+
+struct NormArgs {
+  const void* X;
+  const void* R;  // residual, or null
+  const float* G;
+  float eps;
+  void* H;        // x + r (with R only)
+  uint8_t* Q;
+  float* sQ;
+  float* rstd;    // or null
+  int M, K;
+  bool f32;       // X, R and H are FP32 rather than BF16
+  int fmt;
+};
+cudaError_t launch_rmsnorm_quant(const LaunchCtx& c, const NormArgs& a);
+
+struct NormGradArgs {
+  const void* dY;
+  const void* H;
+  const float* rstd;
+  const float* G;
+  const void* dH;  // gradient that reaches h past the norm, or null
+  void* dX;
+  float* dG;
+  int M, K;
+  bool f32;
+};
+size_t rmsnorm_backward_workspace_bytes(const LaunchCtx& c, int M, int K);
+cudaError_t launch_rmsnorm_backward(const LaunchCtx& c, const NormGradArgs& a, void* ws);
+
+// The paged FP8 cache (kv_cache.cu, kv_attention.cu): codes
+// [num_blocks, heads, block, dim], scales [num_blocks, heads].
+struct KvAppendArgs {
+  const __nv_bfloat16* K;  // [T, heads, dim], ld_* elements from token to token
+  const __nv_bfloat16* V;
+  long long ld_k, ld_v;
+  uint8_t* kc;
+  float* ks;
+  uint8_t* vc;
+  float* vs;
+  const int* table;  // [B, width]
+  const int* lens;   // [B]
+  const int* cu;     // [B + 1], or null: T / B tokens each
+  int T, B, heads, dim, block, width, num_blocks, max_new, fmt;
+};
+cudaError_t launch_kv_append(const LaunchCtx& c, const KvAppendArgs& a);
+
+struct KvAttentionArgs {
+  const __nv_bfloat16* Q;  // [T, heads * group, dim], ld_q elements from token to token
+  long long ld_q;
+  const uint8_t* kc;
+  const float* ks;
+  const uint8_t* vc;
+  const float* vs;
+  const int* table;
+  const int* lens;
+  const int* cu;
+  __nv_bfloat16* O;  // [T, heads * group, dim]
+  float scale;
+  int T, B, heads, group, dim, block, width, num_blocks, max_q, fmt;
+};
+cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a);
+
+// The mixture-of-experts layer for a few tokens (moe_few.cu).
+struct MoeArgs {
+  const uint8_t* A;   // [T, H]
+  const float* sA;
+  const float* logits;  // [T, E]
+  const uint8_t* W1;  // [E, 2 I, H]: gate rows, then up rows
+  const float* s1;
+  const uint8_t* W2;  // [E, H, I]
+  const float* s2;
+  __nv_bfloat16* D;   // [T, H]
+  int* ids;           // [T, k]
+  float* weights;     // [T, k]
+  int T, H, I, E, k, renormalise;
+};
+size_t moe_few_workspace_bytes(const MoeArgs& a);
+cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace, int* launches);
+
 // Fills `c` for the current device and `stream` (SM count, status word);
 // returns an fp8gemm_status code.  Defined in api.cu.
 int make_launch_ctx(cudaStream_t stream, LaunchCtx* c);

@@ -49,7 +49,8 @@
  *    until released or process exit) and zeroes on that stream; fp8gemm_dense_quant_a at
  *    M > 64 without Q/sA keeps its quantised A in a second per-stream buffer,
  *    and fp8gemm_dense_batch and the ordered contiguous form their tile
- *    counters (and order) in small per-stream buffers.
+ *    counters (and order) in small per-stream buffers; fp8_rmsnorm_backward
+ *    and fp8_moe_few keep theirs the same way.
  *    Such a first call must therefore not happen during CUDA graph capture.
  *    Calls on different streams never share a workspace.  The reduction
  *    order is fixed, so results are deterministic.  A caller that retires a
@@ -442,6 +443,155 @@ int fp8gemm_dense_small_m_noalloc(const uint8_t* A, const float* sA, const uint8
                                   const float* sB, void* D, int M, int N, int K,
                                   fp8gemm_stream_t stream);
 
+/* Types of the activations that the norm's calls take. */
+enum fp8gemm_type {
+  FP8GEMM_TYPE_BF16 = 0,
+  FP8GEMM_TYPE_F32 = 1
+};
+
+/*
+ * fp8_rmsnorm_quant -- the producer of a GEMM's A operand from the residual
+ * stream, in one pass: residual addition, root-mean-square norm and 1x128
+ * quantisation.
+ *
+ *   h = x + r, rounded to the stream's type   (h = x without a residual)
+ *   rstd[m] = 1 / sqrt(mean over k of h^2 + eps)
+ *   y = h rstd g;   sQ, Q = fp8_quant_1x128's rule on y (limit of `fmt`)
+ *
+ * All arithmetic is FP32; the norm is taken of the rounded h, which is what
+ * the next layer and the gradient see.
+ *
+ *   X    [M, K] of x_type (FP8GEMM_TYPE_*)
+ *   R, H [M, K] of x_type: the residual in and h out; both NULL for none.  H
+ *        may be R itself (the stream updated in place).
+ *   G    f32 [K]
+ *   Q    u8 [M, K], sQ f32 [M, ceil(K/128)], rstd f32 [M] (NULL: not wanted)
+ *   K % 16 == 0, 0 < K <= 16384; pointers 16-byte aligned (rstd 4).
+ */
+int fp8_rmsnorm_quant(const void* X, const void* R, int x_type, const float* G, float eps, void* H,
+                      uint8_t* Q, float* sQ, float* rstd, int M, int K, int fmt,
+                      fp8gemm_stream_t stream);
+
+/*
+ * fp8_rmsnorm_backward -- gradients of fp8_rmsnorm_quant's norm, the quantiser
+ * passing them straight through.  With xhat = h rstd:
+ *
+ *   dX = rstd (dY g - xhat mean over k of (dY g xhat)) + dH
+ *   dG = sum over m of dY xhat
+ *
+ * dX is the gradient of x and of the residual alike.
+ *
+ *   dY, H, dX [M, K] of x_type; dH the same, or NULL: the gradient that
+ *   reaches h past the norm.  dX may be dY or dH itself.
+ *   rstd f32 [M] as the forward call left it; G, dG f32 [K] (dG is written in
+ *   full, zeros for M = 0).
+ *   Sizes and alignment as fp8_rmsnorm_quant.  Partial sums of dG live in a
+ *   per-(device, stream) workspace (at most 12 K floats for each SM); their
+ *   order is fixed, so dG is deterministic.
+ */
+int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float* rstd,
+                         const float* G, const void* dH, void* dX, float* dG, int M, int K,
+                         fp8gemm_stream_t stream);
+
+/*
+ * The paged FP8 cache of fp8_kv_append and fp8_kv_attention.
+ *
+ *   k_cache, v_cache  u8 [num_blocks, heads, block, dim]: FP8 codes of `fmt`
+ *   k_scale, v_scale  f32 [num_blocks, heads]: value = code * scale
+ *   block_table       i32 [B, table_width] (device): block j of sequence b
+ *                     holds its tokens block j .. block (j + 1) - 1
+ *   seq_lens          i32 [B] (device): tokens of each sequence in the cache,
+ *                     those of this call included
+ *   cu                i32 [B + 1] (device): the call's own tokens lie packed
+ *                     on the token axis, those of sequence b at cu[b] ..
+ *                     cu[b + 1] - 1, at most max_new (max_q) of them.  NULL: T / B each
+ *                     (T % B == 0).
+ *   dim is 64 or 128; block 16, 32, 64 or 128; heads counts the cached heads.
+ *
+ * The launch depends on host sizes only, so a captured graph can be replayed
+ * with new lengths and tables.  A length outside 0 .. block * table_width (or
+ * below the number of the sequence's new tokens, for the append), an offset
+ * out of order and a table entry outside 0 .. num_blocks - 1 set
+ * FP8GEMM_ERR_DEVICE_STATUS; the append skips what it concerns, the attention
+ * counts those tokens as not there.
+ */
+
+/*
+ * fp8_kv_append -- write the newest tokens of every sequence into the cache, at
+ * positions seq_len - n .. seq_len - 1 of a sequence with n new tokens.
+ *
+ * For each (block, head) that gets tokens, over those tokens:
+ *   need = the smallest power of two >= amax / limit (FP32 division; at least
+ *          2^-126; 0 if amax = 0)
+ *   s    = need where the block's first token is new, else max(s_old, need)
+ *   codes of the new tokens: f8(x / s), rounded to nearest even, saturating
+ * and where s > s_old the tokens already there become f8(code * s_old / s).
+ * (A power of two costs a floating code no precision and makes that step
+ * exact but for codes that reach the subnormals.)  NaN and infinities are outside the
+ * contract.  No two sequences may append to the same block.
+ *
+ *   K, V  bf16 [T, heads, dim], ld_k / ld_v elements from token to token
+ *         (multiples of 8, at least heads * dim): parts of the rows of a fused
+ *         projection's output are taken as they lie.
+ *   Alignment: 16 bytes (scales, tables, lengths and offsets 4).
+ */
+int fp8_kv_append(const void* K, const void* V, int64_t ld_k, int64_t ld_v, uint8_t* k_cache,
+                  float* k_scale, uint8_t* v_cache, float* v_scale, const int32_t* block_table,
+                  const int32_t* seq_lens, const int32_t* cu_new, int T, int B, int heads, int dim,
+                  int block, int table_width, int num_blocks, int max_new, int fmt,
+                  fp8gemm_stream_t stream);
+
+/*
+ * fp8_kv_attention -- attention of the newest tokens over the cache:
+ *
+ *   O[t, h] = sum over j of p_j v_j,  p = softmax over the visible j of
+ *             scale * Q[t, h] . k_j,  cached head h / group
+ *
+ * Query i of a sequence's n new ones sees its first seq_len - n + 1 + i tokens
+ * (causal; its own key is in the cache by then).  A query that sees none gives
+ * zeros.  Bytes of the cache at and past seq_len are never used.  Made for
+ * serving: one to a few new tokens per sequence over a long cache (more are
+ * taken 8 rows of n * group at a time).
+ *
+ *   Q  bf16 [T, heads * group, dim], ld_q elements from token to token (a
+ *      multiple of 8, at least heads * group * dim)
+ *   O  bf16 [T, heads * group, dim] (output)
+ *   Alignment as fp8_kv_append.
+ */
+int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
+                     const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
+                     const int32_t* seq_lens, const int32_t* cu_q, float scale, void* O, int T,
+                     int B, int heads, int group, int dim, int block, int table_width,
+                     int num_blocks, int max_q, int fmt, fp8gemm_stream_t stream);
+
+/*
+ * fp8_moe_few -- a whole mixture-of-experts layer for a few tokens.
+ *
+ *   ids[t, :]      the top_k experts of token t by logit, largest first, ties
+ *                  to the lowest index (NaN counts as -infinity)
+ *   weights[t, :]  their softmax: over the chosen ones (renormalise != 0) or over
+ *                  all E.  An expert at -infinity gets weight 0.
+ *   for each choice: u = A W1^T (block scales and promotion as
+ *                  fp8gemm_dense), h = silu(u[:I]) * u[I:] in FP32, quantised by
+ *                  fp8_quant_1x128's rule, y = h W2^T
+ *   D[t] = bf16( sum over the choices of weight * y )
+ *
+ *   A  u8 e4m3 [T, H], sA f32 [T, ceil(H/128)]; logits f32 [T, E]
+ *   W1 u8 e4m3 [E, 2 I, H]: the I gate rows, then the I up rows
+ *   s1 f32 [E, ceil(2 I/128), ceil(H/128)]
+ *   W2 u8 e4m3 [E, H, I], s2 f32 [E, ceil(H/128), ceil(I/128)]
+ *   D  bf16 [T, H], ids i32 [T, top_k], weights f32 [T, top_k] (outputs)
+ *   T <= 64, top_k <= 16, top_k <= E <= 512, H and I positive multiples of 16.
+ *   Alignment: 16 bytes (logits, ids and weights 4).
+ *
+ * Routing and hidden activations live in a per-(device, stream) workspace.
+ * Results are deterministic.  More tokens: fp8gemm_grouped_contiguous.
+ */
+int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,
+                const float* s1, const uint8_t* W2, const float* s2, void* D, int32_t* ids,
+                float* weights, int T, int H, int I, int E, int top_k, int renormalise,
+                fp8gemm_stream_t stream);
+
 /*
  * fp8gemm_get_device_status -- after every kernel enqueued on `stream` so
  * far, read and clear the current device's status word in one atomic step
@@ -468,8 +618,9 @@ uint64_t fp8gemm_num_kernel_launches(void);
  * fp8gemm_release_workspaces -- free every library-owned workspace of
  * `stream` on the current device (the split-K buffer of the decode path, the
  * quantised-activation buffer of fp8gemm_dense_quant_a, the problem table's
- * partials, and the tile counters and order of fp8gemm_dense_batch and of
- * the ordered contiguous form).  It first
+ * partials, the tile counters and order of fp8gemm_dense_batch and of the
+ * ordered contiguous form, and those of the norm's gradient and of the
+ * few-token MoE layer).  It first
  * synchronises `stream`, since work enqueued there may still use them; the
  * next call that needs a workspace on that stream allocates it again.  Call
  * it before cudaStreamDestroy for streams that are retired: a stream handle

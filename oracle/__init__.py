@@ -24,9 +24,11 @@ Modules:
   quantisers, FP32 semantics.
 * :mod:`oracle.gemm`  -- the block-scaled GEMM in FP64: dense, grouped
   contiguous, grouped masked, and a sampled-element form.
+* :mod:`oracle.layer` -- what a decoder layer does around the products: norm,
+  FP8 cache and attention, mixture of experts for a few tokens.
 
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms,
 library routines or brute force; nothing here is "parity unpinned".
 """
 
-from . import e4m3, e5m2, quant, gemm  # noqa: F401
+from . import e4m3, e5m2, quant, gemm, layer  # noqa: F401

@@ -1,0 +1,290 @@
+"""fp8_kv_append bit for bit, and fp8_kv_attention within its rounding,
+against the FP64 oracle.
+
+Attention's bound, derived before the first run: p is rounded to FP16 (2^-11
+relative, or 2^-25 of the largest p absolute), the scores and sums are FP32
+(together under 2^-12 relative here), the output BF16 (2^-9 relative):
+  |got - ref| <= 2^-8 |ref| + 2^-10 sum p |v| + n 2^-24 max |v|
+"""
+
+import numpy as np
+import pytest
+
+from oracle import layer
+from tests.gpu_helpers import dev, host
+
+pytestmark = pytest.mark.gpu
+
+_CODES = {"e4m3": layer.e4m3, "e5m2": layer.e5m2}
+
+
+class Cache:
+    """A paged cache with codes everywhere, and NaN codes behind each sequence."""
+
+    def __init__(self, lens, heads, dim, block, fmt, seed, spread=2, spare=2):
+        g = np.random.default_rng(seed)
+        per = [-(-n // block) for n in lens]
+        self.n, self.width = max(1, sum(per)) + spare, max(1, max(per))
+        order = g.permutation(self.n)
+        self.table = np.zeros((len(lens), self.width), np.int32)
+        at = 0
+        for b, p in enumerate(per):
+            self.table[b, :p] = order[at:at + p]
+            at += p
+        enc = _CODES[fmt].encode_rne_sat
+        limit = 448.0 if fmt == "e4m3" else 57344.0
+        shape = (self.n, heads, block, dim)
+        self.k, self.v = (enc((limit / 5 * g.standard_normal(shape)).astype(np.float32)) for _ in range(2))
+        self.ks, self.vs = (np.exp2(g.integers(-spread, spread + 1, (self.n, heads)) - np.round(np.log2(limit / 5)))
+                            .astype(np.float32) for _ in range(2))
+        self.lens, self.fmt = np.asarray(lens, np.int32), fmt
+
+    def stale(self):
+        used = {int(x) for b, n in enumerate(self.lens) for x in self.table[b, :-(-n // self.k.shape[2])]}
+        for x in (self.k, self.v):
+            for b, n in enumerate(self.lens):
+                if n % x.shape[2]:
+                    x[self.table[b, n // x.shape[2]], :, n % x.shape[2]:] = 0x7F
+            for blk in set(range(self.n)) - used:
+                x[blk] = 0x7F
+        return self
+
+    def on_gpu(self):
+        return [dev(x) for x in (self.k, self.ks, self.v, self.vs, self.table, self.lens)]
+
+
+def _offsets(counts):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_append(block, dim, fmt):
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    new = [1, 0, 3, 150, 17, 1, 64]
+    old = [0, 5, 15, 7, 128, 200, 64]
+    heads = 3
+    c = Cache([a + n for a, n in zip(old, new)], heads, dim, block, fmt, seed=block + dim)
+    g = np.random.default_rng(1)
+    T = sum(new)
+    cu = _offsets(new)
+    wide = (np.exp2(g.integers(-6, 7, (T, 1))) * g.standard_normal((T, 3 * heads * dim))).astype(np.float32)
+    wide[5:60] = 0  # whole blocks of zeros
+    qkv = dev(wide).to(torch.bfloat16)
+    w = heads * dim
+    K, V = (qkv[:, i * w:(i + 1) * w].unflatten(1, (heads, dim)) for i in (1, 2))
+    k, ks, v, vs, table, lens = c.on_gpu()
+    b.fp8_kv_append(K, V, k, ks, v, vs, table, lens, cu_new=dev(cu), max_new=max(new), fmt=fmt)
+    layer.kv_append(K.float().cpu().numpy(), c.k, c.ks, c.table, c.lens, cu, fmt)
+    layer.kv_append(V.float().cpu().numpy(), c.v, c.vs, c.table, c.lens, cu, fmt)
+    for got, ref in ((k, c.k), (ks, c.ks), (v, c.v), (vs, c.vs)):
+        assert np.array_equal(host(got), ref)
+    assert b.fp8gemm_get_device_status() == b.OK
+
+
+def test_append_token_by_token_grows_scales():
+    """A sequence written one token at a time, ever larger: every step requantises."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    heads, dim, block = 2, 128, 16
+    c = Cache([40], heads, dim, block, "e4m3", seed=2)
+    k, ks, v, vs, table, _ = c.on_gpu()
+    g = np.random.default_rng(3)
+    for n in range(1, 41):
+        x = dev((1.7 ** (n % 20) * g.standard_normal((1, heads, dim))).astype(np.float32)).to(torch.bfloat16)
+        b.fp8_kv_append(x, -x, k, ks, v, vs, table, dev(np.array([n], np.int32)))
+        layer.kv_append(x.float().cpu().numpy(), c.k, c.ks, c.table, [n], [0, 1])
+        layer.kv_append(-x.float().cpu().numpy(), c.v, c.vs, c.table, [n], [0, 1])
+    for got, ref in ((k, c.k), (ks, c.ks), (v, c.v), (vs, c.vs)):
+        assert np.array_equal(host(got), ref)
+
+
+def _attend(c, Q, cu, scale, fmt, **kw):
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    tQ = dev(Q).to(torch.bfloat16)
+    k, ks, v, vs, table, lens = c.on_gpu()
+    O = torch.full(tQ.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    b.fp8_kv_attention(tQ, k, ks, v, vs, table, lens, cu_q=None if cu is None else dev(cu), scale=scale, fmt=fmt,
+                       O=O, **kw)
+    return host(O), tQ.double().cpu().numpy()
+
+
+def _check(got, c, Q, cu, scale, fmt):
+    O, A = layer.kv_attention(Q, c.k, c.ks, c.v, c.vs, c.table, c.lens, cu, scale, fmt)
+    vmax = np.nanmax(np.abs(_CODES[fmt].decode(c.v)) * c.vs[:, :, None, None].astype(np.float64))
+    bound = 2.0 ** -8 * np.abs(O) + 2.0 ** -10 * A + max(c.lens.max(), 1) * 2.0 ** -24 * vmax
+    bad = ~(np.abs(got - O) <= bound)
+    assert not bad.any(), (int(bad.sum()), bad.size, got[bad][:4], O[bad][:4])
+
+
+@pytest.mark.parametrize("lens,heads,group,dim,block,fmt,q", [
+    ([1], 1, 1, 64, 16, "e4m3", 1), ([37], 2, 1, 64, 16, "e4m3", 1), ([0, 5, 300, 16], 2, 3, 128, 32, "e4m3", 1),
+    ([1000, 17, 64], 2, 8, 128, 64, "e4m3", 1), ([511, 2], 1, 16, 128, 128, "e5m2", 1),
+    ([200, 3, 0, 65], 3, 5, 64, 64, "e5m2", 4), ([130, 2, 77], 2, 4, 128, 16, "e4m3", 7),
+    ([4099], 2, 8, 128, 64, "e4m3", 2), ([600, 601], 1, 8, 128, 32, "e4m3", 20), ([33] * 70, 2, 2, 64, 16, "e4m3", 1)])
+def test_attention(lens, heads, group, dim, block, fmt, q):
+    c = Cache(lens, heads, dim, block, fmt, seed=sum(lens)).stale()
+    g = np.random.default_rng(7)
+    Q = (2 * g.standard_normal((len(lens) * q, heads * group, dim))).astype(np.float32)
+    cu = _offsets([q] * len(lens))
+    got, Qr = _attend(c, Q, None, dim ** -0.5, fmt)
+    _check(got, c, Qr, cu, dim ** -0.5, fmt)
+    got2, _ = _attend(c, Q, cu, dim ** -0.5, fmt, max_q=q)
+    assert np.array_equal(got, got2)
+
+
+def test_attention_of_ragged_queries_from_a_fused_row():
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    counts, heads, group, dim = [3, 0, 1, 9, 2], 2, 4, 128
+    c = Cache([70, 10, 1, 9, 1], heads, dim, 32, "e4m3", seed=5).stale()  # the last: one token, two queries
+    cu = _offsets(counts)
+    g = np.random.default_rng(6)
+    w = heads * group * dim
+    qkv = dev(g.standard_normal((sum(counts), w + 2 * heads * dim)).astype(np.float32)).to(torch.bfloat16)
+    tQ = qkv[:, :w].unflatten(1, (heads * group, dim))
+    k, ks, v, vs, table, lens = c.on_gpu()
+    O = b.fp8_kv_attention(tQ, k, ks, v, vs, table, lens, cu_q=dev(cu), max_q=9, scale=0.3)
+    _check(host(O), c, tQ.double().cpu().numpy(), cu, 0.3, "e4m3")
+    assert not O[cu[4]].any()  # sees nothing
+
+
+@pytest.mark.parametrize("kind", ["peaked", "flat", "rising", "falling", "tiny_q", "huge_q", "wide_scales"])
+def test_attention_statistics(kind):
+    """Scores that one token dominates, that are all equal, that rise or fall
+    along the cache, queries near the ends of BF16's range, and scales of
+    neighbouring blocks that differ by 2^40."""
+    heads, dim, n = 1, 128, 700
+    c = Cache([n], heads, dim, 16, "e4m3", seed=9, spread=20 if kind == "wide_scales" else 1)
+    g = np.random.default_rng(10)
+    Q = g.standard_normal((1, 8, dim)).astype(np.float32)
+    scale = dim ** -0.5
+    enc = layer.e4m3.encode_rne_sat
+    if kind == "peaked":
+        c.k[c.table[0, 20], 0, 3] = enc((50 * np.sign(Q[0, 0])).astype(np.float32))
+        Q[:] = Q[:, :1]
+        scale = 1.0
+    elif kind == "flat":
+        Q[:] = 0
+    elif kind in ("rising", "falling"):
+        ramp = np.linspace(-1, 1, c.width * 16).astype(np.float32) * (1 if kind == "rising" else -1)
+        for j in range(c.width):
+            c.k[c.table[0, j], 0] = enc(np.repeat(400 * ramp[16 * j:16 * j + 16, None], dim, 1))
+        c.ks[:] = 2.0 ** -9
+        Q[:] = 8
+    elif kind == "tiny_q":
+        Q *= 1e-30
+        scale = 1e29
+    elif kind == "huge_q":
+        Q *= 1e30
+        scale = 1e-31
+    elif kind == "wide_scales":
+        c.ks[:] = 2.0 ** -6
+    got, Qr = _attend(c, Q, None, scale, "e4m3")
+    _check(got, c, Qr, [0, 1], scale, "e4m3")
+
+
+def test_long_cache_past_32_bit_offsets():
+    """A cache whose byte offsets pass 2^32, the sequence in its last blocks."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    heads, dim, block = 8, 128, 128
+    n = 2 ** 32 // (heads * dim * block) + 40
+    c = Cache([1500], heads, dim, block, "e4m3", seed=12, spare=0)
+    k, v = (torch.zeros((n, heads, block, dim), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((n, heads), device="cuda") for _ in range(2))
+    far = n - c.n
+    k[far:], v[far:], ks[far:], vs[far:] = dev(c.k), dev(c.v), dev(c.ks), dev(c.vs)
+    g = np.random.default_rng(13)
+    tQ, tK, tV = (dev(g.standard_normal((1, h, dim)).astype(np.float32)).to(torch.bfloat16) for h in (16, 8, 8))
+    table, lens = dev(c.table + far), dev(c.lens)
+    b.fp8_kv_append(tK, tV, k, ks, v, vs, table, lens)
+    O = b.fp8_kv_attention(tQ, k, ks, v, vs, table, lens)
+    layer.kv_append(tK.float().cpu().numpy(), c.k, c.ks, c.table, c.lens, [0, 1])
+    layer.kv_append(tV.float().cpu().numpy(), c.v, c.vs, c.table, c.lens, [0, 1])
+    assert np.array_equal(host(k[far:]), c.k) and np.array_equal(host(v[far:]), c.v)
+    _check(host(O), c, tQ.double().cpu().numpy(), [0, 1], dim ** -0.5, "e4m3")
+
+
+def test_bad_indices_set_the_status_and_touch_nothing():
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    c = Cache([40, 50], 1, 64, 16, "e4m3", seed=20)
+    g = np.random.default_rng(21)
+    x = dev(g.standard_normal((2, 1, 64)).astype(np.float32)).to(torch.bfloat16)
+    k, ks, v, vs, table, lens = c.on_gpu()
+    before = k.clone()
+
+    def expect(call):
+        call()
+        assert b.fp8gemm_get_device_status() == b.ERR_DEVICE_STATUS
+
+    bad = table.clone()
+    bad[:, -2:] = torch.tensor([c.n, -1], device="cuda", dtype=torch.int32)
+    expect(lambda: b.fp8_kv_append(x, x, k, ks, v, vs, bad, lens))
+    expect(lambda: b.fp8_kv_append(x, x, k, ks, v, vs, table, torch.full_like(lens, 10 ** 6)))
+    expect(lambda: b.fp8_kv_append(x, x, k, ks, v, vs, table, torch.zeros_like(lens)))
+    cu = dev(np.array([0, 3, 2], np.int32))
+    expect(lambda: b.fp8_kv_append(x, x, k, ks, v, vs, table, lens, cu_new=cu))
+    assert torch.equal(k, before)
+    expect(lambda: b.fp8_kv_attention(x, k, ks, v, vs, table, lens, cu_q=cu))
+    O = None
+
+    def run():
+        nonlocal O
+        O = b.fp8_kv_attention(x, k, ks, v, vs, table, torch.tensor([-3, 10 ** 6], device="cuda", dtype=torch.int32))
+    expect(run)
+    assert not O.any()
+    expect(lambda: b.fp8_kv_attention(x, k, ks, v, vs, torch.full_like(table, c.n), lens))
+    expect(lambda: b.fp8_kv_attention(x, k, ks, v, vs, torch.full_like(table, -1), lens))
+    assert b.fp8gemm_get_device_status() == b.OK
+
+
+def test_graph_replay_with_new_lengths():
+    """A captured append and attention replayed with other lengths, tables and
+    tokens equals the calls made directly."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    heads, group, dim, block, B = 2, 4, 128, 32, 3
+    c = Cache([500, 400, 300], heads, dim, block, "e4m3", seed=30)
+    g = np.random.default_rng(31)
+
+    def inputs():
+        return [dev(g.standard_normal((B, h, dim)).astype(np.float32)).to(torch.bfloat16)
+                for h in (heads * group, heads, heads)]
+
+    q, kn, vn = inputs()
+    k, ks, v, vs, table, lens = c.on_gpu()
+    mine = [x.clone() for x in (k, ks, v, vs)]
+    O = torch.empty_like(q)
+
+    def step(cache, o):
+        b.fp8_kv_append(kn, vn, *cache, table, lens)
+        b.fp8_kv_attention(q, *cache, table, lens, O=o)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step([k, ks, v, vs], O)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step([k, ks, v, vs], O)
+    for a, x in zip((k, ks, v, vs), mine):
+        a.copy_(x)
+    for new in ([100, 399, 1], [101, 400, 2], [500, 33, 64]):
+        lens.copy_(dev(np.array(new, np.int32)))
+        for a, x in zip((q, kn, vn), inputs()):
+            a.copy_(x)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+        s.synchronize()
+        want = torch.empty_like(O)
+        step(mine, want)
+        assert torch.equal(O, want)
+        for a, x in zip((k, ks, v, vs), mine):
+            assert torch.equal(a, x)

@@ -1,0 +1,120 @@
+"""fp8_moe_few against the FP64 oracle: routing equal, weights to FP32's
+rounding (an exponential, a sum of at most 512 and a division: 2e-6 relative),
+outputs within the GEMMs' acceptance (tests/gpu_helpers.py), and bit for bit
+against itself."""
+
+import numpy as np
+import pytest
+
+from oracle import layer
+from tests.gpu_helpers import assert_close, dev, host, oquant, quant_weights
+
+pytestmark = pytest.mark.gpu
+
+
+def _operands(T, H, I, E, seed):
+    g = np.random.default_rng(seed)
+    A, sA = oquant.quant_1x128_fast(g.standard_normal((T, H)).astype(np.float32))
+    W = [[quant_weights((0.05 * g.standard_normal(s)).astype(np.float32)) for s in ((2 * I, H), (H, I))]
+         for _ in range(E)]
+    W1, s1 = (np.stack([w[0][i] for w in W]) for i in (0, 1))
+    W2, s2 = (np.stack([w[1][i] for w in W]) for i in (0, 1))
+    return [A, sA, (2 * g.standard_normal((T, E))).astype(np.float32), W1, s1, W2, s2]
+
+
+def _check(ops, k, renormalise=True):
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    t = [dev(x) for x in ops]
+    D = torch.full((ops[0].shape[0], ops[0].shape[1]), float("nan"), dtype=torch.bfloat16, device="cuda")
+    D, ids, w = b.fp8_moe_few(*t, k, renormalise=renormalise, D=D)
+    out, rids, rw = layer.moe(*ops, k, renormalise)
+    assert np.array_equal(host(ids), rids)
+    assert np.all(np.abs(host(w) - rw) <= 2e-6 * rw + 1e-30)
+    assert_close(host(D), out, "moe")
+    D2, _, _ = b.fp8_moe_few(*t, k, renormalise=renormalise)
+    assert torch.equal(D, D2)
+    assert b.fp8gemm_get_device_status() == b.OK
+
+
+@pytest.mark.parametrize("T,H,I,E,k,renormalise", [
+    (1, 16, 16, 1, 1, True), (1, 128, 128, 4, 2, True), (1, 1040, 400, 9, 4, False), (2, 256, 144, 3, 3, True),
+    (7, 400, 208, 40, 8, True), (8, 512, 256, 2, 1, True), (9, 272, 528, 5, 2, False), (16, 256, 384, 6, 16 // 4, True),
+    (17, 144, 128, 1, 1, True), (33, 384, 256, 8, 2, True), (64, 256, 272, 4, 4, True), (64, 512, 128, 16, 2, True),
+    (3, 128, 64, 300, 16, False)])
+def test_moe(T, H, I, E, k, renormalise):
+    _check(_operands(T, H, I, E, seed=T + H + I + E), k, renormalise)
+
+
+def test_all_tokens_on_one_expert():
+    ops = _operands(64, 256, 256, 5, seed=1)
+    ops[2][:, 3] = 50
+    _check(ops, 1)
+
+
+def test_ties_bans_and_nan():
+    ops = _operands(6, 256, 128, 8, seed=2)
+    lg = ops[2]
+    lg[0] = 0                       # all tied
+    lg[1, :6] = -np.inf             # two left
+    lg[2, [1, 5]] = np.nan          # never chosen
+    lg[3] = 1e30
+    lg[4] = np.float32(-3e38)       # the type's lowest region, all tied
+    lg[5, 7] = 90
+    _check(ops, 2)
+
+
+def test_banned_experts_get_weight_zero():
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    ops = _operands(2, 128, 128, 4, seed=3)
+    ops[2][0, 1:] = -np.inf
+    ops[2][1] = -np.inf
+    D, ids, w = b.fp8_moe_few(*[dev(x) for x in ops], 3)
+    assert host(ids).tolist() == [[0, 1, 2], [0, 1, 2]]
+    assert host(w).tolist() == [[1, 0, 0], [0, 0, 0]]
+    assert np.isfinite(host(D)).all() and not host(D)[1].any()
+
+
+def test_matches_the_grouped_calls():
+    """The same layer out of the grouped GEMM, SwiGLU in torch and the quantiser."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    T, H, I, E = 24, 512, 256, 3
+    ops = _operands(T, H, I, E, seed=4)
+    A, sA, lg, W1, s1, W2, s2 = [dev(x) for x in ops]
+    D, ids, w = b.fp8_moe_few(A, sA, lg, W1, s1, W2, s2, 1)
+    mi = torch.full((E, 128), -1, dtype=torch.int32, device="cuda")
+    Ap = torch.zeros((E, 128, H), dtype=torch.uint8, device="cuda")
+    sp = torch.zeros((E, 128, H // 128), device="cuda")
+    for e in range(E):
+        t = torch.nonzero(ids[:, 0] == e).flatten()
+        mi[e, :len(t)] = e
+        Ap[e, :len(t)], sp[e, :len(t)] = A[t], sA[t]
+    u = b.fp8gemm_grouped_contiguous(Ap.view(-1, H), sp.view(-1, H // 128), W1, s1, mi.view(-1)).float()
+    h = torch.where(mi.view(-1, 1) >= 0, torch.nn.functional.silu(u[:, :I]) * u[:, I:], 0)
+    h8, sh = b.fp8_quant_1x128(h.contiguous())
+    y = b.fp8gemm_grouped_contiguous(h8, sh, W2, s2, mi.view(-1)).view(E, 128, H)
+    ref = torch.zeros((T, H), device="cuda")
+    for e in range(E):
+        t = torch.nonzero(ids[:, 0] == e).flatten()
+        ref[t] = y[e, :len(t)].float()
+    # the chain rounds u and y to BF16 on the way and re-rounds h to FP8: a few percent of a typical element
+    err = (D.float() - ref).norm() / ref.norm()
+    assert float(err) < 0.05
+
+
+def test_calls_back_to_back_on_two_streams():
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    a, c = (([dev(x) for x in _operands(T, 512, 256, 6, seed=T)]) for T in (3, 40))
+    want = [b.fp8_moe_few(*x, 2)[0] for x in (a, c)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(6):
+        got.append((i % 2, b.fp8_moe_few(*(a, c)[i % 2], 2, stream=streams[i // 2 % 2])[0]))
+    torch.cuda.synchronize()
+    for i, D in got:
+        assert torch.equal(D, want[i])
+    for s in streams:
+        b.fp8gemm_release_workspaces(s)
