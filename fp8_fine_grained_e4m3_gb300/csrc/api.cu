@@ -157,9 +157,10 @@ int finish(cudaError_t e, int nlaunch) {
 // Slot kWsBatch: the tile counters of the batched dense GEMM.  Slot
 // kWsContig: the tile counters and tile order of the contiguous form.
 // Slot kWsNorm: partial gain gradients of the norm.  Slot kWsMoe: routing and
-// hidden activations of the few-token MoE layer.
+// hidden activations of the few-token MoE layer.  Slot kWsAttention: counters
+// (left at zero) and partial results of the cache attention.
 enum { kWsSplitK = 0, kWsQuantA = 1, kWsTable = 2, kWsBatch = 3, kWsContig = 4, kWsNorm = 5,
-       kWsMoe = 6 };
+       kWsMoe = 6, kWsAttention = 7 };
 
 int workspace_for(cudaStream_t s, size_t bytes, void** out, int slot = kWsSplitK) {
   int dev = 0;
@@ -612,7 +613,9 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
                           v_scale, block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O),
                           scale, T, B, heads, group, dim, block, table_width, num_blocks, max_q,
                           fmt};
-  return finish(launch_kv_attention(c, a), 1);
+  void* ws = nullptr;
+  if (int r = workspace_for(stream, kv_attention_workspace_bytes(c, a), &ws, kWsAttention)) return r;
+  return finish(launch_kv_attention(c, a, ws), 1);
 }
 
 int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,

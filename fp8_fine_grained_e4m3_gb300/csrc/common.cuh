@@ -171,7 +171,8 @@ struct KvAttentionArgs {
   float scale;
   int T, B, heads, group, dim, block, width, num_blocks, max_q, fmt;
 };
-cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a);
+size_t kv_attention_workspace_bytes(const LaunchCtx& c, const KvAttentionArgs& a);
+cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws);
 
 // The mixture-of-experts layer for a few tokens (moe_few.cu).
 struct MoeArgs {
