@@ -578,25 +578,59 @@ def fp8gemm_dense_small_m_noalloc(A, sA, B, sB, D, stream=None):
     return D
 
 
-def _type(t, name):
-    """FP8GEMM_TYPE_* of an activation tensor."""
+# The decoder-layer calls below are short enough on the GPU for the host to be
+# what a caller waits for, so their checks take few attribute reads per tensor.
+def _raw_stream(stream, t):
+    """The stream handle as a number: the given one's, or the current one's."""
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float32:
-        return 1
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    try:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
 
 
-def _like(t, name, X):
-    """A tensor of X's shape and type."""
-    if t.dtype != X.dtype:
-        raise TypeError(f"{name} must be {X.dtype} as the other activations, got {t.dtype}")
-    return _need(t, name, X.numel(), X.shape[-1])
+def _addr(t, name, want, elems, last=None):
+    """Address of a tensor of the type(s) `want` with `elems` elements (in rows
+    of `last` when given); where it lies is checked by _resident."""
+    if t.dtype not in want:
+        raise TypeError(f"{name} must be {' or '.join(str(w) for w in want)}, got {t.dtype}")
+    if t.numel() != elems or (last is not None and elems > 0 and t.size(-1) != last):
+        _need(t, name, elems, last)
+    return t.data_ptr()
 
 
-def _opt(t, name):
-    return None if t is None else _ptr(t, name)
+def _resident(names, *tensors):
+    for i, t in enumerate(tensors):
+        if not (t.is_cuda and t.is_contiguous()):
+            _dev(t, names.split()[i])
+
+
+_TYPES = {}
+
+
+def _types():
+    """Types as _addr wants them (torch is imported on first use)."""
+    if not _TYPES:
+        torch = _torch()
+        _TYPES.update(
+            f32=(torch.float32,), i32=(torch.int32,), bf16=(torch.bfloat16,),
+            act={torch.bfloat16: 0, torch.float32: 1},  # FP8GEMM_TYPE_*
+            e4m3=(torch.uint8, torch.float8_e4m3fn), e5m2=(torch.uint8, torch.float8_e5m2))
+    return _TYPES
+
+
+def _f8_types(types, fmt):
+    _fmt(fmt)
+    return types[fmt]
+
+
+def _act(types, t, name):
+    kind = types["act"].get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return kind
 
 
 def fp8_rmsnorm_quant(X, gain, eps=1e-6, residual=None, fmt="e4m3", H=None, Q=None, sQ=None,
@@ -605,30 +639,36 @@ def fp8_rmsnorm_quant(X, gain, eps=1e-6, residual=None, fmt="e4m3", H=None, Q=No
     f32 [..., K], gain f32 [K] -> (Q u8 [..., K], sQ f32 [..., ceil(K/128)], H,
     rstd f32 [...]).  H is X + residual in X's type (X itself without one);
     H=residual updates the stream in place."""
-    torch = _torch()
-    kind = _type(X, "X")
-    K = X.shape[-1]
-    M = X.numel() // K if K else 0
-    _need(_f32(gain, "gain"), "gain", K)
+    torch, types = _torch(), _types()
+    f32, like, f8 = types["f32"], (X.dtype,), _f8_types(types, fmt)
+    kind = _act(types, X, "X")
+    K = X.size(-1)
+    n = X.numel()
+    M = n // K if K else 0
+    Kb = -(-K // 128)
+    g = _addr(gain, "gain", f32, K, K)
+    r = h = None
     if residual is not None:
-        _like(residual, "residual", X)
-        H = torch.empty_like(X) if H is None else _like(H, "H", X)
+        r = _addr(residual, "residual", like, n, K)
+        if H is None:
+            H = torch.empty_like(X)
+        h = _addr(H, "H", like, n, K)
+        _resident("residual H", residual, H)
     elif H is not None:
         raise ValueError("H is the sum with the residual: give residual too")
     if Q is None:
         Q = torch.empty(X.shape, dtype=torch.uint8, device=X.device)
     if sQ is None:
-        sQ = torch.empty((*X.shape[:-1], _cdiv(K, 128)), dtype=torch.float32, device=X.device)
+        sQ = torch.empty((*X.shape[:-1], Kb), dtype=torch.float32, device=X.device)
     if rstd is None:
         rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-    Qb = _need(_u8_fmt(Q, fmt, "Q"), "Q", M * K, K)
-    _need(_f32(sQ, "sQ"), "sQ", M * _cdiv(K, 128), _cdiv(K, 128))
-    _need(_f32(rstd, "rstd"), "rstd", M)
-    _check(lib().fp8_rmsnorm_quant(_ptr(X, "X"), _opt(residual, "residual"), kind,
-                                   _ptr(gain, "gain"), float(eps),
-                                   _opt(H, "H"), _ptr(Qb, "Q"), _ptr(sQ, "sQ"),
-                                   _ptr(rstd, "rstd"), M, K, FMT[fmt], _stream(stream)),
-           "fp8_rmsnorm_quant")
+    q, s = _addr(Q, "Q", f8, n, K), _addr(sQ, "sQ", f32, M * Kb, Kb)
+    d = _addr(rstd, "rstd", f32, M)
+    _resident("X gain Q sQ rstd", X, gain, Q, sQ, rstd)
+    rc = lib().fp8_rmsnorm_quant(X.data_ptr(), r, kind, g, eps, h, q, s, d, M, K, FMT[fmt],
+                                 _raw_stream(stream, X))
+    if rc:
+        _check(rc, "fp8_rmsnorm_quant")
     return Q, sQ, (X if residual is None else H), rstd
 
 
@@ -636,23 +676,29 @@ def fp8_rmsnorm_backward(dY, H, rstd, gain, dH=None, dX=None, dgain=None, stream
     """Gradients of fp8_rmsnorm_quant's norm (straight through the quantiser):
     dY and H bf16 or f32 [..., K], rstd f32 [...], gain f32 [K], dH (the
     gradient that reaches H past the norm) as dY or None -> (dX, dgain f32 [K])."""
-    torch = _torch()
-    kind = _type(H, "H")
-    K = H.shape[-1]
-    M = H.numel() // K if K else 0
-    _like(dY, "dY", H)
+    torch, types = _torch(), _types()
+    f32, like = types["f32"], (H.dtype,)
+    kind = _act(types, H, "H")
+    K = H.size(-1)
+    n = H.numel()
+    M = n // K if K else 0
+    y = _addr(dY, "dY", like, n, K)
+    up = None
     if dH is not None:
-        _like(dH, "dH", H)
-    dX = torch.empty_like(H) if dX is None else _like(dX, "dX", H)
+        up = _addr(dH, "dH", like, n, K)
+        _resident("dH", dH)
+    if dX is None:
+        dX = torch.empty_like(H)
     if dgain is None:
         dgain = torch.empty(K, dtype=torch.float32, device=H.device)
-    _need(_f32(rstd, "rstd"), "rstd", M)
-    _need(_f32(gain, "gain"), "gain", K)
-    _need(_f32(dgain, "dgain"), "dgain", K)
-    _check(lib().fp8_rmsnorm_backward(_ptr(dY, "dY"), _ptr(H, "H"), kind, _ptr(rstd, "rstd"),
-                                      _ptr(gain, "gain"), _opt(dH, "dH"), _ptr(dX, "dX"),
-                                      _ptr(dgain, "dgain"), M, K, _stream(stream)),
-           "fp8_rmsnorm_backward")
+    x = _addr(dX, "dX", like, n, K)
+    d = _addr(rstd, "rstd", f32, M)
+    g, dg = _addr(gain, "gain", f32, K, K), _addr(dgain, "dgain", f32, K, K)
+    _resident("dY H rstd gain dX dgain", dY, H, rstd, gain, dX, dgain)
+    rc = lib().fp8_rmsnorm_backward(y, H.data_ptr(), kind, d, g, up, x, dg, M, K,
+                                    _raw_stream(stream, H))
+    if rc:
+        _check(rc, "fp8_rmsnorm_backward")
     return dX, dgain
 
 
@@ -660,36 +706,46 @@ def _tokens(t, name, heads, dim):
     """bf16 [T, heads, dim] whose tokens may lie apart (parts of the rows of a
     fused projection's output): returns the token stride in elements."""
     _bf16(t, name)
+    if t.dim() != 3 or t.size(1) != heads or t.size(2) != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [T, {heads}, {dim}]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [T, {heads}, {dim}]")
     ld, sh, sd = t.stride()
-    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
+    if sd != 1 or (heads > 1 and sh != dim):
         raise ValueError(f"{name} must hold each token's heads contiguously")
-    return ld if t.shape[0] > 1 else heads * dim
+    return ld if t.size(0) > 1 else heads * dim
 
 
-def _cache(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T, fmt):
-    """Sizes of a paged cache and its index arrays: (codes k, codes v, blocks,
-    heads, block, dim, B, table width)."""
-    k, v = _u8_fmt(k_cache, fmt, "k_cache"), _u8_fmt(v_cache, fmt, "v_cache")
-    if k.dim() != 4 or v.shape != k.shape:
-        raise ValueError(f"k_cache {tuple(k.shape)} / v_cache {tuple(v.shape)}: the call needs"
-                         " [num_blocks, heads, block, dim] twice")
-    n, heads, block, dim = k.shape
-    _need(_f32(k_scale, "k_scale"), "k_scale", n * heads)
-    _need(_f32(v_scale, "v_scale"), "v_scale", n * heads)
-    if _i32(block_table, "block_table").dim() != 2:
+def _cache(types, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T, fmt):
+    """Checks a paged cache and its index arrays: ((addresses), blocks, heads,
+    block, dim, B, table width)."""
+    f8, f32, i32 = _f8_types(types, fmt), types["f32"], types["i32"]
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache {tuple(k_cache.shape)} / v_cache {tuple(v_cache.shape)}: the"
+                         " call needs [num_blocks, heads, block, dim] twice")
+    n, heads, block, dim = k_cache.shape
+    if block_table.dim() != 2:
         raise ValueError(f"block_table has shape {tuple(block_table.shape)}; the call needs"
                          " [B, table_width]")
     B, width = block_table.shape
-    _need(_i32(seq_lens, "seq_lens"), "seq_lens", B)
-    if cu is not None:
-        _need(_i32(cu, "the offsets"), "the offsets", B + 1)
-    elif B > 0 and T % B != 0:
+    if cu is None and B > 0 and T % B != 0:
         raise ValueError(f"{T} tokens for {B} sequences: give the offsets")
-    return k, v, n, heads, block, dim, B, width
+    size = n * heads * block * dim
+    at = (_addr(k_cache, "k_cache", f8, size, dim),
+          _addr(k_scale, "k_scale", f32, n * heads),
+          _addr(v_cache, "v_cache", f8, size, dim),
+          _addr(v_scale, "v_scale", f32, n * heads),
+          _addr(block_table, "block_table", i32, B * width, width),
+          _addr(seq_lens, "seq_lens", i32, B, B),
+          None if cu is None else _addr(cu, "the offsets", i32, B + 1, B + 1))
+    return at, n, heads, block, dim, B, width
+
+
+def _cache_resident(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu):
+    _resident("k_cache k_scale v_cache v_scale block_table seq_lens", k_cache, k_scale, v_cache,
+              v_scale, block_table, seq_lens)
+    if cu is not None:
+        _resident("cu", cu)
 
 
 def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_new=None,
@@ -699,20 +755,19 @@ def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
     f32 [num_blocks, heads]), at the end of each sequence: seq_lens i32 [B]
     counts them already.  cu_new i32 [B + 1] are the offsets of each sequence's
     tokens (None: T / B each); max_new bounds a sequence's (None: T)."""
-    T = K.shape[0]
-    kc, vc, n, heads, block, dim, B, width = _cache(k_cache, k_scale, v_cache, v_scale,
-                                                    block_table, seq_lens, cu_new, T, fmt)
+    T = K.size(0)
+    at, n, heads, block, dim, B, width = _cache(_types(), k_cache, k_scale, v_cache, v_scale,
+                                                block_table, seq_lens, cu_new, T, fmt)
+    if V.size(0) != T:
+        raise ValueError(f"K holds {T} tokens, V {V.size(0)}")
     ld_k, ld_v = _tokens(K, "K", heads, dim), _tokens(V, "V", heads, dim)
-    if V.shape[0] != T:
-        raise ValueError(f"K holds {T} tokens, V {V.shape[0]}")
+    _cache_resident(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_new)
     if max_new is None:
-        max_new = T if cu_new is not None else _cdiv(T, max(B, 1))
-    _check(lib().fp8_kv_append(K.data_ptr(), V.data_ptr(), ld_k, ld_v,
-                               _ptr(kc, "k_cache"), _ptr(k_scale, "k_scale"),
-                               _ptr(vc, "v_cache"), _ptr(v_scale, "v_scale"),
-                               _ptr(block_table, "block_table"), _ptr(seq_lens, "seq_lens"),
-                               _opt(cu_new, "cu_new"), T, B, heads, dim, block, width, n,
-                               int(max_new), FMT[fmt], _stream(stream)), "fp8_kv_append")
+        max_new = T if cu_new is not None else -(-T // max(B, 1))
+    rc = lib().fp8_kv_append(K.data_ptr(), V.data_ptr(), ld_k, ld_v, *at, T, B, heads, dim, block,
+                             width, n, max_new, FMT[fmt], _raw_stream(stream, K))
+    if rc:
+        _check(rc, "fp8_kv_append")
 
 
 def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q=None,
@@ -721,28 +776,28 @@ def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
     may lie apart) over the paged FP8 cache that holds their keys and values
     already -> O bf16 [T, heads * group, dim].  cu_q and max_q as
     fp8_kv_append's; scale defaults to dim ** -0.5."""
-    torch = _torch()
-    T = Q.shape[0]
-    kc, vc, n, heads, block, dim, B, width = _cache(k_cache, k_scale, v_cache, v_scale,
-                                                    block_table, seq_lens, cu_q, T, fmt)
-    if Q.dim() != 3 or heads == 0 or Q.shape[1] % heads != 0:
+    types = _types()
+    T = Q.size(0)
+    at, n, heads, block, dim, B, width = _cache(types, k_cache, k_scale, v_cache, v_scale,
+                                                block_table, seq_lens, cu_q, T, fmt)
+    if Q.dim() != 3 or heads == 0 or Q.size(1) % heads != 0:
         raise ValueError(f"Q has shape {tuple(Q.shape)}; the call needs [T, heads * group, dim]"
                          f" with {heads} cached heads")
-    group = Q.shape[1] // heads
-    ld_q = _tokens(Q, "Q", heads * group, dim)
+    hq = Q.size(1)
+    ld_q = _tokens(Q, "Q", hq, dim)
     if O is None:
-        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
-    _need(_bf16(O, "O"), "O", T * heads * group * dim, dim)
+        O = _torch().empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    o = _addr(O, "O", types["bf16"], T * hq * dim, dim)
+    _resident("O", O)
+    _cache_resident(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q)
     if max_q is None:
-        max_q = T if cu_q is not None else _cdiv(T, max(B, 1))
+        max_q = T if cu_q is not None else -(-T // max(B, 1))
     if scale is None:
         scale = dim ** -0.5
-    _check(lib().fp8_kv_attention(Q.data_ptr(), ld_q, _ptr(kc, "k_cache"),
-                                  _ptr(k_scale, "k_scale"), _ptr(vc, "v_cache"),
-                                  _ptr(v_scale, "v_scale"), _ptr(block_table, "block_table"),
-                                  _ptr(seq_lens, "seq_lens"), _opt(cu_q, "cu_q"), float(scale),
-                                  _ptr(O, "O"), T, B, heads, group, dim, block, width, n,
-                                  int(max_q), FMT[fmt], _stream(stream)), "fp8_kv_attention")
+    rc = lib().fp8_kv_attention(Q.data_ptr(), ld_q, *at, scale, o, T, B, heads, hq // heads, dim,
+                                block, width, n, max_q, FMT[fmt], _raw_stream(stream, Q))
+    if rc:
+        _check(rc, "fp8_kv_attention")
     return O
 
 
@@ -752,35 +807,34 @@ def fp8_moe_few(A, sA, logits, W1, s1, W2, s2, top_k, renormalise=True, D=None, 
     [T, ceil(H/128)], logits f32 [T, E], W1 u8 [E, 2 I, H] (gate rows, then up
     rows), W2 u8 [E, H, I] with their 128x128 scales -> (D bf16 [T, H], ids i32
     [T, top_k], weights f32 [T, top_k])."""
-    torch = _torch()
-    A, W1, W2 = _u8(A, "A"), _u8(W1, "W1"), _u8(W2, "W2")
+    torch, types = _torch(), _types()
+    f8, f32 = types["e4m3"], types["f32"]
     if A.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
         raise ValueError(f"A {tuple(A.shape)} / W1 {tuple(W1.shape)} / W2 {tuple(W2.shape)}: the"
                          " call needs [T, H], [E, 2 I, H] and [E, H, I]")
     T, H = A.shape
-    E, I2, _ = W1.shape
+    E, I2, Hw = W1.shape
     I = I2 // 2
-    if W1.shape != (E, 2 * I, H) or W2.shape != (E, H, I):
+    if I2 != 2 * I or Hw != H or W2.shape != (E, H, I):
         raise ValueError(f"W1 {tuple(W1.shape)} / W2 {tuple(W2.shape)}: the call needs"
                          f" [E, 2 I, {H}] and [E, {H}, I]")
-    Hb, k = _cdiv(H, 128), int(top_k)
-    _need(_f32(sA, "sA"), "sA", T * Hb, Hb)
-    _need(_f32(logits, "logits"), "logits", T * E, E)
-    _need(_f32(s1, "s1"), "s1", E * _cdiv(2 * I, 128) * Hb, Hb)
-    _need(_f32(s2, "s2"), "s2", E * Hb * _cdiv(I, 128), _cdiv(I, 128))
+    Hb, Ib, k = -(-H // 128), -(-I // 128), int(top_k)
+    at = (_addr(A, "A", f8, T * H, H), _addr(sA, "sA", f32, T * Hb, Hb),
+          _addr(logits, "logits", f32, T * E, E), _addr(W1, "W1", f8, E * I2 * H, H),
+          _addr(s1, "s1", f32, E * -(-I2 // 128) * Hb, Hb), _addr(W2, "W2", f8, E * H * I, I),
+          _addr(s2, "s2", f32, E * Hb * Ib, Ib))
     if D is None:
         D = torch.empty((T, H), dtype=torch.bfloat16, device=A.device)
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=A.device)
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=A.device)
-    _need(_bf16(D, "D"), "D", T * H, H)
-    _need(_i32(ids, "ids"), "ids", T * k, k)
-    _need(_f32(weights, "weights"), "weights", T * k, k)
-    _check(lib().fp8_moe_few(_ptr(A, "A"), _ptr(sA, "sA"), _ptr(logits, "logits"), _ptr(W1, "W1"),
-                             _ptr(s1, "s1"), _ptr(W2, "W2"), _ptr(s2, "s2"), _ptr(D, "D"),
-                             _ptr(ids, "ids"), _ptr(weights, "weights"), T, H, I, E, k,
-                             int(bool(renormalise)), _stream(stream)), "fp8_moe_few")
+    out = (_addr(D, "D", types["bf16"], T * H, H), _addr(ids, "ids", types["i32"], T * k, k),
+           _addr(weights, "weights", f32, T * k, k))
+    _resident("A sA logits W1 s1 W2 s2 D ids weights", A, sA, logits, W1, s1, W2, s2, D, ids, weights)
+    rc = lib().fp8_moe_few(*at, *out, T, H, I, E, k, 1 if renormalise else 0, _raw_stream(stream, A))
+    if rc:
+        _check(rc, "fp8_moe_few")
     return D, ids, weights
 
 
