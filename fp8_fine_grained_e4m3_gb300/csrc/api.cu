@@ -95,6 +95,17 @@ unsigned long long current_context_id() {
   return id;
 }
 
+cudaError_t SmemLimit::raise(const void* fn, size_t bytes) {
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const unsigned long long ctx = current_context_id();
+  if (ctx != 0 && set_in[dev & 63] == ctx) return cudaSuccess;
+  if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)))
+    return e;
+  set_in[dev & 63] = ctx;
+  return cudaSuccess;
+}
+
 namespace {
 
 // Looks up (once per device and context) the SM count, compute capability
@@ -612,7 +623,7 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
   const KvAttentionArgs a{static_cast<const __nv_bfloat16*>(Q), ld_q, k_cache, k_scale, v_cache,
                           v_scale, block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O),
                           scale, T, B, heads, group, dim, block, table_width, num_blocks, max_q,
-                          fmt};
+                          fmt, block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7};
   void* ws = nullptr;
   if (int r = workspace_for(stream, kv_attention_workspace_bytes(c, a), &ws, kWsAttention)) return r;
   return finish(launch_kv_attention(c, a, ws), 1);

@@ -170,6 +170,7 @@ struct KvAttentionArgs {
   __nv_bfloat16* O;  // [T, heads * group, dim]
   float scale;
   int T, B, heads, group, dim, block, width, num_blocks, max_q, fmt;
+  int log_block;
 };
 size_t kv_attention_workspace_bytes(const LaunchCtx& c, const KvAttentionArgs& a);
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws);
@@ -190,6 +191,13 @@ struct MoeArgs {
 };
 size_t moe_few_workspace_bytes(const MoeArgs& a);
 cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace, int* launches);
+
+// Raises a kernel's dynamic shared memory limit, once per device and CUDA context
+// (the attribute belongs to the function in one context).
+struct SmemLimit {
+  unsigned long long set_in[64] = {};  // context id, per device
+  cudaError_t raise(const void* fn, size_t bytes);
+};
 
 // Fills `c` for the current device and `stream` (SM count, status word);
 // returns an fp8gemm_status code.  Defined in api.cu.

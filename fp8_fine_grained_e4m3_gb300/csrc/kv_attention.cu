@@ -7,9 +7,10 @@
 // (its own among them); a row that sees none gives zeros.  Query heads h g ..
 // h g + g - 1 read the cached head h, so their rows share every byte of it.
 //
-// Bound by the cache's bytes: each is read once and straight into the
-// registers of the tensor-core fragment it belongs to, with no pass through
-// shared memory.  Both products are taken transposed so that tokens (and the
+// Bound by the cache's bytes: each is read once, by the lane whose tensor-core
+// fragment it belongs to.  A lane's share of the tiles ahead waits in shared memory
+// that no other lane touches (cp.async, then its own wait: no barrier, no bank
+// conflict, and bytes in flight that cost no registers).  Both products are taken transposed so that tokens (and the
 // head's dimension) fill the 16-row side of m16n8k16 and 8 query rows the other:
 //   S^T [16 tokens, 8 rows] = K [16, dim] Q^T      O^T [dim, 8 rows] += V^T [dim, 16] P^T
 // The order of a contraction is free, so the dimension is dealt to the
@@ -32,6 +33,7 @@ constexpr int kRows = 8;   // query rows per fragment
 constexpr int kWarps = 4;
 constexpr int kUnit = kWarps * kTok;  // tokens of a unit: a tile for each warp
 constexpr int kMinUnits = 4;  // a CTA's least share: fewer would cost more to join than to do
+constexpr int kStages = 4;  // tiles of a warp in shared memory
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -55,64 +57,62 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Cache bytes: read once, so not kept in L1.
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 2^x to FP32's rounding (relative error 2^-22).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-__device__ __forceinline__ uint2 ld_stream8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t src_bytes) {
+  if constexpr (kBytes == 16)
+    cp_async_16(dst, src, src_bytes);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+                 "r"(src_bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A lane's share of 16 tokens of one head.  With lane = 4 g + t:
 //   keys    tokens g and g + 8, bytes 64 c + 16 t .. + 15
 //   values  tokens 2t, 2t + 1, 2t + 8, 2t + 9, bytes (dim / 8) g .. + dim / 8 - 1
+// In a stage each of these pieces is one row of 32 lanes.
 template <int kDim>
-struct Tile {
-  uint32_t k[2][kDim / 64][4];
-  uint32_t v[4][kDim / 32];
-  float ks, vs;
-  bool there;
+struct Stage {
+  uint4 k[2][kDim / 64][32];
+  uint32_t v[4][32][kDim / 32];
+  float ks[32], vs[32];
 };
 
-// Tokens at and past `valid` read as zeros, whatever the cache holds there.
+// Asks for a tile: kv is the lane's byte offset of it in the codes, tile that
+// of its scales.  Tokens at and past `valid` (16 and more: all there) become
+// zeros, whatever the cache holds there.
 template <int kDim>
-__device__ __forceinline__ void load_tile(Tile<kDim>& x, const uint8_t* k, const uint8_t* v,
-                                          int valid, int g, int t) {
+__device__ __forceinline__ void fetch_tile(Stage<kDim>& s, const KvAttentionArgs& a, size_t at,
+                                           size_t tile, int valid, int lane) {
+  const int g = lane / 4, t = lane % 4;
+  const uint8_t* k = a.kc + at + g * kDim + 16 * t;
+  const uint8_t* v = a.vc + at + 2 * t * kDim + g * (kDim / 8);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int c = 0; c < kDim / 64; ++c) {
-      uint4 r = make_uint4(0, 0, 0, 0);
-      if (g + 8 * i < valid) r = ld_stream16(k + (g + 8 * i) * kDim + 64 * c + 16 * t);
-      x.k[i][c][0] = r.x;
-      x.k[i][c][1] = r.y;
-      x.k[i][c][2] = r.z;
-      x.k[i][c][3] = r.w;
-    }
+    for (int c = 0; c < kDim / 64; ++c)
+      copy_async<16>(smem_addr(&s.k[i][c][lane]), k + 8 * i * kDim + 64 * c,
+                     g + 8 * i < valid ? 16u : 0u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
-    const uint8_t* p = v + tok * kDim + g * (kDim / 8);
-    if constexpr (kDim == 128) {
-      uint4 r = make_uint4(0, 0, 0, 0);
-      if (tok < valid) r = ld_stream16(p);
-      x.v[i][0] = r.x;
-      x.v[i][1] = r.y;
-      x.v[i][2] = r.z;
-      x.v[i][3] = r.w;
-    } else {
-      uint2 r = make_uint2(0, 0);
-      if (tok < valid) r = ld_stream8(p);
-      x.v[i][0] = r.x;
-      x.v[i][1] = r.y;
-    }
+    const int tok = (i & 1) + 8 * (i >> 1);
+    copy_async<kDim / 8>(smem_addr(&s.v[i][lane][0]), v + tok * kDim,
+                         2 * t + tok < valid ? uint32_t(kDim / 8) : 0u);
   }
+  copy_async<4>(smem_addr(&s.ks[lane]), a.ks + tile, 4u);
+  copy_async<4>(smem_addr(&s.vs[lane]), a.vs + tile, 4u);
 }
 
 // The queries of 8 rows as the k16 x n8 fragments that match Tile's keys, and
@@ -161,8 +161,9 @@ __device__ __forceinline__ void load_queries(Queries<kDim>& q, const __nv_bfloat
   q.mul[1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
 }
 
-// Running softmax of a lane's two rows and its share of O^T: o[j] holds
-// dimensions (dim/8) g + 2j (rows 2t, 2t + 1) and + 1 (rows 2t, 2t + 1).
+// Running softmax of a lane's two rows and its share of O^T in units of the
+// warp's value scale: o[j] holds dimensions (dim/8) g + 2j (rows 2t, 2t + 1)
+// and + 1 (rows 2t, 2t + 1).
 template <int kDim>
 struct State {
   float m[2], l[2];  // l: this lane's tokens only
@@ -179,68 +180,125 @@ __device__ __forceinline__ void clear(State<kDim>& s) {
     for (int e = 0; e < 4; ++e) s.o[j][e] = 0.f;
 }
 
-// One tile; sees[r]: how many of its tokens the lane's row r sees (may be
-// negative or past 16).
-template <int kDim, bool kE5M2>
-__device__ __forceinline__ void attend_tile(State<kDim>& s, const Tile<kDim>& x,
-                                            const Queries<kDim>& q, const int (&sees)[2], int g) {
-  float c[4] = {0.f, 0.f, 0.f, 0.f};
+// p is brought to the units of O by vs / unit before it is rounded to FP16.
+// The unit follows the tiles' scales so that this stays in (2^-6, 1]; tiles whose
+// scale is 2^60 below the largest met leave it.
+constexpr float kUnitLow = 1.f / 64, kUnitFar = 1152921504606846976.f;
+
+// One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
+// fragment i sees (may be negative or past 16).
+template <int kDim, bool kE5M2, int kNR>
+__device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
+                                            const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
+                                            const int (&limit)[kNR][2], int tok, int lane) {
+  const int g = lane / 4;
+  float c[kNR][4] = {};
 #pragma unroll
-  for (int ks = 0; ks < kDim / 16; ++ks) {
-    const uint32_t k0 = x.k[0][ks / 4][ks % 4], k1 = x.k[1][ks / 4][ks % 4];
-    const uint32_t a[4] = {f8x2_to_f16x2<kE5M2>(uint16_t(k0)), f8x2_to_f16x2<kE5M2>(uint16_t(k1)),
-                           f8x2_to_f16x2<kE5M2>(uint16_t(k0 >> 16)),
-                           f8x2_to_f16x2<kE5M2>(uint16_t(k1 >> 16))};
-    mma_f16(c, a, q.b[ks][0], q.b[ks][1]);
-  }
-  // scores in powers of two; element 2i + r: token g + 8i, row r
+  for (int cc = 0; cc < kDim / 64; ++cc) {
+    const uint4 r0 = x.k[0][cc][lane], r1 = x.k[1][cc][lane];
+    const uint32_t k0[4] = {r0.x, r0.y, r0.z, r0.w}, k1[4] = {r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    c[e] = c[e] * (q.mul[e & 1] * x.ks);
-    if (g + 8 * (e >> 1) >= sees[e & 1]) c[e] = -INFINITY;
-  }
-  const float top0 = fmaxf(c[0], c[2]), top1 = fmaxf(c[1], c[3]);
-  if (__any_sync(0xffffffffu, top0 > s.m[0] + kLazy || top1 > s.m[1] + kLazy)) {
-    float top[2] = {top0, top1};
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t a[4] = {
+          f8x2_to_f16x2<kE5M2>(uint16_t(k0[w])), f8x2_to_f16x2<kE5M2>(uint16_t(k1[w])),
+          f8x2_to_f16x2<kE5M2>(uint16_t(k0[w] >> 16)), f8x2_to_f16x2<kE5M2>(uint16_t(k1[w] >> 16))};
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
-      const float m = fmaxf(s.m[r], top[r]);
-      const float shrink = m == -INFINITY ? 1.f : exp2f(s.m[r] - m);
-      s.m[r] = m;
-      s.l[r] *= shrink;
-#pragma unroll
-      for (int j = 0; j < kDim / 16; ++j) {
-        s.o[j][r] *= shrink;
-        s.o[j][2 + r] *= shrink;
-      }
+      for (int i = 0; i < kNR; ++i) mma_f16(c[i], a, q[i].b[4 * cc + w][0], q[i].b[4 * cc + w][1]);
     }
   }
+  const float ks = x.ks[lane], vs = x.vs[lane];
+  // scores in powers of two; element 2h + r: token g + 8h, row r
+  bool rises = false;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float m = s.m[e & 1];
-    c[e] = exp2f(c[e] - (m == -INFINITY ? 0.f : m));
-    s.l[e & 1] += c[e];
+  for (int i = 0; i < kNR; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[i][e] = c[i][e] * (q[i].mul[e & 1] * ks);
+      if (g + 8 * (e >> 1) + tok >= limit[i][e & 1]) c[i][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) rises |= fmaxf(c[i][r], c[i][2 + r]) > s[i].m[r] + kLazy;
   }
-  const uint32_t b0 = transpose8x8(f16x2_bits(c[0], c[1]));
-  const uint32_t b1 = transpose8x8(f16x2_bits(c[2], c[3]));
+  if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+    for (int i = 0; i < kNR; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float top = fmaxf(c[i][r], c[i][2 + r]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m = fmaxf(s[i].m[r], top);
+        const float shrink = m == -INFINITY ? 1.f : exp2_fast(s[i].m[r] - m);
+        s[i].m[r] = m;
+        s[i].l[r] *= shrink;
+#pragma unroll
+        for (int j = 0; j < kDim / 16; ++j) {
+          s[i].o[j][r] *= shrink;
+          s[i].o[j][2 + r] *= shrink;
+        }
+      }
+  }
+  float to_unit = 1.f;
+  if (vs != unit) {  // the warp's tiles of one block share it
+    if (vs > unit || (vs < kUnitLow * unit && vs * kUnitFar > unit)) {
+      const float grow = __fdiv_rn(unit, vs);
+#pragma unroll
+      for (int i = 0; i < kNR; ++i)
+#pragma unroll
+        for (int j = 0; j < kDim / 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[i].o[j][e] *= grow;
+      unit = vs;
+    } else {
+      to_unit = __fdiv_rn(vs, unit);
+    }
+  }
+  uint32_t b[kNR][2];
+#pragma unroll
+  for (int i = 0; i < kNR; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float m = s[i].m[e & 1];
+      c[i][e] = exp2_fast(c[i][e] - (m == -INFINITY ? 0.f : m));
+      s[i].l[e & 1] += c[i][e];
+      c[i][e] *= to_unit;
+    }
+    b[i][0] = transpose8x8(f16x2_bits(c[i][0], c[i][1]));
+    b[i][1] = transpose8x8(f16x2_bits(c[i][2], c[i][3]));
+  }
+  uint32_t v[4][kDim / 32];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    if constexpr (kDim == 128) {
+      const uint4 r = *reinterpret_cast<const uint4*>(&x.v[h][lane][0]);
+      v[h][0] = r.x;
+      v[h][1] = r.y;
+      v[h][2] = r.z;
+      v[h][3] = r.w;
+    } else {
+      const uint2 r = *reinterpret_cast<const uint2*>(&x.v[h][lane][0]);
+      v[h][0] = r.x;
+      v[h][1] = r.y;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < kDim / 16; ++j) {
     // bytes 2j and 2j + 1 of the four tokens: one matrix row each
     const uint32_t pick = (j & 1) ? 0x7362 : 0x5140;
-    const uint32_t lo = __byte_perm(x.v[0][j / 2], x.v[1][j / 2], pick);
-    const uint32_t hi = __byte_perm(x.v[2][j / 2], x.v[3][j / 2], pick);
+    const uint32_t lo = __byte_perm(v[0][j / 2], v[1][j / 2], pick);
+    const uint32_t hi = __byte_perm(v[2][j / 2], v[3][j / 2], pick);
     const uint32_t a[4] = {f8x2_to_f16x2<kE5M2>(uint16_t(lo)),
                            f8x2_to_f16x2<kE5M2>(uint16_t(lo >> 16)),
                            f8x2_to_f16x2<kE5M2>(uint16_t(hi)),
                            f8x2_to_f16x2<kE5M2>(uint16_t(hi >> 16))};
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_f16(d, a, b0, b1);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s.o[j][e] = fmaf(d[e], x.vs, s.o[j][e]);
+    for (int i = 0; i < kNR; ++i) mma_f16(s[i].o[j], a, b[i][0], b[i][1]);
   }
 }
+
+// CTAs that fit on an SM: by shared memory at dim 128, by registers at dim 64.
+constexpr int kMaxPerSm = 4;
+constexpr int ctas_per_sm(int dim, int fragments) { return dim == 64 && fragments == 1 ? kMaxPerSm : 3; }
 
 __device__ __forceinline__ void add_scaled(float4& o, float& l, const float* v, float vl, float f) {
   l = fmaf(f, vl, l);
@@ -265,18 +323,13 @@ __device__ __forceinline__ void write_out(const KvAttentionArgs& a, int t0, int 
 // as often where a sequence may have more than 8 rows per cached head.
 int row_fragments(const KvAttentionArgs& a) { return (long long)a.max_q * a.group > kRows ? 2 : 1; }
 
-// CTAs that fit on an SM by their registers (168 a thread at dim 128 and one
-// fragment, 255 with two; 128 and 168 at dim 64).
-constexpr int kMaxPerSm = 4;
-int ctas_per_sm(const KvAttentionArgs& a) { return (a.dim == 64 ? 4 : 3) - (row_fragments(a) - 1); }
-
 // CTAs: as many as run at once, or fewer where the tables cannot hold that much work.
 int attention_grid(const LaunchCtx& c, const KvAttentionArgs& a) {
   const long long row_tiles = ((long long)a.max_q * a.group + kRows * row_fragments(a) - 1) /
                               (kRows * row_fragments(a));
   const long long units = max(1LL, ((long long)a.width * a.block + kUnit - 1) / kUnit);
   const long long most = (row_tiles * a.heads * a.B * units + kMinUnits - 1) / kMinUnits;
-  return int(min(most, (long long)ctas_per_sm(a) * c.num_sms));
+  return int(min(most, (long long)ctas_per_sm(a.dim, row_fragments(a)) * c.num_sms));
 }
 
 // The counters' place does not depend on the call: what one call leaves there
@@ -331,17 +384,19 @@ struct Partial {
 //   slot 2c + 1  of an item that begins in its run and goes on
 //   counter c    CTAs done with the item that goes on past CTA c's run (left at 0)
 template <int kDim, bool kE5M2, int kNR>
-__global__ void __launch_bounds__(32 * kWarps) kv_attention_kernel(const KvAttentionArgs a,
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attention_kernel(const KvAttentionArgs a,
                                                                    int* counters,
                                                                    Partial<kDim, kNR>* parts,
                                                                    int* status) {
   constexpr int kR = kRows * kNR;
-  __shared__ float so[kWarps][kR][kDim + 4];
+  extern __shared__ __align__(16) unsigned char shared[];
+  float (*so)[kR][kDim + 4] = reinterpret_cast<float (*)[kR][kDim + 4]>(shared);
   __shared__ float sm[kWarps][kR], sl[kWarps][kR];
   __shared__ long long scan[kWarps];
   __shared__ Place place;
   __shared__ int last_one;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  Stage<kDim>* ring = reinterpret_cast<Stage<kDim>*>(shared) + warp * kStages;
 
   // all units, and each thread's share of the sequences
   const int per_thread = ceil_div(a.B, 32 * kWarps);
@@ -410,36 +465,40 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attention_kernel(const KvAtten
       }
       clear(s[i]);
     }
-    // two tiles in flight: the next one's bytes are asked for before this one is used
-    Tile<kDim> x[2];
-    auto fetch = [&](Tile<kDim>& d, int unit) {
-      const int tok = unit * kUnit + warp * kTok;
-      const int blk = tok < len ? a.table[size_t(b) * a.width + tok / a.block] : -1;
-      const bool there = blk >= 0 && blk < a.num_blocks;
-      if (tok < len && !there && lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-      const size_t tile = there ? size_t(blk) * a.heads + head : 0;
-      const size_t at = there ? (tile * a.block + tok % a.block) * kDim : 0;
-      load_tile<kDim>(d, a.kc + at, a.vc + at, there ? len - tok : 0, g, t);
-      d.ks = there ? a.ks[tile] : 0.f;
-      d.vs = there ? a.vs[tile] : 0.f;
-      d.there = there;
+    // kStages - 1 tiles in flight; the table entry of the next one to ask for
+    // is read a step before
+    float unit = 0.f;
+    const int* table = a.table + size_t(b) * a.width;
+    auto entry = [&](int i) {
+      const int tok = i * kUnit + warp * kTok;
+      return i < s1 && tok < len ? table[tok >> a.log_block] : -1;
     };
-    auto use = [&](const Tile<kDim>& d, int unit) {
-      if (!d.there) return;  // past the end, or a bad table entry: counts as not there
-      const int tok = unit * kUnit + warp * kTok;
-#pragma unroll
-      for (int i = 0; i < kNR; ++i) {
-        const int sees[2] = {limit[i][0] - tok, limit[i][1] - tok};
-        attend_tile<kDim, kE5M2>(s[i], d, q[i], sees, g);
+    int next = entry(s0);
+    uint32_t there = 0;  // bit i % 32: the tile of unit i is in its stage
+    auto fetch = [&](int i) {
+      const int tok = i * kUnit + warp * kTok, blk = next;
+      next = entry(i + 1);
+      const bool ok = blk >= 0 && blk < a.num_blocks;
+      if (ok) {
+        const size_t tile = size_t(blk) * a.heads + head;
+        fetch_tile<kDim>(ring[i % kStages], a,
+                         ((tile << a.log_block) + (tok & (a.block - 1))) * kDim, tile, len - tok, lane);
+      } else if (i < s1 && tok < len && lane == 0) {
+        raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
       }
+      there = (there & ~(1u << i % 32)) | uint32_t(ok) << i % 32;
+      copy_commit();
     };
-    fetch(x[0], s0);
-    for (int i = s0; i < s1; i += 2) {
-      if (i + 1 < s1) fetch(x[1], i + 1);
-      use(x[0], i);
-      if (i + 2 < s1) fetch(x[0], i + 2);
-      if (i + 1 < s1) use(x[1], i + 1);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(s0 + i);
+    for (int i = s0; i < s1; ++i) {
+      copy_wait<kStages - 2>();
+      if (there >> i % 32 & 1)  // else past the end, or a bad table entry: not there
+        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[i % kStages], q, limit, i * kUnit + warp * kTok, lane);
+      fetch(i + kStages - 1);  // into the stage that was used last, by the lanes that read it
     }
+    copy_wait<0>();
+    __syncthreads();  // the rings become the place to join the warps' results
 
 #pragma unroll
     for (int i = 0; i < kNR; ++i)
@@ -455,7 +514,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attention_kernel(const KvAtten
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j)
           *reinterpret_cast<float2*>(&so[warp][row][g * (kDim / 8) + 2 * j]) =
-              make_float2(s[i].o[j][r], s[i].o[j][2 + r]);
+              make_float2(s[i].o[j][r] * unit, s[i].o[j][2 + r] * unit);
       }
     __syncthreads();
     const bool begins = s0 == 0, ends = s1 == q_seq.units;
@@ -470,7 +529,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attention_kernel(const KvAtten
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (m != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) add_scaled(o, l, so[w][r] + d, sl[w][r], exp2f(sm[w][r] - m));
+        for (int w = 0; w < kWarps; ++w) add_scaled(o, l, so[w][r] + d, sl[w][r], exp2_fast(sm[w][r] - m));
       }
       if (begins && ends) {
         if (row < rows) write_out<kDim>(a, q_seq.t0, head, row, d, o, l);
@@ -500,7 +559,7 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attention_kernel(const KvAtten
             for (int c = first; c <= last; ++c) {
               const Partial<kDim, kNR>& p = parts[2 * c + (c == first ? 1 : 0)];
               const float4 v = __ldcg(reinterpret_cast<const float4*>(&p.o[r][d]));
-              add_scaled(o, l, &v.x, __ldcg(&p.l[r]), exp2f(__ldcg(&p.m[r]) - m));
+              add_scaled(o, l, &v.x, __ldcg(&p.l[r]), exp2_fast(__ldcg(&p.m[r]) - m));
             }
           }
           write_out<kDim>(a, q_seq.t0, head, row, d, o, l);
@@ -516,7 +575,13 @@ cudaError_t launch(const LaunchCtx& c, const KvAttentionArgs& a, void* ws) {
   const int grid = attention_grid(c, a);
   int* counters = static_cast<int*>(ws);
   auto* parts = reinterpret_cast<Partial<kDim, kNR>*>(static_cast<char*>(ws) + counter_bytes(c));
-  kv_attention_kernel<kDim, kE5M2, kNR><<<grid, 32 * kWarps, 0, c.stream>>>(a, counters, parts, c.status);
+  constexpr size_t kRings = sizeof(Stage<kDim>) * kStages * kWarps;
+  constexpr size_t kJoin = sizeof(float) * kWarps * kRows * kNR * (kDim + 4);
+  constexpr size_t kSmem = kRings > kJoin ? kRings : kJoin;
+  auto fn = kv_attention_kernel<kDim, kE5M2, kNR>;
+  static SmemLimit limit;
+  if (cudaError_t e = limit.raise(reinterpret_cast<const void*>(fn), kSmem)) return e;
+  fn<<<grid, 32 * kWarps, kSmem, c.stream>>>(a, counters, parts, c.status);
   return cudaGetLastError();
 }
 
