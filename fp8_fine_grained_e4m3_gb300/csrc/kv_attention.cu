@@ -28,12 +28,14 @@
 namespace fp8gemm {
 namespace {
 
-constexpr int kTok = 16;   // tokens per tile: one fragment
+constexpr int kFrag = 16;          // tokens of a fragment
+constexpr int kTok = 2 * kFrag;    // tokens of a tile: two fragments, whose chains of
+                                   // dependent instructions run side by side
 constexpr int kRows = 8;   // query rows per fragment
 constexpr int kWarps = 4;
 constexpr int kUnit = kWarps * kTok;  // tokens of a unit: a tile for each warp
-constexpr int kMinUnits = 4;  // a CTA's least share: fewer would cost more to join than to do
-constexpr int kStages = 4;  // tiles of a warp in shared memory
+constexpr int kMinUnits = 2;  // a CTA's least share: fewer would cost more to join than to do
+constexpr int kStages = 2;  // tiles of a warp in shared memory
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -79,23 +81,23 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's share of 16 tokens of one head.  With lane = 4 g + t:
+// A lane's share of a tile of one head.  With lane = 4 g + t, in each fragment:
 //   keys    tokens g and g + 8, bytes 64 c + 16 t .. + 15
 //   values  tokens 2t, 2t + 1, 2t + 8, 2t + 9, bytes (dim / 8) g .. + dim / 8 - 1
 // In a stage each of these pieces is one row of 32 lanes.
 template <int kDim>
 struct Stage {
-  uint4 k[2][kDim / 64][32];
-  uint32_t v[4][32][kDim / 32];
-  float ks[32], vs[32];
+  uint4 k[2][2][kDim / 64][32];
+  uint32_t v[2][4][32][kDim / 32];
+  float ks[2][32], vs[2][32];
 };
 
-// Asks for a tile: kv is the lane's byte offset of it in the codes, tile that
+// Asks for fragment h of a tile: `at` is its byte offset in the codes, tile that
 // of its scales.  Tokens at and past `valid` (16 and more: all there) become
 // zeros, whatever the cache holds there.
 template <int kDim>
-__device__ __forceinline__ void fetch_tile(Stage<kDim>& s, const KvAttentionArgs& a, size_t at,
-                                           size_t tile, int valid, int lane) {
+__device__ __forceinline__ void fetch_fragment(Stage<kDim>& s, int h, const KvAttentionArgs& a,
+                                               size_t at, size_t tile, int valid, int lane) {
   const int g = lane / 4, t = lane % 4;
   const uint8_t* k = a.kc + at + g * kDim + 16 * t;
   const uint8_t* v = a.vc + at + 2 * t * kDim + g * (kDim / 8);
@@ -103,16 +105,16 @@ __device__ __forceinline__ void fetch_tile(Stage<kDim>& s, const KvAttentionArgs
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int c = 0; c < kDim / 64; ++c)
-      copy_async<16>(smem_addr(&s.k[i][c][lane]), k + 8 * i * kDim + 64 * c,
+      copy_async<16>(smem_addr(&s.k[h][i][c][lane]), k + 8 * i * kDim + 64 * c,
                      g + 8 * i < valid ? 16u : 0u);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int tok = (i & 1) + 8 * (i >> 1);
-    copy_async<kDim / 8>(smem_addr(&s.v[i][lane][0]), v + tok * kDim,
+    copy_async<kDim / 8>(smem_addr(&s.v[h][i][lane][0]), v + tok * kDim,
                          2 * t + tok < valid ? uint32_t(kDim / 8) : 0u);
   }
-  copy_async<4>(smem_addr(&s.ks[lane]), a.ks + tile, 4u);
-  copy_async<4>(smem_addr(&s.vs[lane]), a.vs + tile, 4u);
+  copy_async<4>(smem_addr(&s.ks[h][lane]), a.ks + tile, 4u);
+  copy_async<4>(smem_addr(&s.vs[h][lane]), a.vs + tile, 4u);
 }
 
 // The queries of 8 rows as the k16 x n8 fragments that match Tile's keys, and
@@ -186,45 +188,64 @@ __device__ __forceinline__ void clear(State<kDim>& s) {
 constexpr float kUnitLow = 1.f / 64, kUnitFar = 1152921504606846976.f;
 
 // One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
-// fragment i sees (may be negative or past 16).
+// fragment i sees (may be negative or past its end).  there: bit h where
+// fragment h of the tile is.
 template <int kDim, bool kE5M2, int kNR>
 __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
                                             const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
-                                            const int (&limit)[kNR][2], int tok, int lane) {
+                                            const int (&limit)[kNR][2], int tok, uint32_t there,
+                                            int lane) {
   const int g = lane / 4;
-  float c[kNR][4] = {};
+  float c[2][kNR][4] = {};
 #pragma unroll
   for (int cc = 0; cc < kDim / 64; ++cc) {
-    const uint4 r0 = x.k[0][cc][lane], r1 = x.k[1][cc][lane];
-    const uint32_t k0[4] = {r0.x, r0.y, r0.z, r0.w}, k1[4] = {r1.x, r1.y, r1.z, r1.w};
+    uint32_t k[2][2][4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t a[4] = {
-          f8x2_to_f16x2<kE5M2>(uint16_t(k0[w])), f8x2_to_f16x2<kE5M2>(uint16_t(k1[w])),
-          f8x2_to_f16x2<kE5M2>(uint16_t(k0[w] >> 16)), f8x2_to_f16x2<kE5M2>(uint16_t(k1[w] >> 16))};
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < kNR; ++i) mma_f16(c[i], a, q[i].b[4 * cc + w][0], q[i].b[4 * cc + w][1]);
-    }
+      for (int i = 0; i < 2; ++i) {
+        const uint4 r = x.k[h][i][cc][lane];
+        k[h][i][0] = r.x;
+        k[h][i][1] = r.y;
+        k[h][i][2] = r.z;
+        k[h][i][3] = r.w;
+      }
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t k0 = k[h][0][w], k1 = k[h][1][w];
+        const uint32_t a[4] = {
+            f8x2_to_f16x2<kE5M2>(uint16_t(k0)), f8x2_to_f16x2<kE5M2>(uint16_t(k1)),
+            f8x2_to_f16x2<kE5M2>(uint16_t(k0 >> 16)), f8x2_to_f16x2<kE5M2>(uint16_t(k1 >> 16))};
+#pragma unroll
+        for (int i = 0; i < kNR; ++i)
+          mma_f16(c[h][i], a, q[i].b[4 * cc + w][0], q[i].b[4 * cc + w][1]);
+      }
   }
-  const float ks = x.ks[lane], vs = x.vs[lane];
-  // scores in powers of two; element 2h + r: token g + 8h, row r
+  // scores in powers of two; element 2e + r: token g + 8e, row r
   bool rises = false;
 #pragma unroll
-  for (int i = 0; i < kNR; ++i) {
+  for (int h = 0; h < 2; ++h) {
+    const float ks = x.ks[h][lane];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[i][e] = c[i][e] * (q[i].mul[e & 1] * ks);
-      if (g + 8 * (e >> 1) + tok >= limit[i][e & 1]) c[i][e] = -INFINITY;
+    for (int i = 0; i < kNR; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c[h][i][e] = c[h][i][e] * (q[i].mul[e & 1] * ks);
+        if (g + 8 * (e >> 1) + kFrag * h + tok >= limit[i][e & 1] || !(there >> h & 1))
+          c[h][i][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) rises |= fmaxf(c[h][i][r], c[h][i][2 + r]) > s[i].m[r] + kLazy;
     }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) rises |= fmaxf(c[i][r], c[i][2 + r]) > s[i].m[r] + kLazy;
   }
   if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
     for (int i = 0; i < kNR; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float top = fmaxf(c[i][r], c[i][2 + r]);
+        float top = fmaxf(fmaxf(c[0][i][r], c[0][i][2 + r]), fmaxf(c[1][i][r], c[1][i][2 + r]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float m = fmaxf(s[i].m[r], top);
@@ -238,61 +259,66 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
         }
       }
   }
-  float to_unit = 1.f;
-  if (vs != unit) {  // the warp's tiles of one block share it
-    if (vs > unit || (vs < kUnitLow * unit && vs * kUnitFar > unit)) {
-      const float grow = __fdiv_rn(unit, vs);
+  const float vs[2] = {x.vs[0][lane], x.vs[1][lane]};
+  const float top = fmaxf(vs[0], vs[1]);
+  if (top > unit || (top < kUnitLow * unit && top * kUnitFar > unit)) {
+    const float grow = __fdiv_rn(unit, top);
 #pragma unroll
-      for (int i = 0; i < kNR; ++i)
+    for (int i = 0; i < kNR; ++i)
 #pragma unroll
-        for (int j = 0; j < kDim / 16; ++j)
+      for (int j = 0; j < kDim / 16; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i].o[j][e] *= grow;
-      unit = vs;
-    } else {
-      to_unit = __fdiv_rn(vs, unit);
-    }
+        for (int e = 0; e < 4; ++e) s[i].o[j][e] *= grow;
+    unit = top;
   }
-  uint32_t b[kNR][2];
+  uint32_t b[2][kNR][2];
 #pragma unroll
-  for (int i = 0; i < kNR; ++i) {
+  for (int h = 0; h < 2; ++h) {
+    float to_unit = 1.f;
+    if (vs[h] != unit) to_unit = unit > 0.f ? __fdiv_rn(vs[h], unit) : 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float m = s[i].m[e & 1];
-      c[i][e] = exp2_fast(c[i][e] - (m == -INFINITY ? 0.f : m));
-      s[i].l[e & 1] += c[i][e];
-      c[i][e] *= to_unit;
-    }
-    b[i][0] = transpose8x8(f16x2_bits(c[i][0], c[i][1]));
-    b[i][1] = transpose8x8(f16x2_bits(c[i][2], c[i][3]));
-  }
-  uint32_t v[4][kDim / 32];
+    for (int i = 0; i < kNR; ++i) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    if constexpr (kDim == 128) {
-      const uint4 r = *reinterpret_cast<const uint4*>(&x.v[h][lane][0]);
-      v[h][0] = r.x;
-      v[h][1] = r.y;
-      v[h][2] = r.z;
-      v[h][3] = r.w;
-    } else {
-      const uint2 r = *reinterpret_cast<const uint2*>(&x.v[h][lane][0]);
-      v[h][0] = r.x;
-      v[h][1] = r.y;
+      for (int e = 0; e < 4; ++e) {
+        const float m = s[i].m[e & 1];
+        c[h][i][e] = exp2_fast(c[h][i][e] - (m == -INFINITY ? 0.f : m));
+        s[i].l[e & 1] += c[h][i][e];
+        c[h][i][e] *= to_unit;
+      }
+      b[h][i][0] = transpose8x8(f16x2_bits(c[h][i][0], c[h][i][1]));
+      b[h][i][1] = transpose8x8(f16x2_bits(c[h][i][2], c[h][i][3]));
     }
   }
 #pragma unroll
-  for (int j = 0; j < kDim / 16; ++j) {
-    // bytes 2j and 2j + 1 of the four tokens: one matrix row each
-    const uint32_t pick = (j & 1) ? 0x7362 : 0x5140;
-    const uint32_t lo = __byte_perm(v[0][j / 2], v[1][j / 2], pick);
-    const uint32_t hi = __byte_perm(v[2][j / 2], v[3][j / 2], pick);
-    const uint32_t a[4] = {f8x2_to_f16x2<kE5M2>(uint16_t(lo)),
-                           f8x2_to_f16x2<kE5M2>(uint16_t(lo >> 16)),
-                           f8x2_to_f16x2<kE5M2>(uint16_t(hi)),
-                           f8x2_to_f16x2<kE5M2>(uint16_t(hi >> 16))};
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[4][kDim / 32];
 #pragma unroll
-    for (int i = 0; i < kNR; ++i) mma_f16(s[i].o[j], a, b[i][0], b[i][1]);
+    for (int p = 0; p < 4; ++p) {
+      if constexpr (kDim == 128) {
+        const uint4 r = *reinterpret_cast<const uint4*>(&x.v[h][p][lane][0]);
+        v[p][0] = r.x;
+        v[p][1] = r.y;
+        v[p][2] = r.z;
+        v[p][3] = r.w;
+      } else {
+        const uint2 r = *reinterpret_cast<const uint2*>(&x.v[h][p][lane][0]);
+        v[p][0] = r.x;
+        v[p][1] = r.y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kDim / 16; ++j) {
+      // bytes 2j and 2j + 1 of the four tokens: one matrix row each
+      const uint32_t pick = (j & 1) ? 0x7362 : 0x5140;
+      const uint32_t lo = __byte_perm(v[0][j / 2], v[1][j / 2], pick);
+      const uint32_t hi = __byte_perm(v[2][j / 2], v[3][j / 2], pick);
+      const uint32_t a[4] = {f8x2_to_f16x2<kE5M2>(uint16_t(lo)),
+                             f8x2_to_f16x2<kE5M2>(uint16_t(lo >> 16)),
+                             f8x2_to_f16x2<kE5M2>(uint16_t(hi)),
+                             f8x2_to_f16x2<kE5M2>(uint16_t(hi >> 16))};
+#pragma unroll
+      for (int i = 0; i < kNR; ++i) mma_f16(s[i].o[j], a, b[h][i][0], b[h][i][1]);
+    }
   }
 }
 
@@ -375,6 +401,70 @@ struct Partial {
   float o[kRows * kNR][kDim];
   float m[kRows * kNR], l[kRows * kNR];
 };
+
+// Joins the partials of CTAs first .. last of one item, in that order.  What
+// each one's rows have to be multiplied by comes first (in f: kJoinMax CTAs at a
+// time), so that the loads of the sums do not wait for one another.
+constexpr int kJoinMax = 64;
+
+template <int kDim, int kNR>
+__device__ __forceinline__ void join_partials(const KvAttentionArgs& a,
+                                              const Partial<kDim, kNR>* parts, int first, int last,
+                                              int t0, int head, int row0, int rows, float* f) {
+  constexpr int kR = kRows * kNR, kPer = kR * kDim / 4 / (32 * kWarps);
+  float* ms = f + kJoinMax * kR;  // the running maximum of each row
+  float4 o[kPer];
+  float l[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    l[k] = 0.f;
+  }
+  auto part = [&](int c) -> const Partial<kDim, kNR>& { return parts[2 * c + (c == first ? 1 : 0)]; };
+  if (threadIdx.x < kR) ms[threadIdx.x] = -INFINITY;
+  for (int c0 = first; c0 <= last; c0 += kJoinMax) {
+    const int n = min(kJoinMax, last + 1 - c0);
+    __syncthreads();  // f is free
+    for (int i = threadIdx.x; i < n * kR; i += 32 * kWarps)
+      f[i] = __ldcg(&part(c0 + i / kR).m[i % kR]);
+    __syncthreads();
+    float shrink[kPer];
+    if (threadIdx.x < kR) {
+      const float old = ms[threadIdx.x];
+      float m = old;
+      for (int c = 0; c < n; ++c) m = fmaxf(m, f[c * kR + threadIdx.x]);
+      for (int c = 0; c < n; ++c)
+        f[c * kR + threadIdx.x] = m == -INFINITY ? 0.f : exp2_fast(f[c * kR + threadIdx.x] - m);
+      ms[threadIdx.x] = m;
+      ms[kR + threadIdx.x] = m == -INFINITY ? 1.f : exp2_fast(old - m);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      shrink[k] = ms[kR + (threadIdx.x + 32 * kWarps * k) / (kDim / 4)];
+      l[k] *= shrink[k];
+      o[k].x *= shrink[k];
+      o[k].y *= shrink[k];
+      o[k].z *= shrink[k];
+      o[k].w *= shrink[k];
+    }
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+      const Partial<kDim, kNR>& p = part(c0 + c);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int i = threadIdx.x + 32 * kWarps * k, r = i / (kDim / 4), d = i % (kDim / 4) * 4;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(&p.o[r][d]));
+        add_scaled(o[k], l[k], &v.x, __ldcg(&p.l[r]), f[c * kR + r]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = threadIdx.x + 32 * kWarps * k, r = i / (kDim / 4), d = i % (kDim / 4) * 4;
+    if (row0 + r < rows) write_out<kDim>(a, t0, head, row0 + r, d, o[k], l[k]);
+  }
+}
 
 // The CTAs share the units of all items evenly, in runs.  A CTA joins its
 // warps' results in shared memory for each item of its run; an item that lies in
@@ -465,37 +555,64 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
       }
       clear(s[i]);
     }
-    // kStages - 1 tiles in flight; the table entry of the next one to ask for
-    // is read a step before
+    // kStages - 1 tiles in flight; the table entries of the next one to ask
+    // for are read a step before
     float unit = 0.f;
     const int* table = a.table + size_t(b) * a.width;
-    auto entry = [&](int i) {
+    int next[2];
+    auto entries = [&](int i) {
       const int tok = i * kUnit + warp * kTok;
-      return i < s1 && tok < len ? table[tok >> a.log_block] : -1;
+      next[0] = i < s1 && tok < len ? table[tok >> a.log_block] : -1;
+      next[1] = next[0];
+      if (a.block == kFrag)
+        next[1] = i < s1 && tok + kFrag < len ? table[(tok + kFrag) >> a.log_block] : -1;
     };
-    int next = entry(s0);
-    uint32_t there = 0;  // bit i % 32: the tile of unit i is in its stage
+    uint32_t there = 0;  // two bits a stage: its fragments that are there
     auto fetch = [&](int i) {
-      const int tok = i * kUnit + warp * kTok, blk = next;
-      next = entry(i + 1);
-      const bool ok = blk >= 0 && blk < a.num_blocks;
-      if (ok) {
-        const size_t tile = size_t(blk) * a.heads + head;
-        fetch_tile<kDim>(ring[i % kStages], a,
-                         ((tile << a.log_block) + (tok & (a.block - 1))) * kDim, tile, len - tok, lane);
-      } else if (i < s1 && tok < len && lane == 0) {
-        raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+      const int tok0 = i * kUnit + warp * kTok, stage = i % kStages;
+      uint32_t ok = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tok = tok0 + kFrag * h, blk = next[h];
+        if (i >= s1 || tok >= len) {
+          continue;
+        } else if (blk >= 0 && blk < a.num_blocks) {
+          const size_t tile = size_t(blk) * a.heads + head;
+          fetch_fragment<kDim>(ring[stage], h, a,
+                               ((tile << a.log_block) + (tok & (a.block - 1))) * kDim, tile,
+                               len - tok, lane);
+          ok |= 1u << h;
+        } else if (lane == 0) {  // a bad table entry: its tokens count as not there
+          raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+        }
       }
-      there = (there & ~(1u << i % 32)) | uint32_t(ok) << i % 32;
+      there = (there & ~(3u << 2 * stage)) | ok << 2 * stage;
       copy_commit();
+      entries(i + 1);
+      if (ok == 1) {  // what the second fragment's place still holds must not reach a sum
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int w = 0; w < kDim / 32; ++w) ring[stage].v[1][p][lane][w] = 0u;
+        ring[stage].vs[1][lane] = 0.f;
+      } else if (ok == 2) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int w = 0; w < kDim / 32; ++w) ring[stage].v[0][p][lane][w] = 0u;
+        ring[stage].vs[0][lane] = 0.f;
+      }
     };
+    entries(s0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(s0 + i);
     for (int i = s0; i < s1; ++i) {
-      copy_wait<kStages - 2>();
-      if (there >> i % 32 & 1)  // else past the end, or a bad table entry: not there
-        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[i % kStages], q, limit, i * kUnit + warp * kTok, lane);
-      fetch(i + kStages - 1);  // into the stage that was used last, by the lanes that read it
+      fetch(i + kStages - 1);  // into the stage used last, by the lanes that read it
+      copy_wait<kStages - 1>();
+      const uint32_t ok = there >> 2 * (i % kStages) & 3u;
+      if (ok != 0)
+        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[i % kStages], q, limit,
+                                      i * kUnit + warp * kTok, ok, lane);
     }
     copy_wait<0>();
     __syncthreads();  // the rings become the place to join the warps' results
@@ -547,23 +664,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
       __syncthreads();
       if (last_one) {
         if (threadIdx.x == 0) counters[first] = 0;
-        for (int i = threadIdx.x; i < kR * kDim / 4; i += 32 * kWarps) {
-          const int r = i / (kDim / 4), d = i % (kDim / 4) * 4, row = row0 + r;
-          if (row >= rows) continue;
-          float m = -INFINITY;
-          for (int c = first; c <= last; ++c)
-            m = fmaxf(m, __ldcg(&parts[2 * c + (c == first ? 1 : 0)].m[r]));
-          float l = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (m != -INFINITY) {
-            for (int c = first; c <= last; ++c) {
-              const Partial<kDim, kNR>& p = parts[2 * c + (c == first ? 1 : 0)];
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(&p.o[r][d]));
-              add_scaled(o, l, &v.x, __ldcg(&p.l[r]), exp2_fast(__ldcg(&p.m[r]) - m));
-            }
-          }
-          write_out<kDim>(a, q_seq.t0, head, row, d, o, l);
-        }
+        join_partials<kDim, kNR>(a, parts, first, last, q_seq.t0, head, row0, rows,
+                                 reinterpret_cast<float*>(shared));
+        __syncthreads();
       }
     }
     u = item0 + s1;
