@@ -229,6 +229,21 @@ bool make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint6
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t cols,
+                    uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || rows == 0) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols};
+  const cuuint32_t box[2] = {cols, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_bf16_sw64(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
@@ -572,6 +587,7 @@ static int check_cache(int T, int B, int heads, int dim, int block, int width, i
   if ((dim != 64 && dim != 128) || (block != 16 && block != 32 && block != 64 && block != 128))
     return FP8GEMM_ERR_SHAPE;
   if (B > 32767 || heads > 65535) return FP8GEMM_ERR_SHAPE;
+  if ((long long)num_blocks * heads > 0x7fffffffLL / block) return FP8GEMM_ERR_SHAPE;
   if (!cu && B > 0 && (T % B != 0 || most < T / B)) return FP8GEMM_ERR_SHAPE;
   if (!valid_fmt(fmt)) return FP8GEMM_ERR_FORMAT;
   return FP8GEMM_OK;
@@ -623,7 +639,8 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
   const KvAttentionArgs a{static_cast<const __nv_bfloat16*>(Q), ld_q, k_cache, k_scale, v_cache,
                           v_scale, block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O),
                           scale, T, B, heads, group, dim, block, table_width, num_blocks, max_q,
-                          fmt, block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7};
+                          fmt, block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7,
+                          wait_limit_ns()};
   void* ws = nullptr;
   if (int r = workspace_for(stream, kv_attention_workspace_bytes(c, a), &ws, kWsAttention)) return r;
   return finish(launch_kv_attention(c, a, ws), 1);

@@ -171,6 +171,7 @@ struct KvAttentionArgs {
   float scale;
   int T, B, heads, group, dim, block, width, num_blocks, max_q, fmt;
   int log_block;
+  unsigned long long wait_ns;  // limit of each wait for a copy
 };
 size_t kv_attention_workspace_bytes(const LaunchCtx& c, const KvAttentionArgs& a);
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws);
@@ -214,6 +215,10 @@ unsigned long long wait_limit_ns();
 // rows x cols bytes, box of box_rows x 128 bytes.  Defined in api.cu.
 bool make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                         uint32_t box_rows);
+// The same for rows of `cols` = 64 or 128 bytes, whole rows in a box, swizzled
+// over their own length.  Defined in api.cu.
+bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t cols,
+                    uint32_t box_rows);
 // Encodes a 2-D row-major bf16 tensor map with 64-byte swizzling: rows x
 // cols elements, box of box_rows x 32 elements (64 bytes).  False when the
 // layout cannot be described (base not 16-byte aligned, cols * 2 not a

@@ -7,11 +7,12 @@
 // (its own among them); a row that sees none gives zeros.  Query heads h g ..
 // h g + g - 1 read the cached head h, so their rows share every byte of it.
 //
-// Bound by the cache's bytes: each is read once, by the lane whose tensor-core
-// fragment it belongs to.  A lane's share of the tiles ahead waits in shared memory
-// that no other lane touches (cp.async, then its own wait: no barrier, no bank
-// conflict, and bytes in flight that cost no registers).  Both products are taken transposed so that tokens (and the
-// head's dimension) fill the 16-row side of m16n8k16 and 8 query rows the other:
+// Bound by the cache's bytes: each is read once.  A warp works on its own: one
+// lane asks for the tiles ahead (TMA into the warp's ring in shared memory, one
+// mbarrier a stage), and the 128-byte swizzle lets every lane read its share of
+// a tensor-core fragment as 16 neighbouring bytes without a bank conflict.  Both products
+// are taken transposed so that tokens (and the head's dimension) fill the
+// 16-row side of m16n8k16 and 8 query rows the other:
 //   S^T [16 tokens, 8 rows] = K [16, dim] Q^T      O^T [dim, 8 rows] += V^T [dim, 16] P^T
 // The order of a contraction is free, so the dimension is dealt to the
 // fragment's k index such that a lane's share of a key is 16 neighbouring bytes, and the
@@ -66,55 +67,43 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t src_bytes) {
-  if constexpr (kBytes == 16)
-    cp_async_16(dst, src, src_bytes);
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
-                 "r"(src_bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// A lane's share of a tile of one head.  With lane = 4 g + t, in each fragment:
-//   keys    tokens g and g + 8, bytes 64 c + 16 t .. + 15
+// A tile of one head: 32 tokens, 16-byte chunk c of token r at chunk c ^ (r & 7) of
+// its 128 bytes (64-byte tokens: c ^ (r / 2 & 3), as the TMA writes them).  With lane
+// = 4 g + t, a lane's share of each fragment is
+//   keys    tokens g and g + 8, bytes (dim / 4) t .. + dim / 4 - 1
 //   values  tokens 2t, 2t + 1, 2t + 8, 2t + 9, bytes (dim / 8) g .. + dim / 8 - 1
-// In a stage each of these pieces is one row of 32 lanes.
 template <int kDim>
 struct Stage {
-  uint4 k[2][2][kDim / 64][32];
-  uint32_t v[2][4][32][kDim / 32];
-  float ks[2][32], vs[2][32];
+  uint8_t k[kTok][kDim];
+  uint8_t v[kTok][kDim];
 };
 
-// Asks for fragment h of a tile: `at` is its byte offset in the codes, tile that
-// of its scales.  Tokens at and past `valid` (16 and more: all there) become
-// zeros, whatever the cache holds there.
+// Key chunk c (of dim / 64) of token g + 8 i of fragment h.
 template <int kDim>
-__device__ __forceinline__ void fetch_fragment(Stage<kDim>& s, int h, const KvAttentionArgs& a,
-                                               size_t at, size_t tile, int valid, int lane) {
-  const int g = lane / 4, t = lane % 4;
-  const uint8_t* k = a.kc + at + g * kDim + 16 * t;
-  const uint8_t* v = a.vc + at + 2 * t * kDim + g * (kDim / 8);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int c = 0; c < kDim / 64; ++c)
-      copy_async<16>(smem_addr(&s.k[h][i][c][lane]), k + 8 * i * kDim + 64 * c,
-                     g + 8 * i < valid ? 16u : 0u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tok = (i & 1) + 8 * (i >> 1);
-    copy_async<kDim / 8>(smem_addr(&s.v[h][i][lane][0]), v + tok * kDim,
-                         2 * t + tok < valid ? uint32_t(kDim / 8) : 0u);
+__device__ __forceinline__ uint4 key_chunk(const Stage<kDim>& s, int h, int i, int c, int g, int t) {
+  const int r = kFrag * h + 8 * i + g;
+  if constexpr (kDim == 128)
+    return *reinterpret_cast<const uint4*>(&s.k[r][((2 * t + c) ^ g) * 16]);
+  else
+    return *reinterpret_cast<const uint4*>(&s.k[r][(t ^ (g / 2)) * 16]);
+}
+
+// The lane's bytes of its p-th value token of fragment h.
+template <int kDim>
+__device__ __forceinline__ void value_bytes(const Stage<kDim>& s, int h, int p, int g, int t,
+                                            uint32_t (&v)[kDim / 32]) {
+  const int r = kFrag * h + 2 * t + (p & 1) + 8 * (p >> 1);
+  if constexpr (kDim == 128) {
+    const uint4 x = *reinterpret_cast<const uint4*>(&s.v[r][(g ^ (2 * t + (p & 1))) * 16]);
+    v[0] = x.x;
+    v[1] = x.y;
+    v[2] = x.z;
+    v[3] = x.w;
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(&s.v[r][((g / 2) ^ t) * 16 + g % 2 * 8]);
+    v[0] = x.x;
+    v[1] = x.y;
   }
-  copy_async<4>(smem_addr(&s.ks[h][lane]), a.ks + tile, 4u);
-  copy_async<4>(smem_addr(&s.vs[h][lane]), a.vs + tile, 4u);
 }
 
 // The queries of 8 rows as the k16 x n8 fragments that match Tile's keys, and
@@ -136,7 +125,7 @@ __device__ __forceinline__ void load_queries(Queries<kDim>& q, const __nv_bfloat
     for (int e = 0; e < 2; ++e) {
       Raw8<__nv_bfloat16> r;
       zero8(r);
-      if (row) r = load8(row + 64 * c + 16 * t + 8 * e);
+      if (row) r = load8(row + (kDim / 4) * t + 16 * c + 8 * e);
       float f[8];
       unpack8(r, f);
 #pragma unroll
@@ -189,13 +178,15 @@ constexpr float kUnitLow = 1.f / 64, kUnitFar = 1152921504606846976.f;
 
 // One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
 // fragment i sees (may be negative or past its end).  there: bit h where
-// fragment h of the tile is.
+// fragment h of the tile is; valid: its tokens that exist; ks, vs: the scales
+// of its fragments.
 template <int kDim, bool kE5M2, int kNR>
 __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
                                             const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
                                             const int (&limit)[kNR][2], int tok, uint32_t there,
+                                            int valid, const float (&ks)[2], const float (&vs)[2],
                                             int lane) {
-  const int g = lane / 4;
+  const int g = lane / 4, t = lane % 4;
   float c[2][kNR][4] = {};
 #pragma unroll
   for (int cc = 0; cc < kDim / 64; ++cc) {
@@ -204,7 +195,7 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 r = x.k[h][i][cc][lane];
+        const uint4 r = key_chunk(x, h, i, cc, g, t);
         k[h][i][0] = r.x;
         k[h][i][1] = r.y;
         k[h][i][2] = r.z;
@@ -227,12 +218,11 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
   bool rises = false;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const float ks = x.ks[h][lane];
 #pragma unroll
     for (int i = 0; i < kNR; ++i) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        c[h][i][e] = c[h][i][e] * (q[i].mul[e & 1] * ks);
+        c[h][i][e] = c[h][i][e] * (q[i].mul[e & 1] * ks[h]);
         if (g + 8 * (e >> 1) + kFrag * h + tok >= limit[i][e & 1] || !(there >> h & 1))
           c[h][i][e] = -INFINITY;
       }
@@ -259,7 +249,6 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
         }
       }
   }
-  const float vs[2] = {x.vs[0][lane], x.vs[1][lane]};
   const float top = fmaxf(vs[0], vs[1]);
   if (top > unit || (top < kUnitLow * unit && top * kUnitFar > unit)) {
     const float grow = __fdiv_rn(unit, top);
@@ -293,18 +282,13 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
   for (int h = 0; h < 2; ++h) {
     uint32_t v[4][kDim / 32];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      if constexpr (kDim == 128) {
-        const uint4 r = *reinterpret_cast<const uint4*>(&x.v[h][p][lane][0]);
-        v[p][0] = r.x;
-        v[p][1] = r.y;
-        v[p][2] = r.z;
-        v[p][3] = r.w;
-      } else {
-        const uint2 r = *reinterpret_cast<const uint2*>(&x.v[h][p][lane][0]);
-        v[p][0] = r.x;
-        v[p][1] = r.y;
-      }
+    for (int p = 0; p < 4; ++p) value_bytes(x, h, p, g, t, v[p]);
+    if (valid < kTok || there != 3u) {  // what lies past the end may be anything: not even a 0 times it
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (kFrag * h + 2 * t + (p & 1) + 8 * (p >> 1) >= valid || !(there >> h & 1))
+#pragma unroll
+          for (int w = 0; w < kDim / 32; ++w) v[p][w] = 0u;
     }
 #pragma unroll
     for (int j = 0; j < kDim / 16; ++j) {
@@ -412,6 +396,7 @@ __device__ __forceinline__ void join_partials(const KvAttentionArgs& a,
                                               const Partial<kDim, kNR>* parts, int first, int last,
                                               int t0, int head, int row0, int rows, float* f) {
   constexpr int kR = kRows * kNR, kPer = kR * kDim / 4 / (32 * kWarps);
+  static_assert(kPer * 32 * kWarps * 4 == kR * kDim, "a whole number for each thread");
   float* ms = f + kJoinMax * kR;  // the running maximum of each row
   float4 o[kPer];
   float l[kPer];
@@ -448,7 +433,7 @@ __device__ __forceinline__ void join_partials(const KvAttentionArgs& a,
       o[k].z *= shrink[k];
       o[k].w *= shrink[k];
     }
-#pragma unroll 4
+#pragma unroll(16 / kPer)
     for (int c = 0; c < n; ++c) {
       const Partial<kDim, kNR>& p = part(c0 + c);
 #pragma unroll
@@ -466,6 +451,11 @@ __device__ __forceinline__ void join_partials(const KvAttentionArgs& a,
   }
 }
 
+// The cache's codes as rows of dim bytes, in boxes of min(block, kTok) rows.
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+
 // The CTAs share the units of all items evenly, in runs.  A CTA joins its
 // warps' results in shared memory for each item of its run; an item that lies in
 // several runs is joined from their partials, in CTA order, by whichever of
@@ -475,18 +465,30 @@ __device__ __forceinline__ void join_partials(const KvAttentionArgs& a,
 //   counter c    CTAs done with the item that goes on past CTA c's run (left at 0)
 template <int kDim, bool kE5M2, int kNR>
 __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attention_kernel(const KvAttentionArgs a,
+                                                                   const __grid_constant__ CacheMaps maps,
                                                                    int* counters,
                                                                    Partial<kDim, kNR>* parts,
                                                                    int* status) {
   constexpr int kR = kRows * kNR;
-  extern __shared__ __align__(16) unsigned char shared[];
+  extern __shared__ unsigned char raw[];
+  unsigned char* shared = raw + (1024u - (smem_addr(raw) & 1023u)) % 1024u;
   float (*so)[kR][kDim + 4] = reinterpret_cast<float (*)[kR][kDim + 4]>(shared);
   __shared__ float sm[kWarps][kR], sl[kWarps][kR];
   __shared__ long long scan[kWarps];
   __shared__ Place place;
   __shared__ int last_one;
+  __shared__ int gave_up, never;  // a wait ran out; always 0
+  __shared__ uint64_t bars[kWarps][kStages];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   Stage<kDim>* ring = reinterpret_cast<Stage<kDim>*>(shared) + warp * kStages;
+
+  if (threadIdx.x == 0) {
+    gave_up = never = 0;
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&bars[0][i], 1);
+    fence_mbar_init();
+  }
+  uint32_t phases = 0;     // bit s: the parity that stage s waits for next
+  uint32_t in_flight = 0;  // bit s: it has been asked for
 
   // all units, and each thread's share of the sequences
   const int per_thread = ceil_div(a.B, 32 * kWarps);
@@ -555,67 +557,95 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
       }
       clear(s[i]);
     }
-    // kStages - 1 tiles in flight; the table entries of the next one to ask
-    // for are read a step before
-    float unit = 0.f;
+    // Blocks of the tile of unit i, -1 where it has none.  Past the first kStages
+    // tiles they are read a step before they are needed.
     const int* table = a.table + size_t(b) * a.width;
-    int next[2];
-    auto entries = [&](int i) {
+    auto blocks = [&](int i) -> int2 {
       const int tok = i * kUnit + warp * kTok;
-      next[0] = i < s1 && tok < len ? table[tok >> a.log_block] : -1;
-      next[1] = next[0];
-      if (a.block == kFrag)
-        next[1] = i < s1 && tok + kFrag < len ? table[(tok + kFrag) >> a.log_block] : -1;
+      int2 e = make_int2(-1, -1);
+      if (i >= s1 || tok >= len) return e;
+      e.x = table[tok >> a.log_block];
+      e.y = a.block >= kTok ? e.x : tok + kFrag < len ? table[(tok + kFrag) >> a.log_block] : -1;
+      const bool bad_x = e.x < 0 || e.x >= a.num_blocks;
+      const bool bad_y = (e.y < 0 || e.y >= a.num_blocks) && (a.block >= kTok || tok + kFrag < len);
+      if (bad_x || bad_y) {  // their tokens count as not there
+        if (lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+        if (bad_x) e.x = -1;
+        if (bad_y) e.y = -1;
+      }
+      return e;
     };
-    uint32_t there = 0;  // two bits a stage: its fragments that are there
-    auto fetch = [&](int i) {
-      const int tok0 = i * kUnit + warp * kTok, stage = i % kStages;
-      uint32_t ok = 0;
+    auto fetch = [&](int i, int2 e) {
+      if (e.x < 0 && e.y < 0) return;
+      in_flight |= 1u << i % kStages;
+      if (lane != 0) return;
+      const int tok = (i * kUnit + warp * kTok) & (a.block - 1), stage = i % kStages;
+      const int half = kFrag * kDim;
+      mbar_arrive_expect_tx(&bars[warp][stage], 2 * half * (int(e.x >= 0) + int(e.y >= 0)));
+      if (a.block >= kTok) {
+        const int row = (e.x * a.heads + head) * a.block + tok;
+        tma_load_2d(ring[stage].k, &maps.k, &bars[warp][stage], 0, row);
+        tma_load_2d(ring[stage].v, &maps.v, &bars[warp][stage], 0, row);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = tok0 + kFrag * h, blk = next[h];
-        if (i >= s1 || tok >= len) {
-          continue;
-        } else if (blk >= 0 && blk < a.num_blocks) {
-          const size_t tile = size_t(blk) * a.heads + head;
-          fetch_fragment<kDim>(ring[stage], h, a,
-                               ((tile << a.log_block) + (tok & (a.block - 1))) * kDim, tile,
-                               len - tok, lane);
-          ok |= 1u << h;
-        } else if (lane == 0) {  // a bad table entry: its tokens count as not there
-          raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+        for (int h = 0; h < 2; ++h) {
+          const int blk = h ? e.y : e.x, row = (blk * a.heads + head) * a.block;
+          if (blk < 0) continue;
+          tma_load_2d(ring[stage].k[kFrag * h], &maps.k, &bars[warp][stage], 0, row);
+          tma_load_2d(ring[stage].v[kFrag * h], &maps.v, &bars[warp][stage], 0, row);
         }
       }
-      there = (there & ~(3u << 2 * stage)) | ok << 2 * stage;
-      copy_commit();
-      entries(i + 1);
-      if (ok == 1) {  // what the second fragment's place still holds must not reach a sum
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-          for (int w = 0; w < kDim / 32; ++w) ring[stage].v[1][p][lane][w] = 0u;
-        ring[stage].vs[1][lane] = 0.f;
-      } else if (ok == 2) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-          for (int w = 0; w < kDim / 32; ++w) ring[stage].v[0][p][lane][w] = 0u;
-        ring[stage].vs[0][lane] = 0.f;
-      }
     };
-    entries(s0);
+    struct Scales {
+      float k[2], v[2];
+    };
+    auto scales = [&](int2 e) {
+      Scales x = {};
+      if (e.x >= 0) {
+        x.k[0] = a.ks[size_t(e.x) * a.heads + head];
+        x.v[0] = a.vs[size_t(e.x) * a.heads + head];
+      }
+      if (e.y >= 0) {
+        x.k[1] = a.ks[size_t(e.y) * a.heads + head];
+        x.v[1] = a.vs[size_t(e.y) * a.heads + head];
+      }
+      return x;
+    };
+    float unit = 0.f;
+    int2 ahead[kStages];  // blocks of the tiles in flight, the oldest first
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(s0 + i);
+    for (int i = 0; i < kStages; ++i) ahead[i] = blocks(s0 + i);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(s0 + i, ahead[i]);
+    Scales sc = scales(ahead[0]);
     for (int i = s0; i < s1; ++i) {
-      fetch(i + kStages - 1);  // into the stage used last, by the lanes that read it
-      copy_wait<kStages - 1>();
-      const uint32_t ok = there >> 2 * (i % kStages) & 3u;
-      if (ok != 0)
-        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[i % kStages], q, limit,
-                                      i * kUnit + warp * kTok, ok, lane);
+      const int2 e = ahead[0];
+      const Scales here = sc;
+#pragma unroll
+      for (int k = 0; k + 1 < kStages; ++k) ahead[k] = ahead[k + 1];
+      sc = scales(ahead[0]);
+      ahead[kStages - 1] = blocks(i + kStages);
+      const uint32_t there = uint32_t(e.x >= 0) | uint32_t(e.y >= 0) << 1;
+      if (there != 0) {
+        const int stage = i % kStages, tok = i * kUnit + warp * kTok;
+        if (!mbar_wait(&bars[warp][stage], phases >> stage & 1, &gave_up, a.wait_ns)) {
+          // results are void; what is still in flight lands first, or not at all
+          gave_up = 1;
+          raise_status(status, FP8GEMM_ERR_TIMEOUT);
+          for (int k = 0; k < kStages; ++k)
+            if (in_flight >> k & 1) mbar_wait(&bars[warp][k], phases >> k & 1, &never, a.wait_ns);
+          break;
+        }
+        phases ^= 1u << stage;
+        in_flight &= ~(1u << stage);
+        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[stage], q, limit, tok, there, len - tok, here.k,
+                                      here.v, lane);
+        __syncwarp();  // the stage has been read
+      }
+      fetch(i + kStages, ahead[kStages - 1]);
     }
-    copy_wait<0>();
     __syncthreads();  // the rings become the place to join the warps' results
+    if (gave_up) break;
 
 #pragma unroll
     for (int i = 0; i < kNR; ++i)
@@ -658,7 +688,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
         }
       }
     }
-    __syncthreads();  // the shared buffers are free, and this CTA's partial is written
+    fence_proxy_async_smem();  // the copies that follow come through another proxy
+    __syncthreads();           // the shared buffers are free, and this CTA's partial is written
     if (!(begins && ends)) {
       if (threadIdx.x == 0) last_one = atomic_add_acq_rel_gpu(counters + first, 1) == last - first;
       __syncthreads();
@@ -666,6 +697,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
         if (threadIdx.x == 0) counters[first] = 0;
         join_partials<kDim, kNR>(a, parts, first, last, q_seq.t0, head, row0, rows,
                                  reinterpret_cast<float*>(shared));
+        fence_proxy_async_smem();
         __syncthreads();
       }
     }
@@ -674,25 +706,25 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
 }
 
 template <int kDim, bool kE5M2, int kNR>
-cudaError_t launch(const LaunchCtx& c, const KvAttentionArgs& a, void* ws) {
+cudaError_t launch(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps& maps, void* ws) {
   const int grid = attention_grid(c, a);
   int* counters = static_cast<int*>(ws);
   auto* parts = reinterpret_cast<Partial<kDim, kNR>*>(static_cast<char*>(ws) + counter_bytes(c));
-  constexpr size_t kRings = sizeof(Stage<kDim>) * kStages * kWarps;
+  constexpr size_t kRings = 1024 + sizeof(Stage<kDim>) * kStages * kWarps;
   constexpr size_t kJoin = sizeof(float) * kWarps * kRows * kNR * (kDim + 4);
   constexpr size_t kSmem = kRings > kJoin ? kRings : kJoin;
   auto fn = kv_attention_kernel<kDim, kE5M2, kNR>;
   static SmemLimit limit;
   if (cudaError_t e = limit.raise(reinterpret_cast<const void*>(fn), kSmem)) return e;
-  fn<<<grid, 32 * kWarps, kSmem, c.stream>>>(a, counters, parts, c.status);
+  fn<<<grid, 32 * kWarps, kSmem, c.stream>>>(a, maps, counters, parts, c.status);
   return cudaGetLastError();
 }
 
 template <int kNR>
-cudaError_t launch_rows(const LaunchCtx& c, const KvAttentionArgs& a, void* ws) {
+cudaError_t launch_rows(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps& maps, void* ws) {
   const bool e5 = a.fmt == FP8GEMM_FMT_E5M2;
-  if (a.dim == 128) return e5 ? launch<128, true, kNR>(c, a, ws) : launch<128, false, kNR>(c, a, ws);
-  return e5 ? launch<64, true, kNR>(c, a, ws) : launch<64, false, kNR>(c, a, ws);
+  if (a.dim == 128) return e5 ? launch<128, true, kNR>(c, a, maps, ws) : launch<128, false, kNR>(c, a, maps, ws);
+  return e5 ? launch<64, true, kNR>(c, a, maps, ws) : launch<64, false, kNR>(c, a, maps, ws);
 }
 
 }  // namespace
@@ -703,7 +735,12 @@ size_t kv_attention_workspace_bytes(const LaunchCtx& c, const KvAttentionArgs& a
 }
 
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws) {
-  return row_fragments(a) == 1 ? launch_rows<1>(c, a, ws) : launch_rows<2>(c, a, ws);
+  CacheMaps maps;
+  const uint64_t rows = max(uint64_t(a.num_blocks) * a.heads * a.block, uint64_t(1));
+  const uint32_t box = min(a.block, kTok);
+  if (!make_tmap_rows(&maps.k, a.kc, rows, a.dim, box) || !make_tmap_rows(&maps.v, a.vc, rows, a.dim, box))
+    return cudaErrorInvalidValue;
+  return row_fragments(a) == 1 ? launch_rows<1>(c, a, maps, ws) : launch_rows<2>(c, a, maps, ws);
 }
 
 }  // namespace fp8gemm
