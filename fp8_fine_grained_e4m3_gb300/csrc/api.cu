@@ -664,9 +664,9 @@ int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const ui
   LaunchCtx c;
   if (int r = ctx_for(stream, &c)) return r;
   const MoeArgs a{A, sA, logits, W1, s1, W2, s2, static_cast<__nv_bfloat16*>(D), ids, weights,
-                  T, H, I, E, top_k, renormalise};
+                  T, H, I, E, top_k, renormalise, wait_limit_ns()};
   void* ws = nullptr;
-  if (int r = workspace_for(stream, moe_few_workspace_bytes(a), &ws, kWsMoe)) return r;
+  if (int r = workspace_for(stream, moe_few_workspace_bytes(c, a), &ws, kWsMoe)) return r;
   int launches = 0;
   const cudaError_t e = launch_moe_few(c, a, ws, &launches);
   return finish(e, launches);

@@ -189,8 +189,9 @@ struct MoeArgs {
   int* ids;           // [T, k]
   float* weights;     // [T, k]
   int T, H, I, E, k, renormalise;
+  unsigned long long wait_ns;  // limit of each wait for a copy
 };
-size_t moe_few_workspace_bytes(const MoeArgs& a);
+size_t moe_few_workspace_bytes(const LaunchCtx& c, const MoeArgs& a);
 cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace, int* launches);
 
 // Raises a kernel's dynamic shared memory limit, once per device and CUDA context
@@ -199,6 +200,25 @@ struct SmemLimit {
   unsigned long long set_in[64] = {};  // context id, per device
   cudaError_t raise(const void* fn, size_t bytes);
 };
+
+// Launches a kernel as a programmatic dependent of the one before it on the
+// stream: it may start while that one ends, and waits for it (griddepcontrol)
+// before it reads or writes memory.
+template <class... P, class... A>
+cudaError_t launch_dependent(const LaunchCtx& c, void (*fn)(P...), dim3 grid, dim3 block,
+                             size_t smem, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, P(args)...);
+}
 
 // Fills `c` for the current device and `stream` (SM count, status word);
 // returns an fp8gemm_status code.  Defined in api.cu.

@@ -377,6 +377,7 @@ __device__ __forceinline__ Sequence sequence(const KvAttentionArgs& a, int b, in
 struct Place {
   int b;
   long long before;  // units of the sequences before b
+  Sequence seq;
 };
 
 // A partial result in the workspace: what a CTA knows of an item that it shares.
@@ -490,11 +491,22 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
   uint32_t phases = 0;     // bit s: the parity that stage s waits for next
   uint32_t in_flight = 0;  // bit s: it has been asked for
 
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+
   // all units, and each thread's share of the sequences
   const int per_thread = ceil_div(a.B, 32 * kWarps);
   const int b0 = min(a.B, int(threadIdx.x) * per_thread), b1 = min(a.B, b0 + per_thread);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += sequence<kNR>(a, b, status).total;
+  Sequence seq = {};
+  for (int b = b0; b < b1; ++b) {
+    seq = sequence<kNR>(a, b, status);
+    mine += seq.total;
+  }
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -514,19 +526,19 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
   if (u0 >= u1) return;
   if (u0 >= upto - mine && u0 < upto) {  // one thread's
     long long before = upto - mine;
-    for (int b = b0; b < b1; ++b) {
-      const long long n = sequence<kNR>(a, b, status).total;
-      if (u0 < before + n) {
-        place = Place{b, before};
-        break;
+    int b = b0;
+    if (b1 - b0 > 1)
+      for (;; ++b) {
+        seq = sequence<kNR>(a, b, status);
+        if (u0 < before + seq.total) break;
+        before += seq.total;
       }
-      before += n;
-    }
+    place = Place{b, before, seq};
   }
   __syncthreads();
   int b = place.b;
   long long before = place.before;
-  Sequence q_seq = sequence<kNR>(a, b, status);
+  Sequence q_seq = place.seq;
 
   for (long long u = u0; u < u1;) {
     while (u >= before + q_seq.total) {
@@ -539,24 +551,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
     const int s0 = int(u - item0), s1 = int(min((long long)q_seq.units, u1 - item0));
     const int rows = q_seq.n * a.group, len = q_seq.len;
 
-    Queries<kDim> q[kNR];
-    State<kDim> s[kNR];
-    int limit[kNR][2];  // tokens that the lane's rows see
-#pragma unroll
-    for (int i = 0; i < kNR; ++i) {
-      const int row = row0 + kRows * i + g;  // whose query this lane loads
-      const __nv_bfloat16* p =
-          row < rows ? a.Q + (q_seq.t0 + row / a.group) * a.ld_q +
-                           (head * a.group + row % a.group) * kDim
-                     : nullptr;
-      load_queries<kDim>(q[i], p, a.scale * 1.44269504088896341f, t);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int rr = row0 + kRows * i + 2 * t + r;
-        limit[i][r] = rr < rows ? len - q_seq.n + 1 + rr / a.group : 0;
-      }
-      clear(s[i]);
-    }
     // Blocks of the tile of unit i, -1 where it has none.  Past the first kStages
     // tiles they are read a step before they are needed.
     const int* table = a.table + size_t(b) * a.width;
@@ -618,6 +612,24 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(s0 + i, ahead[i]);
     Scales sc = scales(ahead[0]);
+    Queries<kDim> q[kNR];
+    State<kDim> s[kNR];
+    int limit[kNR][2];  // tokens that the lane's rows see
+#pragma unroll
+    for (int i = 0; i < kNR; ++i) {
+      const int row = row0 + kRows * i + g;  // whose query this lane loads
+      const __nv_bfloat16* p =
+          row < rows ? a.Q + (q_seq.t0 + row / a.group) * a.ld_q +
+                           (head * a.group + row % a.group) * kDim
+                     : nullptr;
+      load_queries<kDim>(q[i], p, a.scale * 1.44269504088896341f, t);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int rr = row0 + kRows * i + 2 * t + r;
+        limit[i][r] = rr < rows ? len - q_seq.n + 1 + rr / a.group : 0;
+      }
+      clear(s[i]);
+    }
     for (int i = s0; i < s1; ++i) {
       const int2 e = ahead[0];
       const Scales here = sc;
@@ -716,8 +728,7 @@ cudaError_t launch(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps
   auto fn = kv_attention_kernel<kDim, kE5M2, kNR>;
   static SmemLimit limit;
   if (cudaError_t e = limit.raise(reinterpret_cast<const void*>(fn), kSmem)) return e;
-  fn<<<grid, 32 * kWarps, kSmem, c.stream>>>(a, maps, counters, parts, c.status);
-  return cudaGetLastError();
+  return launch_dependent(c, fn, grid, 32 * kWarps, kSmem, a, maps, counters, parts, c.status);
 }
 
 template <int kNR>
