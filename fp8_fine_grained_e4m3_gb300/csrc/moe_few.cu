@@ -9,8 +9,9 @@
 // scales; each K block's partial product is multiplied by its scale product
 // and added in FP32).
 //
-// Three launches: routing (one CTA), the up kernel (gate and up products,
-// SwiGLU and quantisation) and the down kernel (down product and weighted sum).
+// Two launches: the up kernel (gate and up products, SwiGLU and quantisation) and
+// the down kernel (down product and weighted sum); routing is done by each of
+// their CTAs for a few tokens, by a launch of one CTA before them for more.
 //
 // Bound by the chosen experts' weights, read once.  In both product kernels
 // the K blocks of all output tiles of all chosen experts form one sequence
@@ -23,6 +24,8 @@
 // lane's share of a row's K block is 32 neighbouring bytes.  A tile that lies in
 // several runs is joined from FP32 partials, in CTA order, by the CTA that
 // finishes last: results do not depend on timing.
+#include <type_traits>
+
 #include "common.cuh"
 #include "f8_convert.cuh"
 #include "moe_few.cuh"
@@ -54,14 +57,14 @@ struct Chunk {
   uint32_t w[8];
 };
 
-// Of an activation row, 0 past its K bytes (a multiple of 16).
-__device__ __forceinline__ Chunk load_chunk(const uint8_t* row, int k0, int K, int t) {
+// Of an activation row; p: the lane's place in it, in[i]: its i-th 16 bytes are
+// inside the row.
+__device__ __forceinline__ Chunk load_chunk(const uint8_t* p, const bool (&in)[2]) {
   Chunk c;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int k = k0 + 32 * t + 16 * i;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (row != nullptr && k < K) v = *reinterpret_cast<const uint4*>(row + k);
+    if (in[i]) v = *reinterpret_cast<const uint4*>(p + 16 * i);
     c.w[4 * i] = v.x;
     c.w[4 * i + 1] = v.y;
     c.w[4 * i + 2] = v.z;
@@ -94,18 +97,36 @@ __device__ __forceinline__ void mma_block(float (&d)[4], const Chunk& lo, const 
 }
 
 // ------------------------------------------------------------------ routing
-// Some (at most 8 NT) of the pairs that chose one expert: one pass over its weights.
+// Pair p = token * k + choice.  A pass is some (at most 8 NT) of the pairs that
+// chose one expert, together: expert, first place in the list, pairs.
+__device__ __forceinline__ uint32_t pack_pass(int e, int first, int cnt) {
+  return uint32_t(e) << 20 | uint32_t(first) << 8 | uint32_t(cnt);
+}
 struct Pass {
-  int e, first, cnt, unused;  // pairs list[first .. first + cnt - 1]
+  int e, first, cnt;
+  Pass() = default;
+  __device__ explicit Pass(uint32_t p) : e(p >> 20), first(p >> 8 & 0xfff), cnt(p & 0xff) {}
 };
 
-// What routing leaves for the product kernels.  Pair p = token * k + choice.
+// Where routing leaves what the product kernels need.
 struct Route {
-  float* weight;  // [T k]
-  int* list;      // [T k] pairs by expert, ascending within each
-  Pass* pass;     // [T k]
-  int* passes;    // how many
+  float* weight;   // [T k]
+  int* list;       // [T k] pairs by expert, ascending within each
+  uint32_t* pass;  // [T k]
+  int* passes;     // how many
 };
+
+// Up to kOwnTokens tokens the product kernels route for themselves, each CTA
+// into its own shared memory: for one token that takes 1 us of latency where a
+// launch before them takes 4.  The work grows with the tokens that a warp has; past
+// 8 (two each) a launch of 32 warps is faster.
+constexpr int kOwnTokens = 8;
+constexpr int kOwnPairs = kOwnTokens * kMoeMaxTopK;
+
+// Scratch of the routing: 4 bytes a pair, 2 an expert, 1 an expert and warp.
+__host__ __device__ constexpr int route_scratch(int warps) {
+  return 32 * warps * 4 + kMoeMaxExperts * (2 + warps) + 2 * 32 * 4;
+}
 
 // A float as an unsigned number of the same order; NaN as -infinity.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -114,124 +135,161 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One CTA: a warp per token chooses its experts; then a thread per expert
-// counts and lists its pairs.
+// One warp chooses the experts of token t; kPer values a lane.  ids and w: of
+// the token, at lane j its j-th choice.
+template <int kPer>
+__device__ __forceinline__ void route_token(const float* logits, int E, int k, int renormalise,
+                                            int* id, float* w) {
+  const int lane = threadIdx.x % 32;
+  float v[kPer];
+  uint32_t key[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = lane + 32 * i < E ? logits[lane + 32 * i] : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < E ? order_key(v[i]) : 0u;  // 0: not to be had
+  float first = 0.f, sum = 0.f, mine = 0.f;
+  int mine_id = 0;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+    int at = lane;
+    float x = v[0];
+#pragma unroll
+    for (int i = 1; i < kPer; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
+        x = v[i];
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int win = __reduce_min_sync(0xffffffffu, best == top ? uint32_t(at) : 0xffffffffu);
+    x = __shfl_sync(0xffffffffu, x, win % 32);
+    if (isnan(x)) x = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (win == lane + 32 * i) key[i] = 0u;
+    if (j == 0) first = x;
+    const float p = x == -INFINITY ? 0.f : expf(x - first);
+    sum += p;
+    if (j == lane) {
+      mine = p;
+      mine_id = win;
+    }
+  }
+  if (!renormalise) {  // over all experts
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += isnan(v[i]) || v[i] == -INFINITY ? 0.f : expf(v[i] - first);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  *id = mine_id;
+  *w = sum > 0.f ? __fdiv_rn(mine, sum) : 0.f;
+}
+
+// The whole CTA (kW warps, T k <= 32 kW) routes all tokens; ids_out and w_out
+// (the call's outputs) may be null.  Ends with the results written and a barrier.
+template <int kW>
+__device__ __forceinline__ void route_all(const float* logits, const Route& r, uint8_t* scratch,
+                                          int32_t* ids_out, float* w_out, int T, int E, int k,
+                                          int renormalise, int per_pass) {
+  int* ids = reinterpret_cast<int*>(scratch);                      // [32 kW]
+  uint32_t* warp_sum = reinterpret_cast<uint32_t*>(ids + 32 * kW);  // [32]
+  uint16_t* first = reinterpret_cast<uint16_t*>(warp_sum + 64);     // [E]
+  uint8_t* hist = reinterpret_cast<uint8_t*>(first + kMoeMaxExperts);  // [kW][kMoeMaxExperts]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, P = T * k;
+  for (int i = threadIdx.x; i < kW * kMoeMaxExperts / 4; i += 32 * kW) reinterpret_cast<uint32_t*>(hist)[i] = 0u;
+  for (int t = warp; t < T; t += kW) {
+    int id;
+    float w;
+    const float* row = logits + size_t(t) * E;
+    if (E <= 32)
+      route_token<1>(row, E, k, renormalise, &id, &w);
+    else if (E <= 128)
+      route_token<4>(row, E, k, renormalise, &id, &w);
+    else
+      route_token<kMoeMaxExperts / 32>(row, E, k, renormalise, &id, &w);
+    if (lane < k) {
+      const int p = t * k + lane;
+      ids[p] = id;
+      r.weight[p] = w;
+      if (ids_out) ids_out[p] = id;
+      if (w_out) w_out[p] = w;
+    }
+  }
+  __syncthreads();
+  // a pair's place: its expert's first, those of the warps before it, those of the lanes before it
+  const int p = threadIdx.x, id = p < P ? ids[p] : -1;
+  const uint32_t same = __match_any_sync(0xffffffffu, id);
+  const int rank = __popc(same & ((1u << lane) - 1u));
+  if (id >= 0 && rank == 0) hist[warp * kMoeMaxExperts + id] = uint8_t(__popc(same));
+  __syncthreads();
+  const int per = ceil_div(E, 32 * kW), e0 = threadIdx.x * per;
+  uint32_t sum = 0;  // pairs << 16 | passes of this thread's experts
+  for (int e = e0; e < min(E, e0 + per); ++e) {
+    int n = 0;
+    for (int w = 0; w * 32 < P; ++w) {
+      const int h = hist[w * kMoeMaxExperts + e];
+      hist[w * kMoeMaxExperts + e] = uint8_t(n);
+      n += h;
+    }
+    first[e] = uint16_t(n);
+    sum += uint32_t(n) << 16 | uint32_t(ceil_div(n, per_pass));
+  }
+  uint32_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += warp_sum[w];
+  if (threadIdx.x == 32 * kW - 1) *r.passes = int(upto & 0xffffu);
+  uint32_t at = upto - sum;
+  for (int e = e0; e < min(E, e0 + per); ++e) {
+    const int n = first[e], begin = int(at >> 16), passes = ceil_div(n, per_pass);
+    for (int i = 0; i < passes; ++i)
+      r.pass[(at & 0xffffu) + i] = pack_pass(e, begin + i * per_pass, min(per_pass, n - i * per_pass));
+    first[e] = uint16_t(begin);
+    at += uint32_t(n) << 16 | uint32_t(passes);
+  }
+  __syncthreads();
+  if (id >= 0) r.list[first[id] + hist[warp * kMoeMaxExperts + id] + rank] = p;
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(1024) moe_route_kernel(const float* __restrict__ logits, Route r,
                                                          int32_t* ids_out, float* w_out, int T,
                                                          int E, int k, int renormalise,
                                                          int per_pass) {
-  constexpr int kPer = kMoeMaxExperts / 32;
-  __shared__ __align__(16) int ids[kMoeMaxTokens * kMoeMaxTopK + 4];
-  __shared__ int warp_pairs[32], warp_passes[32];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  __shared__ __align__(16) uint8_t scratch[route_scratch(32)];
   griddep_launch_dependents();
   griddep_wait();
-  const int per = ceil_div(E, 32);  // values a lane holds
-  for (int t = warp; t < T; t += 32) {
-    float v[kPer];
-    uint32_t key[kPer];
-    uint32_t taken = 0;  // bit i: expert lane + 32 i is chosen already
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = i < per && e < E ? logits[t * E + e] : -INFINITY;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      key[i] = order_key(v[i]);
-      if (lane + 32 * i >= E) taken |= 1u << i;
-    }
-    float first = 0.f, sum = 0.f, mine = 0.f;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = 0, at = 0xffffffffu;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i < per && !(taken >> i & 1) && (at == 0xffffffffu || key[i] > best)) {
-          best = key[i];
-          at = lane + 32 * i;
-        }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, at == 0xffffffffu ? 0u : best);
-      at = __reduce_min_sync(0xffffffffu, best == top ? at : 0xffffffffu);
-      float mine_v = -INFINITY;  // the chosen logit, from the lane that holds it
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == int(at / 32)) mine_v = v[i];
-      float x = __shfl_sync(0xffffffffu, mine_v, at % 32);
-      if (isnan(x)) x = -INFINITY;
-      if (at % 32 == uint32_t(lane)) taken |= 1u << (at / 32);
-      if (j == 0) first = x;
-      const float p = x == -INFINITY ? 0.f : expf(x - first);
-      sum += p;
-      if (j == lane) {
-        mine = p;
-        ids_out[t * k + j] = int(at);
-        ids[t * k + j] = int(at);
-      }
-    }
-    if (!renormalise) {  // over all experts
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i < per) sum += isnan(v[i]) || v[i] == -INFINITY ? 0.f : expf(v[i] - first);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if (lane < k) {
-      const float w = sum > 0.f ? __fdiv_rn(mine, sum) : 0.f;
-      w_out[t * k + lane] = w;
-      r.weight[t * k + lane] = w;
-    }
-  }
-  const int P = T * k;
-  if (threadIdx.x < 4) ids[P + threadIdx.x] = -1;
-  __syncthreads();
-  const int e = threadIdx.x;  // E <= 512 of the 1024 threads
-  int n = 0;
-  if (e < E)
-    for (int p = 0; p < P; p += 4) {
-      const int4 q = *reinterpret_cast<const int4*>(ids + p);
-      n += int(q.x == e) + int(q.y == e) + int(q.z == e) + int(q.w == e);
-    }
-  // exclusive sums over the experts of the pairs and of the passes
-  const int m = ceil_div(n, per_pass);
-  int before = n, pass = m;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, before, o), b = __shfl_up_sync(0xffffffffu, pass, o);
-    if (lane >= o) {
-      before += a;
-      pass += b;
-    }
-  }
-  if (lane == 31) {
-    warp_pairs[warp] = before;
-    warp_passes[warp] = pass;
-  }
-  __syncthreads();
-  before -= n;
-  pass -= m;
-  for (int w = 0; w < warp; ++w) {
-    before += warp_pairs[w];
-    pass += warp_passes[w];
-  }
-  if (threadIdx.x == blockDim.x - 1) *r.passes = pass + m;
-  if (n == 0) return;
-  for (int i = 0; i < m; ++i)
-    r.pass[pass + i] = Pass{e, before + i * per_pass, min(per_pass, n - i * per_pass), 0};
-  for (int p = 0; p < P; ++p)
-    if (ids[p] == e) r.list[before++] = p;
+  route_all<32>(logits, r, scratch, ids_out, w_out, T, E, k, renormalise, per_pass);
 }
+
+// A CTA's own routing.
+struct OwnRoute {
+  float weight[kOwnPairs];
+  int list[kOwnPairs];
+  uint32_t pass[kOwnPairs];
+  int passes;
+  __device__ Route route() { return Route{weight, list, pass, &passes}; }
+};
+static_assert(kOwnPairs <= 32 * kWarps, "a thread for each pair");
+template <int NT>
+constexpr bool kOwnRoute = 8 * NT <= kOwnTokens;
 
 // ------------------------------------------------------------ product kernels
 // A CTA's run of the unit sequence.
 struct Run {
-  long long U, per;
-  long long u0, u1;
-  __device__ Run(long long units) : U(units) {
+  long long per, u0, u1;
+  __device__ explicit Run(long long U) {
     per = max((long long)kMinUnits, (U + gridDim.x - 1) / gridDim.x);
-    u0 = blockIdx.x * per;
+    u0 = min(U, blockIdx.x * per);
     u1 = min(U, u0 + per);
   }
+  __device__ int units() const { return int(u1 - u0); }
 };
 
 // One warp's ring of weight tiles.
@@ -282,7 +340,7 @@ template <int NT>
 constexpr int kUpStages = NT == 4 ? 3 : 2;
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeArgs a, const Route r,
+__global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeArgs a, const Route given,
                                                              const __grid_constant__ CUtensorMap map,
                                                              uint8_t* __restrict__ H8,
                                                              float* __restrict__ sH, int* counters,
@@ -290,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
   constexpr int kPart = kWarps * 4 * NT * 4 * 32;
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
+  __shared__ std::conditional_t<kOwnRoute<NT>, OwnRoute, int> mine;
   __shared__ float amaxes[kWarps][8 * NT];
   __shared__ __align__(16) uint8_t codes[8 * NT][kBlockK];
   uint8_t* rings = init_shared(sh, raw, &map);
@@ -298,107 +357,112 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
   Ring<kUpStages<NT>, 64 * kBlockK> ring{rings + warp * kUpStages<NT> * 64 * kBlockK, sh.bars[warp]};
   griddep_wait();
   griddep_launch_dependents();  // all before this kernel is complete: the next may read weights
+  Route r = given;
+  if constexpr (kOwnRoute<NT>) {  // into the rings' memory first: nothing has been asked for yet
+    r = mine.route();
+    const bool out = blockIdx.x == 0;
+    route_all<kWarps>(a.logits, r, rings, out ? a.ids : nullptr, out ? a.weights : nullptr, a.T, a.E,
+                      a.k, a.renormalise, 8 * NT);
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
   const Run run((long long)*r.passes * Ib * Kb);
-  if (run.u0 >= run.u1) return;
+  int left = run.units();
+  if (left == 0) return;
 
-  // the unit that is asked for next, kUpStages ahead of the one in use
-  long long ask = run.u0;
-  int ask_tile = int(ask / Kb), ask_kb = int(ask % Kb), ask_stage = 0;
-  int ask_e = r.pass[ask_tile / Ib].e;
+  // the tile and K block in use, and those asked for (kUpStages ahead)
+  int tile = int(run.u0 / Kb), kb = int(run.u0 - (long long)tile * Kb);
+  int pi = tile / Ib, ib = tile - pi * Ib;
+  int ask_left = left, ask_pi = pi, ask_ib = ib, ask_kb = kb, ask_stage = 0;
+  int ask_row = Pass(r.pass[pi]).e * 2 * a.I + ib * kBlockK + 32 * warp;
   auto fetch = [&]() {
-    if (ask >= run.u1) return;
+    if (ask_left == 0) return;
+    --ask_left;
     ring.in_flight |= 1u << ask_stage;
     if (lane == 0) {
-      const int row = ask_e * 2 * a.I + ask_tile % Ib * kBlockK + 32 * warp;
       uint8_t* s = ring.stage(ask_stage);
       mbar_arrive_expect_tx(&ring.bar[ask_stage], 64 * kBlockK);
-      tma_load_2d(s, &map, &ring.bar[ask_stage], ask_kb * kBlockK, row);
-      tma_load_2d(s + 32 * kBlockK, &map, &ring.bar[ask_stage], ask_kb * kBlockK, row + a.I);
+      tma_load_2d(s, &map, &ring.bar[ask_stage], ask_kb * kBlockK, ask_row);
+      tma_load_2d(s + 32 * kBlockK, &map, &ring.bar[ask_stage], ask_kb * kBlockK, ask_row + a.I);
     }
     ask_stage = ask_stage + 1 == kUpStages<NT> ? 0 : ask_stage + 1;
-    ++ask;
-    if (++ask_kb == Kb) {
+    if (++ask_kb == Kb && ask_left > 0) {
       ask_kb = 0;
-      ++ask_tile;
-      if (ask < run.u1 && ask_tile % Ib == 0) ask_e = r.pass[ask_tile / Ib].e;
+      if (++ask_ib == Ib) {
+        ask_ib = 0;
+        ++ask_pi;
+      }
+      ask_row = Pass(r.pass[ask_pi]).e * 2 * a.I + ask_ib * kBlockK + 32 * warp;
     }
   };
 #pragma unroll
   for (int i = 0; i < kUpStages<NT>; ++i) fetch();
 
-  // what a unit needs besides weights, loaded a unit ahead
-  struct Side {
-    Chunk x[NT];
-    float sx[NT][2], sg, su[2];
-  } next;
-  Pass pass = {};
-  int side_tile = -1;
-  int tok[NT], col[NT][2];  // the token this lane loads; those of its two columns (-1: none)
-  const float *sg = nullptr, *su[2] = {};
-  auto side = [&](long long u) {
-    const int tile = int(u / Kb), kb = int(u - (long long)tile * Kb);
-    if (tile != side_tile) {
-      if (side_tile < 0 || tile / Ib != side_tile / Ib) {
-        pass = r.pass[tile / Ib];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          tok[n] = 8 * n + g < pass.cnt ? r.list[pass.first + 8 * n + g] / a.k : -1;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            col[n][c] = 8 * n + 2 * t + c < pass.cnt ? r.list[pass.first + 8 * n + 2 * t + c] / a.k : -1;
-        }
-      }
-      side_tile = tile;
-      const int i0 = tile % Ib * kBlockK;
-      const float* s = a.s1 + size_t(pass.e) * Rb * Kb;
-      sg = s + size_t(i0 / kBlockK) * Kb;
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-        su[m] = s + size_t(min((a.I + i0 + 32 * warp + 16 * m) / kBlockK, Rb - 1)) * Kb;
-    }
-    next.sg = sg[kb];
-    next.su[0] = su[0][kb];
-    next.su[1] = su[1][kb];
+  // What a unit needs besides weights.  Columns without a pair take the
+  // pass's last one: their results are not used.
+  Pass at;
+  const uint8_t* x[NT];
+  const float* sx[NT][2];
+  const float *sg, *su[2];
+  auto enter_pass = [&]() {
+    at = Pass(r.pass[pi]);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (8 * n >= pass.cnt) break;
-      next.x[n] = load_chunk(tok[n] >= 0 ? a.A + size_t(tok[n]) * a.H : nullptr, kb * kBlockK, a.H, t);
+      x[n] = a.A + size_t(r.list[at.first + min(8 * n + g, at.cnt - 1)] / a.k) * a.H + 32 * t;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) next.sx[n][c] = col[n][c] >= 0 ? a.sA[size_t(col[n][c]) * Kb + kb] : 0.f;
+      for (int c = 0; c < 2; ++c)
+        sx[n][c] = a.sA + size_t(r.list[at.first + min(8 * n + 2 * t + c, at.cnt - 1)] / a.k) * Kb;
     }
   };
-  side(run.u0);
+  auto enter_tile = [&]() {
+    const float* s = a.s1 + size_t(at.e) * Rb * Kb;
+    sg = s + size_t(ib) * Kb;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+      su[m] = s + size_t(min((a.I + ib * kBlockK + 32 * warp + 16 * m) / kBlockK, Rb - 1)) * Kb;
+  };
+  enter_pass();
+  enter_tile();
 
   float acc[4][NT][4] = {};
   int stage = 0;
   bool dead = false;
-  for (long long u = run.u0; u < run.u1; ++u) {
-    const Side here = next;
-    const Pass at = pass;
-    const int tile = side_tile;
-    if (u + 1 < run.u1) side(u + 1);
+  while (true) {
+    const float sw[3] = {sg[kb], su[0][kb], su[1][kb]};
+    const bool in[2] = {kb * kBlockK + 32 * t < a.H, kb * kBlockK + 32 * t + 16 < a.H};
+    Chunk xc[NT];
+    float sxk[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (8 * n >= at.cnt) break;
+      xc[n] = load_chunk(x[n] + kb * kBlockK, in);
+      sxk[n][0] = sx[n][0][kb];
+      sxk[n][1] = sx[n][1][kb];
+    }
     // After a wait that ran out the warp only keeps the others' barriers company.
     dead = dead || !ring.wait(stage, &sh.gave_up, &sh.never, status, a.wait_ns);
     const uint8_t* w = ring.stage(stage);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const Chunk lo = tile_chunk(w, 16 * m + g, t), hi = tile_chunk(w, 16 * m + 8 + g, t);
-      const float sw = m < 2 ? here.sg : here.su[m - 2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (8 * n >= at.cnt) break;
         float d[4] = {};
-        mma_block(d, lo, hi, here.x[n]);
+        mma_block(d, lo, hi, xc[n]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][n][c] = fmaf(d[c], here.sx[n][c & 1] * sw, acc[m][n][c]);
+        for (int c = 0; c < 4; ++c)
+          acc[m][n][c] = fmaf(d[c], sxk[n][c & 1] * sw[m < 2 ? 0 : m - 1], acc[m][n][c]);
       }
     }
     __syncwarp();  // the stage has been read
     if (!dead) fetch();
     stage = stage + 1 == kUpStages<NT> ? 0 : stage + 1;
-    const long long tile0 = (long long)tile * Kb;
-    if (u + 1 < run.u1 && u + 1 < tile0 + Kb) continue;
+    ++kb;
+    --left;
+    if (kb < Kb && left > 0) continue;
 
+    const long long tile0 = (long long)tile * Kb;
     // the run's share of this tile is done
     const bool whole = tile0 >= run.u0 && tile0 + Kb <= run.u1;
     const int first = int(tile0 / run.per), last = int((tile0 + Kb - 1) / run.per);
@@ -440,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
       }
     }
     if (whole || sh.last_one) {  // SwiGLU and the 1x128 quantisation of the tile
-      const int i0 = tile % Ib * kBlockK;
+      const int i0 = ib * kBlockK;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (8 * n >= at.cnt) break;
@@ -474,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
           for (int w2 = 0; w2 < kWarps; ++w2) top = fmaxf(top, amaxes[w2][j]);
           const float s = __fdiv_rn(top, kE4M3Max);
           if (j < at.cnt && warp == 0 && g == 0)
-            sH[size_t(r.list[at.first + j]) * Ib + tile % Ib] = s;
+            sH[size_t(r.list[at.first + j]) * Ib + ib] = s;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -492,12 +556,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
       }
       __syncthreads();  // amaxes and codes are free
     }
+    if (left == 0) break;
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[m][n][c] = 0.f;
+    kb = 0;
+    ++tile;
+    if (++ib == Ib) {
+      ib = 0;
+      ++pi;
+      enter_pass();
+    }
+    enter_tile();
   }
 }
 
@@ -509,13 +582,14 @@ constexpr int kDownStages = 4;
 constexpr int kSumRow = 36;  // floats from token to token: lanes of a fragment hit all banks
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const MoeArgs a, const Route r,
+__global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const MoeArgs a, const Route given,
                                                                const __grid_constant__ CUtensorMap map,
                                                                const uint8_t* H8, const float* sH,
                                                                int* counters, float* parts,
                                                                int* status) {
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
+  __shared__ std::conditional_t<kOwnRoute<NT>, OwnRoute, int> mine;
   uint8_t* rings = init_shared(sh, raw, &map);
   float* all_sums = reinterpret_cast<float*>(rings + kWarps * kDownStages * 32 * kBlockK);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -524,35 +598,41 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
   for (int i = lane; i < a.T * kSumRow; i += 32) sums[i] = 0.f;
   Ring<kDownStages, 32 * kBlockK> ring{rings + warp * kDownStages * 32 * kBlockK, sh.bars[warp]};
   // The up kernel let this one start after everything before it was complete:
-  // routing and weights may be read, the hidden activations not yet.
-  const int passes = __ldcg(r.passes);
+  // logits, routing and weights may be read, the hidden activations not yet.
+  Route r = given;
+  if constexpr (kOwnRoute<NT>) {
+    r = mine.route();
+    route_all<kWarps>(a.logits, r, rings, nullptr, nullptr, a.T, a.E, a.k, a.renormalise, 8 * NT);
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+  const int passes = *r.passes;
   const long long per_tile = (long long)passes * Kb;
   const Run run(Hb * per_tile);
-  if (run.u0 >= run.u1) {
+  int left = run.units();
+  if (left == 0) {
     griddep_wait();
     return;
   }
-  long long ask = run.u0;
-  int ask_tile = int(ask / per_tile), ask_stage = 0;
-  int ask_pass = int((ask - ask_tile * per_tile) / Kb), ask_kb = int(ask % Kb);
-  int ask_e = __ldcg(&r.pass[ask_pass].e);
+  int tile = int(run.u0 / per_tile), pi = int(run.u0 - tile * per_tile) / Kb, kb = int(run.u0 % Kb);
+  int ask_left = left, ask_tile = tile, ask_pi = pi, ask_kb = kb, ask_stage = 0;
+  int ask_row = Pass(r.pass[pi]).e * a.H + tile * kBlockK + 32 * warp;
   auto fetch = [&]() {
-    if (ask >= run.u1) return;
+    if (ask_left == 0) return;
+    --ask_left;
     ring.in_flight |= 1u << ask_stage;
     if (lane == 0) {
       mbar_arrive_expect_tx(&ring.bar[ask_stage], 32 * kBlockK);
-      tma_load_2d(ring.stage(ask_stage), &map, &ring.bar[ask_stage], ask_kb * kBlockK,
-                  ask_e * a.H + ask_tile * kBlockK + 32 * warp);
+      tma_load_2d(ring.stage(ask_stage), &map, &ring.bar[ask_stage], ask_kb * kBlockK, ask_row);
     }
     ask_stage = (ask_stage + 1) % kDownStages;
-    ++ask;
-    if (++ask_kb == Kb) {
+    if (++ask_kb == Kb && ask_left > 0) {
       ask_kb = 0;
-      if (++ask_pass == passes) {
-        ask_pass = 0;
+      if (++ask_pi == passes) {
+        ask_pi = 0;
         ++ask_tile;
       }
-      if (ask < run.u1) ask_e = __ldcg(&r.pass[ask_pass].e);
+      ask_row = Pass(r.pass[ask_pi]).e * a.H + ask_tile * kBlockK + 32 * warp;
     }
   };
 #pragma unroll
@@ -560,63 +640,40 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
   griddep_launch_dependents();
   griddep_wait();
 
-  struct Side {
-    Chunk x[NT];
-    float sx[NT][2], sw;
-  } next;
-  Pass pass = {};
-  int tile = int(run.u0 / per_tile), pi = int((run.u0 - tile * per_tile) / Kb), kb = int(run.u0 % Kb);
-  int row[NT], col[NT][2];  // the pair this lane loads; those of its two columns (-1: none)
-  const float* sw = nullptr;
-  auto enter = [&]() {  // the side loads enter pass pi of a tile
-    pass = r.pass[pi];
-    sw = a.s2 + (size_t(pass.e) * Hb + tile) * Kb;
+  // What a unit needs besides weights.  Columns without a pair take the
+  // pass's last one: their results are not used.
+  Pass at;
+  const uint8_t* x[NT];
+  const float* sx[NT][2];
+  const float* sw;
+  auto enter = [&]() {
+    at = Pass(r.pass[pi]);
+    sw = a.s2 + (size_t(at.e) * Hb + tile) * Kb;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      row[n] = 8 * n + g < pass.cnt ? r.list[pass.first + 8 * n + g] : -1;
+      x[n] = H8 + size_t(r.list[at.first + min(8 * n + g, at.cnt - 1)]) * a.I + 32 * t;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        col[n][c] = 8 * n + 2 * t + c < pass.cnt ? r.list[pass.first + 8 * n + 2 * t + c] : -1;
-    }
-  };
-  auto side = [&]() {
-    next.sw = sw[kb];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (8 * n >= pass.cnt) break;
-      next.x[n] = load_chunk(row[n] >= 0 ? H8 + size_t(row[n]) * a.I : nullptr, kb * kBlockK, a.I, t);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) next.sx[n][c] = col[n][c] >= 0 ? sH[size_t(col[n][c]) * Kb + kb] : 0.f;
+        sx[n][c] = sH + size_t(r.list[at.first + min(8 * n + 2 * t + c, at.cnt - 1)]) * Kb;
     }
   };
   enter();
-  side();
 
   float acc[2][NT][4] = {};
   int stage = 0;
   bool dead = false;
-  for (long long u = run.u0; u < run.u1; ++u) {
-    const Side here = next;
-    const int cnt = pass.cnt, this_tile = tile;
-    int here_col[NT][2];
+  while (true) {
+    const float swk = sw[kb];
+    const bool in[2] = {kb * kBlockK + 32 * t < a.I, kb * kBlockK + 32 * t + 16 < a.I};
+    Chunk xc[NT];
+    float sxk[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      here_col[n][0] = col[n][0];
-      here_col[n][1] = col[n][1];
+      if (8 * n >= at.cnt) break;
+      xc[n] = load_chunk(x[n] + kb * kBlockK, in);
+      sxk[n][0] = sx[n][0][kb] * swk;
+      sxk[n][1] = sx[n][1][kb] * swk;
     }
-    const bool pass_ends = kb + 1 == Kb || u + 1 == run.u1;
-    if (u + 1 < run.u1) {
-      if (++kb == Kb) {
-        kb = 0;
-        if (++pi == passes) {
-          pi = 0;
-          ++tile;
-        }
-        enter();
-      }
-      side();
-    }
-    // After a wait that ran out the warp only keeps the others' barriers company.
     dead = dead || !ring.wait(stage, &sh.gave_up, &sh.never, status, a.wait_ns);
     const uint8_t* w = ring.stage(stage);
 #pragma unroll
@@ -624,24 +681,29 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
       const Chunk lo = tile_chunk(w, 16 * m + g, t), hi = tile_chunk(w, 16 * m + 8 + g, t);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if (8 * n >= cnt) break;
+        if (8 * n >= at.cnt) break;
         float d[4] = {};
-        mma_block(d, lo, hi, here.x[n]);
+        mma_block(d, lo, hi, xc[n]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][n][c] = fmaf(d[c], here.sx[n][c & 1] * here.sw, acc[m][n][c]);
+        for (int c = 0; c < 4; ++c) acc[m][n][c] = fmaf(d[c], sxk[n][c & 1], acc[m][n][c]);
       }
     }
     __syncwarp();  // the stage has been read
     if (!dead) fetch();
     stage = (stage + 1) % kDownStages;
-    if (!pass_ends) continue;
+    ++kb;
+    --left;
+    if (kb < Kb && left > 0) continue;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      if (8 * n >= at.cnt) break;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (here_col[n][c] >= 0) {
-          const float wt = r.weight[here_col[n][c]];
-          float* s = sums + here_col[n][c] / a.k * kSumRow + g;
+        const int j = 8 * n + 2 * t + c;
+        if (j < at.cnt) {
+          const int pair = r.list[at.first + j];
+          const float wt = r.weight[pair];
+          float* s = sums + pair / a.k * kSumRow + g;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -651,10 +713,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
 #pragma unroll
         for (int m = 0; m < 2; ++m) acc[m][n][c] = acc[m][n][2 + c] = 0.f;
       }
+    }
     __syncwarp();
-    const long long tile0 = this_tile * per_tile;
-    if (u + 1 < run.u1 && u + 1 < tile0 + per_tile) continue;
+    const int this_tile = tile;
+    kb = 0;
+    if (++pi == passes) {
+      pi = 0;
+      ++tile;
+    }
+    if (left > 0) enter();
+    if (left > 0 && tile == this_tile) continue;
 
+    const long long tile0 = this_tile * per_tile;
     // the run's share of this tile is done
     const bool whole = tile0 >= run.u0 && tile0 + per_tile <= run.u1;
     const int first = int(tile0 / run.per), last = int((tile0 + per_tile - 1) / run.per);
@@ -698,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
         o.y = *reinterpret_cast<const uint32_t*>(&hi);
         *reinterpret_cast<uint2*>(a.D + size_t(i / 8) * a.H + h) = o;
       }
+    if (left == 0) break;
     __syncthreads();  // last_one is free
     for (int i = lane; i < a.T * kSumRow; i += 32) sums[i] = 0.f;
     __syncwarp();
@@ -725,7 +796,7 @@ Layout layout(const LaunchCtx& c, const MoeArgs& a) {
   l.sh = take(P * ceil_div(a.I, kBlockK) * 4);
   l.weight = take(P * 4);
   l.list = take(P * 4);
-  l.pass = take(P * sizeof(Pass));
+  l.pass = take(P * 4);
   l.passes = take(4);
   l.up = take(2 * grid * kWarps * 4 * fragments(a) * 4 * 32 * 4);
   l.down = take(2 * grid * kWarps * a.T * 32 * 4);
@@ -754,9 +825,10 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   static SmemLimit up_limit, down_limit;
   if (cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(up), up_smem)) return e;
   if (cudaError_t e = down_limit.raise(reinterpret_cast<const void*>(down), down_most)) return e;
-  if (cudaError_t e = launch_dependent(c, moe_route_kernel, 1, 1024, 0, a.logits, r, a.ids,
-                                       a.weights, a.T, a.E, a.k, a.renormalise, 8 * NT))
-    return e;
+  if constexpr (!kOwnRoute<NT>)
+    if (cudaError_t e = launch_dependent(c, moe_route_kernel, 1, 1024, 0, a.logits, r, a.ids,
+                                         a.weights, a.T, a.E, a.k, a.renormalise, 8 * NT))
+      return e;
   if (cudaError_t e = launch_dependent(c, up, grid, kThreads, up_smem, a, r, m1, H8, sH, counters,
                                        reinterpret_cast<float*>(ws + l.up), c.status))
     return e;
@@ -772,8 +844,8 @@ cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace
   char* ws = static_cast<char*>(workspace);
   const Layout l = layout(c, a);
   const Route r{reinterpret_cast<float*>(ws + l.weight), reinterpret_cast<int*>(ws + l.list),
-                reinterpret_cast<Pass*>(ws + l.pass), reinterpret_cast<int*>(ws + l.passes)};
-  *launches = 3;
+                reinterpret_cast<uint32_t*>(ws + l.pass), reinterpret_cast<int*>(ws + l.passes)};
+  *launches = a.T <= kOwnTokens ? 2 : 3;
   switch (fragments(a)) {
     case 1: return launch_nt<1>(c, a, r, ws, l);
     case 2: return launch_nt<2>(c, a, r, ws, l);
