@@ -45,6 +45,31 @@ __device__ __forceinline__ uint32_t quant4(float4 v, float s, unsigned* n = null
   return cvt_f8x2<kE5M2>(q0, q1) | (cvt_f8x2<kE5M2>(q2, q3) << 16);
 }
 
+// x / s for many x and one s: Markstein's correction of x times the rounded
+// reciprocal ("Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): with r = RN(1/s), q = RN(x r) and the exact remainder
+// x - q s, RN(q + (x - q s) r) is the correctly rounded quotient where nothing
+// over- or underflows on the way.  `safe` says that for 1x128 quantisation (|x| <= 57344
+// s): outside that range of s the plain division is taken.
+struct Reciprocal {
+  float s, r;
+  bool safe;
+};
+__device__ __forceinline__ Reciprocal reciprocal(float s) {
+  return {s, __frcp_rn(s), s >= 1e-25f && s <= 1e25f};
+}
+__device__ __forceinline__ float quotient(float x, const Reciprocal& d) {
+  const float q = __fmul_rn(x, d.r);
+  return __fmaf_rn(__fmaf_rn(-q, d.s, x), d.r, q);
+}
+
+// quant4 with the scale's reciprocal (d.safe).
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t quant4(float4 v, const Reciprocal& d) {
+  return cvt_f8x2<kE5M2>(quotient(v.x, d), quotient(v.y, d)) |
+         (cvt_f8x2<kE5M2>(quotient(v.z, d), quotient(v.w, d)) << 16);
+}
+
 __device__ __forceinline__ float absmax4(float4 v) {
   return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 }

@@ -38,83 +38,115 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
          (cvt_f8x2<kE5M2>(hi.x * ratio, hi.y * ratio) << 16);
 }
 
-constexpr int kMaxRowsInFlight = 8;  // 128 rows of 128 elements on 256 threads
+constexpr int kWarps = 8;
+constexpr int kPieces = 8;  // 8-element pieces of new rows a lane holds
 
-// Grid (slots, heads, 2 B): the slot-th tile that sequence z / 2 touches, of
-// its keys (z even) or values.  kTpr threads cover a row of 8 kTpr elements.
+// A tile that a sequence touches, of its keys or values, is the work of `wpt`
+// neighbouring warps (1, 2, 4 or 8: enough for the rows it can get), so that a
+// whole tile's new rows are in registers at once.  Item i of the call:
+// slot i % slots of the tiles that (i / slots) % heads of sequence
+// i / slots / heads / 2 touches, keys or values in turn.
 template <int kTpr, bool kE5M2>
-__global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendArgs a, int* status) {
-  __shared__ float red[8];
-  const int b = blockIdx.z >> 1, head = blockIdx.y, is_v = blockIdx.z & 1;
-  int t0 = 0, n = 0;
-  if (!sequence_tokens(a.cu, b, a.B, a.T, a.max_new, &t0, &n)) {
-    if (threadIdx.x == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-    return;
+__global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const KvAppendArgs a, int slots,
+                                                                int log_wpt, int* status) {
+  __shared__ float red[kWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int wpt = 1 << log_wpt;
+  griddep_launch_dependents();
+  griddep_wait();
+  const long long item = ((long long)blockIdx.x * kWarps + warp) >> log_wpt;
+  const int slot = int(item % slots), head = int(item / slots % a.heads);
+  const long long seq = item / slots / a.heads;
+  const int b = int(seq >> 1);
+  const bool is_v = seq & 1;
+  int t0 = 0, n = 0, start = 0, r0 = 0, r1 = 0, base = 0, blk = -1;
+  if (b < a.B) {
+    bool ok = sequence_tokens(a.cu, b, a.B, a.T, a.max_new, &t0, &n);
+    if (ok && n > 0) {
+      const int len = a.lens[b];
+      start = len - n;
+      ok = start >= 0 && (long long)len <= (long long)a.width * a.block;
+      const int j = (ok ? start : 0) / a.block + slot;  // block of the sequence
+      base = j * a.block;                               // its first token
+      if (ok) {
+        r0 = max(start - base, 0);
+        r1 = min(len - base, a.block);
+        if (r0 < r1) {
+          blk = a.table[size_t(b) * a.width + j];
+          ok = blk >= 0 && blk < a.num_blocks;
+        }
+      }
+    }
+    if (!ok) {
+      r1 = r0 = 0;
+      if (lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+    }
   }
-  if (n == 0) return;
-  const int len = a.lens[b], start = len - n;
-  if (start < 0 || (long long)len > (long long)a.width * a.block) {
-    if (threadIdx.x == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-    return;
-  }
-  const int j = start / a.block + blockIdx.x;  // block of the sequence
-  const int base = j * a.block;                // its first token
-  const int r0 = max(start - base, 0), r1 = min(len - base, a.block);
-  if (r0 >= r1) return;
-  const int blk = a.table[size_t(b) * a.width + j];
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (threadIdx.x == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-    return;
-  }
+  const bool work = r0 < r1;  // the same for all warps of a tile
   constexpr int dim = 8 * kTpr;
-  const size_t tile = size_t(blk) * a.heads + head;
+  const size_t tile = work ? size_t(blk) * a.heads + head : 0;
   uint8_t* codes = (is_v ? a.vc : a.kc) + tile * a.block * dim;
   float* scale = (is_v ? a.vs : a.ks) + tile;
   const __nv_bfloat16* X = is_v ? a.V : a.K;
   const long long ld = is_v ? a.ld_v : a.ld_k;
 
-  const int lane_row = threadIdx.x / kTpr, col = threadIdx.x % kTpr * 8;
-  const int rows = blockDim.x / kTpr;
-  Raw8<__nv_bfloat16> x[kMaxRowsInFlight];
+  constexpr int kRowsAtOnce = 32 / kTpr;  // rows a warp covers with one piece a lane
+  const int part = warp & (wpt - 1), col = lane % kTpr * 8;
+  const int row = r0 + part * kRowsAtOnce + lane / kTpr, step = kRowsAtOnce << log_wpt;
+  Raw8<__nv_bfloat16> x[kPieces];
+  float old = 0.f;
+  if (work) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      zero8(x[i]);
+      if (row + i * step < r1) x[i] = load8(X + (t0 + base + row + i * step - start) * ld + head * dim + col);
+    }
+    if (r0 > 0) old = *scale;
+  }
   float amax = 0.f;
+  if (work) {
 #pragma unroll
-  for (int i = 0; i < kMaxRowsInFlight; ++i) {
-    const int r = r0 + lane_row + i * rows;
-    zero8(x[i]);
-    if (r < r1) x[i] = load8(X + (t0 + base + r - start) * ld + head * dim + col);
+    for (int i = 0; i < kPieces; ++i) {
+      float v[8];
+      unpack8(x[i], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   }
-  const float old = r0 > 0 ? *scale : 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxRowsInFlight; ++i) {
-    float v[8];
-    unpack8(x[i], v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+  if (wpt > 1) {
+    if (lane == 0) red[warp] = amax;
+    __syncthreads();  // also: every warp of the tile has read the old scale
+    for (int w = 0; w < wpt; ++w) amax = fmaxf(amax, red[warp - part + w]);
   }
+  if (!work) return;
+  const float s = fmaxf(old, pow2_scale<kE5M2>(amax));
+  // A power of two (the reciprocal of one in this range is a normal number): the
+  // product with the reciprocal is the quotient, exactly.  A cache filled by
+  // other means may hold any scale.
+  const uint32_t bits = __float_as_uint(s);
+  const bool pow2 = (bits & 0x807fffffu) == 0u && bits >= 1u << 23 && bits <= 253u << 23;
+  const float inv = pow2 ? __uint_as_float((254u << 23) - bits) : 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = amax;
-  __syncthreads();  // also: every thread has read the old scale
-  for (int w = 0; w < blockDim.x / 32; ++w) amax = fmaxf(amax, red[w]);
-  const float need = pow2_scale<kE5M2>(amax);
-  const float s = fmaxf(old, need);
-#pragma unroll
-  for (int i = 0; i < kMaxRowsInFlight; ++i) {
-    const int r = r0 + lane_row + i * rows;
-    if (r >= r1) continue;
+  for (int i = 0; i < kPieces; ++i) {
+    if (row + i * step >= r1) continue;
     float v[8];
     unpack8(x[i], v);
     uint2 q = make_uint2(0u, 0u);
-    if (s != 0.f) {
+    if (pow2) {
+      q.x = cvt_f8x2<kE5M2>(v[0] * inv, v[1] * inv) | (cvt_f8x2<kE5M2>(v[2] * inv, v[3] * inv) << 16);
+      q.y = cvt_f8x2<kE5M2>(v[4] * inv, v[5] * inv) | (cvt_f8x2<kE5M2>(v[6] * inv, v[7] * inv) << 16);
+    } else if (s != 0.f) {
       q.x = quant4<kE5M2>(make_float4(v[0], v[1], v[2], v[3]), s);
       q.y = quant4<kE5M2>(make_float4(v[4], v[5], v[6], v[7]), s);
     }
-    *reinterpret_cast<uint2*>(codes + r * dim + col) = q;
+    *reinterpret_cast<uint2*>(codes + (row + i * step) * dim + col) = q;
   }
   if (s > old || r0 == 0) {
-    if (threadIdx.x == 0) *scale = s;
+    if (part == 0 && lane == 0) *scale = s;
     const float ratio = s != 0.f ? __fdiv_rn(old, s) : 1.f;
-    for (int r = lane_row; r < r0; r += rows) {
+    for (int r = row - r0; r < r0; r += step) {
       uint2* p = reinterpret_cast<uint2*>(codes + r * dim + col);
       const uint2 q = *p;
       *p = make_uint2(rescale4<kE5M2>(q.x, ratio), rescale4<kE5M2>(q.y, ratio));
@@ -125,16 +157,16 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendArgs a, in
 }  // namespace
 
 cudaError_t launch_kv_append(const LaunchCtx& c, const KvAppendArgs& a) {
-  const int tpr = a.dim / 8;
-  const int rows = min(a.block, a.max_new);
-  // enough threads for the rows one tile can get: 8 a thread at most
-  const int threads = min(256, ceil_div(rows * tpr, 32) * 32);
-  const dim3 grid((a.max_new + a.block - 2) / a.block + 1, a.heads, 2 * a.B);
+  const int slots = (a.max_new + a.block - 2) / a.block + 1;
+  int log_wpt = 0;
+  while (min(a.block, a.max_new) * a.dim > 32 * 8 * kPieces << log_wpt) ++log_wpt;
+  const long long items = 2LL * a.B * a.heads * slots;
+  const long long grid = ((items << log_wpt) + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const bool e5 = a.fmt == FP8GEMM_FMT_E5M2;
   auto fn = a.dim == 128 ? (e5 ? kv_append_kernel<16, true> : kv_append_kernel<16, false>)
                          : (e5 ? kv_append_kernel<8, true> : kv_append_kernel<8, false>);
-  fn<<<grid, threads, 0, c.stream>>>(a, c.status);
-  return cudaGetLastError();
+  return launch_dependent(c, fn, unsigned(grid), 32 * kWarps, 0, a, slots, log_wpt, c.status);
 }
 
 }  // namespace fp8gemm

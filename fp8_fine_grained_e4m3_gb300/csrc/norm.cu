@@ -28,38 +28,54 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
+// Eight values to codes of one scale.
+template <bool kE5M2>
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, const Reciprocal& d) {
+  const float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
+  if (d.safe) return make_uint2(quant4<kE5M2>(a, d), quant4<kE5M2>(b, d));
+  if (amax == 0.f) return make_uint2(0u, 0u);
+  return make_uint2(quant4<kE5M2>(a, d.s), quant4<kE5M2>(b, d.s));
+}
+
 // One CTA per row; thread t holds elements 8 (t + i blockDim.x) .. + 7 for i < kIter.
 // A 1x128 block is 16 neighbouring threads.
 template <class T, int kIter, bool kE5M2, bool kRes>
-__global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(
+__global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     const T* __restrict__ X, const T* R, const float* __restrict__ G, float eps, T* H,
     uint8_t* __restrict__ Q, float* __restrict__ sQ, float* __restrict__ rstd_out, int K) {
   __shared__ float red[32];
   const size_t row = size_t(blockIdx.x) * K;
   const int Kb = ceil_div(K, kBlockK);
+  griddep_launch_dependents();
+  griddep_wait();
+  Raw8<T> x[kIter], r[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int k = 8 * (threadIdx.x + i * blockDim.x);
+    zero8(x[i]);
+    zero8(r[i]);
+    if (k < K) {
+      x[i] = load8(X + row + k);
+      if constexpr (kRes) r[i] = load8(R + row + k);
+    }
+  }
   float h[kIter][8];
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    const int k = 8 * (threadIdx.x + i * blockDim.x);
-    Raw8<T> x;
-    zero8(x);
-    if (k < K) x = load8(X + row + k);
-    unpack8(x, h[i]);
+    unpack8(x[i], h[i]);
     if constexpr (kRes) {
-      Raw8<T> r;
-      zero8(r);
-      if (k < K) r = load8(R + row + k);
+      const int k = 8 * (threadIdx.x + i * blockDim.x);
       float rv[8];
-      unpack8(r, rv);
+      unpack8(r[i], rv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] += rv[j];
-      pack8(h[i], x);  // what the gradient and the next layer see
-      unpack8(x, h[i]);
-      if (k < K) store8(H + row + k, x);
+      pack8(h[i], x[i]);  // what the gradient and the next layer see
+      unpack8(x[i], h[i]);
+      if (k < K) store8(H + row + k, x[i]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum += h[i][j] * h[i][j];
+    for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
   }
   const float rstd = __frsqrt_rn(__fdiv_rn(cta_sum(sum, red), float(K)) + eps);
   if (threadIdx.x == 0 && rstd_out) rstd_out[blockIdx.x] = rstd;
@@ -76,59 +92,86 @@ __global__ void __launch_bounds__(1024) rmsnorm_quant_kernel(
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float s = __fdiv_rn(amax, f8_limit<kE5M2>());
+    const Reciprocal s = reciprocal(__fdiv_rn(amax, f8_limit<kE5M2>()));
     if (k < K) {
-      uint2 q = make_uint2(0u, 0u);
-      if (amax != 0.f) {
-        q.x = quant4<kE5M2>(make_float4(h[i][0], h[i][1], h[i][2], h[i][3]), s);
-        q.y = quant4<kE5M2>(make_float4(h[i][4], h[i][5], h[i][6], h[i][7]), s);
-      }
-      *reinterpret_cast<uint2*>(Q + row + k) = q;
-      if (threadIdx.x % 16 == 0) sQ[size_t(blockIdx.x) * Kb + k / kBlockK] = s;
+      *reinterpret_cast<uint2*>(Q + row + k) = quant8<kE5M2>(h[i], amax, s);
+      if (threadIdx.x % 16 == 0) sQ[size_t(blockIdx.x) * Kb + k / kBlockK] = s.s;
     }
   }
 }
 
 // CTA c takes rows c, c + gridDim.x, ...; thread t owns columns
 // 8 (t + i blockDim.x) .. + 7 of every one of them, so its share of the gain's
-// gradient stays in registers until the CTA leaves it in row c of `part`.
+// gradient stays in registers until the CTA leaves it in row c of `part`.  The
+// next row is asked for before this one is used.
 template <class T, int kIter, bool kRes>
-__global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(
-    const T* __restrict__ dY, const T* __restrict__ H, const float* __restrict__ rstd_in,
+__global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
+    const T* dY, const T* __restrict__ H, const float* __restrict__ rstd_in,
     const float* __restrict__ G, const T* dH, T* dX, float* __restrict__ part, int M, int K) {
   __shared__ float red[2][32];
-  float g[kIter][8], dg[kIter][8];
+  griddep_launch_dependents();
+  griddep_wait();
+  struct Row {
+    Raw8<T> dy[kIter], h[kIter], up[kIter];
+    float rstd;
+  } next;
+  auto load = [&](int m) {
+    const size_t row = size_t(m) * K;
+    next.rstd = rstd_in[m];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int k = 8 * (threadIdx.x + i * blockDim.x);
+      zero8(next.dy[i]);
+      zero8(next.h[i]);
+      zero8(next.up[i]);
+      if (k < K) {
+        next.dy[i] = load8(dY + row + k);
+        next.h[i] = load8(H + row + k);
+        if constexpr (kRes) next.up[i] = load8(dH + row + k);
+      }
+    }
+  };
+  constexpr bool kAhead = kIter < 4;  // else a thread's registers hold one row only
+  if (int(blockIdx.x) < M) load(blockIdx.x);
+  float dg[kIter][8];
+  Raw8<float> g[kAhead ? kIter : 1];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const int k = 8 * (threadIdx.x + i * blockDim.x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[i][j] = dg[i][j] = 0.f;
-    if (k < K) unpack8(load8(G + k), g[i]);
+    for (int j = 0; j < 8; ++j) dg[i][j] = 0.f;
+    if constexpr (kAhead) {
+      zero8(g[i]);
+      if (k < K) g[i] = load8(G + k);
+    }
   }
+  auto gain = [&](int i, float (&v)[8]) {
+    const int k = 8 * (threadIdx.x + i * blockDim.x);
+    if constexpr (kAhead) {
+      unpack8(g[i], v);
+    } else {
+      Raw8<float> r;
+      zero8(r);
+      if (k < K) r = load8(G + k);
+      unpack8(r, v);
+    }
+  };
   int flip = 0;  // two buffers: a row's sums are read while the next row's are written
   for (int m = blockIdx.x; m < M; m += gridDim.x, flip ^= 1) {
-    const size_t row = size_t(m) * K;
-    const float rstd = rstd_in[m];
-    float xh[kIter][8], dx[kIter][8];
+    const Row here = next;
+    if (kAhead && m + int(gridDim.x) < M) load(m + gridDim.x);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-      const int k = 8 * (threadIdx.x + i * blockDim.x);
-      Raw8<T> h, dy;
-      zero8(h);
-      zero8(dy);
-      if (k < K) {
-        h = load8(H + row + k);
-        dy = load8(dY + row + k);
-      }
-      unpack8(h, xh[i]);
-      unpack8(dy, dx[i]);
+      float xh[8], dx[8], w[8];
+      unpack8(here.h[i], xh);
+      unpack8(here.dy[i], dx);
+      gain(i, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= rstd;
-        dg[i][j] += dx[i][j] * xh[i][j];
-        dx[i][j] *= g[i][j];
-        sum += dx[i][j] * xh[i][j];
+        xh[j] *= here.rstd;
+        dg[i][j] = fmaf(dx[j], xh[j], dg[i][j]);
+        sum = fmaf(dx[j] * w[j], xh[j], sum);
       }
     }
     const float c = __fdiv_rn(cta_sum(sum, red[flip]), float(K));
@@ -136,14 +179,19 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(
     for (int i = 0; i < kIter; ++i) {
       const int k = 8 * (threadIdx.x + i * blockDim.x);
       if (k >= K) continue;
-      float up[8] = {};
-      if constexpr (kRes) unpack8(load8(dH + row + k), up);
+      float xh[8], dx[8], up[8], w[8];
+      gain(i, w);
+      unpack8(here.h[i], xh);
+      unpack8(here.dy[i], dx);
+      unpack8(here.up[i], up);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dx[i][j] = (dx[i][j] - xh[i][j] * c) * rstd + up[j];
+      for (int j = 0; j < 8; ++j)
+        dx[j] = fmaf(fmaf(-(xh[j] * here.rstd), c, dx[j] * w[j]), here.rstd, kRes ? up[j] : 0.f);
       Raw8<T> o;
-      pack8(dx[i], o);
-      store8(dX + row + k, o);
+      pack8(dx, o);
+      store8(dX + size_t(m) * K + k, o);
     }
+    if (!kAhead && m + int(gridDim.x) < M) load(m + gridDim.x);
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
@@ -162,8 +210,12 @@ __global__ void __launch_bounds__(1024) gain_reduce_kernel(const float* __restri
   __shared__ float s[32][33];
   const int k = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (k < K)
+  griddep_launch_dependents();
+  griddep_wait();
+  if (k < K) {
+#pragma unroll 8
     for (int p = threadIdx.y; p < P; p += 32) v += part[size_t(p) * K + k];
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = warp_sum(s[threadIdx.x][threadIdx.y]);
@@ -171,11 +223,22 @@ __global__ void __launch_bounds__(1024) gain_reduce_kernel(const float* __restri
   if (threadIdx.x == 0 && kk < K) dG[kk] = v;
 }
 
-// Threads of a row's CTA, and 8-element chunks a thread holds (K <= kMaxNormK).
-void row_shape(int K, int* threads, int* iter) {
+// A row's CTA: iter chunks of 8 elements a thread (K <= kMaxNormK).
+struct RowShape {
+  int threads, iter;
+};
+RowShape row_shape(int chunks, int iter) { return {ceil_div(ceil_div(chunks, iter), 32) * 32, iter}; }
+
+// A few rows want the most threads for the least latency; with rows enough for
+// every SM, several chunks a thread keep more rows in flight between their barriers.
+RowShape forward_shape(const LaunchCtx& c, int M, int K) {
   const int chunks = ceil_div(K, 8);
-  *iter = chunks > 1024 ? 2 : 1;
-  *threads = ceil_div(ceil_div(chunks, *iter), 32) * 32;
+  if (M < 2 * c.num_sms) return row_shape(chunks, chunks > 1024 ? 2 : 1);
+  return row_shape(chunks, chunks >= 256 ? 4 : chunks >= 64 ? 2 : 1);
+}
+RowShape backward_shape(int K) {
+  const int chunks = ceil_div(K, 8);
+  return row_shape(chunks, chunks > 1024 ? 4 : chunks > 512 ? 2 : 1);
 }
 
 template <class T, int kIter>
@@ -188,56 +251,61 @@ cudaError_t launch_fwd(const LaunchCtx& c, const NormArgs& a, int threads) {
                     : rmsnorm_quant_kernel<T, kIter, false, true>)
               : (e5 ? rmsnorm_quant_kernel<T, kIter, true, false>
                     : rmsnorm_quant_kernel<T, kIter, false, false>);
-  fn<<<a.M, threads, 0, c.stream>>>(X, R, a.G, a.eps, H, a.Q, a.sQ, a.rstd, a.K);
-  return cudaGetLastError();
+  return launch_dependent(c, fn, a.M, threads, 0, X, R, a.G, a.eps, H, a.Q, a.sQ, a.rstd, a.K);
 }
 
 template <class T, int kIter>
 cudaError_t launch_bwd(const LaunchCtx& c, const NormGradArgs& a, int threads, int grid,
                        float* part) {
   auto fn = a.dH ? rmsnorm_backward_kernel<T, kIter, true> : rmsnorm_backward_kernel<T, kIter, false>;
-  fn<<<grid, threads, 0, c.stream>>>(static_cast<const T*>(a.dY), static_cast<const T*>(a.H),
-                                     a.rstd, a.G, static_cast<const T*>(a.dH),
-                                     static_cast<T*>(a.dX), part, a.M, a.K);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  gain_reduce_kernel<<<ceil_div(a.K, 32), dim3(32, 32), 0, c.stream>>>(part, a.dG, grid, a.K);
-  return cudaGetLastError();
+  if (cudaError_t e = launch_dependent(c, fn, grid, threads, 0, static_cast<const T*>(a.dY),
+                                       static_cast<const T*>(a.H), a.rstd, a.G,
+                                       static_cast<const T*>(a.dH), static_cast<T*>(a.dX), part,
+                                       a.M, a.K))
+    return e;
+  return launch_dependent(c, gain_reduce_kernel, ceil_div(a.K, 32), dim3(32, 32), 0, part, a.dG, grid,
+                          a.K);
 }
 
-int bwd_grid(const LaunchCtx& c, int M, int threads) {
-  return min(M, c.num_sms * max(1, 1536 / threads));
+// CTAs that run at once: 64 registers a thread with one chunk, 128 with more.
+int backward_grid(const LaunchCtx& c, int M, const RowShape& s) {
+  return min(M, c.num_sms * max(1, (s.iter == 1 ? 1024 : 512) / s.threads));
+}
+
+template <class T>
+cudaError_t launch_fwd(const LaunchCtx& c, const NormArgs& a) {
+  const RowShape s = forward_shape(c, a.M, a.K);
+  switch (s.iter) {
+    case 1: return launch_fwd<T, 1>(c, a, s.threads);
+    case 2: return launch_fwd<T, 2>(c, a, s.threads);
+    default: return launch_fwd<T, 4>(c, a, s.threads);
+  }
+}
+
+template <class T>
+cudaError_t launch_bwd(const LaunchCtx& c, const NormGradArgs& a, float* part) {
+  const RowShape s = backward_shape(a.K);
+  const int grid = backward_grid(c, a.M, s);
+  switch (s.iter) {
+    case 1: return launch_bwd<T, 1>(c, a, s.threads, grid, part);
+    case 2: return launch_bwd<T, 2>(c, a, s.threads, grid, part);
+    default: return launch_bwd<T, 4>(c, a, s.threads, grid, part);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm_quant(const LaunchCtx& c, const NormArgs& a) {
-  int threads, iter;
-  row_shape(a.K, &threads, &iter);
-  switch (iter) {
-    case 1: return a.f32 ? launch_fwd<float, 1>(c, a, threads) : launch_fwd<__nv_bfloat16, 1>(c, a, threads);
-    default: return a.f32 ? launch_fwd<float, 2>(c, a, threads) : launch_fwd<__nv_bfloat16, 2>(c, a, threads);
-  }
+  return a.f32 ? launch_fwd<float>(c, a) : launch_fwd<__nv_bfloat16>(c, a);
 }
 
 size_t rmsnorm_backward_workspace_bytes(const LaunchCtx& c, int M, int K) {
-  int threads, iter;
-  row_shape(K, &threads, &iter);
-  return size_t(bwd_grid(c, M, threads)) * K * 4;
+  return size_t(backward_grid(c, M, backward_shape(K))) * K * 4;
 }
 
 cudaError_t launch_rmsnorm_backward(const LaunchCtx& c, const NormGradArgs& a, void* ws) {
-  int threads, iter;
-  row_shape(a.K, &threads, &iter);
-  const int grid = bwd_grid(c, a.M, threads);
   float* part = static_cast<float*>(ws);
-  switch (iter) {
-    case 1:
-      return a.f32 ? launch_bwd<float, 1>(c, a, threads, grid, part)
-                   : launch_bwd<__nv_bfloat16, 1>(c, a, threads, grid, part);
-    default:
-      return a.f32 ? launch_bwd<float, 2>(c, a, threads, grid, part)
-                   : launch_bwd<__nv_bfloat16, 2>(c, a, threads, grid, part);
-  }
+  return a.f32 ? launch_bwd<float>(c, a, part) : launch_bwd<__nv_bfloat16>(c, a, part);
 }
 
 }  // namespace fp8gemm
