@@ -6,6 +6,8 @@
 // "lpnh.cn/news/2822121" section 6.3: round to nearest).
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include <cstdint>
 
 #include "common.cuh"
@@ -72,6 +74,24 @@ __device__ __forceinline__ uint32_t quant4(float4 v, const Reciprocal& d) {
 
 __device__ __forceinline__ float absmax4(float4 v) {
   return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+}
+
+// Two FP8 bytes as an FP16 pair (low byte in the low half): exact for both
+// formats.
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t f8x2_to_f16x2(uint16_t v) {
+  uint32_t r;
+  if constexpr (kE5M2)
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(r) : "h"(v));
+  else
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+
+template <bool kE5M2>
+__device__ __forceinline__ float2 f8x2_to_float2(uint16_t v) {
+  const uint32_t h = f8x2_to_f16x2<kE5M2>(v);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 }  // namespace fp8gemm

@@ -22,6 +22,7 @@
 // bits, far below the BF16 output's step).  Scores, statistics, sums and the
 // output accumulate in FP32; a tile's scales are applied to its FP32 products.
 #include "common.cuh"
+#include "f8_convert.cuh"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -38,15 +39,6 @@ constexpr int kUnit = kWarps * kTok;  // tokens of a unit: a tile for each warp
 constexpr int kMinUnits = 2;  // a CTA's least share: fewer would cost more to join than to do
 constexpr int kStages = 2;  // tiles of a warp in shared memory
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // Transposes an 8x8 matrix of 16-bit elements held two to a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {

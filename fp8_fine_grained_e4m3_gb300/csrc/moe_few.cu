@@ -19,7 +19,7 @@
 // bytes whatever the number of experts.  A warp owns a share of a tile's rows
 // and works on its own: one lane asks for the weights ahead (TMA into the
 // warp's ring, across tile ends), and the 128-byte swizzle gives every lane its
-// share of an m16n8k32 fragment without a bank conflict.  Weight rows are the
+// share of an m16n8k16 fragment (FP8 codes are exact in FP16) without a bank conflict.  Weight rows are the
 // 16-row side, tokens the 8-column side; a contraction's order is free, so a
 // lane's share of a row's K block is 32 neighbouring bytes.  A tile that lies in
 // several runs is joined from FP32 partials, in CTA order, by the CTA that
@@ -42,15 +42,6 @@ template <int NT>
 constexpr int kPerSm = NT == 4 ? 2 : 3;
 constexpr int kMaxPerSm = 3;
 constexpr int kMinUnits = 2;  // K blocks a CTA takes at least
-
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // A lane's share of one row's K block, bytes 32 t .. + 31.
 struct Chunk {
@@ -87,13 +78,40 @@ __device__ __forceinline__ Chunk tile_chunk(const uint8_t* tile, int r, int t) {
   return c;
 }
 
-// One K block of 16 weight rows (lo: rows 0-7, hi: rows 8-15) times 8 tokens.
-__device__ __forceinline__ void mma_block(float (&d)[4], const Chunk& lo, const Chunk& hi,
-                                          const Chunk& x) {
+// The FP16 pairs of a chunk: word j of it is what a lane holds of k16 step j.
+// (The m16n8k32 product of e4m3 operands takes more instructions on this GPU: it
+// converts both operands anew for every fragment of tokens.)
+struct Halves {
+  uint32_t lo[8], hi[8];
+};
+__device__ __forceinline__ Halves halves(const Chunk& c) {
+  Halves h;
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    mma_e4m3(d, lo.w[2 * s], hi.w[2 * s], lo.w[2 * s + 1], hi.w[2 * s + 1], x.w[2 * s],
-             x.w[2 * s + 1]);
+  for (int j = 0; j < 8; ++j) {
+    h.lo[j] = f8x2_to_f16x2<false>(uint16_t(c.w[j]));
+    h.hi[j] = f8x2_to_f16x2<false>(uint16_t(c.w[j] >> 16));
+  }
+  return h;
+}
+
+// One K block of 16 weight rows (lo: rows 0-7, hi: rows 8-15) times up to 8 NT
+// tokens: d[n] for the fragments that hold any of the cnt tokens.
+template <int NT>
+__device__ __forceinline__ void mma_block(float (&d)[NT][4], const Chunk& lo, const Chunk& hi,
+                                          const Halves (&x)[NT], int cnt) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) d[n][c] = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t a[4] = {
+        f8x2_to_f16x2<false>(uint16_t(lo.w[j])), f8x2_to_f16x2<false>(uint16_t(hi.w[j])),
+        f8x2_to_f16x2<false>(uint16_t(lo.w[j] >> 16)), f8x2_to_f16x2<false>(uint16_t(hi.w[j] >> 16))};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n == 0 || 8 * n < cnt) mma_f16(d[n], a, x[n].lo[j], x[n].hi[j]);
+  }
 }
 
 // ------------------------------------------------------------------ routing
@@ -421,38 +439,54 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
     for (int m = 0; m < 2; ++m)
       su[m] = s + size_t(min((a.I + ib * kBlockK + 32 * warp + 16 * m) / kBlockK, Rb - 1)) * Kb;
   };
+  // loaded a unit ahead of its use
+  Halves xc[NT];
+  Chunk next_x[NT];
+  float sxk[NT][2], next_sx[NT][2], sw[3], next_sw[3];
+  auto load_side = [&](int k) {
+    const bool in[2] = {k * kBlockK + 32 * t < a.H, k * kBlockK + 32 * t + 16 < a.H};
+    next_sw[0] = sg[k];
+    next_sw[1] = su[0][k];
+    next_sw[2] = su[1][k];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (8 * n >= at.cnt) break;
+      next_x[n] = load_chunk(x[n] + k * kBlockK, in);
+      next_sx[n][0] = sx[n][0][k];
+      next_sx[n][1] = sx[n][1][k];
+    }
+  };
   enter_pass();
   enter_tile();
+  load_side(kb);
 
   float acc[4][NT][4] = {};
   int stage = 0;
   bool dead = false;
   while (true) {
-    const float sw[3] = {sg[kb], su[0][kb], su[1][kb]};
-    const bool in[2] = {kb * kBlockK + 32 * t < a.H, kb * kBlockK + 32 * t + 16 < a.H};
-    Chunk xc[NT];
-    float sxk[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (8 * n >= at.cnt) break;
-      xc[n] = load_chunk(x[n] + kb * kBlockK, in);
-      sxk[n][0] = sx[n][0][kb];
-      sxk[n][1] = sx[n][1][kb];
+      xc[n] = halves(next_x[n]);
+      sxk[n][0] = next_sx[n][0];
+      sxk[n][1] = next_sx[n][1];
     }
+#pragma unroll
+    for (int m = 0; m < 3; ++m) sw[m] = next_sw[m];
+    if (kb + 1 < Kb && left > 1) load_side(kb + 1);
     // After a wait that ran out the warp only keeps the others' barriers company.
     dead = dead || !ring.wait(stage, &sh.gave_up, &sh.never, status, a.wait_ns);
     const uint8_t* w = ring.stage(stage);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const Chunk lo = tile_chunk(w, 16 * m + g, t), hi = tile_chunk(w, 16 * m + 8 + g, t);
+      float d[NT][4];
+      mma_block<NT>(d, lo, hi, xc, at.cnt);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (8 * n >= at.cnt) break;
-        float d[4] = {};
-        mma_block(d, lo, hi, xc[n]);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          acc[m][n][c] = fmaf(d[c], sxk[n][c & 1] * sw[m < 2 ? 0 : m - 1], acc[m][n][c]);
+          acc[m][n][c] = fmaf(d[n][c], sxk[n][c & 1] * sw[m < 2 ? 0 : m - 1], acc[m][n][c]);
       }
     }
     __syncwarp();  // the stage has been read
@@ -571,6 +605,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
       enter_pass();
     }
     enter_tile();
+    load_side(0);
   }
 }
 
@@ -578,10 +613,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
 // 128 output columns; warp w takes columns 32 w .. + 31 and keeps a sum per token
 // in shared memory that no other warp touches.
 //   partial: [warp][token][32] floats
-constexpr int kDownStages = 4;
 constexpr int kSumRow = 36;  // floats from token to token: lanes of a fragment hit all banks
 
-template <int NT>
+template <int NT, int kDownStages>
 __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const MoeArgs a, const Route given,
                                                                const __grid_constant__ CUtensorMap map,
                                                                const uint8_t* H8, const float* sH,
@@ -657,35 +691,47 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
         sx[n][c] = sH + size_t(r.list[at.first + min(8 * n + 2 * t + c, at.cnt - 1)]) * Kb;
     }
   };
+  // loaded a unit ahead of its use
+  Halves xc[NT];
+  Chunk next_x[NT];
+  float sxk[NT][2], next_sx[NT][2], next_sw = 0.f;
+  auto load_side = [&](int k) {
+    const bool in[2] = {k * kBlockK + 32 * t < a.I, k * kBlockK + 32 * t + 16 < a.I};
+    next_sw = sw[k];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (8 * n >= at.cnt) break;
+      next_x[n] = load_chunk(x[n] + k * kBlockK, in);
+      next_sx[n][0] = sx[n][0][k];
+      next_sx[n][1] = sx[n][1][k];
+    }
+  };
   enter();
+  load_side(kb);
 
   float acc[2][NT][4] = {};
   int stage = 0;
   bool dead = false;
   while (true) {
-    const float swk = sw[kb];
-    const bool in[2] = {kb * kBlockK + 32 * t < a.I, kb * kBlockK + 32 * t + 16 < a.I};
-    Chunk xc[NT];
-    float sxk[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (8 * n >= at.cnt) break;
-      xc[n] = load_chunk(x[n] + kb * kBlockK, in);
-      sxk[n][0] = sx[n][0][kb] * swk;
-      sxk[n][1] = sx[n][1][kb] * swk;
+      xc[n] = halves(next_x[n]);
+      sxk[n][0] = next_sx[n][0] * next_sw;
+      sxk[n][1] = next_sx[n][1] * next_sw;
     }
+    if (kb + 1 < Kb && left > 1) load_side(kb + 1);
     dead = dead || !ring.wait(stage, &sh.gave_up, &sh.never, status, a.wait_ns);
     const uint8_t* w = ring.stage(stage);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const Chunk lo = tile_chunk(w, 16 * m + g, t), hi = tile_chunk(w, 16 * m + 8 + g, t);
+      float d[NT][4];
+      mma_block<NT>(d, lo, hi, xc, at.cnt);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         if (8 * n >= at.cnt) break;
-        float d[4] = {};
-        mma_block(d, lo, hi, xc[n]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][n][c] = fmaf(d[c], sxk[n][c & 1], acc[m][n][c]);
+        for (int c = 0; c < 4; ++c) acc[m][n][c] = fmaf(d[n][c], sxk[n][c & 1], acc[m][n][c]);
       }
     }
     __syncwarp();  // the stage has been read
@@ -721,8 +767,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
       pi = 0;
       ++tile;
     }
-    if (left > 0) enter();
-    if (left > 0 && tile == this_tile) continue;
+    if (left > 0) {
+      enter();
+      load_side(0);
+      if (tile == this_tile) continue;
+    }
 
     const long long tile0 = this_tile * per_tile;
     // the run's share of this tile is done
@@ -776,7 +825,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
 }
 
 // ------------------------------------------------------------------- launches
-int fragments(const MoeArgs& a) { return a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4; }
+// Fragments of 8 tokens that a pass takes.  Two keep three CTAs on an SM; four
+// save passes over the weights where an expert has more than 16 tokens as a rule
+// (64 tokens through 4 of 32 experts, 8 each: 2 fragments ... us, 4 ... us).
+int fragments(const MoeArgs& a) {
+  return a.T <= 8 ? 1 : a.T <= 16 || a.T * a.k <= 12 * a.E ? 2 : 4;
+}
+
+// Shared memory of an SM, what a CTA takes of it beside its dynamic part (1 KB of
+// the system's and the kernel's static part), and the most a CTA may ask for.
+constexpr size_t kSmemPerSm = 228 * 1024, kSmemReserved = 1024 + 2048, kMaxSmem = 200 * 1024;
+constexpr int kManyStages = 3;
 
 struct Layout {
   size_t counters, h8, sh, weight, list, pass, passes, up, down, total;
@@ -804,7 +863,7 @@ Layout layout(const LaunchCtx& c, const MoeArgs& a) {
   return l;
 }
 
-template <int NT>
+template <int NT, int kDownStages>
 cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char* ws,
                       const Layout& l) {
   CUtensorMap m1, m2;
@@ -818,13 +877,12 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   const size_t up_smem = 1024 + size_t(kWarps) * kUpStages<NT> * 64 * kBlockK;
   const size_t down_smem =
       1024 + size_t(kWarps) * (kDownStages * 32 * kBlockK + size_t(a.T) * kSumRow * 4);
-  const size_t down_most =
-      1024 + size_t(kWarps) * (kDownStages * 32 * kBlockK + size_t(kMoeMaxTokens) * kSumRow * 4);
+  const int down_per_sm = min(kPerSm<NT>, int(kSmemPerSm / (down_smem + kSmemReserved)));
   auto up = moe_up_kernel<NT>;
-  auto down = moe_down_kernel<NT>;
+  auto down = moe_down_kernel<NT, kDownStages>;
   static SmemLimit up_limit, down_limit;
   if (cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(up), up_smem)) return e;
-  if (cudaError_t e = down_limit.raise(reinterpret_cast<const void*>(down), down_most)) return e;
+  if (cudaError_t e = down_limit.raise(reinterpret_cast<const void*>(down), kMaxSmem)) return e;
   if constexpr (!kOwnRoute<NT>)
     if (cudaError_t e = launch_dependent(c, moe_route_kernel, 1, 1024, 0, a.logits, r, a.ids,
                                          a.weights, a.T, a.E, a.k, a.renormalise, 8 * NT))
@@ -832,7 +890,7 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   if (cudaError_t e = launch_dependent(c, up, grid, kThreads, up_smem, a, r, m1, H8, sH, counters,
                                        reinterpret_cast<float*>(ws + l.up), c.status))
     return e;
-  return launch_dependent(c, down, grid, kThreads, down_smem, a, r, m2, H8, sH,
+  return launch_dependent(c, down, down_per_sm * c.num_sms, kThreads, down_smem, a, r, m2, H8, sH,
                           counters + kMaxPerSm * c.num_sms, reinterpret_cast<float*>(ws + l.down), c.status);
 }
 
@@ -847,9 +905,9 @@ cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace
                 reinterpret_cast<uint32_t*>(ws + l.pass), reinterpret_cast<int*>(ws + l.passes)};
   *launches = a.T <= kOwnTokens ? 2 : 3;
   switch (fragments(a)) {
-    case 1: return launch_nt<1>(c, a, r, ws, l);
-    case 2: return launch_nt<2>(c, a, r, ws, l);
-    default: return launch_nt<4>(c, a, r, ws, l);
+    case 1: return launch_nt<1, 4>(c, a, r, ws, l);
+    case 2: return a.T <= 16 ? launch_nt<2, 4>(c, a, r, ws, l) : launch_nt<2, kManyStages>(c, a, r, ws, l);
+    default: return launch_nt<4, 4>(c, a, r, ws, l);
   }
 }
 

@@ -360,6 +360,17 @@ __device__ __forceinline__ void tmem_ld_wait_tied16(uint32_t (&r)[16]) {
       : "memory");
 }
 
+// ------------------------------------------------- warp-level matrix product
+// D += A * B, m16n8k16, FP16 operands and FP32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // Per-warpgroup register budget changes (all four warps of a warpgroup
 // execute the same instruction).  The sum over warpgroups must stay within
 // the registers the CTA was launched with.
