@@ -298,6 +298,23 @@ static_assert(kOwnPairs <= 32 * kWarps, "a thread for each pair");
 template <int NT>
 constexpr bool kOwnRoute = 8 * NT <= kOwnTokens;
 
+// The routing of a launch before, copied into shared memory at `to` (12 bytes a
+// pair; 8 without the weights): a change of pass then waits for nothing.
+__device__ __forceinline__ Route copy_route(const Route& g, uint8_t* to, int pairs, bool weights) {
+  Route r;
+  r.pass = reinterpret_cast<uint32_t*>(to);
+  r.list = reinterpret_cast<int*>(r.pass + pairs);
+  r.weight = reinterpret_cast<float*>(r.list + pairs);
+  r.passes = g.passes;
+  for (int i = threadIdx.x; i < pairs; i += kThreads) {
+    r.pass[i] = __ldcg(g.pass + i);  // past the last pass: not used
+    r.list[i] = __ldcg(g.list + i);
+    if (weights) r.weight[i] = __ldcg(g.weight + i);
+  }
+  __syncthreads();
+  return r;
+}
+
 // ------------------------------------------------------------ product kernels
 // A CTA's run of the unit sequence.
 struct Run {
@@ -383,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
                       a.k, a.renormalise, 8 * NT);
     fence_proxy_async_smem();
     __syncthreads();
+  } else {
+    r = copy_route(given, rings + kWarps * kUpStages<NT> * 64 * kBlockK, a.T * a.k, false);
   }
   const Run run((long long)*r.passes * Ib * Kb);
   int left = run.units();
@@ -639,6 +658,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
     route_all<kWarps>(a.logits, r, rings, nullptr, nullptr, a.T, a.E, a.k, a.renormalise, 8 * NT);
     fence_proxy_async_smem();
     __syncthreads();
+  } else {
+    r = copy_route(given, reinterpret_cast<uint8_t*>(all_sums + kWarps * a.T * kSumRow), a.T * a.k, true);
   }
   const int passes = *r.passes;
   const long long per_tile = (long long)passes * Kb;
@@ -671,7 +692,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
   };
 #pragma unroll
   for (int i = 0; i < kDownStages; ++i) fetch();
-  griddep_launch_dependents();
+  // No early launch of what follows: the next call's routing takes a whole SM's
+  // registers, which this kernel's CTAs would go without (64 tokens: 300 us a
+  // call with it, 261 without).
   griddep_wait();
 
   // What a unit needs besides weights.  Columns without a pair take the
@@ -740,14 +763,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
     ++kb;
     --left;
     if (kb < Kb && left > 0) continue;
+    const int this_tile = tile;
+    const Pass done = at;
+    kb = 0;
+    if (++pi == passes) {
+      pi = 0;
+      ++tile;
+    }
+    if (left > 0) {  // the next pass's activations are on their way meanwhile
+      enter();
+      load_side(0);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if (8 * n >= at.cnt) break;
+      if (8 * n >= done.cnt) break;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int j = 8 * n + 2 * t + c;
-        if (j < at.cnt) {
-          const int pair = r.list[at.first + j];
+        if (j < done.cnt) {
+          const int pair = r.list[done.first + j];
           const float wt = r.weight[pair];
           float* s = sums + pair / a.k * kSumRow + g;
 #pragma unroll
@@ -761,17 +795,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
       }
     }
     __syncwarp();
-    const int this_tile = tile;
-    kb = 0;
-    if (++pi == passes) {
-      pi = 0;
-      ++tile;
-    }
-    if (left > 0) {
-      enter();
-      load_side(0);
-      if (tile == this_tile) continue;
-    }
+    if (left > 0 && tile == this_tile) continue;
 
     const long long tile0 = this_tile * per_tile;
     // the run's share of this tile is done
@@ -832,10 +856,13 @@ int fragments(const MoeArgs& a) {
   return a.T <= 8 ? 1 : a.T <= 16 || a.T * a.k <= 12 * a.E ? 2 : 4;
 }
 
-// Shared memory of an SM, what a CTA takes of it beside its dynamic part (1 KB of
-// the system's and the kernel's static part), and the most a CTA may ask for.
-constexpr size_t kSmemPerSm = 228 * 1024, kSmemReserved = 1024 + 2048, kMaxSmem = 200 * 1024;
-constexpr int kManyStages = 3;
+// Shared memory of an SM, and the most a CTA may ask for.
+constexpr size_t kSmemPerSm = 228 * 1024, kMaxSmem = 200 * 1024;
+// CTAs that an SM holds: a CTA takes 1 KB of the system's beside its own.
+int per_sm(int most, size_t dynamic, size_t fixed) {
+  return max(1, min(most, int(kSmemPerSm / (dynamic + fixed + 1024))));
+}
+constexpr int kManyStages = 2;
 
 struct Layout {
   size_t counters, h8, sh, weight, list, pass, passes, up, down, total;
@@ -873,21 +900,22 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   uint8_t* H8 = reinterpret_cast<uint8_t*>(ws + l.h8);
   float* sH = reinterpret_cast<float*>(ws + l.sh);
   int* counters = reinterpret_cast<int*>(ws + l.counters);
-  const int grid = kPerSm<NT> * c.num_sms;
-  const size_t up_smem = 1024 + size_t(kWarps) * kUpStages<NT> * 64 * kBlockK;
-  const size_t down_smem =
-      1024 + size_t(kWarps) * (kDownStages * 32 * kBlockK + size_t(a.T) * kSumRow * 4);
-  const int down_per_sm = min(kPerSm<NT>, int(kSmemPerSm / (down_smem + kSmemReserved)));
+  const size_t pairs = kOwnRoute<NT> ? 0 : size_t(a.T) * a.k;
+  const size_t up_smem = 1024 + size_t(kWarps) * kUpStages<NT> * 64 * kBlockK + 8 * pairs;
+  const size_t down_smem = 1024 + size_t(kWarps) * kDownStages * 32 * kBlockK +
+                           size_t(kWarps) * a.T * kSumRow * 4 + 12 * pairs;
+  const int up_per_sm = per_sm(kPerSm<NT>, up_smem, 3 * 1024);
+  const int down_per_sm = per_sm(kPerSm<NT>, down_smem, 2 * 1024);
   auto up = moe_up_kernel<NT>;
   auto down = moe_down_kernel<NT, kDownStages>;
   static SmemLimit up_limit, down_limit;
-  if (cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(up), up_smem)) return e;
+  if (cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(up), kMaxSmem)) return e;
   if (cudaError_t e = down_limit.raise(reinterpret_cast<const void*>(down), kMaxSmem)) return e;
   if constexpr (!kOwnRoute<NT>)
     if (cudaError_t e = launch_dependent(c, moe_route_kernel, 1, 1024, 0, a.logits, r, a.ids,
                                          a.weights, a.T, a.E, a.k, a.renormalise, 8 * NT))
       return e;
-  if (cudaError_t e = launch_dependent(c, up, grid, kThreads, up_smem, a, r, m1, H8, sH, counters,
+  if (cudaError_t e = launch_dependent(c, up, up_per_sm * c.num_sms, kThreads, up_smem, a, r, m1, H8, sH, counters,
                                        reinterpret_cast<float*>(ws + l.up), c.status))
     return e;
   return launch_dependent(c, down, down_per_sm * c.num_sms, kThreads, down_smem, a, r, m2, H8, sH,
