@@ -34,10 +34,11 @@ constexpr int kFrag = 16;          // tokens of a fragment
 constexpr int kTok = 2 * kFrag;    // tokens of a tile: two fragments, whose chains of
                                    // dependent instructions run side by side
 constexpr int kRows = 8;   // query rows per fragment
-constexpr int kWarps = 4;
-constexpr int kUnit = kWarps * kTok;  // tokens of a unit: a tile for each warp
-constexpr int kMinUnits = 2;  // a CTA's least share: fewer would cost more to join than to do
+// A unit is kWarps tiles, one for each warp of a CTA.  A CTA's least share of
+// 256 tokens or more: fewer would cost more to join than to do.
+constexpr int min_units(int warps) { return warps >= 8 ? 1 : 8 / warps; }
 constexpr int kStages = 2;  // tiles of a warp in shared memory
+constexpr float kNone = -1e30f;  // the running maximum of nothing: below any score
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
 
 // Transposes an 8x8 matrix of 16-bit elements held two to a lane.
@@ -155,7 +156,7 @@ struct State {
 
 template <int kDim>
 __device__ __forceinline__ void clear(State<kDim>& s) {
-  s.m[0] = s.m[1] = -INFINITY;
+  s.m[0] = s.m[1] = kNone;
   s.l[0] = s.l[1] = 0.f;
 #pragma unroll
   for (int j = 0; j < kDim / 16; ++j)
@@ -169,14 +170,15 @@ __device__ __forceinline__ void clear(State<kDim>& s) {
 constexpr float kUnitLow = 1.f / 64, kUnitFar = 1152921504606846976.f;
 
 // One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
-// fragment i sees (may be negative or past its end).  there: bit h where
+// fragment i sees (may be negative or past its end); least_limit: of the row that sees
+// the fewest.  there: bit h where
 // fragment h of the tile is; valid: its tokens that exist; ks, vs: the scales
 // of its fragments.
 template <int kDim, bool kE5M2, int kNR>
 __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
                                             const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
-                                            const int (&limit)[kNR][2], int tok, uint32_t there,
-                                            int valid, const float (&ks)[2], const float (&vs)[2],
+                                            const int (&limit)[kNR][2], int least_limit, int tok,
+                                            uint32_t there, int valid, const float (&ks)[2], const float (&vs)[2],
                                             int lane) {
   const int g = lane / 4, t = lane % 4;
   float c[2][kNR][4] = {};
@@ -206,32 +208,52 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
           mma_f16(c[h][i], a, q[i].b[4 * cc + w][0], q[i].b[4 * cc + w][1]);
       }
   }
-  // scores in powers of two; element 2e + r: token g + 8e, row r
+  // y: scores in powers of two, less the running maximum; element 2e + r: token g + 8e, row r
+  float mul[2][kNR][2], y[2][kNR][4];
   bool rises = false;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < kNR; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        c[h][i][e] = c[h][i][e] * (q[i].mul[e & 1] * ks[h]);
-        if (g + 8 * (e >> 1) + kFrag * h + tok >= limit[i][e & 1] || !(there >> h & 1))
-          c[h][i][e] = -INFINITY;
-      }
+      for (int r = 0; r < 2; ++r) mul[h][i][r] = q[i].mul[r] * ks[h];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) rises |= fmaxf(c[h][i][r], c[h][i][2 + r]) > s[i].m[r] + kLazy;
+      for (int e = 0; e < 4; ++e) y[h][i][e] = fmaf(c[h][i][e], mul[h][i][e & 1], -s[i].m[e & 1]);
     }
-  }
+  const bool some_hidden = tok + kTok > least_limit || there != 3u;  // the same for the warp
+  auto hide = [&](float (&v)[2][kNR][4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kNR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g + 8 * (e >> 1) + kFrag * h + tok >= limit[i][e & 1] || !(there >> h & 1))
+            v[h][i][e] = -INFINITY;
+  };
+  if (some_hidden) hide(y);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < kNR; ++i)
+      rises |= fmaxf(fmaxf(y[h][i][0], y[h][i][1]), fmaxf(y[h][i][2], y[h][i][3])) > kLazy;
   if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kNR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[h][i][e] = c[h][i][e] * mul[h][i][e & 1];
+    if (some_hidden) hide(y);
 #pragma unroll
     for (int i = 0; i < kNR; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float top = fmaxf(fmaxf(c[0][i][r], c[0][i][2 + r]), fmaxf(c[1][i][r], c[1][i][2 + r]));
+        float top = fmaxf(fmaxf(y[0][i][r], y[0][i][2 + r]), fmaxf(y[1][i][r], y[1][i][2 + r]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float m = fmaxf(s[i].m[r], top);
-        const float shrink = m == -INFINITY ? 1.f : exp2_fast(s[i].m[r] - m);
+        const float shrink = exp2_fast(s[i].m[r] - m);
         s[i].m[r] = m;
         s[i].l[r] *= shrink;
 #pragma unroll
@@ -240,6 +262,12 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
           s[i].o[j][2 + r] *= shrink;
         }
       }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kNR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[h][i][e] -= s[i].m[e & 1];
   }
   const float top = fmaxf(vs[0], vs[1]);
   if (top > unit || (top < kUnitLow * unit && top * kUnitFar > unit)) {
@@ -255,19 +283,24 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
   uint32_t b[2][kNR][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float to_unit = 1.f;
-    if (vs[h] != unit) to_unit = unit > 0.f ? __fdiv_rn(vs[h], unit) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kNR; ++i) {
+    for (int i = 0; i < kNR; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float m = s[i].m[e & 1];
-        c[h][i][e] = exp2_fast(c[h][i][e] - (m == -INFINITY ? 0.f : m));
-        s[i].l[e & 1] += c[h][i][e];
-        c[h][i][e] *= to_unit;
+        y[h][i][e] = exp2_fast(y[h][i][e]);
+        s[i].l[e & 1] += y[h][i][e];
       }
-      b[h][i][0] = transpose8x8(f16x2_bits(c[h][i][0], c[h][i][1]));
-      b[h][i][1] = transpose8x8(f16x2_bits(c[h][i][2], c[h][i][3]));
+    if (vs[h] != unit) {  // the warp's tiles of one block share it
+      const float to_unit = unit > 0.f ? __fdiv_rn(vs[h], unit) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kNR; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[h][i][e] *= to_unit;
+    }
+#pragma unroll
+    for (int i = 0; i < kNR; ++i) {
+      b[h][i][0] = transpose8x8(f16x2_bits(y[h][i][0], y[h][i][1]));
+      b[h][i][1] = transpose8x8(f16x2_bits(y[h][i][2], y[h][i][3]));
     }
   }
 #pragma unroll
@@ -298,9 +331,12 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
   }
 }
 
-// CTAs that fit on an SM: by shared memory at dim 128, by registers at dim 64.
+// CTAs that fit on an SM: by shared memory at dim 128 (12 warps in all), by
+// registers at dim 64.
 constexpr int kMaxPerSm = 4;
-constexpr int ctas_per_sm(int dim, int fragments) { return dim == 64 && fragments == 1 ? kMaxPerSm : 3; }
+constexpr int ctas_per_sm(int warps, int dim, int fragments) {
+  return warps > 4 ? 1 : dim == 64 && fragments == 1 ? kMaxPerSm : 3;
+}
 
 __device__ __forceinline__ void add_scaled(float4& o, float& l, const float* v, float vl, float f) {
   l = fmaf(f, vl, l);
@@ -325,13 +361,25 @@ __device__ __forceinline__ void write_out(const KvAttentionArgs& a, int t0, int 
 // as often where a sequence may have more than 8 rows per cached head.
 int row_fragments(const KvAttentionArgs& a) { return (long long)a.max_q * a.group > kRows ? 2 : 1; }
 
+// Warps of a CTA.  With many items each SM has three CTAs of four, whose starts
+// and joins of items overlap.  With no more items than SMs each is shared by many
+// CTAs: one CTA of twelve then leaves a third of the partials and lets an
+// SM's warps end together (one sequence of 131077 tokens, 8 items: 68 us with four
+// warps, 57 with twelve).
+long long attention_items(const KvAttentionArgs& a) {
+  const int rows = kRows * row_fragments(a);
+  return ((long long)a.max_q * a.group + rows - 1) / rows * a.heads * a.B;
+}
+int attention_warps(const LaunchCtx& c, const KvAttentionArgs& a) {
+  return attention_items(a) <= c.num_sms ? 12 : 4;
+}
+
 // CTAs: as many as run at once, or fewer where the tables cannot hold that much work.
 int attention_grid(const LaunchCtx& c, const KvAttentionArgs& a) {
-  const long long row_tiles = ((long long)a.max_q * a.group + kRows * row_fragments(a) - 1) /
-                              (kRows * row_fragments(a));
-  const long long units = max(1LL, ((long long)a.width * a.block + kUnit - 1) / kUnit);
-  const long long most = (row_tiles * a.heads * a.B * units + kMinUnits - 1) / kMinUnits;
-  return int(min(most, (long long)ctas_per_sm(a.dim, row_fragments(a)) * c.num_sms));
+  const int warps = attention_warps(c, a), unit = warps * kTok;
+  const long long units = max(1LL, ((long long)a.width * a.block + unit - 1) / unit);
+  const long long most = (attention_items(a) * units + min_units(warps) - 1) / min_units(warps);
+  return int(min(most, (long long)ctas_per_sm(warps, a.dim, row_fragments(a)) * c.num_sms));
 }
 
 // The counters' place does not depend on the call: what one call leaves there
@@ -348,7 +396,7 @@ struct Sequence {
   long long total;
 };
 
-template <int kNR>
+template <int kNR, int kUnit>
 __device__ __forceinline__ Sequence sequence(const KvAttentionArgs& a, int b, int* status) {
   Sequence s;
   bool ok = sequence_tokens(a.cu, b, a.B, a.T, a.max_q, &s.t0, &s.n);
@@ -380,67 +428,97 @@ struct Partial {
 };
 
 // Joins the partials of CTAs first .. last of one item, in that order.  What
-// each one's rows have to be multiplied by comes first (in f: kJoinMax CTAs at a
-// time), so that the loads of the sums do not wait for one another.
+// each one's rows have to be multiplied by comes first (in shared memory, kJoinMax
+// CTAs at a time), so that the loads of the sums do not wait for one another.
 constexpr int kJoinMax = 64;
 
-template <int kDim, int kNR>
+template <int kDim, int kNR, int kWarps>
 __device__ __forceinline__ void join_partials(const KvAttentionArgs& a,
                                               const Partial<kDim, kNR>* parts, int first, int last,
-                                              int t0, int head, int row0, int rows, float* f) {
-  constexpr int kR = kRows * kNR, kPer = kR * kDim / 4 / (32 * kWarps);
-  static_assert(kPer * 32 * kWarps * 4 == kR * kDim, "a whole number for each thread");
-  float* ms = f + kJoinMax * kR;  // the running maximum of each row
+                                              int t0, int head, int row0, int rows, float* shared) {
+  constexpr int kR = kRows * kNR;
+  constexpr int kThreads = kWarps >= 8 && kR * kDim >= 1024 ? 256 : 128;  // the others only meet the barriers
+  constexpr int kPer = kR * kDim / 4 / kThreads;
+  static_assert(kPer * kThreads * 4 == kR * kDim, "a whole number for each thread");
+  constexpr int kLanes = kThreads / kR;          // neighbouring lanes for each row's statistics
+  const bool mine = threadIdx.x < kThreads;
+  constexpr int kStep = kPer == 1 ? 16 : 32 / kPer;  // CTAs whose sums are in flight at once
+  float* f = shared;                   // [kJoinMax][kR] factors
+  float* ls = f + kJoinMax * kR;       // [kR] row sums
+  float* shrink = ls + kR;             // [kR] of what was summed before
+  const int r = threadIdx.x / kLanes % kR, q = threadIdx.x % kLanes;
+  float m = kNone, l = 0.f;
   float4 o[kPer];
-  float l[kPer];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    l[k] = 0.f;
-  }
+  for (int k = 0; k < kPer; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   auto part = [&](int c) -> const Partial<kDim, kNR>& { return parts[2 * c + (c == first ? 1 : 0)]; };
-  if (threadIdx.x < kR) ms[threadIdx.x] = -INFINITY;
   for (int c0 = first; c0 <= last; c0 += kJoinMax) {
     const int n = min(kJoinMax, last + 1 - c0);
+    constexpr int kMine = kJoinMax / kLanes;
+    float pm[kMine], pl[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int c = mine ? q + i * kLanes : n;
+      pm[i] = c < n ? __ldcg(&part(c0 + c).m[r]) : -INFINITY;
+      pl[i] = c < n ? __ldcg(&part(c0 + c).l[r]) : 0.f;
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) top = fmaxf(top, pm[i]);
+#pragma unroll
+    for (int x = 1; x < kLanes; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
     __syncthreads();  // f is free
-    for (int i = threadIdx.x; i < n * kR; i += 32 * kWarps)
-      f[i] = __ldcg(&part(c0 + i / kR).m[i % kR]);
-    __syncthreads();
-    float shrink[kPer];
-    if (threadIdx.x < kR) {
-      const float old = ms[threadIdx.x];
-      float m = old;
-      for (int c = 0; c < n; ++c) m = fmaxf(m, f[c * kR + threadIdx.x]);
-      for (int c = 0; c < n; ++c)
-        f[c * kR + threadIdx.x] = m == -INFINITY ? 0.f : exp2_fast(f[c * kR + threadIdx.x] - m);
-      ms[threadIdx.x] = m;
-      ms[kR + threadIdx.x] = m == -INFINITY ? 1.f : exp2_fast(old - m);
+    const float s = exp2_fast(m - top);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const float e = exp2_fast(pm[i] - top);  // 0 past the last CTA
+      sum = fmaf(e, pl[i], sum);
+      if (mine) f[(q + i * kLanes) * kR + r] = e;
+    }
+#pragma unroll
+    for (int x = 1; x < kLanes; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    m = top;
+    l = fmaf(l, s, sum);
+    if (mine && q == 0) {
+      ls[r] = l;
+      shrink[r] = s;
     }
     __syncthreads();
+    if (!mine) continue;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      shrink[k] = ms[kR + (threadIdx.x + 32 * kWarps * k) / (kDim / 4)];
-      l[k] *= shrink[k];
-      o[k].x *= shrink[k];
-      o[k].y *= shrink[k];
-      o[k].z *= shrink[k];
-      o[k].w *= shrink[k];
+      const float x = shrink[(threadIdx.x + kThreads * k) / (kDim / 4)];
+      o[k] = make_float4(o[k].x * x, o[k].y * x, o[k].z * x, o[k].w * x);
     }
-#pragma unroll(16 / kPer)
-    for (int c = 0; c < n; ++c) {
-      const Partial<kDim, kNR>& p = part(c0 + c);
+    for (int c = 0; c < n; c += kStep) {
+      float4 v[kStep][kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int i = threadIdx.x + 32 * kWarps * k, r = i / (kDim / 4), d = i % (kDim / 4) * 4;
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(&p.o[r][d]));
-        add_scaled(o[k], l[k], &v.x, __ldcg(&p.l[r]), f[c * kR + r]);
-      }
+      for (int e = 0; e < kStep; ++e)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int i = threadIdx.x + kThreads * k;
+          v[e][k] = c + e < n ? __ldcg(reinterpret_cast<const float4*>(
+                                    &part(c0 + c + e).o[i / (kDim / 4)][i % (kDim / 4) * 4]))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int e = 0; e < kStep; ++e)
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const float x = f[min(c + e, kJoinMax - 1) * kR + (threadIdx.x + kThreads * k) / (kDim / 4)];
+          o[k].x = fmaf(x, v[e][k].x, o[k].x);
+          o[k].y = fmaf(x, v[e][k].y, o[k].y);
+          o[k].z = fmaf(x, v[e][k].z, o[k].z);
+          o[k].w = fmaf(x, v[e][k].w, o[k].w);
+        }
     }
   }
+  if (!mine) return;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int i = threadIdx.x + 32 * kWarps * k, r = i / (kDim / 4), d = i % (kDim / 4) * 4;
-    if (row0 + r < rows) write_out<kDim>(a, t0, head, row0 + r, d, o[k], l[k]);
+    const int i = threadIdx.x + kThreads * k, row = i / (kDim / 4), d = i % (kDim / 4) * 4;
+    if (row0 + row < rows) write_out<kDim>(a, t0, head, row0 + row, d, o[k], ls[row]);
   }
 }
 
@@ -456,13 +534,13 @@ struct CacheMaps {
 //   slot 2c      CTA c's share of an item that began before its run
 //   slot 2c + 1  of an item that begins in its run and goes on
 //   counter c    CTAs done with the item that goes on past CTA c's run (left at 0)
-template <int kDim, bool kE5M2, int kNR>
-__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attention_kernel(const KvAttentionArgs a,
+template <int kDim, bool kE5M2, int kNR, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) kv_attention_kernel(const KvAttentionArgs a,
                                                                    const __grid_constant__ CacheMaps maps,
                                                                    int* counters,
                                                                    Partial<kDim, kNR>* parts,
                                                                    int* status) {
-  constexpr int kR = kRows * kNR;
+  constexpr int kR = kRows * kNR, kUnit = kWarps * kTok;
   extern __shared__ unsigned char raw[];
   unsigned char* shared = raw + (1024u - (smem_addr(raw) & 1023u)) % 1024u;
   float (*so)[kR][kDim + 4] = reinterpret_cast<float (*)[kR][kDim + 4]>(shared);
@@ -496,7 +574,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
   long long mine = 0;
   Sequence seq = {};
   for (int b = b0; b < b1; ++b) {
-    seq = sequence<kNR>(a, b, status);
+    seq = sequence<kNR, kWarps * kTok>(a, b, status);
     mine += seq.total;
   }
   long long upto = mine;
@@ -513,7 +591,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
     if (w < warp) upto += scan[w];
     U += scan[w];
   }
-  const long long per = max((long long)kMinUnits, (U + gridDim.x - 1) / gridDim.x);
+  const long long per = max((long long)min_units(kWarps), (U + gridDim.x - 1) / gridDim.x);
   const long long u0 = blockIdx.x * per, u1 = min(U, u0 + per);
   if (u0 >= u1) return;
   if (u0 >= upto - mine && u0 < upto) {  // one thread's
@@ -521,7 +599,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
     int b = b0;
     if (b1 - b0 > 1)
       for (;; ++b) {
-        seq = sequence<kNR>(a, b, status);
+        seq = sequence<kNR, kWarps * kTok>(a, b, status);
         if (u0 < before + seq.total) break;
         before += seq.total;
       }
@@ -535,7 +613,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
   for (long long u = u0; u < u1;) {
     while (u >= before + q_seq.total) {
       before += q_seq.total;
-      q_seq = sequence<kNR>(a, ++b, status);
+      q_seq = sequence<kNR, kWarps * kTok>(a, ++b, status);
     }
     const int item = int((u - before) / q_seq.units);  // row tile and head
     const long long item0 = before + (long long)item * q_seq.units;
@@ -543,67 +621,72 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
     const int s0 = int(u - item0), s1 = int(min((long long)q_seq.units, u1 - item0));
     const int rows = q_seq.n * a.group, len = q_seq.len;
 
-    // Blocks of the tile of unit i, -1 where it has none.  Past the first kStages
-    // tiles they are read a step before they are needed.
+    // Where the warp's tiles lie.  Lane l looks up the l-th of 32 at a time: the
+    // cache row of each fragment's first token (-1: not there) and its scales, for
+    // the batch in use and, while that is worked on, the one after it.
     const int* table = a.table + size_t(b) * a.width;
-    auto blocks = [&](int i) -> int2 {
+    const bool halves = a.block < kTok;  // a tile lies in two blocks
+    struct Batch {
+      int row[2];
+      float k[2], v[2];
+    } batch = {}, after = {};
+    auto look_up = [&](Batch& x, int i) {
       const int tok = i * kUnit + warp * kTok;
-      int2 e = make_int2(-1, -1);
-      if (i >= s1 || tok >= len) return e;
-      e.x = table[tok >> a.log_block];
-      e.y = a.block >= kTok ? e.x : tok + kFrag < len ? table[(tok + kFrag) >> a.log_block] : -1;
-      const bool bad_x = e.x < 0 || e.x >= a.num_blocks;
-      const bool bad_y = (e.y < 0 || e.y >= a.num_blocks) && (a.block >= kTok || tok + kFrag < len);
-      if (bad_x || bad_y) {  // their tokens count as not there
-        if (lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-        if (bad_x) e.x = -1;
-        if (bad_y) e.y = -1;
-      }
-      return e;
-    };
-    auto fetch = [&](int i, int2 e) {
-      if (e.x < 0 && e.y < 0) return;
-      in_flight |= 1u << i % kStages;
-      if (lane != 0) return;
-      const int tok = (i * kUnit + warp * kTok) & (a.block - 1), stage = i % kStages;
-      const int half = kFrag * kDim;
-      mbar_arrive_expect_tx(&bars[warp][stage], 2 * half * (int(e.x >= 0) + int(e.y >= 0)));
-      if (a.block >= kTok) {
-        const int row = (e.x * a.heads + head) * a.block + tok;
-        tma_load_2d(ring[stage].k, &maps.k, &bars[warp][stage], 0, row);
-        tma_load_2d(ring[stage].v, &maps.v, &bars[warp][stage], 0, row);
-      } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int blk = h ? e.y : e.x, row = (blk * a.heads + head) * a.block;
-          if (blk < 0) continue;
-          tma_load_2d(ring[stage].k[kFrag * h], &maps.k, &bars[warp][stage], 0, row);
-          tma_load_2d(ring[stage].v[kFrag * h], &maps.v, &bars[warp][stage], 0, row);
+      for (int h = 0; h < 2; ++h) {
+        const int at = tok + kFrag * h;
+        x.row[h] = -1;
+        if (h == 1 && !halves) {
+          x.row[1] = x.row[0] < 0 ? -1 : x.row[0] + kFrag;
+        } else if (i < s1 && at < len) {
+          const int blk = table[at >> a.log_block];
+          if (blk >= 0 && blk < a.num_blocks)
+            x.row[h] = ((blk * a.heads + head) << a.log_block) + (at & (a.block - 1));
+          else  // a bad table entry: its tokens count as not there
+            raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
         }
       }
     };
-    struct Scales {
-      float k[2], v[2];
+    auto look_up_scales = [&](Batch& x) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !halves) {
+          x.k[1] = x.k[0];
+          x.v[1] = x.v[0];
+        } else {
+          x.k[h] = x.row[h] < 0 ? 0.f : a.ks[x.row[h] >> a.log_block];
+          x.v[h] = x.row[h] < 0 ? 0.f : a.vs[x.row[h] >> a.log_block];
+        }
+      }
     };
-    auto scales = [&](int2 e) {
-      Scales x = {};
-      if (e.x >= 0) {
-        x.k[0] = a.ks[size_t(e.x) * a.heads + head];
-        x.v[0] = a.vs[size_t(e.x) * a.heads + head];
+    auto fetch = [&](int stage, const Batch& x, int l) {
+      int row[2];
+      row[0] = __shfl_sync(0xffffffffu, x.row[0], l);
+      row[1] = __shfl_sync(0xffffffffu, x.row[1], l);
+      if (row[0] < 0 && row[1] < 0) return;
+      in_flight |= 1u << stage;
+      if (lane != 0) return;
+      constexpr int kHalf = kFrag * kDim;
+      uint64_t* bar = &bars[warp][stage];
+      mbar_arrive_expect_tx(bar, 2 * kHalf * (int(row[0] >= 0) + int(row[1] >= 0)));
+      if (!halves) {
+        tma_load_2d(ring[stage].k, &maps.k, bar, 0, row[0]);
+        tma_load_2d(ring[stage].v, &maps.v, bar, 0, row[0]);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (row[h] < 0) continue;
+          tma_load_2d(ring[stage].k[kFrag * h], &maps.k, bar, 0, row[h]);
+          tma_load_2d(ring[stage].v[kFrag * h], &maps.v, bar, 0, row[h]);
+        }
       }
-      if (e.y >= 0) {
-        x.k[1] = a.ks[size_t(e.y) * a.heads + head];
-        x.v[1] = a.vs[size_t(e.y) * a.heads + head];
-      }
-      return x;
     };
     float unit = 0.f;
-    int2 ahead[kStages];  // blocks of the tiles in flight, the oldest first
+    look_up(batch, s0 + lane);
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) ahead[i] = blocks(s0 + i);
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(s0 + i, ahead[i]);
-    Scales sc = scales(ahead[0]);
+    for (int i = 0; i < kStages; ++i) fetch(i, batch, i);
+    look_up_scales(batch);
+    look_up(after, s0 + 32 + lane);
     Queries<kDim> q[kNR];
     State<kDim> s[kNR];
     int limit[kNR][2];  // tokens that the lane's rows see
@@ -618,20 +701,26 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int rr = row0 + kRows * i + 2 * t + r;
-        limit[i][r] = rr < rows ? len - q_seq.n + 1 + rr / a.group : 0;
+        limit[i][r] = rr < rows ? len - q_seq.n + 1 + rr / a.group : len;
       }
       clear(s[i]);
     }
+    const int least_limit = len - q_seq.n + 1 + row0 / a.group;
+    int stage = 0;
     for (int i = s0; i < s1; ++i) {
-      const int2 e = ahead[0];
-      const Scales here = sc;
-#pragma unroll
-      for (int k = 0; k + 1 < kStages; ++k) ahead[k] = ahead[k + 1];
-      sc = scales(ahead[0]);
-      ahead[kStages - 1] = blocks(i + kStages);
-      const uint32_t there = uint32_t(e.x >= 0) | uint32_t(e.y >= 0) << 1;
+      const int l = (i - s0) & 31;
+      if (l == 16) look_up_scales(after);
+      const uint32_t there = uint32_t(__shfl_sync(0xffffffffu, batch.row[0], l) >= 0) |
+                             uint32_t(__shfl_sync(0xffffffffu, batch.row[1], l) >= 0) << 1;
       if (there != 0) {
-        const int stage = i % kStages, tok = i * kUnit + warp * kTok;
+        const int tok = i * kUnit + warp * kTok;
+        float ks[2], vs[2];
+        ks[0] = ks[1] = __shfl_sync(0xffffffffu, batch.k[0], l);
+        vs[0] = vs[1] = __shfl_sync(0xffffffffu, batch.v[0], l);
+        if (halves) {
+          ks[1] = __shfl_sync(0xffffffffu, batch.k[1], l);
+          vs[1] = __shfl_sync(0xffffffffu, batch.v[1], l);
+        }
         if (!mbar_wait(&bars[warp][stage], phases >> stage & 1, &gave_up, a.wait_ns)) {
           // results are void; what is still in flight lands first, or not at all
           gave_up = 1;
@@ -642,11 +731,19 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
         }
         phases ^= 1u << stage;
         in_flight &= ~(1u << stage);
-        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[stage], q, limit, tok, there, len - tok, here.k,
-                                      here.v, lane);
+        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[stage], q, limit, least_limit, tok, there,
+                                      len - tok, ks, vs, lane);
         __syncwarp();  // the stage has been read
       }
-      fetch(i + kStages, ahead[kStages - 1]);
+      if (l + kStages < 32)
+        fetch(stage, batch, l + kStages);
+      else
+        fetch(stage, after, l + kStages - 32);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (l == 31) {
+        batch = after;
+        look_up(after, i + 33 + lane);
+      }
     }
     __syncthreads();  // the rings become the place to join the warps' results
     if (gave_up) break;
@@ -673,15 +770,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
     Partial<kDim, kNR>* part = parts + 2 * blockIdx.x + (begins ? 1 : 0);
     for (int i = threadIdx.x; i < kR * kDim / 4; i += 32 * kWarps) {
       const int r = i / (kDim / 4), d = i % (kDim / 4) * 4, row = row0 + r;
-      float m = -INFINITY;
+      float m = kNone;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w][r]);
       float l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) add_scaled(o, l, so[w][r] + d, sl[w][r], exp2_fast(sm[w][r] - m));
-      }
+      for (int w = 0; w < kWarps; ++w) add_scaled(o, l, so[w][r] + d, sl[w][r], exp2_fast(sm[w][r] - m));
       if (begins && ends) {
         if (row < rows) write_out<kDim>(a, q_seq.t0, head, row, d, o, l);
       } else {
@@ -699,7 +794,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
       __syncthreads();
       if (last_one) {
         if (threadIdx.x == 0) counters[first] = 0;
-        join_partials<kDim, kNR>(a, parts, first, last, q_seq.t0, head, row0, rows,
+        join_partials<kDim, kNR, kWarps>(a, parts, first, last, q_seq.t0, head, row0, rows,
                                  reinterpret_cast<float*>(shared));
         fence_proxy_async_smem();
         __syncthreads();
@@ -709,25 +804,28 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kDim, kNR)) kv_attent
   }
 }
 
-template <int kDim, bool kE5M2, int kNR>
+template <int kDim, bool kE5M2, int kNR, int kWarps>
 cudaError_t launch(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps& maps, void* ws) {
   const int grid = attention_grid(c, a);
   int* counters = static_cast<int*>(ws);
   auto* parts = reinterpret_cast<Partial<kDim, kNR>*>(static_cast<char*>(ws) + counter_bytes(c));
-  constexpr size_t kRings = 1024 + sizeof(Stage<kDim>) * kStages * kWarps;
+  constexpr size_t kRings = sizeof(Stage<kDim>) * kStages * kWarps;
   constexpr size_t kJoin = sizeof(float) * kWarps * kRows * kNR * (kDim + 4);
-  constexpr size_t kSmem = kRings > kJoin ? kRings : kJoin;
-  auto fn = kv_attention_kernel<kDim, kE5M2, kNR>;
+  constexpr size_t kFactors = sizeof(float) * (kJoinMax + 2) * kRows * kNR;
+  constexpr size_t kMore = kJoin > kFactors ? kJoin : kFactors;
+  constexpr size_t kSmem = 1024 + (kRings > kMore ? kRings : kMore);
+  auto fn = kv_attention_kernel<kDim, kE5M2, kNR, kWarps>;
   static SmemLimit limit;
   if (cudaError_t e = limit.raise(reinterpret_cast<const void*>(fn), kSmem)) return e;
   return launch_dependent(c, fn, grid, 32 * kWarps, kSmem, a, maps, counters, parts, c.status);
 }
 
-template <int kNR>
-cudaError_t launch_rows(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps& maps, void* ws) {
+template <int kNR, int kWarps>
+cudaError_t launch_shape(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps& maps, void* ws) {
   const bool e5 = a.fmt == FP8GEMM_FMT_E5M2;
-  if (a.dim == 128) return e5 ? launch<128, true, kNR>(c, a, maps, ws) : launch<128, false, kNR>(c, a, maps, ws);
-  return e5 ? launch<64, true, kNR>(c, a, maps, ws) : launch<64, false, kNR>(c, a, maps, ws);
+  if (a.dim == 128)
+    return e5 ? launch<128, true, kNR, kWarps>(c, a, maps, ws) : launch<128, false, kNR, kWarps>(c, a, maps, ws);
+  return e5 ? launch<64, true, kNR, kWarps>(c, a, maps, ws) : launch<64, false, kNR, kWarps>(c, a, maps, ws);
 }
 
 }  // namespace
@@ -743,7 +841,9 @@ cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, vo
   const uint32_t box = min(a.block, kTok);
   if (!make_tmap_rows(&maps.k, a.kc, rows, a.dim, box) || !make_tmap_rows(&maps.v, a.vc, rows, a.dim, box))
     return cudaErrorInvalidValue;
-  return row_fragments(a) == 1 ? launch_rows<1>(c, a, maps, ws) : launch_rows<2>(c, a, maps, ws);
+  if (attention_warps(c, a) == 12)
+    return row_fragments(a) == 1 ? launch_shape<1, 12>(c, a, maps, ws) : launch_shape<2, 12>(c, a, maps, ws);
+  return row_fragments(a) == 1 ? launch_shape<1, 4>(c, a, maps, ws) : launch_shape<2, 4>(c, a, maps, ws);
 }
 
 }  // namespace fp8gemm
