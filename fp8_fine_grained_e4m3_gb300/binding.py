@@ -580,57 +580,57 @@ def fp8gemm_dense_small_m_noalloc(A, sA, B, sB, D, stream=None):
 
 # The decoder-layer calls below are short enough on the GPU for the host to be
 # what a caller waits for, so their checks take few attribute reads per tensor.
-def _raw_stream(stream, t):
-    """The stream handle as a number: the given one's, or the current one's."""
-    if stream is not None:
-        return stream.cuda_stream
-    torch = _torch()
-    try:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
+_fast = None
 
 
-def _addr(t, name, want, elems, last=None):
-    """Address of a tensor of the type(s) `want` with `elems` elements (in rows
-    of `last` when given); where it lies is checked by _resident."""
-    if t.dtype not in want:
-        raise TypeError(f"{name} must be {' or '.join(str(w) for w in want)}, got {t.dtype}")
-    if t.numel() != elems or (last is not None and elems > 0 and t.size(-1) != last):
-        _need(t, name, elems, last)
-    return t.data_ptr()
+class _Fast:
+    """What those calls look up once: torch's types and the handle of the
+    current stream as a number."""
 
-
-def _resident(names, *tensors):
-    for i, t in enumerate(tensors):
-        if not (t.is_cuda and t.is_contiguous()):
-            _dev(t, names.split()[i])
-
-
-_TYPES = {}
-
-
-def _types():
-    """Types as _addr wants them (torch is imported on first use)."""
-    if not _TYPES:
+    def __init__(self):
         torch = _torch()
-        _TYPES.update(
-            f32=(torch.float32,), i32=(torch.int32,), bf16=(torch.bfloat16,),
-            act={torch.bfloat16: 0, torch.float32: 1},  # FP8GEMM_TYPE_*
-            e4m3=(torch.uint8, torch.float8_e4m3fn), e5m2=(torch.uint8, torch.float8_e5m2))
-    return _TYPES
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.u8, self.f32, self.i32, self.bf16 = (torch.uint8, torch.float32, torch.int32,
+                                                  torch.bfloat16)
+        self.f8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+        self.kind = {torch.bfloat16: 0, torch.float32: 1}  # FP8GEMM_TYPE_*
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            self.current = lambda t: torch.cuda.current_stream().cuda_stream
+        else:
+            self.current = lambda t: raw(t.get_device())
+        L = lib()
+        self.rmsnorm_quant, self.rmsnorm_backward = L.fp8_rmsnorm_quant, L.fp8_rmsnorm_backward
+        self.kv_append, self.kv_attention = L.fp8_kv_append, L.fp8_kv_attention
+        self.moe_few = L.fp8_moe_few
 
 
-def _f8_types(types, fmt):
-    _fmt(fmt)
-    return types[fmt]
+def _lookup():
+    global _fast
+    if _fast is None:
+        _fast = _Fast()
+    return _fast
 
 
-def _act(types, t, name):
-    kind = types["act"].get(t.dtype)
-    if kind is None:
-        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    return kind
+def _size(t, name, want, elems, last=None):
+    """Refuses a tensor of another type or size: the slow end of the checks
+    below (`last`: the length of a row)."""
+    if t.dtype != want:
+        raise TypeError(f"{name} must be {want}, got {t.dtype}")
+    _need(t, name, elems, last)
+
+
+def _codes(f, t, name, fmt):
+    """FP8 bytes in format `fmt`: uint8, or the float8 type of that format."""
+    if t.dtype is not f.u8 and t.dtype is not f.f8[fmt]:
+        _u8_fmt(t, fmt, name)
+
+
+def _here(t, name):
+    """Address of a contiguous CUDA tensor."""
+    if not (t.is_cuda and t.is_contiguous()):
+        _dev(t, name)
+    return t.data_ptr()
 
 
 def fp8_rmsnorm_quant(X, gain, eps=1e-6, residual=None, fmt="e4m3", H=None, Q=None, sQ=None,
@@ -639,34 +639,46 @@ def fp8_rmsnorm_quant(X, gain, eps=1e-6, residual=None, fmt="e4m3", H=None, Q=No
     f32 [..., K], gain f32 [K] -> (Q u8 [..., K], sQ f32 [..., ceil(K/128)], H,
     rstd f32 [...]).  H is X + residual in X's type (X itself without one);
     H=residual updates the stream in place."""
-    torch, types = _torch(), _types()
-    f32, like, f8 = types["f32"], (X.dtype,), _f8_types(types, fmt)
-    kind = _act(types, X, "X")
-    K = X.size(-1)
-    n = X.numel()
+    f = _fast or _lookup()
+    dtype, shape = X.dtype, X.shape
+    kind = f.kind.get(dtype)
+    if kind is None:
+        raise TypeError(f"X must be bfloat16 or float32, got {dtype}")
+    code = _fmt(fmt)
+    K, n = shape[-1], X.numel()
     M = n // K if K else 0
     Kb = -(-K // 128)
-    g = _addr(gain, "gain", f32, K, K)
+    if gain.dtype is not f.f32 or gain.numel() != K:
+        _size(gain, "gain", f.f32, K)
     r = h = None
     if residual is not None:
-        r = _addr(residual, "residual", like, n, K)
+        if residual.dtype is not dtype or residual.shape != shape:
+            _size(residual, "residual", dtype, n, K)
         if H is None:
-            H = torch.empty_like(X)
-        h = _addr(H, "H", like, n, K)
-        _resident("residual H", residual, H)
+            H = f.empty_like(X)
+        elif H is not residual and (H.dtype is not dtype or H.shape != shape):
+            _size(H, "H", dtype, n, K)
     elif H is not None:
         raise ValueError("H is the sum with the residual: give residual too")
     if Q is None:
-        Q = torch.empty(X.shape, dtype=torch.uint8, device=X.device)
+        Q = f.empty(shape, dtype=f.u8, device=X.device)
+    else:
+        _codes(f, Q, "Q", fmt)
+        if Q.shape != shape:
+            _need(Q, "Q", n, K)
     if sQ is None:
-        sQ = torch.empty((*X.shape[:-1], Kb), dtype=torch.float32, device=X.device)
+        sQ = f.empty((*shape[:-1], Kb), dtype=f.f32, device=X.device)
+    elif sQ.dtype is not f.f32 or sQ.numel() != M * Kb or (M and sQ.size(-1) != Kb):
+        _size(sQ, "sQ", f.f32, M * Kb, Kb)
     if rstd is None:
-        rstd = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-    q, s = _addr(Q, "Q", f8, n, K), _addr(sQ, "sQ", f32, M * Kb, Kb)
-    d = _addr(rstd, "rstd", f32, M)
-    _resident("X gain Q sQ rstd", X, gain, Q, sQ, rstd)
-    rc = lib().fp8_rmsnorm_quant(X.data_ptr(), r, kind, g, eps, h, q, s, d, M, K, FMT[fmt],
-                                 _raw_stream(stream, X))
+        rstd = f.empty(shape[:-1], dtype=f.f32, device=X.device)
+    elif rstd.dtype is not f.f32 or rstd.numel() != M:
+        _size(rstd, "rstd", f.f32, M)
+    if residual is not None:
+        r, h = _here(residual, "residual"), _here(H, "H")
+    rc = f.rmsnorm_quant(_here(X, "X"), r, kind, _here(gain, "gain"), eps, h, _here(Q, "Q"),
+                         _here(sQ, "sQ"), _here(rstd, "rstd"), M, K, code,
+                         f.current(X) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_rmsnorm_quant")
     return Q, sQ, (X if residual is None else H), rstd
@@ -676,76 +688,82 @@ def fp8_rmsnorm_backward(dY, H, rstd, gain, dH=None, dX=None, dgain=None, stream
     """Gradients of fp8_rmsnorm_quant's norm (straight through the quantiser):
     dY and H bf16 or f32 [..., K], rstd f32 [...], gain f32 [K], dH (the
     gradient that reaches H past the norm) as dY or None -> (dX, dgain f32 [K])."""
-    torch, types = _torch(), _types()
-    f32, like = types["f32"], (H.dtype,)
-    kind = _act(types, H, "H")
-    K = H.size(-1)
-    n = H.numel()
+    f = _fast or _lookup()
+    dtype, shape = H.dtype, H.shape
+    kind = f.kind.get(dtype)
+    if kind is None:
+        raise TypeError(f"H must be bfloat16 or float32, got {dtype}")
+    K, n = shape[-1], H.numel()
     M = n // K if K else 0
-    y = _addr(dY, "dY", like, n, K)
-    up = None
-    if dH is not None:
-        up = _addr(dH, "dH", like, n, K)
-        _resident("dH", dH)
+    if dY.dtype is not dtype or dY.shape != shape:
+        _size(dY, "dY", dtype, n, K)
+    if dH is not None and (dH.dtype is not dtype or dH.shape != shape):
+        _size(dH, "dH", dtype, n, K)
     if dX is None:
-        dX = torch.empty_like(H)
+        dX = f.empty_like(H)
+    elif dX.dtype is not dtype or dX.shape != shape:
+        _size(dX, "dX", dtype, n, K)
     if dgain is None:
-        dgain = torch.empty(K, dtype=torch.float32, device=H.device)
-    x = _addr(dX, "dX", like, n, K)
-    d = _addr(rstd, "rstd", f32, M)
-    g, dg = _addr(gain, "gain", f32, K, K), _addr(dgain, "dgain", f32, K, K)
-    _resident("dY H rstd gain dX dgain", dY, H, rstd, gain, dX, dgain)
-    rc = lib().fp8_rmsnorm_backward(y, H.data_ptr(), kind, d, g, up, x, dg, M, K,
-                                    _raw_stream(stream, H))
+        dgain = f.empty(K, dtype=f.f32, device=H.device)
+    elif dgain.dtype is not f.f32 or dgain.numel() != K:
+        _size(dgain, "dgain", f.f32, K)
+    if rstd.dtype is not f.f32 or rstd.numel() != M:
+        _size(rstd, "rstd", f.f32, M)
+    if gain.dtype is not f.f32 or gain.numel() != K:
+        _size(gain, "gain", f.f32, K)
+    rc = f.rmsnorm_backward(_here(dY, "dY"), _here(H, "H"), kind, _here(rstd, "rstd"),
+                            _here(gain, "gain"), None if dH is None else _here(dH, "dH"),
+                            _here(dX, "dX"), _here(dgain, "dgain"), M, K,
+                            f.current(H) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_rmsnorm_backward")
     return dX, dgain
 
 
-def _tokens(t, name, heads, dim):
+def _tokens(f, t, name, T, heads, dim):
     """bf16 [T, heads, dim] whose tokens may lie apart (parts of the rows of a
     fused projection's output): returns the token stride in elements."""
-    _bf16(t, name)
-    if t.dim() != 3 or t.size(1) != heads or t.size(2) != dim:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [T, {heads}, {dim}]")
+    if t.dtype is not f.bf16:
+        _bf16(t, name)
+    if t.shape != (T, heads, dim):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{T}, {heads}, {dim}]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     ld, sh, sd = t.stride()
-    if sd != 1 or (heads > 1 and sh != dim):
+    if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"{name} must hold each token's heads contiguously")
-    return ld if t.size(0) > 1 else heads * dim
+    return ld if T > 1 else heads * dim
 
 
-def _cache(types, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T, fmt):
-    """Checks a paged cache and its index arrays: ((addresses), blocks, heads,
-    block, dim, B, table width)."""
-    f8, f32, i32 = _f8_types(types, fmt), types["f32"], types["i32"]
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache {tuple(k_cache.shape)} / v_cache {tuple(v_cache.shape)}: the"
+def _cache(f, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu, T, fmt):
+    """Checks a paged cache and its index arrays: blocks, heads, block, dim, B,
+    table width."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache {tuple(shape)} / v_cache {tuple(v_cache.shape)}: the"
                          " call needs [num_blocks, heads, block, dim] twice")
-    n, heads, block, dim = k_cache.shape
+    n, heads, block, dim = shape
+    if block_table.dtype is not f.i32:
+        _i32(block_table, "block_table")
     if block_table.dim() != 2:
         raise ValueError(f"block_table has shape {tuple(block_table.shape)}; the call needs"
                          " [B, table_width]")
     B, width = block_table.shape
-    if cu is None and B > 0 and T % B != 0:
-        raise ValueError(f"{T} tokens for {B} sequences: give the offsets")
-    size = n * heads * block * dim
-    at = (_addr(k_cache, "k_cache", f8, size, dim),
-          _addr(k_scale, "k_scale", f32, n * heads),
-          _addr(v_cache, "v_cache", f8, size, dim),
-          _addr(v_scale, "v_scale", f32, n * heads),
-          _addr(block_table, "block_table", i32, B * width, width),
-          _addr(seq_lens, "seq_lens", i32, B, B),
-          None if cu is None else _addr(cu, "the offsets", i32, B + 1, B + 1))
-    return at, n, heads, block, dim, B, width
-
-
-def _cache_resident(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu):
-    _resident("k_cache k_scale v_cache v_scale block_table seq_lens", k_cache, k_scale, v_cache,
-              v_scale, block_table, seq_lens)
-    if cu is not None:
-        _resident("cu", cu)
+    _codes(f, k_cache, "k_cache", fmt)
+    _codes(f, v_cache, "v_cache", fmt)
+    nh = n * heads
+    if k_scale.dtype is not f.f32 or k_scale.numel() != nh:
+        _size(k_scale, "k_scale", f.f32, nh)
+    if v_scale.dtype is not f.f32 or v_scale.numel() != nh:
+        _size(v_scale, "v_scale", f.f32, nh)
+    if seq_lens.dtype is not f.i32 or seq_lens.numel() != B:
+        _size(seq_lens, "seq_lens", f.i32, B)
+    if cu is None:
+        if B > 0 and T % B != 0:
+            raise ValueError(f"{T} tokens for {B} sequences: give the offsets")
+    elif cu.dtype is not f.i32 or cu.numel() != B + 1:
+        _size(cu, "the offsets", f.i32, B + 1)
+    return n, heads, block, dim, B, width
 
 
 def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_new=None,
@@ -755,17 +773,21 @@ def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
     f32 [num_blocks, heads]), at the end of each sequence: seq_lens i32 [B]
     counts them already.  cu_new i32 [B + 1] are the offsets of each sequence's
     tokens (None: T / B each); max_new bounds a sequence's (None: T)."""
+    f = _fast or _lookup()
+    code = _fmt(fmt)
     T = K.size(0)
-    at, n, heads, block, dim, B, width = _cache(_types(), k_cache, k_scale, v_cache, v_scale,
-                                                block_table, seq_lens, cu_new, T, fmt)
-    if V.size(0) != T:
-        raise ValueError(f"K holds {T} tokens, V {V.size(0)}")
-    ld_k, ld_v = _tokens(K, "K", heads, dim), _tokens(V, "V", heads, dim)
-    _cache_resident(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_new)
+    n, heads, block, dim, B, width = _cache(f, k_cache, k_scale, v_cache, v_scale, block_table,
+                                            seq_lens, cu_new, T, fmt)
+    ld_k, ld_v = _tokens(f, K, "K", T, heads, dim), _tokens(f, V, "V", T, heads, dim)
     if max_new is None:
         max_new = T if cu_new is not None else -(-T // max(B, 1))
-    rc = lib().fp8_kv_append(K.data_ptr(), V.data_ptr(), ld_k, ld_v, *at, T, B, heads, dim, block,
-                             width, n, max_new, FMT[fmt], _raw_stream(stream, K))
+    rc = f.kv_append(K.data_ptr(), V.data_ptr(), ld_k, ld_v, _here(k_cache, "k_cache"),
+                     _here(k_scale, "k_scale"), _here(v_cache, "v_cache"),
+                     _here(v_scale, "v_scale"), _here(block_table, "block_table"),
+                     _here(seq_lens, "seq_lens"),
+                     None if cu_new is None else _here(cu_new, "cu_new"), T, B, heads, dim, block,
+                     width, n, max_new, code,
+                     f.current(K) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_kv_append")
 
@@ -776,26 +798,30 @@ def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
     may lie apart) over the paged FP8 cache that holds their keys and values
     already -> O bf16 [T, heads * group, dim].  cu_q and max_q as
     fp8_kv_append's; scale defaults to dim ** -0.5."""
-    types = _types()
+    f = _fast or _lookup()
+    code = _fmt(fmt)
     T = Q.size(0)
-    at, n, heads, block, dim, B, width = _cache(types, k_cache, k_scale, v_cache, v_scale,
-                                                block_table, seq_lens, cu_q, T, fmt)
+    n, heads, block, dim, B, width = _cache(f, k_cache, k_scale, v_cache, v_scale, block_table,
+                                            seq_lens, cu_q, T, fmt)
     if Q.dim() != 3 or heads == 0 or Q.size(1) % heads != 0:
         raise ValueError(f"Q has shape {tuple(Q.shape)}; the call needs [T, heads * group, dim]"
                          f" with {heads} cached heads")
     hq = Q.size(1)
-    ld_q = _tokens(Q, "Q", hq, dim)
+    ld_q = _tokens(f, Q, "Q", T, hq, dim)
     if O is None:
-        O = _torch().empty(Q.shape, dtype=Q.dtype, device=Q.device)
-    o = _addr(O, "O", types["bf16"], T * hq * dim, dim)
-    _resident("O", O)
-    _cache_resident(k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q)
+        O = f.empty(Q.shape, dtype=f.bf16, device=Q.device)
+    elif O.dtype is not f.bf16 or O.shape != Q.shape:
+        _size(O, "O", f.bf16, T * hq * dim, dim)
     if max_q is None:
         max_q = T if cu_q is not None else -(-T // max(B, 1))
     if scale is None:
         scale = dim ** -0.5
-    rc = lib().fp8_kv_attention(Q.data_ptr(), ld_q, *at, scale, o, T, B, heads, hq // heads, dim,
-                                block, width, n, max_q, FMT[fmt], _raw_stream(stream, Q))
+    rc = f.kv_attention(Q.data_ptr(), ld_q, _here(k_cache, "k_cache"), _here(k_scale, "k_scale"),
+                        _here(v_cache, "v_cache"), _here(v_scale, "v_scale"),
+                        _here(block_table, "block_table"), _here(seq_lens, "seq_lens"),
+                        None if cu_q is None else _here(cu_q, "cu_q"), scale, _here(O, "O"), T, B,
+                        heads, hq // heads, dim, block, width, n, max_q, code,
+                        f.current(Q) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_kv_attention")
     return O
@@ -807,32 +833,45 @@ def fp8_moe_few(A, sA, logits, W1, s1, W2, s2, top_k, renormalise=True, D=None, 
     [T, ceil(H/128)], logits f32 [T, E], W1 u8 [E, 2 I, H] (gate rows, then up
     rows), W2 u8 [E, H, I] with their 128x128 scales -> (D bf16 [T, H], ids i32
     [T, top_k], weights f32 [T, top_k])."""
-    torch, types = _torch(), _types()
-    f8, f32 = types["e4m3"], types["f32"]
-    if A.dim() != 2 or W1.dim() != 3 or W2.dim() != 3:
-        raise ValueError(f"A {tuple(A.shape)} / W1 {tuple(W1.shape)} / W2 {tuple(W2.shape)}: the"
-                         " call needs [T, H], [E, 2 I, H] and [E, H, I]")
-    T, H = A.shape
-    E, I2, Hw = W1.shape
+    f = _fast or _lookup()
+    f32 = f.f32
+    a, w1, w2 = A.shape, W1.shape, W2.shape
+    if len(a) != 2 or len(w1) != 3:
+        raise ValueError(f"A {tuple(a)} / W1 {tuple(w1)}: the call needs [T, H] and [E, 2 I, H]")
+    T, H = a
+    E, I2, Hw = w1
     I = I2 // 2
-    if I2 != 2 * I or Hw != H or W2.shape != (E, H, I):
-        raise ValueError(f"W1 {tuple(W1.shape)} / W2 {tuple(W2.shape)}: the call needs"
-                         f" [E, 2 I, {H}] and [E, {H}, I]")
+    if I2 != 2 * I or Hw != H or w2 != (E, H, I):
+        raise ValueError(f"W1 {tuple(w1)} / W2 {tuple(w2)}: the call needs [E, 2 I, {H}] and"
+                         f" [E, {H}, I]")
+    _codes(f, A, "A", "e4m3")
+    _codes(f, W1, "W1", "e4m3")
+    _codes(f, W2, "W2", "e4m3")
     Hb, Ib, k = -(-H // 128), -(-I // 128), int(top_k)
-    at = (_addr(A, "A", f8, T * H, H), _addr(sA, "sA", f32, T * Hb, Hb),
-          _addr(logits, "logits", f32, T * E, E), _addr(W1, "W1", f8, E * I2 * H, H),
-          _addr(s1, "s1", f32, E * -(-I2 // 128) * Hb, Hb), _addr(W2, "W2", f8, E * H * I, I),
-          _addr(s2, "s2", f32, E * Hb * Ib, Ib))
+    if sA.dtype is not f32 or sA.shape != (T, Hb):
+        _size(sA, "sA", f32, T * Hb, Hb)
+    if logits.dtype is not f32 or logits.shape != (T, E):
+        _size(logits, "logits", f32, T * E, E)
+    if s1.dtype is not f32 or s1.shape != (E, -(-I2 // 128), Hb):
+        _size(s1, "s1", f32, E * -(-I2 // 128) * Hb, Hb)
+    if s2.dtype is not f32 or s2.shape != (E, Hb, Ib):
+        _size(s2, "s2", f32, E * Hb * Ib, Ib)
     if D is None:
-        D = torch.empty((T, H), dtype=torch.bfloat16, device=A.device)
+        D = f.empty((T, H), dtype=f.bf16, device=A.device)
+    elif D.dtype is not f.bf16 or D.shape != a:
+        _size(D, "D", f.bf16, T * H, H)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=A.device)
+        ids = f.empty((T, k), dtype=f.i32, device=A.device)
+    elif ids.dtype is not f.i32 or ids.shape != (T, k):
+        _size(ids, "ids", f.i32, T * k, k)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=A.device)
-    out = (_addr(D, "D", types["bf16"], T * H, H), _addr(ids, "ids", types["i32"], T * k, k),
-           _addr(weights, "weights", f32, T * k, k))
-    _resident("A sA logits W1 s1 W2 s2 D ids weights", A, sA, logits, W1, s1, W2, s2, D, ids, weights)
-    rc = lib().fp8_moe_few(*at, *out, T, H, I, E, k, 1 if renormalise else 0, _raw_stream(stream, A))
+        weights = f.empty((T, k), dtype=f32, device=A.device)
+    elif weights.dtype is not f32 or weights.shape != (T, k):
+        _size(weights, "weights", f32, T * k, k)
+    rc = f.moe_few(_here(A, "A"), _here(sA, "sA"), _here(logits, "logits"), _here(W1, "W1"),
+                   _here(s1, "s1"), _here(W2, "W2"), _here(s2, "s2"), _here(D, "D"),
+                   _here(ids, "ids"), _here(weights, "weights"), T, H, I, E, k,
+                   1 if renormalise else 0, f.current(A) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_moe_few")
     return D, ids, weights

@@ -579,6 +579,8 @@ int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float*
   return finish(launch_rmsnorm_backward(c, a, ws), 2);
 }
 
+static int log2_block(int block) { return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7; }
+
 // What the cache's two calls have in common.
 static int check_cache(int T, int B, int heads, int dim, int block, int width, int num_blocks,
                        int most, const int32_t* cu, int fmt) {
@@ -613,7 +615,8 @@ int fp8_kv_append(const void* K, const void* V, int64_t ld_k, int64_t ld_v, uint
   if (int r = ctx_for(stream, &c)) return r;
   const KvAppendArgs a{static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V),
                        ld_k, ld_v, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
-                       cu_new, T, B, heads, dim, block, table_width, num_blocks, max_new, fmt};
+                       cu_new, T, B, heads, dim, block, table_width, num_blocks, max_new, fmt,
+                       log2_block(block)};
   return finish(launch_kv_append(c, a), 1);
 }
 
@@ -639,7 +642,7 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
   const KvAttentionArgs a{static_cast<const __nv_bfloat16*>(Q), ld_q, k_cache, k_scale, v_cache,
                           v_scale, block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O),
                           scale, T, B, heads, group, dim, block, table_width, num_blocks, max_q,
-                          fmt, block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7,
+                          fmt, log2_block(block),
                           wait_limit_ns()};
   void* ws = nullptr;
   if (int r = workspace_for(stream, kv_attention_workspace_bytes(c, a), &ws, kWsAttention)) return r;

@@ -154,6 +154,7 @@ struct KvAppendArgs {
   const int* lens;   // [B]
   const int* cu;     // [B + 1], or null: T / B tokens each
   int T, B, heads, dim, block, width, num_blocks, max_new, fmt;
+  int log_block;
 };
 cudaError_t launch_kv_append(const LaunchCtx& c, const KvAppendArgs& a);
 
