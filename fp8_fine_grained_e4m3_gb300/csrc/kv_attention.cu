@@ -34,9 +34,15 @@ constexpr int kFrag = 16;          // tokens of a fragment
 constexpr int kTok = 2 * kFrag;    // tokens of a tile: two fragments, whose chains of
                                    // dependent instructions run side by side
 constexpr int kRows = 8;   // query rows per fragment
-// A unit is kWarps tiles, one for each warp of a CTA.  A CTA's least share of
-// 256 tokens or more: fewer would cost more to join than to do.
-constexpr int min_units(int warps) { return warps >= 8 ? 1 : 8 / warps; }
+// Work is shared out in tiles.  A CTA's least share is 256 tokens: fewer would
+// cost more to join than to do.
+constexpr int kMinTiles = 8;
+// What beginning and joining an item costs, in tiles (about 4 us, in which the
+// warps of a CTA would do three each).  It counts in a CTA's share as if the item
+// began with that many tiles more: 64 ragged sequences took 108 us with equal
+// shares of the tiles alone, for which the CTAs with many short items were late, and
+// 99 us with it.
+constexpr int kItemCost = 12;
 constexpr int kStages = 2;  // tiles of a warp in shared memory
 constexpr float kNone = -1e30f;  // the running maximum of nothing: below any score
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
@@ -362,10 +368,10 @@ __device__ __forceinline__ void write_out(const KvAttentionArgs& a, int t0, int 
 int row_fragments(const KvAttentionArgs& a) { return (long long)a.max_q * a.group > kRows ? 2 : 1; }
 
 // Warps of a CTA.  With many items each SM has three CTAs of four, whose starts
-// and joins of items overlap.  With no more items than SMs each is shared by many
-// CTAs: one CTA of twelve then leaves a third of the partials and lets an
-// SM's warps end together (one sequence of 131077 tokens, 8 items: 68 us with four
-// warps, 57 with twelve).
+// and joins of items overlap.  With no more items than SMs each is shared by several
+// CTAs: one CTA of twelve to an SM, each with a part of one item, leaves a third of
+// the partials and lets an SM's warps end together (one sequence of 131077 tokens,
+// 8 items: 68 us with four warps, 57 with twelve).
 long long attention_items(const KvAttentionArgs& a) {
   const int rows = kRows * row_fragments(a);
   return ((long long)a.max_q * a.group + rows - 1) / rows * a.heads * a.B;
@@ -376,9 +382,12 @@ int attention_warps(const LaunchCtx& c, const KvAttentionArgs& a) {
 
 // CTAs: as many as run at once, or fewer where the tables cannot hold that much work.
 int attention_grid(const LaunchCtx& c, const KvAttentionArgs& a) {
-  const int warps = attention_warps(c, a), unit = warps * kTok;
-  const long long units = max(1LL, ((long long)a.width * a.block + unit - 1) / unit);
-  const long long most = (attention_items(a) * units + min_units(warps) - 1) / min_units(warps);
+  const int warps = attention_warps(c, a);
+  const long long tiles = max(1LL, ((long long)a.width * a.block + kTok - 1) / kTok);
+  const long long items = attention_items(a);
+  if (warps > 4) return int(min(items * ((tiles + kMinTiles - 1) / kMinTiles), (long long)c.num_sms));
+  const int least = kMinTiles + kItemCost;
+  const long long most = (items * (tiles + kItemCost) + least - 1) / least;
   return int(min(most, (long long)ctas_per_sm(warps, a.dim, row_fragments(a)) * c.num_sms));
 }
 
@@ -388,15 +397,15 @@ size_t counter_bytes(const LaunchCtx& c) { return (size_t(kMaxPerSm) * c.num_sms
 
 
 // The flattened work of a call: items (sequence, row tile, cached head) in
-// that order, each a run of units.  A sequence with no
-// cached token still has one unit per row tile and head, which writes zeros.
+// that order, each a run of tiles (behind what it costs).  A sequence with no
+// cached token still has one tile per row tile and head, which writes zeros.
 struct Sequence {
   int t0, n, len;      // first token on the packed axis, new tokens, cached tokens
-  int row_tiles, units;  // per row tile and head
-  long long total;
+  int row_tiles, tiles;  // tiles of each row tile and head
+  long long total;       // with their items' costs
 };
 
-template <int kNR, int kUnit>
+template <int kNR>
 __device__ __forceinline__ Sequence sequence(const KvAttentionArgs& a, int b, int* status) {
   Sequence s;
   bool ok = sequence_tokens(a.cu, b, a.B, a.T, a.max_q, &s.t0, &s.n);
@@ -408,15 +417,15 @@ __device__ __forceinline__ Sequence sequence(const KvAttentionArgs& a, int b, in
   }
   if (!ok) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
   s.row_tiles = ceil_div(s.n * a.group, kRows * kNR);
-  s.units = max(1, ceil_div(s.len, kUnit));
-  s.total = (long long)s.row_tiles * a.heads * s.units;
+  s.tiles = max(1, ceil_div(s.len, kTok));
+  s.total = (long long)s.row_tiles * a.heads * (s.tiles + kItemCost);
   return s;
 }
 
-// Where a unit lies: its sequence and what is before that, found by the whole CTA.
+// Where a run begins: its sequence and what is before that, found by the whole CTA.
 struct Place {
   int b;
-  long long before;  // units of the sequences before b
+  long long before;  // work of the sequences before b
   Sequence seq;
 };
 
@@ -527,7 +536,8 @@ struct CacheMaps {
   CUtensorMap k, v;
 };
 
-// The CTAs share the units of all items evenly, in runs.  A CTA joins its
+// The CTAs share the work of all items evenly, in runs (or, where there are few
+// items, in parts of one item each).  A CTA joins its
 // warps' results in shared memory for each item of its run; an item that lies in
 // several runs is joined from their partials, in CTA order, by whichever of
 // them finishes last, so results do not depend on timing.
@@ -540,7 +550,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
                                                                    int* counters,
                                                                    Partial<kDim, kNR>* parts,
                                                                    int* status) {
-  constexpr int kR = kRows * kNR, kUnit = kWarps * kTok;
+  constexpr int kR = kRows * kNR;
+  constexpr bool kWholeItems = kWarps > 4;
   extern __shared__ unsigned char raw[];
   unsigned char* shared = raw + (1024u - (smem_addr(raw) & 1023u)) % 1024u;
   float (*so)[kR][kDim + 4] = reinterpret_cast<float (*)[kR][kDim + 4]>(shared);
@@ -568,60 +579,127 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
   griddep_launch_dependents();
   griddep_wait();
 
-  // all units, and each thread's share of the sequences
-  const int per_thread = ceil_div(a.B, 32 * kWarps);
-  const int b0 = min(a.B, int(threadIdx.x) * per_thread), b1 = min(a.B, b0 + per_thread);
-  long long mine = 0;
-  Sequence seq = {};
-  for (int b = b0; b < b1; ++b) {
-    seq = sequence<kNR, kWarps * kTok>(a, b, status);
-    mine += seq.total;
-  }
-  long long upto = mine;
+  int b, item, s0, s1, first, last;  // sequence, item in it, tiles, CTAs that share the item
+  Sequence q_seq;
+  long long u0 = 0, u1 = 1, u = 0, before = 0, per = 0;
+  if constexpr (kWholeItems) {
+    // One part of one item: the items in parts of `per` tiles, the fewest that
+    // leaves no more parts than CTAs.  Thread b holds sequence b.
+    Sequence seq = {};
+    if (int(threadIdx.x) < a.B) seq = sequence<kNR>(a, threadIdx.x, status);
+    const int items = seq.row_tiles * a.heads;
+    auto cta_total = [&](long long v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) scan[warp] = upto;
-  __syncthreads();
-  long long U = 0;
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      __syncthreads();  // scan is free
+      if (lane == 0) scan[warp] = v;
+      __syncthreads();
+      v = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += scan[w];
-    U += scan[w];
-  }
-  const long long per = max((long long)min_units(kWarps), (U + gridDim.x - 1) / gridDim.x);
-  const long long u0 = blockIdx.x * per, u1 = min(U, u0 + per);
-  if (u0 >= u1) return;
-  if (u0 >= upto - mine && u0 < upto) {  // one thread's
-    long long before = upto - mine;
-    int b = b0;
-    if (b1 - b0 > 1)
-      for (;; ++b) {
-        seq = sequence<kNR, kWarps * kTok>(a, b, status);
-        if (u0 < before + seq.total) break;
-        before += seq.total;
-      }
-    place = Place{b, before, seq};
-  }
-  __syncthreads();
-  int b = place.b;
-  long long before = place.before;
-  Sequence q_seq = place.seq;
-
-  for (long long u = u0; u < u1;) {
-    while (u >= before + q_seq.total) {
-      before += q_seq.total;
-      q_seq = sequence<kNR, kWarps * kTok>(a, ++b, status);
+      for (int w = 0; w < kWarps; ++w) v += scan[w];
+      return v;
+    };
+    const long long all = cta_total((long long)items * seq.tiles);
+    int part = max(kMinTiles, int((all + gridDim.x - 1) / gridDim.x));
+    int mine;
+    long long parts_all;
+    while (true) {
+      mine = items > 0 ? items * ceil_div(seq.tiles, part) : 0;
+      parts_all = cta_total(mine);
+      if (parts_all <= gridDim.x) break;
+      part = max(part + 1, int(part * parts_all / gridDim.x));
     }
-    const int item = int((u - before) / q_seq.units);  // row tile and head
-    const long long item0 = before + (long long)item * q_seq.units;
-    const int head = item % a.heads, row0 = item / a.heads * kR;
-    const int s0 = int(u - item0), s1 = int(min((long long)q_seq.units, u1 - item0));
+    if (blockIdx.x >= parts_all) return;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += int(scan[w]);
+    if (int(blockIdx.x) < upto && int(blockIdx.x) >= upto - mine) place = Place{int(threadIdx.x), upto - mine, seq};
+    __syncthreads();
+    b = place.b;
+    q_seq = place.seq;
+    const int parts = ceil_div(q_seq.tiles, part), at = int(blockIdx.x - place.before);
+    item = at / parts;
+    s0 = at % parts * part;
+    s1 = min(q_seq.tiles, s0 + part);
+    first = int(blockIdx.x) - at % parts;
+    last = first + parts - 1;
+  } else {
+    // A run of the work of all items; a thread has a share of the sequences.
+    const int per_thread = ceil_div(a.B, 32 * kWarps);
+    const int b0 = min(a.B, int(threadIdx.x) * per_thread), b1 = min(a.B, b0 + per_thread);
+    long long mine = 0;
+    Sequence seq = {};
+    for (int i = b0; i < b1; ++i) {
+      seq = sequence<kNR>(a, i, status);
+      mine += seq.total;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    long long U = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += scan[w];
+      U += scan[w];
+    }
+    per = max((long long)(kMinTiles + kItemCost), (U + gridDim.x - 1) / gridDim.x);
+    u0 = blockIdx.x * per;
+    u1 = min(U, u0 + per);
+    if (u0 >= u1) return;
+    if (u0 >= upto - mine && u0 < upto) {  // one thread's
+      long long at = upto - mine;
+      int i = b0;
+      if (b1 - b0 > 1)
+        for (;; ++i) {
+          seq = sequence<kNR>(a, i, status);
+          if (u0 < at + seq.total) break;
+          at += seq.total;
+        }
+      place = Place{i, at, seq};
+    }
+    __syncthreads();
+    b = place.b;
+    before = place.before;
+    q_seq = place.seq;
+    u = u0;
+  }
+
+  while (u < u1) {
+    if constexpr (kWholeItems) {
+      u = u1;
+    } else {
+      while (u >= before + q_seq.total) {
+        before += q_seq.total;
+        q_seq = sequence<kNR>(a, ++b, status);
+      }
+      item = int((u - before) / (q_seq.tiles + kItemCost));
+      const long long item0 = before + (long long)item * (q_seq.tiles + kItemCost) + kItemCost;
+      s0 = int(max(u - item0, 0LL));
+      s1 = int(min((long long)q_seq.tiles, u1 - item0));
+      u = item0 + s1;
+      if (s1 <= 0) continue;  // the run ends within the item's cost
+      first = int(item0 / per);
+      last = int((item0 + q_seq.tiles - 1) / per);
+    }
+    const int head = item % a.heads, row0 = item / a.heads * kR;  // item: row tile and head
     const int rows = q_seq.n * a.group, len = q_seq.len;
 
-    // Where the warp's tiles lie.  Lane l looks up the l-th of 32 at a time: the
+    // The warp takes tiles s0 + warp, s0 + warp + kWarps, ...: n_mine of them.
+    const int n_mine = max(0, ceil_div(s1 - s0 - warp, kWarps));
+    auto token_of = [&](int i) { return (s0 + warp + i * kWarps) * kTok; };
+    // Where they lie.  Lane l looks up the l-th of 32 at a time: the
     // cache row of each fragment's first token (-1: not there) and its scales, for
     // the batch in use and, while that is worked on, the one after it.
     const int* table = a.table + size_t(b) * a.width;
@@ -631,14 +709,14 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
       float k[2], v[2];
     } batch = {}, after = {};
     auto look_up = [&](Batch& x, int i) {
-      const int tok = i * kUnit + warp * kTok;
+      const int tok = token_of(i);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int at = tok + kFrag * h;
         x.row[h] = -1;
         if (h == 1 && !halves) {
           x.row[1] = x.row[0] < 0 ? -1 : x.row[0] + kFrag;
-        } else if (i < s1 && at < len) {
+        } else if (i < n_mine && at < len) {
           const int blk = table[at >> a.log_block];
           if (blk >= 0 && blk < a.num_blocks)
             x.row[h] = ((blk * a.heads + head) << a.log_block) + (at & (a.block - 1));
@@ -682,11 +760,11 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
       }
     };
     float unit = 0.f;
-    look_up(batch, s0 + lane);
+    look_up(batch, lane);
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(i, batch, i);
     look_up_scales(batch);
-    look_up(after, s0 + 32 + lane);
+    look_up(after, 32 + lane);
     Queries<kDim> q[kNR];
     State<kDim> s[kNR];
     int limit[kNR][2];  // tokens that the lane's rows see
@@ -707,13 +785,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
     }
     const int least_limit = len - q_seq.n + 1 + row0 / a.group;
     int stage = 0;
-    for (int i = s0; i < s1; ++i) {
-      const int l = (i - s0) & 31;
+    for (int i = 0; i < n_mine; ++i) {
+      const int l = i & 31;
       if (l == 16) look_up_scales(after);
       const uint32_t there = uint32_t(__shfl_sync(0xffffffffu, batch.row[0], l) >= 0) |
                              uint32_t(__shfl_sync(0xffffffffu, batch.row[1], l) >= 0) << 1;
       if (there != 0) {
-        const int tok = i * kUnit + warp * kTok;
+        const int tok = token_of(i);
         float ks[2], vs[2];
         ks[0] = ks[1] = __shfl_sync(0xffffffffu, batch.k[0], l);
         vs[0] = vs[1] = __shfl_sync(0xffffffffu, batch.v[0], l);
@@ -765,8 +843,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
               make_float2(s[i].o[j][r] * unit, s[i].o[j][2 + r] * unit);
       }
     __syncthreads();
-    const bool begins = s0 == 0, ends = s1 == q_seq.units;
-    const int first = int(item0 / per), last = int((item0 + q_seq.units - 1) / per);
+    const bool begins = s0 == 0, ends = s1 == q_seq.tiles;
     Partial<kDim, kNR>* part = parts + 2 * blockIdx.x + (begins ? 1 : 0);
     for (int i = threadIdx.x; i < kR * kDim / 4; i += 32 * kWarps) {
       const int r = i / (kDim / 4), d = i % (kDim / 4) * 4, row = row0 + r;
@@ -800,7 +877,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         __syncthreads();
       }
     }
-    u = item0 + s1;
   }
 }
 
