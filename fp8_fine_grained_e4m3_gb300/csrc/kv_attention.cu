@@ -44,7 +44,7 @@ constexpr int kMinTiles = 8;
 // 99 us with it.
 constexpr int kItemCost = 12;
 constexpr int kStages = 2;  // tiles of a warp in shared memory
-constexpr float kNone = -1e30f;  // the running maximum of nothing: below any score
+constexpr float kNone = -1e30f;  // the maximum of nothing: below any score
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
 
 // Transposes an 8x8 matrix of 16-bit elements held two to a lane.
@@ -162,7 +162,7 @@ struct State {
 
 template <int kDim>
 __device__ __forceinline__ void clear(State<kDim>& s) {
-  s.m[0] = s.m[1] = kNone;
+  s.m[0] = s.m[1] = 0.f;  // the first tile sets it
   s.l[0] = s.l[1] = 0.f;
 #pragma unroll
   for (int j = 0; j < kDim / 16; ++j)
@@ -177,14 +177,14 @@ constexpr float kUnitLow = 1.f / 64, kUnitFar = 1152921504606846976.f;
 
 // One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
 // fragment i sees (may be negative or past its end); least_limit: of the row that sees
-// the fewest.  there: bit h where
+// the fewest.  fresh: the item's first tile of this warp.  there: bit h where
 // fragment h of the tile is; valid: its tokens that exist; ks, vs: the scales
 // of its fragments.
 template <int kDim, bool kE5M2, int kNR>
 __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
                                             const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
                                             const int (&limit)[kNR][2], int least_limit, int tok,
-                                            uint32_t there, int valid, const float (&ks)[2], const float (&vs)[2],
+                                            uint32_t there, bool fresh, int valid, const float (&ks)[2], const float (&vs)[2],
                                             int lane) {
   const int g = lane / 4, t = lane % 4;
   float c[2][kNR][4] = {};
@@ -214,20 +214,16 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
           mma_f16(c[h][i], a, q[i].b[4 * cc + w][0], q[i].b[4 * cc + w][1]);
       }
   }
-  // y: scores in powers of two, less the running maximum; element 2e + r: token g + 8e, row r
-  float mul[2][kNR][2], y[2][kNR][4];
-  bool rises = false;
+  // scores in powers of two, less the running maximum; element 2e + r: token g + 8e, row r
+  bool rises = fresh;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < kNR; ++i) {
+    for (int i = 0; i < kNR; ++i)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) mul[h][i][r] = q[i].mul[r] * ks[h];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[h][i][e] = fmaf(c[h][i][e], mul[h][i][e & 1], -s[i].m[e & 1]);
-    }
-  const bool some_hidden = tok + kTok > least_limit || there != 3u;  // the same for the warp
-  auto hide = [&](float (&v)[2][kNR][4]) {
+      for (int e = 0; e < 4; ++e)
+        c[h][i][e] = fmaf(c[h][i][e], q[i].mul[e & 1] * ks[h], -s[i].m[e & 1]);
+  if (tok + kTok > least_limit || there != 3u) {  // the same for the warp
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -235,45 +231,40 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (g + 8 * (e >> 1) + kFrag * h + tok >= limit[i][e & 1] || !(there >> h & 1))
-            v[h][i][e] = -INFINITY;
-  };
-  if (some_hidden) hide(y);
+            c[h][i][e] = -INFINITY;
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < kNR; ++i)
-      rises |= fmaxf(fmaxf(y[h][i][0], y[h][i][1]), fmaxf(y[h][i][2], y[h][i][3])) > kLazy;
+      rises |= fmaxf(fmaxf(c[h][i][0], c[h][i][1]), fmaxf(c[h][i][2], c[h][i][3])) > kLazy;
   if (__any_sync(0xffffffffu, rises)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < kNR; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[h][i][e] = c[h][i][e] * mul[h][i][e & 1];
-    if (some_hidden) hide(y);
 #pragma unroll
     for (int i = 0; i < kNR; ++i)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float top = fmaxf(fmaxf(y[0][i][r], y[0][i][2 + r]), fmaxf(y[1][i][r], y[1][i][2 + r]));
+        float up = fmaxf(fmaxf(c[0][i][r], c[0][i][2 + r]), fmaxf(c[1][i][r], c[1][i][2 + r]));
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float m = fmaxf(s[i].m[r], top);
-        const float shrink = exp2_fast(s[i].m[r] - m);
-        s[i].m[r] = m;
-        s[i].l[r] *= shrink;
+        for (int o = 4; o < 32; o <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+        // by how much the maximum rises: the first tile's sets it (m was 0), unless it is all
+        // hidden -- tokens are seen from the first on, so then all of them are
+        up = fresh ? (up == -INFINITY ? 0.f : up) : fmaxf(up, 0.f);
+        const float shrink = exp2_fast(-up);
+        s[i].m[r] += up;
+        if (!fresh) {
+          s[i].l[r] *= shrink;
 #pragma unroll
-        for (int j = 0; j < kDim / 16; ++j) {
-          s[i].o[j][r] *= shrink;
-          s[i].o[j][2 + r] *= shrink;
+          for (int j = 0; j < kDim / 16; ++j) {
+            s[i].o[j][r] *= shrink;
+            s[i].o[j][2 + r] *= shrink;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          c[h][i][r] -= up;
+          c[h][i][2 + r] -= up;
         }
       }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < kNR; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[h][i][e] -= s[i].m[e & 1];
   }
   const float top = fmaxf(vs[0], vs[1]);
   if (top > unit || (top < kUnitLow * unit && top * kUnitFar > unit)) {
@@ -293,20 +284,20 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
     for (int i = 0; i < kNR; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        y[h][i][e] = exp2_fast(y[h][i][e]);
-        s[i].l[e & 1] += y[h][i][e];
+        c[h][i][e] = exp2_fast(c[h][i][e]);
+        s[i].l[e & 1] += c[h][i][e];
       }
     if (vs[h] != unit) {  // the warp's tiles of one block share it
       const float to_unit = unit > 0.f ? __fdiv_rn(vs[h], unit) : 0.f;
 #pragma unroll
       for (int i = 0; i < kNR; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[h][i][e] *= to_unit;
+        for (int e = 0; e < 4; ++e) c[h][i][e] *= to_unit;
     }
 #pragma unroll
     for (int i = 0; i < kNR; ++i) {
-      b[h][i][0] = transpose8x8(f16x2_bits(y[h][i][0], y[h][i][1]));
-      b[h][i][1] = transpose8x8(f16x2_bits(y[h][i][2], y[h][i][3]));
+      b[h][i][0] = transpose8x8(f16x2_bits(c[h][i][0], c[h][i][1]));
+      b[h][i][1] = transpose8x8(f16x2_bits(c[h][i][2], c[h][i][3]));
     }
   }
 #pragma unroll
@@ -422,11 +413,16 @@ __device__ __forceinline__ Sequence sequence(const KvAttentionArgs& a, int b, in
   return s;
 }
 
-// Where a run begins: its sequence and what is before that, found by the whole CTA.
-struct Place {
+// Where a CTA is in its work.  It lies in shared memory, for what only the ends
+// of an item need would crowd the registers of the loop between them.
+struct Walk {
+  long long u, u1;    // next and end of its run
+  long long before;   // work of the sequences before b
+  long long per;      // of a run
   int b;
-  long long before;  // work of the sequences before b
   Sequence seq;
+  int item, s0, s1;   // item in the sequence (row tile and head), tiles of it
+  int first, last;    // CTAs that share it
 };
 
 // A partial result in the workspace: what a CTA knows of an item that it shares.
@@ -557,7 +553,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
   float (*so)[kR][kDim + 4] = reinterpret_cast<float (*)[kR][kDim + 4]>(shared);
   __shared__ float sm[kWarps][kR], sl[kWarps][kR];
   __shared__ long long scan[kWarps];
-  __shared__ Place place;
+  __shared__ Walk walks[2];  // the item's, and the next one's
   __shared__ int last_one;
   __shared__ int gave_up, never;  // a wait ran out; always 0
   __shared__ uint64_t bars[kWarps][kStages];
@@ -579,9 +575,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
   griddep_launch_dependents();
   griddep_wait();
 
-  int b, item, s0, s1, first, last;  // sequence, item in it, tiles, CTAs that share the item
-  Sequence q_seq;
-  long long u0 = 0, u1 = 1, u = 0, before = 0, per = 0;
   if constexpr (kWholeItems) {
     // One part of one item: the items in parts of `per` tiles, the fewest that
     // leaves no more parts than CTAs.  Thread b holds sequence b.
@@ -620,16 +613,19 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
     if (lane == 31) scan[warp] = upto;
     __syncthreads();
     for (int w = 0; w < warp; ++w) upto += int(scan[w]);
-    if (int(blockIdx.x) < upto && int(blockIdx.x) >= upto - mine) place = Place{int(threadIdx.x), upto - mine, seq};
-    __syncthreads();
-    b = place.b;
-    q_seq = place.seq;
-    const int parts = ceil_div(q_seq.tiles, part), at = int(blockIdx.x - place.before);
-    item = at / parts;
-    s0 = at % parts * part;
-    s1 = min(q_seq.tiles, s0 + part);
-    first = int(blockIdx.x) - at % parts;
-    last = first + parts - 1;
+    if (int(blockIdx.x) < upto && int(blockIdx.x) >= upto - mine) {  // one thread's
+      const int parts = ceil_div(seq.tiles, part), at = int(blockIdx.x) - (upto - mine);
+      Walk w = {};
+      w.u1 = 1;
+      w.b = threadIdx.x;
+      w.seq = seq;
+      w.item = at / parts;
+      w.s0 = at % parts * part;
+      w.s1 = min(seq.tiles, w.s0 + part);
+      w.first = int(blockIdx.x) - at % parts;
+      w.last = w.first + parts - 1;
+      walks[0] = w;
+    }
   } else {
     // A run of the work of all items; a thread has a share of the sequences.
     const int per_thread = ceil_div(a.B, 32 * kWarps);
@@ -654,9 +650,8 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
       if (w < warp) upto += scan[w];
       U += scan[w];
     }
-    per = max((long long)(kMinTiles + kItemCost), (U + gridDim.x - 1) / gridDim.x);
-    u0 = blockIdx.x * per;
-    u1 = min(U, u0 + per);
+    const long long per = max((long long)(kMinTiles + kItemCost), (U + gridDim.x - 1) / gridDim.x);
+    const long long u0 = blockIdx.x * per, u1 = min(U, u0 + per);
     if (u0 >= u1) return;
     if (u0 >= upto - mine && u0 < upto) {  // one thread's
       long long at = upto - mine;
@@ -667,33 +662,33 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
           if (u0 < at + seq.total) break;
           at += seq.total;
         }
-      place = Place{i, at, seq};
+      walks[0] = Walk{u0, u1, at, per, i, seq, 0, 0, 0, 0, 0};
     }
-    __syncthreads();
-    b = place.b;
-    before = place.before;
-    q_seq = place.seq;
-    u = u0;
   }
+  __syncthreads();
 
-  while (u < u1) {
+  for (int flip = 0; walks[flip].u < walks[flip].u1; flip ^= 1) {
+    Walk w = walks[flip];
     if constexpr (kWholeItems) {
-      u = u1;
+      w.u = w.u1;
     } else {
-      while (u >= before + q_seq.total) {
-        before += q_seq.total;
-        q_seq = sequence<kNR>(a, ++b, status);
+      while (w.u >= w.before + w.seq.total) {
+        w.before += w.seq.total;
+        w.seq = sequence<kNR>(a, ++w.b, status);
       }
-      item = int((u - before) / (q_seq.tiles + kItemCost));
-      const long long item0 = before + (long long)item * (q_seq.tiles + kItemCost) + kItemCost;
-      s0 = int(max(u - item0, 0LL));
-      s1 = int(min((long long)q_seq.tiles, u1 - item0));
-      u = item0 + s1;
-      if (s1 <= 0) continue;  // the run ends within the item's cost
-      first = int(item0 / per);
-      last = int((item0 + q_seq.tiles - 1) / per);
+      w.item = int((w.u - w.before) / (w.seq.tiles + kItemCost));
+      const long long item0 = w.before + (long long)w.item * (w.seq.tiles + kItemCost) + kItemCost;
+      w.s0 = int(max(w.u - item0, 0LL));
+      w.s1 = int(min((long long)w.seq.tiles, w.u1 - item0));
+      w.u = item0 + w.s1;
+      if (w.s1 <= 0) break;  // the run ends within the item's cost
+      w.first = int(item0 / w.per);
+      w.last = int((item0 + w.seq.tiles - 1) / w.per);
     }
-    const int head = item % a.heads, row0 = item / a.heads * kR;  // item: row tile and head
+    if (threadIdx.x == 0) walks[flip ^ 1] = w;
+    const int b = w.b, s0 = w.s0, s1 = w.s1;
+    const Sequence q_seq = w.seq;
+    const int head = w.item % a.heads, row0 = w.item / a.heads * kR;
     const int rows = q_seq.n * a.group, len = q_seq.len;
 
     // The warp takes tiles s0 + warp, s0 + warp + kWarps, ...: n_mine of them.
@@ -785,6 +780,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
     }
     const int least_limit = len - q_seq.n + 1 + row0 / a.group;
     int stage = 0;
+    bool fresh = true;
     for (int i = 0; i < n_mine; ++i) {
       const int l = i & 31;
       if (l == 16) look_up_scales(after);
@@ -809,8 +805,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         }
         phases ^= 1u << stage;
         in_flight &= ~(1u << stage);
-        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[stage], q, limit, least_limit, tok, there,
+        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[stage], q, limit, least_limit, tok, there, fresh,
                                       len - tok, ks, vs, lane);
+        fresh = false;
         __syncwarp();  // the stage has been read
       }
       if (l + kStages < 32)
@@ -834,7 +831,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) s[i].l[r] += __shfl_xor_sync(0xffffffffu, s[i].l[r], o);
         if (g == 0) {
-          sm[warp][row] = s[i].m[r];
+          sm[warp][row] = s[i].l[r] == 0.f ? kNone : s[i].m[r];
           sl[warp][row] = s[i].l[r];
         }
 #pragma unroll
@@ -843,10 +840,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
               make_float2(s[i].o[j][r] * unit, s[i].o[j][2 + r] * unit);
       }
     __syncthreads();
-    const bool begins = s0 == 0, ends = s1 == q_seq.tiles;
+    const Walk& done = walks[flip ^ 1];
+    const bool begins = done.s0 == 0, ends = done.s1 == done.seq.tiles;
+    const int out_head = done.item % a.heads, out_row0 = done.item / a.heads * kR;
+    const int out_rows = done.seq.n * a.group;
     Partial<kDim, kNR>* part = parts + 2 * blockIdx.x + (begins ? 1 : 0);
     for (int i = threadIdx.x; i < kR * kDim / 4; i += 32 * kWarps) {
-      const int r = i / (kDim / 4), d = i % (kDim / 4) * 4, row = row0 + r;
+      const int r = i / (kDim / 4), d = i % (kDim / 4) * 4, row = out_row0 + r;
       float m = kNone;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w][r]);
@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) add_scaled(o, l, so[w][r] + d, sl[w][r], exp2_fast(sm[w][r] - m));
       if (begins && ends) {
-        if (row < rows) write_out<kDim>(a, q_seq.t0, head, row, d, o, l);
+        if (row < out_rows) write_out<kDim>(a, done.seq.t0, out_head, row, d, o, l);
       } else {
         *reinterpret_cast<float4*>(&part->o[r][d]) = o;
         if (d == 0) {
@@ -867,11 +867,12 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
     fence_proxy_async_smem();  // the copies that follow come through another proxy
     __syncthreads();           // the shared buffers are free, and this CTA's partial is written
     if (!(begins && ends)) {
-      if (threadIdx.x == 0) last_one = atomic_add_acq_rel_gpu(counters + first, 1) == last - first;
+      if (threadIdx.x == 0) last_one = atomic_add_acq_rel_gpu(counters + done.first, 1) == done.last - done.first;
       __syncthreads();
       if (last_one) {
-        if (threadIdx.x == 0) counters[first] = 0;
-        join_partials<kDim, kNR, kWarps>(a, parts, first, last, q_seq.t0, head, row0, rows,
+        if (threadIdx.x == 0) counters[done.first] = 0;
+        join_partials<kDim, kNR, kWarps>(a, parts, done.first, done.last, done.seq.t0, out_head,
+                                         out_row0, out_rows,
                                  reinterpret_cast<float*>(shared));
         fence_proxy_async_smem();
         __syncthreads();
