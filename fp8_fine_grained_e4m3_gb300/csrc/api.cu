@@ -657,7 +657,11 @@ int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const ui
     return FP8GEMM_ERR_SHAPE;
   if (E <= 0 || E > kMoeMaxExperts || top_k <= 0 || top_k > kMoeMaxTopK || top_k > E)
     return FP8GEMM_ERR_SHAPE;
-  if ((long long)I * 2 > 0x7fffffffLL) return FP8GEMM_ERR_SHAPE;
+  if ((long long)I * 2 > 0x7fffffffLL || (long long)E * I * 2 > 0x7fffffffLL ||
+      (long long)E * H > 0x7fffffffLL)
+    return FP8GEMM_ERR_SHAPE;  // rows of the weights are 32-bit coordinates
+  if ((long long)T * top_k * ceil_div(I, kBlockK) * ceil_div(H, kBlockK) > 0x7fffffffLL)
+    return FP8GEMM_ERR_SHAPE;
   if (T == 0) return FP8GEMM_OK;
   if (!A || !sA || !logits || !W1 || !s1 || !W2 || !s2 || !D || !ids || !weights)
     return FP8GEMM_ERR_NULL;

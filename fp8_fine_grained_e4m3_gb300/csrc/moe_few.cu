@@ -10,8 +10,9 @@
 // and added in FP32).
 //
 // Two launches: the up kernel (gate and up products, SwiGLU and quantisation) and
-// the down kernel (down product and weighted sum); routing is done by each of
-// their CTAs for a few tokens, by a launch of one CTA before them for more.
+// the down kernel (down product and weighted sum).  For a few tokens each of
+// their CTAs routes for itself and the last CTA of an output tile adds what several
+// share; for more, two small launches do that.
 //
 // Bound by the chosen experts' weights, read once.  In both product kernels
 // the K blocks of all output tiles of all chosen experts form one sequence
@@ -30,6 +31,7 @@
 #include "f8_convert.cuh"
 #include "moe_few.cuh"
 #include "ptx.cuh"
+#include "vec.cuh"
 
 namespace fp8gemm {
 namespace {
@@ -204,6 +206,16 @@ __device__ __forceinline__ void route_token(const float* logits, int E, int k, i
   *w = sum > 0.f ? __fdiv_rn(mine, sum) : 0.f;
 }
 
+__device__ __forceinline__ void route_any(const float* logits, int E, int k, int renormalise, int* id,
+                                          float* w) {
+  if (E <= 32)
+    route_token<1>(logits, E, k, renormalise, id, w);
+  else if (E <= 128)
+    route_token<4>(logits, E, k, renormalise, id, w);
+  else
+    route_token<kMoeMaxExperts / 32>(logits, E, k, renormalise, id, w);
+}
+
 // The whole CTA (kW warps, T k <= 32 kW) routes all tokens; ids_out and w_out
 // (the call's outputs) may be null.  Ends with the results written and a barrier.
 template <int kW>
@@ -215,17 +227,30 @@ __device__ __forceinline__ void route_all(const float* logits, const Route& r, u
   uint16_t* first = reinterpret_cast<uint16_t*>(warp_sum + 64);     // [E]
   uint8_t* hist = reinterpret_cast<uint8_t*>(first + kMoeMaxExperts);  // [kW][kMoeMaxExperts]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, P = T * k;
+  if (T == 1) {  // every chosen expert has one pair: their order is all there is to find
+    if (warp == 0) {
+      int id;
+      float w;
+      route_any(logits, E, k, renormalise, &id, &w);
+      int place = 0;
+      for (int i = 0; i < k; ++i) place += __shfl_sync(0xffffffffu, id, i) < id;
+      if (lane < k) {
+        r.list[place] = lane;
+        r.pass[place] = pack_pass(id, place, 1);
+        r.weight[lane] = w;
+        if (ids_out) ids_out[lane] = id;
+        if (w_out) w_out[lane] = w;
+      }
+      if (lane == 0) *r.passes = k;
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = threadIdx.x; i < kW * kMoeMaxExperts / 4; i += 32 * kW) reinterpret_cast<uint32_t*>(hist)[i] = 0u;
   for (int t = warp; t < T; t += kW) {
     int id;
     float w;
-    const float* row = logits + size_t(t) * E;
-    if (E <= 32)
-      route_token<1>(row, E, k, renormalise, &id, &w);
-    else if (E <= 128)
-      route_token<4>(row, E, k, renormalise, &id, &w);
-    else
-      route_token<kMoeMaxExperts / 32>(row, E, k, renormalise, &id, &w);
+    route_any(logits + size_t(t) * E, E, k, renormalise, &id, &w);
     if (lane < k) {
       const int p = t * k + lane;
       ids[p] = id;
@@ -316,15 +341,15 @@ __device__ __forceinline__ Route copy_route(const Route& g, uint8_t* to, int pai
 }
 
 // ------------------------------------------------------------ product kernels
-// A CTA's run of the unit sequence.
+// A CTA's run of the unit sequence (under 2^31 units: the host checks).
 struct Run {
-  long long per, u0, u1;
-  __device__ explicit Run(long long U) {
-    per = max((long long)kMinUnits, (U + gridDim.x - 1) / gridDim.x);
-    u0 = min(U, blockIdx.x * per);
-    u1 = min(U, u0 + per);
+  int per, u0, u1;
+  __device__ Run(int units, int ctas, int cta) {
+    per = max(kMinUnits, int((units + unsigned(ctas) - 1) / unsigned(ctas)));
+    u0 = int(min((long long)units, (long long)cta * per));
+    u1 = int(min((long long)units, (long long)u0 + per));
   }
-  __device__ int units() const { return int(u1 - u0); }
+  __device__ int units() const { return u1 - u0; }
 };
 
 // One warp's ring of weight tiles.
@@ -367,6 +392,10 @@ __device__ __forceinline__ uint8_t* init_shared(Shared& sh, uint8_t* raw, const 
   return raw + (1024u - (smem_addr(raw) & 1023u)) % 1024u;
 }
 
+__device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float4& v) {
+  *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_bits(v.x, v.y), bf16x2_bits(v.z, v.w));
+}
+
 // Gate and up products.  Unit: one K block of a tile (pass, 128 hidden
 // columns); warp w takes hidden columns 32 w .. + 31 of it, rows of gate and of
 // up alike, so that SwiGLU stays within a lane.
@@ -403,12 +432,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
   } else {
     r = copy_route(given, rings + kWarps * kUpStages<NT> * 64 * kBlockK, a.T * a.k, false);
   }
-  const Run run((long long)*r.passes * Ib * Kb);
+  const Run run(*r.passes * Ib * Kb, gridDim.x, blockIdx.x);
   int left = run.units();
   if (left == 0) return;
 
   // the tile and K block in use, and those asked for (kUpStages ahead)
-  int tile = int(run.u0 / Kb), kb = int(run.u0 - (long long)tile * Kb);
+  int tile = run.u0 / Kb, kb = run.u0 - tile * Kb;
   int pi = tile / Ib, ib = tile - pi * Ib;
   int ask_left = left, ask_pi = pi, ask_ib = ib, ask_kb = kb, ask_stage = 0;
   int ask_row = Pass(r.pass[pi]).e * 2 * a.I + ib * kBlockK + 32 * warp;
@@ -515,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
     --left;
     if (kb < Kb && left > 0) continue;
 
-    const long long tile0 = (long long)tile * Kb;
+    const int tile0 = tile * Kb;
     // the run's share of this tile is done
     const bool whole = tile0 >= run.u0 && tile0 + Kb <= run.u1;
-    const int first = int(tile0 / run.per), last = int((tile0 + Kb - 1) / run.per);
+    const int first = tile0 / run.per, last = (tile0 + Kb - 1) / run.per;
     if (!whole) {
       float* part = parts + size_t(2 * blockIdx.x + (tile0 >= run.u0 ? 1 : 0)) * kPart +
                     warp * (4 * NT * 4 * 32) + lane;
@@ -628,6 +657,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
   }
 }
 
+// The down kernel's partials hold 512 bytes a token and warp.  For a few tokens the
+// last CTA of a tile adds them; for more that took one CTA 20 us at the end of a
+// call (64 tokens, 9 partials of 32 KB), so a launch of many CTAs does it.
+template <int NT>
+constexpr bool kJoinHere = NT == 1;
+
 // Down product and weighted sum.  Unit: one K block of one pass for a tile of
 // 128 output columns; warp w takes columns 32 w .. + 31 and keeps a sum per token
 // in shared memory that no other warp touches.
@@ -662,14 +697,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
     r = copy_route(given, reinterpret_cast<uint8_t*>(all_sums + kWarps * a.T * kSumRow), a.T * a.k, true);
   }
   const int passes = *r.passes;
-  const long long per_tile = (long long)passes * Kb;
-  const Run run(Hb * per_tile);
+  const int per_tile = passes * Kb;
+  const Run run(Hb * per_tile, gridDim.x, blockIdx.x);
   int left = run.units();
   if (left == 0) {
     griddep_wait();
     return;
   }
-  int tile = int(run.u0 / per_tile), pi = int(run.u0 - tile * per_tile) / Kb, kb = int(run.u0 % Kb);
+  int tile = run.u0 / per_tile, pi = (run.u0 - tile * per_tile) / Kb, kb = run.u0 % Kb;
   int ask_left = left, ask_tile = tile, ask_pi = pi, ask_kb = kb, ask_stage = 0;
   int ask_row = Pass(r.pass[pi]).e * a.H + tile * kBlockK + 32 * warp;
   auto fetch = [&]() {
@@ -692,9 +727,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
   };
 #pragma unroll
   for (int i = 0; i < kDownStages; ++i) fetch();
-  // No early launch of what follows: the next call's routing takes a whole SM's
-  // registers, which this kernel's CTAs would go without (64 tokens: 300 us a
-  // call with it, 261 without).
+  // With the sum in a launch of its own, that may come early.  The next call's
+  // routing may not: it takes a whole SM's registers, which this kernel's CTAs would
+  // go without (64 tokens: 300 us a call with it, 261 without).
+  if constexpr (!kJoinHere<NT>) griddep_launch_dependents();
   griddep_wait();
 
   // What a unit needs besides weights.  Columns without a pair take the
@@ -797,10 +833,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
     __syncwarp();
     if (left > 0 && tile == this_tile) continue;
 
-    const long long tile0 = this_tile * per_tile;
+    const int tile0 = this_tile * per_tile;
     // the run's share of this tile is done
     const bool whole = tile0 >= run.u0 && tile0 + per_tile <= run.u1;
-    const int first = int(tile0 / run.per), last = int((tile0 + per_tile - 1) / run.per);
+    const int first = tile0 / run.per, last = (tile0 + per_tile - 1) / run.per;
     const size_t part_size = size_t(kWarps) * a.T * 32;
     const int h0 = this_tile * kBlockK + 32 * warp;
     if (!whole) {
@@ -808,44 +844,78 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
       for (int i = lane; i < a.T * 8; i += 32)
         reinterpret_cast<float4*>(part)[i] =
             *reinterpret_cast<const float4*>(sums + i / 8 * kSumRow + i % 8 * 4);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        sh.last_one = atomic_add_acq_rel_gpu(counters + first, 1) == last - first;
-        if (sh.last_one) counters[first] = 0;
-      }
-      __syncthreads();
-      if (sh.last_one)
-        for (int i = lane; i < a.T * 8; i += 32) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int q = first; q <= last; ++q) {
-            const float4 p = __ldcg(reinterpret_cast<const float4*>(
-                                        parts + (2 * q + (q == first ? 1 : 0)) * part_size + warp * a.T * 32) + i);
-            v.x += p.x;
-            v.y += p.y;
-            v.z += p.z;
-            v.w += p.w;
-          }
-          *reinterpret_cast<float4*>(sums + i / 8 * kSumRow + i % 8 * 4) = v;
+      if constexpr (kJoinHere<NT>) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          sh.last_one = atomic_add_acq_rel_gpu(counters + first, 1) == last - first;
+          if (sh.last_one) counters[first] = 0;
         }
-      __syncwarp();
+        __syncthreads();
+        if (sh.last_one)
+          for (int i = lane; i < a.T * 8; i += 32) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll 8
+            for (int q = first; q <= last; ++q) {
+              const float4 p = __ldcg(reinterpret_cast<const float4*>(
+                                          parts + (2 * q + (q == first ? 1 : 0)) * part_size + warp * a.T * 32) + i);
+              v.x += p.x;
+              v.y += p.y;
+              v.z += p.z;
+              v.w += p.w;
+            }
+            *reinterpret_cast<float4*>(sums + i / 8 * kSumRow + i % 8 * 4) = v;
+          }
+        __syncwarp();
+      }
     }
-    if (whole || sh.last_one)
+    if (whole || (kJoinHere<NT> && sh.last_one))
       for (int i = lane; i < a.T * 8; i += 32) {
         const int h = h0 + i % 8 * 4;
         if (h >= a.H) continue;  // H is a multiple of 16
-        const float* s = sums + i / 8 * kSumRow + i % 8 * 4;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(s[0], s[1]), hi = __floats2bfloat162_rn(s[2], s[3]);
-        uint2 o;
-        o.x = *reinterpret_cast<const uint32_t*>(&lo);
-        o.y = *reinterpret_cast<const uint32_t*>(&hi);
-        *reinterpret_cast<uint2*>(a.D + size_t(i / 8) * a.H + h) = o;
+        store_bf16x4(a.D + size_t(i / 8) * a.H + h,
+                     *reinterpret_cast<const float4*>(sums + i / 8 * kSumRow + i % 8 * 4));
       }
     if (left == 0) break;
     __syncthreads();  // last_one is free
     for (int i = lane; i < a.T * kSumRow; i += 32) sums[i] = 0.f;
     __syncwarp();
   }
+}
+
+// The tiles that lie in several runs of the down kernel: the sum of their
+// partials in CTA order.  Grid (tiles, tokens / 4); a thread has 4 columns of one token.
+__global__ void __launch_bounds__(128) moe_sum_kernel(const MoeArgs a, const int* passes,
+                                                      const float* parts, int ctas) {
+  const int Kb = ceil_div(a.I, kBlockK), Hb = ceil_div(a.H, kBlockK);
+  const int tile = blockIdx.x, token = blockIdx.y * 4 + threadIdx.x / 32;
+  const int warp = threadIdx.x % 32 / 8, c = threadIdx.x % 8;  // of the down kernel
+  const int per_tile = __ldcg(passes) * Kb;  // routing was complete before the down kernel began
+  const Run run(Hb * per_tile, ctas, 0);
+  const int tile0 = tile * per_tile, first = tile0 / run.per, last = (tile0 + per_tile - 1) / run.per;
+  const int h = tile * kBlockK + 32 * warp + 4 * c;
+  griddep_wait();
+  if (first == last || token >= a.T || h >= a.H) return;
+  constexpr int kAtOnce = 8;
+  const size_t size = size_t(kWarps) * a.T * 32;
+  const float* p = parts + (size_t(warp) * a.T + token) * 32 + 4 * c;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q0 = first; q0 <= last; q0 += kAtOnce) {
+    float4 v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int q = q0 + i;
+      v[i] = q <= last ? __ldcg(reinterpret_cast<const float4*>(p + size_t(2 * q + (q == first ? 1 : 0)) * size))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      sum.x += v[i].x;
+      sum.y += v[i].y;
+      sum.z += v[i].z;
+      sum.w += v[i].w;
+    }
+  }
+  store_bf16x4(a.D + size_t(token) * a.H + h, sum);
 }
 
 // ------------------------------------------------------------------- launches
@@ -918,8 +988,14 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   if (cudaError_t e = launch_dependent(c, up, up_per_sm * c.num_sms, kThreads, up_smem, a, r, m1, H8, sH, counters,
                                        reinterpret_cast<float*>(ws + l.up), c.status))
     return e;
-  return launch_dependent(c, down, down_per_sm * c.num_sms, kThreads, down_smem, a, r, m2, H8, sH,
-                          counters + kMaxPerSm * c.num_sms, reinterpret_cast<float*>(ws + l.down), c.status);
+  float* parts = reinterpret_cast<float*>(ws + l.down);
+  const int ctas = down_per_sm * c.num_sms;
+  if (cudaError_t e = launch_dependent(c, down, ctas, kThreads, down_smem, a, r, m2, H8, sH,
+                                       counters + kMaxPerSm * c.num_sms, parts, c.status))
+    return e;
+  if constexpr (kJoinHere<NT>) return cudaSuccess;
+  return launch_dependent(c, moe_sum_kernel, dim3(ceil_div(a.H, kBlockK), ceil_div(a.T, 4)), 128, 0, a,
+                          r.passes, parts, ctas);
 }
 
 }  // namespace
@@ -931,7 +1007,7 @@ cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace
   const Layout l = layout(c, a);
   const Route r{reinterpret_cast<float*>(ws + l.weight), reinterpret_cast<int*>(ws + l.list),
                 reinterpret_cast<uint32_t*>(ws + l.pass), reinterpret_cast<int*>(ws + l.passes)};
-  *launches = a.T <= kOwnTokens ? 2 : 3;
+  *launches = a.T <= kOwnTokens ? 2 : 4;
   switch (fragments(a)) {
     case 1: return launch_nt<1, 4>(c, a, r, ws, l);
     case 2: return a.T <= 16 ? launch_nt<2, 4>(c, a, r, ws, l) : launch_nt<2, kManyStages>(c, a, r, ws, l);
