@@ -206,8 +206,11 @@ __device__ __forceinline__ void route_token(const float* logits, int E, int k, i
   *w = sum > 0.f ? __fdiv_rn(mine, sum) : 0.f;
 }
 
-__device__ __forceinline__ void route_any(const float* logits, int E, int k, int renormalise, int* id,
-                                          float* w) {
+// One copy of it for all callers: code that runs once in a launch is fetched line
+// by line, and the product kernels wait for it (one token: 42.6 us a call with every
+// width inlined at both calls, 40.0 with one function).
+__device__ __noinline__ void route_any(const float* logits, int E, int k, int renormalise, int* id,
+                                       float* w) {
   if (E <= 32)
     route_token<1>(logits, E, k, renormalise, id, w);
   else if (E <= 128)
@@ -392,9 +395,40 @@ __device__ __forceinline__ uint8_t* init_shared(Shared& sh, uint8_t* raw, const 
   return raw + (1024u - (smem_addr(raw) & 1023u)) % 1024u;
 }
 
+// Four columns of the partials of CTAs first .. last, added in that order, eight
+// of their loads in flight.
+__device__ __forceinline__ float4 sum_partials(const float* parts, size_t size, int first, int last) {
+  constexpr int kAtOnce = 8;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q0 = first; q0 <= last; q0 += kAtOnce) {
+    float4 v[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int q = q0 + i;
+      v[i] = q <= last ? __ldcg(reinterpret_cast<const float4*>(
+                             parts + size_t(2 * q + (q == first ? 1 : 0)) * size))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      sum.x += v[i].x;
+      sum.y += v[i].y;
+      sum.z += v[i].z;
+      sum.w += v[i].w;
+    }
+  }
+  return sum;
+}
+
 __device__ __forceinline__ void store_bf16x4(__nv_bfloat16* to, const float4& v) {
   *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2_bits(v.x, v.y), bf16x2_bits(v.z, v.w));
 }
+
+// x / (1 + e^-x), to some 2^-21 of it (h is rounded to 4 bits next).  This and the
+// quantisation run once in a CTA, right behind its last copy, from instructions that
+// are not in any cache yet: the division's and the exponential's full sequences
+// in their place cost a call 2 us.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
 // Gate and up products.  Unit: one K block of a tile (pass, 128 hidden
 // columns); warp w takes hidden columns 32 w .. + 31 of it, rows of gate and of
@@ -596,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float gate = acc[m][n][c];
-            float h = __fdiv_rn(gate, 1.f + expf(-gate)) * acc[2 + m][n][c];
+            float h = silu(gate) * acc[2 + m][n][c];
             if (i0 + 32 * warp + 16 * m + g + 8 * (c >> 1) >= a.I) h = 0.f;
             acc[m][n][c] = h;
             top[c & 1] = fmaxf(top[c & 1], fabsf(h));
@@ -621,12 +655,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
           const float s = __fdiv_rn(top, kE4M3Max);
           if (j < at.cnt && warp == 0 && g == 0)
             sH[size_t(r.list[at.first + j]) * Ib + ib] = s;
+          // h / s without the division's sequence (see silu): both times a power of two that
+          // brings s into the range of the corrected quotient (h that this makes too small
+          // to hold has the code 0)
+          const float pre = s < 1e-25f ? 0x1p100f : s > 1e25f ? 0x1p-100f : 1.f;
+          const Reciprocal d = reciprocal(top != 0.f ? s * pre : 1.f);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
               codes[j][32 * warp + 16 * m + 8 * e + g] =
-                  top != 0.f ? uint8_t(cvt_f8x2<false>(__fdiv_rn(acc[m][n][2 * e + c], s), 0.f)) : 0;
+                  uint8_t(cvt_f8x2<false>(quotient(acc[m][n][2 * e + c] * pre, d), 0.f));
         }
       }
       __syncthreads();
@@ -853,16 +892,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
         __syncthreads();
         if (sh.last_one)
           for (int i = lane; i < a.T * 8; i += 32) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  #pragma unroll 8
-            for (int q = first; q <= last; ++q) {
-              const float4 p = __ldcg(reinterpret_cast<const float4*>(
-                                          parts + (2 * q + (q == first ? 1 : 0)) * part_size + warp * a.T * 32) + i);
-              v.x += p.x;
-              v.y += p.y;
-              v.z += p.z;
-              v.w += p.w;
-            }
+            const float4 v = sum_partials(parts + warp * a.T * 32 + 4 * i, part_size, first, last);
             *reinterpret_cast<float4*>(sums + i / 8 * kSumRow + i % 8 * 4) = v;
           }
         __syncwarp();
@@ -895,27 +925,9 @@ __global__ void __launch_bounds__(128) moe_sum_kernel(const MoeArgs a, const int
   const int h = tile * kBlockK + 32 * warp + 4 * c;
   griddep_wait();
   if (first == last || token >= a.T || h >= a.H) return;
-  constexpr int kAtOnce = 8;
-  const size_t size = size_t(kWarps) * a.T * 32;
-  const float* p = parts + (size_t(warp) * a.T + token) * 32 + 4 * c;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int q0 = first; q0 <= last; q0 += kAtOnce) {
-    float4 v[kAtOnce];
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int q = q0 + i;
-      v[i] = q <= last ? __ldcg(reinterpret_cast<const float4*>(p + size_t(2 * q + (q == first ? 1 : 0)) * size))
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      sum.x += v[i].x;
-      sum.y += v[i].y;
-      sum.z += v[i].z;
-      sum.w += v[i].w;
-    }
-  }
-  store_bf16x4(a.D + size_t(token) * a.H + h, sum);
+  store_bf16x4(a.D + size_t(token) * a.H + h,
+               sum_partials(parts + (size_t(warp) * a.T + token) * 32 + 4 * c,
+                            size_t(kWarps) * a.T * 32, first, last));
 }
 
 // ------------------------------------------------------------------- launches
