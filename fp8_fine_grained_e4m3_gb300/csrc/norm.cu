@@ -28,6 +28,14 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
+// amax / limit: the corrected quotient where that is exact.
+template <bool kE5M2>
+__device__ __forceinline__ float block_scale(float amax) {
+  constexpr float kLimit = kE5M2 ? 57344.f : 448.f;
+  const Reciprocal d{kLimit, 1.f / kLimit, true};
+  return amax >= 1e-25f && amax <= 1e30f ? quotient(amax, d) : __fdiv_rn(amax, kLimit);
+}
+
 // Eight values to codes of one scale.
 template <bool kE5M2>
 __device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, const Reciprocal& d) {
@@ -63,17 +71,12 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    unpack8(x[i], h[i]);
     if constexpr (kRes) {
       const int k = 8 * (threadIdx.x + i * blockDim.x);
-      float rv[8];
-      unpack8(r[i], rv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] += rv[j];
-      pack8(h[i], x[i]);  // what the gradient and the next layer see
-      unpack8(x[i], h[i]);
+      x[i] = add8(x[i], r[i]);  // what the gradient and the next layer see
       if (k < K) store8(H + row + k, x[i]);
     }
+    unpack8(x[i], h[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
   }
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const Reciprocal s = reciprocal(__fdiv_rn(amax, f8_limit<kE5M2>()));
+    const Reciprocal s = reciprocal(block_scale<kE5M2>(amax));
     if (k < K) {
       *reinterpret_cast<uint2*>(Q + row + k) = quant8<kE5M2>(h[i], amax, s);
       if (threadIdx.x % 16 == 0) sQ[size_t(blockIdx.x) * Kb + k / kBlockK] = s.s;
@@ -158,37 +161,38 @@ __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
   };
   int flip = 0;  // two buffers: a row's sums are read while the next row's are written
   for (int m = blockIdx.x; m < M; m += gridDim.x, flip ^= 1) {
-    const Row here = next;
-    if (kAhead && m + int(gridDim.x) < M) load(m + gridDim.x);
+    float xh[kIter][8], dx[kIter][8];  // h rstd and dy g, kept over the row's sum
+    Raw8<T> up[kIter];
+    const float rstd = next.rstd;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-      float xh[8], dx[8], w[8];
-      unpack8(here.h[i], xh);
-      unpack8(here.dy[i], dx);
+      float w[8];
+      unpack8(next.h[i], xh[i]);
+      unpack8(next.dy[i], dx[i]);
+      up[i] = next.up[i];
       gain(i, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xh[j] *= here.rstd;
-        dg[i][j] = fmaf(dx[j], xh[j], dg[i][j]);
-        sum = fmaf(dx[j] * w[j], xh[j], sum);
+        xh[i][j] *= rstd;
+        dg[i][j] = fmaf(dx[i][j], xh[i][j], dg[i][j]);
+        dx[i][j] *= w[j];
+        sum = fmaf(dx[i][j], xh[i][j], sum);
       }
     }
+    if (kAhead && m + int(gridDim.x) < M) load(m + gridDim.x);
     const float c = __fdiv_rn(cta_sum(sum, red[flip]), float(K));
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int k = 8 * (threadIdx.x + i * blockDim.x);
       if (k >= K) continue;
-      float xh[8], dx[8], up[8], w[8];
-      gain(i, w);
-      unpack8(here.h[i], xh);
-      unpack8(here.dy[i], dx);
-      unpack8(here.up[i], up);
+      float u[8];
+      unpack8(up[i], u);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        dx[j] = fmaf(fmaf(-(xh[j] * here.rstd), c, dx[j] * w[j]), here.rstd, kRes ? up[j] : 0.f);
+        dx[i][j] = fmaf(fmaf(-xh[i][j], c, dx[i][j]), rstd, kRes ? u[j] : 0.f);
       Raw8<T> o;
-      pack8(dx, o);
+      pack8(dx[i], o);
       store8(dX + size_t(m) * K + k, o);
     }
     if (!kAhead && m + int(gridDim.x) < M) load(m + gridDim.x);
@@ -238,7 +242,7 @@ RowShape forward_shape(const LaunchCtx& c, int M, int K) {
 }
 RowShape backward_shape(int K) {
   const int chunks = ceil_div(K, 8);
-  return row_shape(chunks, chunks > 1024 ? 4 : chunks > 512 ? 2 : 1);
+  return row_shape(chunks, chunks > 1024 ? 4 : chunks > 256 ? 2 : 1);
 }
 
 template <class T, int kIter>

@@ -70,6 +70,32 @@ __device__ __forceinline__ void pack8(const float (&v)[8], Raw8<float>& r) {
                    __float_as_uint(v[7]));
 }
 
+// Sums rounded to the type.  For BF16 the instruction rounds the exact sum once;
+// that is also the FP32 sum rounded to BF16, for the FP32 sum is exact unless one
+// operand is 2^-16 of the other or less, and then both are the larger one.
+__device__ __forceinline__ Raw8<__nv_bfloat16> add8(const Raw8<__nv_bfloat16>& x,
+                                                    const Raw8<__nv_bfloat16>& y) {
+  const uint32_t a[4] = {x.a.x, x.a.y, x.a.z, x.a.w}, b[4] = {y.a.x, y.a.y, y.a.z, y.a.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 s = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b[i]));
+    c[i] = *reinterpret_cast<const uint32_t*>(&s);
+  }
+  return {make_uint4(c[0], c[1], c[2], c[3])};
+}
+__device__ __forceinline__ Raw8<float> add8(const Raw8<float>& x, const Raw8<float>& y) {
+  float a[8], b[8];
+  unpack8(x, a);
+  unpack8(y, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] += b[i];
+  Raw8<float> r;
+  pack8(a, r);
+  return r;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
