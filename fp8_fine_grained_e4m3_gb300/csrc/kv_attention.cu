@@ -795,12 +795,12 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
           ks[1] = __shfl_sync(0xffffffffu, batch.k[1], l);
           vs[1] = __shfl_sync(0xffffffffu, batch.v[1], l);
         }
-        if (!mbar_wait(&bars[warp][stage], phases >> stage & 1, &gave_up, a.wait_ns)) {
+        if (!mbar_wait_within(&bars[warp][stage], phases >> stage & 1, &gave_up, a.wait_ns)) {
           // results are void; what is still in flight lands first, or not at all
           gave_up = 1;
           raise_status(status, FP8GEMM_ERR_TIMEOUT);
           for (int k = 0; k < kStages; ++k)
-            if (in_flight >> k & 1) mbar_wait(&bars[warp][k], phases >> k & 1, &never, a.wait_ns);
+            if (in_flight >> k & 1) mbar_wait_within(&bars[warp][k], phases >> k & 1, &never, a.wait_ns);
           break;
         }
         phases ^= 1u << stage;

@@ -56,7 +56,7 @@ __device__ __forceinline__ Span span(const KvAppendArgs& a, int b, int* status) 
   const int len = a.lens[b];
   bool ok = sequence_tokens(a.cu, b, a.B, a.T, a.max_new, &s.t0, &s.n);
   s.start = len - s.n;
-  ok = ok && (s.n == 0 || (s.start >= 0 && (long long)len <= (long long)a.width * a.block));
+  ok = ok && s.start >= 0 && (long long)len <= (long long)a.width * a.block;
   if (!ok) {
     s.n = 0;
     raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);

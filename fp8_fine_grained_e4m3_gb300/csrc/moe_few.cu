@@ -365,12 +365,12 @@ struct Ring {
   __device__ uint8_t* stage(int s) const { return buf + s * kStageBytes; }
   // Waits for stage s; false if that ran out (or another warp's wait did).
   __device__ bool wait(int s, int* gave_up, int* never, int* status, unsigned long long limit_ns) {
-    if (!mbar_wait(&bar[s], phases >> s & 1, gave_up, limit_ns)) {
+    if (!mbar_wait_within(&bar[s], phases >> s & 1, gave_up, limit_ns)) {
       // results are void; what is still in flight lands first, or not at all
       *reinterpret_cast<volatile int*>(gave_up) = 1;
       raise_status(status, FP8GEMM_ERR_TIMEOUT);
       for (int k = 0; k < kStages; ++k)
-        if (in_flight >> k & 1) mbar_wait(&bar[k], phases >> k & 1, never, limit_ns);
+        if (in_flight >> k & 1) mbar_wait_within(&bar[k], phases >> k & 1, never, limit_ns);
       return false;
     }
     phases ^= 1u << s;

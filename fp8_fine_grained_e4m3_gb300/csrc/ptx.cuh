@@ -75,6 +75,33 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// The wait above for limits of any length: one try of it may sleep for many microseconds,
+// so a limit under 100 us is kept by polling.
+__device__ __forceinline__ bool mbar_wait_within(uint64_t* bar, uint32_t parity,
+                                                 const volatile int* abort_flag,
+                                                 uint64_t limit_ns) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (limit_ns < 100000 ? mbar_test(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // ------------------------------------------------ cp.async (16-byte copies)
 // Copy 16 bytes global -> shared; bytes past `src_bytes` (0 or 16 here) are
 // written as zeros and not read.

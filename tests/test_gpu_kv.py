@@ -288,3 +288,90 @@ def test_graph_replay_with_new_lengths():
         assert torch.equal(O, want)
         for a, x in zip((k, ks, v, vs), mine):
             assert torch.equal(a, x)
+
+
+def test_append_of_ragged_prompts_finds_its_tiles():
+    """Many more places than tiles (one long prompt among short ones): the tiles
+    are found by a running sum, over more than 32 sequences."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    new = [0, 1, 300] + [2, 0, 17] * 14
+    old = [5] * len(new)
+    c = Cache([a + n for a, n in zip(old, new)], 2, 64, 16, "e4m3", seed=40)
+    g = np.random.default_rng(41)
+    cu, T = _offsets(new), sum(new)
+    K, V = (dev(g.standard_normal((T, 2, 64)).astype(np.float32)).to(torch.bfloat16) for _ in range(2))
+    k, ks, v, vs, table, lens = c.on_gpu()
+    b.fp8_kv_append(K, V, k, ks, v, vs, table, lens, cu_new=dev(cu), max_new=300)
+    layer.kv_append(K.float().cpu().numpy(), c.k, c.ks, c.table, c.lens, cu)
+    layer.kv_append(V.float().cpu().numpy(), c.v, c.vs, c.table, c.lens, cu)
+    for got, ref in ((k, c.k), (ks, c.ks), (v, c.v), (vs, c.vs)):
+        assert np.array_equal(host(got), ref)
+    bad = lens.clone()
+    bad[40] = -1
+    b.fp8_kv_append(K, V, k, ks, v, vs, table, bad, cu_new=dev(cu), max_new=300)
+    assert b.fp8gemm_get_device_status() == b.ERR_DEVICE_STATUS
+
+
+def test_append_to_a_cache_with_other_scales():
+    """A block filled by other means may hold any scale: not a power of two, and kept
+    where it is large enough."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    c = Cache([40, 40], 1, 64, 64, "e4m3", seed=42)
+    c.ks[:], c.vs[:] = 0.3, 1e-30
+    g = np.random.default_rng(43)
+    X = dev(g.standard_normal((2, 1, 64)).astype(np.float32)).to(torch.bfloat16)
+    k, ks, v, vs, table, lens = c.on_gpu()
+    b.fp8_kv_append(X, X, k, ks, v, vs, table, lens)
+    for codes, s, got, gs in ((c.k, c.ks, k, ks), (c.v, c.vs, v, vs)):
+        layer.kv_append(X.float().cpu().numpy(), codes, s, c.table, c.lens, [0, 1, 2])
+        assert np.array_equal(host(got), codes) and np.array_equal(host(gs), s)
+
+
+@pytest.mark.parametrize("B,heads,group,q,longest", [
+    (1, 1, 8, 1, 9000), (1, 8, 4, 4, 5000), (3, 2, 1, 1, 3000), (40, 4, 2, 1, 700), (64, 3, 8, 2, 400),
+    (19, 8, 1, 1, 900), (200, 1, 4, 1, 300)])
+def test_attention_shared_among_ctas(B, heads, group, q, longest):
+    """Few items in many parts and many items in runs, sequences of very
+    different lengths among them: against the oracle on sampled rows, and bit
+    for bit on a second call."""
+    import torch
+    g = np.random.default_rng(B)
+    lens = [longest] + [int(x) for x in g.integers(0, longest, B - 1)]
+    dim = 128
+    c = Cache(lens, heads, dim, 32, "e4m3", seed=B + heads).stale()
+    Q = g.standard_normal((B * q, heads * group, dim)).astype(np.float32)
+    got, Qr = _attend(c, Q, None, dim ** -0.5, "e4m3")
+    got2, _ = _attend(c, Q, None, dim ** -0.5, "e4m3")
+    assert np.array_equal(got, got2)
+    pick = sorted(set([0, B - 1] + [int(x) for x in g.integers(0, B, 4)]))
+    table, clens = c.table, c.lens
+    for b_ in pick:
+        c.table, c.lens = table[b_:b_ + 1], clens[b_:b_ + 1]
+        _check(got[b_ * q:(b_ + 1) * q], c, Qr[b_ * q:(b_ + 1) * q], [0, q], dim ** -0.5, "e4m3")
+
+
+@pytest.mark.parametrize("B,length", [(1, 262144), (64, 4096)])
+def test_a_wait_that_runs_out_is_reported(B, length):
+    """A cache four times the L2 and a 1 ns limit: waits for its copies are
+    genuine, the attention gives up and says so; the next call is right."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    heads, dim, block = 8, 128, 64
+    n = B * length // block
+    k, v = (torch.randint(0, 120, (n, heads, block, dim), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((n, heads), 2.0 ** -7, device="cuda") for _ in range(2))
+    table = torch.randperm(n, device="cuda").to(torch.int32).view(B, -1)
+    lens = torch.full((B,), length, dtype=torch.int32, device="cuda")
+    q = torch.randn((B, heads * 2, dim), device="cuda").to(torch.bfloat16)
+    want = b.fp8_kv_attention(q, k, ks, v, vs, table, lens)
+    torch.cuda.synchronize()
+    b.set_wait_limit_ns(1)
+    try:
+        b.fp8_kv_attention(q, k, ks, v, vs, table, lens)
+        assert b.fp8gemm_get_device_status() == b.ERR_TIMEOUT
+    finally:
+        b.set_wait_limit_ns(0)
+    assert torch.equal(b.fp8_kv_attention(q, k, ks, v, vs, table, lens), want)
+    assert b.fp8gemm_get_device_status() == b.OK

@@ -118,3 +118,55 @@ def test_calls_back_to_back_on_two_streams():
         assert torch.equal(D, want[i])
     for s in streams:
         b.fp8gemm_release_workspaces(s)
+
+
+@pytest.mark.parametrize("T,k", [(1, 8), (40, 1)])
+def test_a_wait_that_runs_out_is_reported(T, k):
+    """Weights of more than the L2, few tokens for each of them and a 1 ns limit:
+    waits for their copies are genuine, the layer gives up and says so; the
+    next call is right."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    H, I, E = 7168, 2048, 8
+    W1 = torch.randint(0, 100, (E, 2 * I, H), dtype=torch.uint8, device="cuda")
+    W2 = torch.randint(0, 100, (E, H, I), dtype=torch.uint8, device="cuda")
+    s1, s2 = (torch.full(s, 1e-3, device="cuda") for s in ((E, 2 * I // 128, H // 128), (E, H // 128, I // 128)))
+    A = torch.randint(0, 256, (T, H), dtype=torch.uint8, device="cuda") & 0xF7  # no NaN
+    sA = torch.full((T, H // 128), 1e-2, device="cuda")
+    args = (A, sA, torch.randn((T, E), device="cuda"), W1, s1, W2, s2, k)
+    want = b.fp8_moe_few(*args)[0]
+    torch.cuda.synchronize()
+    b.set_wait_limit_ns(1)
+    try:
+        b.fp8_moe_few(*args)
+        assert b.fp8gemm_get_device_status() == b.ERR_TIMEOUT
+    finally:
+        b.set_wait_limit_ns(0)
+    assert torch.equal(b.fp8_moe_few(*args)[0], want)
+    assert b.fp8gemm_get_device_status() == b.OK
+
+
+@pytest.mark.parametrize("scale", [1e-32, 1e30])
+def test_extreme_hidden_scales(scale):
+    """Hidden activations whose block scale is far from 1: the corrected quotient
+    works on values brought into its range."""
+    ops = _operands(3, 256, 128, 3, seed=9)
+    ops[4] = (ops[4] * np.float32(np.sqrt(scale))).astype(np.float32)
+    ops[6] = (ops[6] / np.float32(scale)).astype(np.float32)
+    _check(ops, 2)
+
+
+def test_more_calls_of_other_sizes_share_a_workspace():
+    """Small and large calls in turn on one stream: the counters a call leaves
+    are zeros wherever the next one's buffers lie."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    sets = [[dev(x) for x in _operands(T, H, I, E, seed=T)] for T, H, I, E in
+            ((1, 128, 128, 2), (64, 512, 256, 8), (7, 1040, 400, 9), (20, 256, 128, 3))]
+    want = []
+    for s in sets:
+        b.fp8gemm_release_workspaces()
+        want.append(b.fp8_moe_few(*s, 2)[0].clone())
+    for _ in range(3):
+        for s, w in zip(sets, want):
+            assert torch.equal(b.fp8_moe_few(*s, 2)[0], w)
