@@ -573,8 +573,7 @@ int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float*
   if (M == 0)  // a sum over no rows
     return finish(cudaMemsetAsync(dG, 0, size_t(K) * 4, stream), 0);
   void* ws = nullptr;
-  if (int r = workspace_for(stream, rmsnorm_backward_workspace_bytes(c, M, K), &ws, kWsNorm))
-    return r;
+  if (int r = workspace_for(stream, rmsnorm_backward_workspace_bytes(c), &ws, kWsNorm)) return r;
   const NormGradArgs a{dY, H, rstd, G, dH, dX, dG, M, K, x_type == FP8GEMM_TYPE_F32};
   return finish(launch_rmsnorm_backward(c, a, ws), 2);
 }
@@ -645,7 +644,7 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
                           fmt, log2_block(block),
                           wait_limit_ns()};
   void* ws = nullptr;
-  if (int r = workspace_for(stream, kv_attention_workspace_bytes(c, a), &ws, kWsAttention)) return r;
+  if (int r = workspace_for(stream, kv_attention_workspace_bytes(c), &ws, kWsAttention)) return r;
   return finish(launch_kv_attention(c, a, ws), 1);
 }
 

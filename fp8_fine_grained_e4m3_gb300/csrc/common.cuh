@@ -137,7 +137,7 @@ struct NormGradArgs {
   int M, K;
   bool f32;
 };
-size_t rmsnorm_backward_workspace_bytes(const LaunchCtx& c, int M, int K);
+size_t rmsnorm_backward_workspace_bytes(const LaunchCtx& c);
 cudaError_t launch_rmsnorm_backward(const LaunchCtx& c, const NormGradArgs& a, void* ws);
 
 // The paged FP8 cache (kv_cache.cu, kv_attention.cu): codes
@@ -174,7 +174,7 @@ struct KvAttentionArgs {
   int log_block;
   unsigned long long wait_ns;  // limit of each wait for a copy
 };
-size_t kv_attention_workspace_bytes(const LaunchCtx& c, const KvAttentionArgs& a);
+size_t kv_attention_workspace_bytes(const LaunchCtx& c);
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws);
 
 // The mixture-of-experts layer for a few tokens (moe_few.cu).

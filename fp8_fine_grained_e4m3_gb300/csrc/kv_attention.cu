@@ -359,16 +359,18 @@ __device__ __forceinline__ void write_out(const KvAttentionArgs& a, int t0, int 
 int row_fragments(const KvAttentionArgs& a) { return (long long)a.max_q * a.group > kRows ? 2 : 1; }
 
 // Warps of a CTA.  With many items each SM has three CTAs of four, whose starts
-// and joins of items overlap.  With no more items than SMs each is shared by several
-// CTAs: one CTA of twelve to an SM, each with a part of one item, leaves a third of
-// the partials and lets an SM's warps end together (one sequence of 131077 tokens,
-// 8 items: 68 us with four warps, 57 with twelve).
+// and joins of items overlap.  Where the SMs are at least twice the items, one CTA of
+// twelve to an SM, each with a part of one item, leaves a third of the partials and
+// lets an SM's warps end together (one sequence of 131077 tokens, 8 items: 68 us
+// with four warps, 57 with twelve; 8 ragged ones of up to 16384, 64 items: 41 and
+// 38).  Nearer to the SMs' number whole parts no longer fit ragged lengths (16 of up
+// to 8192, 128 items: 37 us with four, 43 with twelve).
 long long attention_items(const KvAttentionArgs& a) {
   const int rows = kRows * row_fragments(a);
   return ((long long)a.max_q * a.group + rows - 1) / rows * a.heads * a.B;
 }
 int attention_warps(const LaunchCtx& c, const KvAttentionArgs& a) {
-  return attention_items(a) <= c.num_sms ? 12 : 4;
+  return 2 * attention_items(a) <= c.num_sms ? 12 : 4;
 }
 
 // CTAs: as many as run at once, or fewer where the tables cannot hold that much work.
@@ -385,7 +387,6 @@ int attention_grid(const LaunchCtx& c, const KvAttentionArgs& a) {
 // The counters' place does not depend on the call: what one call leaves there
 // (zeros) is what the next one, of whatever size, finds.
 size_t counter_bytes(const LaunchCtx& c) { return (size_t(kMaxPerSm) * c.num_sms * 4 + 255) / 256 * 256; }
-
 
 // The flattened work of a call: items (sequence, row tile, cached head) in
 // that order, each a run of tiles (behind what it costs).  A sequence with no
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
     int part = max(kMinTiles, int((all + gridDim.x - 1) / gridDim.x));
     int mine;
     long long parts_all;
-    while (true) {
+    while (true) {  // ends: there are no more items than CTAs, and a part may be a whole one
       mine = items > 0 ? items * ceil_div(seq.tiles, part) : 0;
       parts_all = cta_total(mine);
       if (parts_all <= gridDim.x) break;
@@ -907,9 +908,12 @@ cudaError_t launch_shape(const LaunchCtx& c, const KvAttentionArgs& a, const Cac
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(const LaunchCtx& c, const KvAttentionArgs& a) {
-  const int grid = attention_grid(c, a);
-  return counter_bytes(c) + size_t(2) * grid * row_fragments(a) * kRows * (a.dim + 2) * 4;
+// Two partials for each CTA of the widest variant, for every call alike: a
+// stream's buffer stays where it is (a captured graph holds its address).
+size_t kv_attention_workspace_bytes(const LaunchCtx& c) {
+  constexpr size_t kWide = ctas_per_sm(4, 128, 2) * sizeof(Partial<128, 2>);
+  constexpr size_t kNarrow = ctas_per_sm(4, 64, 1) * sizeof(Partial<64, 1>);
+  return counter_bytes(c) + 2 * c.num_sms * (kWide > kNarrow ? kWide : kNarrow);
 }
 
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws) {

@@ -70,7 +70,7 @@ __device__ __forceinline__ Span span(const KvAppendArgs& a, int b, int* status) 
 // heads), keys or values in turn, of the call's tiles: with `slots` places for each
 // sequence where that wastes few (slots > 0), else found by a running sum
 // over the sequences, which a warp takes 32 at a time (prompts of up to 4097
-// tokens, 5 sequences: 22 us with places for the longest, ... by the sum).
+// tokens, 5 sequences: 22 us with places for the longest, 19 by the sum).
 template <int kTpr, bool kE5M2>
 __global__ void __launch_bounds__(32 * kWarps) kv_append_kernel(const KvAppendArgs a, int slots,
                                                                 int log_wpt, int* status) {

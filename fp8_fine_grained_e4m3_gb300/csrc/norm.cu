@@ -8,7 +8,8 @@
 //   with xhat = h rstd  (the quantiser passes the gradient straight through)
 //
 // Both are bound by memory: a row is read once into registers, reduced there
-// and written once.  Sums and statistics are FP32.
+// and written once.  Sums and statistics are FP32.  Measured, BF16 with a residual:
+// 4096 x 7168 forward 36.6 us, 5.6 TB/s; 8192 x 4096 backward 46.3 us, 5.8 TB/s.
 #include "common.cuh"
 #include "f8_convert.cuh"
 #include "ptx.cuh"
@@ -47,6 +48,8 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, const R
 
 // One CTA per row; thread t holds elements 8 (t + i blockDim.x) .. + 7 for i < kIter.
 // A 1x128 block is 16 neighbouring threads.
+// CTAs that stay and take row after row, the next one asked for ahead, were slower
+// (4096 x 7168: 39 us and more): the CTAs' starts already overlap.
 template <class T, int kIter, bool kE5M2, bool kRes>
 __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     const T* __restrict__ X, const T* R, const float* __restrict__ G, float eps, T* H,
@@ -106,7 +109,9 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
 // CTA c takes rows c, c + gridDim.x, ...; thread t owns columns
 // 8 (t + i blockDim.x) .. + 7 of every one of them, so its share of the gain's
 // gradient stays in registers until the CTA leaves it in row c of `part`.  The
-// next row is asked for before this one is used.
+// next row is asked for before this one is used.  CTAs that stay keep the partial
+// gains few (one row of them for each CTA, 2 to 5 MB); one CTA a row would write as
+// many bytes of them as it reads of the row.
 template <class T, int kIter, bool kRes>
 __global__ void __launch_bounds__(512) rmsnorm_backward_kernel(
     const T* dY, const T* __restrict__ H, const float* __restrict__ rstd_in,
@@ -234,7 +239,9 @@ struct RowShape {
 RowShape row_shape(int chunks, int iter) { return {ceil_div(ceil_div(chunks, iter), 32) * 32, iter}; }
 
 // A few rows want the most threads for the least latency; with rows enough for
-// every SM, several chunks a thread keep more rows in flight between their barriers.
+// every SM, several chunks a thread keep more rows in flight between their barriers
+// (K 7168, BF16 with a residual: 1 row 2.1 us with one chunk a thread, 3.4 with four;
+// 303 rows 3.3 and 4.3; 400 rows 5.4 and 5.1; 4096 rows 41.9 and 36.6).
 RowShape forward_shape(const LaunchCtx& c, int M, int K) {
   const int chunks = ceil_div(K, 8);
   if (M < 2 * c.num_sms) return row_shape(chunks, chunks > 1024 ? 2 : 1);
@@ -303,9 +310,10 @@ cudaError_t launch_rmsnorm_quant(const LaunchCtx& c, const NormArgs& a) {
   return a.f32 ? launch_fwd<float>(c, a) : launch_fwd<__nv_bfloat16>(c, a);
 }
 
-size_t rmsnorm_backward_workspace_bytes(const LaunchCtx& c, int M, int K) {
-  return size_t(backward_grid(c, M, backward_shape(K))) * K * 4;
-}
+// A row of K floats for each CTA, at most kMaxNormK floats an SM (a CTA of t
+// threads with i chunks has K <= 8 i t, and an SM has 1024 / t or 512 / t of them):
+// the same for every call, so that a stream's buffer stays where it is.
+size_t rmsnorm_backward_workspace_bytes(const LaunchCtx& c) { return size_t(c.num_sms) * kMaxNormK * 4; }
 
 cudaError_t launch_rmsnorm_backward(const LaunchCtx& c, const NormGradArgs& a, void* ws) {
   float* part = static_cast<float*>(ws);

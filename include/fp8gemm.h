@@ -50,7 +50,8 @@
  *    M > 64 without Q/sA keeps its quantised A in a second per-stream buffer,
  *    and fp8gemm_dense_batch and the ordered contiguous form their tile
  *    counters (and order) in small per-stream buffers; fp8_rmsnorm_backward
- *    and fp8_moe_few keep theirs the same way.
+ *    (10 MB), fp8_kv_attention (8 MB) and fp8_moe_few (60 MB + 1 KB for each
+ *    element of I) keep theirs the same way.
  *    Such a first call must therefore not happen during CUDA graph capture.
  *    Calls on different streams never share a workspace.  The reduction
  *    order is fixed, so results are deterministic.  A caller that retires a
@@ -486,8 +487,8 @@ int fp8_rmsnorm_quant(const void* X, const void* R, int x_type, const float* G, 
  *   rstd f32 [M] as the forward call left it; G, dG f32 [K] (dG is written in
  *   full, zeros for M = 0).
  *   Sizes and alignment as fp8_rmsnorm_quant.  Partial sums of dG live in a
- *   per-(device, stream) workspace (at most 12 K floats for each SM); their
- *   order is fixed, so dG is deterministic.
+ *   per-(device, stream) workspace (64 KB for each SM); their order is fixed, so
+ *   dG is deterministic.
  */
 int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float* rstd,
                          const float* G, const void* dH, void* dX, float* dG, int M, int K,
@@ -551,7 +552,10 @@ int fp8_kv_append(const void* K, const void* V, int64_t ld_k, int64_t ld_v, uint
  * (causal; its own key is in the cache by then).  A query that sees none gives
  * zeros.  Bytes of the cache at and past seq_len are never used.  Made for
  * serving: one to a few new tokens per sequence over a long cache (more are
- * taken 8 rows of n * group at a time).
+ * taken 16 rows of n * group at a time, each reading the cache anew).  Work is
+ * shared out evenly over the SMs whatever the lengths; partial results and
+ * their counters live in a per-(device, stream) workspace of one size for all
+ * calls.  Results are deterministic for given host sizes and lengths.
  *
  *   Q  bf16 [T, heads * group, dim], ld_q elements from token to token (a
  *      multiple of 8, at least heads * group * dim)
@@ -582,9 +586,12 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  *   W2 u8 e4m3 [E, H, I], s2 f32 [E, ceil(H/128), ceil(I/128)]
  *   D  bf16 [T, H], ids i32 [T, top_k], weights f32 [T, top_k] (outputs)
  *   T <= 64, top_k <= 16, top_k <= E <= 512, H and I positive multiples of 16.
+ *   E * 2 I, E * H and T * top_k * ceil(I/128) * ceil(H/128) below 2^31.
  *   Alignment: 16 bytes (logits, ids and weights 4).
  *
- * Routing and hidden activations live in a per-(device, stream) workspace.
+ * Routing, hidden activations and partial sums live in a per-(device, stream)
+ * workspace whose size depends on I alone: make the call with the largest I on
+ * a stream before capturing one there (a graph keeps the workspace's address).
  * Results are deterministic.  More tokens: fp8gemm_grouped_contiguous.
  */
 int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,
@@ -619,8 +626,8 @@ uint64_t fp8gemm_num_kernel_launches(void);
  * `stream` on the current device (the split-K buffer of the decode path, the
  * quantised-activation buffer of fp8gemm_dense_quant_a, the problem table's
  * partials, the tile counters and order of fp8gemm_dense_batch and of the
- * ordered contiguous form, and those of the norm's gradient and of the
- * few-token MoE layer).  It first
+ * ordered contiguous form, and those of the norm's gradient, the cache
+ * attention and the few-token MoE layer).  It first
  * synchronises `stream`, since work enqueued there may still use them; the
  * next call that needs a workspace on that stream allocates it again.  Call
  * it before cudaStreamDestroy for streams that are retired: a stream handle
@@ -638,7 +645,7 @@ uint64_t fp8gemm_workspace_bytes(void);
 
 /*
  * fp8gemm_set_wait_limit_ns -- time limit, in nanoseconds of the GPU's global
- * timer, of every pipeline wait inside the GEMM kernels launched after this
+ * timer, of every pipeline wait inside the kernels launched after this
  * call (process-wide; 0 restores the default of 2 s).  A wait that exceeds
  * it is treated as a deadlock: the CTA stops, lets its copies and tensor-core
  * operations in flight finish, frees its TMEM, exits, and the status word
