@@ -702,13 +702,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
 template <int NT>
 constexpr bool kJoinHere = NT == 1;
 
+// Stages of a warp's ring of 4 KB tiles: beside the tokens' sums two leave room for
+// three CTAs (16 tokens through 4 of 32 experts, H 7168, I 2048: a call takes 223 us
+// with two, 231 with four).
+template <int NT>
+constexpr int kDownStages = NT == 2 ? 2 : 4;
+
 // Down product and weighted sum.  Unit: one K block of one pass for a tile of
 // 128 output columns; warp w takes columns 32 w .. + 31 and keeps a sum per token
 // in shared memory that no other warp touches.
 //   partial: [warp][token][32] floats
 constexpr int kSumRow = 36;  // floats from token to token: lanes of a fragment hit all banks
 
-template <int NT, int kDownStages>
+template <int NT>
 __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const MoeArgs a, const Route given,
                                                                const __grid_constant__ CUtensorMap map,
                                                                const uint8_t* H8, const float* sH,
@@ -718,12 +724,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
   __shared__ Shared sh;
   __shared__ std::conditional_t<kOwnRoute<NT>, OwnRoute, int> mine;
   uint8_t* rings = init_shared(sh, raw, &map);
-  float* all_sums = reinterpret_cast<float*>(rings + kWarps * kDownStages * 32 * kBlockK);
+  float* all_sums = reinterpret_cast<float*>(rings + kWarps * kDownStages<NT> * 32 * kBlockK);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int Kb = ceil_div(a.I, kBlockK), Hb = ceil_div(a.H, kBlockK);
   float* sums = all_sums + warp * a.T * kSumRow;
   for (int i = lane; i < a.T * kSumRow; i += 32) sums[i] = 0.f;
-  Ring<kDownStages, 32 * kBlockK> ring{rings + warp * kDownStages * 32 * kBlockK, sh.bars[warp]};
+  Ring<kDownStages<NT>, 32 * kBlockK> ring{rings + warp * kDownStages<NT> * 32 * kBlockK, sh.bars[warp]};
   // The up kernel let this one start after everything before it was complete:
   // logits, routing and weights may be read, the hidden activations not yet.
   Route r = given;
@@ -754,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
       mbar_arrive_expect_tx(&ring.bar[ask_stage], 32 * kBlockK);
       tma_load_2d(ring.stage(ask_stage), &map, &ring.bar[ask_stage], ask_kb * kBlockK, ask_row);
     }
-    ask_stage = (ask_stage + 1) % kDownStages;
+    ask_stage = (ask_stage + 1) % kDownStages<NT>;
     if (++ask_kb == Kb && ask_left > 0) {
       ask_kb = 0;
       if (++ask_pi == passes) {
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
     }
   };
 #pragma unroll
-  for (int i = 0; i < kDownStages; ++i) fetch();
+  for (int i = 0; i < kDownStages<NT>; ++i) fetch();
   // With the sum in a launch of its own, that may come early.  The next call's
   // routing may not: it takes a whole SM's registers, which this kernel's CTAs would
   // go without (64 tokens: 300 us a call with it, 261 without).
@@ -834,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
     }
     __syncwarp();  // the stage has been read
     if (!dead) fetch();
-    stage = (stage + 1) % kDownStages;
+    stage = (stage + 1) % kDownStages<NT>;
     ++kb;
     --left;
     if (kb < Kb && left > 0) continue;
@@ -932,10 +938,12 @@ __global__ void __launch_bounds__(128) moe_sum_kernel(const MoeArgs a, const int
 
 // ------------------------------------------------------------------- launches
 // Fragments of 8 tokens that a pass takes.  Two keep three CTAs on an SM; four
-// save passes over the weights where an expert has more than 16 tokens as a rule
-// (64 tokens through 4 of 32 experts, 8 each: 278 us with two, 344 with four).
+// save passes over the weights where an expert has more than 32 tokens as a rule
+// (64 tokens, H 7168, I 2048: through 8 of 32 experts, 16 tokens each, 313 us with
+// two, 351 with four; 4 of 8, 32 each, 154 and 161; 8 of 8, 64 each, 239 and 223).
+constexpr int kMaxFragments = 4;
 int fragments(const MoeArgs& a) {
-  return a.T <= 8 ? 1 : a.T <= 16 || a.T * a.k <= 12 * a.E ? 2 : 4;
+  return a.T <= 8 ? 1 : a.T * a.k <= 32 * a.E ? 2 : 4;
 }
 
 // Shared memory of an SM, and the most a CTA may ask for.
@@ -944,14 +952,15 @@ constexpr size_t kSmemPerSm = 228 * 1024, kMaxSmem = 200 * 1024;
 int per_sm(int most, size_t dynamic, size_t fixed) {
   return max(1, min(most, int(kSmemPerSm / (dynamic + fixed + 1024))));
 }
-constexpr int kManyStages = 2;
 
 struct Layout {
   size_t counters, h8, sh, weight, list, pass, passes, up, down, total;
 };
 
+// Places for the most tokens and choices: only I changes them, so that a stream's
+// buffer stays where it is (a captured graph holds its address).
 Layout layout(const LaunchCtx& c, const MoeArgs& a) {
-  const size_t P = size_t(a.T) * a.k, grid = size_t(kMaxPerSm) * c.num_sms;
+  const size_t P = size_t(kMoeMaxTokens) * kMoeMaxTopK, grid = size_t(kMaxPerSm) * c.num_sms;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -959,20 +968,20 @@ Layout layout(const LaunchCtx& c, const MoeArgs& a) {
     return here;
   };
   Layout l;
-  l.counters = take(2 * grid * 4);  // first: its place does not depend on the call's sizes
+  l.counters = take(2 * grid * 4);  // first: zeros that one call leaves are what the next one finds
   l.h8 = take(P * a.I);
   l.sh = take(P * ceil_div(a.I, kBlockK) * 4);
   l.weight = take(P * 4);
   l.list = take(P * 4);
   l.pass = take(P * 4);
   l.passes = take(4);
-  l.up = take(2 * grid * kWarps * 4 * fragments(a) * 4 * 32 * 4);
-  l.down = take(2 * grid * kWarps * a.T * 32 * 4);
+  l.up = take(2 * grid * kWarps * 4 * kMaxFragments * 4 * 32 * 4);
+  l.down = take(2 * grid * kWarps * kMoeMaxTokens * 32 * 4);
   l.total = at;
   return l;
 }
 
-template <int NT, int kDownStages>
+template <int NT>
 cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char* ws,
                       const Layout& l) {
   CUtensorMap m1, m2;
@@ -984,12 +993,12 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   int* counters = reinterpret_cast<int*>(ws + l.counters);
   const size_t pairs = kOwnRoute<NT> ? 0 : size_t(a.T) * a.k;
   const size_t up_smem = 1024 + size_t(kWarps) * kUpStages<NT> * 64 * kBlockK + 8 * pairs;
-  const size_t down_smem = 1024 + size_t(kWarps) * kDownStages * 32 * kBlockK +
+  const size_t down_smem = 1024 + size_t(kWarps) * kDownStages<NT> * 32 * kBlockK +
                            size_t(kWarps) * a.T * kSumRow * 4 + 12 * pairs;
   const int up_per_sm = per_sm(kPerSm<NT>, up_smem, 3 * 1024);
   const int down_per_sm = per_sm(kPerSm<NT>, down_smem, 2 * 1024);
   auto up = moe_up_kernel<NT>;
-  auto down = moe_down_kernel<NT, kDownStages>;
+  auto down = moe_down_kernel<NT>;
   static SmemLimit up_limit, down_limit;
   if (cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(up), kMaxSmem)) return e;
   if (cudaError_t e = down_limit.raise(reinterpret_cast<const void*>(down), kMaxSmem)) return e;
@@ -1021,9 +1030,9 @@ cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace
                 reinterpret_cast<uint32_t*>(ws + l.pass), reinterpret_cast<int*>(ws + l.passes)};
   *launches = a.T <= kOwnTokens ? 2 : 4;
   switch (fragments(a)) {
-    case 1: return launch_nt<1, 4>(c, a, r, ws, l);
-    case 2: return a.T <= 16 ? launch_nt<2, 4>(c, a, r, ws, l) : launch_nt<2, kManyStages>(c, a, r, ws, l);
-    default: return launch_nt<4, 4>(c, a, r, ws, l);
+    case 1: return launch_nt<1>(c, a, r, ws, l);
+    case 2: return launch_nt<2>(c, a, r, ws, l);
+    default: return launch_nt<4>(c, a, r, ws, l);
   }
 }
 
