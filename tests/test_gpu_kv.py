@@ -375,3 +375,23 @@ def test_a_wait_that_runs_out_is_reported(B, length):
         b.set_wait_limit_ns(0)
     assert torch.equal(b.fp8_kv_attention(q, k, ks, v, vs, table, lens), want)
     assert b.fp8gemm_get_device_status() == b.OK
+
+
+@pytest.mark.parametrize("counts,group,heads,dim,block,fmt", [
+    ([1], 17, 1, 128, 64, "e4m3"), ([4, 1, 2, 3], 8, 2, 128, 16, "e4m3"), ([11, 0, 1], 3, 5, 64, 32, "e5m2"),
+    ([8] * 24, 5, 8, 128, 16, "e4m3"), ([5, 1, 3] * 20, 4, 8, 64, 128, "e4m3"), ([65, 2], 1, 2, 128, 32, "e5m2")])
+def test_attention_of_more_rows_than_a_warp_takes(counts, group, heads, dim, block, fmt):
+    """More than 16 rows for a cached head, up to many times that, next to
+    sequences with few or none; few items and many."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    g = np.random.default_rng(len(counts) + group)
+    lens = [n + int(x) for n, x in zip(counts, g.integers(0, 900, len(counts)))]
+    lens[0] = 1237
+    c = Cache(lens, heads, dim, block, fmt, seed=group).stale()
+    cu = _offsets(counts)
+    Q = (2 * g.standard_normal((sum(counts), heads * group, dim))).astype(np.float32)
+    got, Qr = _attend(c, Q, cu, dim ** -0.5, fmt, max_q=max(counts))
+    _check(got, c, Qr, cu, dim ** -0.5, fmt)
+    assert np.array_equal(got, _attend(c, Q, cu, dim ** -0.5, fmt, max_q=max(counts))[0])
+    assert b.fp8gemm_get_device_status() == b.OK
