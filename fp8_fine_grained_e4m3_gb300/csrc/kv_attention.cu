@@ -113,8 +113,27 @@ struct Queries {
   float mul[2];
 };
 
+// A lane's share of one row's query, as it lies; zeros without a row.
 template <int kDim>
-__device__ __forceinline__ void load_queries(Queries<kDim>& q, const __nv_bfloat16* row,
+struct RawQuery {
+  Raw8<__nv_bfloat16> r[kDim / 64][2];
+};
+
+template <int kDim>
+__device__ __forceinline__ RawQuery<kDim> load_query(const __nv_bfloat16* row, int t) {
+  RawQuery<kDim> q;
+#pragma unroll
+  for (int c = 0; c < kDim / 64; ++c)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      zero8(q.r[c][e]);
+      if (row) q.r[c][e] = load8(row + (kDim / 4) * t + 16 * c + 8 * e);
+    }
+  return q;
+}
+
+template <int kDim>
+__device__ __forceinline__ void take_queries(Queries<kDim>& q, const RawQuery<kDim>& raw,
                                              float scale_log2, int t) {
   float x[kDim / 64][16];
   float top = 0.f;
@@ -122,11 +141,8 @@ __device__ __forceinline__ void load_queries(Queries<kDim>& q, const __nv_bfloat
   for (int c = 0; c < kDim / 64; ++c)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      Raw8<__nv_bfloat16> r;
-      zero8(r);
-      if (row) r = load8(row + (kDim / 4) * t + 16 * c + 8 * e);
       float f[8];
-      unpack8(r, f);
+      unpack8(raw.r[c][e], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[c][8 * e + i] = f[i];
@@ -757,21 +773,26 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
     };
     float unit = 0.f;
     look_up(batch, lane);
+    // Queries and scales are asked for before the tiles: behind the first tiles of all
+    // warps (29 MB) they would come microseconds late.
+    RawQuery<kDim> raw_q[kNR];
+#pragma unroll
+    for (int i = 0; i < kNR; ++i) {
+      const int row = row0 + kRows * i + g;  // whose query this lane loads
+      raw_q[i] = load_query<kDim>(row < rows ? a.Q + (q_seq.t0 + row / a.group) * a.ld_q +
+                                                   (head * a.group + row % a.group) * kDim
+                                             : nullptr, t);
+    }
+    look_up_scales(batch);
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(i, batch, i);
-    look_up_scales(batch);
     look_up(after, 32 + lane);
     Queries<kDim> q[kNR];
     State<kDim> s[kNR];
     int limit[kNR][2];  // tokens that the lane's rows see
 #pragma unroll
     for (int i = 0; i < kNR; ++i) {
-      const int row = row0 + kRows * i + g;  // whose query this lane loads
-      const __nv_bfloat16* p =
-          row < rows ? a.Q + (q_seq.t0 + row / a.group) * a.ld_q +
-                           (head * a.group + row % a.group) * kDim
-                     : nullptr;
-      load_queries<kDim>(q[i], p, a.scale * 1.44269504088896341f, t);
+      take_queries<kDim>(q[i], raw_q[i], a.scale * 1.44269504088896341f, t);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int rr = row0 + kRows * i + 2 * t + r;
