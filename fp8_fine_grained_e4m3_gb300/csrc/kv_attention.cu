@@ -21,6 +21,9 @@
 // FP16's range (BF16 has fewer mantissa bits); p is rounded to FP16 (11
 // bits, far below the BF16 output's step).  Scores, statistics, sums and the
 // output accumulate in FP32; a tile's scales are applied to its FP32 products.
+// Measured: 64 ragged sequences of up to 8192 tokens, 8 heads of 128 (584 MB) 101 us, 5.8
+// TB/s; one of 131077 with 16 rows a head (268 MB) 55 us, 4.9 TB/s, of which the start
+// takes 5 and the join of the CTAs' results 6.
 #include "common.cuh"
 #include "f8_convert.cuh"
 #include "kv_cache.cuh"
@@ -39,9 +42,9 @@ constexpr int kRows = 8;   // query rows per fragment
 constexpr int kMinTiles = 8;
 // What beginning and joining an item costs, in tiles (about 4 us, in which the
 // warps of a CTA would do three each).  It counts in a CTA's share as if the item
-// began with that many tiles more: 64 ragged sequences took 108 us with equal
+// began with that many tiles more: 64 ragged sequences took 120 us with equal
 // shares of the tiles alone, for which the CTAs with many short items were late, and
-// 99 us with it.
+// 101 us with it.
 constexpr int kItemCost = 12;
 constexpr int kStages = 2;  // tiles of a warp in shared memory
 constexpr float kNone = -1e30f;  // the maximum of nothing: below any score
@@ -371,16 +374,19 @@ __device__ __forceinline__ void write_out(const KvAttentionArgs& a, int t0, int 
 }
 
 // Row fragments that a CTA takes at a time: two (16 rows) read the cache half
-// as often where a sequence may have more than 8 rows per cached head.
+// as often where a sequence may have more than 8 rows per cached head (131077 tokens, 16
+// rows: 66 us with one, 55 with two); for up to 8 the second would be idle work (64
+// sequences, 8 rows: 101 us with one, 112 with two).  More rows take further passes:
+// the products bound those already (64 of up to 8192 tokens: 101 us for 8 rows, 206 for 32).
 int row_fragments(const KvAttentionArgs& a) { return (long long)a.max_q * a.group > kRows ? 2 : 1; }
 
 // Warps of a CTA.  With many items each SM has three CTAs of four, whose starts
 // and joins of items overlap.  Where the SMs are at least twice the items, one CTA of
 // twelve to an SM, each with a part of one item, leaves a third of the partials and
-// lets an SM's warps end together (one sequence of 131077 tokens, 8 items: 68 us
-// with four warps, 57 with twelve; 8 ragged ones of up to 16384, 64 items: 41 and
-// 38).  Nearer to the SMs' number whole parts no longer fit ragged lengths (16 of up
-// to 8192, 128 items: 37 us with four, 43 with twelve).
+// lets an SM's warps end together (one sequence of 131077 tokens, 8 items: 70 us
+// with four warps, 55 with twelve; 8 ragged ones of up to 16384, 64 items: 39 and
+// 37).  Nearer to the SMs' number whole parts no longer fit ragged lengths (16 of up
+// to 8192, 128 items: 35 us with four, 42 with twelve).
 long long attention_items(const KvAttentionArgs& a) {
   const int rows = kRows * row_fragments(a);
   return ((long long)a.max_q * a.group + rows - 1) / rows * a.heads * a.B;

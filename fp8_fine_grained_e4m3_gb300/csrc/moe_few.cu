@@ -25,6 +25,9 @@
 // lane's share of a row's K block is 32 neighbouring bytes.  A tile that lies in
 // several runs is joined from FP32 partials, in CTA order, by the CTA that
 // finishes last: results do not depend on timing.
+//
+// Measured, H 7168, I 2048, 4 of 32 experts: one token (176 MB) 39.5 us, 4.5 TB/s, of
+// which the two kernels' starts and joins take 12; 64 tokens (1.41 GB) 237 us, 5.9 TB/s.
 #include <type_traits>
 
 #include "common.cuh"
@@ -792,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
   for (int i = 0; i < kDownStages<NT>; ++i) fetch();
   // With the sum in a launch of its own, that may come early.  The next call's
   // routing may not: it takes a whole SM's registers, which this kernel's CTAs would
-  // go without (64 tokens: 300 us a call with it, 261 without).
+  // go without (64 tokens: that cost a call 39 us).
   if constexpr (!kJoinHere<NT>) griddep_launch_dependents();
   griddep_wait();
 
