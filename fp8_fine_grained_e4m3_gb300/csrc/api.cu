@@ -95,14 +95,11 @@ unsigned long long current_context_id() {
   return id;
 }
 
-cudaError_t SmemLimit::raise(const void* fn, size_t bytes) {
-  int dev = 0;
-  if (cudaError_t e = cudaGetDevice(&dev)) return e;
-  const unsigned long long ctx = current_context_id();
-  if (ctx != 0 && set_in[dev & 63] == ctx) return cudaSuccess;
+cudaError_t SmemLimit::raise(const LaunchCtx& c, const void* fn, size_t bytes) {
+  if (c.ctx != 0 && set_in[c.dev & 63] == c.ctx) return cudaSuccess;
   if (cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)))
     return e;
-  set_in[dev & 63] = ctx;
+  set_in[c.dev & 63] = c.ctx;
   return cudaSuccess;
 }
 
@@ -110,9 +107,10 @@ namespace {
 
 // Looks up (once per device and context) the SM count, compute capability
 // and the device address of the status word.
-int device_info(DeviceInfo* out) {
+int device_info(DeviceInfo* out, int* device = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8GEMM_ERR_LAUNCH;
+  if (device) *device = dev;
   unsigned long long ctx = current_context_id();
   if (ctx == 0) {  // no context yet on this thread: the runtime creates it
     if (cudaFree(nullptr) != cudaSuccess) return FP8GEMM_ERR_LAUNCH;
@@ -173,11 +171,9 @@ int finish(cudaError_t e, int nlaunch) {
 enum { kWsSplitK = 0, kWsQuantA = 1, kWsTable = 2, kWsBatch = 3, kWsContig = 4, kWsNorm = 5,
        kWsMoe = 6, kWsAttention = 7 };
 
-int workspace_for(cudaStream_t s, size_t bytes, void** out, int slot = kWsSplitK) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FP8GEMM_ERR_LAUNCH;
-  DeviceInfo d;  // drops the workspaces of an ended context first
-  if (int r = device_info(&d)) return r;
+// The buffer on device `dev` in the context `ctx`, both of device_info, which drops
+// the workspaces of an ended context.
+int workspace_on(int dev, unsigned long long ctx, cudaStream_t s, size_t bytes, void** out, int slot) {
   std::lock_guard<std::mutex> lk(g_mu);
   auto key = std::make_tuple(dev, s, slot);
   auto it = g_workspaces.find(key);
@@ -198,9 +194,16 @@ int workspace_for(cudaStream_t s, size_t bytes, void** out, int slot = kWsSplitK
     cudaFree(p);
     return FP8GEMM_ERR_LAUNCH;
   }
-  g_workspaces[key] = Workspace{p, bytes, d.ctx};
+  g_workspaces[key] = Workspace{p, bytes, ctx};
   *out = p;
   return FP8GEMM_OK;
+}
+
+int workspace_for(cudaStream_t s, size_t bytes, void** out, int slot = kWsSplitK) {
+  int dev = 0;
+  DeviceInfo d;
+  if (int r = device_info(&d, &dev)) return r;
+  return workspace_on(dev, d.ctx, s, bytes, out, slot);
 }
 
 constexpr int kSmallM = 64;  // dense calls with M <= this use the swap-AB stream-K kernel
@@ -278,11 +281,12 @@ int check_common(int M, int N, int K) {
 
 int ctx_for(cudaStream_t stream, LaunchCtx* c) {
   DeviceInfo d;
-  const int r = device_info(&d);
+  const int r = device_info(&d, &c->dev);
   if (r != FP8GEMM_OK) return r;
   c->stream = stream;
   c->num_sms = d.num_sms;
   c->status = d.status;
+  c->ctx = d.ctx;
   return FP8GEMM_OK;
 }
 
@@ -573,7 +577,7 @@ int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float*
   if (M == 0)  // a sum over no rows
     return finish(cudaMemsetAsync(dG, 0, size_t(K) * 4, stream), 0);
   void* ws = nullptr;
-  if (int r = workspace_for(stream, rmsnorm_backward_workspace_bytes(c), &ws, kWsNorm)) return r;
+  if (int r = workspace_on(c.dev, c.ctx, stream, rmsnorm_backward_workspace_bytes(c), &ws, kWsNorm)) return r;
   const NormGradArgs a{dY, H, rstd, G, dH, dX, dG, M, K, x_type == FP8GEMM_TYPE_F32};
   return finish(launch_rmsnorm_backward(c, a, ws), 2);
 }
@@ -644,7 +648,8 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
                           fmt, log2_block(block),
                           wait_limit_ns()};
   void* ws = nullptr;
-  if (int r = workspace_for(stream, kv_attention_workspace_bytes(c), &ws, kWsAttention)) return r;
+  if (int r = workspace_on(c.dev, c.ctx, stream, kv_attention_workspace_bytes(c), &ws, kWsAttention))
+    return r;
   return finish(launch_kv_attention(c, a, ws), 1);
 }
 
@@ -672,7 +677,8 @@ int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const ui
   const MoeArgs a{A, sA, logits, W1, s1, W2, s2, static_cast<__nv_bfloat16*>(D), ids, weights,
                   T, H, I, E, top_k, renormalise, wait_limit_ns()};
   void* ws = nullptr;
-  if (int r = workspace_for(stream, moe_few_workspace_bytes(c, a), &ws, kWsMoe)) return r;
+  if (int r = workspace_on(c.dev, c.ctx, stream, moe_few_workspace_bytes(c, a), &ws, kWsMoe))
+    return r;
   int launches = 0;
   const cudaError_t e = launch_moe_few(c, a, ws, &launches);
   return finish(e, launches);

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/fp8gemm.h"
 
 namespace fp8gemm {
@@ -30,6 +32,8 @@ struct LaunchCtx {
   cudaStream_t stream;
   int num_sms;
   int* status;  // device address of the status word
+  int dev;      // the current device and its context's id, when the call began
+  unsigned long long ctx;
 };
 
 // The quantisers; sat (device, may be null) receives the saturation count.
@@ -198,8 +202,8 @@ cudaError_t launch_moe_few(const LaunchCtx& c, const MoeArgs& a, void* workspace
 // Raises a kernel's dynamic shared memory limit, once per device and CUDA context
 // (the attribute belongs to the function in one context).
 struct SmemLimit {
-  unsigned long long set_in[64] = {};  // context id, per device
-  cudaError_t raise(const void* fn, size_t bytes);
+  std::atomic<unsigned long long> set_in[64] = {};  // context id, per device
+  cudaError_t raise(const LaunchCtx& c, const void* fn, size_t bytes);
 };
 
 // Launches a kernel as a programmatic dependent of the one before it on the

@@ -921,7 +921,7 @@ cudaError_t launch(const LaunchCtx& c, const KvAttentionArgs& a, const CacheMaps
   constexpr size_t kSmem = 1024 + (kRings > kMore ? kRings : kMore);
   auto fn = kv_attention_kernel<kDim, kE5M2, kNR, kWarps>;
   static SmemLimit limit;
-  if (cudaError_t e = limit.raise(reinterpret_cast<const void*>(fn), kSmem)) return e;
+  if (cudaError_t e = limit.raise(c, reinterpret_cast<const void*>(fn), kSmem)) return e;
   return launch_dependent(c, fn, grid, 32 * kWarps, kSmem, a, maps, counters, parts, c.status);
 }
 

@@ -1021,8 +1021,8 @@ cudaError_t launch_nt(const LaunchCtx& c, const MoeArgs& a, const Route& r, char
   auto up = moe_up_kernel<NT>;
   auto down = moe_down_kernel<NT>;
   static SmemLimit up_limit, down_limit;
-  if (cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(up), kMaxSmem)) return e;
-  if (cudaError_t e = down_limit.raise(reinterpret_cast<const void*>(down), kMaxSmem)) return e;
+  if (cudaError_t e = up_limit.raise(c, reinterpret_cast<const void*>(up), kMaxSmem)) return e;
+  if (cudaError_t e = down_limit.raise(c, reinterpret_cast<const void*>(down), kMaxSmem)) return e;
   if constexpr (!kOwnRoute<NT>)
     if (cudaError_t e = launch_dependent(c, moe_route_kernel, 1, 1024, 0, a.logits, r, a.ids,
                                          a.weights, a.T, a.E, a.k, a.renormalise, 8 * NT))
