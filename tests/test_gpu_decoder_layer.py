@@ -119,3 +119,58 @@ def test_training_step_against_autograd():
     assert float((out.float() - y).norm() / y.norm()) < 0.06
     assert float((dx.float() - h.grad).norm() / h.grad.norm()) < 0.08
     assert float((dgain - gg.grad).norm() / gg.grad.norm()) < 0.08
+
+
+def test_a_captured_graph_outlives_larger_calls():
+    """Calls captured on a stream, then larger ones made there, which need more
+    of the same workspaces: replays of the graph still equal the direct calls, and the
+    workspaces have not grown."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+
+    def bf16(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    def codes(*shape):
+        return torch.randint(0, 112, shape, generator=g, dtype=torch.uint8, device="cuda")
+
+    def norm(M, K):
+        dy, h, rstd, gain = bf16(M, K), bf16(M, K), torch.ones(M, device="cuda"), torch.ones(K, device="cuda")
+        return lambda: b.fp8_rmsnorm_backward(dy, h, rstd, gain)
+
+    def attend(B, group, tokens):
+        k, v = codes(B * tokens // 64, 2, 64, 128), codes(B * tokens // 64, 2, 64, 128)
+        s = torch.full(k.shape[:2], 2.0 ** -7, device="cuda")
+        table = torch.arange(k.shape[0], dtype=torch.int32, device="cuda").view(B, -1)
+        lens, q = torch.full((B,), tokens - 5, dtype=torch.int32, device="cuda"), bf16(B, 2 * group, 128)
+        return lambda: (b.fp8_kv_attention(q, k, s, v, s, table, lens),)
+
+    def moe(T, E, k, H=512, I=256):
+        A, W1, W2 = codes(T, H), codes(E, 2 * I, H), codes(E, H, I)
+        one = [torch.full(n, 2.0 ** -6, device="cuda") for n in ((T, H // 128), (E, 2 * I // 128, H // 128),
+                                                                (E, H // 128, I // 128))]
+        logits = torch.randn((T, E), generator=g, device="cuda")
+        return lambda: b.fp8_moe_few(A, one[0], logits, W1, one[1], W2, one[2], k)
+
+    s = torch.cuda.Stream()
+    for small, large in ((norm(3, 64), norm(700, 16384)), (attend(1, 1, 1024), attend(40, 16, 4096)),
+                         (moe(1, 4, 2), moe(64, 32, 16))):
+        want = small()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            small()
+            s.synchronize()
+            held = b.workspace_bytes()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                got = small()
+            large()
+            s.synchronize()
+            assert b.workspace_bytes() == held
+            graph.replay()
+            s.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert b.fp8gemm_get_device_status() == b.OK
+    b.fp8gemm_release_workspaces(s)
