@@ -40,12 +40,13 @@ constexpr int kRows = 8;   // query rows per fragment
 // Work is shared out in tiles.  A CTA's least share is 256 tokens: fewer would
 // cost more to join than to do.
 constexpr int kMinTiles = 8;
-// What beginning and joining an item costs, in tiles (about 4 us, in which the
-// warps of a CTA would do three each).  It counts in a CTA's share as if the item
+// What beginning and joining an item costs, in tiles (about 5 us, in which the
+// warps of a CTA would do four each).  It counts in a CTA's share as if the item
 // began with that many tiles more: 64 ragged sequences took 120 us with equal
 // shares of the tiles alone, for which the CTAs with many short items were late, and
-// 101 us with it.
-constexpr int kItemCost = 12;
+// 100 us with it (16 ragged ones: 35.5 us with 12 for it, 34.6 with 16, 33.9 with 20; the 64:
+// 99.7, 100.0, 100.3).
+constexpr int kItemCost = 16;
 constexpr int kStages = 2;  // tiles of a warp in shared memory
 constexpr float kNone = -1e30f;  // the maximum of nothing: below any score
 constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
