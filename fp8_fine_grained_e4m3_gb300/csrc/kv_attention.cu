@@ -824,7 +824,9 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
           ks[1] = __shfl_sync(0xffffffffu, batch.k[1], l);
           vs[1] = __shfl_sync(0xffffffffu, batch.v[1], l);
         }
-        if (!mbar_wait_within(&bars[warp][stage], phases >> stage & 1, &gave_up, a.wait_ns)) {
+        // one outcome for the warp: what follows is warp-wide
+        if (!__all_sync(0xffffffffu, mbar_wait_within(&bars[warp][stage], phases >> stage & 1,
+                                                      &gave_up, a.wait_ns))) {
           // results are void; what is still in flight lands first, or not at all
           gave_up = 1;
           raise_status(status, FP8GEMM_ERR_TIMEOUT);

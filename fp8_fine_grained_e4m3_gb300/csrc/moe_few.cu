@@ -384,9 +384,10 @@ struct Ring {
   uint32_t phases = 0, in_flight = 0;  // bit s: parity to wait for; asked for
 
   __device__ uint8_t* stage(int s) const { return buf + s * kStageBytes; }
-  // Waits for stage s; false if that ran out (or another warp's wait did).
+  // Waits for stage s; false, for the whole warp, if that ran out for any of its
+  // lanes (or another warp's wait did).
   __device__ bool wait(int s, int* gave_up, int* never, int* status, unsigned long long limit_ns) {
-    if (!mbar_wait_within(&bar[s], phases >> s & 1, gave_up, limit_ns)) {
+    if (!__all_sync(0xffffffffu, mbar_wait_within(&bar[s], phases >> s & 1, gave_up, limit_ns))) {
       // results are void; what is still in flight lands first, or not at all
       *reinterpret_cast<volatile int*>(gave_up) = 1;
       raise_status(status, FP8GEMM_ERR_TIMEOUT);
