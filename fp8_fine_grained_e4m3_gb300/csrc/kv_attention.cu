@@ -579,13 +579,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
   __shared__ long long scan[kWarps];
   __shared__ Walk walks[2];  // the item's, and the next one's
   __shared__ int last_one;
-  __shared__ int gave_up, never;  // a wait ran out; always 0
+  __shared__ int gave_up;  // a wait ran out
   __shared__ uint64_t bars[kWarps][kStages];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   Stage<kDim>* ring = reinterpret_cast<Stage<kDim>*>(shared) + warp * kStages;
 
   if (threadIdx.x == 0) {
-    gave_up = never = 0;
+    gave_up = 0;
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&bars[0][i], 1);
     fence_mbar_init();
   }
@@ -827,11 +827,11 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         // one outcome for the warp: what follows is warp-wide
         if (!__all_sync(0xffffffffu, mbar_wait_within(&bars[warp][stage], phases >> stage & 1,
                                                       &gave_up, a.wait_ns))) {
-          // results are void; what is still in flight lands first, or not at all
+          // results are void; what is still in flight lands before the CTA ends
           gave_up = 1;
           raise_status(status, FP8GEMM_ERR_TIMEOUT);
           for (int k = 0; k < kStages; ++k)
-            if (in_flight >> k & 1) mbar_wait_within(&bars[warp][k], phases >> k & 1, &never, a.wait_ns);
+            if (in_flight >> k & 1) mbar_drain(&bars[warp][k], phases >> k & 1);
           break;
         }
         phases ^= 1u << stage;

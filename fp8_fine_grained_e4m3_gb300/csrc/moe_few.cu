@@ -386,13 +386,13 @@ struct Ring {
   __device__ uint8_t* stage(int s) const { return buf + s * kStageBytes; }
   // Waits for stage s; false, for the whole warp, if that ran out for any of its
   // lanes (or another warp's wait did).
-  __device__ bool wait(int s, int* gave_up, int* never, int* status, unsigned long long limit_ns) {
+  __device__ bool wait(int s, int* gave_up, int* status, unsigned long long limit_ns) {
     if (!__all_sync(0xffffffffu, mbar_wait_within(&bar[s], phases >> s & 1, gave_up, limit_ns))) {
-      // results are void; what is still in flight lands first, or not at all
+      // results are void; what is still in flight lands before the CTA ends
       *reinterpret_cast<volatile int*>(gave_up) = 1;
       raise_status(status, FP8GEMM_ERR_TIMEOUT);
       for (int k = 0; k < kStages; ++k)
-        if (in_flight >> k & 1) mbar_wait_within(&bar[k], phases >> k & 1, never, limit_ns);
+        if (in_flight >> k & 1) mbar_drain(&bar[k], phases >> k & 1);
       return false;
     }
     phases ^= 1u << s;
@@ -403,12 +403,12 @@ struct Ring {
 
 struct Shared {
   uint64_t bars[kWarps][4];
-  int gave_up, never, last_one;  // a wait ran out; always 0; this CTA joins
+  int gave_up, last_one;  // a wait ran out; this CTA joins
 };
 
 __device__ __forceinline__ uint8_t* init_shared(Shared& sh, uint8_t* raw, const CUtensorMap* map) {
   if (threadIdx.x == 0) {
-    sh.gave_up = sh.never = 0;
+    sh.gave_up = 0;
     for (int i = 0; i < kWarps * 4; ++i) mbar_init(&sh.bars[0][i], 1);
     fence_mbar_init();
     tma_prefetch_desc(map);
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
     for (int m = 0; m < 3; ++m) sw[m] = next_sw[m];
     if (kb + 1 < Kb && left > 1) load_side(kb + 1);
     // After a wait that ran out the warp only keeps the others' barriers company.
-    dead = dead || !ring.wait(stage, &sh.gave_up, &sh.never, status, a.wait_ns);
+    dead = dead || !ring.wait(stage, &sh.gave_up, status, a.wait_ns);
     const uint8_t* w = ring.stage(stage);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_down_kernel(const Mo
       sxk[n][1] = next_sx[n][1] * next_sw;
     }
     if (kb + 1 < Kb && left > 1) load_side(kb + 1);
-    dead = dead || !ring.wait(stage, &sh.gave_up, &sh.never, status, a.wait_ns);
+    dead = dead || !ring.wait(stage, &sh.gave_up, status, a.wait_ns);
     const uint8_t* w = ring.stage(stage);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {

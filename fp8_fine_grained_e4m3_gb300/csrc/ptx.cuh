@@ -102,6 +102,14 @@ __device__ __forceinline__ bool mbar_wait_within(uint64_t* bar, uint32_t parity,
   }
 }
 
+// Lets a copy in flight land before its CTA leaves the shared memory that it goes to:
+// no abort flag, and a limit of its own (200 ms), whatever the launch's is.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > 200000000ull) break;
+}
+
 // ------------------------------------------------ cp.async (16-byte copies)
 // Copy 16 bytes global -> shared; bytes past `src_bytes` (0 or 16 here) are
 // written as zeros and not read.

@@ -1,10 +1,7 @@
 """Waits that run out in the cache attention and the MoE layer: whatever the
-limit, every warp of the launch ends."""
+limit, every warp of the launch ends, and no copy outlives its CTA."""
 
-import numpy as np
 import pytest
-
-from tests.gpu_helpers import dev
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +64,36 @@ def test_limits_from_no_time_to_enough(name):
         assert torch.equal(call(), want)
         assert b.fp8gemm_get_device_status() == b.OK
     assert b.OK in seen
+
+
+@pytest.mark.parametrize("gives_up", CALLS)
+@pytest.mark.parametrize("beside", ["attention, runs", "moe, 8 tokens a pass"])
+def test_calls_beside_and_behind_one_that_gave_up(gives_up, beside):
+    """Shared memory that the CTAs of a call which gave up leave is taken at once by
+    the CTAs of the next call on the stream and of a call on another one: a copy
+    that landed after its CTA had gone would fall into theirs."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    bad, good = CALLS[gives_up](), CALLS[beside]()
+    want = good()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        assert torch.equal(good(), want)
+    torch.cuda.synchronize()
+    behind = []
+    for _ in range(6):
+        b.set_wait_limit_ns(1)
+        try:
+            bad()
+        finally:
+            b.set_wait_limit_ns(0)
+        with torch.cuda.stream(other):
+            behind.append(good())
+        # the bad call leaves its own counters mid-count: only calls with other buffers follow it
+        if gives_up.split(",")[0] != beside.split(",")[0]:
+            behind.append(good())
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in behind)
+    assert b.fp8gemm_get_device_status() in (b.OK, b.ERR_TIMEOUT)
+    assert torch.equal(good(), want)
+    b.fp8gemm_release_workspaces(other)
