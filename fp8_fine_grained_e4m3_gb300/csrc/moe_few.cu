@@ -679,9 +679,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<NT>) moe_up_kernel(const MoeA
             sH[size_t(r.list[at.first + j]) * Ib + ib] = s;
           // h / s without the division's sequence (see silu): both times a power of two that
           // brings s into the range of the corrected quotient (h that this makes too small
-          // to hold has the code 0)
+          // to hold has the code 0, and so has a block whose s itself is: h pre < 2^-40)
           const float pre = s < 1e-25f ? 0x1p100f : s > 1e25f ? 0x1p-100f : 1.f;
-          const Reciprocal d = reciprocal(top != 0.f ? s * pre : 1.f);
+          const Reciprocal d = reciprocal(s != 0.f ? s * pre : 1.f);
 #pragma unroll
           for (int m = 0; m < 2; ++m)
 #pragma unroll

@@ -577,7 +577,8 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  *                  all E.  An expert at -infinity gets weight 0.
  *   for each choice: u = A W1^T (block scales and promotion as
  *                  fp8gemm_dense), h = silu(u[:I]) * u[I:] in FP32, quantised by
- *                  fp8_quant_1x128's rule, y = h W2^T
+ *                  fp8_quant_1x128's rule (zeros where a block's scale underflows
+ *                  to 0), y = h W2^T
  *   D[t] = bf16( sum over the choices of weight * y )
  *
  *   A  u8 e4m3 [T, H], sA f32 [T, ceil(H/128)]; logits f32 [T, E]

@@ -170,3 +170,18 @@ def test_more_calls_of_other_sizes_share_a_workspace():
     for _ in range(3):
         for s, w in zip(sets, want):
             assert torch.equal(b.fp8_moe_few(*s, 2)[0], w)
+
+
+def test_a_hidden_scale_that_underflows():
+    """|h| of 1e-44 to 3e-43: max |h| / 448 is 0 in FP32.  The codes are zeros and
+    the token's output is 0, for a token beside others that are ordinary too."""
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    ops = _operands(3, 256, 128, 3, seed=10)
+    ops[4] = (ops[4] * np.float32(2e-22)).astype(np.float32)
+    D, _, _ = b.fp8_moe_few(*[dev(x) for x in ops], 2)
+    assert (host(D) == 0).all()
+    ops = _operands(3, 256, 128, 3, seed=11)
+    ops[1][1] *= np.float32(2e-22)
+    _check(ops, 2)
+    D, _, _ = b.fp8_moe_few(*[dev(x) for x in ops], 2)
+    assert (host(D)[1] == 0).all()
