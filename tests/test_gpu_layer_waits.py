@@ -77,6 +77,7 @@ def test_calls_beside_and_behind_one_that_gave_up(gives_up, beside):
     bad, good = CALLS[gives_up](), CALLS[beside]()
     want = good()
     other = torch.cuda.Stream()
+    torch.cuda.synchronize()  # the inputs were made on the first stream
     with torch.cuda.stream(other):
         assert torch.equal(good(), want)
     torch.cuda.synchronize()
