@@ -9,6 +9,7 @@
 #include <mutex>
 #include <tuple>
 #include <utility>
+#include <vector>
 
 #include "common.cuh"
 #include "moe_few.cuh"
@@ -47,6 +48,8 @@ struct Workspace {
 std::mutex g_mu;
 std::map<int, DeviceInfo> g_devices;
 std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_workspaces;
+// One for each (device, stream) that has had a workspace; never removed.
+std::map<std::pair<int, cudaStream_t>, std::recursive_mutex> g_stream_mu;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -171,8 +174,23 @@ int finish(cudaError_t e, int nlaunch) {
 enum { kWsSplitK = 0, kWsQuantA = 1, kWsTable = 2, kWsBatch = 3, kWsContig = 4, kWsNorm = 5,
        kWsMoe = 6, kWsAttention = 7 };
 
+// A call that takes a workspace holds its stream's lock from the look-up to its last
+// launch.  Host threads may share a stream: without it one call's kernels, which
+// hand data on through the workspace, could be enqueued between another's, and a call
+// that needs a larger buffer could free the one that another is about to launch with.
+// Recursive: fp8gemm_dense_quant_a goes on into the dense call.  Never taken with g_mu held.
+using StreamLock = std::unique_lock<std::recursive_mutex>;
+StreamLock lock_stream(int dev, cudaStream_t s) {
+  std::recursive_mutex* m;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    m = &g_stream_mu[std::make_pair(dev, s)];
+  }
+  return StreamLock(*m);
+}
+
 // The buffer on device `dev` in the context `ctx`, both of device_info, which drops
-// the workspaces of an ended context.
+// the workspaces of an ended context.  The caller holds the stream's lock.
 int workspace_on(int dev, unsigned long long ctx, cudaStream_t s, size_t bytes, void** out, int slot) {
   std::lock_guard<std::mutex> lk(g_mu);
   auto key = std::make_tuple(dev, s, slot);
@@ -197,13 +215,6 @@ int workspace_on(int dev, unsigned long long ctx, cudaStream_t s, size_t bytes, 
   g_workspaces[key] = Workspace{p, bytes, ctx};
   *out = p;
   return FP8GEMM_OK;
-}
-
-int workspace_for(cudaStream_t s, size_t bytes, void** out, int slot = kWsSplitK) {
-  int dev = 0;
-  DeviceInfo d;
-  if (int r = device_info(&d, &dev)) return r;
-  return workspace_on(dev, d.ctx, s, bytes, out, slot);
 }
 
 constexpr int kSmallM = 64;  // dense calls with M <= this use the swap-AB stream-K kernel
@@ -370,7 +381,8 @@ int fp8gemm_dense_ex(const uint8_t* A, const float* sA, int a_fmt, const uint8_t
     if (!small_m_uses_workspace(c, a)) return finish(launch_gemm_small_m_any(c, a, nullptr, 0), 1);
     const size_t bytes = small_m_workspace_bytes(c.num_sms, N);
     void* ws = nullptr;
-    if (int r = workspace_for(stream, bytes, &ws)) return r;
+    const StreamLock lk = lock_stream(c.dev, stream);
+    if (int r = workspace_on(c.dev, c.ctx, stream, bytes, &ws, kWsSplitK)) return r;
     return finish(launch_gemm_small_m_any(c, a, ws, bytes), 1);
   }
   return run_gemm_tc(c, a);
@@ -410,11 +422,15 @@ int fp8gemm_dense_quant_a_ex(const float* X, uint8_t* Q, float* sA, const uint8_
     const cudaError_t e = launch_gemm_small_m_quant(c, a, X, Q, sA, &taken);
     if (taken) return finish(e, 1);
   }
+  StreamLock lk;
   if (!Q) {  // quantised A in the library's buffer: bytes, then (16-B aligned) scales
     const size_t qbytes = (size_t(M) * K + 15) / 16 * 16;
     void* ws = nullptr;
-    if (int r = workspace_for(stream, qbytes + size_t(M) * ceil_div(K, kBlockK) * 4, &ws,
-                              kWsQuantA))
+    LaunchCtx c;
+    if (int r = ctx_for(stream, &c)) return r;
+    lk = lock_stream(c.dev, stream);
+    if (int r = workspace_on(c.dev, c.ctx, stream, qbytes + size_t(M) * ceil_div(K, kBlockK) * 4,
+                             &ws, kWsQuantA))
       return r;
     Q = static_cast<uint8_t*>(ws);
     sA = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + qbytes);
@@ -442,7 +458,8 @@ int fp8gemm_grouped_table(const fp8gemm_problem* problems, int num_problems, int
   if (int r = ctx_for(stream, &c)) return r;
   const size_t bytes = table_workspace_bytes(c, max_M);
   void* ws = nullptr;
-  if (int r = workspace_for(stream, bytes, &ws, kWsTable)) return r;
+  const StreamLock lk = lock_stream(c.dev, stream);
+  if (int r = workspace_on(c.dev, c.ctx, stream, bytes, &ws, kWsTable)) return r;
   return finish(launch_gemm_table(c, problems, num_problems, max_M, ws, bytes), 1);
 }
 
@@ -471,7 +488,8 @@ int fp8gemm_dense_batch(const fp8gemm_problem* problems, int num_problems,
   LaunchCtx c;
   if (int r = ctx_for(stream, &c)) return r;
   void* ws = nullptr;
-  if (int r = workspace_for(stream, 256, &ws, kWsBatch)) return r;
+  const StreamLock lk = lock_stream(c.dev, stream);
+  if (int r = workspace_on(c.dev, c.ctx, stream, 256, &ws, kWsBatch)) return r;
   int launches = 0;
   const cudaError_t e = launch_gemm_tc_batch(c, problems, num_problems,
                                              static_cast<unsigned int*>(ws), &launches);
@@ -501,7 +519,8 @@ int fp8gemm_grouped_contiguous_fmt(const uint8_t* A, const float* sA, int a_fmt,
   // dynamically (the largest and the smallest experts' tiles side by side)
   if (const size_t bytes = contig_order_workspace_bytes(c, a)) {
     void* ws = nullptr;
-    if (int r = workspace_for(stream, bytes, &ws, kWsContig)) return r;
+    const StreamLock lk = lock_stream(c.dev, stream);
+    if (int r = workspace_on(c.dev, c.ctx, stream, bytes, &ws, kWsContig)) return r;
     int launches = 0;
     const cudaError_t e = launch_gemm_tc_contiguous_ordered(c, a, ws, bytes, &launches);
     return finish(e, launches);
@@ -577,6 +596,7 @@ int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float*
   if (M == 0)  // a sum over no rows
     return finish(cudaMemsetAsync(dG, 0, size_t(K) * 4, stream), 0);
   void* ws = nullptr;
+  const StreamLock lk = lock_stream(c.dev, stream);
   if (int r = workspace_on(c.dev, c.ctx, stream, rmsnorm_backward_workspace_bytes(c), &ws, kWsNorm)) return r;
   const NormGradArgs a{dY, H, rstd, G, dH, dX, dG, M, K, x_type == FP8GEMM_TYPE_F32};
   return finish(launch_rmsnorm_backward(c, a, ws), 2);
@@ -648,6 +668,7 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
                           fmt, log2_block(block),
                           wait_limit_ns()};
   void* ws = nullptr;
+  const StreamLock lk = lock_stream(c.dev, stream);
   if (int r = workspace_on(c.dev, c.ctx, stream, kv_attention_workspace_bytes(c), &ws, kWsAttention))
     return r;
   return finish(launch_kv_attention(c, a, ws), 1);
@@ -677,6 +698,7 @@ int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const ui
   const MoeArgs a{A, sA, logits, W1, s1, W2, s2, static_cast<__nv_bfloat16*>(D), ids, weights,
                   T, H, I, E, top_k, renormalise, wait_limit_ns()};
   void* ws = nullptr;
+  const StreamLock lk = lock_stream(c.dev, stream);
   if (int r = workspace_on(c.dev, c.ctx, stream, moe_few_workspace_bytes(c, a), &ws, kWsMoe))
     return r;
   int launches = 0;
@@ -701,11 +723,20 @@ int fp8gemm_get_device_status(fp8gemm_stream_t stream, int* out) {
     // arrival counters not back at zero: drop every workspace of this device
     // (after the device is idle) so that the next calls start from zeroed ones
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
-      return FP8GEMM_ERR_LAUNCH;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FP8GEMM_ERR_LAUNCH;
+    std::map<cudaStream_t, StreamLock> held;  // no other thread is between look-up and launch
+    std::vector<cudaStream_t> streams;
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      for (auto& m : g_stream_mu)
+        if (m.first.first == dev) streams.push_back(m.first.second);
+    }
+    for (cudaStream_t s : streams) held[s] = lock_stream(dev, s);  // in the map's order
+    if (cudaDeviceSynchronize() != cudaSuccess) return FP8GEMM_ERR_LAUNCH;
     std::lock_guard<std::mutex> lk(g_mu);
     for (auto w = g_workspaces.begin(); w != g_workspaces.end();) {
-      if (std::get<0>(w->first) != dev) {
+      // (a stream that is new since then has nothing that gave up)
+      if (std::get<0>(w->first) != dev || held.count(std::get<1>(w->first)) == 0) {
         ++w;
         continue;
       }
@@ -742,6 +773,7 @@ int fp8gemm_release_workspaces(fp8gemm_stream_t stream) {
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8GEMM_ERR_LAUNCH;
   DeviceInfo d;  // forgets workspaces of an ended context (not freed twice)
   if (int r = device_info(&d)) return r;
+  const StreamLock held = lock_stream(dev, stream);
   std::lock_guard<std::mutex> lk(g_mu);
   bool synced = false;
   int rc = FP8GEMM_OK;

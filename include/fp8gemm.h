@@ -53,7 +53,9 @@
  *    (10 MB), fp8_kv_attention (8 MB) and fp8_moe_few (60 MB + 1 KB for each
  *    element of I) keep theirs the same way.
  *    Such a first call must therefore not happen during CUDA graph capture.
- *    Calls on different streams never share a workspace.  The reduction
+ *    Calls on different streams never share a workspace.  Host threads may
+ *    call at the same time, on one stream too: a call that needs a workspace
+ *    holds a lock of its stream until its last kernel is enqueued.  The reduction
  *    order is fixed, so results are deterministic.  A caller that retires a
  *    stream frees its workspaces with fp8gemm_release_workspaces() before
  *    destroying it; fp8gemm_workspace_bytes() reports what is held.
