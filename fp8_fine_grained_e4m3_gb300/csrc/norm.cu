@@ -10,6 +10,8 @@
 // Both are bound by memory: a row is read once into registers, reduced there
 // and written once.  Sums and statistics are FP32.  Measured, BF16 with a residual:
 // 4096 x 7168 forward 36.6 us, 5.6 TB/s; 8192 x 4096 backward 46.3 us, 5.8 TB/s.
+#include <cfloat>
+
 #include "common.cuh"
 #include "f8_convert.cuh"
 #include "ptx.cuh"
@@ -54,7 +56,7 @@ template <class T, int kIter, bool kE5M2, bool kRes>
 __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     const T* __restrict__ X, const T* R, const float* __restrict__ G, float eps, T* H,
     uint8_t* __restrict__ Q, float* __restrict__ sQ, float* __restrict__ rstd_out, int K) {
-  __shared__ float red[32];
+  __shared__ float red[2][32];
   const size_t row = size_t(blockIdx.x) * K;
   const int Kb = ceil_div(K, kBlockK);
   griddep_launch_dependents();
@@ -83,7 +85,26 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
   }
-  const float rstd = __frsqrt_rn(__fdiv_rn(cta_sum(sum, red), float(K)) + eps);
+  sum = cta_sum(sum, red[0]);
+  float rstd = __frsqrt_rn(__fdiv_rn(sum, float(K)) + eps);
+  float ry = rstd;
+  // The squares left FP32's range (|h| above 1e17; or, with eps = 0, below 1e-19): from
+  // here on h times a power of two, beside which eps is nothing.  A row of zeros gives zeros.
+  if (!(sum <= FLT_MAX) || rstd == INFINITY) {  // the same in every thread
+    const float f = sum > 1.f ? 0x1p-100f : 0x1p100f;
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        h[i][j] *= f;
+        sum = fmaf(h[i][j], h[i][j], sum);
+      }
+    sum = cta_sum(sum, red[1]);
+    ry = __frsqrt_rn(__fdiv_rn(sum, float(K)));
+    rstd = ry * f;
+    if (sum == 0.f) ry = 0.f;
+  }
   if (threadIdx.x == 0 && rstd_out) rstd_out[blockIdx.x] = rstd;
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
@@ -93,7 +114,7 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     float amax = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      h[i][j] = h[i][j] * rstd * g[j];
+      h[i][j] = h[i][j] * ry * g[j];
       amax = fmaxf(amax, fabsf(h[i][j]));
     }
 #pragma unroll

@@ -462,7 +462,9 @@ enum fp8gemm_type {
  *   y = h rstd g;   sQ, Q = fp8_quant_1x128's rule on y (limit of `fmt`)
  *
  * All arithmetic is FP32; the norm is taken of the rounded h, which is what
- * the next layer and the gradient see.
+ * the next layer and the gradient see.  The sum of h^2 may leave FP32's range
+ * (it is then taken of h times a power of two); a row of zeros with eps = 0 gives
+ * zeros and rstd = infinity.
  *
  *   X    [M, K] of x_type (FP8GEMM_TYPE_*)
  *   R, H [M, K] of x_type: the residual in and h out; both NULL for none.  H

@@ -181,3 +181,32 @@ def test_no_rows():
     dG = torch.full((256,), 3.0, device="cuda")
     b.fp8_rmsnorm_backward(x, x, rstd, gain, dgain=dG)
     assert not dG.any()
+
+
+@pytest.mark.parametrize("M,K,kind,residual", [(3, 400, "bf16", True), (5, 7168, "f32", False), (320, 2048, "bf16", True),
+                                               (310, 7168, "f32", True), (2, 16384, "bf16", False)])
+@pytest.mark.parametrize("size,eps", [(1e25, EPS), (1e38, 0.0), (1e-30, 0.0)])
+def test_squares_past_the_range_of_fp32(M, K, kind, residual, size, eps):
+    """Finite rows whose squares over- or underflow, beside an ordinary row and one
+    of zeros.  Bounds as above: the sum is the same one, of h times a power of two."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    g = np.random.default_rng(K)
+    t = torch.bfloat16 if kind == "bf16" else torch.float32
+    X, R = (g.uniform(0.25, 1, (M, K)).astype(np.float32) * np.float32(size) for _ in range(2))
+    X[0], R[0] = g.standard_normal(K), g.standard_normal(K)
+    X[-1] = R[-1] = 0
+    gain = (1 + 0.2 * g.standard_normal(K)).astype(np.float32)
+    tX, tR = dev(X).to(t), dev(R).to(t) if residual else None
+    got = b.fp8_rmsnorm_quant(tX, dev(gain), eps, residual=tR)
+    live = slice(0, M - 1)
+    h, r, y = layer.rmsnorm(tX.double().cpu().numpy()[live], tR.double().cpu().numpy()[live] if residual else None, gain,
+                            eps, kind == "bf16")
+    assert np.array_equal(got[2].double().cpu().numpy()[live], h)
+    assert np.all(np.abs(host(got[3])[live] - r) <= 2e-6 * r)
+    q, s = host(got[0]), host(got[1]).astype(np.float64)
+    amax = np.stack([np.max(np.abs(y[:, k:k + 128]), 1) for k in range(0, K, 128)], 1)
+    assert np.all(np.abs(s[live] - amax / 448) <= 2.5e-6 * amax / 448)
+    v = layer.e4m3.decode(q[live]) * np.repeat(s[live], 128, 1)[:, :K]
+    assert np.all(np.abs(v - y) <= np.abs(y) / 15 + np.repeat(amax / 448, 128, 1)[:, :K] * 2.0 ** -9)
+    assert not q[-1].any() and not s[-1].any()
