@@ -86,11 +86,11 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     for (int j = 0; j < 8; ++j) sum = fmaf(h[i][j], h[i][j], sum);
   }
   sum = cta_sum(sum, red[0]);
-  float rstd = __frsqrt_rn(__fdiv_rn(sum, float(K)) + eps);
-  float ry = rstd;
-  // The squares left FP32's range (|h| above 1e17; or, with eps = 0, below 1e-19): from
-  // here on h times a power of two, beside which eps is nothing.  A row of zeros gives zeros.
-  if (!(sum <= FLT_MAX) || rstd == INFINITY) {  // the same in every thread
+  const float square = __fdiv_rn(sum, float(K)) + eps;
+  float rstd = __frsqrt_rn(square), ry = rstd;
+  // The squares leave FP32's range (|h| above 1e17; or, with next to no eps, below 1e-15): from
+  // here on h times a power of two.  A row of zeros gives zeros whatever eps.
+  if (!(sum <= FLT_MAX) || square < 0x1p-100f) {  // the same in every thread
     const float f = sum > 1.f ? 0x1p-100f : 0x1p100f;
     sum = 0.f;
 #pragma unroll
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
         sum = fmaf(h[i][j], h[i][j], sum);
       }
     sum = cta_sum(sum, red[1]);
-    ry = __frsqrt_rn(__fdiv_rn(sum, float(K)));
+    ry = __frsqrt_rn(__fdiv_rn(sum, float(K)) + eps * f * f);
     rstd = ry * f;
     if (sum == 0.f) ry = 0.f;
   }

@@ -185,7 +185,7 @@ def test_no_rows():
 
 @pytest.mark.parametrize("M,K,kind,residual", [(3, 400, "bf16", True), (5, 7168, "f32", False), (320, 2048, "bf16", True),
                                                (310, 7168, "f32", True), (2, 16384, "bf16", False)])
-@pytest.mark.parametrize("size,eps", [(1e25, EPS), (1e38, 0.0), (1e-30, 0.0)])
+@pytest.mark.parametrize("size,eps", [(1e25, EPS), (1e38, 0.0), (1e-30, 0.0), (3e-21, 0.0), (1e-18, 1e-36)])
 def test_squares_past_the_range_of_fp32(M, K, kind, residual, size, eps):
     """Finite rows whose squares over- or underflow, beside an ordinary row and one
     of zeros.  Bounds as above: the sum is the same one, of h times a power of two."""
