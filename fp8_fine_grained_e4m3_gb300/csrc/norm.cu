@@ -31,6 +31,14 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
+// The larger value, or NaN if one is: a NaN in a block must not look like the others' maximum
+// (a diverged row would become codes and scales of 0).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // amax / limit: the corrected quotient where that is exact.
 template <bool kE5M2>
 __device__ __forceinline__ float block_scale(float amax) {
@@ -115,10 +123,10 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       h[i][j] = h[i][j] * ry * g[j];
-      amax = fmaxf(amax, fabsf(h[i][j]));
+      amax = max_nan(amax, fabsf(h[i][j]));
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const Reciprocal s = reciprocal(block_scale<kE5M2>(amax));
     if (k < K) {
       *reinterpret_cast<uint2*>(Q + row + k) = quant8<kE5M2>(h[i], amax, s);

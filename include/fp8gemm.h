@@ -464,7 +464,9 @@ enum fp8gemm_type {
  * All arithmetic is FP32; the norm is taken of the rounded h, which is what
  * the next layer and the gradient see.  The sum of h^2 may leave FP32's range
  * (it is then taken of h times a power of two); a row of zeros with eps = 0 gives
- * zeros and rstd = infinity.
+ * zeros and rstd = infinity.  A NaN in a row makes its scales and codes NaN; an
+ * infinity makes rstd 0 and the scale and code of its own block NaN: a product
+ * with the row is NaN either way.
  *
  *   X    [M, K] of x_type (FP8GEMM_TYPE_*)
  *   R, H [M, K] of x_type: the residual in and h out; both NULL for none.  H

@@ -210,3 +210,40 @@ def test_squares_past_the_range_of_fp32(M, K, kind, residual, size, eps):
     v = layer.e4m3.decode(q[live]) * np.repeat(s[live], 128, 1)[:, :K]
     assert np.all(np.abs(v - y) <= np.abs(y) / 15 + np.repeat(amax / 448, 128, 1)[:, :K] * 2.0 ** -9)
     assert not q[-1].any() and not s[-1].any()
+
+
+@pytest.mark.parametrize("K,M,kind", [(400, 3, "bf16"), (7168, 2, "f32"), (2048, 320, "bf16")])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_a_row_that_is_not_finite_stays_so(K, M, kind, bad, fmt):
+    """One NaN or infinity: the row's product with anything is NaN, other rows are
+    what they were."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    g = np.random.default_rng(4)
+    X = g.standard_normal((M, K)).astype(np.float32)
+    t = torch.bfloat16 if kind == "bf16" else torch.float32
+    gain = dev((1 + 0.2 * g.standard_normal(K)).astype(np.float32))
+    clean = b.fp8_rmsnorm_quant(dev(X).to(t), gain, EPS, fmt=fmt)
+    X[1, K - 3] = bad
+    got = b.fp8_rmsnorm_quant(dev(X).to(t), gain, EPS, fmt=fmt)
+    values = _CODES[fmt].decode(host(got[0])) * np.repeat(host(got[1]), 128, 1)[:, :K]
+    rows = np.arange(M) != 1
+    assert np.isnan(values[1].sum())
+    assert np.isfinite(values[rows]).all()
+    for a, c in zip(got[:2], clean[:2]):
+        assert np.array_equal(host(a)[rows], host(c)[rows])
+    if np.isnan(bad):
+        assert np.isnan(host(got[1])[1]).all()
+    W, sW = b.fp8_quant_128x128(dev(g.standard_normal((128, K)).astype(np.float32)))
+    D = b.fp8gemm_dense_fmt(got[0], got[1], fmt, W, sW, "e4m3")
+    assert bool(D[1].isnan().all()) and bool(D[torch.from_numpy(rows).cuda()].isfinite().all())
+
+
+def test_a_gain_that_is_not_a_number_shows():
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    g = np.random.default_rng(5)
+    X, gain = g.standard_normal((2, 512)).astype(np.float32), np.ones(512, np.float32)
+    gain[128:256] = np.nan
+    _, s, _, _ = b.fp8_rmsnorm_quant(dev(X), dev(gain), EPS)
+    assert np.array_equal(np.isnan(host(s)), [[False, True, False, False]] * 2)
