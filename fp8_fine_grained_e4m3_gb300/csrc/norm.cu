@@ -47,12 +47,13 @@ __device__ __forceinline__ float block_scale(float amax) {
   return amax >= 1e-25f && amax <= 1e30f ? quotient(amax, d) : __fdiv_rn(amax, kLimit);
 }
 
-// Eight values to codes of one scale.
+// Eight values to codes of one scale; zeros where it is 0 (all zeros, or a maximum so
+// small that the scale underflows: the quotient of a 0 there would be NaN).
 template <bool kE5M2>
-__device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, const Reciprocal& d) {
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], const Reciprocal& d) {
   const float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
   if (d.safe) return make_uint2(quant4<kE5M2>(a, d), quant4<kE5M2>(b, d));
-  if (amax == 0.f) return make_uint2(0u, 0u);
+  if (d.s == 0.f) return make_uint2(0u, 0u);
   return make_uint2(quant4<kE5M2>(a, d.s), quant4<kE5M2>(b, d.s));
 }
 
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kIter == 4 ? 512 : 1024) rmsnorm_quant_kernel(
     for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const Reciprocal s = reciprocal(block_scale<kE5M2>(amax));
     if (k < K) {
-      *reinterpret_cast<uint2*>(Q + row + k) = quant8<kE5M2>(h[i], amax, s);
+      *reinterpret_cast<uint2*>(Q + row + k) = quant8<kE5M2>(h[i], s);
       if (threadIdx.x % 16 == 0) sQ[size_t(blockIdx.x) * Kb + k / kBlockK] = s.s;
     }
   }

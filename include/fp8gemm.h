@@ -459,7 +459,8 @@ enum fp8gemm_type {
  *
  *   h = x + r, rounded to the stream's type   (h = x without a residual)
  *   rstd[m] = 1 / sqrt(mean over k of h^2 + eps)
- *   y = h rstd g;   sQ, Q = fp8_quant_1x128's rule on y (limit of `fmt`)
+ *   y = h rstd g;   sQ, Q = fp8_quant_1x128's rule on y (limit of `fmt`; zeros
+ *                   where a block's scale underflows to 0)
  *
  * All arithmetic is FP32; the norm is taken of the rounded h, which is what
  * the next layer and the gradient see.  The sum of h^2 may leave FP32's range

@@ -247,3 +247,18 @@ def test_a_gain_that_is_not_a_number_shows():
     gain[128:256] = np.nan
     _, s, _, _ = b.fp8_rmsnorm_quant(dev(X), dev(gain), EPS)
     assert np.array_equal(np.isnan(host(s)), [[False, True, False, False]] * 2)
+
+
+def test_a_scale_that_underflows():
+    """|y| of at most 2e-43 in a block: its scale is 0 in FP32, its codes are zeros,
+    and the row's product is that of the other blocks."""
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    g = np.random.default_rng(6)
+    X, gain = g.uniform(-1, 1, (3, 384)).astype(np.float32), np.ones(384, np.float32)
+    X[:, ::5] = 0
+    gain[128:256] = 1e-43
+    Q, s, _, _ = b.fp8_rmsnorm_quant(dev(X), dev(gain), EPS)
+    assert not host(Q)[:, 128:256].any() and not host(s)[:, 1].any()
+    assert host(Q)[:, :128].any() and host(s)[:, 0].all()
+    W, sW = b.fp8_quant_128x128(dev(g.standard_normal((128, 384)).astype(np.float32)))
+    assert bool(b.fp8gemm_dense(Q, s, W, sW).isfinite().all())
