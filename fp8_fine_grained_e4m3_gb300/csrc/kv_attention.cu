@@ -20,7 +20,10 @@
 // FP8 codes are exact in FP16; q is shifted by a power of two per row to use
 // FP16's range (BF16 has fewer mantissa bits); p is rounded to FP16 (11
 // bits, far below the BF16 output's step).  Scores, statistics, sums and the
-// output accumulate in FP32; a tile's scales are applied to its FP32 products.
+// output accumulate in FP32; a tile's scales are applied to its FP32 products, the
+// values' as they are added to O: a scale inside p would take p out of FP16's range
+// where neighbouring blocks' scales differ (64 ragged sequences with 8 rows a head: 100 us
+// either way; 32 rows, which the products bound: 195 with the scale in p, 216 so).
 // Measured: 64 ragged sequences of up to 8192 tokens, 8 heads of 128 (584 MB) 101 us, 5.8
 // TB/s; one of 131077 with 16 rows a head (268 MB) 55 us, 4.9 TB/s, of which the start
 // takes 5 and the join of the CTAs' results 6.
@@ -171,8 +174,7 @@ __device__ __forceinline__ void take_queries(Queries<kDim>& q, const RawQuery<kD
   q.mul[1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
 }
 
-// Running softmax of a lane's two rows and its share of O^T in units of the
-// warp's value scale: o[j] holds dimensions (dim/8) g + 2j (rows 2t, 2t + 1)
+// Running softmax of a lane's two rows and its share of O^T: o[j] holds dimensions (dim/8) g + 2j (rows 2t, 2t + 1)
 // and + 1 (rows 2t, 2t + 1).
 template <int kDim>
 struct State {
@@ -190,18 +192,13 @@ __device__ __forceinline__ void clear(State<kDim>& s) {
     for (int e = 0; e < 4; ++e) s.o[j][e] = 0.f;
 }
 
-// p is brought to the units of O by vs / unit before it is rounded to FP16.
-// The unit follows the tiles' scales so that this stays in (2^-6, 1]; tiles whose
-// scale is 2^60 below the largest met leave it.
-constexpr float kUnitLow = 1.f / 64, kUnitFar = 1152921504606846976.f;
-
 // One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
 // fragment i sees (may be negative or past its end); least_limit: of the row that sees
 // the fewest.  fresh: the item's first tile of this warp.  there: bit h where
 // fragment h of the tile is; valid: its tokens that exist; ks, vs: the scales
 // of its fragments.
 template <int kDim, bool kE5M2, int kNR>
-__device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
+__device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR],
                                             const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
                                             const int (&limit)[kNR][2], int least_limit, int tok,
                                             uint32_t there, bool fresh, int valid, const float (&ks)[2], const float (&vs)[2],
@@ -286,17 +283,6 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
         }
       }
   }
-  const float top = fmaxf(vs[0], vs[1]);
-  if (top > unit || (top < kUnitLow * unit && top * kUnitFar > unit)) {
-    const float grow = __fdiv_rn(unit, top);
-#pragma unroll
-    for (int i = 0; i < kNR; ++i)
-#pragma unroll
-      for (int j = 0; j < kDim / 16; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i].o[j][e] *= grow;
-    unit = top;
-  }
   uint32_t b[2][kNR][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -307,13 +293,6 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
         c[h][i][e] = exp2_fast(c[h][i][e]);
         s[i].l[e & 1] += c[h][i][e];
       }
-    if (vs[h] != unit) {  // the warp's tiles of one block share it
-      const float to_unit = unit > 0.f ? __fdiv_rn(vs[h], unit) : 0.f;
-#pragma unroll
-      for (int i = 0; i < kNR; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[h][i][e] *= to_unit;
-    }
 #pragma unroll
     for (int i = 0; i < kNR; ++i) {
       b[h][i][0] = transpose8x8(f16x2_bits(c[h][i][0], c[h][i][1]));
@@ -343,7 +322,11 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR], float& unit,
                              f8x2_to_f16x2<kE5M2>(uint16_t(hi)),
                              f8x2_to_f16x2<kE5M2>(uint16_t(hi >> 16))};
 #pragma unroll
-      for (int i = 0; i < kNR; ++i) mma_f16(s[i].o[j], a, b[h][i][0], b[h][i][1]);
+      for (int i = 0; i < kNR; ++i) {
+        float d[4];
+        mma_f16_new(d, a, b[h][i][0], b[h][i][1]);
+        add_scaled4(s[i].o[j], vs[h], d);
+      }
     }
   }
 }
@@ -778,7 +761,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         }
       }
     };
-    float unit = 0.f;
     look_up(batch, lane);
     // Queries and scales are asked for before the tiles: behind the first tiles of all
     // warps (29 MB) they would come microseconds late.
@@ -836,7 +818,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         }
         phases ^= 1u << stage;
         in_flight &= ~(1u << stage);
-        attend_tile<kDim, kE5M2, kNR>(s, unit, ring[stage], q, limit, least_limit, tok, there, fresh,
+        attend_tile<kDim, kE5M2, kNR>(s, ring[stage], q, limit, least_limit, tok, there, fresh,
                                       len - tok, ks, vs, lane);
         fresh = false;
         __syncwarp();  // the stage has been read
@@ -868,7 +850,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j)
           *reinterpret_cast<float2*>(&so[warp][row][g * (kDim / 8) + 2 * j]) =
-              make_float2(s[i].o[j][r] * unit, s[i].o[j][2 + r] * unit);
+              make_float2(s[i].o[j][r], s[i].o[j][2 + r]);
       }
     __syncthreads();
     const Walk& done = walks[flip ^ 1];

@@ -406,6 +406,28 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// D = A * B of the same shape and types.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// o += f d, two elements an instruction, each rounded once.
+__device__ __forceinline__ void add_scaled4(float (&o)[4], float f, const float (&d)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2)
+    asm("{\n\t.reg .b64 o, f, d;\n\t"
+        "mov.b64 o, {%0, %1};\n\tmov.b64 f, {%2, %2};\n\tmov.b64 d, {%3, %4};\n\t"
+        "fma.rn.f32x2 o, f, d, o;\n\t"
+        "mov.b64 {%0, %1}, o;\n\t}"
+        : "+f"(o[e]), "+f"(o[e + 1])
+        : "f"(f), "f"(d[e]), "f"(d[e + 1]));
+}
+
 // Per-warpgroup register budget changes (all four warps of a warpgroup
 // execute the same instruction).  The sum over warpgroups must stay within
 // the registers the CTA was launched with.

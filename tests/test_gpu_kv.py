@@ -395,3 +395,38 @@ def test_attention_of_more_rows_than_a_warp_takes(counts, group, heads, dim, blo
     _check(got, c, Qr, cu, dim ** -0.5, fmt)
     assert np.array_equal(got, _attend(c, Q, cu, dim ** -0.5, fmt, max_q=max(counts))[0])
     assert b.fp8gemm_get_device_status() == b.OK
+
+
+@pytest.mark.parametrize("dim,group,fmt", [(128, 1, "e4m3"), (64, 4, "e5m2"), (128, 16, "e4m3")])
+@pytest.mark.parametrize("apart", [20, -20, 60])
+def test_attention_keeps_the_smaller_of_two_scales(dim, group, fmt, apart):
+    """Blocks of 16, two to a tile, whose value scales differ by 2^20 or 2^60, all the
+    probability on every other one.  Bound relative to those: the others' p is below
+    2^-100 by construction, so the terms of FP16's range above do not arise."""
+    c = Cache([16 * 41], 1, dim, 16, fmt, seed=50, spread=0)
+    enc, limit = _CODES[fmt].encode_rne_sat, 448.0 if fmt == "e4m3" else 57344.0
+    lead = c.table[0, :c.width]
+    c.k[lead[::2]], c.k[lead[1::2]] = enc(np.float32(limit)), enc(np.float32(-limit))  # scores of one sign each
+    c.ks[:] = 1 / limit
+    c.vs[lead[1::2]] *= np.float32(2.0 ** apart)
+    Q = np.full((1, group, dim), 1.0, np.float32)
+    got, Qr = _attend(c, Q, None, 100.0 / dim, fmt)  # scores +-100
+    O, A = layer.kv_attention(Qr, c.k, c.ks, c.v, c.vs, c.table, c.lens, [0, 1], 100.0 / dim, fmt)
+    assert np.all(np.abs(got - O) <= 2.0 ** -8 * np.abs(O) + 2.0 ** -10 * A)
+    assert np.abs(O).max() > 0.01
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_over_falling_scales(dim):
+    """Value scales 1, 2^-59 and 2^-118 along a sequence, met one after the other by
+    every warp: finite throughout."""
+    heads, n = 400, 36 * 32
+    c = Cache([n], heads, dim, 32, "e4m3", seed=51, spread=0)
+    for j in range(36):
+        c.vs[c.table[0, j]] = np.float32(2.0 ** (-59 * (j // 12)))
+    g = np.random.default_rng(52)
+    Q = g.standard_normal((1, heads, dim)).astype(np.float32)
+    got, Qr = _attend(c, Q, None, dim ** -0.5, "e4m3")
+    assert np.isfinite(got).all()
+    c.k, c.ks, c.v, c.vs = (x[:, :3] for x in (c.k, c.ks, c.v, c.vs))
+    _check(got[:, :3], c, Qr[:, :3], [0, 1], dim ** -0.5, "e4m3")
