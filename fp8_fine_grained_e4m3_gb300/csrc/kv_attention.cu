@@ -19,11 +19,11 @@
 // output dimension to V^T's rows such that a lane's share of a value is too.
 // FP8 codes are exact in FP16; q is shifted by a power of two per row to use
 // FP16's range (BF16 has fewer mantissa bits); p is rounded to FP16 (11
-// bits, far below the BF16 output's step).  Scores, statistics, sums and the
+// bits where it is 2^-25 of the largest or more, the BF16 output has 8).  Scores, statistics, sums and the
 // output accumulate in FP32; a tile's scales are applied to its FP32 products, the
 // values' as they are added to O: a scale inside p would take p out of FP16's range
 // where neighbouring blocks' scales differ (64 ragged sequences with 8 rows a head: 100 us
-// either way; 32 rows, which the products bound: 195 with the scale in p, 216 so).
+// either way; 32 rows, which the products bound: 195 with the scale in p, 210 so).
 // Measured: 64 ragged sequences of up to 8192 tokens, 8 heads of 128 (584 MB) 101 us, 5.8
 // TB/s; one of 131077 with 16 rows a head (268 MB) 55 us, 4.9 TB/s, of which the start
 // takes 5 and the join of the CTAs' results 6.
@@ -52,7 +52,12 @@ constexpr int kMinTiles = 8;
 constexpr int kItemCost = 16;
 constexpr int kStages = 2;  // tiles of a warp in shared memory
 constexpr float kNone = -1e30f;  // the maximum of nothing: below any score
-constexpr float kLazy = 8.f;  // the running maximum may lag by 2^8: p stays below 256
+// p is held times 2^kLift, and the running maximum may lag by 2^kLazy: FP16's largest
+// numbers are in use, so that p keeps its 11 bits down to 2^-(14 + kLift) of the largest one
+// and is lost below 2^-(25 + kLift) only (131072 tokens there are 2^-19 of the sum).  The lift
+// is added to the difference of score and maximum: it would be lost in a large maximum.
+constexpr float kLazy = 4.f, kLift = 11.f;
+constexpr float kUnlift = 1.f / 2048;  // 2^-kLift
 
 // Transposes an 8x8 matrix of 16-bit elements held two to a lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -178,7 +183,7 @@ __device__ __forceinline__ void take_queries(Queries<kDim>& q, const RawQuery<kD
 // and + 1 (rows 2t, 2t + 1).
 template <int kDim>
 struct State {
-  float m[2], l[2];  // l: this lane's tokens only
+  float m[2], l[2];  // l: this lane's tokens only, times 2^kLift
   float o[kDim / 16][4];
 };
 
@@ -290,7 +295,7 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR],
     for (int i = 0; i < kNR; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        c[h][i][e] = exp2_fast(c[h][i][e]);
+        c[h][i][e] = exp2_fast(c[h][i][e] + kLift);
         s[i].l[e & 1] += c[h][i][e];
       }
 #pragma unroll
@@ -325,7 +330,7 @@ __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR],
       for (int i = 0; i < kNR; ++i) {
         float d[4];
         mma_f16_new(d, a, b[h][i][0], b[h][i][1]);
-        add_scaled4(s[i].o[j], vs[h], d);
+        add_scaled4(s[i].o[j], vs[h] * kUnlift, d);
       }
     }
   }
@@ -845,7 +850,7 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         for (int o = 4; o < 32; o <<= 1) s[i].l[r] += __shfl_xor_sync(0xffffffffu, s[i].l[r], o);
         if (g == 0) {
           sm[warp][row] = s[i].l[r] == 0.f ? kNone : s[i].m[r];
-          sl[warp][row] = s[i].l[r];
+          sl[warp][row] = s[i].l[r] * kUnlift;
         }
 #pragma unroll
         for (int j = 0; j < kDim / 16; ++j)

@@ -418,15 +418,52 @@ def test_attention_keeps_the_smaller_of_two_scales(dim, group, fmt, apart):
 
 @pytest.mark.parametrize("dim", [64, 128])
 def test_attention_over_falling_scales(dim):
-    """Value scales 1, 2^-59 and 2^-118 along a sequence, met one after the other by
-    every warp: finite throughout."""
-    heads, n = 400, 36 * 32
-    c = Cache([n], heads, dim, 32, "e4m3", seed=51, spread=0)
-    for j in range(36):
-        c.vs[c.table[0, j]] = np.float32(2.0 ** (-59 * (j // 12)))
+    """Value scales 1, 2^-59 and 2^-118 along a sequence, 384 tokens each in turn, so
+    that warps meet them one after the other: finite throughout."""
+    n = 60000
+    c = Cache([n], 1, dim, 32, "e4m3", seed=51, spread=0)
+    for j in range(c.width):
+        c.vs[c.table[0, j]] = np.float32(2.0 ** (-59 * (j // 12 % 3)))
     g = np.random.default_rng(52)
-    Q = g.standard_normal((1, heads, dim)).astype(np.float32)
+    Q = g.standard_normal((1, 2, dim)).astype(np.float32)
     got, Qr = _attend(c, Q, None, dim ** -0.5, "e4m3")
     assert np.isfinite(got).all()
-    c.k, c.ks, c.v, c.vs = (x[:, :3] for x in (c.k, c.ks, c.v, c.vs))
-    _check(got[:, :3], c, Qr[:, :3], [0, 1], dim ** -0.5, "e4m3")
+    _check(got, c, Qr, [0, 1], dim ** -0.5, "e4m3")
+
+
+@pytest.mark.parametrize("tail", [18.4, 14.0, 20.8])
+@pytest.mark.parametrize("heads", [1, 40])
+def test_attention_of_a_flat_tail_below_a_peak(tail, heads):
+    """One token above 131072 others of equal scores and values of one sign, e^tail
+    times as probable as each (2^26.5, 2^20, 2^30 times), its own value 0: the output is the
+    tail alone.  p's rounding is 2^-12 relative, or, next to FP16's end, half of its
+    least step, 2^-25, under the factor 2^11 that p is held with: 2^-36 of the peak a token."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    dim, n, block = 128, 131073, 128
+    nb = -(-n // block)
+    k = torch.zeros((nb, heads, block, dim), dtype=torch.uint8, device="cuda")
+    v = torch.full_like(k, 0x70)  # 128
+    k[77, :, 5], v[77, :, 5] = 0x38, 0  # 1
+    ks, vs = (torch.full((nb, heads), x, device="cuda") for x in (1.0, 2.0 ** -7))
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    scale = float(np.float32(tail / dim))
+    got = host(b.fp8_kv_attention(torch.ones((1, heads, dim), device="cuda").to(torch.bfloat16), k, ks, v, vs, table,
+                                  torch.tensor([n], dtype=torch.int32, device="cuda"), scale=scale))
+    p = np.exp(-scale * dim)
+    O, v = (n - 1) * p / (1 + (n - 1) * p), 1.0
+    assert np.all(np.abs(got - O) <= 2.0 ** -8 * O + 2.0 ** -10 * O + n * 2.0 ** -36 * v)
+    assert O > 4 * n * 2.0 ** -36 * v
+
+
+@pytest.mark.parametrize("height", [2.0 ** 24, 1.7e8, 3e9])
+def test_attention_of_scores_past_fp32_s_whole_numbers(height):
+    """Scores whose spacing in FP32 is 1 to 256: the lift of p must not be lost in them.
+    Equal ones give the mean of their values, whatever they round to."""
+    dim = 64
+    c = Cache([700], 3, dim, 32, "e4m3", seed=54, spread=0)
+    c.k[:] = layer.e4m3.encode_rne_sat(np.float32(1))
+    c.ks[:] = 1
+    Q = np.full((1, 24, dim), 1.0, np.float32)
+    got, Qr = _attend(c, Q, None, height / dim, "e4m3")
+    _check(got, c, Qr, [0, 1], height / dim, "e4m3")
