@@ -27,6 +27,8 @@
 // Measured: 64 ragged sequences of up to 8192 tokens, 8 heads of 128 (584 MB) 101 us, 5.8
 // TB/s; one of 131077 with 16 rows a head (268 MB) 55 us, 4.9 TB/s, of which the start
 // takes 5 and the join of the CTAs' results 6.
+#include <cfloat>
+
 #include "common.cuh"
 #include "f8_convert.cuh"
 #include "kv_cache.cuh"
@@ -51,7 +53,7 @@ constexpr int kMinTiles = 8;
 // 99.7, 100.0, 100.3).
 constexpr int kItemCost = 16;
 constexpr int kStages = 2;  // tiles of a warp in shared memory
-constexpr float kNone = -1e30f;  // the maximum of nothing: below any score
+constexpr float kNone = -FLT_MAX;  // the maximum of nothing: not above any score
 // p is held times 2^kLift, and the running maximum may lag by 2^kLazy: FP16's largest
 // numbers are in use, so that p keeps its 11 bits down to 2^-(14 + kLift) of the largest one
 // and is lost below 2^-(25 + kLift) only (131072 tokens there are 2^-19 of the sum).  The lift

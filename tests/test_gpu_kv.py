@@ -467,3 +467,18 @@ def test_attention_of_scores_past_fp32_s_whole_numbers(height):
     Q = np.full((1, 24, dim), 1.0, np.float32)
     got, Qr = _attend(c, Q, None, height / dim, "e4m3")
     _check(got, c, Qr, [0, 1], height / dim, "e4m3")
+
+
+@pytest.mark.parametrize("lens,heads", [([37], 1), ([5, 300, 41], 2), ([37] * 60, 3)])
+@pytest.mark.parametrize("q", [-1e31, -1e36])
+def test_attention_of_very_low_scores(lens, heads, q):
+    """Scores of -1e33 and -1e38, all equal: the mean of the values, also where most
+    warps have no token."""
+    dim = 128
+    c = Cache(lens, heads, dim, 32, "e4m3", seed=55)
+    c.k[:] = layer.e4m3.encode_rne_sat(np.float32(1))
+    c.ks[:] = 1
+    Q = np.full((len(lens), heads * 2, dim), q, np.float32)
+    got, Qr = _attend(c, Q, None, 1.0, "e4m3")
+    _check(got, c, Qr, _offsets([1] * len(lens)), 1.0, "e4m3")
+    assert np.abs(got).min(axis=(1, 2)).max() > 0
