@@ -199,6 +199,39 @@ __device__ __forceinline__ void clear(State<kDim>& s) {
     for (int e = 0; e < 4; ++e) s.o[j][e] = 0.f;
 }
 
+// A tile that some rows do not see whole may hold values (or have a scale) that are not
+// finite, of tokens that some row does not see, and 0 times one is NaN.  Whether it does:
+// lane l looks at token l, if that is such a one.
+template <int kDim, bool kE5M2>
+__device__ __forceinline__ bool any_not_finite(const Stage<kDim>& x, bool mine, int lane,
+                                               const float (&vs)[2]) {
+  constexpr uint32_t kBad = kE5M2 ? 0x7c7c7c7cu : 0x7f7f7f7fu;  // of a byte that is not finite
+  uint32_t any = !(fabsf(vs[0]) <= FLT_MAX) || !(fabsf(vs[1]) <= FLT_MAX);
+  if (mine)
+#pragma unroll
+    for (int w = 0; w < kDim / 16; ++w) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&x.v[lane][(w + lane) % (kDim / 16) * 16]);
+      any |= __vcmpeq4(v.x & kBad, kBad) | __vcmpeq4(v.y & kBad, kBad) | __vcmpeq4(v.z & kBad, kBad) |
+             __vcmpeq4(v.w & kBad, kBad);
+    }
+  return __any_sync(0xffffffffu, any != 0u);
+}
+
+// Then those values become 0 for the products; mark_not_finite does the rest when the item ends.
+template <int kDim, bool kE5M2>
+__device__ __forceinline__ void hide_not_finite(Stage<kDim>& x, bool mine, int lane, float (&vs)[2]) {
+  constexpr uint32_t kBad = kE5M2 ? 0x7c7c7c7cu : 0x7f7f7f7fu;
+  if (mine) {
+    uint32_t* row = reinterpret_cast<uint32_t*>(x.v[lane]);
+#pragma unroll 1
+    for (int w = 0; w < kDim / 4; ++w) row[w] &= ~__vcmpeq4(row[w] & kBad, kBad);
+  }
+  if (!(fabsf(vs[0]) <= FLT_MAX)) vs[0] = 0.f;
+  if (!(fabsf(vs[1]) <= FLT_MAX)) vs[1] = 0.f;
+  fence_proxy_async_smem();  // the stage's next copy comes through another proxy
+  __syncwarp();
+}
+
 // One tile; limit[i][r] - tok: how many of its tokens the lane's row r of
 // fragment i sees (may be negative or past its end); least_limit: of the row that sees
 // the fewest.  fresh: the item's first tile of this warp.  there: bit h where
@@ -439,6 +472,31 @@ struct Walk {
   int first, last;    // CTAs that share it
 };
 
+// Outputs of an item that see a value, or a token of a block whose scale, that is not finite
+// among its new tokens become NaN: by a look at those tokens' codes in the cache, into
+// one warp's results.  Not inlined: few calls need it, and code that others have to jump
+// over at the end of an item is fetched line by line (131077 tokens, 16 rows: 55 us so, 62 with
+// the marks of those outputs kept in shared memory).
+template <int kDim, bool kE5M2, int kR>
+__device__ __noinline__ void mark_not_finite(const KvAttentionArgs& a, const Walk& w, float* so) {
+  constexpr int kBad = kE5M2 ? 0x7c : 0x7f;
+  const int head = w.item % a.heads, row0 = w.item / a.heads * kR;
+  const int rows = w.seq.n * a.group, first_limit = w.seq.len - w.seq.n + 1;
+  auto limit = [&](int r) { return row0 + r < rows ? first_limit + (row0 + r) / a.group : w.seq.len; };
+  const int from = max(w.s0 * kTok, max(limit(0), 0) / kTok * kTok), to = min(w.s1 * kTok, w.seq.len);
+  for (int tok = from + int(threadIdx.x) / 32; tok < to; tok += int(blockDim.x) / 32) {
+    const int blk = a.table[size_t(w.b) * a.width + (tok >> a.log_block)];
+    if (blk < 0 || blk >= a.num_blocks) continue;
+    const size_t tile = size_t(blk) * a.heads + head;
+    const uint8_t* v = a.vc + (tile * a.block + (tok & (a.block - 1))) * kDim;
+    const bool scale = !(fabsf(a.vs[tile]) <= FLT_MAX);
+    for (int d = threadIdx.x % 32; d < kDim; d += 32)
+      if (scale || (v[d] & kBad) == kBad)
+        for (int r = 0; r < kR; ++r)
+          if (tok < limit(r)) so[r * (kDim + 4) + d] = NAN;
+  }
+}
+
 // A partial result in the workspace: what a CTA knows of an item that it shares.
 template <int kDim, int kNR>
 struct Partial {
@@ -555,7 +613,7 @@ struct CacheMaps {
 //   slot 2c + 1  of an item that begins in its run and goes on
 //   counter c    CTAs done with the item that goes on past CTA c's run (left at 0)
 template <int kDim, bool kE5M2, int kNR, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) kv_attention_kernel(const KvAttentionArgs a,
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) kv_attention_kernel(const __grid_constant__ KvAttentionArgs a,
                                                                    const __grid_constant__ CacheMaps maps,
                                                                    int* counters,
                                                                    Partial<kDim, kNR>* parts,
@@ -571,11 +629,12 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
   __shared__ int last_one;
   __shared__ int gave_up;  // a wait ran out
   __shared__ uint64_t bars[kWarps][kStages];
+  __shared__ int not_finite;  // values of the item were hidden
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   Stage<kDim>* ring = reinterpret_cast<Stage<kDim>*>(shared) + warp * kStages;
 
   if (threadIdx.x == 0) {
-    gave_up = 0;
+    gave_up = not_finite = 0;
     for (int i = 0; i < kWarps * kStages; ++i) mbar_init(&bars[0][i], 1);
     fence_mbar_init();
   }
@@ -825,6 +884,13 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
         }
         phases ^= 1u << stage;
         in_flight &= ~(1u << stage);
+        if (tok + kTok > least_limit && least_limit < len) {  // the same for the warp
+          const bool mine = tok + lane >= least_limit && tok + lane < len && (there >> (lane / kFrag) & 1);
+          if (any_not_finite<kDim, kE5M2>(ring[stage], mine, lane, vs)) {
+            hide_not_finite<kDim, kE5M2>(ring[stage], mine, lane, vs);
+            not_finite = 1;
+          }
+        }
         attend_tile<kDim, kE5M2, kNR>(s, ring[stage], q, limit, least_limit, tok, there, fresh,
                                       len - tok, ks, vs, lane);
         fresh = false;
@@ -861,6 +927,11 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) k
       }
     __syncthreads();
     const Walk& done = walks[flip ^ 1];
+    if (not_finite) {
+      mark_not_finite<kDim, kE5M2, kR>(a, done, &so[0][0][0]);
+      __syncthreads();
+      if (threadIdx.x == 0) not_finite = 0;
+    }
     const bool begins = done.s0 == 0, ends = done.s1 == done.seq.tiles;
     const int out_head = done.item % a.heads, out_row0 = done.item / a.heads * kR;
     const int out_rows = done.seq.n * a.group;

@@ -557,7 +557,9 @@ int fp8_kv_append(const void* K, const void* V, int64_t ld_k, int64_t ld_v, uint
  *
  * Query i of a sequence's n new ones sees its first seq_len - n + 1 + i tokens
  * (causal; its own key is in the cache by then).  A query that sees none gives
- * zeros.  Bytes of the cache at and past seq_len are never used.  Made for
+ * zeros.  Bytes of the cache at and past seq_len are never used, and a key, value
+ * or scale that is not finite reaches only the queries that see its token (among new
+ * tokens an infinite value counts as NaN).  Made for
  * serving: one to a few new tokens per sequence over a long cache (more are
  * taken 16 rows of n * group at a time, each reading the cache anew).  Work is
  * shared out evenly over the SMs whatever the lengths; partial results and

@@ -482,3 +482,44 @@ def test_attention_of_very_low_scores(lens, heads, q):
     got, Qr = _attend(c, Q, None, 1.0, "e4m3")
     _check(got, c, Qr, _offsets([1] * len(lens)), 1.0, "e4m3")
     assert np.abs(got).min(axis=(1, 2)).max() > 0
+
+
+@pytest.mark.parametrize("dim,group,block,fmt,q,what", [
+    (*c, w) for c in ((128, 1, 16, "e4m3", 4), (64, 8, 32, "e5m2", 5), (128, 4, 64, "e4m3", 12),
+                      (128, 16, 128, "e5m2", 3), (64, 1, 16, "e4m3", 40))
+    for w in ("values", "keys", "infinite values", "scale") if c[3] == "e5m2" or w != "infinite values"])
+@pytest.mark.parametrize("B", [1, 50])
+def test_attention_hides_what_is_not_finite_from_those_before_it(dim, group, block, fmt, q, what, B):
+    """A new token whose value, key or (first of a block) scale is not finite: the
+    queries before it are what they are without it, those that see it are not finite."""
+    heads, at = 2, q // 2  # the new token concerned
+    n = 5 * block + q - at  # so that it begins a block
+    clean = Cache([n] * B, heads, dim, block, fmt, seed=60)
+    g = np.random.default_rng(61)
+    Q = g.standard_normal((B * q, heads * group, dim)).astype(np.float32)
+    want, Qr = _attend(clean, Q, None, dim ** -0.5, fmt)
+    c = Cache([n] * B, heads, dim, block, fmt, seed=60)
+    hit = [0, B // 2] if B > 1 else [0]
+    for b_ in hit:
+        blk = c.table[b_, 5]
+        if what == "values":
+            c.v[blk, 1, 0, ::3] = 0x7F if fmt == "e4m3" else 0x7E
+        elif what == "infinite values":
+            c.v[blk, 1, 0, ::3] = 0xFC
+        elif what == "keys":
+            c.k[blk, 1, 0] = 0x7F
+        else:
+            c.vs[blk, 1] = np.nan
+    got, _ = _attend(c, Q, None, dim ** -0.5, fmt)
+    got, want = (x.reshape(B, q, heads, group, dim) for x in (got, want))
+    seen = np.zeros(got.shape, bool)
+    seen[hit, at:, 1] = True
+    if "values" in what:
+        dims = np.arange(dim) % 3 == 0
+        seen &= dims
+    assert np.array_equal(got[~seen], want[~seen])
+    assert not np.isfinite(got[seen]).any()
+    if what != "infinite values":
+        cu = _offsets([q] * B)
+        O, _ = layer.kv_attention(Qr, c.k, c.ks, c.v, c.vs, c.table, c.lens, cu, dim ** -0.5, fmt)
+        assert np.array_equal(np.isnan(O).reshape(got.shape), np.isnan(got))
