@@ -594,11 +594,10 @@ class _Fast:
                                                   torch.bfloat16)
         self.f8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
         self.kind = {torch.bfloat16: 0, torch.float32: 1}  # FP8GEMM_TYPE_*
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
-            self.current = lambda t: torch.cuda.current_stream().cuda_stream
-        else:
-            self.current = lambda t: raw(t.get_device())
+        self.current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if self.current is None:
+            self.current = lambda device: torch.cuda.current_stream(device).cuda_stream
+        self.device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         L = lib()
         self.rmsnorm_quant, self.rmsnorm_backward = L.fp8_rmsnorm_quant, L.fp8_rmsnorm_backward
         self.kv_append, self.kv_attention = L.fp8_kv_append, L.fp8_kv_attention
@@ -626,10 +625,29 @@ def _codes(f, t, name, fmt):
         _u8_fmt(t, fmt, name)
 
 
-def _here(t, name):
-    """Address of a contiguous CUDA tensor."""
-    if not (t.is_cuda and t.is_contiguous()):
+def _on(f, t, name):
+    """The device of a call: its first tensor's, which has to be the current one,
+    where the library launches."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device != f.device():
+        raise ValueError(f"{name} is on cuda:{device}; the current device is cuda:{f.device()}")
+    return device
+
+
+def _at(t, name, device):
+    """Address of a tensor on that device."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is not on cuda:{device}, the device of the call")
+    return t.data_ptr()
+
+
+def _here(t, name, device):
+    """Address of a contiguous tensor on that device."""
+    if t.get_device() != device or not t.is_contiguous():
         _dev(t, name)
+        raise ValueError(f"{name} is on cuda:{t.get_device()}; the call is on cuda:{device}")
     return t.data_ptr()
 
 
@@ -674,11 +692,13 @@ def fp8_rmsnorm_quant(X, gain, eps=1e-6, residual=None, fmt="e4m3", H=None, Q=No
         rstd = f.empty(shape[:-1], dtype=f.f32, device=X.device)
     elif rstd.dtype is not f.f32 or rstd.numel() != M:
         _size(rstd, "rstd", f.f32, M)
+    device = _on(f, X, "X")
     if residual is not None:
-        r, h = _here(residual, "residual"), _here(H, "H")
-    rc = f.rmsnorm_quant(_here(X, "X"), r, kind, _here(gain, "gain"), eps, h, _here(Q, "Q"),
-                         _here(sQ, "sQ"), _here(rstd, "rstd"), M, K, code,
-                         f.current(X) if stream is None else stream.cuda_stream)
+        r, h = _here(residual, "residual", device), _here(H, "H", device)
+    rc = f.rmsnorm_quant(_here(X, "X", device), r, kind, _here(gain, "gain", device), eps, h,
+                         _here(Q, "Q", device), _here(sQ, "sQ", device),
+                         _here(rstd, "rstd", device), M, K, code,
+                         f.current(device) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_rmsnorm_quant")
     return Q, sQ, (X if residual is None else H), rstd
@@ -711,10 +731,12 @@ def fp8_rmsnorm_backward(dY, H, rstd, gain, dH=None, dX=None, dgain=None, stream
         _size(rstd, "rstd", f.f32, M)
     if gain.dtype is not f.f32 or gain.numel() != K:
         _size(gain, "gain", f.f32, K)
-    rc = f.rmsnorm_backward(_here(dY, "dY"), _here(H, "H"), kind, _here(rstd, "rstd"),
-                            _here(gain, "gain"), None if dH is None else _here(dH, "dH"),
-                            _here(dX, "dX"), _here(dgain, "dgain"), M, K,
-                            f.current(H) if stream is None else stream.cuda_stream)
+    device = _on(f, H, "H")
+    rc = f.rmsnorm_backward(_here(dY, "dY", device), _here(H, "H", device), kind,
+                            _here(rstd, "rstd", device), _here(gain, "gain", device),
+                            None if dH is None else _here(dH, "dH", device),
+                            _here(dX, "dX", device), _here(dgain, "dgain", device), M, K,
+                            f.current(device) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_rmsnorm_backward")
     return dX, dgain
@@ -727,8 +749,6 @@ def _tokens(f, t, name, T, heads, dim):
         _bf16(t, name)
     if t.shape != (T, heads, dim):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{T}, {heads}, {dim}]")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     ld, sh, sd = t.stride()
     if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"{name} must hold each token's heads contiguously")
@@ -781,13 +801,16 @@ def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
     ld_k, ld_v = _tokens(f, K, "K", T, heads, dim), _tokens(f, V, "V", T, heads, dim)
     if max_new is None:
         max_new = T if cu_new is not None else -(-T // max(B, 1))
-    rc = f.kv_append(K.data_ptr(), V.data_ptr(), ld_k, ld_v, _here(k_cache, "k_cache"),
-                     _here(k_scale, "k_scale"), _here(v_cache, "v_cache"),
-                     _here(v_scale, "v_scale"), _here(block_table, "block_table"),
-                     _here(seq_lens, "seq_lens"),
-                     None if cu_new is None else _here(cu_new, "cu_new"), T, B, heads, dim, block,
+    device = _on(f, K, "K")
+    rc = f.kv_append(K.data_ptr(), _at(V, "V", device), ld_k, ld_v,
+                     _here(k_cache, "k_cache", device), _here(k_scale, "k_scale", device),
+                     _here(v_cache, "v_cache", device), _here(v_scale, "v_scale", device),
+                     _here(block_table, "block_table", device),
+                     _here(seq_lens, "seq_lens", device),
+                     None if cu_new is None else _here(cu_new, "cu_new", device), T, B, heads,
+                     dim, block,
                      width, n, max_new, code,
-                     f.current(K) if stream is None else stream.cuda_stream)
+                     f.current(device) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_kv_append")
 
@@ -816,12 +839,16 @@ def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
         max_q = T if cu_q is not None else -(-T // max(B, 1))
     if scale is None:
         scale = dim ** -0.5
-    rc = f.kv_attention(Q.data_ptr(), ld_q, _here(k_cache, "k_cache"), _here(k_scale, "k_scale"),
-                        _here(v_cache, "v_cache"), _here(v_scale, "v_scale"),
-                        _here(block_table, "block_table"), _here(seq_lens, "seq_lens"),
-                        None if cu_q is None else _here(cu_q, "cu_q"), scale, _here(O, "O"), T, B,
+    device = _on(f, Q, "Q")
+    rc = f.kv_attention(Q.data_ptr(), ld_q, _here(k_cache, "k_cache", device),
+                        _here(k_scale, "k_scale", device), _here(v_cache, "v_cache", device),
+                        _here(v_scale, "v_scale", device),
+                        _here(block_table, "block_table", device),
+                        _here(seq_lens, "seq_lens", device),
+                        None if cu_q is None else _here(cu_q, "cu_q", device), scale,
+                        _here(O, "O", device), T, B,
                         heads, hq // heads, dim, block, width, n, max_q, code,
-                        f.current(Q) if stream is None else stream.cuda_stream)
+                        f.current(device) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_kv_attention")
     return O
@@ -868,10 +895,13 @@ def fp8_moe_few(A, sA, logits, W1, s1, W2, s2, top_k, renormalise=True, D=None, 
         weights = f.empty((T, k), dtype=f32, device=A.device)
     elif weights.dtype is not f32 or weights.shape != (T, k):
         _size(weights, "weights", f32, T * k, k)
-    rc = f.moe_few(_here(A, "A"), _here(sA, "sA"), _here(logits, "logits"), _here(W1, "W1"),
-                   _here(s1, "s1"), _here(W2, "W2"), _here(s2, "s2"), _here(D, "D"),
-                   _here(ids, "ids"), _here(weights, "weights"), T, H, I, E, k,
-                   1 if renormalise else 0, f.current(A) if stream is None else stream.cuda_stream)
+    device = _on(f, A, "A")
+    rc = f.moe_few(_here(A, "A", device), _here(sA, "sA", device),
+                   _here(logits, "logits", device), _here(W1, "W1", device),
+                   _here(s1, "s1", device), _here(W2, "W2", device), _here(s2, "s2", device),
+                   _here(D, "D", device), _here(ids, "ids", device),
+                   _here(weights, "weights", device), T, H, I, E, k, 1 if renormalise else 0,
+                   f.current(device) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_moe_few")
     return D, ids, weights
