@@ -262,3 +262,42 @@ def test_a_scale_that_underflows():
     assert host(Q)[:, :128].any() and host(s)[:, 0].all()
     W, sW = b.fp8_quant_128x128(dev(g.standard_normal((128, 384)).astype(np.float32)))
     assert bool(b.fp8gemm_dense(Q, s, W, sW).isfinite().all())
+
+
+@pytest.mark.parametrize("M,K,kind,fmt,residual", [
+    (400, 2048, "bf16", "e4m3", True), (320, 7168, "bf16", "e5m2", True), (310, 16384, "f32", "e4m3", False),
+    (305, 8208, "f32", "e4m3", True), (330, 7168, "bf16", "e4m3", False)])
+def test_forward_of_rows_in_four_chunks_a_thread(M, K, kind, fmt, residual):
+    """Rows for every SM and wide: the form that a prompt takes.  Its sum of squares is 32
+    terms in sequence in a thread, then 5 + 4 levels of additions, a division and a sum:
+    at most 43 u of itself, so rstd at most 21.5 u + 1 u = 1.4e-6: within the 2e-6 above."""
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    tX, tR, tg, X, R, gain = _inputs(M, K, kind, residual, seed=M + K)
+    _check_forward(b.fp8_rmsnorm_quant(tX, tg, EPS, residual=tR, fmt=fmt), X, R, gain, kind, fmt)
+
+
+@pytest.mark.parametrize("M,K,kind,residual", [
+    (1300, 4096, "bf16", True), (400, 16384, "f32", True), (500, 8208, "bf16", False), (1400, 2048, "f32", True),
+    (2000, 1024, "bf16", True)])
+def test_backward_of_ctas_that_take_several_rows(M, K, kind, residual):
+    """CTAs of several warps with more than one row each, in all three shapes.  dg: at
+    most 14 rows in sequence in a thread and 10 + 5 partials: below the 2^-17 above."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    tX, _, tg, X, _, gain = _inputs(M, K, kind, False, seed=M * K)
+    g = np.random.default_rng(M)
+    tdY = dev((0.1 * g.standard_normal((M, K))).astype(np.float32)).to(tX.dtype)
+    tdH = dev(g.standard_normal((M, K)).astype(np.float32)).to(tX.dtype) if residual else None
+    _, _, _, rstd = b.fp8_rmsnorm_quant(tX, tg, EPS)
+    dX, dG = b.fp8_rmsnorm_backward(tdY, tX, rstd, tg, dH=tdH)
+    dY, dH = tdY.double().cpu().numpy(), (tdH.double().cpu().numpy() if residual else None)
+    rx, rg = layer.rmsnorm_backward(dY, X, host(rstd), gain, dH)
+    r = host(rstd).astype(np.float64)[:, None]
+    terms = np.abs(r * dY * gain) + np.abs(X * r * r) * np.mean(np.abs(dY * gain * X * r), 1, keepdims=True)
+    if residual:
+        terms = terms + np.abs(dH)
+    bound = 2.0 ** -18 * terms + (2.0 ** -8 * np.abs(rx) if kind == "bf16" else 0)
+    assert np.all(np.abs(dX.double().cpu().numpy() - rx) <= bound)
+    assert np.all(np.abs(host(dG) - rg) <= 2.0 ** -17 * np.sum(np.abs(dY * X * r), 0))
+    dX2, dG2 = b.fp8_rmsnorm_backward(tdY, tX, rstd, tg, dH=tdH)
+    assert torch.equal(dX, dX2) and torch.equal(dG, dG2)
