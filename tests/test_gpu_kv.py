@@ -418,17 +418,24 @@ def test_attention_keeps_the_smaller_of_two_scales(dim, group, fmt, apart):
 
 @pytest.mark.parametrize("dim", [64, 128])
 def test_attention_over_falling_scales(dim):
-    """Value scales 1, 2^-59 and 2^-118 along a sequence, 384 tokens each in turn, so
-    that warps meet them one after the other: finite throughout."""
-    n = 60000
-    c = Cache([n], 1, dim, 32, "e4m3", seed=51, spread=0)
-    for j in range(c.width):
-        c.vs[c.table[0, j]] = np.float32(2.0 ** (-59 * (j // 12 % 3)))
-    g = np.random.default_rng(52)
-    Q = g.standard_normal((1, 2, dim)).astype(np.float32)
-    got, Qr = _attend(c, Q, None, dim ** -0.5, "e4m3")
-    assert np.isfinite(got).all()
-    _check(got, c, Qr, [0, 1], dim ** -0.5, "e4m3")
+    """Value scales 1, 2^-59 and 2^-118 along a sequence, 384 tokens each in turn and
+    long enough for a warp to meet all three one after the other: finite throughout."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    n, block = 150000, 32
+    nb = -(-n // block)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(51)
+    k, v = (torch.randint(lo, 0x7F, (nb, 1, block, dim), generator=g, dtype=torch.uint8, device="cuda") for lo in (0, 0x60))
+    ks = torch.full((nb, 1), 2.0 ** -7, device="cuda")
+    vs = torch.exp2(-59.0 * (torch.arange(nb, device="cuda") // 12 % 3))[:, None]
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    q = (0.01 * torch.randn((1, 2, dim), generator=g, device="cuda")).to(torch.bfloat16)
+    got = b.fp8_kv_attention(q, k, ks, v, vs, table, torch.tensor([n], dtype=torch.int32, device="cuda")).double()
+    deq = lambda c, s: (c.view(torch.float8_e4m3fn).double() * s.double()[..., None, None]).view(-1, dim)[:n]  # noqa: E731
+    p = torch.softmax(q[0].double() @ deq(k, ks).t() * dim ** -0.5, 1)
+    O = p @ deq(v, vs)  # values are positive: O is its own sum of magnitudes
+    assert bool(((got[0] - O).abs() <= (2.0 ** -8 + 2.0 ** -10) * O + n * 2.0 ** -36 * 448).all())
 
 
 @pytest.mark.parametrize("tail", [18.4, 14.0, 20.8])
