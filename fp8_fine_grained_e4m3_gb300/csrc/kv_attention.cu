@@ -18,15 +18,16 @@
 // fragment's k index such that a lane's share of a key is 16 neighbouring bytes, and the
 // output dimension to V^T's rows such that a lane's share of a value is too.
 // FP8 codes are exact in FP16; q is shifted by a power of two per row to use
-// FP16's range (BF16 has fewer mantissa bits); p is rounded to FP16 (11
-// bits where it is 2^-25 of the largest or more, the BF16 output has 8).  Scores, statistics, sums and the
-// output accumulate in FP32; a tile's scales are applied to its FP32 products, the
+// FP16's range (BF16 has fewer mantissa bits); p is rounded to FP16 (11 bits where it
+// is 2^-25 of the largest or more; the BF16 output has 8).  Scores, statistics, sums and
+// the output accumulate in FP32; a tile's scales are applied to its FP32 products, the
 // values' as they are added to O: a scale inside p would take p out of FP16's range
 // where neighbouring blocks' scales differ (64 ragged sequences with 8 rows a head: 100 us
-// either way; 32 rows, which the products bound: 195 with the scale in p, 210 so).
-// Measured: 64 ragged sequences of up to 8192 tokens, 8 heads of 128 (584 MB) 101 us, 5.8
+// either way; 32 rows, which the products bound: 195 with the scale in p, 208 so).
+// Measured: 64 ragged sequences of up to 8192 tokens, 8 heads of 128 (584 MB) 100 us, 5.8
 // TB/s; one of 131077 with 16 rows a head (268 MB) 55 us, 4.9 TB/s, of which the start
-// takes 5 and the join of the CTAs' results 6.
+// takes 5 and the join of the CTAs' results 6.  Past 16 rows a head conversions and
+// products bind (64 sequences with 32 rows: 208 us).
 #include <cfloat>
 
 #include "common.cuh"
@@ -401,7 +402,7 @@ __device__ __forceinline__ void write_out(const KvAttentionArgs& a, int t0, int 
 // as often where a sequence may have more than 8 rows per cached head (131077 tokens, 16
 // rows: 66 us with one, 55 with two); for up to 8 the second would be idle work (64
 // sequences, 8 rows: 101 us with one, 112 with two).  More rows take further passes:
-// the products bound those already (64 of up to 8192 tokens: 101 us for 8 rows, 206 for 32).
+// the products bound those already (64 of up to 8192 tokens: 100 us for 8 rows, 208 for 32).
 int row_fragments(const KvAttentionArgs& a) { return (long long)a.max_q * a.group > kRows ? 2 : 1; }
 
 // Warps of a CTA.  With many items each SM has three CTAs of four, whose starts

@@ -515,6 +515,8 @@ int fp8_rmsnorm_backward(const void* dY, const void* H, int x_type, const float*
  *                     cu[b + 1] - 1, at most max_new (max_q) of them.  NULL: T / B each
  *                     (T % B == 0).
  *   dim is 64 or 128; block 16, 32, 64 or 128; heads counts the cached heads.
+ *   num_blocks * heads * block below 2^31, B at most 32767, heads (for the
+ *   attention heads * group) at most 65535: FP8GEMM_ERR_SHAPE past that.
  *
  * The launch depends on host sizes only, so a captured graph can be replayed
  * with new lengths and tables.  A length outside 0 .. block * table_width (or
@@ -618,7 +620,8 @@ int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const ui
  * returned here or left for the next read.  On FP8GEMM_ERR_TIMEOUT the call
  * also synchronises the device and frees every library workspace of it (a
  * launch that gave up can leave a split-K reduction's counters mid-count);
- * the next calls allocate fresh, zeroed ones.  Returns FP8GEMM_OK, or
+ * the next calls allocate fresh, zeroed ones, and a graph that captured calls
+ * with a workspace has to be captured again.  Returns FP8GEMM_OK, or
  * FP8GEMM_ERR_NULL / FP8GEMM_ERR_LAUNCH if `out` is NULL or the CUDA calls
  * fail.
  */
