@@ -182,8 +182,8 @@ __device__ __forceinline__ void take_queries(Queries<kDim>& q, const RawQuery<kD
   q.mul[1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
 }
 
-// Running softmax of a lane's two rows and its share of O^T: o[j] holds dimensions (dim/8) g + 2j (rows 2t, 2t + 1)
-// and + 1 (rows 2t, 2t + 1).
+// Running softmax of a lane's two rows and its share of O^T: o[j] holds dimensions
+// (dim/8) g + 2j (rows 2t, 2t + 1) and + 1 (rows 2t, 2t + 1).
 template <int kDim>
 struct State {
   float m[2], l[2];  // l: this lane's tokens only, times 2^kLift
@@ -242,8 +242,8 @@ template <int kDim, bool kE5M2, int kNR>
 __device__ __forceinline__ void attend_tile(State<kDim> (&s)[kNR],
                                             const Stage<kDim>& x, const Queries<kDim> (&q)[kNR],
                                             const int (&limit)[kNR][2], int least_limit, int tok,
-                                            uint32_t there, bool fresh, int valid, const float (&ks)[2], const float (&vs)[2],
-                                            int lane) {
+                                            uint32_t there, bool fresh, int valid,
+                                            const float (&ks)[2], const float (&vs)[2], int lane) {
   const int g = lane / 4, t = lane % 4;
   float c[2][kNR][4] = {};
 #pragma unroll
@@ -614,11 +614,10 @@ struct CacheMaps {
 //   slot 2c + 1  of an item that begins in its run and goes on
 //   counter c    CTAs done with the item that goes on past CTA c's run (left at 0)
 template <int kDim, bool kE5M2, int kNR, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR)) kv_attention_kernel(const __grid_constant__ KvAttentionArgs a,
-                                                                   const __grid_constant__ CacheMaps maps,
-                                                                   int* counters,
-                                                                   Partial<kDim, kNR>* parts,
-                                                                   int* status) {
+__global__ void __launch_bounds__(32 * kWarps, ctas_per_sm(kWarps, kDim, kNR))
+    kv_attention_kernel(const __grid_constant__ KvAttentionArgs a,
+                        const __grid_constant__ CacheMaps maps, int* counters,
+                        Partial<kDim, kNR>* parts, int* status) {
   constexpr int kR = kRows * kNR;
   constexpr bool kWholeItems = kWarps > 4;
   extern __shared__ unsigned char raw[];
