@@ -65,6 +65,10 @@ SIGNATURES = [
      [_P, _P, _L, _L, _P, _P, _P, _P, _P, _P, _P, *[_I] * 9, _P]),
     ("fp8_kv_attention", _I,
      [_P, _L, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, *[_I] * 10, _P]),
+    ("fp8gemm_gated", _I, [_P, _P, _I, _P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P]),
+    ("fp8gemm_gated_backward", _I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _P]),
+    ("fp8_rope", _I,
+     [_P, _L, _P, _L, _I, _P, _L, _P, _L, _P, _P, _P, _P, ctypes.c_float, *[_I] * 8, _P]),
     ("fp8_moe_few", _I, [*[_P] * 10, *[_I] * 6, _P]),
     ("fp8gemm_get_device_status", _I, [_P, ctypes.POINTER(ctypes.c_int)]),
     ("fp8gemm_strerror", ctypes.c_char_p, [_I]),
@@ -601,7 +605,8 @@ class _Fast:
         L = lib()
         self.rmsnorm_quant, self.rmsnorm_backward = L.fp8_rmsnorm_quant, L.fp8_rmsnorm_backward
         self.kv_append, self.kv_attention = L.fp8_kv_append, L.fp8_kv_attention
-        self.moe_few = L.fp8_moe_few
+        self.moe_few, self.rope = L.fp8_moe_few, L.fp8_rope
+        self.gated, self.gated_backward = L.fp8gemm_gated, L.fp8gemm_gated_backward
 
 
 def _lookup():
@@ -742,11 +747,14 @@ def fp8_rmsnorm_backward(dY, H, rstd, gain, dH=None, dX=None, dgain=None, stream
     return dX, dgain
 
 
-def _tokens(f, t, name, T, heads, dim):
-    """bf16 [T, heads, dim] whose tokens may lie apart (parts of the rows of a
-    fused projection's output): returns the token stride in elements."""
-    if t.dtype is not f.bf16:
-        _bf16(t, name)
+def _tokens(f, t, name, T, heads, dim, dtype=None):
+    """bf16 (or `dtype`) [T, heads, dim] whose tokens may lie apart (parts of the rows
+    of a fused projection's output): returns the token stride in elements."""
+    if dtype is None:
+        if t.dtype is not f.bf16:
+            _bf16(t, name)
+    elif t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (T, heads, dim):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{T}, {heads}, {dim}]")
     ld, sh, sd = t.stride()
@@ -852,6 +860,151 @@ def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
     if rc:
         _check(rc, "fp8_kv_attention")
     return O
+
+
+def _gated_operands(f, A, sA, W, sW, a_fmt, b_fmt, rows, names):
+    """Checks A [M, K] and W [rows a multiple of `rows`, K] with their scales: M, K, I."""
+    a, w = A.shape, W.shape
+    if len(a) != 2 or len(w) != 2 or w[1] != a[1] or w[0] % rows != 0:
+        raise ValueError(f"{names[0]} {tuple(a)} / {names[2]} {tuple(w)}: the call needs [M, K] and"
+                         f" [{'2 I' if rows == 2 else 'I'}, K]")
+    M, K = a
+    _codes(f, A, names[0], a_fmt)
+    _codes(f, W, names[2], b_fmt)
+    Kb, Nb = -(-K // 128), -(-w[0] // 128)
+    if sA.dtype is not f.f32 or sA.shape != (M, Kb):
+        _size(sA, names[1], f.f32, M * Kb, Kb)
+    if sW.dtype is not f.f32 or sW.shape != (Nb, Kb):
+        _size(sW, names[3], f.f32, Nb * Kb, Kb)
+    return M, K, w[0] // rows
+
+
+def _codes_out(f, Q, sQ, fmt, M, N, device):
+    """Codes [M, N] and their scales, given or new."""
+    Nb = -(-N // 128)
+    if Q is None:
+        Q = f.empty((M, N), dtype=f.u8, device=device)
+    else:
+        _codes(f, Q, "Q", fmt)
+        if Q.shape != (M, N):
+            _need(Q, "Q", M * N, N)
+    if sQ is None:
+        sQ = f.empty((M, Nb), dtype=f.f32, device=device)
+    elif sQ.dtype is not f.f32 or sQ.shape != (M, Nb):
+        _size(sQ, "sQ", f.f32, M * Nb, Nb)
+    return Q, sQ
+
+
+def fp8gemm_gated(A, sA, W1, s1, a_fmt="e4m3", b_fmt="e4m3", fmt="e4m3", GU=None, Q=None, sQ=None,
+                  stream=None):
+    """h = silu(A Wg^T) (A Wu^T) with 1x128 codes in one kernel: A u8 [M, K], sA f32
+    [M, ceil(K/128)], W1 u8 [2 I, K] (gate rows, then up rows), s1 f32 [ceil(2 I/128),
+    ceil(K/128)] -> (Q u8 [M, I] of `fmt`, sQ f32 [M, ceil(I/128)]).  GU bf16 [M, 2 I]: also
+    gets gate and up values, for fp8gemm_gated_backward."""
+    f = _fast or _lookup()
+    codes = _fmt(a_fmt), _fmt(b_fmt), _fmt(fmt)
+    M, K, I = _gated_operands(f, A, sA, W1, s1, a_fmt, b_fmt, 2, ("A", "sA", "W1", "s1"))
+    Q, sQ = _codes_out(f, Q, sQ, fmt, M, I, A.device)
+    if GU is not None and (GU.dtype is not f.bf16 or GU.shape != (M, 2 * I)):
+        _size(GU, "GU", f.bf16, M * 2 * I, 2 * I)
+    device = _on(f, A, "A")
+    rc = f.gated(_here(A, "A", device), _here(sA, "sA", device), codes[0], _here(W1, "W1", device),
+                 _here(s1, "s1", device), codes[1], _here(Q, "Q", device), _here(sQ, "sQ", device),
+                 codes[2], None if GU is None else _here(GU, "GU", device), M, I, K,
+                 f.current(device) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "fp8gemm_gated")
+    return Q, sQ
+
+
+def fp8gemm_gated_backward(dY, sdY, W2T, s2T, GU, a_fmt="e5m2", b_fmt="e4m3", fmt="e5m2", dGU=None,
+                           Q=None, sQ=None, stream=None):
+    """Gradients of fp8gemm_gated's gate and up values, quantised: dY u8 [M, K] of
+    a_fmt (the gradient of the block's output), W2T u8 [I, K] (the down weight, transposed),
+    GU bf16 [M, 2 I] -> (Q u8 [M, 2 Ip] of `fmt`, sQ f32 [M, 2 Ip/128]), Ip = I up to a multiple
+    of 128: dgate in columns 0 .. I - 1, dup from column Ip on, zeros elsewhere.  dGU bf16
+    [M, 2 I]: also gets both gradients."""
+    f = _fast or _lookup()
+    codes = _fmt(a_fmt), _fmt(b_fmt), _fmt(fmt)
+    M, K, I = _gated_operands(f, dY, sdY, W2T, s2T, a_fmt, b_fmt, 1, ("dY", "sdY", "W2T", "s2T"))
+    if GU.dtype is not f.bf16 or GU.shape != (M, 2 * I):
+        _size(GU, "GU", f.bf16, M * 2 * I, 2 * I)
+    Q, sQ = _codes_out(f, Q, sQ, fmt, M, 2 * (-(-I // 128) * 128), dY.device)
+    if dGU is not None and (dGU.dtype is not f.bf16 or dGU.shape != (M, 2 * I)):
+        _size(dGU, "dGU", f.bf16, M * 2 * I, 2 * I)
+    device = _on(f, dY, "dY")
+    rc = f.gated_backward(_here(dY, "dY", device), _here(sdY, "sdY", device), codes[0],
+                          _here(W2T, "W2T", device), _here(s2T, "s2T", device), codes[1],
+                          _here(GU, "GU", device), _here(Q, "Q", device), _here(sQ, "sQ", device),
+                          codes[2], None if dGU is None else _here(dGU, "dGU", device), M, I, K,
+                          f.current(device) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "fp8gemm_gated_backward")
+    return Q, sQ
+
+
+def fp8_rope(Q, K, freq, positions=None, seq_lens=None, cu=None, interleaved=False, amplitude=1.0,
+             backward=False, Qo=None, Ko=None, stream=None):
+    """Rotary positions: Q bf16 or f32 [T, heads_q, dim], K the same with heads_k (None:
+    no keys), tokens may lie apart; freq f32 [rot / 2] radians a position (rotary.frequencies
+    makes it) -> (Qo, Ko).  positions i32 [T], or seq_lens i32 [B] and cu as
+    fp8_kv_append's (None: T / B each).  Qo=Q, Ko=K turns them in place.  backward:
+    Q and K are gradients of the outputs, Qo and Ko those of the inputs."""
+    f = _fast or _lookup()
+    dtype = Q.dtype
+    kind = f.kind.get(dtype)
+    if kind is None:
+        raise TypeError(f"Q must be bfloat16 or float32, got {dtype}")
+    if Q.dim() != 3:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}; the call needs [T, heads, dim]")
+    T, hq, dim = Q.shape
+    rot = 2 * freq.numel()
+    if freq.dtype is not f.f32:
+        _size(freq, "freq", f.f32, rot // 2)
+    if (positions is None) == (seq_lens is None):
+        raise ValueError("give either positions or seq_lens")
+    B = 0
+    if positions is not None:
+        if cu is not None:
+            raise ValueError("cu goes with seq_lens: positions has one entry for each token")
+        if positions.dtype is not f.i32 or positions.numel() != T:
+            _size(positions, "positions", f.i32, T)
+    else:
+        B = seq_lens.numel()
+        if seq_lens.dtype is not f.i32:
+            _size(seq_lens, "seq_lens", f.i32, B)
+        if cu is None:
+            if B > 0 and T % B != 0:
+                raise ValueError(f"{T} tokens for {B} sequences: give the offsets")
+        elif cu.dtype is not f.i32 or cu.numel() != B + 1:
+            _size(cu, "the offsets", f.i32, B + 1)
+    ld_q = _tokens(f, Q, "Q", T, hq, dim, dtype)
+    if Qo is None:
+        Qo = f.empty(Q.shape, dtype=dtype, device=Q.device)
+    ld_qo = ld_q if Qo is Q else _tokens(f, Qo, "Qo", T, hq, dim, dtype)
+    hk = ld_k = ld_ko = 0
+    if K is not None:
+        if K.dim() != 3:
+            raise ValueError(f"K has shape {tuple(K.shape)}; the call needs [{T}, heads, {dim}]")
+        hk = K.size(1)
+        ld_k = _tokens(f, K, "K", T, hk, dim, dtype)
+        if Ko is None:
+            Ko = f.empty(K.shape, dtype=dtype, device=K.device)
+        ld_ko = ld_k if Ko is K else _tokens(f, Ko, "Ko", T, hk, dim, dtype)
+    elif Ko is not None:
+        raise ValueError("Ko without K")
+    device = _on(f, Q, "Q")
+    rc = f.rope(Q.data_ptr(), ld_q, None if K is None else _at(K, "K", device), ld_k, kind,
+                _at(Qo, "Qo", device), ld_qo, None if K is None else _at(Ko, "Ko", device), ld_ko,
+                _here(freq, "freq", device),
+                None if positions is None else _here(positions, "positions", device),
+                None if seq_lens is None else _here(seq_lens, "seq_lens", device),
+                None if cu is None else _here(cu, "cu", device), amplitude, T, B, hq, hk, dim, rot,
+                1 if interleaved else 0, 1 if backward else 0,
+                f.current(device) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "fp8_rope")
+    return Qo, Ko
 
 
 def fp8_moe_few(A, sA, logits, W1, s1, W2, s2, top_k, renormalise=True, D=None, ids=None,

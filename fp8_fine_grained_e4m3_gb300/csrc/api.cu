@@ -5,6 +5,7 @@
 // checking and configuration on the host, so the kernel only loops; section
 // 6.3, first point: TMA wants 16-byte aligned addresses and strides).
 #include <atomic>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -672,6 +673,75 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
   if (int r = workspace_on(c.dev, c.ctx, stream, kv_attention_workspace_bytes(c), &ws, kWsAttention))
     return r;
   return finish(launch_kv_attention(c, a, ws), 1);
+}
+
+// What the gated products' two calls have in common (rows of B: 2 I or I).
+static int check_gated(int M, int I, int K, int a_fmt, int b_fmt, int q_fmt) {
+  if (int r = check_common(M, I, K)) return r;
+  if (I == 0 || I % kKAlign != 0 || I > (1 << 29)) return FP8GEMM_ERR_SHAPE;
+  if ((long long)ceil_div(M, kBlockM) * ceil_div(I, kBlockK) > 0x3fffffffLL) return FP8GEMM_ERR_SHAPE;
+  if (!valid_fmt(a_fmt) || !valid_fmt(b_fmt) || !valid_fmt(q_fmt)) return FP8GEMM_ERR_FORMAT;
+  return FP8GEMM_OK;
+}
+
+int fp8gemm_gated(const uint8_t* A, const float* sA, int a_fmt, const uint8_t* W1, const float* s1,
+                  int b_fmt, uint8_t* Q, float* sQ, int q_fmt, void* GU, int M, int I, int K,
+                  fp8gemm_stream_t stream) {
+  if (int r = check_gated(M, I, K, a_fmt, b_fmt, q_fmt)) return r;
+  if (M == 0) return FP8GEMM_OK;
+  if (!A || !sA || !W1 || !s1 || !Q || !sQ) return FP8GEMM_ERR_NULL;
+  if (!aligned16(A) || !aligned16(sA) || !aligned16(W1) || !aligned16(s1) || !aligned16(Q) ||
+      !aligned16(sQ) || !aligned16(GU))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const GatedArgs a{A, sA, W1, s1, Q, sQ, static_cast<__nv_bfloat16*>(GU), nullptr, M, I, K, a_fmt,
+                    b_fmt, q_fmt};
+  return finish(launch_gemm_gated(c, a), 1);
+}
+
+int fp8gemm_gated_backward(const uint8_t* dY, const float* sdY, int a_fmt, const uint8_t* W2T,
+                           const float* s2T, int b_fmt, const void* GU, uint8_t* Q, float* sQ,
+                           int q_fmt, void* dGU, int M, int I, int K, fp8gemm_stream_t stream) {
+  if (int r = check_gated(M, I, K, a_fmt, b_fmt, q_fmt)) return r;
+  if (M == 0) return FP8GEMM_OK;
+  if (!dY || !sdY || !W2T || !s2T || !GU || !Q || !sQ) return FP8GEMM_ERR_NULL;
+  if (!aligned16(dY) || !aligned16(sdY) || !aligned16(W2T) || !aligned16(s2T) || !aligned16(GU) ||
+      !aligned16(Q) || !aligned16(sQ) || !aligned16(dGU))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const GatedArgs a{dY, sdY, W2T, s2T, Q, sQ, static_cast<__nv_bfloat16*>(const_cast<void*>(GU)),
+                    static_cast<__nv_bfloat16*>(dGU), M, I, K, a_fmt, b_fmt, q_fmt};
+  return finish(launch_gemm_gated_backward(c, a), 1);
+}
+
+int fp8_rope(const void* Q, int64_t ld_q, const void* K, int64_t ld_k, int x_type, void* Qo,
+             int64_t ld_qo, void* Ko, int64_t ld_ko, const float* freq, const int32_t* positions,
+             const int32_t* seq_lens, const int32_t* cu, float amplitude, int T, int B, int heads_q,
+             int heads_k, int dim, int rot, int interleaved, int backward, fp8gemm_stream_t stream) {
+  if (T < 0 || B < 0 || heads_q < 0 || heads_k < 0 || heads_q > 65535 || heads_k > 65535)
+    return FP8GEMM_ERR_SHAPE;
+  if (dim <= 0 || dim % 16 != 0 || dim > kMaxRopeDim || rot <= 0 || rot % 16 != 0 || rot > dim)
+    return FP8GEMM_ERR_SHAPE;
+  if (x_type != FP8GEMM_TYPE_BF16 && x_type != FP8GEMM_TYPE_F32) return FP8GEMM_ERR_FORMAT;
+  if (!positions && !cu && B > 0 && T % B != 0) return FP8GEMM_ERR_SHAPE;
+  if (T == 0 || heads_q + heads_k == 0 || (!positions && B == 0)) return FP8GEMM_OK;
+  for (int64_t ld : {heads_q ? ld_q : int64_t(0), heads_q ? ld_qo : int64_t(0)})
+    if (ld % 8 != 0 || ld < int64_t(heads_q) * dim) return FP8GEMM_ERR_SHAPE;
+  for (int64_t ld : {heads_k ? ld_k : int64_t(0), heads_k ? ld_ko : int64_t(0)})
+    if (ld % 8 != 0 || ld < int64_t(heads_k) * dim) return FP8GEMM_ERR_SHAPE;
+  if (!freq || (heads_q && (!Q || !Qo)) || (heads_k && (!K || !Ko)) || (!positions && !seq_lens))
+    return FP8GEMM_ERR_NULL;
+  if ((heads_q && (!aligned16(Q) || !aligned16(Qo))) || (heads_k && (!aligned16(K) || !aligned16(Ko))) ||
+      !aligned4(freq) || !aligned4(positions) || !aligned4(seq_lens) || !aligned4(cu))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const RopeArgs a{Q, K, Qo, Ko, ld_q, ld_k, ld_qo, ld_ko, freq, positions, seq_lens, cu, amplitude,
+                   T, B, heads_q, heads_k, dim, rot, x_type == FP8GEMM_TYPE_F32, interleaved != 0,
+                   backward != 0};
+  return finish(launch_rope(c, a), 1);
 }
 
 int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,

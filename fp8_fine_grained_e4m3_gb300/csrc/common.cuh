@@ -181,6 +181,42 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace_bytes(const LaunchCtx& c);
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws);
 
+// The gated feed-forward products (gemm_gated.cu).
+struct GatedArgs {
+  const uint8_t* A;  // [M, K]: activations, or dY
+  const float* sA;
+  const uint8_t* B;  // W1 [2 I, K], or W2 transposed [I, K]
+  const float* sB;
+  uint8_t* Q;        // codes of h [M, I], or of its gradients [M, 2 Ip]
+  float* sQ;
+  __nv_bfloat16* GU;   // gate and up values [M, 2 I]: an output (or null), or the gradient's input
+  __nv_bfloat16* dGU;  // their gradients [M, 2 I], or null
+  int M, I, K, a_fmt, b_fmt, q_fmt;
+  int split = 1;
+  unsigned long long wait_ns = 0;
+};
+cudaError_t launch_gemm_gated(const LaunchCtx& c, const GatedArgs& a);
+cudaError_t launch_gemm_gated_backward(const LaunchCtx& c, const GatedArgs& a);
+
+// Rotary positions (rope.cu).
+constexpr int kMaxRopeDim = 512;
+
+struct RopeArgs {
+  const void* Q;  // [T, heads_q, dim], ld_* elements from token to token
+  const void* K;
+  void* Qo;
+  void* Ko;
+  long long ld_q, ld_k, ld_qo, ld_ko;
+  const float* freq;     // [rot / 2]
+  const int* positions;  // [T], or null: from lens and cu
+  const int* lens;       // [B]
+  const int* cu;         // [B + 1], or null: T / B each
+  float amplitude;
+  int T, B, heads_q, heads_k, dim, rot;
+  bool f32, interleaved, backward;
+};
+cudaError_t launch_rope(const LaunchCtx& c, const RopeArgs& a);
+
 // The mixture-of-experts layer for a few tokens (moe_few.cu).
 struct MoeArgs {
   const uint8_t* A;   // [T, H]

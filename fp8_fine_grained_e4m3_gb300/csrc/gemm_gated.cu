@@ -1,0 +1,657 @@
+// gemm_gated.cu -- the gated feed-forward block's FP8 products with what follows them in one
+// kernel, and its gradient.
+//
+// Forward   u = A W1^T (gate rows, then up rows; block scales as in gemm_tc.cu)
+//           h = silu(u_gate) u_up,  one scale and FP8 codes per 1x128 block of h
+// Backward  dh = dY W2 (as dY W2T^T),  s = 1 / (1 + e^-g) of the kept gate g and up u:
+//           dg = dh u s (1 + g (1 - s)),  du = dh g s,  codes of both per 1x128 block
+//
+// The products are those of gemm_tc.cu -- operands by TMA into a ring, one tcgen05
+// contraction per 128-wide K block into one of two TMEM buffers, each block's partial
+// promoted with its scale product into FP32 registers -- and the same CTA layout (384
+// threads; see there).  What differs is which columns meet in a thread:
+//   forward   a tile is 128 rows of 128 columns of h: its 256 accumulator columns are
+//             gate 0-63, up 0-63, gate 64-127, up 64-127 (four boxes of W1's rows a K
+//             block), so that each promotion thread holds 64 gate values and the up values
+//             of the same columns, and a row's maximum is one exchange between two threads
+//   backward  256 columns of dh: each promotion thread holds one whole 1x128 block of a row
+// so the activations never leave the chip in 16 or 32 bits.
+//
+// Bound by the tensor cores and the promotion for prompts, by the weights' bytes for a few
+// tokens: then all tiles fit in one wave, and each is split along K over a cluster (as in
+// gemm_tc.cu), whose CTAs share the rows of the epilogue.
+#include "common.cuh"
+#include "f8_convert.cuh"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace fp8gemm {
+namespace {
+
+constexpr int kGroupM = 16;  // M blocks per rasterisation group
+constexpr int kBN = 256;     // accumulator columns of a tile
+constexpr int kStages = 4;
+constexpr int kPromoWarps = 8;
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;
+// 65536 / 384 -> 168 registers at launch; 128 * 72 + 256 * 216 = 384 * 168
+constexpr uint32_t kLowRegs = 72, kHighRegs = 216;
+constexpr int kABytes = kBlockM * kBlockK, kBBytes = kBN * kBlockK;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kPitch = kBN + 4;  // floats of a staged row (split tiles)
+constexpr size_t kSmemBytes = 1024 + size_t(kStages) * kStageBytes + 2 * 2 * kBlockM * 4 + 512;
+static_assert(kSmemBytes <= 232448, "227 KB of shared memory per CTA");
+static_assert(size_t(kBlockM) * kPitch * 4 <= size_t(kStages) * kStageBytes, "staging fits the ring");
+static_assert(128 * kLowRegs + 256 * kHighRegs <= 384 * 168, "register split");
+
+// Columns of h (or dh) of a tile.
+template <bool kGrad>
+__host__ __device__ constexpr int tile_cols() {
+  return kGrad ? kBN : kBN / 2;
+}
+
+struct GatedTile {
+  int row0, rows, col0;  // first row, rows that exist, first column of h
+};
+
+template <bool kGrad>
+__device__ __forceinline__ GatedTile gated_tile(const GatedArgs& a, int t) {
+  const int num_n = ceil_div(a.I, tile_cols<kGrad>()), num_m = ceil_div(a.M, kBlockM);
+  const int per_group = kGroupM * num_n;
+  const int first_m = t / per_group * kGroupM, gs = min(kGroupM, num_m - first_m);
+  const int r = t % per_group;
+  GatedTile w;
+  w.row0 = (first_m + r % gs) * kBlockM;
+  w.rows = min(kBlockM, a.M - w.row0);
+  w.col0 = r / gs * tile_cols<kGrad>();
+  return w;
+}
+
+// e^-x, to FP32's rounding (relative error 2^-22 and x's own).
+__device__ __forceinline__ float exp_minus(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * -1.4426950408889634f));
+  return r;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + exp_minus(g)) * u; }
+
+// dg and du of one element.
+__device__ __forceinline__ float2 swiglu_grad(float dh, float g, float u) {
+  const float s = __fdividef(1.f, 1.f + exp_minus(g));
+  return make_float2(dh * (u * (s * fmaf(g, 1.f - s, 1.f))), dh * (g * s));
+}
+
+// Sixteen values to codes of one scale, stored at p.
+template <bool kE5M2>
+__device__ __forceinline__ void store_codes16(uint8_t* p, const float (&v)[16], const Reciprocal& s) {
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = v[i];
+    b[i] = v[8 + i];
+  }
+  const uint2 x = quant8<kE5M2>(a, s), y = quant8<kE5M2>(b, s);
+  *reinterpret_cast<uint4*>(p) = make_uint4(x.x, x.y, y.x, y.y);
+}
+
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t codes4(const float (&v)[4], const Reciprocal& s) {
+  const float4 x = make_float4(v[0], v[1], v[2], v[3]);
+  if (s.safe) return quant4<kE5M2>(x, s);
+  return s.s == 0.f ? 0u : quant4<kE5M2>(x, s.s);
+}
+
+__device__ __forceinline__ float warp_max_nan(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ---- whole tiles: a thread's 64 columns of h (acc: 64 gate, 64 up values)
+template <bool kE5M2>
+__device__ __forceinline__ void store_h(const GatedArgs& a, const float2 (&acc)[64], int row, int col,
+                                        float scale) {
+  const Reciprocal s = reciprocal(scale);
+  uint8_t* q = a.Q + size_t(row) * a.I + col;
+#pragma unroll
+  for (int c = 0; c < 64; c += 16) {
+    if (col + c >= a.I) break;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = acc[c / 2 + i].x;
+      v[2 * i + 1] = acc[c / 2 + i].y;
+    }
+    store_codes16<kE5M2>(q + c, v, s);
+  }
+}
+
+// ---- whole tiles: a thread's 128 columns of dh; the block's maxima first, then the codes
+// (the gradients of 128 columns do not fit in registers beside dh, so they are formed twice)
+template <bool kE5M2>
+__device__ __forceinline__ void store_dgu(const GatedArgs& a, const float2 (&acc)[64], int row, int col) {
+  const __nv_bfloat16* g = a.GU + size_t(row) * 2 * a.I + col;
+  const int Ip = ceil_div(a.I, kBlockK) * kBlockK;
+  float top_g = 0.f, top_u = 0.f;
+#pragma unroll
+  for (int c = 0; c < 128; c += 8) {
+    if (col + c >= a.I) break;
+    float gv[8], uv[8];
+    unpack8(load8(g + c), gv);
+    unpack8(load8(g + a.I + c), uv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float dh = i % 2 ? acc[(c + i) / 2].y : acc[(c + i) / 2].x;
+      const float2 d = swiglu_grad(dh, gv[i], uv[i]);
+      top_g = max_nan(top_g, fabsf(d.x));
+      top_u = max_nan(top_u, fabsf(d.y));
+    }
+  }
+  const Reciprocal sg = reciprocal(block_scale<kE5M2>(top_g)), su = reciprocal(block_scale<kE5M2>(top_u));
+  float* sq = a.sQ + size_t(row) * (2 * Ip / kBlockK) + col / kBlockK;
+  sq[0] = sg.s;
+  sq[Ip / kBlockK] = su.s;
+  uint8_t* q = a.Q + size_t(row) * 2 * Ip + col;
+  __nv_bfloat16* o = a.dGU ? a.dGU + size_t(row) * 2 * a.I + col : nullptr;
+#pragma unroll
+  for (int c = 0; c < 128; c += 16) {
+    float dg[16], du[16];
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+      float gv[8] = {}, uv[8] = {};
+      if (col + c < a.I) {
+        unpack8(load8(g + c + e), gv);
+        unpack8(load8(g + a.I + c + e), uv);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float dh = i % 2 ? acc[(c + e + i) / 2].y : acc[(c + e + i) / 2].x;
+        const float2 d = swiglu_grad(dh, gv[i], uv[i]);
+        dg[e + i] = d.x;
+        du[e + i] = d.y;
+      }
+    }
+    if (col + c < a.I) {
+      store_codes16<kE5M2>(q + c, dg, sg);
+      store_codes16<kE5M2>(q + Ip + c, du, su);
+      if (o) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          float x[8], y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = dg[e + i];
+            y[i] = du[e + i];
+          }
+          Raw8<__nv_bfloat16> r;
+          pack8(x, r);
+          store8(o + c + e, r);
+          pack8(y, r);
+          store8(o + a.I + c + e, r);
+        }
+      }
+    } else {  // the rest of the last block, up to the next half
+      *reinterpret_cast<uint4*>(q + c) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(q + Ip + c) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// ---- split tiles: a warp's row of one 1x128 block, four columns a lane
+template <bool kE5M2>
+__device__ __forceinline__ void finish_h(const GatedArgs& a, int row, int col, int lane, float4 g,
+                                         float4 u) {
+  const bool in = col + 4 * lane < a.I;
+  float h[4] = {swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z), swiglu(g.w, u.w)};
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max_nan(top, in ? fabsf(h[i]) : 0.f);
+  const Reciprocal s = reciprocal(block_scale<kE5M2>(warp_max_nan(top)));
+  if (lane == 0) a.sQ[size_t(row) * ceil_div(a.I, kBlockK) + col / kBlockK] = s.s;
+  if (!in) return;
+  *reinterpret_cast<uint32_t*>(a.Q + size_t(row) * a.I + col + 4 * lane) = codes4<kE5M2>(h, s);
+  if (a.GU) {
+    __nv_bfloat16* o = a.GU + size_t(row) * 2 * a.I + col + 4 * lane;
+    *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_bits(g.x, g.y), bf16x2_bits(g.z, g.w));
+    *reinterpret_cast<uint2*>(o + a.I) = make_uint2(bf16x2_bits(u.x, u.y), bf16x2_bits(u.z, u.w));
+  }
+}
+
+template <bool kE5M2>
+__device__ __forceinline__ void finish_dgu(const GatedArgs& a, int row, int col, int lane, float4 dh4) {
+  const int Ip = ceil_div(a.I, kBlockK) * kBlockK;
+  const bool in = col + 4 * lane < a.I;
+  float dg[4] = {}, du[4] = {};
+  if (in) {
+    const __nv_bfloat16* p = a.GU + size_t(row) * 2 * a.I + col + 4 * lane;
+    const uint2 g = *reinterpret_cast<const uint2*>(p), u = *reinterpret_cast<const uint2*>(p + a.I);
+    const uint32_t gw[2] = {g.x, g.y}, uw[2] = {u.x, u.y};
+    const float dh[4] = {dh4.x, dh4.y, dh4.z, dh4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float gv = __uint_as_float(i % 2 ? gw[i / 2] & 0xffff0000u : gw[i / 2] << 16);
+      const float uv = __uint_as_float(i % 2 ? uw[i / 2] & 0xffff0000u : uw[i / 2] << 16);
+      const float2 d = swiglu_grad(dh[i], gv, uv);
+      dg[i] = d.x;
+      du[i] = d.y;
+    }
+  }
+  float top_g = 0.f, top_u = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top_g = max_nan(top_g, fabsf(dg[i]));
+    top_u = max_nan(top_u, fabsf(du[i]));
+  }
+  const Reciprocal sg = reciprocal(block_scale<kE5M2>(warp_max_nan(top_g)));
+  const Reciprocal su = reciprocal(block_scale<kE5M2>(warp_max_nan(top_u)));
+  if (lane == 0) {
+    float* sq = a.sQ + size_t(row) * (2 * Ip / kBlockK) + col / kBlockK;
+    sq[0] = sg.s;
+    sq[Ip / kBlockK] = su.s;
+  }
+  uint8_t* q = a.Q + size_t(row) * 2 * Ip + col + 4 * lane;
+  *reinterpret_cast<uint32_t*>(q) = in ? codes4<kE5M2>(dg, sg) : 0u;
+  *reinterpret_cast<uint32_t*>(q + Ip) = in ? codes4<kE5M2>(du, su) : 0u;
+  if (in && a.dGU) {
+    __nv_bfloat16* o = a.dGU + size_t(row) * 2 * a.I + col + 4 * lane;
+    *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_bits(dg[0], dg[1]), bf16x2_bits(dg[2], dg[3]));
+    *reinterpret_cast<uint2*>(o + a.I) = make_uint2(bf16x2_bits(du[0], du[1]), bf16x2_bits(du[2], du[3]));
+  }
+}
+
+// kSplit: cluster c of args.split CTAs computes tile c, CTA rank r the r-th share of its K blocks.
+template <bool kGrad, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ GatedArgs args, int* status) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smA = smem;
+  uint8_t* smB = smem + kStages * kABytes;
+  float* tops = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // [2][2][kBlockM]
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(tops + 2 * 2 * kBlockM);
+  uint64_t* empty_bar = full_bar + kStages;
+  uint64_t* tfull_bar = empty_bar + kStages;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint64_t* pair_bar = tempty_bar + 2;  // the two promotion warps of the same rows
+  uint64_t* drain_bar = pair_bar + 4;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], kPromoWarps);
+    }
+    for (int p = 0; p < 4; ++p) mbar_init(&pair_bar[p], 2);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_holder, 2 * kBN);
+    tmem_relinquish();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  // a programmatic dependent: nothing below may read before the stream's earlier work is complete
+  griddep_wait();
+  griddep_launch_dependents();
+
+  const int Kb = ceil_div(args.K, kBlockK);
+  const int total = ceil_div(args.M, kBlockM) * ceil_div(args.I, tile_cols<kGrad>());
+  int t_begin = blockIdx.x, t_step = gridDim.x, kb0 = 0, kb1 = Kb, part = 0;
+  if constexpr (kSplit) {
+    part = int(cluster_ctarank());
+    t_begin = blockIdx.x / args.split;
+    t_step = total;  // one tile
+    kb0 = part * Kb / args.split;
+    kb1 = (part + 1) * Kb / args.split;
+  }
+  auto fail = [&]() {
+    *abort_flag = 1;
+    raise_status(status, FP8GEMM_ERR_TIMEOUT);
+  };
+
+  if (warp == kTmaWarp) {
+    regs_decrease<kLowRegs>();
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = t_begin; t < total && ok; t += t_step) {
+        const GatedTile w = gated_tile<kGrad>(args, t);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(&empty_bar[s], ((it / kStages) & 1) ^ 1, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full_bar[s], kStageBytes);
+          tma_load_2d(smA + s * kABytes, &tmA, &full_bar[s], kb * kBlockK, w.row0);
+          uint8_t* b = smB + s * kBBytes;
+          if constexpr (kGrad) {
+            tma_load_2d(b, &tmB, &full_bar[s], kb * kBlockK, w.col0);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tma_load_2d(b + i * (kBBytes / 4), &tmB, &full_bar[s], kb * kBlockK,
+                          w.col0 + 64 * (i / 2) + (i % 2 ? args.I : 0));
+          }
+        }
+      }
+      // let the last copies into each stage land before the CTA can exit
+      const uint32_t n = it < uint32_t(kStages) ? it : uint32_t(kStages);
+      for (uint32_t i = it - n; i < it; ++i) mbar_drain(&full_bar[i % kStages], (i / kStages) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    regs_decrease<kLowRegs>();
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f8_f32(kBlockM, kBN, uint32_t(args.a_fmt), uint32_t(args.b_fmt));
+      const uint32_t a_base = smem_addr(smA), b_base = smem_addr(smB);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = t_begin; t < total && ok; t += t_step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kStages, buf = it & 1;
+          if (!mbar_wait(&tempty_bar[buf], ((it / 2) & 1) ^ 1, abort_flag, args.wait_ns) ||
+              !mbar_wait(&full_bar[s], (it / kStages) & 1, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kBlockK / 32; ++k)
+            umma_e4m3(tmem_base + buf * kBN, smem_desc_sw128_kmajor(a_base + s * kABytes + k * 32),
+                      smem_desc_sw128_kmajor(b_base + s * kBBytes + k * 32), idesc, k > 0 ? 1u : 0u);
+          umma_commit(&empty_bar[s]);
+          umma_commit(&tfull_bar[buf]);
+        }
+      }
+      if (it > 0) {  // every issued MMA has finished before TMEM is released
+        umma_commit(drain_bar);
+        mbar_drain(drain_bar, 0);
+      }
+    }
+  } else if (warp < kPromoWarps) {
+    regs_increase<kHighRegs>();
+    const int wg = warp / 4;
+    const int row = (warp % 4) * 32 + lane;  // TMEM lane = tile row
+    const uint32_t lane_base = uint32_t((warp % 4) * 32) << 16;
+    const int Nb = ceil_div(kGrad ? args.I : 2 * args.I, kBlockK);
+    uint32_t it = 0, tiles = 0;
+    bool ok = true;
+    for (int t = t_begin; t < total && ok; t += t_step, ++tiles) {
+      const GatedTile w = gated_tile<kGrad>(args, t);
+      const bool row_ok = row < w.rows;
+      const int col = w.col0 + wg * (tile_cols<kGrad>() / 2);  // the thread's first column of h
+      const float* sa_ptr = args.sA + size_t(w.row0 + row) * Kb;
+      // The up rows of W1 may begin inside a 128-row scale block: of the thread's 64 up
+      // columns the first 16 n_low belong to one block, the rest to the next.
+      const int b0 = min(col / kBlockK, Nb - 1);
+      const int b1 = kGrad ? b0 : min((args.I + col) / kBlockK, Nb - 1);
+      const int b2 = kGrad ? b0 : min(b1 + 1, Nb - 1);
+      const int n_low = kGrad ? 4 : (kBlockK - (args.I + col) % kBlockK) / 16;
+      const float* s0_ptr = args.sB + size_t(b0) * Kb;
+      const float* s1_ptr = args.sB + size_t(b1) * Kb;
+      const float* s2_ptr = args.sB + size_t(b2) * Kb;
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      float sa = row_ok ? __ldg(sa_ptr + kb0) : 0.f;
+      float s0 = __ldg(s0_ptr + kb0), s1 = kGrad ? s0 : __ldg(s1_ptr + kb0), s2 = kGrad ? s0 : __ldg(s2_ptr + kb0);
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const float c0 = sa * s0, c1 = kGrad ? c0 : sa * s1, c2 = kGrad ? c0 : sa * s2;
+        if (kb + 1 < kb1) {
+          sa = row_ok ? __ldg(sa_ptr + kb + 1) : 0.f;
+          s0 = __ldg(s0_ptr + kb + 1);
+          if constexpr (!kGrad) {
+            s1 = __ldg(s1_ptr + kb + 1);
+            s2 = __ldg(s2_ptr + kb + 1);
+          }
+        }
+        const int buf = it & 1;
+        if (!mbar_wait(&tfull_bar[buf], (it / 2) & 1, abort_flag, args.wait_ns)) {
+          fail();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + lane_base + buf * kBN + wg * (kBN / 2);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[64];
+          tmem_ld_32x32b_x64(taddr + c * 64, r);
+          tmem_ld_wait_tied(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+          reg_tie32(&r[32]);
+          if (c == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float f = c == 0 || kGrad ? c0 : j / 8 < n_low ? c1 : c2;
+            acc[c * 32 + j] = __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
+                                         make_float2(f, f), acc[c * 32 + j]);
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if constexpr (kSplit) {
+        float4* srow = reinterpret_cast<float4*>(smem) + (row * kPitch + wg * (kBN / 2)) / 4;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          srow[j] = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
+        continue;
+      }
+      const int m = w.row0 + row;
+      if constexpr (kGrad) {
+        if (row_ok && col < args.I) {
+          if (args.q_fmt == FP8GEMM_FMT_E5M2)
+            store_dgu<true>(args, acc, m, col);
+          else
+            store_dgu<false>(args, acc, m, col);
+        }
+      } else {
+        if (args.GU && row_ok) {
+          __nv_bfloat16* o = args.GU + size_t(m) * 2 * args.I + col;
+#pragma unroll
+          for (int c = 0; c < 64; c += 8) {
+            if (col + c >= args.I) break;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float2* p = &acc[32 * half + c / 2];
+              *reinterpret_cast<uint4*>(o + half * args.I + c) =
+                  make_uint4(bf16x2_bits(p[0].x, p[0].y), bf16x2_bits(p[1].x, p[1].y),
+                             bf16x2_bits(p[2].x, p[2].y), bf16x2_bits(p[3].x, p[3].y));
+            }
+          }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          acc[j] = make_float2(swiglu(acc[j].x, acc[32 + j].x), swiglu(acc[j].y, acc[32 + j].y));
+          if (col + 2 * j < args.I) top = max_nan(top, max_nan(fabsf(acc[j].x), fabsf(acc[j].y)));
+        }
+        // the other half of the row's block, from the thread that holds it
+        float* mine = tops + (tiles & 1) * 2 * kBlockM;
+        mine[wg * kBlockM + row] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair_bar[warp % 4]);
+        ok = mbar_wait(&pair_bar[warp % 4], tiles & 1, abort_flag, args.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          fail();
+          break;
+        }
+        top = max_nan(top, mine[(1 - wg) * kBlockM + row]);
+        const bool e5 = args.q_fmt == FP8GEMM_FMT_E5M2;
+        const float scale = e5 ? block_scale<true>(top) : block_scale<false>(top);
+        if (row_ok) {
+          if (wg == 0) args.sQ[size_t(m) * ceil_div(args.I, kBlockK) + col / kBlockK] = scale;
+          if (e5)
+            store_h<true>(args, acc, m, col, scale);
+          else
+            store_h<false>(args, acc, m, col, scale);
+        }
+      }
+    }
+  } else {
+    regs_decrease<kLowRegs>();  // warps 10-11: no work
+  }
+
+  if constexpr (kSplit) {
+    // every CTA of the cluster has staged its partial (or given up, and the status says so)
+    __syncwarp();
+    cluster_sync();
+    if (warp < kPromoWarps && t_begin < total) {
+      // rows of the tile shared by the cluster's CTAs, a warp for each 1x128 block; partials are
+      // summed in rank order
+      const GatedTile w = gated_tile<kGrad>(args, t_begin);
+      const int S = args.split;
+      const int r0 = part * w.rows / S, r1 = (part + 1) * w.rows / S;
+      constexpr int kBlocks = kGrad ? 2 : 1;
+      const float4* mine = reinterpret_cast<const float4*>(smem);
+      auto sum = [&](int r, int c) {  // columns c .. c + 3 of staged row r
+        const float4* p = mine + (r * kPitch + c) / 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < S; ++q) {
+          const float4 x = *map_shared_rank(p, uint32_t(q));
+          v.x += x.x;
+          v.y += x.y;
+          v.z += x.z;
+          v.w += x.w;
+        }
+        return v;
+      };
+      for (int i = r0 * kBlocks + warp; i < r1 * kBlocks; i += kPromoWarps) {
+        const int r = i / kBlocks, blk = i % kBlocks;
+        const bool e5 = args.q_fmt == FP8GEMM_FMT_E5M2;
+        if constexpr (kGrad) {
+          const int col = w.col0 + 128 * blk;
+          if (col >= args.I) continue;
+          const float4 dh = sum(r, 128 * blk + 4 * lane);
+          if (e5)
+            finish_dgu<true>(args, w.row0 + r, col, lane, dh);
+          else
+            finish_dgu<false>(args, w.row0 + r, col, lane, dh);
+        } else {
+          const int c = 4 * lane + 64 * (lane / 16);  // gate 0-63, up 0-63, gate 64-127, up 64-127
+          const float4 g = sum(r, c), u = sum(r, c + 64);
+          if (e5)
+            finish_h<true>(args, w.row0 + r, w.col0, lane, g, u);
+          else
+            finish_h<false>(args, w.row0 + r, w.col0, lane, g, u);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another still reads its partial
+  }
+
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 2 * kBN);
+  }
+}
+
+// Clusters of `s` CTAs that can be resident at once (0: none).
+template <bool kGrad>
+int max_clusters(int dev, int s) {
+  static std::atomic<int> known[64][kMaxSplit + 1] = {};  // 0 unknown, -1 none, else the count
+  std::atomic<int>& k = known[dev & 63][s];
+  if (k == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = s;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, gemm_gated_kernel<kGrad, true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // a refused query leaves no sticky error
+      n = 0;
+    }
+    k = n > 0 ? n : -1;
+  }
+  return k > 0 ? int(k) : 0;
+}
+
+// Parts per tile when all tiles fit in one wave: as many as leave every tile's cluster resident, of
+// at least kMinPartKb K blocks each.
+constexpr int kMinPartKb = 4;
+
+template <bool kGrad>
+int choose_split(const LaunchCtx& c, long long tiles, int Kb) {
+  if (tiles >= c.num_sms) return 1;
+  long long s = c.num_sms / tiles;
+  if (s > Kb / kMinPartKb) s = Kb / kMinPartKb;
+  if (s > kMaxSplit) s = kMaxSplit;
+  for (; s >= 2; --s)
+    if (max_clusters<kGrad>(c.dev, int(s)) >= tiles) return int(s);
+  return 1;
+}
+
+template <bool kGrad>
+cudaError_t run(const LaunchCtx& c, GatedArgs a) {
+  a.wait_ns = wait_limit_ns();
+  CUtensorMap tmA, tmB;
+  if (!make_tmap_u8_sw128(&tmA, a.A, uint64_t(a.M), a.K, kBlockM)) return cudaErrorInvalidValue;
+  if (!make_tmap_u8_sw128(&tmB, a.B, kGrad ? uint64_t(a.I) : 2 * uint64_t(a.I), a.K, kGrad ? kBN : 64))
+    return cudaErrorInvalidValue;
+  static SmemLimit whole, split;
+  if (cudaError_t e = whole.raise(c, reinterpret_cast<const void*>(gemm_gated_kernel<kGrad, false>), kSmemBytes))
+    return e;
+  if (cudaError_t e = split.raise(c, reinterpret_cast<const void*>(gemm_gated_kernel<kGrad, true>), kSmemBytes))
+    return e;
+  const long long tiles = (long long)ceil_div(a.M, kBlockM) * ceil_div(a.I, tile_cols<kGrad>());
+  if (tiles > 0x3fffffffLL) return cudaErrorInvalidValue;
+  a.split = choose_split<kGrad>(c, tiles, ceil_div(a.K, kBlockK));
+  if (a.split == 1)
+    return launch_dependent(c, gemm_gated_kernel<kGrad, false>, unsigned(tiles < c.num_sms ? tiles : c.num_sms),
+                            kThreads, kSmemBytes, tmA, tmB, a, c.status);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles * a.split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(a.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_gated_kernel<kGrad, true>, tmA, tmB, a, c.status);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_gated(const LaunchCtx& c, const GatedArgs& a) { return run<false>(c, a); }
+cudaError_t launch_gemm_gated_backward(const LaunchCtx& c, const GatedArgs& a) { return run<true>(c, a); }
+
+}  // namespace fp8gemm

@@ -31,32 +31,6 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
-// The larger value, or NaN if one is: a NaN in a block must not look like the others' maximum
-// (a diverged row would become codes and scales of 0).
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// amax / limit: the corrected quotient where that is exact.
-template <bool kE5M2>
-__device__ __forceinline__ float block_scale(float amax) {
-  constexpr float kLimit = kE5M2 ? 57344.f : 448.f;
-  const Reciprocal d{kLimit, 1.f / kLimit, true};
-  return amax >= 1e-25f && amax <= 1e30f ? quotient(amax, d) : __fdiv_rn(amax, kLimit);
-}
-
-// Eight values to codes of one scale; zeros where it is 0 (all zeros, or a maximum so
-// small that the scale underflows: the quotient of a 0 there would be NaN).
-template <bool kE5M2>
-__device__ __forceinline__ uint2 quant8(const float (&v)[8], const Reciprocal& d) {
-  const float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
-  if (d.safe) return make_uint2(quant4<kE5M2>(a, d), quant4<kE5M2>(b, d));
-  if (d.s == 0.f) return make_uint2(0u, 0u);
-  return make_uint2(quant4<kE5M2>(a, d.s), quant4<kE5M2>(b, d.s));
-}
-
 // One CTA per row; thread t holds elements 8 (t + i blockDim.x) .. + 7 for i < kIter.
 // A 1x128 block is 16 neighbouring threads.
 // CTAs that stay and take row after row, the next one asked for ahead, were slower

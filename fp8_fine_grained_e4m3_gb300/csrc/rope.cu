@@ -1,0 +1,211 @@
+// rope.cu -- rotary positions of queries and keys, and their gradient.
+//
+// With t = position * freq[i] for the i-th pair (x1, x2) of a head,
+//   y1 = a (x1 cos t - x2 sin t),  y2 = a (x2 cos t + x1 sin t)
+// and the gradient is the same with -t (a times a rotation, transposed).  Pairs are
+// elements i and i + rot / 2 of the head, or 2 i and 2 i + 1; elements past rot pass through.
+//
+// A far position times a frequency has more bits than FP32 holds (131072 radians would be
+// known to 2^-7), so the angle is formed in FP64, in half turns, and brought into
+// [-1, 1] there; its sine and cosine are FP32's (sincospi, 1 to 2 ulp).  That is ten FP64
+// operations for a pair of a token, shared by all heads of the token through shared memory.
+//
+// Bound by memory: every element is read and written once, 16 bytes a lane.
+#include "common.cuh"
+#include "ptx.cuh"
+#include "vec.cuh"
+
+namespace fp8gemm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTokens = 8;  // of a CTA: a warp looks up each one's position
+constexpr int kMaxPairs = kMaxRopeDim / 2;
+
+// The sequence b with cu[b] <= t < cu[b + 1], by one warp: 32 offsets a step.  -1: none (behind the
+// last sequence or before the first); -2: the offsets fall.
+__device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int lane) {
+  int lo = 0, n = B + 1;  // the last of cu[lo .. lo + n) that is not above t
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lo + lane * step;
+    const bool le = lane * step < n && cu[i] <= t;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    if (m == 0u) return -1;
+    const int last = 31 - __clz(m);
+    n = min(step, n - last * step);
+    lo += last * step;
+    if (step == 1) break;
+  }
+  if (lo >= B) return -1;
+  return cu[lo] <= t && t < cu[lo + 1] ? lo : -2;
+}
+
+// A token's position; false where it has none (its rows are then left as they are).
+__device__ __forceinline__ bool token_position(const RopeArgs& a, int t, int lane, int* status,
+                                               int* pos) {
+  if (a.positions) {
+    *pos = a.positions[t];
+    return true;
+  }
+  int b, t0, n;
+  if (a.cu) {
+    b = find_sequence(a.cu, a.B, t, lane);
+    if (b < 0) {
+      if (b == -2 && lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+      return false;
+    }
+    t0 = a.cu[b];
+    n = a.cu[b + 1] - t0;
+    if (t0 < 0 || a.cu[b + 1] > a.T) {
+      if (lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+      return false;
+    }
+  } else {
+    n = a.T / a.B;
+    b = t / n;
+    t0 = b * n;
+  }
+  const int start = a.lens[b] - n;
+  if (start < 0) {
+    if (lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+    return false;
+  }
+  *pos = start + t - t0;
+  return true;
+}
+
+template <class T>
+struct Unit {  // 16 elements of a head: the two halves of 8 pairs, or 8 pairs (or none) in a row
+  const T* x;
+  T* y;
+  int gap;   // from the first eight elements to the second eight
+  int pair;  // first pair in the CTA's table, -1: to be copied, -2: nothing to do
+};
+
+template <class T, bool kInterleaved>
+__device__ __forceinline__ void turn(const Raw8<T>& r0, const Raw8<T>& r1, const float2* cs, Raw8<T>& o0,
+                                     Raw8<T>& o1) {
+  float a[8], b[8];
+  unpack8(r0, a);
+  unpack8(r1, b);
+  if constexpr (kInterleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = cs[i], q = cs[i + 4];
+      const float u = a[2 * i], v = b[2 * i];
+      a[2 * i] = fmaf(u, p.x, -(a[2 * i + 1] * p.y));
+      a[2 * i + 1] = fmaf(a[2 * i + 1], p.x, u * p.y);
+      b[2 * i] = fmaf(v, q.x, -(b[2 * i + 1] * q.y));
+      b[2 * i + 1] = fmaf(b[2 * i + 1], q.x, v * q.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 p = cs[i];
+      const float u = a[i];
+      a[i] = fmaf(u, p.x, -(b[i] * p.y));
+      b[i] = fmaf(b[i], p.x, u * p.y);
+    }
+  }
+  pack8(a, o0);
+  pack8(b, o1);
+}
+
+// CTA (x, y): tokens x tokens .. + tokens - 1, the y-th of gridDim.y shares of their heads' units.
+template <class T, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tokens, int* status) {
+  __shared__ float2 cs[kMaxTokens * 32 > kMaxPairs ? kMaxTokens * 32 : kMaxPairs];
+  __shared__ int pos[kMaxTokens];
+  __shared__ bool has[kMaxTokens];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int t_first = blockIdx.x * tokens, n_tok = min(tokens, a.T - t_first);
+  const int pairs = a.rot / 2;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (warp < n_tok) {
+    int p = 0;
+    const bool ok = token_position(a, t_first + warp, lane, status, &p);
+    if (lane == 0) {
+      pos[warp] = p;
+      has[warp] = ok;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_tok * pairs; i += kThreads) {
+    const int k = i / pairs;
+    // 1 / pi in two parts: a position of 2^31 would lose 2^-21 of a turn in one
+    constexpr double kInvPi = 0.31830988618379067154, kInvPiLow = -1.9678676675182486e-17;
+    const double x = double(pos[k]) * double(a.freq[i - k * pairs]);  // radians
+    const double t = x * kInvPi;                                      // half turns
+    const double low = fma(x, kInvPi, -t) + x * kInvPiLow;
+    float s, c;
+    sincospif(float(fma(-2.0, rint(0.5 * t), t) + low), &s, &c);
+    cs[i] = make_float2(a.amplitude * c, a.backward ? -a.amplitude * s : a.amplitude * s);
+  }
+  __syncthreads();
+  const int U = a.dim / 16, per_token = (a.heads_q + a.heads_k) * U;
+  auto unit = [&](int u) {
+    Unit<T> r = {nullptr, nullptr, 0, -2};
+    const int k = u / per_token;
+    if (k >= n_tok || !has[k]) return r;
+    u -= k * per_token;
+    int h = u / U;
+    const int c = u - h * U;
+    const bool key = h >= a.heads_q;
+    if (key) h -= a.heads_q;
+    const long long t = t_first + k;
+    const T* x = static_cast<const T*>(key ? a.K : a.Q) + t * (key ? a.ld_k : a.ld_q) + h * a.dim;
+    T* y = static_cast<T*>(key ? a.Ko : a.Qo) + t * (key ? a.ld_ko : a.ld_qo) + h * a.dim;
+    const bool turned = 16 * c < a.rot;
+    if (!turned && x == y) return r;
+    const bool half = turned && !kInterleaved;
+    r.x = x + (half ? 8 : 16) * c;
+    r.y = y + (half ? 8 : 16) * c;
+    r.gap = half ? pairs : 8;
+    r.pair = turned ? k * pairs + 8 * c : -1;
+    return r;
+  };
+  const int end = n_tok * per_token;
+  constexpr int kAhead = 2;  // units whose loads a thread has in flight
+  for (int u = blockIdx.y * kThreads + threadIdx.x; u < end; u += kAhead * gridDim.y * kThreads) {
+    Unit<T> w[kAhead];
+    Raw8<T> r0[kAhead], r1[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      w[j] = unit(u + j * int(gridDim.y) * kThreads);
+      zero8(r0[j]);
+      zero8(r1[j]);
+      if (w[j].pair != -2) {
+        r0[j] = load8(w[j].x);
+        r1[j] = load8(w[j].x + w[j].gap);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (w[j].pair == -2) continue;
+      if (w[j].pair >= 0) turn<T, kInterleaved>(r0[j], r1[j], cs + w[j].pair, r0[j], r1[j]);
+      store8(w[j].y, r0[j]);
+      store8(w[j].y + w[j].gap, r1[j]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const LaunchCtx& c, const RopeArgs& a) {
+  // As many tokens as give each thread an angle, where that still leaves a CTA or more an SM; with
+  // few tokens one each, its heads shared by several CTAs.
+  int tokens = min(kMaxTokens, max(1, kThreads / (a.rot / 2)));
+  while (tokens > 1 && ceil_div(a.T, tokens) < 2 * c.num_sms) tokens /= 2;
+  const int grid_x = ceil_div(a.T, tokens);
+  const long long units = (long long)tokens * (a.heads_q + a.heads_k) * (a.dim / 16);
+  const long long most = (units + kThreads - 1) / kThreads;
+  const int grid_y = int(max(1LL, min(most, (long long)c.num_sms / grid_x)));
+  auto fn = a.f32 ? (a.interleaved ? rope_kernel<float, true> : rope_kernel<float, false>)
+                  : (a.interleaved ? rope_kernel<__nv_bfloat16, true> : rope_kernel<__nv_bfloat16, false>);
+  return launch_dependent(c, fn, dim3(grid_x, grid_y), kThreads, 0, a, tokens, c.status);
+}
+
+}  // namespace fp8gemm

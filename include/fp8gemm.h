@@ -580,6 +580,80 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
                      int num_blocks, int max_q, int fmt, fp8gemm_stream_t stream);
 
 /*
+ * fp8gemm_gated -- the first half of a gated feed-forward block in one kernel: both
+ * projections, the activation, their product and the quantiser of the second half's A.
+ *
+ *   u = A W1^T (block scales and promotion as fp8gemm_dense; FP32)
+ *   h = silu(u[:, :I]) u[:, I:] in FP32;  sQ, Q = fp8_quant_1x128's rule on h (limit of
+ *       q_fmt; zeros where a block's scale underflows to 0).  A NaN in a block makes its scale
+ *       NaN.
+ *
+ *   A   u8 [M, K] of a_fmt, sA f32 [M, ceil(K/128)]
+ *   W1  u8 [2 I, K] of b_fmt: the I gate rows, then the I up rows (as fp8_moe_few's)
+ *   s1  f32 [ceil(2 I/128), ceil(K/128)]
+ *   Q   u8 [M, I] of q_fmt, sQ f32 [M, ceil(I/128)] (outputs)
+ *   GU  bf16 [M, 2 I]: u, rounded, for fp8gemm_gated_backward; or NULL: not wanted
+ *   I and K positive multiples of 16, I at most 2^29; alignment 16 bytes.
+ */
+int fp8gemm_gated(const uint8_t* A, const float* sA, int a_fmt, const uint8_t* W1, const float* s1,
+                  int b_fmt, uint8_t* Q, float* sQ, int q_fmt, void* GU, int M, int I, int K,
+                  fp8gemm_stream_t stream);
+
+/*
+ * fp8gemm_gated_backward -- gradients of u of fp8gemm_gated, the quantiser passing them
+ * straight through, from the gradient dY of the block's output y = h W2^T:
+ *
+ *   dh = dY W2 (block scales and promotion as fp8gemm_dense; FP32)
+ *   with g = GU[:, :I], u = GU[:, I:], s = 1 / (1 + exp(-g)), all in FP32:
+ *   dg = dh u s (1 + g (1 - s)),   du = dh g s
+ *   Q, sQ: 1x128 codes and scales of dg and du (rule as above), the A operand of
+ *   dX = [dg, du] W1.  Each half begins at a scale block: with Ip = 128 ceil(I/128), columns
+ *   0 .. I - 1 hold dg, Ip .. Ip + I - 1 du, and the columns between are zeros.
+ *
+ *   dY   u8 [M, K] of a_fmt, sdY f32 [M, ceil(K/128)] (K: the block's output width)
+ *   W2T  u8 [I, K] of b_fmt: W2 [K, I] transposed; s2T f32 [ceil(I/128), ceil(K/128)]
+ *   GU   bf16 [M, 2 I], as fp8gemm_gated left it
+ *   Q    u8 [M, 2 Ip] of q_fmt, sQ f32 [M, 2 Ip/128] (outputs)
+ *   dGU  bf16 [M, 2 I]: dg, then du, rounded (for the weights' gradient); or NULL
+ *   Sizes and alignment as fp8gemm_gated.
+ */
+int fp8gemm_gated_backward(const uint8_t* dY, const float* sdY, int a_fmt, const uint8_t* W2T,
+                           const float* s2T, int b_fmt, const void* GU, uint8_t* Q, float* sQ,
+                           int q_fmt, void* dGU, int M, int I, int K, fp8gemm_stream_t stream);
+
+/*
+ * fp8_rope -- rotary positions of queries and keys, between the product that makes
+ * them and the cache (fp8_kv_append) or the attention.  With t = position * freq[i] for the
+ * i-th of a head's rot / 2 pairs,
+ *
+ *   y1 = amplitude (x1 cos t - x2 sin t),   y2 = amplitude (x2 cos t + x1 sin t)
+ *
+ * Pair i is elements i and i + rot / 2 of the head, or (interleaved != 0) 2 i and
+ * 2 i + 1.  Elements rot .. dim - 1 pass through.  backward != 0: the gradient -- Q and
+ * K are those of the outputs, and t turns the other way.  Angles are formed in
+ * FP64 from the FP32 frequency, so far positions lose nothing; arithmetic is FP32,
+ * rounded once to the type.
+ *
+ *   Q, Qo  [T, heads_q, dim] of x_type, ld_q / ld_qo elements from token to token
+ *          (multiples of 8, at least heads_q * dim); K, Ko the same with heads_k.  heads_q
+ *          or heads_k may be 0 (pointers NULL).  Qo may be Q and Ko K, each with its
+ *          input's stride (in place); otherwise outputs overlap no input.
+ *   freq   f32 [rot / 2] (device): radians a position
+ *   positions  i32 [T] (device), any values; or NULL: as fp8_kv_append's, token i of a
+ *          sequence's n new ones stands at seq_len - n + i.  seq_lens i32 [B] counts the new
+ *          ones; cu i32 [B + 1] are their offsets (NULL: T / B each, T % B == 0).
+ *          Rows that belong to no sequence are left as they were.  Offsets that fall or leave
+ *          0 .. T and lengths below a sequence's new tokens set FP8GEMM_ERR_DEVICE_STATUS; the
+ *          rows concerned are left as they were.
+ *   dim a multiple of 16 up to 512, rot a multiple of 16 up to dim, heads up to 65535.
+ *   Alignment: 16 bytes (freq, positions, seq_lens, cu 4).
+ */
+int fp8_rope(const void* Q, int64_t ld_q, const void* K, int64_t ld_k, int x_type, void* Qo,
+             int64_t ld_qo, void* Ko, int64_t ld_ko, const float* freq, const int32_t* positions,
+             const int32_t* seq_lens, const int32_t* cu, float amplitude, int T, int B, int heads_q,
+             int heads_k, int dim, int rot, int interleaved, int backward, fp8gemm_stream_t stream);
+
+/*
  * fp8_moe_few -- a whole mixture-of-experts layer for a few tokens.
  *
  *   ids[t, :]      the top_k experts of token t by logit, largest first, ties

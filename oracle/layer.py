@@ -149,3 +149,37 @@ def moe(A, sA, logits, W1, s1, W2, s2, k, renormalise=True):
             h[:, kb * BLOCK:(kb + 1) * BLOCK] = q * s
         np.add.at(out, t, w[t, j][:, None] * (h @ _dequant(W2[e], s2[e]).T))
     return out, ids, w
+
+
+# --------------------------------------------------------- rotary positions
+def rope(X, positions, freq, amplitude=1.0, interleaved=False, backward=False):
+    """X [T, heads, dim] turned by positions [T] times freq [rot / 2]."""
+    y = np.asarray(X, dtype=np.float64).copy()
+    half = len(freq)
+    t = np.asarray(positions, dtype=np.float64)[:, None] * np.asarray(freq, dtype=np.float64)
+    c, s = amplitude * np.cos(t)[:, None], amplitude * np.sin(t)[:, None]
+    if backward:
+        s = -s
+    i, j = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    a, b = y[..., i].copy(), y[..., j].copy()
+    y[..., i], y[..., j] = a * c - b * s, b * c + a * s
+    return y
+
+
+# ------------------------------------------------------- gated feed-forward
+def gated(A, sA, W1, s1, a_fmt="e4m3"):
+    """(h, u) of u = A W1^T [M, 2 I], h = silu(u[:, :I]) u[:, I:]."""
+    x = _FORMATS[a_fmt][2](A) * np.repeat(sA.astype(np.float64), BLOCK, 1)[:, :A.shape[1]]
+    u = x @ _dequant(W1, s1).T
+    I = u.shape[1] // 2
+    return u[:, :I] / (1.0 + np.exp(-u[:, :I])) * u[:, I:], u
+
+
+def gated_backward(dY, sdY, W2T, s2T, GU, fmt="e5m2"):
+    """(dgate, dup, dh) for dh = dY W2T^T and the gate and up values GU [M, 2 I]."""
+    x = _FORMATS[fmt][2](dY) * np.repeat(sdY.astype(np.float64), BLOCK, 1)[:, :dY.shape[1]]
+    dh = x @ _dequant(W2T, s2T).T
+    I = dh.shape[1]
+    g, u = GU[:, :I].astype(np.float64), GU[:, I:].astype(np.float64)
+    s = 1.0 / (1.0 + np.exp(-g))
+    return dh * u * s * (1.0 + g * (1.0 - s)), dh * g * s, dh
