@@ -65,6 +65,8 @@ SIGNATURES = [
      [_P, _P, _L, _L, _P, _P, _P, _P, _P, _P, _P, *[_I] * 9, _P]),
     ("fp8_kv_attention", _I,
      [_P, _L, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, *[_I] * 10, _P]),
+    ("fp8_kv_attention_chunk", _I,
+     [_P, _L, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _I, _P, *[_I] * 10, _P]),
     ("fp8gemm_gated", _I, [_P, _P, _I, _P, _P, _I, _P, _P, _I, _P, _I, _I, _I, _P]),
     ("fp8gemm_gated_backward", _I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _P]),
     ("fp8_rope", _I,
@@ -605,6 +607,7 @@ class _Fast:
         L = lib()
         self.rmsnorm_quant, self.rmsnorm_backward = L.fp8_rmsnorm_quant, L.fp8_rmsnorm_backward
         self.kv_append, self.kv_attention = L.fp8_kv_append, L.fp8_kv_attention
+        self.kv_attention_chunk = L.fp8_kv_attention_chunk
         self.moe_few, self.rope = L.fp8_moe_few, L.fp8_rope
         self.gated, self.gated_backward = L.fp8gemm_gated, L.fp8gemm_gated_backward
 
@@ -823,17 +826,9 @@ def fp8_kv_append(K, V, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
         _check(rc, "fp8_kv_append")
 
 
-def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q=None,
-                     max_q=None, scale=None, fmt="e4m3", O=None, stream=None):
-    """Attention of the newest tokens (Q bf16 [T, heads * group, dim], tokens
-    may lie apart) over the paged FP8 cache that holds their keys and values
-    already -> O bf16 [T, heads * group, dim].  cu_q and max_q as
-    fp8_kv_append's; scale defaults to dim ** -0.5."""
-    f = _fast or _lookup()
-    code = _fmt(fmt)
-    T = Q.size(0)
-    n, heads, block, dim, B, width = _cache(f, k_cache, k_scale, v_cache, v_scale, block_table,
-                                            seq_lens, cu_q, T, fmt)
+def _queries(f, Q, O, T, B, heads, dim, cu_q, max_q, scale):
+    """Checks the queries of an attention call and fills in what is not given: query heads,
+    token stride, output, most queries a sequence, scale."""
     if Q.dim() != 3 or heads == 0 or Q.size(1) % heads != 0:
         raise ValueError(f"Q has shape {tuple(Q.shape)}; the call needs [T, heads * group, dim]"
                          f" with {heads} cached heads")
@@ -845,8 +840,21 @@ def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
         _size(O, "O", f.bf16, T * hq * dim, dim)
     if max_q is None:
         max_q = T if cu_q is not None else -(-T // max(B, 1))
-    if scale is None:
-        scale = dim ** -0.5
+    return hq, ld_q, O, max_q, dim ** -0.5 if scale is None else scale
+
+
+def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q=None,
+                     max_q=None, scale=None, fmt="e4m3", O=None, stream=None):
+    """Attention of the newest tokens (Q bf16 [T, heads * group, dim], tokens
+    may lie apart) over the paged FP8 cache that holds their keys and values
+    already -> O bf16 [T, heads * group, dim].  cu_q and max_q as
+    fp8_kv_append's; scale defaults to dim ** -0.5."""
+    f = _fast or _lookup()
+    code = _fmt(fmt)
+    T = Q.size(0)
+    n, heads, block, dim, B, width = _cache(f, k_cache, k_scale, v_cache, v_scale, block_table,
+                                            seq_lens, cu_q, T, fmt)
+    hq, ld_q, O, max_q, scale = _queries(f, Q, O, T, B, heads, dim, cu_q, max_q, scale)
     device = _on(f, Q, "Q")
     rc = f.kv_attention(Q.data_ptr(), ld_q, _here(k_cache, "k_cache", device),
                         _here(k_scale, "k_scale", device), _here(v_cache, "v_cache", device),
@@ -859,6 +867,31 @@ def fp8_kv_attention(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_len
                         f.current(device) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "fp8_kv_attention")
+    return O
+
+
+def fp8_kv_attention_chunk(Q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens, cu_q=None,
+                           max_q=None, scale=None, causal=True, fmt="e4m3", O=None, stream=None):
+    """fp8_kv_attention for many queries a sequence (prompts, chunks of them), with
+    causal=False for queries that all see the whole sequence (cross attention)."""
+    f = _fast or _lookup()
+    code = _fmt(fmt)
+    T = Q.size(0)
+    n, heads, block, dim, B, width = _cache(f, k_cache, k_scale, v_cache, v_scale, block_table,
+                                            seq_lens, cu_q, T, fmt)
+    hq, ld_q, O, max_q, scale = _queries(f, Q, O, T, B, heads, dim, cu_q, max_q, scale)
+    device = _on(f, Q, "Q")
+    rc = f.kv_attention_chunk(Q.data_ptr(), ld_q, _here(k_cache, "k_cache", device),
+                              _here(k_scale, "k_scale", device), _here(v_cache, "v_cache", device),
+                              _here(v_scale, "v_scale", device),
+                              _here(block_table, "block_table", device),
+                              _here(seq_lens, "seq_lens", device),
+                              None if cu_q is None else _here(cu_q, "cu_q", device), scale,
+                              1 if causal else 0, _here(O, "O", device), T, B, heads, hq // heads,
+                              dim, block, width, n, max_q, code,
+                              f.current(device) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "fp8_kv_attention_chunk")
     return O
 
 

@@ -744,6 +744,34 @@ int fp8_rope(const void* Q, int64_t ld_q, const void* K, int64_t ld_k, int x_typ
   return finish(launch_rope(c, a), 1);
 }
 
+int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
+                           const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* cu_q, float scale, int causal,
+                           void* O, int T, int B, int heads, int group, int dim, int block,
+                           int table_width, int num_blocks, int max_q, int fmt,
+                           fp8gemm_stream_t stream) {
+  if (int r = check_cache(T, B, heads, dim, block, table_width, num_blocks, max_q, cu_q, fmt))
+    return r;
+  if (group < 0 || (long long)heads * group > 65535 || (long long)max_q * group > 0x7fffffffLL ||
+      (long long)T * group > 0x7fffffffLL || (long long)table_width * block > 0x7fffffffLL)
+    return FP8GEMM_ERR_SHAPE;
+  if (T == 0 || B == 0 || heads == 0 || group == 0 || max_q == 0) return FP8GEMM_OK;
+  if (ld_q < int64_t(heads) * group * dim || ld_q % 8 != 0) return FP8GEMM_ERR_SHAPE;
+  if (!Q || !k_cache || !k_scale || !v_cache || !v_scale || !block_table || !seq_lens || !O)
+    return FP8GEMM_ERR_NULL;
+  if (!aligned16(Q) || !aligned16(k_cache) || !aligned4(k_scale) || !aligned16(v_cache) ||
+      !aligned4(v_scale) || !aligned4(block_table) || !aligned4(seq_lens) ||
+      !aligned4(cu_q) || !aligned16(O))
+    return FP8GEMM_ERR_ALIGN;
+  LaunchCtx c;
+  if (int r = ctx_for(stream, &c)) return r;
+  const KvChunkArgs a{static_cast<const __nv_bfloat16*>(Q), ld_q, k_cache, k_scale, v_cache, v_scale,
+                      block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O), scale, T, B, heads,
+                      group, dim, block, table_width, num_blocks, max_q, fmt, log2_block(block),
+                      causal != 0, wait_limit_ns()};
+  return finish(launch_kv_chunk(c, a), 1);
+}
+
 int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,
                 const float* s1, const uint8_t* W2, const float* s2, void* D, int32_t* ids,
                 float* weights, int T, int H, int I, int E, int top_k, int renormalise,

@@ -181,6 +181,26 @@ struct KvAttentionArgs {
 size_t kv_attention_workspace_bytes(const LaunchCtx& c);
 cudaError_t launch_kv_attention(const LaunchCtx& c, const KvAttentionArgs& a, void* ws);
 
+// Attention of a chunk of new tokens over the cache (kv_chunk.cu).
+struct KvChunkArgs {
+  const __nv_bfloat16* Q;  // [T, heads * group, dim], ld_q elements from token to token
+  long long ld_q;
+  const uint8_t* kc;
+  const float* ks;
+  const uint8_t* vc;
+  const float* vs;
+  const int* table;
+  const int* lens;
+  const int* cu;
+  __nv_bfloat16* O;  // [T, heads * group, dim]
+  float scale;
+  int T, B, heads, group, dim, block, width, num_blocks, max_q, fmt;
+  int log_block;
+  bool causal;
+  unsigned long long wait_ns;
+};
+cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a);
+
 // The gated feed-forward products (gemm_gated.cu).
 struct GatedArgs {
   const uint8_t* A;  // [M, K]: activations, or dY

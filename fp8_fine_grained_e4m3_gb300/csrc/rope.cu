@@ -12,6 +12,7 @@
 //
 // Bound by memory: every element is read and written once, 16 bytes a lane.
 #include "common.cuh"
+#include "kv_cache.cuh"
 #include "ptx.cuh"
 #include "vec.cuh"
 
@@ -22,25 +23,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokens = 8;  // of a CTA: a warp looks up each one's position
 constexpr int kMaxPairs = kMaxRopeDim / 2;
-
-// The sequence b with cu[b] <= t < cu[b + 1], by one warp: 32 offsets a step.  -1: none (behind the
-// last sequence or before the first); -2: the offsets fall.
-__device__ __forceinline__ int find_sequence(const int* cu, int B, int t, int lane) {
-  int lo = 0, n = B + 1;  // the last of cu[lo .. lo + n) that is not above t
-  while (n > 0) {
-    const int step = (n + 31) / 32;
-    const int i = lo + lane * step;
-    const bool le = lane * step < n && cu[i] <= t;
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
-    if (m == 0u) return -1;
-    const int last = 31 - __clz(m);
-    n = min(step, n - last * step);
-    lo += last * step;
-    if (step == 1) break;
-  }
-  if (lo >= B) return -1;
-  return cu[lo] <= t && t < cu[lo + 1] ? lo : -2;
-}
 
 // A token's position; false where it has none (its rows are then left as they are).
 __device__ __forceinline__ bool token_position(const RopeArgs& a, int t, int lane, int* status,

@@ -580,6 +580,25 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
                      int num_blocks, int max_q, int fmt, fp8gemm_stream_t stream);
 
 /*
+ * fp8_kv_attention_chunk -- fp8_kv_attention for many queries a sequence: a prompt, a chunk of
+ * one behind what is cached, or queries over states of another length.
+ *
+ *   causal != 0: query i of a sequence's n sees its first seq_len - n + 1 + i tokens, as in
+ *     fp8_kv_attention (its own key is in the cache by then)
+ *   causal = 0: every query sees all seq_len tokens (cross attention)
+ *
+ * Layouts, cache, index arrays, refusals and what the status word says are those of
+ * fp8_kv_attention; a query that sees no token gives zeros.  Rows of O that belong to no
+ * sequence are left as they were.  T * group, max_q * group and table_width * block below 2^31.
+ */
+int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
+                           const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* cu_q, float scale, int causal,
+                           void* O, int T, int B, int heads, int group, int dim, int block,
+                           int table_width, int num_blocks, int max_q, int fmt,
+                           fp8gemm_stream_t stream);
+
+/*
  * fp8gemm_gated -- the first half of a gated feed-forward block in one kernel: both
  * projections, the activation, their product and the quantiser of the second half's A.
  *

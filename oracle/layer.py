@@ -113,6 +113,34 @@ def kv_attention(Q, kc, ks, vc, vs, table, lens, cu, scale, fmt="e4m3"):
     return O, A
 
 
+def kv_attention_chunk(Q, kc, ks, vc, vs, table, lens, cu, scale, fmt="e4m3", causal=True):
+    """kv_attention for many queries; causal=False: each sees the whole sequence.  NaN where no
+    sequence has the row."""
+    decode = _FORMATS[fmt][2]
+    heads, block, dim = kc.shape[1:]
+    group = Q.shape[1] // heads
+    O, A = np.full(Q.shape, np.nan), np.full(Q.shape, np.nan)
+    for b in range(len(lens)):
+        L, t0, n = int(lens[b]), int(cu[b]), int(cu[b + 1] - cu[b])
+        blocks = [int(x) for x in table[b, :-(-L // block)]]
+        O[t0:t0 + n], A[t0:t0 + n] = 0.0, 0.0
+        for h in range(heads):
+            if not blocks:
+                continue
+            k, v = (np.concatenate([decode(c[x, h]) * np.float64(s[x, h]) for x in blocks])[:L]
+                    for c, s in ((kc, ks), (vc, vs)))
+            x = scale * np.einsum("ngd,ld->ngl", Q[t0:t0 + n, h * group:h * group + group].astype(np.float64), k)
+            sees = L - n + 1 + np.arange(n) if causal else np.full(n, L)
+            hidden = np.arange(L) >= sees[:, None, None]
+            x = np.where(hidden, -np.inf, x)
+            top = np.max(x, axis=2, keepdims=True)
+            p = np.where(hidden, 0.0, np.exp(x - np.where(np.isneginf(top), 0, top)))
+            p /= np.maximum(np.sum(p, axis=2, keepdims=True), 1e-300)
+            O[t0:t0 + n, h * group:h * group + group] = np.einsum("ngl,ld->ngd", p, v)
+            A[t0:t0 + n, h * group:h * group + group] = np.einsum("ngl,ld->ngd", p, np.abs(v))
+    return O, A
+
+
 # -------------------------------------------------------------------- MoE
 def moe_route(logits, k, renormalise=True):
     logits = np.asarray(logits, dtype=np.float64)
