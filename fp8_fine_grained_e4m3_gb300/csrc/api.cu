@@ -171,9 +171,10 @@ int finish(cudaError_t e, int nlaunch) {
 // kWsContig: the tile counters and tile order of the contiguous form.
 // Slot kWsNorm: partial gain gradients of the norm.  Slot kWsMoe: routing and
 // hidden activations of the few-token MoE layer.  Slot kWsAttention: counters
-// (left at zero) and partial results of the cache attention.
+// (left at zero) and partial results of the cache attention.  Slot kWsChunk: partial results of
+// the chunk's.
 enum { kWsSplitK = 0, kWsQuantA = 1, kWsTable = 2, kWsBatch = 3, kWsContig = 4, kWsNorm = 5,
-       kWsMoe = 6, kWsAttention = 7 };
+       kWsMoe = 6, kWsAttention = 7, kWsChunk = 8 };
 
 // A call that takes a workspace holds its stream's lock from the look-up to its last
 // launch.  Host threads may share a stream: without it one call's kernels, which
@@ -769,7 +770,10 @@ int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, 
                       block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O), scale, T, B, heads,
                       group, dim, block, table_width, num_blocks, max_q, fmt, log2_block(block),
                       causal != 0, wait_limit_ns()};
-  return finish(launch_kv_chunk(c, a), 1);
+  void* ws = nullptr;
+  const StreamLock lk = lock_stream(c.dev, stream);
+  if (int r = workspace_on(c.dev, c.ctx, stream, kv_chunk_workspace_bytes(c), &ws, kWsChunk)) return r;
+  return finish(launch_kv_chunk(c, a, ws), 2);
 }
 
 int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,

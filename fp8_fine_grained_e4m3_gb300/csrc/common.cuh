@@ -197,9 +197,10 @@ struct KvChunkArgs {
   int T, B, heads, group, dim, block, width, num_blocks, max_q, fmt;
   int log_block;
   bool causal;
-  unsigned long long wait_ns;
+  unsigned long long wait_ns;  // limit of each wait
 };
-cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a);
+size_t kv_chunk_workspace_bytes(const LaunchCtx& c);
+cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws);
 
 // The gated feed-forward products (gemm_gated.cu).
 struct GatedArgs {

@@ -1,8 +1,36 @@
-// kv_chunk.cu -- attention of a chunk of new tokens over the paged FP8 cache.
+// kv_chunk.cu -- attention of a chunk of new tokens over the paged FP8 cache (kv_cache.cu has the
+// layout): prompts, chunks of them behind what is cached, queries over another sequence's states.
 //
 //   o = sum_j p_j v_j,  p = softmax over the visible j of (scale q . k_j)
 //
-// A warp for each query row: lanes are tokens for the scores, dimensions for the output.
+// The rows of a cached head are the (token, query head of its group) pairs, in that order: they
+// share every byte of it, and neighbouring rows lie side by side in Q and O.  A unit of work is
+// 256 rows of one head of one sequence, in two tiles of 128, against the tokens that its last
+// row sees, 128 at a time:
+//   S [128, 128] = Q K^T, P = 2^(S - reference), O [128, dim] += P V
+// both products by tcgen05 on FP16 operands (FP8 codes are exact in FP16; q is shifted by a power
+// of two per row into its range, as BF16 has fewer bits; P has 11).  S and O live in TMEM -- the
+// two tiles' S and O fill its 512 columns -- and P takes the place of S there.
+//
+//   warps 0-3, 4-7   softmax of tile 0 and of tile 1: thread = row = TMEM lane
+//   warps 8-11       keys and values: 16-byte pieces of codes from the cache's blocks into registers, a
+//                    tile ahead; FP16 into a two-stage ring in shared memory (128-byte swizzle)
+//   warp 12          issues the products (one thread): while tile 0's softmax runs, tile 1's
+//                    products do
+//   warp 13          finds the CTA's units and hands them on through a ring
+//
+// Scales act in FP32 where they can: a key block's on the scores.  A value block's cannot act
+// behind the product, whose sum runs over blocks, nor inside P or V as it is, which FP16's range
+// would not take; so P carries it as a power: P = 2^(s + log2|v_scale| - reference) with the
+// reference the running maximum of that sum, which is what the terms p v_scale are relative to
+// the largest.  The sum of p itself is formed per block from P / |v_scale|.
+//
+// The reference may lag behind the maximum by 2^kLazy before O is multiplied up (in TMEM), and
+// P is held times 2^kLift, so that its 11 bits reach down to 2^-25 of the largest term.
+//
+// Units are shared out evenly over the CTAs by their tiles of 128 tokens (a unit's start and end
+// count as kUnitCost more), whatever the lengths: a CTA's share may begin and end inside a unit, whose
+// parts are then joined, in CTA order, by a second kernel.
 #include <cfloat>
 
 #include "common.cuh"
@@ -14,93 +42,901 @@
 namespace fp8gemm {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTileRows = 128, kUnitRows = 2 * kTileRows;
+constexpr int kTok = 128;   // tokens of a tile
+constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of one instruction
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
+// 2 x 184 + 96 + 48 = 512 registers a lane of the four sub-partitions = 65536 / 128
+constexpr uint32_t kSoftRegs = 184, kConvRegs = 96, kLowRegs = 48;
+static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
+constexpr int kStages = 2;  // of keys and of values
+constexpr int kTabs = 4;    // tiles' scales
+constexpr int kRing = 4;    // units
+constexpr int kUnitCost = 3;  // what a unit's start and end cost, in tiles
+constexpr int kMinShare = 4;  // tiles of a CTA's share, at least
+constexpr float kLazy = 4.f, kLift = 11.f;
+constexpr uint32_t kSCol = 0, kOCol = 256;  // TMEM columns: S of tile i at 128 i, O at 256 + 128 i
+
+// A part of a unit: tokens 128 j0 .. 128 j1 - 1 of what its rows see.
+enum { kEnd = -1, kWhole = 0, kLater = 1, kFirst = 2 };  // kLater, kFirst: which of the CTA's two slots
+struct Unit {
+  int kind;
+  int head, b;
+  int t0, n;        // the sequence's new tokens
+  int len;          // its tokens
+  int row0, rows;   // rows of the sequence: token * group + query head
+  int j0, j1;
+  int bad;          // values that are not finite were hidden in tiles that some rows do not see whole
+  float vref;       // value scale that the sums of p are relative to
+};
+
+// What the join has to know of a unit that CTA c begins and others go on with.
+struct Split {
+  int parts;  // 0: none
+  int head, t0, row0, rows;
+};
+
+struct Tab {  // 16 tokens' scales
+  float k;        // of the keys
+  float add;      // log2 |v_scale| (of 1 for scales of 0 and such as are not finite), -infinity without a block
+  float per;      // vref / |v_scale|
+  uint32_t mode;  // what becomes of the values' codes: see kZero, kNegate, kNotFinite
+};
+enum : uint32_t { kZero = 1, kNegate = 2, kNotFinite = 4 };
+
+// Tokens that row r of a sequence sees.
+__device__ __forceinline__ int row_limit(const KvChunkArgs& a, int len, int n, int r) {
+  return a.causal ? max(0, len - n + 1 + r / a.group) : len;
+}
+__device__ __forceinline__ int unit_tiles(const KvChunkArgs& a, int len, int n, int u) {
+  const int last = min(n * a.group, (u + 1) * kUnitRows) - 1;
+  return (row_limit(a, len, n, last) + kTok - 1) / kTok;
+}
+
+struct Seq {
+  int t0, n, len;
+};
+// Sequence b; n = 0 where its offsets are out of order, len = 0 where its length is.
+__device__ __forceinline__ Seq sequence(const KvChunkArgs& a, int b, int* status) {
+  Seq s = {0, 0, 0};
+  if (b >= a.B) return s;
+  bool ok = sequence_tokens(a.cu, b, a.B, a.T, a.max_q, &s.t0, &s.n);
+  if (!ok) s.n = 0;
+  s.len = a.lens[b];
+  if (s.len < 0 || (long long)s.len > (long long)a.width * a.block) {
+    s.len = 0;
+    ok = false;
+  }
+  if (!ok) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+  return s;
+}
+__device__ __forceinline__ int units_of(const KvChunkArgs& a, int n) {
+  return (n * a.group + kUnitRows - 1) / kUnitRows;
+}
+
+__device__ __forceinline__ long long shfl_up_ll(long long v, int o) { return __shfl_up_sync(0xffffffffu, v, o); }
+
+// What the units of the lane's sequence cost together; called by whole warps.
+__device__ __forceinline__ long long sequence_cost(const KvChunkArgs& a, const Seq& s, int lane) {
+  const int units = units_of(a, s.n);
+  long long w = 0;
+  if (units <= 4)
+    for (int u = 0; u < units; ++u) w += unit_tiles(a, s.len, s.n, u) + kUnitCost;
+  uint32_t many = __ballot_sync(0xffffffffu, units > 4);
+  while (many) {  // the lanes share a long sequence's
+    const int l = __ffs(many) - 1;
+    many &= many - 1;
+    const int n = __shfl_sync(0xffffffffu, s.n, l), len = __shfl_sync(0xffffffffu, s.len, l);
+    long long sum = 0;
+    for (int u = lane; u < units_of(a, n); u += 32) sum += unit_tiles(a, len, n, u) + kUnitCost;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == l) w = sum;
+  }
+  return w;
+}
+
+// The CTA's share of the work: [lo, hi) of the heads' lists of units, one list after the other.
+struct Share {
+  long long lo, hi, list, total;  // list: what one head's units cost
+  int ctas;
+  int b;               // where it begins: sequence, and cost of its units before
+  long long off;
+};
+__device__ long long first_of(long long total, int ctas, int c) { return total / ctas * c + total % ctas * c / ctas; }
+
+__device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, int* status) {
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  long long list = 0;
+  Seq s = {0, 0, 0};
+  long long w = 0, upto = 0;  // the thread's sequence and the cost up to its end (last round)
+  int base = 0;
+  // one round of 512 sequences: costs and their running sum
+  auto round = [&]() {
+    s = sequence(a, base + tid, status);
+    w = sequence_cost(a, s, lane);
+    upto = w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = shfl_up_ll(upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    long long all = 0;
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) upto += sums[i];
+      all += sums[i];
+    }
+    __syncthreads();
+    return all;
+  };
+  for (base = 0; base < a.B; base += kThreads) list += round();
+  const long long total = list * a.heads;
+  Share sh;
+  sh.list = list;
+  sh.total = total;
+  sh.ctas = int(min((long long)gridDim.x, max(1LL, total / kMinShare)));
+  sh.b = 0;
+  sh.off = 0;
+  const int c = blockIdx.x;
+  sh.lo = c < sh.ctas ? first_of(total, sh.ctas, c) : total;
+  sh.hi = c < sh.ctas ? first_of(total, sh.ctas, c + 1) : total;
+  if (tid == 0) *out = sh;
+  __syncthreads();
+  if (sh.lo >= sh.hi) return;
+  const long long at = sh.lo % list;
+  long long before = 0;
+  for (base = 0; base < a.B; base += kThreads) {
+    const long long all = a.B > kThreads ? round() : list;  // (one round: the first one's are still there)
+    if (at < before + all) {
+      if (at >= before + upto - w && at < before + upto) {
+        out->b = base + tid;
+        out->off = at - (before + upto - w);
+      }
+      break;
+    }
+    before += all;
+  }
+  __syncthreads();
+}
+
+template <int kDim>
+struct Smem {
+  static constexpr int kTileBytes = kTok * kDim * 2;         // 128 rows of FP16
+  static constexpr int kSubBytes = kTok * 128;
+  static constexpr size_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + kStages * kTileBytes;
+  static constexpr size_t kTab = kV + kStages * kTileBytes;
+  static constexpr size_t kUnits = kTab + kTabs * kGroups * sizeof(Tab);
+  static constexpr size_t kBars = kUnits + kRing * 64;
+  static constexpr size_t kBytes = 1024 + kBars + 512;
+  static_assert(sizeof(Unit) <= 64, "ring slot");
+  static_assert(kBytes <= 232448, "227 KB of shared memory per CTA");
+};
+
+struct Bars {
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t tab_full[kTabs];
+  uint64_t ring_full[kRing], ring_empty[kRing];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier area");
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 16-byte chunk c of a row of the 64-element tiles that make up one of FP16.
+template <int kDim>
+__device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
+  return tile + (c / 8) * Smem<kDim>::kSubBytes + row * 128 + (((c % 8) ^ (row & 7)) << 4);
+}
+
+// A row of Q into shared memory as FP16 times a power of two that brings its largest element
+// into [2^10, 2^11); returns the reciprocal of that power.
+template <int kDim>
+__device__ __forceinline__ float stage_query(uint8_t* tile, int row, const __nv_bfloat16* q) {
+  Raw8<__nv_bfloat16> raw[kDim / 8];
+  float top = 0.f;
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) {
+    zero8(raw[c]);
+    if (q) raw[c] = load8(q + 8 * c);
+  }
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) {
+    float f[8];
+    unpack8(raw[c], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+  }
+  // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
+  const int exp = max(int(__float_as_uint(top) >> 23), 10);
+  const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) {
+    float f[8];
+    unpack8(raw[c], f);
+    *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c)) =
+        make_uint4(f16x2_bits(f[0] * up, f[1] * up), f16x2_bits(f[2] * up, f[3] * up),
+                   f16x2_bits(f[4] * up, f[5] * up), f16x2_bits(f[6] * up, f[7] * up));
+  }
+  return __uint_as_float(uint32_t(exp - 10) << 23);
+}
+
+// Bits of the bytes of a word that are no finite number (0xff in each).
+template <bool kE5M2>
+__device__ __forceinline__ uint32_t not_finite4(uint32_t w) {
+  constexpr uint32_t kBad = kE5M2 ? 0x7c7c7c7cu : 0x7f7f7f7fu;
+  return __vcmpeq4(w & kBad, kBad);
+}
+
+// Block of token tok of the unit's sequence, -1 where there is none.
+__device__ __forceinline__ int block_of(const KvChunkArgs& a, int b, int tok, int vis, int* status) {
+  if (tok >= vis) return -1;
+  const int blk = a.table[(long long)b * a.width + (tok >> a.log_block)];
+  if (blk >= 0 && blk < a.num_blocks) return blk;
+  raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+  return -1;
+}
+
+// Dimensions of tokens from .. to - 1 of which some value is not finite: bit d of `mask`.
+template <int kDim, bool kE5M2>
+__device__ __noinline__ void find_not_finite(const KvChunkArgs& a, int b, int head, int from, int to,
+                                             int* status, uint32_t (&mask)[kDim / 32]) {
+  for (int tok = from; tok < to; ++tok) {
+    const int blk = block_of(a, b, tok, to, status);
+    if (blk < 0) continue;
+    const long long tile = (long long)blk * a.heads + head;
+    const bool all = !(fabsf(a.vs[tile]) <= FLT_MAX);
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(a.vc + (tile * a.block + (tok & (a.block - 1))) * kDim);
+#pragma unroll
+    for (int w = 0; w < kDim / 4; ++w) {
+      const uint32_t m = all ? 0xffffffffu : not_finite4<kE5M2>(v[w]);
+      // one bit of each byte, side by side
+      mask[w / 8] |= ((m & 1u) | (m >> 7 & 2u) | (m >> 14 & 4u) | (m >> 21 & 8u)) << (w % 8 * 4);
+    }
+  }
+}
 
 template <int kDim, bool kE5M2>
-__global__ void __launch_bounds__(32 * kWarps) kv_chunk_kernel(const KvChunkArgs a, int* status) {
-  __shared__ float q_smem[kWarps][kDim];
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_chunk_kernel(const __grid_constant__ KvChunkArgs a, float* parts, Split* splits, int* status) {
+  using S = Smem<kDim>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Tab* tabs = reinterpret_cast<Tab*>(smem + S::kTab);
+  auto ring = [&](int slot) { return reinterpret_cast<Unit*>(smem + S::kUnits + 64 * slot); };
+  Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
+  volatile int* abort_flag = &bar.abort;
+  __shared__ Share share;
+  __shared__ long long sums[kThreads / 32];
+
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hq = a.heads * a.group;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.k_full[i], 4);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 4);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 4);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.o_full[i], 1);
+    }
+    for (int i = 0; i < kTabs; ++i) mbar_init(&bar.tab_full[i], 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar.ring_full[i], 1);
+      mbar_init(&bar.ring_empty[i], 8 + 4 + 1);
+    }
+    mbar_init(&bar.drain, 1);
+    bar.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
   griddep_launch_dependents();
   griddep_wait();
-  const long long row = (long long)blockIdx.x * kWarps + warp;
-  if (row >= (long long)a.T * hq) return;
-  const int t = int(row / hq), head = int(row % hq), hk = head / a.group;
-  int b, t0, n;
-  if (a.cu) {
-    b = find_sequence(a.cu, a.B, t, lane);
-    if (b == -1) return;
-    if (b == -2 || !sequence_tokens(a.cu, b, a.B, a.T, a.max_q, &t0, &n)) {
-      raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-      return;
+  find_share(a, &share, sums, status);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+
+  auto fail = [&]() {
+    *abort_flag = 1;
+    raise_status(status, FP8GEMM_ERR_TIMEOUT);
+  };
+  // a whole warp's wait has one outcome
+  auto warp_wait = [&](uint64_t* b, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_within(b, parity, abort_flag, a.wait_ns));
+    if (!ok) fail();
+    return ok;
+  };
+  auto thread_wait = [&](uint64_t* b, uint32_t parity) {
+    const bool ok = mbar_wait_within(b, parity, abort_flag, a.wait_ns);
+    if (!ok) fail();
+    return ok;
+  };
+
+  if (warp < kConvWarp) {
+    // ------------------------------------------------------------ softmax
+    regs_increase<kSoftRegs>();
+    const int i = warp / 4;                  // the tile
+    const int row = (warp % 4) * 32 + lane;  // of the tile: TMEM lane
+    const uint32_t lanes = uint32_t((warp % 4) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + kSCol + 128 * i, o_at = tmem + lanes + kOCol + 128 * i;
+    uint8_t* q_tile = smem + S::kQ + i * S::kTileBytes;
+    uint32_t it = 0;     // tiles of tokens, as all roles count them
+    uint32_t mine = 0;   // those in which this tile of rows took part
+    for (uint32_t taken = 0;; ++taken) {
+      const int slot = taken % kRing;
+      if (!warp_wait(&bar.ring_full[slot], (taken / kRing) & 1)) break;
+      const Unit* u = ring(slot);
+      const int kind = u->kind, rows = u->rows, j0 = u->j0, j1 = u->j1;
+      if (kind == kEnd) break;
+      if (rows <= kTileRows * i) {  // no rows for this tile
+        it += j1 - j0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
+        continue;
+      }
+      const int r = kTileRows * i + row;  // row of the unit
+      const bool row_ok = r < rows;
+      const int seq_row = u->row0 + r, token = u->t0 + seq_row / a.group;
+      const int head = u->head * a.group + seq_row % a.group;
+      const int limit = row_ok ? row_limit(a, u->len, u->n, seq_row) : 0x7fffffff;
+      const int least = __shfl_sync(0xffffffffu, limit, 0);  // rows see more and more
+      float ref = 0.f, sum = 0.f;
+      bool unset = true;
+      if (j1 > j0) {
+        const float down = stage_query<kDim>(
+            q_tile, row, row_ok ? a.Q + (long long)token * a.ld_q + (long long)head * kDim : nullptr);
+        const float q_mul = down * (a.scale * 1.44269504088896341f);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_full[i]);
+        bool ok = true;
+        for (int j = j0; j < j1; ++j, ++it, ++mine) {
+          const Tab* tab = tabs + (it % kTabs) * kGroups;
+          // (in this order: a tile of rows that sat out a unit may be ahead of the scales' ring, but
+          // its own scores are there only once the tile's scales are)
+          if (!(ok = warp_wait(&bar.s_full[i], mine & 1))) break;
+          if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
+          tc_fence_after();
+          uint32_t c[128];
+          tmem_ld_32x32b_x64(s_at, *reinterpret_cast<uint32_t(*)[64]>(&c[0]));
+          tmem_ld_32x32b_x64(s_at + 64, *reinterpret_cast<uint32_t(*)[64]>(&c[64]));
+          tmem_ld_wait_tied(*reinterpret_cast<uint32_t(*)[32]>(&c[0]));
+          reg_tie32(&c[32]);
+          reg_tie32(&c[64]);
+          reg_tie32(&c[96]);
+          float2 x[64];  // scores in powers of two, with the value scale's, less the reference
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) {
+            const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              x[8 * g + e] = __ffma2_rn(
+                  make_float2(__uint_as_float(c[16 * g + 2 * e]), __uint_as_float(c[16 * g + 2 * e + 1])),
+                  make_float2(mul, mul), make_float2(add, add));
+          }
+          const int tok = j * kTok;
+          if (tok + kTok > least) {  // the same for the warp
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              if (tok + 2 * e >= limit) x[e].x = -INFINITY;
+              if (tok + 2 * e + 1 >= limit) x[e].y = -INFINITY;
+            }
+          }
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e) top4[e % 4] = max3(top4[e % 4], x[e].x, x[e].y);
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          const bool rises = unset ? top > -INFINITY : top > kLift + kLazy;
+          if (__any_sync(0xffffffffu, rises)) {
+            // by how much the reference rises; the first score that is there sets it
+            float up = 0.f, shrink = 1.f;
+            if (unset) {
+              if (top > -INFINITY) up = top - kLift;
+            } else {
+              up = fmaxf(top - kLift, 0.f);
+              shrink = exp2_fast(-up);
+            }
+            unset = unset && !(top > -INFINITY);
+            ref += up;
+            sum *= shrink;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              x[e].x -= up;
+              x[e].y -= up;
+            }
+            if (j > j0 && __any_sync(0xffffffffu, shrink != 1.f)) {
+              if (!(ok = warp_wait(&bar.o_full[i], (mine - 1) & 1))) break;
+              tc_fence_after();
+#pragma unroll
+              for (int d = 0; d < kDim; d += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(o_at + d, o);
+                tmem_ld_wait_tied16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+                tmem_st_32x32b_x16(o_at + d, o);
+              }
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int g = 0; g < kGroups / 2; ++g) {
+              float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float2 v = x[32 * h + 8 * g + e];
+                v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                s2 = __fadd2_rn(s2, v);
+                p[8 * g + e] = f16x2_bits(v.x, v.y);
+              }
+              sum = fmaf(s2.x + s2.y, tab[4 * h + g].per, sum);
+            }
+            tmem_st_32x32b_x32(s_at + 32 * h, p);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[i]);
+        }
+        if (!ok || !warp_wait(&bar.o_full[i], (mine - 1) & 1)) break;
+        tc_fence_after();
+      }
+      // ---- the rows' end: whole units go to O, parts to the workspace
+      const float vref = u->vref;
+      uint32_t lost[kDim / 32] = {};
+      if (u->bad) {
+        const int from = row_limit(a, u->len, u->n, u->row0) / kTok * kTok;
+        if (row_ok)
+          find_not_finite<kDim, kE5M2>(a, u->b, u->head, max(from, j0 * kTok), min(limit, j1 * kTok), status, lost);
+      }
+      const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
+      float* part = parts + (size_t(blockIdx.x) * 2 + (kind == kFirst)) * (kUnitRows * (kDim + 4));
+#pragma unroll
+      for (int d = 0; d < kDim; d += 32) {
+        uint32_t o[32];
+        if (j1 > j0) {
+          tmem_ld_32x32b_x32(o_at + d, o);
+          tmem_ld_wait_tied(o);
+        }
+        if (row_ok && kind == kWhole) {
+          __nv_bfloat16* out = a.O + ((long long)token * a.heads * a.group + head) * kDim + d;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float v[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              v[y] = f == 0.f ? 0.f : __uint_as_float(o[e + y]) * f * vref;
+              if (lost[d / 32] >> (e + y) & 1u) v[y] = NAN;
+            }
+            Raw8<__nv_bfloat16> w;
+            pack8(v, w);
+            store8(out + e, w);
+          }
+        } else if (row_ok) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                   __uint_as_float(o[e + 3]));
+            if (lost[d / 32] >> e & 1u) v.x = NAN;
+            if (lost[d / 32] >> e & 2u) v.y = NAN;
+            if (lost[d / 32] >> e & 4u) v.z = NAN;
+            if (lost[d / 32] >> e & 8u) v.w = NAN;
+            *reinterpret_cast<float4*>(part + size_t(r) * kDim + d + e) = v;
+          }
+        }
+        __syncwarp();
+      }
+      if (kind != kWhole && row_ok)
+        *reinterpret_cast<float4*>(part + size_t(kUnitRows) * kDim + 4 * r) =
+            make_float4(unset ? -INFINITY : ref, sum, vref, 0.f);
+      tc_fence_before();  // O has been read before its next product, which waits for P
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------------- keys and values
+    regs_decrease<kConvRegs>();
+    const int ct = threadIdx.x - 32 * kConvWarp;
+    constexpr int kPieces = kDim / 16;          // 16-byte pieces of a token's codes
+    constexpr int kRowsAtOnce = 128 / kPieces;  // tokens that the 128 threads cover at once
+    constexpr int kLoads = kTok / kRowsAtOnce;
+    const int piece = ct % kPieces, row0 = ct / kPieces;
+    uint32_t it = 0;
+    for (uint32_t taken = 0;; ++taken) {
+      const int slot = taken % kRing;
+      if (!warp_wait(&bar.ring_full[slot], (taken / kRing) & 1)) break;
+      Unit* u = ring(slot);
+      if (u->kind == kEnd) break;
+      const int b = u->b, head = u->head, j0 = u->j0, j1 = u->j1;
+      const int first = row_limit(a, u->len, u->n, u->row0);                // what the first row sees
+      const int vis = row_limit(a, u->len, u->n, u->row0 + u->rows - 1);    // and the last
+      int ids[kLoads];
+      uint4 kr[kLoads], vr[kLoads];
+      auto load_ids = [&](int j) {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          ids[l] = j < j1 ? block_of(a, b, j * kTok + row0 + kRowsAtOnce * l, vis, status) : -1;
+      };
+      auto load_codes = [&](const uint8_t* cache, int j, uint4 (&x)[kLoads]) {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) {
+          x[l] = make_uint4(0u, 0u, 0u, 0u);
+          const int tok = j * kTok + row0 + kRowsAtOnce * l;
+          if (ids[l] >= 0)
+            x[l] = __ldg(reinterpret_cast<const uint4*>(
+                cache + (((long long)ids[l] * a.heads + head) * a.block + (tok & (a.block - 1))) * kDim + 16 * piece));
+        }
+      };
+      // the scales of 16 tokens, by the first eight lanes
+      float ks = 0.f, vs = 0.f;
+      bool there = false;
+      auto load_scales = [&](int j) {
+        there = false;
+        if (ct < kGroups && j < j1) {
+          const int blk = block_of(a, b, j * kTok + 16 * ct, vis, status);
+          there = blk >= 0;
+          if (there) {
+            ks = a.ks[(long long)blk * a.heads + head];
+            vs = a.vs[(long long)blk * a.heads + head];
+          }
+        }
+      };
+      load_ids(j0);
+      load_scales(j0);
+      load_codes(a.kc, j0, kr);
+      load_codes(a.vc, j0, vr);
+      load_ids(j0 + 1);
+      float vref = 1.f;
+      bool ok = true;
+      for (int j = j0; j < j1; ++j, ++it) {
+        const int st = it % kStages;
+        const uint32_t ph = (it / kStages) & 1;
+        if (!(ok = warp_wait(&bar.k_empty[st], ph ^ 1))) break;
+        if (warp == kConvWarp) {  // the tile's scales (its place was read long ago: see kTabs)
+          const bool fin = fabsf(vs) <= FLT_MAX;
+          const float av = there && fin && vs != 0.f ? fabsf(vs) : 1.f;
+          if (j == j0) {
+            vref = __shfl_sync(0xffffffffu, av, 0);
+            if (lane == 0) {
+              u->vref = vref;
+            }
+          }
+          if (lane < kGroups) {
+            Tab t;
+            t.k = there ? ks : 0.f;
+            t.add = there ? log2f(av) : -INFINITY;
+            t.per = there ? __fdiv_rn(vref, av) : 0.f;
+            t.mode = !there ? 0u : !fin ? kNotFinite : vs == 0.f ? kZero : vs < 0.f ? kNegate : 0u;
+            tabs[(it % kTabs) * kGroups + lane] = t;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.tab_full[it % kTabs]);
+          load_scales(j + 1);
+        }
+        uint8_t* kt = smem + S::kK + st * S::kTileBytes;
+        uint8_t* vt = smem + S::kV + st * S::kTileBytes;
+        // a piece becomes two chunks; lanes of the second half of the dimensions write theirs in the other
+        // order, so that eight lanes meet all banks
+        auto put = [&](uint8_t* tile, int row, uint4 codes, uint32_t keep, uint32_t flip) {
+          const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[2 * e] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e])) & keep) ^ flip;
+            h[2 * e + 1] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16)) & keep) ^ flip;
+          }
+          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+          const bool swap = kDim == 128 && piece >= 4;
+          *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece + swap)) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece + !swap)) = swap ? lo : hi;
+        };
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) put(kt, row0 + kRowsAtOnce * l, kr[l], 0xffffffffu, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.k_full[st]);
+        load_codes(a.kc, j + 1, kr);
+        if (!(ok = warp_wait(&bar.v_empty[st], ph ^ 1))) break;
+        if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
+        const bool mixed = (j + 1) * kTok > first;  // some row does not see all of it
+        uint32_t bad = 0u;
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) {
+          const int r = row0 + kRowsAtOnce * l;
+          const uint32_t mode = tabs[(it % kTabs) * kGroups + r / 16].mode;
+          uint32_t keep = mode & kZero ? 0u : 0xffffffffu;
+          uint32_t flip = mode & kNegate ? 0x80008000u : 0u;
+          uint4 x = vr[l];
+          if (mode & kNotFinite) {
+            keep = 0u;
+            if (!mixed)
+              flip = 0x7fff7fffu;
+            else if (j * kTok + r < vis)
+              bad = 1u;
+          } else if (mixed) {
+            // 0 times what is not finite would reach rows that do not see it: they get 0 here, and the rows
+            // that do see it are marked when the unit ends
+            const uint32_t m[4] = {not_finite4<kE5M2>(x.x), not_finite4<kE5M2>(x.y), not_finite4<kE5M2>(x.z),
+                                   not_finite4<kE5M2>(x.w)};
+            bad |= m[0] | m[1] | m[2] | m[3];
+            x = make_uint4(x.x & ~m[0], x.y & ~m[1], x.z & ~m[2], x.w & ~m[3]);
+          }
+          put(vt, r, x, keep, flip);
+        }
+        if (bad != 0u) u->bad = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.v_full[st]);
+        load_codes(a.vc, j + 1, vr);
+        load_ids(j + 2);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------- the products
+    regs_decrease<kLowRegs>();
+    if (lane == 0) {
+      constexpr uint32_t kDescS = idesc_f16_f32(kTileRows, kTok, false);
+      constexpr uint32_t kDescO = idesc_f16_f32(kTileRows, kDim, true);
+      const uint32_t q_at = smem_addr(smem + S::kQ), k_at = smem_addr(smem + S::kK), v_at = smem_addr(smem + S::kV);
+      uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+      bool issued = false;
+      auto scores = [&](int i, int st) {
+#pragma unroll
+        for (int k = 0; k < kDim / 16; ++k) {
+          const uint32_t off = (k / 4) * S::kSubBytes + (k % 4) * 32;
+          umma_f16(tmem + kSCol + 128 * i, smem_desc_sw128_kmajor(q_at + i * S::kTileBytes + off),
+                   smem_desc_sw128_kmajor(k_at + st * S::kTileBytes + off), kDescS, k > 0 ? 1u : 0u);
+        }
+        umma_commit(&bar.s_full[i]);
+        issued = true;
+      };
+      auto values = [&](int i, int st, bool first) {
+#pragma unroll
+        for (int k = 0; k < kTok / 16; ++k)
+          umma_f16_ta(tmem + kOCol + 128 * i, tmem + kSCol + 128 * i + 8 * k,
+                      smem_desc_sw128_mnmajor(v_at + st * S::kTileBytes + k * 2048, S::kSubBytes), kDescO,
+                      first && k == 0 ? 0u : 1u);
+        umma_commit(&bar.o_full[i]);
+      };
+      bool ok = true;
+      for (uint32_t taken = 0; ok; ++taken) {
+        const int slot = taken % kRing;
+        if (!thread_wait(&bar.ring_full[slot], (taken / kRing) & 1)) break;
+        const Unit* u = ring(slot);
+        const int kind = u->kind, n = u->j1 - u->j0, tiles = u->rows > kTileRows ? 2 : 1;
+        if (kind == kEnd) break;
+        if (n > 0) {
+          ok = thread_wait(&bar.k_full[it % kStages], (it / kStages) & 1);
+          for (int i = 0; i < tiles && ok; ++i) {
+            ok = thread_wait(&bar.q_full[i], n_q[i]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(i, it % kStages);
+          }
+          if (ok) umma_commit(&bar.k_empty[it % kStages]);
+        }
+        for (int j = 0; j < n && ok; ++j, ++it) {
+          const int st = it % kStages, st1 = (it + 1) % kStages;
+          ok = thread_wait(&bar.v_full[st], (it / kStages) & 1);
+          for (int i = 0; i < tiles && ok; ++i) {
+            ok = thread_wait(&bar.p_full[i], n_p[i]++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            values(i, st, j == 0);
+            if (j + 1 < n) {
+              if (i == 0) ok = thread_wait(&bar.k_full[st1], ((it + 1) / kStages) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              scores(i, st1);
+            }
+          }
+          if (!ok) break;
+          umma_commit(&bar.v_empty[st]);
+          if (j + 1 < n) umma_commit(&bar.k_empty[st1]);
+        }
+        if (ok) mbar_arrive(&bar.ring_empty[slot]);
+      }
+      if (issued) {  // every issued product has finished before TMEM is released
+        umma_commit(&bar.drain);
+        mbar_drain(&bar.drain, 0);
+      }
     }
   } else {
-    sequence_tokens(a.cu, t / (a.T / a.B), a.B, a.T, a.max_q, &t0, &n);
-    b = t / n;
+    regs_decrease<kLowRegs>();
+    if (warp == kPlanWarp) {
+      // ------------------------------------------------- units of the CTA's share
+      Split split = {0, 0, 0, 0, 0};
+      uint32_t given = 0;
+      bool ok = true;
+      auto give = [&](const Unit& unit) {
+        const int slot = given % kRing;
+        if (!warp_wait(&bar.ring_empty[slot], ((given / kRing) & 1) ^ 1)) return false;
+        if (lane == 0) {
+          *ring(slot) = unit;
+          mbar_arrive(&bar.ring_full[slot]);
+        }
+        ++given;
+        return true;
+      };
+      const long long lo = share.lo, hi = share.hi;
+      if (lo < hi) {
+        long long at = lo, off = share.off;  // off: cost before `at` within the sequence, then the unit
+        int head = int(lo / share.list), b = share.b, un = 0;
+        Seq s = sequence(a, b, status);
+        // the unit that holds the offset, 32 at a time
+        while (true) {
+          const int u = un + lane;
+          const int w = u < units_of(a, s.n) ? unit_tiles(a, s.len, s.n, u) + kUnitCost : 0;
+          int upto = w;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, off < upto);
+          if (past) {
+            const int l = __ffs(past) - 1;
+            off -= __shfl_sync(0xffffffffu, upto - w, l);
+            un += l;
+            break;
+          }
+          off -= __shfl_sync(0xffffffffu, upto, 31);
+          un += 32;
+          if (un >= units_of(a, s.n)) break;  // (cannot be: the offset lies in the sequence)
+        }
+        while (at < hi && ok) {
+          while (un >= units_of(a, s.n)) {  // on to the next sequence, or the next head's list
+            un = 0;
+            if (++b == a.B) {
+              b = 0;
+              ++head;
+            }
+            s = sequence(a, b, status);
+          }
+          const int tiles = unit_tiles(a, s.len, s.n, un);
+          const long long cost = tiles + kUnitCost, begin = at - off;
+          const long long x1 = min(cost, off + (hi - at));
+          Unit unit;
+          unit.head = head;
+          unit.b = b;
+          unit.t0 = s.t0;
+          unit.n = s.n;
+          unit.len = s.len;
+          unit.row0 = un * kUnitRows;
+          unit.rows = min(kUnitRows, s.n * a.group - unit.row0);
+          unit.j0 = int(max(0LL, off - kUnitCost));
+          unit.j1 = int(max(0LL, x1 - kUnitCost));
+          unit.bad = 0;
+          unit.vref = 1.f;
+          unit.kind = unit.j0 > 0 ? kLater : unit.j1 < tiles ? kFirst : kWhole;
+          if (tiles == 0 ? off == 0 : unit.j1 > unit.j0) {
+            if (unit.kind == kFirst) {
+              const long long end = begin + cost;  // its parts: this CTA's and those that begin before its end
+              int last = blockIdx.x;
+              while (last + 1 < share.ctas && first_of(share.total, share.ctas, last + 1) < end) ++last;
+              split = {last - int(blockIdx.x) + 1, head, s.t0, unit.row0, unit.rows};
+            }
+            ok = give(unit);
+          }
+          at += x1 - off;
+          off = 0;
+          ++un;
+        }
+      }
+      if (lane == 0) splits[blockIdx.x] = split;
+      Unit end = {};
+      end.kind = kEnd;
+      if (ok) give(end);
+    }
   }
-  int len = a.lens[b];
-  if (len < 0 || (long long)len > (long long)a.width * a.block) {
-    raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-    len = 0;
+
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  const int sees = a.causal ? len - n + 1 + (t - t0) : len;
-  for (int d = lane; d < kDim; d += 32) q_smem[warp][d] = __bfloat162float(a.Q[t * a.ld_q + head * kDim + d]);
-  __syncwarp();
+}
+
+// Joins the parts of the unit that CTA blockIdx.x of the kernel above began: a warp for each row, in
+// the order of the CTAs.
+constexpr int kJoinWarps = 8, kJoinY = kUnitRows / kJoinWarps;
+template <int kDim>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_chunk_join_kernel(const __grid_constant__ KvChunkArgs a,
+                                                                        const float* __restrict__ parts,
+                                                                        const Split* __restrict__ splits) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const Split s = splits[blockIdx.x];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int r = blockIdx.y * kJoinWarps + warp;
+  if (s.parts == 0 || r >= s.rows) return;
+  constexpr size_t kSlot = size_t(kUnitRows) * (kDim + 4);
+  const float* first = parts + (size_t(blockIdx.x) * 2 + 1) * kSlot;
+  auto part = [&](int p) { return p == 0 ? first : parts + size_t(blockIdx.x + p) * 2 * kSlot; };
+  auto stat = [&](int p) { return *reinterpret_cast<const float4*>(part(p) + size_t(kUnitRows) * kDim + 4 * r); };
+  float top = -INFINITY;
+  for (int p = 0; p < s.parts; ++p) top = max_nan(top, stat(p).x);
+  const float vref = stat(0).z;
   constexpr int kPer = kDim / 32;
-  float o[kPer] = {}, m = -INFINITY, l = 0.f;
-  for (int base = 0; base < sees; base += 32) {
-    const int j = base + lane;
-    float x = -INFINITY;
-    int blk = -1;
-    if (j < sees) {
-      blk = a.table[(long long)b * a.width + j / a.block];
-      if (blk < 0 || blk >= a.num_blocks) {
-        raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-        blk = -1;
-      }
-    }
-    const long long tile = (long long)blk * a.heads + hk;
-    if (blk >= 0) {
-      const uint8_t* k = a.kc + (tile * a.block + j % a.block) * kDim;
-      float dot = 0.f;
-      for (int d = 0; d < kDim; d += 2) {
-        const float2 v = f8x2_to_float2<kE5M2>(*reinterpret_cast<const uint16_t*>(k + d));
-        dot = fmaf(v.x, q_smem[warp][d], dot);
-        dot = fmaf(v.y, q_smem[warp][d + 1], dot);
-      }
-      x = dot * (a.scale * a.ks[tile]);
-    }
-    float top = x;
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    top = fmaxf(top, m);
-    if (top == -INFINITY) continue;
-    const float shrink = expf(m - top), p = expf(x - top);
-    m = top;
-    l = l * shrink + warp_sum(p);
-    for (int i = 0; i < kPer; ++i) o[i] *= shrink;
-    for (int s = 0; s < 32; ++s) {
-      const int blk_s = __shfl_sync(0xffffffffu, blk, s);
-      const float ps = __shfl_sync(0xffffffffu, p, s);
-      if (blk_s < 0) continue;
-      const long long ts = (long long)blk_s * a.heads + hk;
-      const uint8_t* v = a.vc + (ts * a.block + (base + s) % a.block) * kDim;
-      const float f = a.vs[ts];
-      for (int i = 0; i < kPer; ++i)
-        o[i] = fmaf(ps, f8x2_to_float2<kE5M2>(v[lane + 32 * i]).x * f, o[i]);
-    }
+  float o[kPer] = {}, sum = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < s.parts; ++p) {
+    const float4 t = stat(p);
+    const float f = t.x == -INFINITY ? 0.f : exp2_fast(t.x - top);
+    sum = fmaf(t.y, f * __fdiv_rn(vref, t.z), sum);
+    const float* v = part(p) + size_t(r) * kDim + kPer * lane;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = fmaf(v[i], f, o[i]);
   }
-  for (int i = 0; i < kPer; ++i)
-    a.O[(row)*kDim + lane + 32 * i] = __float2bfloat16(l > 0.f || isnan(l) ? o[i] / l : 0.f);
+  const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
+  const int row = s.row0 + r;
+  __nv_bfloat16* out = a.O + (((long long)s.t0 + row / a.group) * a.heads * a.group + s.head * a.group + row % a.group) * kDim +
+                       kPer * lane;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = f == 0.f ? 0.f : o[i] * f * vref;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
+  else
+    *reinterpret_cast<uint32_t*>(out) = bf16x2_bits(o[0], o[1]);
+}
+
+template <int kDim, bool kE5M2>
+cudaError_t run(const LaunchCtx& c, const KvChunkArgs& a, void* ws) {
+  static SmemLimit limit;
+  auto fn = kv_chunk_kernel<kDim, kE5M2>;
+  if (cudaError_t e = limit.raise(c, reinterpret_cast<const void*>(fn), Smem<kDim>::kBytes)) return e;
+  // no more CTAs than there can be work for
+  const long long units = (long long)a.heads * ((long long)a.T * a.group / kUnitRows + a.B);
+  const long long tiles = ((long long)a.width * a.block + kTok - 1) / kTok + kUnitCost;
+  const long long most = units > c.num_sms ? c.num_sms : max(1LL, units * tiles / kMinShare);
+  const int grid = int(min((long long)c.num_sms, most));
+  Split* splits = static_cast<Split*>(ws);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + size_t(c.num_sms) * 64);
+  if (cudaError_t e = launch_dependent(c, fn, grid, kThreads, Smem<kDim>::kBytes, a, parts, splits, c.status)) return e;
+  return launch_dependent(c, kv_chunk_join_kernel<kDim>, dim3(grid, kJoinY), 32 * kJoinWarps, 0, a, parts, splits);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a) {
-  const long long rows = (long long)a.T * a.heads * a.group;
+// Two parts of a unit for each CTA, at dim 128: the same for every call, so that a stream's buffer stays
+// where it is.
+size_t kv_chunk_workspace_bytes(const LaunchCtx& c) {
+  static_assert(sizeof(Split) <= 64, "split record");
+  return size_t(c.num_sms) * (64 + 2 * size_t(kUnitRows) * (128 + 4) * 4);
+}
+
+cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws) {
   const bool e5 = a.fmt == FP8GEMM_FMT_E5M2;
-  auto fn = a.dim == 128 ? (e5 ? kv_chunk_kernel<128, true> : kv_chunk_kernel<128, false>)
-                         : (e5 ? kv_chunk_kernel<64, true> : kv_chunk_kernel<64, false>);
-  return launch_dependent(c, fn, unsigned((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, a, c.status);
+  if (a.dim == 128) return e5 ? run<128, true>(c, a, ws) : run<128, false>(c, a, ws);
+  return e5 ? run<64, true>(c, a, ws) : run<64, false>(c, a, ws);
 }
 
 }  // namespace fp8gemm

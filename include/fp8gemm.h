@@ -50,8 +50,8 @@
  *    M > 64 without Q/sA keeps its quantised A in a second per-stream buffer,
  *    and fp8gemm_dense_batch and the ordered contiguous form their tile
  *    counters (and order) in small per-stream buffers; fp8_rmsnorm_backward
- *    (10 MB), fp8_kv_attention (8 MB) and fp8_moe_few (60 MB + 1 KB for each
- *    element of I) keep theirs the same way.
+ *    (10 MB), fp8_kv_attention (8 MB), fp8_kv_attention_chunk (42 MB) and
+ *    fp8_moe_few (60 MB + 1 KB for each element of I) keep theirs the same way.
  *    Such a first call must therefore not happen during CUDA graph capture.
  *    Calls on different streams never share a workspace.  Host threads may
  *    call at the same time, on one stream too: a call that needs a workspace
@@ -590,6 +590,10 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  * Layouts, cache, index arrays, refusals and what the status word says are those of
  * fp8_kv_attention; a query that sees no token gives zeros.  Rows of O that belong to no
  * sequence are left as they were.  T * group, max_q * group and table_width * block below 2^31.
+ *
+ * Work is shared out evenly over the SMs whatever the lengths; parts of a sequence's rows are
+ * joined through a per-(device, stream) workspace of one size for all calls.  Results are
+ * deterministic for given host sizes, lengths and offsets.
  */
 int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
                            const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
@@ -733,7 +737,7 @@ uint64_t fp8gemm_num_kernel_launches(void);
  * quantised-activation buffer of fp8gemm_dense_quant_a, the problem table's
  * partials, the tile counters and order of fp8gemm_dense_batch and of the
  * ordered contiguous form, and those of the norm's gradient, the cache
- * attention and the few-token MoE layer).  It first
+ * attentions and the few-token MoE layer).  It first
  * synchronises `stream`, since work enqueued there may still use them; the
  * next call that needs a workspace on that stream allocates it again.  Call
  * it before cudaStreamDestroy for streams that are retired: a stream handle
