@@ -13,8 +13,8 @@
 // two tiles' S and O fill its 512 columns -- and P takes the place of S there.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1: thread = row = TMEM lane
-//   warps 8-11       keys and values: 16-byte pieces of codes from the cache's blocks into registers, a
-//                    tile ahead; FP16 into a two-stage ring in shared memory (128-byte swizzle)
+//   warps 8-11       keys and values: codes from the cache's blocks by asynchronous copies, a
+//                    tile ahead; as FP16 into a two-stage ring in shared memory (128-byte swizzle)
 //   warp 12          issues the products (one thread): while tile 0's softmax runs, tile 1's
 //                    products do
 //   warp 13          finds the CTA's units and hands them on through a ring
@@ -25,8 +25,10 @@
 // reference the running maximum of that sum, which is what the terms p v_scale are relative to
 // the largest.  The sum of p itself is formed per block from P / |v_scale|.
 //
-// The reference may lag behind the maximum by 2^kLazy before O is multiplied up (in TMEM), and
-// P is held times 2^kLift, so that its 11 bits reach down to 2^-25 of the largest term.
+// The reference lags behind the maximum until a P passes 2^15: a first tile sets it so that its largest
+// P is 2^kLift, and O is multiplied up (in TMEM) when later ones have risen by 2^10.  P keeps its
+// 11 bits down to 2^-(14 + kLift) of the largest term and is lost below 2^-(25 + kLift) (131072
+// tokens there are 2^-13 of the sum; the output is BF16).
 //
 // Units are shared out evenly over the CTAs by their tiles of 128 tokens (a unit's start and end
 // count as kUnitCost more), whatever the lengths: a CTA's share may begin and end inside a unit, whose
@@ -47,15 +49,16 @@ constexpr int kTok = 128;   // tokens of a tile
 constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of one instruction
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
-// 2 x 184 + 96 + 48 = 512 registers a lane of the four sub-partitions = 65536 / 128
-constexpr uint32_t kSoftRegs = 184, kConvRegs = 96, kLowRegs = 48;
+// 2 x 152 + 112 + 96 = 512 registers a lane of the four sub-partitions = 65536 / 128
+constexpr uint32_t kSoftRegs = 152, kConvRegs = 112, kLowRegs = 96;
 static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
 constexpr int kStages = 2;  // of keys and of values
 constexpr int kTabs = 4;    // tiles' scales
 constexpr int kRing = 4;    // units
 constexpr int kUnitCost = 3;  // what a unit's start and end cost, in tiles
 constexpr int kMinShare = 4;  // tiles of a CTA's share, at least
-constexpr float kLazy = 4.f, kLift = 11.f;
+constexpr float kLift = 5.f;
+constexpr float kMostP = 32768.f;  // of P (FP16 ends at 65504)
 constexpr uint32_t kSCol = 0, kOCol = 256;  // TMEM columns: S of tile i at 128 i, O at 256 + 128 i
 
 // A part of a unit: tokens 128 j0 .. 128 j1 - 1 of what its rows see.
@@ -205,7 +208,8 @@ struct Smem {
   static constexpr int kTileBytes = kTok * kDim * 2;         // 128 rows of FP16
   static constexpr int kSubBytes = kTok * 128;
   static constexpr size_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + kStages * kTileBytes;
-  static constexpr size_t kTab = kV + kStages * kTileBytes;
+  static constexpr size_t kCodes = kV + kStages * kTileBytes;  // keys' and values' codes on their way
+  static constexpr size_t kTab = kCodes + 2 * kTok * kDim;
   static constexpr size_t kUnits = kTab + kTabs * kGroups * sizeof(Tab);
   static constexpr size_t kBars = kUnits + kRing * 64;
   static constexpr size_t kBytes = 1024 + kBars + 512;
@@ -421,57 +425,80 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&bar.s_full[i], mine & 1))) break;
           if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
           tc_fence_after();
-          uint32_t c[128];
-          tmem_ld_32x32b_x64(s_at, *reinterpret_cast<uint32_t(*)[64]>(&c[0]));
-          tmem_ld_32x32b_x64(s_at + 64, *reinterpret_cast<uint32_t(*)[64]>(&c[64]));
-          tmem_ld_wait_tied(*reinterpret_cast<uint32_t(*)[32]>(&c[0]));
-          reg_tie32(&c[32]);
-          reg_tie32(&c[64]);
-          reg_tie32(&c[96]);
-          float2 x[64];  // scores in powers of two, with the value scale's, less the reference
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              x[8 * g + e] = __ffma2_rn(
-                  make_float2(__uint_as_float(c[16 * g + 2 * e]), __uint_as_float(c[16 * g + 2 * e + 1])),
-                  make_float2(mul, mul), make_float2(add, add));
-          }
           const int tok = j * kTok;
-          if (tok + kTok > least) {  // the same for the warp
+          // The plain case, to which most tiles belong: all rows see all tokens, and the reference need not
+          // rise -- as is known once P is there, in registers.  (Code that runs per tile is kept
+          // short: the roles' loops have to fit in the instruction cache together.)
+          bool slow = __any_sync(0xffffffffu, unset) || tok + kTok > least;
+          if (!slow) {
+            uint32_t p[64], c[2][32];
+            float part = 0.f, most = 0.f;
+            tmem_ld_32x32b_x32(s_at, c[0]);
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              if (tok + 2 * e >= limit) x[e].x = -INFINITY;
-              if (tok + 2 * e + 1 >= limit) x[e].y = -INFINITY;
+            for (int h = 0; h < 4; ++h) {
+              tmem_ld_wait_tied(c[h & 1]);
+              if (h < 3) tmem_ld_32x32b_x32(s_at + 32 * (h + 1), c[(h + 1) & 1]);
+#pragma unroll
+              for (int g = 2 * h; g < 2 * h + 2; ++g) {
+                const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
+                float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const uint32_t* at = &c[h & 1][16 * (g & 1) + e];
+                  const float2 x = __ffma2_rn(make_float2(__uint_as_float(at[0]), __uint_as_float(at[1])),
+                                              make_float2(mul, mul), make_float2(add, add));
+                  const float2 v = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                  sum2 = __fadd2_rn(sum2, v);
+                  p[8 * g + e / 2] = f16x2_bits(v.x, v.y);
+                }
+                const float sum1 = sum2.x + sum2.y;
+                most = fmaxf(most, sum1);  // no P is larger
+                part = fmaf(sum1, tab[g].per, part);
+              }
+            }
+            slow = __any_sync(0xffffffffu, most > kMostP);
+            if (!slow) {
+              sum += part;
+              tmem_st_32x32b_x32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
+              tmem_st_32x32b_x32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
             }
           }
-          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (slow) {
+            // two neighbouring scores; those that the row does not see are -infinity
+            auto score = [&](uint32_t lo, uint32_t hi, float mul, float add, int at) {
+              float2 x = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(mul, mul),
+                                    make_float2(add, add));
+              if (at >= limit) x.x = -INFINITY;
+              if (at + 1 >= limit) x.y = -INFINITY;
+              return x;
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < kGroups; ++g) {
+              const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
+              uint32_t c[16];
+              tmem_ld_32x32b_x16(s_at + 16 * g, c);
+              tmem_ld_wait_tied16(c);
 #pragma unroll
-          for (int e = 0; e < 64; ++e) top4[e % 4] = max3(top4[e % 4], x[e].x, x[e].y);
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-          const bool rises = unset ? top > -INFINITY : top > kLift + kLazy;
-          if (__any_sync(0xffffffffu, rises)) {
+              for (int e = 0; e < 16; e += 2) {
+                const float2 x = score(c[e], c[e + 1], mul, add, tok + 16 * g + e);
+                top = max3(top, x.x, x.y);
+              }
+            }
             // by how much the reference rises; the first score that is there sets it
             float up = 0.f, shrink = 1.f;
-            if (unset) {
-              if (top > -INFINITY) up = top - kLift;
-            } else {
+            if (!unset) {
               up = fmaxf(top - kLift, 0.f);
               shrink = exp2_fast(-up);
+            } else if (top > -INFINITY) {
+              up = top - kLift;
+              unset = false;
             }
-            unset = unset && !(top > -INFINITY);
-            ref += up;
             sum *= shrink;
-#pragma unroll
-            for (int e = 0; e < 64; ++e) {
-              x[e].x -= up;
-              x[e].y -= up;
-            }
             if (j > j0 && __any_sync(0xffffffffu, shrink != 1.f)) {
               if (!(ok = warp_wait(&bar.o_full[i], (mine - 1) & 1))) break;
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int d = 0; d < kDim; d += 16) {
                 uint32_t o[16];
                 tmem_ld_32x32b_x16(o_at + d, o);
@@ -481,23 +508,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_32x32b_x16(o_at + d, o);
               }
             }
-          }
+#pragma unroll 1
+            for (int g = 0; g < kGroups; ++g) {  // (P of 16 tokens lands where scores have been used)
+              const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
+              uint32_t c[16], p[8];
+              tmem_ld_32x32b_x16(s_at + 16 * g, c);
+              tmem_ld_wait_tied16(c);
+              float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int g = 0; g < kGroups / 2; ++g) {
-              float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float2 v = x[32 * h + 8 * g + e];
-                v = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-                s2 = __fadd2_rn(s2, v);
-                p[8 * g + e] = f16x2_bits(v.x, v.y);
+              for (int e = 0; e < 16; e += 2) {
+                const float2 x = score(c[e], c[e + 1], mul, add, tok + 16 * g + e);
+                const float2 v = make_float2(exp2_fast(x.x - up), exp2_fast(x.y - up));
+                sum2 = __fadd2_rn(sum2, v);
+                p[e / 2] = f16x2_bits(v.x, v.y);
               }
-              sum = fmaf(s2.x + s2.y, tab[4 * h + g].per, sum);
+              sum = fmaf(sum2.x + sum2.y, tab[g].per, sum);
+              tmem_st_32x32b_x8(s_at + 8 * g, p);
             }
-            tmem_st_32x32b_x32(s_at + 32 * h, p);
+            ref += up;
           }
           tmem_st_wait();
           tc_fence_before();
@@ -517,9 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
       float* part = parts + (size_t(blockIdx.x) * 2 + (kind == kFirst)) * (kUnitRows * (kDim + 4));
-#pragma unroll
+#pragma unroll 1
       for (int d = 0; d < kDim; d += 32) {
         uint32_t o[32];
+        const uint32_t lost_d = lost[d / 32];
         if (j1 > j0) {
           tmem_ld_32x32b_x32(o_at + d, o);
           tmem_ld_wait_tied(o);
@@ -532,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               v[y] = f == 0.f ? 0.f : __uint_as_float(o[e + y]) * f * vref;
-              if (lost[d / 32] >> (e + y) & 1u) v[y] = NAN;
+              if (lost_d >> (e + y) & 1u) v[y] = NAN;
             }
             Raw8<__nv_bfloat16> w;
             pack8(v, w);
@@ -543,10 +572,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 32; e += 4) {
             float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                    __uint_as_float(o[e + 3]));
-            if (lost[d / 32] >> e & 1u) v.x = NAN;
-            if (lost[d / 32] >> e & 2u) v.y = NAN;
-            if (lost[d / 32] >> e & 4u) v.z = NAN;
-            if (lost[d / 32] >> e & 8u) v.w = NAN;
+            if (lost_d >> e & 1u) v.x = NAN;
+            if (lost_d >> e & 2u) v.y = NAN;
+            if (lost_d >> e & 4u) v.z = NAN;
+            if (lost_d >> e & 8u) v.w = NAN;
             *reinterpret_cast<float4*>(part + size_t(r) * kDim + d + e) = v;
           }
         }
@@ -562,144 +591,201 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- keys and values
     regs_decrease<kConvRegs>();
+    // Four tiles are in hand at once: one whose table entry is on its way, one whose scales are, one whose
+    // codes are (into this thread's places in shared memory, so that no other has to be waited for), and
+    // the one that becomes FP16.
     const int ct = threadIdx.x - 32 * kConvWarp;
-    constexpr int kPieces = kDim / 16;          // 16-byte pieces of a token's codes
-    constexpr int kRowsAtOnce = 128 / kPieces;  // tokens that the 128 threads cover at once
+    // Eight neighbouring threads have four pieces of two neighbouring tokens: their chunks of FP16 meet
+    // all banks.
+    const int piece = kDim == 128 ? (ct & 3) | (ct >> 1 & 4) : ct & 3;
+    const int row0 = kDim == 128 ? (ct >> 2 & 1) | (ct >> 4 << 1) : ct >> 2;
+    constexpr int kRowsAtOnce = 128 / (kDim / 16);  // tokens that the 128 threads cover at once
     constexpr int kLoads = kTok / kRowsAtOnce;
-    const int piece = ct % kPieces, row0 = ct / kPieces;
-    uint32_t it = 0;
-    for (uint32_t taken = 0;; ++taken) {
-      const int slot = taken % kRing;
-      if (!warp_wait(&bar.ring_full[slot], (taken / kRing) & 1)) break;
-      Unit* u = ring(slot);
-      if (u->kind == kEnd) break;
-      const int b = u->b, head = u->head, j0 = u->j0, j1 = u->j1;
-      const int first = row_limit(a, u->len, u->n, u->row0);                // what the first row sees
-      const int vis = row_limit(a, u->len, u->n, u->row0 + u->rows - 1);    // and the last
-      int ids[kLoads];
-      uint4 kr[kLoads], vr[kLoads];
-      auto load_ids = [&](int j) {
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l)
-          ids[l] = j < j1 ? block_of(a, b, j * kTok + row0 + kRowsAtOnce * l, vis, status) : -1;
-      };
-      auto load_codes = [&](const uint8_t* cache, int j, uint4 (&x)[kLoads]) {
-#pragma unroll
+    struct InHand {
+      bool valid, last;  // of its unit
+      int slot, j, vis, first;
+      int blk;           // lane g < 8: block of tokens 16 g .. 16 g + 15
+      long long off;     // and where its head's codes begin there
+      float ks, vs;
+    };
+    InHand h0, h1, h2, h3;
+    h0.valid = h1.valid = h2.valid = h3.valid = false;
+    uint32_t taken = 0, it = 0;
+    bool ended = false, ok = true;
+    int b = 0, head = 0, j = 0, j1 = 0, vis = 0, first = 0, slot = 0;  // what is looked up next
+    float vref = 1.f;
+    uint8_t* codes_k = smem + S::kCodes;
+    uint8_t* codes_v = codes_k + kTok * kDim;
+    auto fetch = [&](const uint8_t* cache, uint8_t* to, const InHand& h) {
+      if (h.valid) {
+#pragma unroll 4
         for (int l = 0; l < kLoads; ++l) {
-          x[l] = make_uint4(0u, 0u, 0u, 0u);
-          const int tok = j * kTok + row0 + kRowsAtOnce * l;
-          if (ids[l] >= 0)
-            x[l] = __ldg(reinterpret_cast<const uint4*>(
-                cache + (((long long)ids[l] * a.heads + head) * a.block + (tok & (a.block - 1))) * kDim + 16 * piece));
+          const int g = kDim == 128 ? l : 2 * l + (ct >> 6);
+          const long long off = __shfl_sync(0xffffffffu, h.off, g);
+          const uint8_t* from = cache + (off < 0 ? 0 : off + (row0 & 15) * kDim + 16 * piece);
+          cp_async_16(smem_addr(to + (l * 128 + ct) * 16), from, off < 0 ? 0u : 16u);
         }
-      };
-      // the scales of 16 tokens, by the first eight lanes
-      float ks = 0.f, vs = 0.f;
-      bool there = false;
-      auto load_scales = [&](int j) {
-        there = false;
-        if (ct < kGroups && j < j1) {
-          const int blk = block_of(a, b, j * kTok + 16 * ct, vis, status);
-          there = blk >= 0;
-          if (there) {
-            ks = a.ks[(long long)blk * a.heads + head];
-            vs = a.vs[(long long)blk * a.heads + head];
-          }
-        }
-      };
-      load_ids(j0);
-      load_scales(j0);
-      load_codes(a.kc, j0, kr);
-      load_codes(a.vc, j0, vr);
-      load_ids(j0 + 1);
-      float vref = 1.f;
-      bool ok = true;
-      for (int j = j0; j < j1; ++j, ++it) {
-        const int st = it % kStages;
-        const uint32_t ph = (it / kStages) & 1;
+      }
+      cp_async_commit();
+    };
+    auto put = [&](uint8_t* tile, int row, const uint32_t (&w)[4], uint32_t keep, uint32_t flip) {
+      uint32_t x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e])) & keep) ^ flip;
+        x[2 * e + 1] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16)) & keep) ^ flip;
+      }
+      *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece)) = make_uint4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
+    };
+    while (true) {
+      const int st = it % kStages;
+      const uint32_t ph = (it / kStages) & 1;
+      const Tab* tab = tabs + (it % kTabs) * kGroups;
+      if (h0.valid) {
         if (!(ok = warp_wait(&bar.k_empty[st], ph ^ 1))) break;
         if (warp == kConvWarp) {  // the tile's scales (its place was read long ago: see kTabs)
-          const bool fin = fabsf(vs) <= FLT_MAX;
-          const float av = there && fin && vs != 0.f ? fabsf(vs) : 1.f;
-          if (j == j0) {
+          const bool there = h0.blk >= 0, fin = fabsf(h0.vs) <= FLT_MAX;
+          const float av = there && fin && h0.vs != 0.f ? fabsf(h0.vs) : 1.f;
+          if (h0.j == ring(h0.slot)->j0) {
             vref = __shfl_sync(0xffffffffu, av, 0);
-            if (lane == 0) {
-              u->vref = vref;
-            }
+            if (lane == 0) ring(h0.slot)->vref = vref;
           }
           if (lane < kGroups) {
             Tab t;
-            t.k = there ? ks : 0.f;
+            t.k = there ? h0.ks : 0.f;
             t.add = there ? log2f(av) : -INFINITY;
             t.per = there ? __fdiv_rn(vref, av) : 0.f;
-            t.mode = !there ? 0u : !fin ? kNotFinite : vs == 0.f ? kZero : vs < 0.f ? kNegate : 0u;
+            t.mode = !there ? 0u : !fin ? kNotFinite : h0.vs == 0.f ? kZero : h0.vs < 0.f ? kNegate : 0u;
             tabs[(it % kTabs) * kGroups + lane] = t;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.tab_full[it % kTabs]);
-          load_scales(j + 1);
         }
-        uint8_t* kt = smem + S::kK + st * S::kTileBytes;
-        uint8_t* vt = smem + S::kV + st * S::kTileBytes;
-        // a piece becomes two chunks; lanes of the second half of the dimensions write theirs in the other
-        // order, so that eight lanes meet all banks
-        auto put = [&](uint8_t* tile, int row, uint4 codes, uint32_t keep, uint32_t flip) {
-          const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[2 * e] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e])) & keep) ^ flip;
-            h[2 * e + 1] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16)) & keep) ^ flip;
-          }
-          const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-          const bool swap = kDim == 128 && piece >= 4;
-          *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece + swap)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece + !swap)) = swap ? lo : hi;
-        };
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l) put(kt, row0 + kRowsAtOnce * l, kr[l], 0xffffffffu, 0u);
+        cp_async_wait<1>();
+        uint8_t* tile = smem + S::kK + st * S::kTileBytes;
+#pragma unroll 4
+        for (int l = 0; l < kLoads; ++l) {
+          const uint4 x = *reinterpret_cast<const uint4*>(codes_k + (l * 128 + ct) * 16);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          put(tile, row0 + kRowsAtOnce * l, w, 0xffffffffu, 0u);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.k_full[st]);
-        load_codes(a.kc, j + 1, kr);
+      }
+      fetch(a.kc, codes_k, h1);
+      if (h0.valid) {
         if (!(ok = warp_wait(&bar.v_empty[st], ph ^ 1))) break;
         if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
-        const bool mixed = (j + 1) * kTok > first;  // some row does not see all of it
-        uint32_t bad = 0u;
-#pragma unroll
-        for (int l = 0; l < kLoads; ++l) {
-          const int r = row0 + kRowsAtOnce * l;
-          const uint32_t mode = tabs[(it % kTabs) * kGroups + r / 16].mode;
-          uint32_t keep = mode & kZero ? 0u : 0xffffffffu;
-          uint32_t flip = mode & kNegate ? 0x80008000u : 0u;
-          uint4 x = vr[l];
-          if (mode & kNotFinite) {
-            keep = 0u;
-            if (!mixed)
-              flip = 0x7fff7fffu;
-            else if (j * kTok + r < vis)
-              bad = 1u;
-          } else if (mixed) {
-            // 0 times what is not finite would reach rows that do not see it: they get 0 here, and the rows
-            // that do see it are marked when the unit ends
-            const uint32_t m[4] = {not_finite4<kE5M2>(x.x), not_finite4<kE5M2>(x.y), not_finite4<kE5M2>(x.z),
-                                   not_finite4<kE5M2>(x.w)};
-            bad |= m[0] | m[1] | m[2] | m[3];
-            x = make_uint4(x.x & ~m[0], x.y & ~m[1], x.z & ~m[2], x.w & ~m[3]);
+        cp_async_wait<1>();
+        uint8_t* tile = smem + S::kV + st * S::kTileBytes;
+        const uint32_t modes = lane < kGroups ? tab[lane].mode : 0u;
+        const int there = h0.vis - h0.j * kTok;  // tokens of the tile that are there
+        if (h0.j * kTok + kTok <= h0.first && !__any_sync(0xffffffffu, modes != 0u)) {
+#pragma unroll 4
+          for (int l = 0; l < kLoads; ++l) {
+            const uint4 x = *reinterpret_cast<const uint4*>(codes_v + (l * 128 + ct) * 16);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            put(tile, row0 + kRowsAtOnce * l, w, 0xffffffffu, 0u);
           }
-          put(vt, r, x, keep, flip);
+        } else {
+          // Some scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times what is
+          // not finite would reach rows that do not see it: such values become 0, and the rows that do see
+          // them are marked when the unit ends.
+          const bool mixed = h0.j * kTok + kTok > h0.first;
+          uint32_t bad = 0u;
+#pragma unroll 1
+          for (int l = 0; l < kLoads; ++l) {
+            const int r = row0 + kRowsAtOnce * l;
+            const uint4 x = *reinterpret_cast<const uint4*>(codes_v + (l * 128 + ct) * 16);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t mode = tab[r / 16].mode;
+            uint32_t keep = mode & kZero || r >= there ? 0u : 0xffffffffu;
+            uint32_t flip = mode & kNegate ? 0x80008000u : 0u;
+            if (mode & kNotFinite) {
+              keep = 0u;
+              if (!mixed)
+                flip = 0x7fff7fffu;
+              else if (r < there)
+                bad = 1u;
+            } else if (mixed) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t m = not_finite4<kE5M2>(w[e]);
+                if (r < there) bad |= m;
+                w[e] &= ~m;
+              }
+            }
+            put(tile, r, w, keep, flip);
+          }
+          if (bad != 0u) ring(h0.slot)->bad = 1;
         }
-        if (bad != 0u) u->bad = 1;
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.v_full[st]);
-        load_codes(a.vc, j + 1, vr);
-        load_ids(j + 2);
+        if (lane == 0) {
+          mbar_arrive(&bar.v_full[st]);
+          if (h0.last) mbar_arrive(&bar.ring_empty[h0.slot]);
+        }
+        ++it;
+      }
+      fetch(a.vc, codes_v, h1);
+      // ---- on by one
+      h0 = h1;
+      h1 = h2;
+      h2 = h3;
+      if (h2.valid) {
+        h2.off = -1;
+        h2.ks = h2.vs = 0.f;
+        if (h2.blk >= a.num_blocks || h2.blk < -1) {
+          raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+          h2.blk = -1;
+        }
+        if (h2.blk >= 0) {
+          const long long t = (long long)h2.blk * a.heads + ring(h2.slot)->head;
+          h2.off = (t * a.block + (16 * lane & (a.block - 1))) * kDim;
+          h2.ks = a.ks[t];
+          h2.vs = a.vs[t];
+        }
+      }
+      h3.valid = false;
+      while (j == j1 && !ended) {
+        slot = taken % kRing;
+        if (!(ok = warp_wait(&bar.ring_full[slot], (taken / kRing) & 1))) break;
+        const Unit* u = ring(slot);
+        if (u->kind == kEnd) {
+          ended = true;
+          break;
+        }
+        ++taken;
+        b = u->b;
+        head = u->head;
+        j = u->j0;
+        j1 = u->j1;
+        first = row_limit(a, u->len, u->n, u->row0);               // what the first row sees
+        vis = row_limit(a, u->len, u->n, u->row0 + u->rows - 1);   // and the last
+        if (j == j1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
+        }
       }
       if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
+      if (j < j1) {
+        h3.valid = true;
+        h3.last = j + 1 == j1;
+        h3.slot = slot;
+        h3.j = j;
+        h3.vis = vis;
+        h3.first = first;
+        const int tok = j * kTok + 16 * lane;
+        h3.blk = lane < kGroups && tok < vis ? a.table[(long long)b * a.width + (tok >> a.log_block)] : -1;
+        // (an entry of -1 counts as no block; it is reported like any other that is out of range)
+        if (lane < kGroups && tok < vis && h3.blk == -1) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+        ++j;
+      }
+      if (ended && !h0.valid && !h1.valid && !h2.valid && !h3.valid) break;
     }
+    cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- the products
     regs_decrease<kLowRegs>();
@@ -710,20 +796,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
       bool issued = false;
       auto scores = [&](int i, int st) {
-#pragma unroll
+        const uint64_t q_desc = smem_desc_sw128_kmajor(q_at + i * S::kTileBytes);
+        const uint64_t k_desc = smem_desc_sw128_kmajor(k_at + st * S::kTileBytes);
+#pragma unroll 2
         for (int k = 0; k < kDim / 16; ++k) {
-          const uint32_t off = (k / 4) * S::kSubBytes + (k % 4) * 32;
-          umma_f16(tmem + kSCol + 128 * i, smem_desc_sw128_kmajor(q_at + i * S::kTileBytes + off),
-                   smem_desc_sw128_kmajor(k_at + st * S::kTileBytes + off), kDescS, k > 0 ? 1u : 0u);
+          const uint32_t off = ((k / 4) * S::kSubBytes + (k % 4) * 32) >> 4;
+          umma_f16(tmem + kSCol + 128 * i, q_desc + off, k_desc + off, kDescS, k > 0 ? 1u : 0u);
         }
         umma_commit(&bar.s_full[i]);
         issued = true;
       };
       auto values = [&](int i, int st, bool first) {
-#pragma unroll
+        const uint64_t v_desc = smem_desc_sw128_mnmajor(v_at + st * S::kTileBytes, S::kSubBytes);
+#pragma unroll 2
         for (int k = 0; k < kTok / 16; ++k)
-          umma_f16_ta(tmem + kOCol + 128 * i, tmem + kSCol + 128 * i + 8 * k,
-                      smem_desc_sw128_mnmajor(v_at + st * S::kTileBytes + k * 2048, S::kSubBytes), kDescO,
+          umma_f16_ta(tmem + kOCol + 128 * i, tmem + kSCol + 128 * i + 8 * k, v_desc + k * (2048 >> 4), kDescO,
                       first && k == 0 ? 0u : 1u);
         umma_commit(&bar.o_full[i]);
       };
