@@ -15,7 +15,7 @@
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1: thread = row = TMEM lane
 //   warps 8-11       keys and values: codes from the cache's blocks by asynchronous copies, a
 //                    tile ahead; as FP16 into a two-stage ring in shared memory (128-byte swizzle)
-//   warp 12          issues the products (one thread): while tile 0's softmax runs, tile 1's
+//   warp 12          issues the products: while tile 0's softmax runs, tile 1's
 //                    products do
 //   warp 13          finds the CTA's units and hands them on through a ring
 //
@@ -371,11 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // a whole warp's wait has one outcome
   auto warp_wait = [&](uint64_t* b, uint32_t parity) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait_within(b, parity, abort_flag, a.wait_ns));
-    if (!ok) fail();
-    return ok;
-  };
-  auto thread_wait = [&](uint64_t* b, uint32_t parity) {
-    const bool ok = mbar_wait_within(b, parity, abort_flag, a.wait_ns);
     if (!ok) fail();
     return ok;
   };
@@ -788,74 +783,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- the products
+    // The whole warp runs this, in step, so that descriptors stay in uniform registers; one lane issues.
     regs_decrease<kLowRegs>();
-    if (lane == 0) {
-      constexpr uint32_t kDescS = idesc_f16_f32(kTileRows, kTok, false);
-      constexpr uint32_t kDescO = idesc_f16_f32(kTileRows, kDim, true);
-      const uint32_t q_at = smem_addr(smem + S::kQ), k_at = smem_addr(smem + S::kK), v_at = smem_addr(smem + S::kV);
-      uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
-      bool issued = false;
-      auto scores = [&](int i, int st) {
-        const uint64_t q_desc = smem_desc_sw128_kmajor(q_at + i * S::kTileBytes);
-        const uint64_t k_desc = smem_desc_sw128_kmajor(k_at + st * S::kTileBytes);
-#pragma unroll 2
+    constexpr uint32_t kDescS = idesc_f16_f32(kTileRows, kTok, false);
+    constexpr uint32_t kDescO = idesc_f16_f32(kTileRows, kDim, true);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+    const uint64_t q_desc = smem_desc_sw128_kmajor(smem_addr(smem + S::kQ));
+    const uint64_t k_desc = smem_desc_sw128_kmajor(smem_addr(smem + S::kK));
+    const uint64_t v_desc = smem_desc_sw128_mnmajor(smem_addr(smem + S::kV), S::kSubBytes);
+    uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    bool issued = false;
+    auto scores = [&](int i, int st) {
+      if (elect_one()) {
+#pragma unroll
         for (int k = 0; k < kDim / 16; ++k) {
           const uint32_t off = ((k / 4) * S::kSubBytes + (k % 4) * 32) >> 4;
-          umma_f16(tmem + kSCol + 128 * i, q_desc + off, k_desc + off, kDescS, k > 0 ? 1u : 0u);
+          umma_f16(tm + kSCol + 128 * i, q_desc + (off + i * (S::kTileBytes >> 4)),
+                   k_desc + (off + st * (S::kTileBytes >> 4)), kDescS, k > 0 ? 1u : 0u);
         }
         umma_commit(&bar.s_full[i]);
-        issued = true;
-      };
-      auto values = [&](int i, int st, bool first) {
-        const uint64_t v_desc = smem_desc_sw128_mnmajor(v_at + st * S::kTileBytes, S::kSubBytes);
-#pragma unroll 2
+      }
+      issued = true;
+    };
+    auto values = [&](int i, int st, bool first) {
+      if (elect_one()) {
+#pragma unroll
         for (int k = 0; k < kTok / 16; ++k)
-          umma_f16_ta(tmem + kOCol + 128 * i, tmem + kSCol + 128 * i + 8 * k, v_desc + k * (2048 >> 4), kDescO,
-                      first && k == 0 ? 0u : 1u);
+          umma_f16_ta(tm + kOCol + 128 * i, tm + kSCol + 128 * i + 8 * k,
+                      v_desc + (k * (2048 >> 4) + st * (S::kTileBytes >> 4)), kDescO, first && k == 0 ? 0u : 1u);
         umma_commit(&bar.o_full[i]);
-      };
-      bool ok = true;
-      for (uint32_t taken = 0; ok; ++taken) {
-        const int slot = taken % kRing;
-        if (!thread_wait(&bar.ring_full[slot], (taken / kRing) & 1)) break;
-        const Unit* u = ring(slot);
-        const int kind = u->kind, n = u->j1 - u->j0, tiles = u->rows > kTileRows ? 2 : 1;
-        if (kind == kEnd) break;
-        if (n > 0) {
-          ok = thread_wait(&bar.k_full[it % kStages], (it / kStages) & 1);
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = thread_wait(&bar.q_full[i], n_q[i]++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            scores(i, it % kStages);
-          }
-          if (ok) umma_commit(&bar.k_empty[it % kStages]);
-        }
-        for (int j = 0; j < n && ok; ++j, ++it) {
-          const int st = it % kStages, st1 = (it + 1) % kStages;
-          ok = thread_wait(&bar.v_full[st], (it / kStages) & 1);
-          for (int i = 0; i < tiles && ok; ++i) {
-            ok = thread_wait(&bar.p_full[i], n_p[i]++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            values(i, st, j == 0);
-            if (j + 1 < n) {
-              if (i == 0) ok = thread_wait(&bar.k_full[st1], ((it + 1) / kStages) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              scores(i, st1);
-            }
-          }
-          if (!ok) break;
-          umma_commit(&bar.v_empty[st]);
-          if (j + 1 < n) umma_commit(&bar.k_empty[st1]);
-        }
-        if (ok) mbar_arrive(&bar.ring_empty[slot]);
       }
-      if (issued) {  // every issued product has finished before TMEM is released
-        umma_commit(&bar.drain);
-        mbar_drain(&bar.drain, 0);
+    };
+    auto commit = [&](uint64_t* b) {
+      if (elect_one()) umma_commit(b);
+    };
+    bool ok = true;
+    for (uint32_t taken = 0; ok; ++taken) {
+      const int slot = taken % kRing;
+      if (!warp_wait(&bar.ring_full[slot], (taken / kRing) & 1)) break;
+      const Unit* u = ring(slot);
+      const int n = __reduce_max_sync(0xffffffffu, u->kind == kEnd ? -1 : u->j1 - u->j0);
+      const int tiles = __reduce_max_sync(0xffffffffu, u->rows > kTileRows ? 2 : 1);
+      if (n < 0) break;
+      if (n > 0) {
+        ok = warp_wait(&bar.k_full[it % kStages], (it / kStages) & 1);
+        for (int i = 0; i < tiles && ok; ++i) {
+          if (!(ok = warp_wait(&bar.q_full[i], n_q[i]++ & 1))) break;
+          tc_fence_after();
+          scores(i, it % kStages);
+        }
+        if (ok) commit(&bar.k_empty[it % kStages]);
       }
+      for (int j = 0; j < n && ok; ++j, ++it) {
+        const int st = it % kStages, st1 = (it + 1) % kStages;
+        if (!(ok = warp_wait(&bar.v_full[st], (it / kStages) & 1))) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i == tiles) break;
+          if (!(ok = warp_wait(&bar.p_full[i], n_p[i]++ & 1))) break;
+          tc_fence_after();
+          values(i, st, j == 0);
+          if (j + 1 < n) {
+            if (i == 0 && !(ok = warp_wait(&bar.k_full[st1], ((it + 1) / kStages) & 1))) break;
+            tc_fence_after();
+            scores(i, st1);
+          }
+        }
+        if (!ok) break;
+        commit(&bar.v_empty[st]);
+        if (j + 1 < n) commit(&bar.k_empty[st1]);
+      }
+      if (ok && lane == 0) mbar_arrive(&bar.ring_empty[slot]);
+    }
+    if (issued) {  // every issued product has finished before TMEM is released
+      commit(&bar.drain);
+      mbar_drain(&bar.drain, 0);
     }
   } else {
     regs_decrease<kLowRegs>();

@@ -304,6 +304,18 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
       : "memory");
 }
 
+// True in one lane of a warp that runs this together, the same one each time: what
+// issues tcgen05 operations, whose completion is tracked per thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(is));
+  return is != 0;
+}
+
 // ------------------------------------------------ tcgen05 on FP16 operands
 // Descriptor of an operand tile whose M (or N) elements lie side by side ("MN-major"), with
 // 128-byte swizzling: rows of 64 two-byte elements, one a K index, 8 rows (1024 bytes) a swizzle
