@@ -49,16 +49,15 @@ constexpr int kTok = 128;   // tokens of a tile
 constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of one instruction
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
-// 2 x 152 + 112 + 96 = 512 registers a lane of the four sub-partitions = 65536 / 128
-constexpr uint32_t kSoftRegs = 152, kConvRegs = 112, kLowRegs = 96;
+// 512 threads are launched with 128 registers each: 512 for the four warps of a sub-partition
+constexpr uint32_t kSoftRegs = 176, kConvRegs = 80, kLowRegs = 80;
 static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
 constexpr int kStages = 2;  // of keys and of values
 constexpr int kTabs = 4;    // tiles' scales
 constexpr int kRing = 4;    // units
 constexpr int kUnitCost = 3;  // what a unit's start and end cost, in tiles
 constexpr int kMinShare = 4;  // tiles of a CTA's share, at least
-constexpr float kLift = 5.f;
-constexpr float kMostP = 32768.f;  // of P (FP16 ends at 65504)
+constexpr float kLift = 5.f, kMost = 15.f, kMostP = 32768.f;  // (FP16 ends below 2^16)
 constexpr uint32_t kSCol = 0, kOCol = 256;  // TMEM columns: S of tile i at 128 i, O at 256 + 128 i
 
 // A part of a unit: tokens 128 j0 .. 128 j1 - 1 of what its rows see.
@@ -70,6 +69,7 @@ struct Unit {
   int len;          // its tokens
   int row0, rows;   // rows of the sequence: token * group + query head
   int j0, j1;
+  int first, vis;   // tokens that its first row and its last one see
   int bad;          // values that are not finite were hidden in tiles that some rows do not see whole
   float vref;       // value scale that the sums of p are relative to
 };
@@ -141,12 +141,10 @@ __device__ __forceinline__ long long sequence_cost(const KvChunkArgs& a, const S
 
 // The CTA's share of the work: [lo, hi) of the heads' lists of units, one list after the other.
 struct Share {
-  long long lo, hi, list, total;  // list: what one head's units cost
-  int ctas;
-  int b;               // where it begins: sequence, and cost of its units before
+  long long lo, hi, total, each;  // each: a CTA's share (the last one's may be less)
+  int head, b;                    // where it begins: head, sequence, and cost of the sequence's units before
   long long off;
 };
-__device__ long long first_of(long long total, int ctas, int c) { return total / ctas * c + total % ctas * c / ctas; }
 
 __device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, int* status) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -166,6 +164,7 @@ __device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, in
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     long long all = 0;
+#pragma unroll 1
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) upto += sums[i];
       all += sums[i];
@@ -174,20 +173,18 @@ __device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, in
     return all;
   };
   for (base = 0; base < a.B; base += kThreads) list += round();
-  const long long total = list * a.heads;
   Share sh;
-  sh.list = list;
-  sh.total = total;
-  sh.ctas = int(min((long long)gridDim.x, max(1LL, total / kMinShare)));
+  sh.total = list * a.heads;
+  sh.each = max((long long)kMinShare, (long long)((unsigned long long)(sh.total + gridDim.x - 1) / gridDim.x));
+  sh.lo = min(sh.total, sh.each * blockIdx.x);
+  sh.hi = min(sh.total, sh.lo + sh.each);
+  sh.head = list > 0 ? int((unsigned long long)sh.lo / (unsigned long long)list) : 0;
   sh.b = 0;
   sh.off = 0;
-  const int c = blockIdx.x;
-  sh.lo = c < sh.ctas ? first_of(total, sh.ctas, c) : total;
-  sh.hi = c < sh.ctas ? first_of(total, sh.ctas, c + 1) : total;
   if (tid == 0) *out = sh;
   __syncthreads();
   if (sh.lo >= sh.hi) return;
-  const long long at = sh.lo % list;
+  const long long at = sh.lo - sh.head * list;
   long long before = 0;
   for (base = 0; base < a.B; base += kThreads) {
     const long long all = a.B > kThreads ? round() : list;  // (one round: the first one's are still there)
@@ -243,6 +240,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // 16-byte chunk c of a row of the 64-element tiles that make up one of FP16.
 template <int kDim>
 __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
@@ -253,27 +256,27 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
 // into [2^10, 2^11); returns the reciprocal of that power.
 template <int kDim>
 __device__ __forceinline__ float stage_query(uint8_t* tile, int row, const __nv_bfloat16* q) {
-  Raw8<__nv_bfloat16> raw[kDim / 8];
   float top = 0.f;
-#pragma unroll
+#pragma unroll 4
   for (int c = 0; c < kDim / 8; ++c) {
-    zero8(raw[c]);
-    if (q) raw[c] = load8(q + 8 * c);
-  }
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) {
+    Raw8<__nv_bfloat16> raw;
+    zero8(raw);
+    if (q) raw = load8(q + 8 * c);
     float f[8];
-    unpack8(raw[c], f);
+    unpack8(raw, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
   }
   // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
   const int exp = max(int(__float_as_uint(top) >> 23), 10);
   const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) {
+#pragma unroll 4
+  for (int c = 0; c < kDim / 8; ++c) {  // (read again, from the cache: a row would fill the registers)
+    Raw8<__nv_bfloat16> raw;
+    zero8(raw);
+    if (q) raw = load8(q + 8 * c);
     float f[8];
-    unpack8(raw[c], f);
+    unpack8(raw, f);
     *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c)) =
         make_uint4(f16x2_bits(f[0] * up, f[1] * up), f16x2_bits(f[2] * up, f[3] * up),
                    f16x2_bits(f[4] * up, f[5] * up), f16x2_bits(f[6] * up, f[7] * up));
@@ -368,11 +371,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     raise_status(status, FP8GEMM_ERR_TIMEOUT);
   };
-  // a whole warp's wait has one outcome
+  // A whole warp's wait, with one outcome.  (Short: the roles' loops have to fit in the instruction
+  // cache together.)
   auto warp_wait = [&](uint64_t* b, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_within(b, parity, abort_flag, a.wait_ns));
-    if (!ok) fail();
-    return ok;
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(b, parity))) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t0 > a.wait_ns)) {
+        fail();
+        return false;
+      }
+    }
+    return true;
   };
 
   if (warp < kConvWarp) {
@@ -421,107 +432,153 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
           tc_fence_after();
           const int tok = j * kTok;
-          // The plain case, to which most tiles belong: all rows see all tokens, and the reference need not
-          // rise -- as is known once P is there, in registers.  (Code that runs per tile is kept
-          // short: the roles' loops have to fit in the instruction cache together.)
-          bool slow = __any_sync(0xffffffffu, unset) || tok + kTok > least;
-          if (!slow) {
-            uint32_t p[64], c[2][32];
+          // The plain case, to which most tiles belong: all rows see all tokens and the reference need not
+          // rise, as is known once P is there, in registers.
+          bool plain = !__any_sync(0xffffffffu, unset) && tok + kTok <= least;
+          if (plain) {
+            uint32_t c[3][32], p[4][16];
             float part = 0.f, most = 0.f;
-            tmem_ld_32x32b_x32(s_at, c[0]);
+            auto take = [&](const uint32_t (&from)[32], int h) {  // 32 tokens
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              tmem_ld_wait_tied(c[h & 1]);
-              if (h < 3) tmem_ld_32x32b_x32(s_at + 32 * (h + 1), c[(h + 1) & 1]);
-#pragma unroll
-              for (int g = 2 * h; g < 2 * h + 2; ++g) {
-                const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
+              for (int g = 0; g < 2; ++g) {
+                const float mul = q_mul * tab[2 * h + g].k, add = tab[2 * h + g].add - ref;
                 float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                  const uint32_t* at = &c[h & 1][16 * (g & 1) + e];
-                  const float2 x = __ffma2_rn(make_float2(__uint_as_float(at[0]), __uint_as_float(at[1])),
-                                              make_float2(mul, mul), make_float2(add, add));
+                  const float2 x =
+                      __ffma2_rn(make_float2(__uint_as_float(from[16 * g + e]), __uint_as_float(from[16 * g + e + 1])),
+                                 make_float2(mul, mul), make_float2(add, add));
                   const float2 v = make_float2(exp2_fast(x.x), exp2_fast(x.y));
                   sum2 = __fadd2_rn(sum2, v);
-                  p[8 * g + e / 2] = f16x2_bits(v.x, v.y);
+                  p[h][8 * g + e / 2] = f16x2_bits(v.x, v.y);
                 }
                 const float sum1 = sum2.x + sum2.y;
                 most = fmaxf(most, sum1);  // no P is larger
-                part = fmaf(sum1, tab[g].per, part);
+                part = fmaf(sum1, tab[2 * h + g].per, part);
               }
-            }
-            slow = __any_sync(0xffffffffu, most > kMostP);
-            if (!slow) {
-              sum += part;
-              tmem_st_32x32b_x32(s_at, *reinterpret_cast<uint32_t(*)[32]>(&p[0]));
-              tmem_st_32x32b_x32(s_at + 32, *reinterpret_cast<uint32_t(*)[32]>(&p[32]));
-            }
-          }
-          if (slow) {
-            // two neighbouring scores; those that the row does not see are -infinity
-            auto score = [&](uint32_t lo, uint32_t hi, float mul, float add, int at) {
-              float2 x = __ffma2_rn(make_float2(__uint_as_float(lo), __uint_as_float(hi)), make_float2(mul, mul),
-                                    make_float2(add, add));
-              if (at >= limit) x.x = -INFINITY;
-              if (at + 1 >= limit) x.y = -INFINITY;
-              return x;
             };
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int g = 0; g < kGroups; ++g) {
-              const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
-              uint32_t c[16];
-              tmem_ld_32x32b_x16(s_at + 16 * g, c);
-              tmem_ld_wait_tied16(c);
+            // two loads ahead: they take long beside the products' own traffic
+            tmem_ld_32x32b_x32(s_at, c[0]);
+            tmem_ld_32x32b_x32(s_at + 32, c[1]);
+            tmem_ld_wait_tied(c[0]);
+            reg_tie32(c[1]);
+            tmem_ld_32x32b_x32(s_at + 64, c[2]);
+            take(c[0], 0);
+            tmem_ld_32x32b_x32(s_at + 96, c[0]);
+            take(c[1], 1);
+            tmem_ld_wait_tied(c[2]);
+            reg_tie32(c[0]);
+            take(c[2], 2);
+            take(c[0], 3);
+            plain = !__any_sync(0xffffffffu, most > kMostP);
+            if (plain) {
+              sum += part;
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 x = score(c[e], c[e + 1], mul, add, tok + 16 * g + e);
-                top = max3(top, x.x, x.y);
-              }
+              for (int h = 0; h < 4; ++h) tmem_st_32x32b_x16(s_at + 16 * h, p[h]);
             }
-            // by how much the reference rises; the first score that is there sets it
-            float up = 0.f, shrink = 1.f;
-            if (!unset) {
-              up = fmaxf(top - kLift, 0.f);
-              shrink = exp2_fast(-up);
-            } else if (top > -INFINITY) {
-              up = top - kLift;
-              unset = false;
-            }
-            sum *= shrink;
-            if (j > j0 && __any_sync(0xffffffffu, shrink != 1.f)) {
-              if (!(ok = warp_wait(&bar.o_full[i], (mine - 1) & 1))) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int d = 0; d < kDim; d += 16) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(o_at + d, o);
-                tmem_ld_wait_tied16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
-                tmem_st_32x32b_x16(o_at + d, o);
-              }
-            }
-#pragma unroll 1
-            for (int g = 0; g < kGroups; ++g) {  // (P of 16 tokens lands where scores have been used)
-              const float mul = q_mul * tab[g].k, add = tab[g].add - ref;
-              uint32_t c[16], p[8];
-              tmem_ld_32x32b_x16(s_at + 16 * g, c);
-              tmem_ld_wait_tied16(c);
-              float2 sum2 = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float2 x = score(c[e], c[e + 1], mul, add, tok + 16 * g + e);
-                const float2 v = make_float2(exp2_fast(x.x - up), exp2_fast(x.y - up));
-                sum2 = __fadd2_rn(sum2, v);
-                p[e / 2] = f16x2_bits(v.x, v.y);
-              }
-              sum = fmaf(sum2.x + sum2.y, tab[g].per, sum);
-              tmem_st_32x32b_x8(s_at + 8 * g, p);
-            }
-            ref += up;
           }
+#pragma unroll 1
+          for (int h = plain ? kTok / 32 : 0; h < kTok / 32; ++h) {  // 32 tokens at a time
+            const int sees = limit - tok - 32 * h;
+            uint32_t p[16];
+            float sums[2];
+            // Once as if the reference need not rise; if it has to, again with the new one.
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+              uint32_t c[32];
+              tmem_ld_32x32b_x32(s_at + 32 * h, c);
+              tmem_ld_wait_tied(c);
+              float2 x[16];  // scores in powers of two, with the value scale's, less the reference
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const float mul = q_mul * tab[2 * h + g].k, add = tab[2 * h + g].add - ref;
+#pragma unroll
+                for (int e = 8 * g; e < 8 * g + 8; ++e)
+                  x[e] = __ffma2_rn(make_float2(__uint_as_float(c[2 * e]), __uint_as_float(c[2 * e + 1])),
+                                    make_float2(mul, mul), make_float2(add, add));
+              }
+              if (tok + 32 * h + 32 > least) {  // the same for the warp: some row does not see all of these
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  if (2 * e >= sees) x[e].x = -INFINITY;
+                  if (2 * e + 1 >= sees) x[e].y = -INFINITY;
+                }
+              }
+              if (again) {  // scores of 2^27 and more: a rounded reference may lie far below the largest
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  x[e].x = min_nan(x[e].x, kLift + 1.f);
+                  x[e].y = min_nan(x[e].y, kLift + 1.f);
+                }
+              }
+              float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 8 * g; e < 8 * g + 8; ++e) {
+                  if (e % 2)
+                    top1 = max3(top1, x[e].x, x[e].y);
+                  else
+                    top0 = max3(top0, x[e].x, x[e].y);
+                  const float2 v = make_float2(exp2_fast(x[e].x), exp2_fast(x[e].y));
+                  s2 = __fadd2_rn(s2, v);
+                  p[e] = f16x2_bits(v.x, v.y);
+                }
+                sums[g] = s2.x + s2.y;
+              }
+              const float top = fmaxf(top0, top1);
+              if (again || !__any_sync(0xffffffffu, unset ? top > -INFINITY : top > kMost)) break;
+              // by how much the reference rises; the first score that is there sets it
+              float up = 0.f, shrink = 1.f;
+              if (!unset) {
+                const float to = ref + fmaxf(ceilf(top - kLift), 0.f);
+                up = to - ref;
+                shrink = exp2_fast(-up);
+                ref = to;
+              } else if (top > -INFINITY) {
+                ref = ceilf(top - kLift);
+                unset = false;
+              }
+              sum *= shrink;
+              if (__any_sync(0xffffffffu, shrink != 1.f)) {
+                if (h > 0) {  // P of the tile's tokens before these
+                  const __half2 f = __float2half2_rn(shrink);
+                  tmem_st_wait();
+#pragma unroll 1
+                  for (int d = 0; d < 16 * h; d += 16) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(s_at + d, o);
+                    tmem_ld_wait_tied16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f);
+                      o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    tmem_st_32x32b_x16(s_at + d, o);
+                  }
+                }
+                if (j > j0) {
+                  if (!(ok = warp_wait(&bar.o_full[i], (mine - 1) & 1))) break;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int d = 0; d < kDim; d += 16) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(o_at + d, o);
+                    tmem_ld_wait_tied16(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+                    tmem_st_32x32b_x16(o_at + d, o);
+                  }
+                }
+              }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) sum = fmaf(sums[g], tab[2 * h + g].per, sum);
+            tmem_st_32x32b_x16(s_at + 16 * h, p);  // (where scores have been used)
+          }
+          if (!ok) break;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -534,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float vref = u->vref;
       uint32_t lost[kDim / 32] = {};
       if (u->bad) {
-        const int from = row_limit(a, u->len, u->n, u->row0) / kTok * kTok;
+        const int from = u->first / kTok * kTok;
         if (row_ok)
           find_not_finite<kDim, kE5M2>(a, u->b, u->head, max(from, j0 * kTok), min(limit, j1 * kTok), status, lost);
       }
@@ -585,165 +642,153 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- keys and values
+    // Three tiles are in hand at once: one whose table entries are on their way, one whose codes and scales
+    // are, and the one that becomes FP16.
     regs_decrease<kConvRegs>();
-    // Four tiles are in hand at once: one whose table entry is on its way, one whose scales are, one whose
-    // codes are (into this thread's places in shared memory, so that no other has to be waited for), and
-    // the one that becomes FP16.
     const int ct = threadIdx.x - 32 * kConvWarp;
     // Eight neighbouring threads have four pieces of two neighbouring tokens: their chunks of FP16 meet
     // all banks.
     const int piece = kDim == 128 ? (ct & 3) | (ct >> 1 & 4) : ct & 3;
     const int row0 = kDim == 128 ? (ct >> 2 & 1) | (ct >> 4 << 1) : ct >> 2;
-    constexpr int kRowsAtOnce = 128 / (kDim / 16);  // tokens that the 128 threads cover at once
+    constexpr int kRowsAtOnce = 128 / (kDim / 16);  // tokens that the 128 threads cover at once: a multiple of 8
     constexpr int kLoads = kTok / kRowsAtOnce;
+    const int in_block = (row0 & 15) * kDim + 16 * piece;
+    const uint32_t to0 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece) - smem);
+    const uint32_t to1 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece + 1) - smem);
     struct InHand {
-      bool valid, last;  // of its unit
-      int slot, j, vis, first;
-      int blk;           // lane g < 8: block of tokens 16 g .. 16 g + 15
-      long long off;     // and where its head's codes begin there
-      float ks, vs;
+      int slot, j;  // slot < 0: none
+      bool last;    // of its unit
     };
-    InHand h0, h1, h2, h3;
-    h0.valid = h1.valid = h2.valid = h3.valid = false;
+    InHand h0 = {-1, 0, false}, h1 = h0, h2 = h0;
+    long long off = -1;     // of h1: lane g < 8: where tokens 16 g .. 16 g + 15 lie; -1: nowhere
+    int blk = 0;            // of h2: their block, where one is wanted
+    bool wanted = false;
+    bool there = false, there1 = false;  // scales of h0 and h1
+    float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f, vref = 1.f;
+    uint8_t* codes_k = smem + S::kCodes + 16 * ct;
+    uint8_t* codes_v = codes_k + kTok * kDim;
     uint32_t taken = 0, it = 0;
     bool ended = false, ok = true;
-    int b = 0, head = 0, j = 0, j1 = 0, vis = 0, first = 0, slot = 0;  // what is looked up next
-    float vref = 1.f;
-    uint8_t* codes_k = smem + S::kCodes;
-    uint8_t* codes_v = codes_k + kTok * kDim;
-    auto fetch = [&](const uint8_t* cache, uint8_t* to, const InHand& h) {
-      if (h.valid) {
-#pragma unroll 4
+    int j = 0, j1 = 0, slot = 0;  // what is looked up next
+    // codes of h1 into this thread's places in shared memory: no other thread has to be waited for, and
+    // what is on its way takes no registers
+    auto fetch = [&](const uint8_t* cache, uint8_t* codes) {
+      if (h1.slot >= 0) {
+#pragma unroll
         for (int l = 0; l < kLoads; ++l) {
-          const int g = kDim == 128 ? l : 2 * l + (ct >> 6);
-          const long long off = __shfl_sync(0xffffffffu, h.off, g);
-          const uint8_t* from = cache + (off < 0 ? 0 : off + (row0 & 15) * kDim + 16 * piece);
-          cp_async_16(smem_addr(to + (l * 128 + ct) * 16), from, off < 0 ? 0u : 16u);
+          const long long from = __shfl_sync(0xffffffffu, off, kDim == 128 ? l : 2 * l + (ct >> 6));
+          cp_async_16(smem_addr(codes + l * 2048), cache + (from < 0 ? 0 : from + in_block), from < 0 ? 0u : 16u);
         }
       }
       cp_async_commit();
     };
-    auto put = [&](uint8_t* tile, int row, const uint32_t (&w)[4], uint32_t keep, uint32_t flip) {
-      uint32_t x[8];
+    auto convert = [&](uint8_t* tile, const uint8_t* codes, uint64_t* full) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e])) & keep) ^ flip;
-        x[2 * e + 1] = (f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16)) & keep) ^ flip;
+      for (int l = 0; l < kLoads; ++l) {
+        const uint4 v = *reinterpret_cast<const uint4*>(codes + l * 2048);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[2 * e] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e]));
+          x[2 * e + 1] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16));
+        }
+        *reinterpret_cast<uint4*>(tile + to0 + l * kRowsAtOnce * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(tile + to1 + l * kRowsAtOnce * 128) = make_uint4(x[4], x[5], x[6], x[7]);
       }
-      *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece)) = make_uint4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, 2 * piece + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
     };
     while (true) {
       const int st = it % kStages;
       const uint32_t ph = (it / kStages) & 1;
-      const Tab* tab = tabs + (it % kTabs) * kGroups;
-      if (h0.valid) {
+      Tab* tab = tabs + (it % kTabs) * kGroups;
+      if (h0.slot >= 0) {
         if (!(ok = warp_wait(&bar.k_empty[st], ph ^ 1))) break;
-        if (warp == kConvWarp) {  // the tile's scales (its place was read long ago: see kTabs)
-          const bool there = h0.blk >= 0, fin = fabsf(h0.vs) <= FLT_MAX;
-          const float av = there && fin && h0.vs != 0.f ? fabsf(h0.vs) : 1.f;
+        if (warp == kConvWarp) {  // the tile's scales (their place was read long ago: see kTabs)
+          const bool fin = fabsf(vs) <= FLT_MAX;
+          const float av = there && fin && vs != 0.f ? fabsf(vs) : 1.f;
           if (h0.j == ring(h0.slot)->j0) {
             vref = __shfl_sync(0xffffffffu, av, 0);
             if (lane == 0) ring(h0.slot)->vref = vref;
           }
           if (lane < kGroups) {
             Tab t;
-            t.k = there ? h0.ks : 0.f;
-            t.add = there ? log2f(av) : -INFINITY;
-            t.per = there ? __fdiv_rn(vref, av) : 0.f;
-            t.mode = !there ? 0u : !fin ? kNotFinite : h0.vs == 0.f ? kZero : h0.vs < 0.f ? kNegate : 0u;
-            tabs[(it % kTabs) * kGroups + lane] = t;
+            t.k = there ? ks : 0.f;
+            // (an error of either is one of the block's weight, 2^-15 at most)
+            t.add = there ? __log2f(av) : -INFINITY;
+            t.per = there ? __fdividef(vref, av) : 0.f;
+            t.mode = !there ? 0u : !fin ? kNotFinite : vs == 0.f ? kZero : vs < 0.f ? kNegate : 0u;
+            tab[lane] = t;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.tab_full[it % kTabs]);
         }
         cp_async_wait<1>();
-        uint8_t* tile = smem + S::kK + st * S::kTileBytes;
-#pragma unroll 4
-        for (int l = 0; l < kLoads; ++l) {
-          const uint4 x = *reinterpret_cast<const uint4*>(codes_k + (l * 128 + ct) * 16);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-          put(tile, row0 + kRowsAtOnce * l, w, 0xffffffffu, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.k_full[st]);
+        convert(smem + S::kK + st * S::kTileBytes, codes_k, &bar.k_full[st]);
       }
-      fetch(a.kc, codes_k, h1);
-      if (h0.valid) {
+      fetch(a.kc, codes_k);
+      if (h0.slot >= 0) {
         if (!(ok = warp_wait(&bar.v_empty[st], ph ^ 1))) break;
         if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
         cp_async_wait<1>();
-        uint8_t* tile = smem + S::kV + st * S::kTileBytes;
-        const uint32_t modes = lane < kGroups ? tab[lane].mode : 0u;
-        const int there = h0.vis - h0.j * kTok;  // tokens of the tile that are there
-        if (h0.j * kTok + kTok <= h0.first && !__any_sync(0xffffffffu, modes != 0u)) {
-#pragma unroll 4
-          for (int l = 0; l < kLoads; ++l) {
-            const uint4 x = *reinterpret_cast<const uint4*>(codes_v + (l * 128 + ct) * 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            put(tile, row0 + kRowsAtOnce * l, w, 0xffffffffu, 0u);
-          }
-        } else {
-          // Some scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times what is
-          // not finite would reach rows that do not see it: such values become 0, and the rows that do see
-          // them are marked when the unit ends.
-          const bool mixed = h0.j * kTok + kTok > h0.first;
-          uint32_t bad = 0u;
+        Unit* u = ring(h0.slot);
+        const bool mixed = h0.j * kTok + kTok > u->first;
+        if (__any_sync(0xffffffffu, mixed || (lane < kGroups && tab[lane].mode != 0u))) {
+          // Some value scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times
+          // what is not finite would reach rows that do not see it: such values become 0, and the rows that
+          // do see them are marked when the unit ends.
+          const int n = u->vis - h0.j * kTok;  // tokens of the tile that are there
+          bool bad = false;
 #pragma unroll 1
           for (int l = 0; l < kLoads; ++l) {
             const int r = row0 + kRowsAtOnce * l;
-            const uint4 x = *reinterpret_cast<const uint4*>(codes_v + (l * 128 + ct) * 16);
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
             const uint32_t mode = tab[r / 16].mode;
-            uint32_t keep = mode & kZero || r >= there ? 0u : 0xffffffffu;
-            uint32_t flip = mode & kNegate ? 0x80008000u : 0u;
-            if (mode & kNotFinite) {
-              keep = 0u;
-              if (!mixed)
-                flip = 0x7fff7fffu;
-              else if (r < there)
-                bad = 1u;
-            } else if (mixed) {
+            uint4* at = reinterpret_cast<uint4*>(codes_v + l * 2048);
+            const uint4 v = *at;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t m = not_finite4<kE5M2>(w[e]);
-                if (r < there) bad |= m;
-                w[e] &= ~m;
+            for (int e = 0; e < 4; ++e) {
+              uint32_t lost = mode & kNotFinite ? 0xffffffffu : mixed ? not_finite4<kE5M2>(w[e]) : 0u;
+              if (r >= n || (mode & kZero)) {
+                w[e] = lost = 0u;
+              } else if (mode & kNegate) {
+                w[e] ^= 0x80808080u;
               }
+              bad |= mixed && lost != 0u;
+              w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
             }
-            put(tile, r, w, keep, flip);
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (bad != 0u) ring(h0.slot)->bad = 1;
+          if (bad) u->bad = 1;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar.v_full[st]);
-          if (h0.last) mbar_arrive(&bar.ring_empty[h0.slot]);
-        }
+        convert(smem + S::kV + st * S::kTileBytes, codes_v, &bar.v_full[st]);
+        if (h0.last && lane == 0) mbar_arrive(&bar.ring_empty[h0.slot]);
         ++it;
       }
-      fetch(a.vc, codes_v, h1);
+      fetch(a.vc, codes_v);
       // ---- on by one
       h0 = h1;
+      there = there1;
+      ks = ks1;
+      vs = vs1;
       h1 = h2;
-      h2 = h3;
-      if (h2.valid) {
-        h2.off = -1;
-        h2.ks = h2.vs = 0.f;
-        if (h2.blk >= a.num_blocks || h2.blk < -1) {
-          raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-          h2.blk = -1;
-        }
-        if (h2.blk >= 0) {
-          const long long t = (long long)h2.blk * a.heads + ring(h2.slot)->head;
-          h2.off = (t * a.block + (16 * lane & (a.block - 1))) * kDim;
-          h2.ks = a.ks[t];
-          h2.vs = a.vs[t];
+      if (h1.slot >= 0) {
+        off = -1;
+        there1 = wanted && blk >= 0 && blk < a.num_blocks;
+        if (wanted && !there1) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+        ks1 = vs1 = 0.f;
+        if (there1) {
+          const long long t = (long long)blk * a.heads + ring(h1.slot)->head;
+          off = (t * a.block + ((16 * lane) & (a.block - 1))) * kDim;
+          if (warp == kConvWarp) {
+            ks1 = a.ks[t];
+            vs1 = a.vs[t];
+          }
         }
       }
-      h3.valid = false;
+      h2.slot = -1;
       while (j == j1 && !ended) {
         slot = taken % kRing;
         if (!(ok = warp_wait(&bar.ring_full[slot], (taken / kRing) & 1))) break;
@@ -753,12 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++taken;
-        b = u->b;
-        head = u->head;
         j = u->j0;
         j1 = u->j1;
-        first = row_limit(a, u->len, u->n, u->row0);               // what the first row sees
-        vis = row_limit(a, u->len, u->n, u->row0 + u->rows - 1);   // and the last
         if (j == j1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
@@ -766,19 +807,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (j < j1) {
-        h3.valid = true;
-        h3.last = j + 1 == j1;
-        h3.slot = slot;
-        h3.j = j;
-        h3.vis = vis;
-        h3.first = first;
+        const Unit* u = ring(slot);
+        h2 = {slot, j, j + 1 == j1};
         const int tok = j * kTok + 16 * lane;
-        h3.blk = lane < kGroups && tok < vis ? a.table[(long long)b * a.width + (tok >> a.log_block)] : -1;
-        // (an entry of -1 counts as no block; it is reported like any other that is out of range)
-        if (lane < kGroups && tok < vis && h3.blk == -1) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+        wanted = lane < kGroups && tok < u->vis;
+        if (wanted) blk = a.table[(long long)u->b * a.width + (tok >> a.log_block)];  // (not looked at yet)
         ++j;
       }
-      if (ended && !h0.valid && !h1.valid && !h2.valid && !h3.valid) break;
+      if (ended && h0.slot < 0 && h1.slot < 0 && h2.slot < 0) break;
     }
     cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
@@ -791,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t q_desc = smem_desc_sw128_kmajor(smem_addr(smem + S::kQ));
     const uint64_t k_desc = smem_desc_sw128_kmajor(smem_addr(smem + S::kK));
     const uint64_t v_desc = smem_desc_sw128_mnmajor(smem_addr(smem + S::kV), S::kSubBytes);
-    uint32_t it = 0, n_q[2] = {0, 0}, n_p[2] = {0, 0};
+    uint32_t it = 0, n_0 = 0, n_1 = 0, units_0 = 0, units_1 = 0;
     bool issued = false;
     auto scores = [&](int i, int st) {
       if (elect_one()) {
@@ -825,34 +861,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = __reduce_max_sync(0xffffffffu, u->kind == kEnd ? -1 : u->j1 - u->j0);
       const int tiles = __reduce_max_sync(0xffffffffu, u->rows > kTileRows ? 2 : 1);
       if (n < 0) break;
-      if (n > 0) {
-        ok = warp_wait(&bar.k_full[it % kStages], (it / kStages) & 1);
+#pragma unroll 1
+      for (int j = 0; j <= n && n > 0; ++j) {  // scores of tile j behind the values of tile j - 1
+        const uint32_t before = it - 1;
+        if (j < n) ok = warp_wait(&bar.k_full[it % kStages], (it / kStages) & 1);
+        if (ok && j > 0) ok = warp_wait(&bar.v_full[before % kStages], (before / kStages) & 1);
+#pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
-          if (!(ok = warp_wait(&bar.q_full[i], n_q[i]++ & 1))) break;
+          const uint32_t n_i = i ? n_1 : n_0;  // tiles of tokens that this tile of rows has had
+          if (j == 0)
+            ok = warp_wait(&bar.q_full[i], (i ? units_1++ : units_0++) & 1);
+          else
+            ok = warp_wait(&bar.p_full[i], (n_i + j - 1) & 1);
+          if (!ok) break;
           tc_fence_after();
-          scores(i, it % kStages);
-        }
-        if (ok) commit(&bar.k_empty[it % kStages]);
-      }
-      for (int j = 0; j < n && ok; ++j, ++it) {
-        const int st = it % kStages, st1 = (it + 1) % kStages;
-        if (!(ok = warp_wait(&bar.v_full[st], (it / kStages) & 1))) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i == tiles) break;
-          if (!(ok = warp_wait(&bar.p_full[i], n_p[i]++ & 1))) break;
-          tc_fence_after();
-          values(i, st, j == 0);
-          if (j + 1 < n) {
-            if (i == 0 && !(ok = warp_wait(&bar.k_full[st1], ((it + 1) / kStages) & 1))) break;
-            tc_fence_after();
-            scores(i, st1);
-          }
+          if (j > 0) values(i, before % kStages, j == 1);
+          if (j < n) scores(i, it % kStages);
         }
         if (!ok) break;
-        commit(&bar.v_empty[st]);
-        if (j + 1 < n) commit(&bar.k_empty[st1]);
+        if (j > 0) commit(&bar.v_empty[before % kStages]);
+        if (j < n) {
+          commit(&bar.k_empty[it % kStages]);
+          ++it;
+        }
       }
+      n_0 += n;
+      if (tiles > 1) n_1 += n;
       if (ok && lane == 0) mbar_arrive(&bar.ring_empty[slot]);
     }
     if (issued) {  // every issued product has finished before TMEM is released
@@ -879,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long lo = share.lo, hi = share.hi;
       if (lo < hi) {
         long long at = lo, off = share.off;  // off: cost before `at` within the sequence, then the unit
-        int head = int(lo / share.list), b = share.b, un = 0;
+        int head = share.head, b = share.b, un = 0;
         Seq s = sequence(a, b, status);
         // the unit that holds the offset, 32 at a time
         while (true) {
@@ -923,6 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           unit.rows = min(kUnitRows, s.n * a.group - unit.row0);
           unit.j0 = int(max(0LL, off - kUnitCost));
           unit.j1 = int(max(0LL, x1 - kUnitCost));
+          unit.first = row_limit(a, s.len, s.n, unit.row0);
+          unit.vis = row_limit(a, s.len, s.n, unit.row0 + unit.rows - 1);
           unit.bad = 0;
           unit.vref = 1.f;
           unit.kind = unit.j0 > 0 ? kLater : unit.j1 < tiles ? kFirst : kWhole;
@@ -930,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (unit.kind == kFirst) {
               const long long end = begin + cost;  // its parts: this CTA's and those that begin before its end
               int last = blockIdx.x;
-              while (last + 1 < share.ctas && first_of(share.total, share.ctas, last + 1) < end) ++last;
+              while (share.each * (last + 1) < end) ++last;
               split = {last - int(blockIdx.x) + 1, head, s.t0, unit.row0, unit.rows};
             }
             ok = give(unit);
