@@ -18,6 +18,7 @@
 //   warp 12          issues the products: while tile 0's softmax runs, tile 1's
 //                    products do
 //   warp 13          finds the CTA's units and hands them on through a ring
+//   warp 14          looks up where the units' tiles lie and their scales, ahead of the others
 //
 // Scales act in FP32 where they can: a key block's on the scores.  A value block's cannot act
 // behind the product, whose sum runs over blocks, nor inside P or V as it is, which FP16's range
@@ -48,12 +49,12 @@ constexpr int kTileRows = 128, kUnitRows = 2 * kTileRows;
 constexpr int kTok = 128;   // tokens of a tile
 constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of one instruction
 constexpr int kThreads = 512;
-constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kScoutWarp = 14;
 // 512 threads are launched with 128 registers each: 512 for the four warps of a sub-partition
-constexpr uint32_t kSoftRegs = 176, kConvRegs = 80, kLowRegs = 80;
+constexpr uint32_t kSoftRegs = 168, kConvRegs = 96, kLowRegs = 80;
 static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
 constexpr int kStages = 2;  // of keys and of values
-constexpr int kTabs = 4;    // tiles' scales
+constexpr int kTabs = 8;    // tiles of which it is known where they lie
 constexpr int kRing = 4;    // units
 constexpr int kUnitCost = 3;  // what a unit's start and end cost, in tiles
 constexpr int kMinShare = 4;  // tiles of a CTA's share, at least
@@ -71,7 +72,6 @@ struct Unit {
   int j0, j1;
   int first, vis;   // tokens that its first row and its last one see
   int bad;          // values that are not finite were hidden in tiles that some rows do not see whole
-  float vref;       // value scale that the sums of p are relative to
 };
 
 // What the join has to know of a unit that CTA c begins and others go on with.
@@ -80,12 +80,23 @@ struct Split {
   int head, t0, row0, rows;
 };
 
-struct Tab {  // 16 tokens' scales
+// What the roles need of a tile of tokens, found ahead of them.
+struct Scales {   // of 16 tokens
   float k;        // of the keys
   float add;      // log2 |v_scale| (of 1 for scales of 0 and such as are not finite), -infinity without a block
-  float per;      // vref / |v_scale|
+  float inv;      // 1 / |v_scale|
   uint32_t mode;  // what becomes of the values' codes: see kZero, kNegate, kNotFinite
 };
+struct Tab {
+  Scales g[kGroups];
+  int row[kGroups];  // of the cache's rows [num_blocks, heads, block]: where 16 tokens begin, -1: nowhere
+  int slot;          // the tile's unit; -1: no more tiles
+  int last;          // of its unit
+  int there, whole;  // tokens that the unit's last row sees, and its first one (may lie outside 0 .. 128)
+  float v0;          // |v_scale| of its first tokens
+  int pad[3];
+};
+static_assert(sizeof(Tab) == 192, "tile record");
 enum : uint32_t { kZero = 1, kNegate = 2, kNotFinite = 4 };
 
 // Tokens that row r of a sequence sees.
@@ -207,9 +218,9 @@ struct Smem {
   static constexpr size_t kQ = 0, kK = kQ + 2 * kTileBytes, kV = kK + kStages * kTileBytes;
   static constexpr size_t kCodes = kV + kStages * kTileBytes;  // keys' and values' codes on their way
   static constexpr size_t kTab = kCodes + 2 * kTok * kDim;
-  static constexpr size_t kUnits = kTab + kTabs * kGroups * sizeof(Tab);
+  static constexpr size_t kUnits = kTab + kTabs * sizeof(Tab);
   static constexpr size_t kBars = kUnits + kRing * 64;
-  static constexpr size_t kBytes = 1024 + kBars + 512;
+  static constexpr size_t kBytes = kBars + 512;
   static_assert(sizeof(Unit) <= 64, "ring slot");
   static_assert(kBytes <= 232448, "227 KB of shared memory per CTA");
 };
@@ -217,11 +228,12 @@ struct Smem {
 struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  uint64_t tab_full[kTabs];
+  uint64_t tab_full[kTabs], tab_empty[kTabs];
   uint64_t ring_full[kRing], ring_empty[kRing];
   uint64_t drain;
   uint32_t tmem;
   int abort;
+  Share share;
 };
 static_assert(sizeof(Bars) <= 512, "barrier area");
 
@@ -291,6 +303,10 @@ __device__ __forceinline__ uint32_t not_finite4(uint32_t w) {
   return __vcmpeq4(w & kBad, kBad);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Block of token tok of the unit's sequence, -1 where there is none.
 __device__ __forceinline__ int block_of(const KvChunkArgs& a, int b, int tok, int vis, int* status) {
   if (tok >= vis) return -1;
@@ -323,14 +339,12 @@ template <int kDim, bool kE5M2>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_chunk_kernel(const __grid_constant__ KvChunkArgs a, float* parts, Split* splits, int* status) {
   using S = Smem<kDim>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (no static shared memory before it)
   Tab* tabs = reinterpret_cast<Tab*>(smem + S::kTab);
   auto ring = [&](int slot) { return reinterpret_cast<Unit*>(smem + S::kUnits + 64 * slot); };
   Bars& bar = *reinterpret_cast<Bars*>(smem + S::kBars);
   volatile int* abort_flag = &bar.abort;
-  __shared__ Share share;
-  __shared__ long long sums[kThreads / 32];
+  Share& share = bar.share;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -346,7 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_full[i], 1);
     }
-    for (int i = 0; i < kTabs; ++i) mbar_init(&bar.tab_full[i], 1);
+    for (int i = 0; i < kTabs; ++i) {
+      mbar_init(&bar.tab_full[i], 1);
+      mbar_init(&bar.tab_empty[i], 4);
+    }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar.ring_full[i], 1);
       mbar_init(&bar.ring_empty[i], 8 + 4 + 1);
@@ -361,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  find_share(a, &share, sums, status);
+  find_share(a, &share, reinterpret_cast<long long*>(smem), status);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = u->head * a.group + seq_row % a.group;
       const int limit = row_ok ? row_limit(a, u->len, u->n, seq_row) : 0x7fffffff;
       const int least = __shfl_sync(0xffffffffu, limit, 0);  // rows see more and more
-      float ref = 0.f, sum = 0.f;
+      float ref = 0.f, sum = 0.f, vref = 1.f;  // sum: of p over vref's share of |v_scale|
       bool unset = true;
       if (j1 > j0) {
         const float down = stage_query<kDim>(
@@ -425,13 +442,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.q_full[i]);
         bool ok = true;
         for (int j = j0; j < j1; ++j, ++it, ++mine) {
-          const Tab* tab = tabs + (it % kTabs) * kGroups;
+          const Scales* tab = tabs[it % kTabs].g;
           // (in this order: a tile of rows that sat out a unit may be ahead of the scales' ring, but
-          // its own scores are there only once the tile's scales are)
+          // its own scores are there only once the tile's record is)
           if (!(ok = warp_wait(&bar.s_full[i], mine & 1))) break;
           if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
           tc_fence_after();
           const int tok = j * kTok;
+          if (j == j0) vref = tabs[it % kTabs].v0;
           // The plain case, to which most tiles belong: all rows see all tokens and the reference need not
           // rise, as is known once P is there, in registers.
           bool plain = !__any_sync(0xffffffffu, unset) && tok + kTok <= least;
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float sum1 = sum2.x + sum2.y;
                 most = fmaxf(most, sum1);  // no P is larger
-                part = fmaf(sum1, tab[2 * h + g].per, part);
+                part = fmaf(sum1, tab[2 * h + g].inv * vref, part);
               }
             };
             // two loads ahead: they take long beside the products' own traffic
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) sum = fmaf(sums[g], tab[2 * h + g].per, sum);
+            for (int g = 0; g < 2; ++g) sum = fmaf(sums[g], tab[2 * h + g].inv * vref, sum);
             tmem_st_32x32b_x16(s_at + 16 * h, p);  // (where scores have been used)
           }
           if (!ok) break;
@@ -588,7 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       // ---- the rows' end: whole units go to O, parts to the workspace
-      const float vref = u->vref;
       uint32_t lost[kDim / 32] = {};
       if (u->bad) {
         const int from = u->first / kTok * kTok;
@@ -642,8 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- keys and values
-    // Three tiles are in hand at once: one whose table entries are on their way, one whose codes and scales
-    // are, and the one that becomes FP16.
     regs_decrease<kConvRegs>();
     const int ct = threadIdx.x - 32 * kConvWarp;
     // Eight neighbouring threads have four pieces of two neighbouring tokens: their chunks of FP16 meet
@@ -655,166 +670,107 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int in_block = (row0 & 15) * kDim + 16 * piece;
     const uint32_t to0 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece) - smem);
     const uint32_t to1 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece + 1) - smem);
-    struct InHand {
-      int slot, j;  // slot < 0: none
-      bool last;    // of its unit
-    };
-    InHand h0 = {-1, 0, false}, h1 = h0, h2 = h0;
-    long long off = -1;     // of h1: lane g < 8: where tokens 16 g .. 16 g + 15 lie; -1: nowhere
-    int blk = 0;            // of h2: their block, where one is wanted
-    bool wanted = false;
-    bool there = false, there1 = false;  // scales of h0 and h1
-    float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f, vref = 1.f;
     uint8_t* codes_k = smem + S::kCodes + 16 * ct;
     uint8_t* codes_v = codes_k + kTok * kDim;
-    uint32_t taken = 0, it = 0;
-    bool ended = false, ok = true;
-    int j = 0, j1 = 0, slot = 0;  // what is looked up next
-    // codes of h1 into this thread's places in shared memory: no other thread has to be waited for, and
-    // what is on its way takes no registers
-    auto fetch = [&](const uint8_t* cache, uint8_t* codes) {
-      if (h1.slot >= 0) {
+    // A tile's codes into this thread's places in shared memory: no other thread has to be waited for, and
+    // what is on its way takes no registers.
+    auto fetch = [&](const uint8_t* cache, uint8_t* codes, const Tab& t) {
 #pragma unroll
-        for (int l = 0; l < kLoads; ++l) {
-          const long long from = __shfl_sync(0xffffffffu, off, kDim == 128 ? l : 2 * l + (ct >> 6));
-          cp_async_16(smem_addr(codes + l * 2048), cache + (from < 0 ? 0 : from + in_block), from < 0 ? 0u : 16u);
-        }
+      for (int l = 0; l < kLoads; ++l) {
+        const int row = t.row[kDim == 128 ? l : 2 * l + (ct >> 6)];
+        cp_async_16(smem_addr(codes + l * 2048), cache + ((long long)max(row, 0) * kDim + in_block), row < 0 ? 0u : 16u);
       }
-      cp_async_commit();
     };
     auto convert = [&](uint8_t* tile, const uint8_t* codes, uint64_t* full) {
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        const uint4 v = *reinterpret_cast<const uint4*>(codes + l * 2048);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t x[8];
+      for (int l0 = 0; l0 < kLoads; l0 += 4) {
+        uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e]));
-          x[2 * e + 1] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16));
+        for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const uint4*>(codes + (l0 + l) * 2048);
+#pragma unroll
+        for (int l = 0; l < 4; ++l) {
+          const uint32_t w[4] = {v[l].x, v[l].y, v[l].z, v[l].w};
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e]));
+            x[2 * e + 1] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16));
+          }
+          const int at = (l0 + l) * kRowsAtOnce * 128;
+          *reinterpret_cast<uint4*>(tile + to0 + at) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(tile + to1 + at) = make_uint4(x[4], x[5], x[6], x[7]);
         }
-        *reinterpret_cast<uint4*>(tile + to0 + l * kRowsAtOnce * 128) = make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4*>(tile + to1 + l * kRowsAtOnce * 128) = make_uint4(x[4], x[5], x[6], x[7]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     };
-    while (true) {
+    auto tab_of = [&](uint32_t n) -> const Tab& { return tabs[n % kTabs]; };
+    bool ok = warp_wait(&bar.tab_full[0], 0);
+    if (ok && tab_of(0).slot >= 0) {
+      fetch(a.kc, codes_k, tab_of(0));
+      cp_async_commit();
+      fetch(a.vc, codes_v, tab_of(0));
+      cp_async_commit();
+    }
+    for (uint32_t it = 0; ok && tab_of(it).slot >= 0; ++it) {
       const int st = it % kStages;
       const uint32_t ph = (it / kStages) & 1;
-      Tab* tab = tabs + (it % kTabs) * kGroups;
-      if (h0.slot >= 0) {
-        if (!(ok = warp_wait(&bar.k_empty[st], ph ^ 1))) break;
-        if (warp == kConvWarp) {  // the tile's scales (their place was read long ago: see kTabs)
-          const bool fin = fabsf(vs) <= FLT_MAX;
-          const float av = there && fin && vs != 0.f ? fabsf(vs) : 1.f;
-          if (h0.j == ring(h0.slot)->j0) {
-            vref = __shfl_sync(0xffffffffu, av, 0);
-            if (lane == 0) ring(h0.slot)->vref = vref;
-          }
-          if (lane < kGroups) {
-            Tab t;
-            t.k = there ? ks : 0.f;
-            // (an error of either is one of the block's weight, 2^-15 at most)
-            t.add = there ? __log2f(av) : -INFINITY;
-            t.per = there ? __fdividef(vref, av) : 0.f;
-            t.mode = !there ? 0u : !fin ? kNotFinite : vs == 0.f ? kZero : vs < 0.f ? kNegate : 0u;
-            tab[lane] = t;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.tab_full[it % kTabs]);
-        }
-        cp_async_wait<1>();
-        convert(smem + S::kK + st * S::kTileBytes, codes_k, &bar.k_full[st]);
-      }
-      fetch(a.kc, codes_k);
-      if (h0.slot >= 0) {
-        if (!(ok = warp_wait(&bar.v_empty[st], ph ^ 1))) break;
-        if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
-        cp_async_wait<1>();
-        Unit* u = ring(h0.slot);
-        const bool mixed = h0.j * kTok + kTok > u->first;
-        if (__any_sync(0xffffffffu, mixed || (lane < kGroups && tab[lane].mode != 0u))) {
-          // Some value scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times
-          // what is not finite would reach rows that do not see it: such values become 0, and the rows that
-          // do see them are marked when the unit ends.
-          const int n = u->vis - h0.j * kTok;  // tokens of the tile that are there
-          bool bad = false;
+      const Tab& tab = tab_of(it);
+      const Tab& next = tab_of(it + 1);
+      uint64_t* next_full = &bar.tab_full[(it + 1) % kTabs];
+      const uint32_t next_ph = ((it + 1) / kTabs) & 1;
+      if (!(ok = warp_wait(&bar.k_empty[st], ph ^ 1))) break;
+      cp_async_wait<1>();
+      convert(smem + S::kK + st * S::kTileBytes, codes_k, &bar.k_full[st]);
+      // The next tile's keys, if it is known yet.  (It may be that of a unit which has to wait for the end of this
+      // one's: behind units without tiles.)
+      const bool early = __all_sync(0xffffffffu, mbar_test(next_full, next_ph));
+      if (early && next.slot >= 0) fetch(a.kc, codes_k, next);
+      cp_async_commit();
+      if (!(ok = warp_wait(&bar.v_empty[st], ph ^ 1))) break;
+      // the values of two tiles ago have been used, and so have their scales
+      if (lane == 0 && it >= 2) mbar_arrive(&bar.tab_empty[(it - 2) % kTabs]);
+      cp_async_wait<1>();
+      const bool mixed = tab.whole < kTok;
+      if (__any_sync(0xffffffffu, mixed || tab.g[lane % kGroups].mode != 0u)) {
+        // Some value scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times
+        // what is not finite would reach rows that do not see it: such values become 0, and the rows that
+        // do see them are marked when the unit ends.
+        bool bad = false;
 #pragma unroll 1
-          for (int l = 0; l < kLoads; ++l) {
-            const int r = row0 + kRowsAtOnce * l;
-            const uint32_t mode = tab[r / 16].mode;
-            uint4* at = reinterpret_cast<uint4*>(codes_v + l * 2048);
-            const uint4 v = *at;
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int l = 0; l < kLoads; ++l) {
+          const int r = row0 + kRowsAtOnce * l;
+          const uint32_t mode = tab.g[r / 16].mode;
+          uint4* at = reinterpret_cast<uint4*>(codes_v + l * 2048);
+          const uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t lost = mode & kNotFinite ? 0xffffffffu : mixed ? not_finite4<kE5M2>(w[e]) : 0u;
-              if (r >= n || (mode & kZero)) {
-                w[e] = lost = 0u;
-              } else if (mode & kNegate) {
-                w[e] ^= 0x80808080u;
-              }
-              bad |= mixed && lost != 0u;
-              w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
+          for (int e = 0; e < 4; ++e) {
+            uint32_t lost = mode & kNotFinite ? 0xffffffffu : mixed ? not_finite4<kE5M2>(w[e]) : 0u;
+            if (r >= tab.there || (mode & kZero)) {
+              w[e] = lost = 0u;
+            } else if (mode & kNegate) {
+              w[e] ^= 0x80808080u;
             }
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            bad |= mixed && lost != 0u;
+            w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
           }
-          if (bad) u->bad = 1;
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        convert(smem + S::kV + st * S::kTileBytes, codes_v, &bar.v_full[st]);
-        if (h0.last && lane == 0) mbar_arrive(&bar.ring_empty[h0.slot]);
-        ++it;
+        if (bad) ring(tab.slot)->bad = 1;
       }
-      fetch(a.vc, codes_v);
-      // ---- on by one
-      h0 = h1;
-      there = there1;
-      ks = ks1;
-      vs = vs1;
-      h1 = h2;
-      if (h1.slot >= 0) {
-        off = -1;
-        there1 = wanted && blk >= 0 && blk < a.num_blocks;
-        if (wanted && !there1) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
-        ks1 = vs1 = 0.f;
-        if (there1) {
-          const long long t = (long long)blk * a.heads + ring(h1.slot)->head;
-          off = (t * a.block + ((16 * lane) & (a.block - 1))) * kDim;
-          if (warp == kConvWarp) {
-            ks1 = a.ks[t];
-            vs1 = a.vs[t];
-          }
+      convert(smem + S::kV + st * S::kTileBytes, codes_v, &bar.v_full[st]);
+      if (tab.last && lane == 0) mbar_arrive(&bar.ring_empty[tab.slot]);
+      if (!early && !(ok = warp_wait(next_full, next_ph))) break;
+      if (next.slot >= 0) {
+        if (!early) {
+          fetch(a.kc, codes_k, next);
+          cp_async_commit();
         }
+        fetch(a.vc, codes_v, next);
       }
-      h2.slot = -1;
-      while (j == j1 && !ended) {
-        slot = taken % kRing;
-        if (!(ok = warp_wait(&bar.ring_full[slot], (taken / kRing) & 1))) break;
-        const Unit* u = ring(slot);
-        if (u->kind == kEnd) {
-          ended = true;
-          break;
-        }
-        ++taken;
-        j = u->j0;
-        j1 = u->j1;
-        if (j == j1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
-        }
-      }
-      if (!ok) break;
-      if (j < j1) {
-        const Unit* u = ring(slot);
-        h2 = {slot, j, j + 1 == j1};
-        const int tok = j * kTok + 16 * lane;
-        wanted = lane < kGroups && tok < u->vis;
-        if (wanted) blk = a.table[(long long)u->b * a.width + (tok >> a.log_block)];  // (not looked at yet)
-        ++j;
-      }
-      if (ended && h0.slot < 0 && h1.slot < 0 && h2.slot < 0) break;
+      cp_async_commit();
     }
     cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
@@ -960,7 +916,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           unit.first = row_limit(a, s.len, s.n, unit.row0);
           unit.vis = row_limit(a, s.len, s.n, unit.row0 + unit.rows - 1);
           unit.bad = 0;
-          unit.vref = 1.f;
           unit.kind = unit.j0 > 0 ? kLater : unit.j1 < tiles ? kFirst : kWhole;
           if (tiles == 0 ? off == 0 : unit.j1 > unit.j0) {
             if (unit.kind == kFirst) {
@@ -980,6 +935,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit end = {};
       end.kind = kEnd;
       if (ok) give(end);
+    } else if (warp == kScoutWarp) {
+      // ------------------------------------------- where tiles lie, and their scales
+      // Up to four tiles at a time, eight lanes each: table entries, then scales, are the latencies that nothing
+      // else of the tile can start before.
+      uint32_t it = 0, taken = 0;
+      int j = 0, j1 = 0, slot = 0;
+      bool ended = false, ok = true;
+      while (ok && !ended) {
+        int mine = -1, mine_j = 0;  // the lane's tile: its unit's slot
+        int n = 0;
+        for (; n < 4; ++n) {
+          while (j == j1) {
+            const int s = taken % kRing;
+            const uint32_t ph = (taken / kRing) & 1;
+            // what has been found is not held back for a unit that is not there yet
+            if (n > 0 && !__all_sync(0xffffffffu, mbar_test(&bar.ring_full[s], ph))) break;
+            if (!(ok = warp_wait(&bar.ring_full[s], ph))) break;
+            const Unit* u = ring(s);
+            if (u->kind == kEnd) {
+              ended = true;
+              break;
+            }
+            ++taken;
+            slot = s;
+            j = u->j0;
+            j1 = u->j1;
+            if (j == j1) {  // no tiles: the converters will not see it
+              __syncwarp();
+              if (lane < 4) mbar_arrive(&bar.ring_empty[s]);
+            }
+          }
+          if (j == j1) break;
+          if (lane / kGroups == n) {
+            mine = slot;
+            mine_j = j;
+          }
+          ++j;
+        }
+        if (!ok) break;
+        const int g = lane % kGroups;
+        const Unit* u = ring(max(mine, 0));
+        const int tok = mine_j * kTok + 16 * g;
+        const bool wanted = mine >= 0 && tok < u->vis;
+        int blk = -1;
+        if (wanted) {
+          blk = a.table[(long long)u->b * a.width + (tok >> a.log_block)];
+          if (blk < 0 || blk >= a.num_blocks) {
+            raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+            blk = -1;
+          }
+        }
+        float ks = 0.f, vs = 0.f;
+        int row = -1;
+        if (blk >= 0) {
+          const int tile = blk * a.heads + u->head;  // (rows of the cache are fewer than 2^31)
+          ks = a.ks[tile];
+          vs = a.vs[tile];
+          row = tile * a.block + (tok & (a.block - 1));
+          prefetch_l2(a.kc + (long long)row * kDim, 16 * kDim);
+          prefetch_l2(a.vc + (long long)row * kDim, 16 * kDim);
+        }
+        const bool fin = fabsf(vs) <= FLT_MAX, used = fin && fabsf(vs) >= FLT_MIN;
+        const float av = used ? fabsf(vs) : 1.f;
+        Scales x;
+        x.k = ks;
+        // (its error is one of the weight of these tokens: 2^-15 at most)
+        x.add = blk >= 0 ? __log2f(av) : -INFINITY;
+        x.inv = blk >= 0 ? __frcp_rn(av) : 0.f;
+        x.mode = blk < 0 ? 0u : !fin ? kNotFinite : !used ? kZero : vs < 0.f ? kNegate : 0u;
+        const int total = n + (ended ? 1 : 0);  // and the end
+        for (int q = 0; q < total && ok; ++q, ++it) {
+          Tab& t = tabs[it % kTabs];
+          if (!(ok = warp_wait(&bar.tab_empty[it % kTabs], ((it / kTabs) & 1) ^ 1))) break;
+          if (q == n) {
+            if (lane == 0) t.slot = -1;
+          } else if (lane / kGroups == q) {
+            t.g[g] = x;
+            t.row[g] = row;
+            if (g == 0) {
+              t.slot = mine;
+              t.last = mine_j + 1 == u->j1;
+              t.there = u->vis - mine_j * kTok;
+              t.whole = u->first - mine_j * kTok;
+              t.v0 = av;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.tab_full[it % kTabs]);
+        }
+      }
     }
   }
 
