@@ -13,12 +13,13 @@
 // two tiles' S and O fill its 512 columns -- and P takes the place of S there.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1: thread = row = TMEM lane
-//   warps 8-11       keys and values: codes from the cache's blocks by asynchronous copies, a
-//                    tile ahead; as FP16 into a two-stage ring in shared memory (128-byte swizzle)
+//   warps 8-11       keys and values: codes to FP16, into a two-stage ring in shared memory
+//                    (128-byte swizzle)
 //   warp 12          issues the products: while tile 0's softmax runs, tile 1's
 //                    products do
 //   warp 13          finds the CTA's units and hands them on through a ring
 //   warp 14          looks up where the units' tiles lie and their scales, ahead of the others
+//   warp 15          asks for their codes
 //
 // Scales act in FP32 where they can: a key block's on the scores.  A value block's cannot act
 // behind the product, whose sum runs over blocks, nor inside P or V as it is, which FP16's range
@@ -49,9 +50,9 @@ constexpr int kTileRows = 128, kUnitRows = 2 * kTileRows;
 constexpr int kTok = 128;   // tokens of a tile
 constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of one instruction
 constexpr int kThreads = 512;
-constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kScoutWarp = 14;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kScoutWarp = 14, kLoadWarp = 15;
 // 512 threads are launched with 128 registers each: 512 for the four warps of a sub-partition
-constexpr uint32_t kSoftRegs = 168, kConvRegs = 96, kLowRegs = 80;
+constexpr uint32_t kSoftRegs = 176, kConvRegs = 80, kLowRegs = 80;
 static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
 constexpr int kStages = 2;  // of keys and of values
 constexpr int kTabs = 8;    // tiles of which it is known where they lie
@@ -91,10 +92,11 @@ struct Tab {
   Scales g[kGroups];
   int row[kGroups];  // of the cache's rows [num_blocks, heads, block]: where 16 tokens begin, -1: nowhere
   int slot;          // the tile's unit; -1: no more tiles
+  int all;           // all of them lie somewhere
   int last;          // of its unit
   int there, whole;  // tokens that the unit's last row sees, and its first one (may lie outside 0 .. 128)
   float v0;          // |v_scale| of its first tokens
-  int pad[3];
+  int pad[2];
 };
 static_assert(sizeof(Tab) == 192, "tile record");
 enum : uint32_t { kZero = 1, kNegate = 2, kNotFinite = 4 };
@@ -229,6 +231,7 @@ struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
   uint64_t tab_full[kTabs], tab_empty[kTabs];
+  uint64_t codes_full[2], codes_empty[2];  // keys', values'
   uint64_t ring_full[kRing], ring_empty[kRing];
   uint64_t drain;
   uint32_t tmem;
@@ -268,27 +271,27 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
 // into [2^10, 2^11); returns the reciprocal of that power.
 template <int kDim>
 __device__ __forceinline__ float stage_query(uint8_t* tile, int row, const __nv_bfloat16* q) {
+  Raw8<__nv_bfloat16> raw[kDim / 8];
   float top = 0.f;
-#pragma unroll 4
+#pragma unroll
   for (int c = 0; c < kDim / 8; ++c) {
-    Raw8<__nv_bfloat16> raw;
-    zero8(raw);
-    if (q) raw = load8(q + 8 * c);
+    zero8(raw[c]);
+    if (q) raw[c] = load8(q + 8 * c);
+  }
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) {
     float f[8];
-    unpack8(raw, f);
+    unpack8(raw[c], f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
   }
   // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
   const int exp = max(int(__float_as_uint(top) >> 23), 10);
   const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
-#pragma unroll 4
-  for (int c = 0; c < kDim / 8; ++c) {  // (read again, from the cache: a row would fill the registers)
-    Raw8<__nv_bfloat16> raw;
-    zero8(raw);
-    if (q) raw = load8(q + 8 * c);
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) {
     float f[8];
-    unpack8(raw, f);
+    unpack8(raw[c], f);
     *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c)) =
         make_uint4(f16x2_bits(f[0] * up, f[1] * up), f16x2_bits(f[2] * up, f[3] * up),
                    f16x2_bits(f[4] * up, f[5] * up), f16x2_bits(f[6] * up, f[7] * up));
@@ -355,6 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.codes_full[i], 1);
+      mbar_init(&bar.codes_empty[i], 4);
       mbar_init(&bar.q_full[i], 4);
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 4);
@@ -450,6 +455,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const int tok = j * kTok;
           if (j == j0) vref = tabs[it % kTabs].v0;
+          if (__any_sync(0xffffffffu, unset)) {  // a first reference, from the first 32 tokens that are there
+#pragma unroll 1
+            for (int h = 0; h < kTok / 32; ++h) {
+              uint32_t c[32];
+              tmem_ld_32x32b_x32(s_at + 32 * h, c);
+              tmem_ld_wait_tied(c);
+              float top = -INFINITY;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const float mul = q_mul * tab[2 * h + g].k, add = tab[2 * h + g].add;
+#pragma unroll
+                for (int e = 16 * g; e < 16 * g + 16; ++e) {
+                  const float x = fmaf(__uint_as_float(c[e]), mul, add);
+                  if (tok + 32 * h + e < limit) top = fmaxf(top, x);
+                }
+              }
+              if (unset && top > -INFINITY) {
+                ref = ceilf(top - kLift);
+                unset = false;
+              }
+              if (!__any_sync(0xffffffffu, unset)) break;
+            }
+          }
           // The plain case, to which most tiles belong: all rows see all tokens and the reference need not
           // rise, as is known once P is there, in registers.
           bool plain = !__any_sync(0xffffffffu, unset) && tok + kTok <= least;
@@ -661,32 +689,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------- keys and values
     regs_decrease<kConvRegs>();
     const int ct = threadIdx.x - 32 * kConvWarp;
-    // Eight neighbouring threads have four pieces of two neighbouring tokens: their chunks of FP16 meet
-    // all banks.
-    const int piece = kDim == 128 ? (ct & 3) | (ct >> 1 & 4) : ct & 3;
-    const int row0 = kDim == 128 ? (ct >> 2 & 1) | (ct >> 4 << 1) : ct >> 2;
+    // Eight neighbouring threads have the eight (four) pieces of two neighbouring tokens such that both the
+    // codes and the chunks of FP16 that they become meet all banks.
+    const int piece = kDim == 128 ? ct & 7 : ct & 3;
+    const int row0 = kDim == 128 ? ct >> 3 ^ (piece >> 2) : ct >> 2;
     constexpr int kRowsAtOnce = 128 / (kDim / 16);  // tokens that the 128 threads cover at once: a multiple of 8
     constexpr int kLoads = kTok / kRowsAtOnce;
-    const int in_block = (row0 & 15) * kDim + 16 * piece;
     const uint32_t to0 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece) - smem);
     const uint32_t to1 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece + 1) - smem);
-    uint8_t* codes_k = smem + S::kCodes + 16 * ct;
+    uint8_t* codes_k = smem + S::kCodes + row0 * kDim + 16 * piece;
     uint8_t* codes_v = codes_k + kTok * kDim;
-    // A tile's codes into this thread's places in shared memory: no other thread has to be waited for, and
-    // what is on its way takes no registers.
-    auto fetch = [&](const uint8_t* cache, uint8_t* codes, const Tab& t) {
-#pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        const int row = t.row[kDim == 128 ? l : 2 * l + (ct >> 6)];
-        cp_async_16(smem_addr(codes + l * 2048), cache + ((long long)max(row, 0) * kDim + in_block), row < 0 ? 0u : 16u);
-      }
-    };
-    auto convert = [&](uint8_t* tile, const uint8_t* codes, uint64_t* full) {
+    auto convert = [&](uint8_t* tile, const uint8_t* codes, uint64_t* full, uint64_t* empty) {
 #pragma unroll
       for (int l0 = 0; l0 < kLoads; l0 += 4) {
         uint4 v[4];
 #pragma unroll
-        for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const uint4*>(codes + (l0 + l) * 2048);
+        for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const uint4*>(codes + (l0 + l) * kRowsAtOnce * kDim);
 #pragma unroll
         for (int l = 0; l < 4; ++l) {
           const uint32_t w[4] = {v[l].x, v[l].y, v[l].z, v[l].w};
@@ -703,35 +721,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full);
+      if (lane == 0) {
+        mbar_arrive(full);
+        mbar_arrive(empty);
+      }
     };
-    auto tab_of = [&](uint32_t n) -> const Tab& { return tabs[n % kTabs]; };
-    bool ok = warp_wait(&bar.tab_full[0], 0);
-    if (ok && tab_of(0).slot >= 0) {
-      fetch(a.kc, codes_k, tab_of(0));
-      cp_async_commit();
-      fetch(a.vc, codes_v, tab_of(0));
-      cp_async_commit();
-    }
-    for (uint32_t it = 0; ok && tab_of(it).slot >= 0; ++it) {
+    for (uint32_t it = 0;; ++it) {
       const int st = it % kStages;
       const uint32_t ph = (it / kStages) & 1;
-      const Tab& tab = tab_of(it);
-      const Tab& next = tab_of(it + 1);
-      uint64_t* next_full = &bar.tab_full[(it + 1) % kTabs];
-      const uint32_t next_ph = ((it + 1) / kTabs) & 1;
-      if (!(ok = warp_wait(&bar.k_empty[st], ph ^ 1))) break;
-      cp_async_wait<1>();
-      convert(smem + S::kK + st * S::kTileBytes, codes_k, &bar.k_full[st]);
-      // The next tile's keys, if it is known yet.  (It may be that of a unit which has to wait for the end of this
-      // one's: behind units without tiles.)
-      const bool early = __all_sync(0xffffffffu, mbar_test(next_full, next_ph));
-      if (early && next.slot >= 0) fetch(a.kc, codes_k, next);
-      cp_async_commit();
-      if (!(ok = warp_wait(&bar.v_empty[st], ph ^ 1))) break;
+      const Tab& tab = tabs[it % kTabs];
+      if (!warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1) || tab.slot < 0) break;
+      if (!warp_wait(&bar.k_empty[st], ph ^ 1)) break;
+      if (!warp_wait(&bar.codes_full[0], it & 1)) break;
+      if (!tab.all) {  // tokens without a block: nothing was copied to their places
+#pragma unroll 1
+        for (int l = 0; l < kLoads; ++l)
+          if (tab.row[(row0 + kRowsAtOnce * l) / 16] < 0)
+            *reinterpret_cast<uint4*>(codes_k + l * kRowsAtOnce * kDim) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      convert(smem + S::kK + st * S::kTileBytes, codes_k, &bar.k_full[st], &bar.codes_empty[0]);
+      if (!warp_wait(&bar.v_empty[st], ph ^ 1)) break;
       // the values of two tiles ago have been used, and so have their scales
       if (lane == 0 && it >= 2) mbar_arrive(&bar.tab_empty[(it - 2) % kTabs]);
-      cp_async_wait<1>();
+      if (!warp_wait(&bar.codes_full[1], it & 1)) break;
       const bool mixed = tab.whole < kTok;
       if (__any_sync(0xffffffffu, mixed || tab.g[lane % kGroups].mode != 0u)) {
         // Some value scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times
@@ -742,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int l = 0; l < kLoads; ++l) {
           const int r = row0 + kRowsAtOnce * l;
           const uint32_t mode = tab.g[r / 16].mode;
-          uint4* at = reinterpret_cast<uint4*>(codes_v + l * 2048);
+          uint4* at = reinterpret_cast<uint4*>(codes_v + l * kRowsAtOnce * kDim);
           const uint4 v = *at;
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -760,19 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (bad) ring(tab.slot)->bad = 1;
       }
-      convert(smem + S::kV + st * S::kTileBytes, codes_v, &bar.v_full[st]);
+      convert(smem + S::kV + st * S::kTileBytes, codes_v, &bar.v_full[st], &bar.codes_empty[1]);
       if (tab.last && lane == 0) mbar_arrive(&bar.ring_empty[tab.slot]);
-      if (!early && !(ok = warp_wait(next_full, next_ph))) break;
-      if (next.slot >= 0) {
-        if (!early) {
-          fetch(a.kc, codes_k, next);
-          cp_async_commit();
-        }
-        fetch(a.vc, codes_v, next);
-      }
-      cp_async_commit();
     }
-    cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- the products
     // The whole warp runs this, in step, so that descriptors stay in uniform registers; one lane issues.
@@ -935,6 +937,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit end = {};
       end.kind = kEnd;
       if (ok) give(end);
+    } else if (warp == kLoadWarp) {
+      // ------------------------------------------- codes into shared memory, 16 tokens a copy
+      constexpr uint32_t kBytes = 16 * kDim;
+      bool ok = true;
+      uint32_t asked[2] = {0, 0};
+      for (uint32_t it = 0; ok; ++it) {
+        const Tab& tab = tabs[it % kTabs];
+        if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1)) || tab.slot < 0) break;
+        const int row = lane < kGroups ? tab.row[lane] : -1;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (!(ok = warp_wait(&bar.codes_empty[v], (it & 1) ^ 1))) break;
+          ++asked[v];
+          if (lane == 0) mbar_arrive_expect_tx(&bar.codes_full[v], n * kBytes);
+          __syncwarp();
+          if (row >= 0)
+            bulk_load(smem + S::kCodes + v * kTok * kDim + lane * kBytes, (v ? a.vc : a.kc) + (long long)row * kDim,
+                      kBytes, &bar.codes_full[v]);
+        }
+      }
+      // what is on its way lands before the CTA's end
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        if (asked[v] > 0) mbar_drain(&bar.codes_full[v], (asked[v] - 1) & 1);
     } else if (warp == kScoutWarp) {
       // ------------------------------------------- where tiles lie, and their scales
       // Up to four tiles at a time, eight lanes each: table entries, then scales, are the latencies that nothing
@@ -1003,7 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (its error is one of the weight of these tokens: 2^-15 at most)
         x.add = blk >= 0 ? __log2f(av) : -INFINITY;
         x.inv = blk >= 0 ? __frcp_rn(av) : 0.f;
-        x.mode = blk < 0 ? 0u : !fin ? kNotFinite : !used ? kZero : vs < 0.f ? kNegate : 0u;
+        x.mode = blk < 0 ? kZero : !fin ? kNotFinite : !used ? kZero : vs < 0.f ? kNegate : 0u;
+        const uint32_t lie = __ballot_sync(0xffffffffu, row >= 0);
         const int total = n + (ended ? 1 : 0);  // and the end
         for (int q = 0; q < total && ok; ++q, ++it) {
           Tab& t = tabs[it % kTabs];
@@ -1015,6 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             t.row[g] = row;
             if (g == 0) {
               t.slot = mine;
+              t.all = (lie >> (8 * q) & 0xffu) == 0xffu;
               t.last = mine_j + 1 == u->j1;
               t.there = u->vis - mine_j * kTok;
               t.whole = u->first - mine_j * kTok;

@@ -125,14 +125,6 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Closes this thread's pending cp.async copies into one group; waits until at most N groups are
-// still on their way.
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Arrive on `bar` when every cp.async this thread issued so far has landed
 // (the arrival is one of the barrier's expected ones).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint64_t* bar) {
@@ -150,6 +142,16 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // --------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// Copy of `bytes` bytes (a multiple of 16, both addresses 16-byte aligned) global -> shared,
+// completion counted on `bar` in bytes.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
 }
 
 // 2-D tiled load global -> shared, completion counted on `bar` in bytes.
