@@ -52,7 +52,7 @@ constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of on
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kScoutWarp = 14, kLoadWarp = 15;
 // 512 threads are launched with 128 registers each: 512 for the four warps of a sub-partition
-constexpr uint32_t kSoftRegs = 176, kConvRegs = 80, kLowRegs = 80;
+constexpr uint32_t kSoftRegs = 184, kConvRegs = 64, kLowRegs = 80;
 static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
 constexpr int kStages = 2;  // of keys and of values
 constexpr int kTabs = 8;    // tiles of which it is known where they lie
@@ -267,34 +267,40 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
   return tile + (c / 8) * Smem<kDim>::kSubBytes + row * 128 + (((c % 8) ^ (row & 7)) << 4);
 }
 
-// A row of Q into shared memory as FP16 times a power of two that brings its largest element
-// into [2^10, 2^11); returns the reciprocal of that power.
+// A warp's 32 rows of Q into shared memory as FP16 times a power of two for each that brings its largest
+// element into [2^10, 2^11); returns the reciprocal of that power for the lane's row, the `row`-th of the
+// tile, whose elements begin at `at` (< 0: no such row).  (Code that runs once a unit is kept short too: it
+// comes from beyond the instruction cache each time.)
 template <int kDim>
-__device__ __forceinline__ float stage_query(uint8_t* tile, int row, const __nv_bfloat16* q) {
-  Raw8<__nv_bfloat16> raw[kDim / 8];
-  float top = 0.f;
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) {
-    zero8(raw[c]);
-    if (q) raw[c] = load8(q + 8 * c);
+__device__ __forceinline__ float stage_queries(uint8_t* tile, int row, int lane, const __nv_bfloat16* Q, long long at) {
+  constexpr int kChunks = kDim / 8, kRowsAtOnce = 32 / kChunks;  // whole rows are read by neighbouring lanes
+#pragma unroll 8
+  for (int y = 0; y < 32; y += kRowsAtOnce) {
+    const int from = y + lane / kChunks;
+    const long long q = __shfl_sync(0xffffffffu, at, from);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (q >= 0) v = *reinterpret_cast<const uint4*>(Q + q + 8 * (lane % kChunks));
+    *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row - lane + from, lane % kChunks)) = v;
   }
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) {
-    float f[8];
-    unpack8(raw[c], f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+  __syncwarp();
+  uint32_t top2 = 0u;  // of the even elements and of the odd ones: magnitudes of BF16 order as whole numbers do
+#pragma unroll 4
+  for (int c = 0; c < kChunks; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<kDim>(tile, row, c));
+    top2 = __vmaxu2(__vmaxu2(__vmaxu2(top2, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
+                    v.w & 0x7fff7fffu);
   }
+  const uint32_t top = max(top2 >> 16, top2 & 0xffffu);
   // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
-  const int exp = max(int(__float_as_uint(top) >> 23), 10);
+  const int exp = max(int(top >> 7), 10);
   const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) {
+#pragma unroll 2
+  for (int c = 0; c < kChunks; ++c) {
+    uint4* p = reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c));
     float f[8];
-    unpack8(raw[c], f);
-    *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c)) =
-        make_uint4(f16x2_bits(f[0] * up, f[1] * up), f16x2_bits(f[2] * up, f[3] * up),
-                   f16x2_bits(f[4] * up, f[5] * up), f16x2_bits(f[6] * up, f[7] * up));
+    unpack8(Raw8<__nv_bfloat16>{*p}, f);
+    *p = make_uint4(f16x2_bits(f[0] * up, f[1] * up), f16x2_bits(f[2] * up, f[3] * up),
+                    f16x2_bits(f[4] * up, f[5] * up), f16x2_bits(f[6] * up, f[7] * up));
   }
   return __uint_as_float(uint32_t(exp - 10) << 23);
 }
@@ -436,11 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int head = u->head * a.group + seq_row % a.group;
       const int limit = row_ok ? row_limit(a, u->len, u->n, seq_row) : 0x7fffffff;
       const int least = __shfl_sync(0xffffffffu, limit, 0);  // rows see more and more
+      const int most_seen = u->vis;
       float ref = 0.f, sum = 0.f, vref = 1.f;  // sum: of p over vref's share of |v_scale|
       bool unset = true;
       if (j1 > j0) {
-        const float down = stage_query<kDim>(
-            q_tile, row, row_ok ? a.Q + (long long)token * a.ld_q + (long long)head * kDim : nullptr);
+        const float down = stage_queries<kDim>(
+            q_tile, row, lane, a.Q, row_ok ? (long long)token * a.ld_q + (long long)head * kDim : -1LL);
         const float q_mul = down * (a.scale * 1.44269504088896341f);
         fence_proxy_async_smem();
         __syncwarp();
@@ -455,13 +462,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const int tok = j * kTok;
           if (j == j0) vref = tabs[it % kTabs].v0;
-          if (__any_sync(0xffffffffu, unset)) {  // a first reference, from the first 32 tokens that are there
+          if (__any_sync(0xffffffffu, unset)) {  // a first reference, from the first tile that is there
+            float top = -INFINITY;
 #pragma unroll 1
             for (int h = 0; h < kTok / 32; ++h) {
               uint32_t c[32];
               tmem_ld_32x32b_x32(s_at + 32 * h, c);
               tmem_ld_wait_tied(c);
-              float top = -INFINITY;
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
                 const float mul = q_mul * tab[2 * h + g].k, add = tab[2 * h + g].add;
@@ -471,17 +478,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (tok + 32 * h + e < limit) top = fmaxf(top, x);
                 }
               }
-              if (unset && top > -INFINITY) {
-                ref = ceilf(top - kLift);
-                unset = false;
-              }
-              if (!__any_sync(0xffffffffu, unset)) break;
+            }
+            if (unset && top > -INFINITY) {
+              ref = ceilf(top - kLift);
+              unset = false;
             }
           }
-          // The plain case, to which most tiles belong: all rows see all tokens and the reference need not
-          // rise, as is known once P is there, in registers.
+          // What has been summed so far shrinks as the reference rises.
+          auto rescale = [&](float shrink) {
+            sum *= shrink;
+            if (j == j0 || !__any_sync(0xffffffffu, shrink != 1.f)) return true;
+            if (!warp_wait(&bar.o_full[i], (mine - 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < kDim; d += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(o_at + d, o);
+              tmem_ld_wait_tied16(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+              tmem_st_32x32b_x16(o_at + d, o);
+            }
+            return true;
+          };
+          // The plain case, to which most tiles belong: all rows see all tokens.  That the reference need not rise
+          // is known once P is there, in registers; if it has to, P is formed again.
           bool plain = !__any_sync(0xffffffffu, unset) && tok + kTok <= least;
-          if (plain) {
+#pragma unroll 1
+          while (plain) {
             uint32_t c[3][32], p[4][16];
             float part = 0.f, most = 0.f;
             auto take = [&](const uint32_t (&from)[32], int h) {  // 32 tokens
@@ -516,18 +540,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             reg_tie32(c[0]);
             take(c[2], 2);
             take(c[0], 3);
-            plain = !__any_sync(0xffffffffu, most > kMostP);
-            if (plain) {
+            if (!__any_sync(0xffffffffu, most > kMostP)) {
               sum += part;
 #pragma unroll
               for (int h = 0; h < 4; ++h) tmem_st_32x32b_x16(s_at + 16 * h, p[h]);
+              break;
+            }
+            // (`most` is up to 16 times the largest P.  What it cannot tell goes the other way: infinity, and
+            // references so large that they hardly rise.)
+            float up = 0.f;
+            if (most > kMostP) up = float(int(__float_as_uint(most) >> 23) - 127) - kLift;
+            const float to = ref + up;
+            plain = !__any_sync(0xffffffffu, most == INFINITY || to - ref != up);
+            if (plain) {
+              ref = to;
+              if (!(ok = rescale(exp2_fast(-up)))) break;
             }
           }
+          if (!ok) break;
 #pragma unroll 1
           for (int h = plain ? kTok / 32 : 0; h < kTok / 32; ++h) {  // 32 tokens at a time
             const int sees = limit - tok - 32 * h;
             uint32_t p[16];
             float sums[2];
+            if (tok + 32 * h >= most_seen) {  // no row sees any of these
+#pragma unroll
+              for (int e = 0; e < 16; ++e) p[e] = 0u;
+              tmem_st_32x32b_x16(s_at + 16 * h, p);
+              continue;
+            }
             // Once as if the reference need not rise; if it has to, again with the new one.
 #pragma unroll 1
             for (bool again = false;; again = true) {
@@ -586,38 +627,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ref = ceilf(top - kLift);
                 unset = false;
               }
-              sum *= shrink;
-              if (__any_sync(0xffffffffu, shrink != 1.f)) {
-                if (h > 0) {  // P of the tile's tokens before these
-                  const __half2 f = __float2half2_rn(shrink);
-                  tmem_st_wait();
+              if (h > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {  // P of the tile's tokens before these
+                const __half2 f = __float2half2_rn(shrink);
+                tmem_st_wait();
 #pragma unroll 1
-                  for (int d = 0; d < 16 * h; d += 16) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(s_at + d, o);
-                    tmem_ld_wait_tied16(o);
+                for (int d = 0; d < 16 * h; d += 16) {
+                  uint32_t o[16];
+                  tmem_ld_32x32b_x16(s_at + d, o);
+                  tmem_ld_wait_tied16(o);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f);
-                      o[e] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
-                    tmem_st_32x32b_x16(s_at + d, o);
+                  for (int e = 0; e < 16; ++e) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f);
+                    o[e] = *reinterpret_cast<const uint32_t*>(&v);
                   }
-                }
-                if (j > j0) {
-                  if (!(ok = warp_wait(&bar.o_full[i], (mine - 1) & 1))) break;
-                  tc_fence_after();
-#pragma unroll 1
-                  for (int d = 0; d < kDim; d += 16) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(o_at + d, o);
-                    tmem_ld_wait_tied16(o);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
-                    tmem_st_32x32b_x16(o_at + d, o);
-                  }
+                  tmem_st_32x32b_x16(s_at + d, o);
                 }
               }
+              if (!(ok = rescale(shrink))) break;
             }
             if (!ok) break;
 #pragma unroll
@@ -634,53 +660,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       // ---- the rows' end: whole units go to O, parts to the workspace
-      uint32_t lost[kDim / 32] = {};
-      if (u->bad) {
-        const int from = u->first / kTok * kTok;
+      if (u->bad) {  // such rows' O becomes NaN where they see a value that is not finite
+        uint32_t lost[kDim / 32] = {};
         if (row_ok)
-          find_not_finite<kDim, kE5M2>(a, u->b, u->head, max(from, j0 * kTok), min(limit, j1 * kTok), status, lost);
+          find_not_finite<kDim, kE5M2>(a, u->b, u->head, max(u->first / kTok * kTok, j0 * kTok), min(limit, j1 * kTok),
+                                       status, lost);
+        __syncwarp();
+#pragma unroll 1
+        for (int d = 0; d < kDim; d += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(o_at + d, o);
+          tmem_ld_wait_tied(o);
+          const uint32_t m = lost[d / 32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (m >> e & 1u) o[e] = 0x7fc00000u;
+          tmem_st_32x32b_x32(o_at + d, o);
+        }
+        tmem_st_wait();
       }
       const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
-      float* part = parts + (size_t(blockIdx.x) * 2 + (kind == kFirst)) * (kUnitRows * (kDim + 4));
+      const long long out_at = ((long long)token * a.heads * a.group + head) * kDim;
+      // parts: [kDim / 4][rows][4], then [rows][4], so that neighbouring lanes write neighbouring places
+      float4* part = reinterpret_cast<float4*>(parts) +
+                     (size_t(blockIdx.x) * 2 + (kind == kFirst)) * (kUnitRows * (kDim / 4 + 1)) + r;
 #pragma unroll 1
       for (int d = 0; d < kDim; d += 32) {
-        uint32_t o[32];
-        const uint32_t lost_d = lost[d / 32];
+        uint32_t o[32] = {};
         if (j1 > j0) {
           tmem_ld_32x32b_x32(o_at + d, o);
           tmem_ld_wait_tied(o);
         }
-        if (row_ok && kind == kWhole) {
-          __nv_bfloat16* out = a.O + ((long long)token * a.heads * a.group + head) * kDim + d;
+        if (kind == kWhole) {  // by way of the warp's rows of Q, which have been used: rows leave whole
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             float v[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              v[y] = f == 0.f ? 0.f : __uint_as_float(o[e + y]) * f * vref;
-              if (lost_d >> (e + y) & 1u) v[y] = NAN;
-            }
+            for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(o[e + y]) * f * vref;
             Raw8<__nv_bfloat16> w;
             pack8(v, w);
-            store8(out + e, w);
+            *reinterpret_cast<uint4*>(chunk_at<kDim>(q_tile, row, (d + e) / 8)) = w.a;
           }
         } else if (row_ok) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 v = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
-                                   __uint_as_float(o[e + 3]));
-            if (lost_d >> e & 1u) v.x = NAN;
-            if (lost_d >> e & 2u) v.y = NAN;
-            if (lost_d >> e & 4u) v.z = NAN;
-            if (lost_d >> e & 8u) v.w = NAN;
-            *reinterpret_cast<float4*>(part + size_t(r) * kDim + d + e) = v;
-          }
+          for (int e = 0; e < 32; e += 4)
+            part[size_t(d + e) / 4 * kUnitRows] =
+                make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                            __uint_as_float(o[e + 3]));
         }
         __syncwarp();
       }
-      if (kind != kWhole && row_ok)
-        *reinterpret_cast<float4*>(part + size_t(kUnitRows) * kDim + 4 * r) =
-            make_float4(unset ? -INFINITY : ref, sum, vref, 0.f);
+      if (kind == kWhole) {
+        constexpr int kChunks = kDim / 8, kRowsAtOnce = 32 / kChunks;
+#pragma unroll 4
+        for (int y = 0; y < 32; y += kRowsAtOnce) {
+          const int from = y + lane / kChunks;  // row of the warp
+          const long long to = __shfl_sync(0xffffffffu, out_at, from);
+          const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<kDim>(q_tile, row - lane + from, lane % kChunks));
+          if (kTileRows * i + row - lane + from < rows) *reinterpret_cast<uint4*>(a.O + to + 8 * (lane % kChunks)) = v;
+        }
+        __syncwarp();
+      } else if (row_ok) {
+        part[size_t(kUnitRows) * (kDim / 4)] = make_float4(unset ? -INFINITY : ref, sum, vref, 0.f);
+      }
       tc_fence_before();  // O has been read before its next product, which waits for P
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
@@ -927,6 +969,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               split = {last - int(blockIdx.x) + 1, head, s.t0, unit.row0, unit.rows};
             }
             ok = give(unit);
+            const int t0 = unit.t0 + unit.row0 / a.group, t1 = unit.t0 + (unit.row0 + unit.rows - 1) / a.group;
+            for (int t = t0 + lane; t <= t1; t += 32)  // its queries
+              prefetch_l2(a.Q + (long long)t * a.ld_q + (long long)head * a.group * kDim, a.group * kDim * 2);
           }
           at += x1 - off;
           off = 0;
@@ -1064,47 +1109,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of the unit that CTA blockIdx.x of the kernel above began: a warp for each row, in
-// the order of the CTAs.
-constexpr int kJoinWarps = 8, kJoinY = kUnitRows / kJoinWarps;
+// Joins the parts of the unit that CTA blockIdx.x of the kernel above began, in the order of the CTAs: a
+// thread for each row, 16 dimensions a CTA.
+constexpr int kJoinDims = 16;
 template <int kDim>
-__global__ void __launch_bounds__(32 * kJoinWarps) kv_chunk_join_kernel(const __grid_constant__ KvChunkArgs a,
-                                                                        const float* __restrict__ parts,
-                                                                        const Split* __restrict__ splits) {
+__global__ void __launch_bounds__(kUnitRows) kv_chunk_join_kernel(const __grid_constant__ KvChunkArgs a,
+                                                                  const float4* __restrict__ parts,
+                                                                  const Split* __restrict__ splits) {
   griddep_launch_dependents();
   griddep_wait();
   const Split s = splits[blockIdx.x];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int r = blockIdx.y * kJoinWarps + warp;
+  const int r = threadIdx.x, d = blockIdx.y * kJoinDims;
   if (s.parts == 0 || r >= s.rows) return;
-  constexpr size_t kSlot = size_t(kUnitRows) * (kDim + 4);
-  const float* first = parts + (size_t(blockIdx.x) * 2 + 1) * kSlot;
-  auto part = [&](int p) { return p == 0 ? first : parts + size_t(blockIdx.x + p) * 2 * kSlot; };
-  auto stat = [&](int p) { return *reinterpret_cast<const float4*>(part(p) + size_t(kUnitRows) * kDim + 4 * r); };
+  constexpr size_t kSlot = size_t(kUnitRows) * (kDim / 4 + 1);
+  auto part = [&](int p) { return parts + (size_t(blockIdx.x + p) * 2 + (p == 0)) * kSlot + r; };
+  auto stat = [&](int p) { return part(p)[size_t(kUnitRows) * (kDim / 4)]; };
   float top = -INFINITY;
+#pragma unroll 4
   for (int p = 0; p < s.parts; ++p) top = max_nan(top, stat(p).x);
   const float vref = stat(0).z;
-  constexpr int kPer = kDim / 32;
-  float o[kPer] = {}, sum = 0.f;
-#pragma unroll 4
+  float4 o[kJoinDims / 4] = {};
+  float sum = 0.f;
+#pragma unroll 2
   for (int p = 0; p < s.parts; ++p) {
     const float4 t = stat(p);
     const float f = t.x == -INFINITY ? 0.f : exp2_fast(t.x - top);
     sum = fmaf(t.y, f * __fdiv_rn(vref, t.z), sum);
-    const float* v = part(p) + size_t(r) * kDim + kPer * lane;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = fmaf(v[i], f, o[i]);
+    for (int i = 0; i < kJoinDims / 4; ++i) {
+      const float4 v = part(p)[size_t(d / 4 + i) * kUnitRows];
+      o[i].x = fmaf(v.x, f, o[i].x);
+      o[i].y = fmaf(v.y, f, o[i].y);
+      o[i].z = fmaf(v.z, f, o[i].z);
+      o[i].w = fmaf(v.w, f, o[i].w);
+    }
   }
   const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
   const int row = s.row0 + r;
-  __nv_bfloat16* out = a.O + (((long long)s.t0 + row / a.group) * a.heads * a.group + s.head * a.group + row % a.group) * kDim +
-                       kPer * lane;
+  __nv_bfloat16* out =
+      a.O + (((long long)s.t0 + row / a.group) * a.heads * a.group + s.head * a.group + row % a.group) * kDim + d;
+  auto scaled = [&](float v) { return v * f * vref; };
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = f == 0.f ? 0.f : o[i] * f * vref;
-  if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2_bits(o[0], o[1]), bf16x2_bits(o[2], o[3]));
-  else
-    *reinterpret_cast<uint32_t*>(out) = bf16x2_bits(o[0], o[1]);
+  for (int i = 0; i < kJoinDims / 4; i += 2)
+    *reinterpret_cast<uint4*>(out + 4 * i) =
+        make_uint4(bf16x2_bits(scaled(o[i].x), scaled(o[i].y)), bf16x2_bits(scaled(o[i].z), scaled(o[i].w)),
+                   bf16x2_bits(scaled(o[i + 1].x), scaled(o[i + 1].y)), bf16x2_bits(scaled(o[i + 1].z), scaled(o[i + 1].w)));
 }
 
 template <int kDim, bool kE5M2>
@@ -1120,7 +1169,8 @@ cudaError_t run(const LaunchCtx& c, const KvChunkArgs& a, void* ws) {
   Split* splits = static_cast<Split*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + size_t(c.num_sms) * 64);
   if (cudaError_t e = launch_dependent(c, fn, grid, kThreads, Smem<kDim>::kBytes, a, parts, splits, c.status)) return e;
-  return launch_dependent(c, kv_chunk_join_kernel<kDim>, dim3(grid, kJoinY), 32 * kJoinWarps, 0, a, parts, splits);
+  return launch_dependent(c, kv_chunk_join_kernel<kDim>, dim3(grid, kDim / kJoinDims), kUnitRows, 0, a,
+                          reinterpret_cast<const float4*>(parts), splits);
 }
 
 }  // namespace
