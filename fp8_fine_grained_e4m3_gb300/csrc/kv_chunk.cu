@@ -739,83 +739,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kLoads = kTok / kRowsAtOnce;
     const uint32_t to0 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece) - smem);
     const uint32_t to1 = uint32_t(chunk_at<kDim>(smem, row0, 2 * piece + 1) - smem);
-    uint8_t* codes_k = smem + S::kCodes + row0 * kDim + 16 * piece;
-    uint8_t* codes_v = codes_k + kTok * kDim;
-    auto convert = [&](uint8_t* tile, const uint8_t* codes, uint64_t* full, uint64_t* empty) {
-#pragma unroll
-      for (int l0 = 0; l0 < kLoads; l0 += 4) {
-        uint4 v[4];
-#pragma unroll
-        for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const uint4*>(codes + (l0 + l) * kRowsAtOnce * kDim);
-#pragma unroll
-        for (int l = 0; l < 4; ++l) {
-          const uint32_t w[4] = {v[l].x, v[l].y, v[l].z, v[l].w};
-          uint32_t x[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[2 * e] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e]));
-            x[2 * e + 1] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16));
-          }
-          const int at = (l0 + l) * kRowsAtOnce * 128;
-          *reinterpret_cast<uint4*>(tile + to0 + at) = make_uint4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint4*>(tile + to1 + at) = make_uint4(x[4], x[5], x[6], x[7]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(full);
-        mbar_arrive(empty);
-      }
-    };
-    for (uint32_t it = 0;; ++it) {
+    bool ok = true;
+    for (uint32_t it = 0; ok; ++it) {
       const int st = it % kStages;
       const uint32_t ph = (it / kStages) & 1;
       const Tab& tab = tabs[it % kTabs];
       if (!warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1) || tab.slot < 0) break;
-      if (!warp_wait(&bar.k_empty[st], ph ^ 1)) break;
-      if (!warp_wait(&bar.codes_full[0], it & 1)) break;
-      if (!tab.all) {  // tokens without a block: nothing was copied to their places
 #pragma unroll 1
-        for (int l = 0; l < kLoads; ++l)
-          if (tab.row[(row0 + kRowsAtOnce * l) / 16] < 0)
-            *reinterpret_cast<uint4*>(codes_k + l * kRowsAtOnce * kDim) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      convert(smem + S::kK + st * S::kTileBytes, codes_k, &bar.k_full[st], &bar.codes_empty[0]);
-      if (!warp_wait(&bar.v_empty[st], ph ^ 1)) break;
-      // the values of two tiles ago have been used, and so have their scales
-      if (lane == 0 && it >= 2) mbar_arrive(&bar.tab_empty[(it - 2) % kTabs]);
-      if (!warp_wait(&bar.codes_full[1], it & 1)) break;
-      const bool mixed = tab.whole < kTok;
-      if (__any_sync(0xffffffffu, mixed || tab.g[lane % kGroups].mode != 0u)) {
-        // Some value scale is 0, negative or not finite, or some row does not see the whole tile.  There 0 times
-        // what is not finite would reach rows that do not see it: such values become 0, and the rows that
-        // do see them are marked when the unit ends.
-        bool bad = false;
+      for (int v = 0; v < 2; ++v) {  // keys, values
+        uint8_t* codes = smem + S::kCodes + v * kTok * kDim + row0 * kDim + 16 * piece;
+        if (!(ok = warp_wait(v ? &bar.v_empty[st] : &bar.k_empty[st], ph ^ 1))) break;
+        // the values of two tiles ago have been used, and so have their scales
+        if (v == 1 && lane == 0 && it >= 2) mbar_arrive(&bar.tab_empty[(it - 2) % kTabs]);
+        if (!(ok = warp_wait(&bar.codes_full[v], it & 1))) break;
+        const bool mixed = tab.whole < kTok;
+        if (!tab.all || (v == 1 && __any_sync(0xffffffffu, mixed || tab.g[lane % kGroups].mode != 0u))) {
+          // Tokens without a block: nothing was copied to their places.  Or some value scale is 0, negative or not
+          // finite, or some row does not see the whole tile.  There 0 times what is not finite would
+          // reach rows that do not see it: such values become 0, and the rows that do see them are
+          // marked when the unit ends.
+          bool bad = false;
 #pragma unroll 1
-        for (int l = 0; l < kLoads; ++l) {
-          const int r = row0 + kRowsAtOnce * l;
-          const uint32_t mode = tab.g[r / 16].mode;
-          uint4* at = reinterpret_cast<uint4*>(codes_v + l * kRowsAtOnce * kDim);
-          const uint4 v = *at;
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int l = 0; l < kLoads; ++l) {
+            const int r = row0 + kRowsAtOnce * l;
+            const uint32_t mode = v == 1 ? tab.g[r / 16].mode : 0u;
+            uint4* at = reinterpret_cast<uint4*>(codes + l * kRowsAtOnce * kDim);
+            const uint4 x = *at;
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t lost = mode & kNotFinite ? 0xffffffffu : mixed ? not_finite4<kE5M2>(w[e]) : 0u;
-            if (r >= tab.there || (mode & kZero)) {
-              w[e] = lost = 0u;
-            } else if (mode & kNegate) {
-              w[e] ^= 0x80808080u;
+            for (int e = 0; e < 4; ++e) {
+              uint32_t lost = mode & kNotFinite ? 0xffffffffu : mixed && v == 1 ? not_finite4<kE5M2>(w[e]) : 0u;
+              if (tab.row[r / 16] < 0 || r >= tab.there || (mode & kZero)) {
+                w[e] = lost = 0u;
+              } else if (mode & kNegate) {
+                w[e] ^= 0x80808080u;
+              }
+              bad |= mixed && lost != 0u;
+              w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
             }
-            bad |= mixed && lost != 0u;
-            w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *at = make_uint4(w[0], w[1], w[2], w[3]);
+          if (bad) ring(tab.slot)->bad = 1;
         }
-        if (bad) ring(tab.slot)->bad = 1;
+        uint8_t* tile = smem + (v ? S::kV : S::kK) + st * S::kTileBytes;
+#pragma unroll
+        for (int l0 = 0; l0 < kLoads; l0 += 4) {
+          uint4 x[4];
+#pragma unroll
+          for (int l = 0; l < 4; ++l) x[l] = *reinterpret_cast<const uint4*>(codes + (l0 + l) * kRowsAtOnce * kDim);
+#pragma unroll
+          for (int l = 0; l < 4; ++l) {
+            const uint32_t w[4] = {x[l].x, x[l].y, x[l].z, x[l].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[2 * e] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e]));
+              y[2 * e + 1] = f8x2_to_f16x2<kE5M2>(uint16_t(w[e] >> 16));
+            }
+            const int at = (l0 + l) * kRowsAtOnce * 128;
+            *reinterpret_cast<uint4*>(tile + to0 + at) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(tile + to1 + at) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(v ? &bar.v_full[st] : &bar.k_full[st]);
+          mbar_arrive(&bar.codes_empty[v]);
+        }
       }
-      convert(smem + S::kV + st * S::kTileBytes, codes_v, &bar.v_full[st], &bar.codes_empty[1]);
-      if (tab.last && lane == 0) mbar_arrive(&bar.ring_empty[tab.slot]);
+      if (ok && tab.last && lane == 0) mbar_arrive(&bar.ring_empty[tab.slot]);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------- the products
