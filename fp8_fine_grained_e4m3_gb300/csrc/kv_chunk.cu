@@ -312,6 +312,14 @@ __device__ __forceinline__ uint32_t not_finite4(uint32_t w) {
   return __vcmpeq4(w & kBad, kBad);
 }
 
+// The same value, of which the compiler knows nothing any more: it then makes no second copy of a loop's body
+// for the first pass.
+__device__ __forceinline__ bool opaque(bool b) {
+  int x = b;
+  asm volatile("" : "+r"(x));
+  return x != 0;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -329,6 +337,7 @@ __device__ __forceinline__ int block_of(const KvChunkArgs& a, int b, int tok, in
 template <int kDim, bool kE5M2>
 __device__ __noinline__ void find_not_finite(const KvChunkArgs& a, int b, int head, int from, int to,
                                              int* status, uint32_t (&mask)[kDim / 32]) {
+#pragma unroll 1
   for (int tok = from; tok < to; ++tok) {
     const int blk = block_of(a, b, tok, to, status);
     if (blk < 0) continue;
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // is known once P is there, in registers; if it has to, P is formed again.
           bool plain = !__any_sync(0xffffffffu, unset) && tok + kTok <= least;
 #pragma unroll 1
-          while (plain) {
+          while (opaque(plain)) {
             uint32_t c[3][32], p[4][16];
             float part = 0.f, most = 0.f;
             auto take = [&](const uint32_t (&from)[32], int h) {  // 32 tokens
@@ -571,48 +580,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Once as if the reference need not rise; if it has to, again with the new one.
 #pragma unroll 1
-            for (bool again = false;; again = true) {
+            for (bool again = opaque(false);; again = opaque(true)) {
               uint32_t c[32];
               tmem_ld_32x32b_x32(s_at + 32 * h, c);
               tmem_ld_wait_tied(c);
-              float2 x[16];  // scores in powers of two, with the value scale's, less the reference
+              float x[32];  // scores in powers of two, with the value scale's, less the reference
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const float mul = q_mul * tab[2 * h + g].k, add = tab[2 * h + g].add - ref;
-#pragma unroll
-                for (int e = 8 * g; e < 8 * g + 8; ++e)
-                  x[e] = __ffma2_rn(make_float2(__uint_as_float(c[2 * e]), __uint_as_float(c[2 * e + 1])),
-                                    make_float2(mul, mul), make_float2(add, add));
-              }
+              for (int e = 0; e < 32; ++e)
+                x[e] = fmaf(__uint_as_float(c[e]), q_mul * tab[2 * h + e / 16].k, tab[2 * h + e / 16].add - ref);
               if (tok + 32 * h + 32 > least) {  // the same for the warp: some row does not see all of these
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  if (2 * e >= sees) x[e].x = -INFINITY;
-                  if (2 * e + 1 >= sees) x[e].y = -INFINITY;
-                }
+                for (int e = 0; e < 32; ++e)
+                  if (e >= sees) x[e] = -INFINITY;
               }
               if (again) {  // scores of 2^27 and more: a rounded reference may lie far below the largest
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  x[e].x = min_nan(x[e].x, kLift + 1.f);
-                  x[e].y = min_nan(x[e].y, kLift + 1.f);
-                }
+                for (int e = 0; e < 32; ++e) x[e] = min_nan(x[e], kLift + 1.f);
               }
               float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
               for (int g = 0; g < 2; ++g) {
-                float2 s2 = make_float2(0.f, 0.f);
+                float sum_a = 0.f, sum_b = 0.f;
 #pragma unroll
-                for (int e = 8 * g; e < 8 * g + 8; ++e) {
-                  if (e % 2)
-                    top1 = max3(top1, x[e].x, x[e].y);
+                for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+                  if (e % 4)
+                    top1 = max3(top1, x[e], x[e + 1]);
                   else
-                    top0 = max3(top0, x[e].x, x[e].y);
-                  const float2 v = make_float2(exp2_fast(x[e].x), exp2_fast(x[e].y));
-                  s2 = __fadd2_rn(s2, v);
-                  p[e] = f16x2_bits(v.x, v.y);
+                    top0 = max3(top0, x[e], x[e + 1]);
+                  const float va = exp2_fast(x[e]), vb = exp2_fast(x[e + 1]);
+                  sum_a += va;
+                  sum_b += vb;
+                  p[e / 2] = f16x2_bits(va, vb);
                 }
-                sums[g] = s2.x + s2.y;
+                sums[g] = sum_a + sum_b;
               }
               const float top = fmaxf(top0, top1);
               if (again || !__any_sync(0xffffffffu, unset ? top > -INFINITY : top > kMost)) break;
@@ -979,16 +979,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------- codes into shared memory, 16 tokens a copy
       constexpr uint32_t kBytes = 16 * kDim;
       bool ok = true;
-      uint32_t asked[2] = {0, 0};
+      uint32_t asked = 0;  // copies, keys' and values' in turn
       for (uint32_t it = 0; ok; ++it) {
         const Tab& tab = tabs[it % kTabs];
         if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1)) || tab.slot < 0) break;
         const int row = lane < kGroups ? tab.row[lane] : -1;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-#pragma unroll
+#pragma unroll 1
         for (int v = 0; v < 2; ++v) {
           if (!(ok = warp_wait(&bar.codes_empty[v], (it & 1) ^ 1))) break;
-          ++asked[v];
+          ++asked;
           if (lane == 0) mbar_arrive_expect_tx(&bar.codes_full[v], n * kBytes);
           __syncwarp();
           if (row >= 0)
@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // what is on its way lands before the CTA's end
 #pragma unroll
       for (int v = 0; v < 2; ++v)
-        if (asked[v] > 0) mbar_drain(&bar.codes_full[v], (asked[v] - 1) & 1);
+        if (asked > uint32_t(v)) mbar_drain(&bar.codes_full[v], ((asked - v + 1) / 2 - 1) & 1);
     } else if (warp == kScoutWarp) {
       // ------------------------------------------- where tiles lie, and their scales
       // Up to four tiles at a time, eight lanes each: table entries, then scales, are the latencies that nothing
@@ -1010,6 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && !ended) {
         int mine = -1, mine_j = 0;  // the lane's tile: its unit's slot
         int n = 0;
+#pragma unroll 1
         for (; n < 4; ++n) {
           while (j == j1) {
             const int s = taken % kRing;
@@ -1071,6 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.mode = blk < 0 ? kZero : !fin ? kNotFinite : !used ? kZero : vs < 0.f ? kNegate : 0u;
         const uint32_t lie = __ballot_sync(0xffffffffu, row >= 0);
         const int total = n + (ended ? 1 : 0);  // and the end
+#pragma unroll 1
         for (int q = 0; q < total && ok; ++q, ++it) {
           Tab& t = tabs[it % kTabs];
           if (!(ok = warp_wait(&bar.tab_empty[it % kTabs], ((it / kTabs) & 1) ^ 1))) break;
