@@ -267,21 +267,26 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
   return tile + (c / 8) * Smem<kDim>::kSubBytes + row * 128 + (((c % 8) ^ (row & 7)) << 4);
 }
 
-// A warp's 32 rows of Q into shared memory as FP16 times a power of two for each that brings its largest
-// element into [2^10, 2^11); returns the reciprocal of that power for the lane's row, the `row`-th of the
-// tile, whose elements begin at `at` (< 0: no such row).  (Code that runs once a unit is kept short too: it
-// comes from beyond the instruction cache each time.)
+// A warp's 32 rows of Q are asked for as they lie (`at`: where the lane's row begins, < 0: no such row;
+// whole rows are read by neighbouring lanes) and become FP16 in place, times a power of two for each that
+// brings its largest element into [2^10, 2^11): stage_queries returns the reciprocal of that power for the
+// lane's row, the `row`-th of the tile.  (Code that runs once a unit is kept short too: it comes from
+// beyond the instruction cache each time.)
 template <int kDim>
-__device__ __forceinline__ float stage_queries(uint8_t* tile, int row, int lane, const __nv_bfloat16* Q, long long at) {
-  constexpr int kChunks = kDim / 8, kRowsAtOnce = 32 / kChunks;  // whole rows are read by neighbouring lanes
-#pragma unroll 8
+__device__ __forceinline__ void request_queries(uint8_t* tile, int row, int lane, const __nv_bfloat16* Q, long long at) {
+  constexpr int kChunks = kDim / 8, kRowsAtOnce = 32 / kChunks;
+#pragma unroll 4
   for (int y = 0; y < 32; y += kRowsAtOnce) {
     const int from = y + lane / kChunks;
     const long long q = __shfl_sync(0xffffffffu, at, from);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (q >= 0) v = *reinterpret_cast<const uint4*>(Q + q + 8 * (lane % kChunks));
-    *reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row - lane + from, lane % kChunks)) = v;
+    cp_async_16(smem_addr(chunk_at<kDim>(tile, row - lane + from, lane % kChunks)),
+                Q + (q < 0 ? 0 : q + 8 * (lane % kChunks)), q < 0 ? 0u : 16u);
   }
+}
+template <int kDim>
+__device__ __forceinline__ float stage_queries(uint8_t* tile, int row) {
+  constexpr int kChunks = kDim / 8;
+  cp_async_wait_all();
   __syncwarp();
   uint32_t top2 = 0u;  // of the even elements and of the odd ones: magnitudes of BF16 order as whole numbers do
 #pragma unroll 4
@@ -294,7 +299,7 @@ __device__ __forceinline__ float stage_queries(uint8_t* tile, int row, int lane,
   // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
   const int exp = max(int(top >> 7), 10);
   const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
-#pragma unroll 2
+#pragma unroll 4
   for (int c = 0; c < kChunks; ++c) {
     uint4* p = reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c));
     float f[8];
@@ -431,6 +436,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t((warp % 4) * 32) << 16;
     const uint32_t s_at = tmem + lanes + kSCol + 128 * i, o_at = tmem + lanes + kOCol + 128 * i;
     uint8_t* q_tile = smem + S::kQ + i * S::kTileBytes;
+    // where the lane's row of a unit lies in Q
+    auto query_at = [&](const Unit* u) -> long long {
+      const int r = kTileRows * i + row, sr = u->row0 + r;
+      if (r >= u->rows) return -1;
+      return (long long)(u->t0 + sr / a.group) * a.ld_q + (long long)(u->head * a.group + sr % a.group) * kDim;
+    };
+    bool asked = false;  // for the next unit's queries
     uint32_t it = 0;     // tiles of tokens, as all roles count them
     uint32_t mine = 0;   // those in which this tile of rows took part
     for (uint32_t taken = 0;; ++taken) {
@@ -447,16 +459,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int r = kTileRows * i + row;  // row of the unit
       const bool row_ok = r < rows;
-      const int seq_row = u->row0 + r, token = u->t0 + seq_row / a.group;
-      const int head = u->head * a.group + seq_row % a.group;
+      const int seq_row = u->row0 + r;
       const int limit = row_ok ? row_limit(a, u->len, u->n, seq_row) : 0x7fffffff;
       const int least = __shfl_sync(0xffffffffu, limit, 0);  // rows see more and more
       const int most_seen = u->vis;
       float ref = 0.f, sum = 0.f, vref = 1.f;  // sum: of p over vref's share of |v_scale|
       bool unset = true;
       if (j1 > j0) {
-        const float down = stage_queries<kDim>(
-            q_tile, row, lane, a.Q, row_ok ? (long long)token * a.ld_q + (long long)head * kDim : -1LL);
+        if (!asked) request_queries<kDim>(q_tile, row, lane, a.Q, query_at(u));
+        const float down = stage_queries<kDim>(q_tile, row);
+        asked = false;
         const float q_mul = down * (a.scale * 1.44269504088896341f);
         fence_proxy_async_smem();
         __syncwarp();
@@ -469,6 +481,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(&bar.s_full[i], mine & 1))) break;
           if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1))) break;
           tc_fence_after();
+          if (j + 1 == j1) {  // the unit's queries have been used: those of the next one, if it is known yet
+            const int next = (taken + 1) % kRing;
+            if (__all_sync(0xffffffffu, mbar_test(&bar.ring_full[next], ((taken + 1) / kRing) & 1))) {
+              const Unit* v = ring(next);
+              asked = v->kind != kEnd && v->rows > kTileRows * i && v->j1 > v->j0;
+              if (asked) request_queries<kDim>(q_tile, row, lane, a.Q, query_at(v));
+            }
+          }
           const int tok = j * kTok;
           if (j == j0) vref = tabs[it % kTabs].v0;
           if (__any_sync(0xffffffffu, unset)) {  // a first reference, from the first tile that is there
@@ -680,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
       }
       const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
-      const long long out_at = ((long long)token * a.heads * a.group + head) * kDim;
+      __nv_bfloat16* out = a.O + ((long long)(u->t0 + seq_row / a.group) * a.heads * a.group + u->head * a.group +
+                                  seq_row % a.group) * kDim;
       // parts: [kDim / 4][rows][4], then [rows][4], so that neighbouring lanes write neighbouring places
       float4* part = reinterpret_cast<float4*>(parts) +
                      (size_t(blockIdx.x) * 2 + (kind == kFirst)) * (kUnitRows * (kDim / 4 + 1)) + r;
@@ -691,7 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(o_at + d, o);
           tmem_ld_wait_tied(o);
         }
-        if (kind == kWhole) {  // by way of the warp's rows of Q, which have been used: rows leave whole
+        if (!row_ok) {
+        } else if (kind == kWhole) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             float v[8];
@@ -699,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(o[e + y]) * f * vref;
             Raw8<__nv_bfloat16> w;
             pack8(v, w);
-            *reinterpret_cast<uint4*>(chunk_at<kDim>(q_tile, row, (d + e) / 8)) = w.a;
+            store8(out + d + e, w);
           }
-        } else if (row_ok) {
+        } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             part[size_t(d + e) / 4 * kUnitRows] =
@@ -710,23 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      if (kind == kWhole) {
-        constexpr int kChunks = kDim / 8, kRowsAtOnce = 32 / kChunks;
-#pragma unroll 4
-        for (int y = 0; y < 32; y += kRowsAtOnce) {
-          const int from = y + lane / kChunks;  // row of the warp
-          const long long to = __shfl_sync(0xffffffffu, out_at, from);
-          const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<kDim>(q_tile, row - lane + from, lane % kChunks));
-          if (kTileRows * i + row - lane + from < rows) *reinterpret_cast<uint4*>(a.O + to + 8 * (lane % kChunks)) = v;
-        }
-        __syncwarp();
-      } else if (row_ok) {
+      if (kind != kWhole && row_ok) {
         part[size_t(kUnitRows) * (kDim / 4)] = make_float4(unset ? -INFINITY : ref, sum, vref, 0.f);
       }
       tc_fence_before();  // O has been read before its next product, which waits for P
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar.ring_empty[slot]);
     }
+    cp_async_wait_all();
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------- keys and values
     regs_decrease<kConvRegs>();
