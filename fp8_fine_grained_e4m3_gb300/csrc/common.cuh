@@ -301,6 +301,10 @@ bool make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint6
 // over their own length.  Defined in api.cu.
 bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t cols,
                     uint32_t box_rows);
+// Encodes a 2-D bf16 tensor map with 128-byte swizzling: rows x cols elements, `pitch` elements from row to
+// row, box of box_rows x 64 elements (128 bytes).  False as below.  Defined in api.cu.
+bool make_tmap_bf16_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch,
+                          uint32_t box_rows);
 // Encodes a 2-D row-major bf16 tensor map with 64-byte swizzling: rows x
 // cols elements, box of box_rows x 32 elements (64 bytes).  False when the
 // layout cannot be described (base not 16-byte aligned, cols * 2 not a

@@ -15,11 +15,18 @@
 //             block), so that each promotion thread holds 64 gate values and the up values
 //             of the same columns, and a row's maximum is one exchange between two threads
 //   backward  256 columns of dh: each promotion thread holds one whole 1x128 block of a row
-// so the activations never leave the chip in 16 or 32 bits.
+// so the activations never leave the chip in 16 or 32 bits.  The backward form's gate and up values come
+// through the operand ring too, behind the tile's last K block (direct loads of 16 bytes a row, each
+// from another line, took longer than the product: 257 us at 8192 x 2048 x 7168); du waits in their places
+// until the block's maximum is known, and the 16-bit gradients leave from there.  (Four promotion
+// warpgroups of 64 columns each, to hide the TMEM loads' latency and shorten the epilogue, were slower:
+// 178 us forward at 4096 x 2048 x 7168 for 124.)
 //
 // Bound by the tensor cores and the promotion for prompts, by the weights' bytes for a few
 // tokens: then all tiles fit in one wave, and each is split along K over a cluster (as in
 // gemm_tc.cu), whose CTAs share the rows of the epilogue.
+#include <cstring>
+
 #include "common.cuh"
 #include "f8_convert.cuh"
 #include "ptx.cuh"
@@ -31,18 +38,22 @@ namespace {
 constexpr int kGroupM = 16;  // M blocks per rasterisation group
 constexpr int kBN = 256;     // accumulator columns of a tile
 constexpr int kStages = 4;
-constexpr int kPromoWarps = 8;
-constexpr int kTmaWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 384;
+constexpr int kGroups = 2;            // promotion warpgroups
+constexpr int kCols = kBN / kGroups;  // accumulator columns of a thread
+constexpr int kPromoWarps = 4 * kGroups;
+constexpr int kTmaWarp = kPromoWarps, kMmaWarp = kPromoWarps + 1;
+constexpr int kThreads = 128 * (kGroups + 1);
 // 65536 / 384 -> 168 registers at launch; 128 * 72 + 256 * 216 = 384 * 168
 constexpr uint32_t kLowRegs = 72, kHighRegs = 216;
+static_assert(kGroups * kHighRegs + kLowRegs <= 3 * 168, "register split");
 constexpr int kABytes = kBlockM * kBlockK, kBBytes = kBN * kBlockK;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kPitch = kBN + 4;  // floats of a staged row (split tiles)
-constexpr size_t kSmemBytes = 1024 + size_t(kStages) * kStageBytes + 2 * 2 * kBlockM * 4 + 512;
+constexpr int kBoxBytes = kBlockM * 128;  // 64 columns of gate or up values: one of three in a stage
+constexpr int kGuStages = 3;              // stages that a tile's eight boxes take
+constexpr size_t kSmemBytes = 1024 + size_t(kStages) * kStageBytes + 2 * kGroups * kBlockM * 4 + 512;
 static_assert(kSmemBytes <= 232448, "227 KB of shared memory per CTA");
 static_assert(size_t(kBlockM) * kPitch * 4 <= size_t(kStages) * kStageBytes, "staging fits the ring");
-static_assert(128 * kLowRegs + 256 * kHighRegs <= 384 * 168, "register split");
 
 // Columns of h (or dh) of a tile.
 template <bool kGrad>
@@ -83,16 +94,23 @@ __device__ __forceinline__ float2 swiglu_grad(float dh, float g, float u) {
 }
 
 // Sixteen values to codes of one scale, stored at p.
-template <bool kE5M2>
-__device__ __forceinline__ void store_codes16(uint8_t* p, const float (&v)[16], const Reciprocal& s) {
-  float a[8], b[8];
+__device__ __forceinline__ void store_codes16(uint8_t* p, const float (&v)[16], const Reciprocal& s, bool e5m2) {
+  uint32_t c[4];
+  if (s.safe) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a[i] = v[i];
-    b[i] = v[8 + i];
+    for (int i = 0; i < 4; ++i) {
+      const float a = quotient(v[4 * i], s), b = quotient(v[4 * i + 1], s), x = quotient(v[4 * i + 2], s),
+                  y = quotient(v[4 * i + 3], s);
+      c[i] = e5m2 ? cvt_f8x2<true>(a, b) | (cvt_f8x2<true>(x, y) << 16) : cvt_f8x2<false>(a, b) | (cvt_f8x2<false>(x, y) << 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      c[i] = s.s == 0.f ? 0u : e5m2 ? quant4<true>(x, s.s) : quant4<false>(x, s.s);
+    }
   }
-  const uint2 x = quant8<kE5M2>(a, s), y = quant8<kE5M2>(b, s);
-  *reinterpret_cast<uint4*>(p) = make_uint4(x.x, x.y, y.x, y.y);
+  *reinterpret_cast<uint4*>(p) = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 template <bool kE5M2>
@@ -106,96 +124,6 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
-}
-
-// ---- whole tiles: a thread's 64 columns of h (acc: 64 gate, 64 up values)
-template <bool kE5M2>
-__device__ __forceinline__ void store_h(const GatedArgs& a, const float2 (&acc)[64], int row, int col,
-                                        float scale) {
-  const Reciprocal s = reciprocal(scale);
-  uint8_t* q = a.Q + size_t(row) * a.I + col;
-#pragma unroll
-  for (int c = 0; c < 64; c += 16) {
-    if (col + c >= a.I) break;
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = acc[c / 2 + i].x;
-      v[2 * i + 1] = acc[c / 2 + i].y;
-    }
-    store_codes16<kE5M2>(q + c, v, s);
-  }
-}
-
-// ---- whole tiles: a thread's 128 columns of dh; the block's maxima first, then the codes
-// (the gradients of 128 columns do not fit in registers beside dh, so they are formed twice)
-template <bool kE5M2>
-__device__ __forceinline__ void store_dgu(const GatedArgs& a, const float2 (&acc)[64], int row, int col) {
-  const __nv_bfloat16* g = a.GU + size_t(row) * 2 * a.I + col;
-  const int Ip = ceil_div(a.I, kBlockK) * kBlockK;
-  float top_g = 0.f, top_u = 0.f;
-#pragma unroll
-  for (int c = 0; c < 128; c += 8) {
-    if (col + c >= a.I) break;
-    float gv[8], uv[8];
-    unpack8(load8(g + c), gv);
-    unpack8(load8(g + a.I + c), uv);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float dh = i % 2 ? acc[(c + i) / 2].y : acc[(c + i) / 2].x;
-      const float2 d = swiglu_grad(dh, gv[i], uv[i]);
-      top_g = max_nan(top_g, fabsf(d.x));
-      top_u = max_nan(top_u, fabsf(d.y));
-    }
-  }
-  const Reciprocal sg = reciprocal(block_scale<kE5M2>(top_g)), su = reciprocal(block_scale<kE5M2>(top_u));
-  float* sq = a.sQ + size_t(row) * (2 * Ip / kBlockK) + col / kBlockK;
-  sq[0] = sg.s;
-  sq[Ip / kBlockK] = su.s;
-  uint8_t* q = a.Q + size_t(row) * 2 * Ip + col;
-  __nv_bfloat16* o = a.dGU ? a.dGU + size_t(row) * 2 * a.I + col : nullptr;
-#pragma unroll
-  for (int c = 0; c < 128; c += 16) {
-    float dg[16], du[16];
-#pragma unroll
-    for (int e = 0; e < 16; e += 8) {
-      float gv[8] = {}, uv[8] = {};
-      if (col + c < a.I) {
-        unpack8(load8(g + c + e), gv);
-        unpack8(load8(g + a.I + c + e), uv);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float dh = i % 2 ? acc[(c + e + i) / 2].y : acc[(c + e + i) / 2].x;
-        const float2 d = swiglu_grad(dh, gv[i], uv[i]);
-        dg[e + i] = d.x;
-        du[e + i] = d.y;
-      }
-    }
-    if (col + c < a.I) {
-      store_codes16<kE5M2>(q + c, dg, sg);
-      store_codes16<kE5M2>(q + Ip + c, du, su);
-      if (o) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          float x[8], y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = dg[e + i];
-            y[i] = du[e + i];
-          }
-          Raw8<__nv_bfloat16> r;
-          pack8(x, r);
-          store8(o + c + e, r);
-          pack8(y, r);
-          store8(o + a.I + c + e, r);
-        }
-      }
-    } else {  // the rest of the last block, up to the next half
-      *reinterpret_cast<uint4*>(q + c) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(q + Ip + c) = make_uint4(0, 0, 0, 0);
-    }
-  }
 }
 
 // ---- split tiles: a warp's row of one 1x128 block, four columns a lane
@@ -261,21 +189,26 @@ __device__ __forceinline__ void finish_dgu(const GatedArgs& a, int row, int col,
 }
 
 // kSplit: cluster c of args.split CTAs computes tile c, CTA rank r the r-th share of its K blocks.
+// tmG, tmU: gate and up values, and tmDG, tmDU their gradients (backward, whole tiles).
 template <bool kGrad, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_gated_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
+                      const __grid_constant__ CUtensorMap tmDG, const __grid_constant__ CUtensorMap tmDU,
                       const __grid_constant__ GatedArgs args, int* status) {
+  constexpr bool kRingGu = kGrad && !kSplit;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smA = smem;
   uint8_t* smB = smem + kStages * kABytes;
-  float* tops = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // [2][2][kBlockM]
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(tops + 2 * 2 * kBlockM);
+  float* tops = reinterpret_cast<float*>(smem + kStages * kStageBytes);  // [2][kGroups][kBlockM]
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(tops + 2 * kGroups * kBlockM);
   uint64_t* empty_bar = full_bar + kStages;
   uint64_t* tfull_bar = empty_bar + kStages;
   uint64_t* tempty_bar = tfull_bar + 2;
-  uint64_t* pair_bar = tempty_bar + 2;  // the two promotion warps of the same rows
-  uint64_t* drain_bar = pair_bar + 4;
+  uint64_t* row_bar = tempty_bar + 2;  // the promotion warps of the same rows
+  uint64_t* gu_bar = row_bar + 4;      // a tile's gate and up values have been used
+  uint64_t* drain_bar = gu_bar + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -290,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tfull_bar[b], 1);
       mbar_init(&tempty_bar[b], kPromoWarps);
     }
-    for (int p = 0; p < 4; ++p) mbar_init(&pair_bar[p], 2);
+    for (int p = 0; p < 4; ++p) mbar_init(&row_bar[p], kGroups);
+    mbar_init(gu_bar, kPromoWarps);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -302,6 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    if constexpr (kRingGu) {
+      tma_prefetch_desc(&tmG);
+      tma_prefetch_desc(&tmU);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -329,28 +267,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kTmaWarp) {
     regs_decrease<kLowRegs>();
     if (lane == 0) {
-      uint32_t it = 0;
+      uint32_t it = 0;          // uses of the ring
+      uint32_t was_gu = 0;      // bit s: stage s held gate and up values last
+      uint32_t parity = 0xf;    // bit s: of the next completion of empty_bar[s] to wait for
+      uint32_t gu_tiles = 0;
+      // the stage's last contents have been used
+      auto free_stage = [&](int s) {
+        bool ok;
+        if (kRingGu && (was_gu >> s & 1u)) {
+          ok = mbar_wait(gu_bar, (gu_tiles - 1) & 1, abort_flag, args.wait_ns);
+        } else {
+          ok = mbar_wait(&empty_bar[s], parity >> s & 1u, abort_flag, args.wait_ns);
+          parity ^= 1u << s;
+        }
+        if (!ok) fail();
+        return ok;
+      };
       bool ok = true;
       for (int t = t_begin; t < total && ok; t += t_step) {
         const GatedTile w = gated_tile<kGrad>(args, t);
+        if constexpr (kRingGu)  // what the epilogue will read, into the L2 meanwhile
+          for (int h = 0; h < 4; ++h) {
+            tma_prefetch_l2_2d(&tmG, w.col0 + 64 * h, w.row0);
+            tma_prefetch_l2_2d(&tmU, w.col0 + 64 * h, w.row0);
+          }
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % kStages;
-          if (!mbar_wait(&empty_bar[s], ((it / kStages) & 1) ^ 1, abort_flag, args.wait_ns)) {
-            fail();
-            ok = false;
-            break;
-          }
+          if (!(ok = free_stage(s))) break;
+          was_gu &= ~(1u << s);
           mbar_arrive_expect_tx(&full_bar[s], kStageBytes);
           tma_load_2d(smA + s * kABytes, &tmA, &full_bar[s], kb * kBlockK, w.row0);
           uint8_t* b = smB + s * kBBytes;
           if constexpr (kGrad) {
             tma_load_2d(b, &tmB, &full_bar[s], kb * kBlockK, w.col0);
           } else {
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 4; ++i)
               tma_load_2d(b + i * (kBBytes / 4), &tmB, &full_bar[s], kb * kBlockK,
                           w.col0 + 64 * (i / 2) + (i % 2 ? args.I : 0));
           }
+        }
+        if constexpr (kRingGu) {
+#pragma unroll 1
+          for (int g = 0; g < kGuStages && ok; ++g, ++it) {
+            const int s = it % kStages, boxes = g < 2 ? 3 : 2;
+            if (!(ok = free_stage(s))) break;
+            was_gu |= 1u << s;
+            mbar_arrive_expect_tx(&full_bar[s], boxes * kBoxBytes);
+            for (int i = 0; i < boxes; ++i) {  // box 2 h: gate values of columns 64 h .. 64 h + 63, 2 h + 1: up values
+              const int box = 3 * g + i;
+              tma_load_2d(i == 0 ? smA + s * kABytes : smB + s * kBBytes + (i - 1) * kBoxBytes,
+                          box % 2 ? &tmU : &tmG, &full_bar[s], w.col0 + 64 * (box / 2), w.row0);
+            }
+          }
+          ++gu_tiles;
         }
       }
       // let the last copies into each stage land before the CTA can exit
@@ -361,13 +331,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_decrease<kLowRegs>();
     if (lane == 0) {
       const uint32_t idesc = idesc_f8_f32(kBlockM, kBN, uint32_t(args.a_fmt), uint32_t(args.b_fmt));
-      const uint32_t a_base = smem_addr(smA), b_base = smem_addr(smB);
-      uint32_t it = 0;
+      const uint64_t a_desc = smem_desc_sw128_kmajor(smem_addr(smA)), b_desc = smem_desc_sw128_kmajor(smem_addr(smB));
+      uint32_t it = 0, n_mma = 0;
       bool ok = true;
       for (int t = t_begin; t < total && ok; t += t_step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kStages, buf = it & 1;
-          if (!mbar_wait(&tempty_bar[buf], ((it / 2) & 1) ^ 1, abort_flag, args.wait_ns) ||
+        for (int kb = kb0; kb < kb1; ++kb, ++it, ++n_mma) {
+          const int s = it % kStages, buf = n_mma & 1;
+          if (!mbar_wait(&tempty_bar[buf], ((n_mma / 2) & 1) ^ 1, abort_flag, args.wait_ns) ||
               !mbar_wait(&full_bar[s], (it / kStages) & 1, abort_flag, args.wait_ns)) {
             fail();
             ok = false;
@@ -376,13 +346,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < kBlockK / 32; ++k)
-            umma_e4m3(tmem_base + buf * kBN, smem_desc_sw128_kmajor(a_base + s * kABytes + k * 32),
-                      smem_desc_sw128_kmajor(b_base + s * kBBytes + k * 32), idesc, k > 0 ? 1u : 0u);
+            umma_e4m3(tmem_base + buf * kBN, a_desc + ((s * kABytes + k * 32) >> 4), b_desc + ((s * kBBytes + k * 32) >> 4),
+                      idesc, k > 0 ? 1u : 0u);
           umma_commit(&empty_bar[s]);
           umma_commit(&tfull_bar[buf]);
         }
+        if constexpr (kRingGu) {
+          // Each use of a stage is seen in turn, these too: a wait for a barrier's next phase but one would end
+          // at once.
+          for (int g = 0; g < kGuStages && ok; ++g, ++it)
+            if (!mbar_wait(&full_bar[it % kStages], (it / kStages) & 1, abort_flag, args.wait_ns)) {
+              fail();
+              ok = false;
+            }
+        }
       }
-      if (it > 0) {  // every issued MMA has finished before TMEM is released
+      if (n_mma > 0) {  // every issued MMA has finished before TMEM is released
         umma_commit(drain_bar);
         mbar_drain(drain_bar, 0);
       }
@@ -391,54 +370,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_increase<kHighRegs>();
     const int wg = warp / 4;
     const int row = (warp % 4) * 32 + lane;  // TMEM lane = tile row
-    const uint32_t lane_base = uint32_t((warp % 4) * 32) << 16;
+    const uint32_t taddr0 = tmem_base + (uint32_t((warp % 4) * 32) << 16) + wg * kCols;
     const int Nb = ceil_div(kGrad ? args.I : 2 * args.I, kBlockK);
-    uint32_t it = 0, tiles = 0;
+    uint32_t n_mma = 0, it = 0, tiles = 0;
     bool ok = true;
     for (int t = t_begin; t < total && ok; t += t_step, ++tiles) {
       const GatedTile w = gated_tile<kGrad>(args, t);
       const bool row_ok = row < w.rows;
-      const int col = w.col0 + wg * (tile_cols<kGrad>() / 2);  // the thread's first column of h
-      const float* sa_ptr = args.sA + size_t(w.row0 + row) * Kb;
-      // The up rows of W1 may begin inside a 128-row scale block: of the thread's 64 up
-      // columns the first 16 n_low belong to one block, the rest to the next.
+      const int col = w.col0 + wg * (tile_cols<kGrad>() / kGroups);  // the thread's first column of h
+      // The up rows of W1 may begin inside a 128-row scale block: of the thread's 64 up columns the first
+      // 16 n_low belong to one block, the rest to the next.
       const int b0 = min(col / kBlockK, Nb - 1);
       const int b1 = kGrad ? b0 : min((args.I + col) / kBlockK, Nb - 1);
       const int b2 = kGrad ? b0 : min(b1 + 1, Nb - 1);
       const int n_low = kGrad ? 4 : (kBlockK - (args.I + col) % kBlockK) / 16;
+      const float* sa_ptr = args.sA + size_t(w.row0 + (row_ok ? row : 0)) * Kb;
       const float* s0_ptr = args.sB + size_t(b0) * Kb;
       const float* s1_ptr = args.sB + size_t(b1) * Kb;
       const float* s2_ptr = args.sB + size_t(b2) * Kb;
-      float2 acc[64];
+      float2 acc[kCols / 2];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      float sa = row_ok ? __ldg(sa_ptr + kb0) : 0.f;
-      float s0 = __ldg(s0_ptr + kb0), s1 = kGrad ? s0 : __ldg(s1_ptr + kb0), s2 = kGrad ? s0 : __ldg(s2_ptr + kb0);
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      float sa = __ldg(sa_ptr + kb0), s0 = __ldg(s0_ptr + kb0);
+      float s1 = kGrad ? s0 : __ldg(s1_ptr + kb0), s2 = kGrad ? s0 : __ldg(s2_ptr + kb0);
+      for (int kb = kb0; kb < kb1; ++kb, ++n_mma) {
         const float c0 = sa * s0, c1 = kGrad ? c0 : sa * s1, c2 = kGrad ? c0 : sa * s2;
         if (kb + 1 < kb1) {
-          sa = row_ok ? __ldg(sa_ptr + kb + 1) : 0.f;
+          sa = __ldg(sa_ptr + kb + 1);
           s0 = __ldg(s0_ptr + kb + 1);
           if constexpr (!kGrad) {
             s1 = __ldg(s1_ptr + kb + 1);
             s2 = __ldg(s2_ptr + kb + 1);
           }
         }
-        const int buf = it & 1;
-        if (!mbar_wait(&tfull_bar[buf], (it / 2) & 1, abort_flag, args.wait_ns)) {
+        const int buf = n_mma & 1;
+        if (!mbar_wait(&tfull_bar[buf], (n_mma / 2) & 1, abort_flag, args.wait_ns)) {
           fail();
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t taddr = tmem_base + lane_base + buf * kBN + wg * (kBN / 2);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t r[64];
-          tmem_ld_32x32b_x64(taddr + c * 64, r);
+          tmem_ld_32x32b_x64(taddr0 + buf * kBN + c * 64, r);
           tmem_ld_wait_tied(*reinterpret_cast<uint32_t(*)[32]>(&r[0]));
           reg_tie32(&r[32]);
-          if (c == 1) {
+          if (c == 1 && (kSplit || kb + 1 < kb1)) {  // (the last one's place is the epilogue's)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty_bar[buf]);
@@ -451,69 +429,195 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      it += kb1 - kb0;
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if constexpr (kSplit) {
-        float4* srow = reinterpret_cast<float4*>(smem) + (row * kPitch + wg * (kBN / 2)) / 4;
+        float4* srow = reinterpret_cast<float4*>(smem) + (row * kPitch + wg * kCols) / 4;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < kCols / 4; ++j)
           srow[j] = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
         continue;
       }
+      // The sums go back to TMEM, where the last K block's were, and the epilogue takes them from there 16
+      // columns at a time, in loops: unrolled over registers its code (16000 instructions) did not fit in the
+      // instruction cache, which cost more than its arithmetic (24 us a tile instead of XX).
       const int m = w.row0 + row;
+      const int last_buf = (n_mma - 1) & 1;
+      const uint32_t tacc = taddr0 + last_buf * kBN;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(j % 2 ? acc[16 * c + j / 2].y : acc[16 * c + j / 2].x);
+        tmem_st_32x32b_x32(tacc + 32 * c, r);
+      }
+      tmem_st_wait();
+      const bool e5 = args.q_fmt == FP8GEMM_FMT_E5M2;
       if constexpr (kGrad) {
-        if (row_ok && col < args.I) {
-          if (args.q_fmt == FP8GEMM_FMT_E5M2)
-            store_dgu<true>(args, acc, m, col);
-          else
-            store_dgu<false>(args, acc, m, col);
+        // the thread's boxes: 4 wg .. 4 wg + 3
+        const uint32_t last = it + (4 * wg + 3) / 3;
+        for (uint32_t use = it + (4 * wg) / 3; use <= last && ok; ++use)
+          if (!mbar_wait(&full_bar[use % kStages], (use / kStages) & 1, abort_flag, args.wait_ns)) {
+            fail();
+            ok = false;
+          }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        auto box = [&](int b) {
+          const int s = (it + b / 3) % kStages;
+          return (b % 3 == 0 ? smA + s * kABytes : smB + s * kBBytes + (b % 3 - 1) * kBoxBytes) + row * 128;
+        };
+        const int swizzle = row & 7;
+        float top_g = 0.f, top_u = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {  // dg to TMEM, du to the places of g and u
+          uint8_t* g_row = box(4 * wg + 2 * (c / 64));
+          uint8_t* u_row = box(4 * wg + 2 * (c / 64) + 1);
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tacc + c, r);
+          tmem_ld_wait_tied16(r);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint4* gp = reinterpret_cast<uint4*>(g_row + (((c % 64 / 8 + e) ^ swizzle) << 4));
+            uint4* up = reinterpret_cast<uint4*>(u_row + (((c % 64 / 8 + e) ^ swizzle) << 4));
+            float g[8], u[8];
+            unpack8(Raw8<__nv_bfloat16>{*gp}, g);
+            unpack8(Raw8<__nv_bfloat16>{*up}, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 d = swiglu_grad(__uint_as_float(r[8 * e + i]), g[i], u[i]);
+              r[8 * e + i] = __float_as_uint(d.x);
+              u[i] = d.y;
+              if (col + c < args.I) {
+                top_g = max_nan(top_g, fabsf(d.x));
+                top_u = max_nan(top_u, fabsf(d.y));
+              }
+            }
+            *gp = make_uint4(__float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]), __float_as_uint(u[3]));
+            *up = make_uint4(__float_as_uint(u[4]), __float_as_uint(u[5]), __float_as_uint(u[6]), __float_as_uint(u[7]));
+          }
+          tmem_st_32x32b_x16(tacc + c, r);
         }
-      } else {
-        if (args.GU && row_ok) {
-          __nv_bfloat16* o = args.GU + size_t(m) * 2 * args.I + col;
+        tmem_st_wait();
+        const Reciprocal sg = reciprocal(e5 ? block_scale<true>(top_g) : block_scale<false>(top_g));
+        const Reciprocal su = reciprocal(e5 ? block_scale<true>(top_u) : block_scale<false>(top_u));
+        const int Ip = ceil_div(args.I, kBlockK) * kBlockK;
+        if (row_ok && col < args.I) {
+          float* sq = args.sQ + size_t(m) * (2 * Ip / kBlockK) + col / kBlockK;
+          sq[0] = sg.s;
+          sq[Ip / kBlockK] = su.s;
+        }
+        uint8_t* q = args.Q + size_t(m) * 2 * Ip + col;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+          uint8_t* g_row = box(4 * wg + 2 * (c / 64));
+          uint8_t* u_row = box(4 * wg + 2 * (c / 64) + 1);
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tacc + c, r);
+          tmem_ld_wait_tied16(r);
+          float dg[16], du[16];
 #pragma unroll
-          for (int c = 0; c < 64; c += 8) {
-            if (col + c >= args.I) break;
+          for (int e = 0; e < 2; ++e) {
+            const int at = ((c % 64 / 8 + e) ^ swizzle) << 4;
+            const float4 lo = *reinterpret_cast<const float4*>(g_row + at), hi = *reinterpret_cast<const float4*>(u_row + at);
+            const float d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float2* p = &acc[32 * half + c / 2];
-              *reinterpret_cast<uint4*>(o + half * args.I + c) =
-                  make_uint4(bf16x2_bits(p[0].x, p[0].y), bf16x2_bits(p[1].x, p[1].y),
-                             bf16x2_bits(p[2].x, p[2].y), bf16x2_bits(p[3].x, p[3].y));
+            for (int i = 0; i < 8; ++i) {
+              dg[8 * e + i] = __uint_as_float(r[8 * e + i]);
+              du[8 * e + i] = d[i];
+            }
+            if (args.dGU) {
+              const float* v = dg + 8 * e;
+              *reinterpret_cast<uint4*>(g_row + at) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                                                                 bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+              *reinterpret_cast<uint4*>(u_row + at) = make_uint4(bf16x2_bits(d[0], d[1]), bf16x2_bits(d[2], d[3]),
+                                                                 bf16x2_bits(d[4], d[5]), bf16x2_bits(d[6], d[7]));
             }
           }
+          if (row_ok && col + c < args.I) {
+            store_codes16(q + c, dg, sg, e5);
+            store_codes16(q + Ip + c, du, su, e5);
+          } else if (row_ok && col + c < Ip) {  // the rest of the last block, up to the next half
+            *reinterpret_cast<uint4*>(q + c) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(q + Ip + c) = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
         }
+        fence_proxy_async_smem();  // before the stores and the ring's next copies
+        __syncwarp();
+        if (args.dGU && lane == 0) {  // the warp's 32 rows (rows and columns that do not exist are not written)
+          for (int half = 0; half < 2; ++half)
+            if (col + 64 * half < args.I) {
+              tma_store_2d(&tmDG, box(4 * wg + 2 * half), col + 64 * half, w.row0 + (warp % 4) * 32);
+              tma_store_2d(&tmDU, box(4 * wg + 2 * half + 1), col + 64 * half, w.row0 + (warp % 4) * 32);
+            }
+          bulk_commit_group();
+          bulk_wait_group_read<0>();
+        }
+        if (lane == 0) mbar_arrive(gu_bar);
+        it += kGuStages;
+      } else {
         float top = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {  // h to the places of the gate values
+          uint32_t g[16], u[16];
+          tmem_ld_32x32b_x16(tacc + c, g);
+          tmem_ld_32x32b_x16(tacc + 64 + c, u);
+          tmem_ld_wait_tied16(g);
+          reg_tie16(u);
+          if (args.GU && row_ok && col + c < args.I) {
+            __nv_bfloat16* o = args.GU + size_t(m) * 2 * args.I + col + c;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          acc[j] = make_float2(swiglu(acc[j].x, acc[32 + j].x), swiglu(acc[j].y, acc[32 + j].y));
-          if (col + 2 * j < args.I) top = max_nan(top, max_nan(fabsf(acc[j].x), fabsf(acc[j].y)));
+            for (int e = 0; e < 16; e += 8) {
+              auto pair = [](const uint32_t* p) { return bf16x2_bits(__uint_as_float(p[0]), __uint_as_float(p[1])); };
+              *reinterpret_cast<uint4*>(o + e) = make_uint4(pair(g + e), pair(g + e + 2), pair(g + e + 4), pair(g + e + 6));
+              *reinterpret_cast<uint4*>(o + args.I + e) =
+                  make_uint4(pair(u + e), pair(u + e + 2), pair(u + e + 4), pair(u + e + 6));
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float h = swiglu(__uint_as_float(g[i]), __uint_as_float(u[i]));
+            g[i] = __float_as_uint(h);
+            if (col + c < args.I) top = max_nan(top, fabsf(h));
+          }
+          tmem_st_32x32b_x16(tacc + c, g);
         }
+        tmem_st_wait();
         // the other half of the row's block, from the thread that holds it
-        float* mine = tops + (tiles & 1) * 2 * kBlockM;
+        float* mine = tops + (tiles & 1) * kGroups * kBlockM;
         mine[wg * kBlockM + row] = top;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pair_bar[warp % 4]);
-        ok = mbar_wait(&pair_bar[warp % 4], tiles & 1, abort_flag, args.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) mbar_arrive(&row_bar[warp % 4]);
+        ok = __all_sync(0xffffffffu, mbar_wait(&row_bar[warp % 4], tiles & 1, abort_flag, args.wait_ns));
         if (!ok) {
           fail();
           break;
         }
         top = max_nan(top, mine[(1 - wg) * kBlockM + row]);
-        const bool e5 = args.q_fmt == FP8GEMM_FMT_E5M2;
-        const float scale = e5 ? block_scale<true>(top) : block_scale<false>(top);
-        if (row_ok) {
-          if (wg == 0) args.sQ[size_t(m) * ceil_div(args.I, kBlockK) + col / kBlockK] = scale;
-          if (e5)
-            store_h<true>(args, acc, m, col, scale);
-          else
-            store_h<false>(args, acc, m, col, scale);
+        const Reciprocal s = reciprocal(e5 ? block_scale<true>(top) : block_scale<false>(top));
+        if (row_ok && wg == 0) args.sQ[size_t(m) * ceil_div(args.I, kBlockK) + col / kBlockK] = s.s;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tacc + c, r);
+          tmem_ld_wait_tied16(r);
+          float h[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = __uint_as_float(r[i]);
+          if (row_ok && col + c < args.I) store_codes16(args.Q + size_t(m) * args.I + col + c, h, s, e5);
+          __syncwarp();
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty_bar[last_buf]);
     }
+    if (kRingGu && lane == 0) bulk_wait_group_all();  // before this warp's shared memory can go
   } else {
-    regs_decrease<kLowRegs>();  // warps 10-11: no work
+    regs_decrease<kLowRegs>();  // no work: the rest of the last warpgroup
   }
 
   if constexpr (kSplit) {
@@ -617,10 +721,23 @@ int choose_split(const LaunchCtx& c, long long tiles, int Kb) {
 template <bool kGrad>
 cudaError_t run(const LaunchCtx& c, GatedArgs a) {
   a.wait_ns = wait_limit_ns();
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmG, tmU, tmDG, tmDU;
   if (!make_tmap_u8_sw128(&tmA, a.A, uint64_t(a.M), a.K, kBlockM)) return cudaErrorInvalidValue;
   if (!make_tmap_u8_sw128(&tmB, a.B, kGrad ? uint64_t(a.I) : 2 * uint64_t(a.I), a.K, kGrad ? kBN : 64))
     return cudaErrorInvalidValue;
+  memset(&tmG, 0, sizeof(tmG));
+  memset(&tmU, 0, sizeof(tmU));
+  memset(&tmDG, 0, sizeof(tmDG));
+  memset(&tmDU, 0, sizeof(tmDU));
+  if constexpr (kGrad) {  // each half on its own: what lies past it does not exist
+    const uint64_t pitch = 2 * uint64_t(a.I);
+    if (!make_tmap_bf16_sw128(&tmG, a.GU, a.M, a.I, pitch, kBlockM) ||
+        !make_tmap_bf16_sw128(&tmU, a.GU + a.I, a.M, a.I, pitch, kBlockM))
+      return cudaErrorInvalidValue;
+    if (a.dGU && (!make_tmap_bf16_sw128(&tmDG, a.dGU, a.M, a.I, pitch, 32) ||
+                  !make_tmap_bf16_sw128(&tmDU, a.dGU + a.I, a.M, a.I, pitch, 32)))
+      return cudaErrorInvalidValue;
+  }
   static SmemLimit whole, split;
   if (cudaError_t e = whole.raise(c, reinterpret_cast<const void*>(gemm_gated_kernel<kGrad, false>), kSmemBytes))
     return e;
@@ -631,7 +748,7 @@ cudaError_t run(const LaunchCtx& c, GatedArgs a) {
   a.split = choose_split<kGrad>(c, tiles, ceil_div(a.K, kBlockK));
   if (a.split == 1)
     return launch_dependent(c, gemm_gated_kernel<kGrad, false>, unsigned(tiles < c.num_sms ? tiles : c.num_sms),
-                            kThreads, kSmemBytes, tmA, tmB, a, c.status);
+                            kThreads, kSmemBytes, tmA, tmB, tmG, tmU, tmDG, tmDU, a, c.status);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles * a.split));
   cfg.blockDim = dim3(kThreads);
@@ -646,7 +763,7 @@ cudaError_t run(const LaunchCtx& c, GatedArgs a) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_gated_kernel<kGrad, true>, tmA, tmB, a, c.status);
+  return cudaLaunchKernelEx(&cfg, gemm_gated_kernel<kGrad, true>, tmA, tmB, tmG, tmU, tmDG, tmDU, a, c.status);
 }
 
 }  // namespace

@@ -463,6 +463,13 @@ __device__ __forceinline__ void reg_tie32(uint32_t* r) {
                  "+r"(r[30]), "+r"(r[31]));
 }
 
+__device__ __forceinline__ void reg_tie16(uint32_t* r) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 // Waits for this warp's outstanding tcgen05.ld and ties the loaded registers
 // to the wait, so that no use of them can be scheduled before it.
 __device__ __forceinline__ void tmem_ld_wait_tied(uint32_t (&r)[32]) {

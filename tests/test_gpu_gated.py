@@ -62,7 +62,8 @@ def _check_bf16(got, ref, err):
 
 
 SHAPES = [(1, 16, 16), (1, 7168, 128), (3, 400, 400), (64, 1040, 272), (65, 4096, 48), (130, 272, 144), (200, 2064, 112),
-          (300, 512, 1040), (129, 2048, 2064), (1300, 144, 2048), (2500, 256, 1296)]
+          (300, 512, 1040), (129, 2048, 2064), (1300, 144, 2048), (2500, 256, 1296),
+          (2700, 144, 2064), (2700, 16, 2064)]  # the last two: several tiles a CTA
 
 
 @pytest.mark.parametrize("M,K,I", SHAPES)
