@@ -85,12 +85,19 @@ __device__ __forceinline__ float exp_minus(float x) {
   return r;
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.f + exp_minus(g)) * u; }
+// 1 / (1 + e^-g), to a few units in FP32's last place; 0 where e^-g is past FP32's range.
+__device__ __forceinline__ float sigmoid(float g) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_minus(g)));
+  return r;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return g * sigmoid(g) * u; }
 
 // dg and du of one element.
 __device__ __forceinline__ float2 swiglu_grad(float dh, float g, float u) {
-  const float s = __fdividef(1.f, 1.f + exp_minus(g));
-  return make_float2(dh * (u * (s * fmaf(g, 1.f - s, 1.f))), dh * (g * s));
+  const float s = sigmoid(g), ds = dh * s;
+  return make_float2(ds * (u * fmaf(g, 1.f - s, 1.f)), ds * g);
 }
 
 // Sixteen values to codes of one scale, stored at p.
@@ -477,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[16];
           tmem_ld_32x32b_x16(tacc + c, r);
           tmem_ld_wait_tied16(r);
+          float chunk_g = 0.f, chunk_u = 0.f;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint4* gp = reinterpret_cast<uint4*>(g_row + (((c % 64 / 8 + e) ^ swizzle) << 4));
@@ -489,15 +497,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 d = swiglu_grad(__uint_as_float(r[8 * e + i]), g[i], u[i]);
               r[8 * e + i] = __float_as_uint(d.x);
               u[i] = d.y;
-              if (col + c < args.I) {
-                top_g = max_nan(top_g, fabsf(d.x));
-                top_u = max_nan(top_u, fabsf(d.y));
-              }
+              chunk_g = max_nan(chunk_g, fabsf(d.x));
+              chunk_u = max_nan(chunk_u, fabsf(d.y));
             }
             *gp = make_uint4(__float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]), __float_as_uint(u[3]));
             *up = make_uint4(__float_as_uint(u[4]), __float_as_uint(u[5]), __float_as_uint(u[6]), __float_as_uint(u[7]));
           }
           tmem_st_32x32b_x16(tacc + c, r);
+          if (col + c < args.I) {
+            top_g = max_nan(top_g, chunk_g);
+            top_u = max_nan(top_u, chunk_u);
+          }
         }
         tmem_st_wait();
         const Reciprocal sg = reciprocal(e5 ? block_scale<true>(top_g) : block_scale<false>(top_g));
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it += kGuStages;
       } else {
         float top = 0.f;
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; c < 64; c += 16) {  // h to the places of the gate values
           uint32_t g[16], u[16];
           tmem_ld_32x32b_x16(tacc + c, g);
@@ -577,12 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
+          float chunk_top = 0.f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float h = swiglu(__uint_as_float(g[i]), __uint_as_float(u[i]));
             g[i] = __float_as_uint(h);
-            if (col + c < args.I) top = max_nan(top, fabsf(h));
+            chunk_top = max_nan(chunk_top, fabsf(h));
           }
+          if (col + c < args.I) top = max_nan(top, chunk_top);
           tmem_st_32x32b_x16(tacc + c, g);
         }
         tmem_st_wait();
@@ -599,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         top = max_nan(top, mine[(1 - wg) * kBlockM + row]);
         const Reciprocal s = reciprocal(e5 ? block_scale<true>(top) : block_scale<false>(top));
         if (row_ok && wg == 0) args.sQ[size_t(m) * ceil_div(args.I, kBlockK) + col / kBlockK] = s.s;
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; c < 64; c += 16) {
           uint32_t r[16];
           tmem_ld_32x32b_x16(tacc + c, r);
