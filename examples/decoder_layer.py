@@ -4,14 +4,17 @@
 
 Serving, for a batch of sequences with a paged FP8 cache:
 
-    norm (8-bit output) -> QKV product -> append to the cache -> attention ->
+    norm (8-bit output) -> QKV product -> rotary positions -> append to the cache -> attention ->
     output product -> residual + norm (8-bit output) -> router -> mixture of experts
 
-Training, for the norm and the linear layer behind it: the output's gradient in
-e5m2 -> product with the transposed weight -> the norm's gradient.
+(prompts attend a chunk of tokens at a time, single tokens by the other call).
 
-Weights are random; positions are not encoded (a rotary embedding would go between
-the QKV product and the append).
+Training, for the norm and the linear layer behind it: the output's gradient in
+e5m2 -> product with the transposed weight -> the norm's gradient; and for a gated
+feed-forward block: gate and up products with SwiGLU -> down product, and back
+through both.
+
+Weights are random.
 """
 
 import argparse
@@ -23,6 +26,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from fp8_fine_grained_e4m3_gb300 import binding as fp8  # noqa: E402
+from fp8_fine_grained_e4m3_gb300 import rotary  # noqa: E402
 
 BF16 = torch.bfloat16
 
@@ -54,7 +58,9 @@ class Cache:
 
 
 class Layer:
-    def __init__(self, hidden, heads, group, dim, experts, expert_hidden, top_k, seed=0):
+    def __init__(self, hidden, heads, group, dim, experts, expert_hidden, top_k, seed=0, positions=None):
+        """positions: rotary.frequencies' result, or None for none."""
+        self.positions = positions
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
 
@@ -90,8 +96,12 @@ class Layer:
         nq, nk = self.group * self.heads, self.heads
         q, k, v = (t.unflatten(1, (-1, self.dim)) for t in qkv.split(
             [nq * self.dim, nk * self.dim, nk * self.dim], dim=1))
+        if self.positions is not None:  # in place: parts of the product's rows
+            freq, amplitude = self.positions
+            fp8.fp8_rope(q, k, freq, seq_lens=cache.lens, cu=cu, amplitude=amplitude, Qo=q, Ko=k)
         fp8.fp8_kv_append(k, v, *cache.tensors(), cu_new=cu, max_new=most)
-        o = fp8.fp8_kv_attention(q, *cache.tensors(), cu_q=cu, max_q=most)
+        attend = fp8.fp8_kv_attention if cu is None else fp8.fp8_kv_attention_chunk
+        o = attend(q, *cache.tensors(), cu_q=cu, max_q=most)
         o8, so = fp8.fp8_quant_1x128(o.view(T, -1).float())
         y = fp8.fp8gemm_dense(o8, so, *self.out)
         A, sA, stream, rstd = fp8.fp8_rmsnorm_quant(y, self.gain2, residual=stream)
@@ -113,13 +123,32 @@ def norm_linear_backward(dy, dh, saved, gain, wt8, swt):
     return fp8.fp8_rmsnorm_backward(dnorm, h, rstd, gain, dH=dh)
 
 
+def gated_ffn(A, sA, w1, w2):
+    """y = (silu(gate) up) W2^T of A's rows in FP8, w1 and w2 (codes, scales) of [gate; up] and
+    W2 -> y bf16 and what the gradient needs."""
+    GU = torch.empty((A.shape[0], w1[0].shape[0]), dtype=BF16, device=A.device)
+    h, sh = fp8.fp8gemm_gated(A, sA, *w1, GU=GU)
+    return fp8.fp8gemm_dense(h, sh, *w2), GU
+
+
+def gated_ffn_backward(dy, GU, w1t, w2t):
+    """Gradients of A's rows (bf16) and of gate and up values (bf16) from dy: w2t is W2
+    transposed, w1t [hidden, 2 Ip] is [gate; up] transposed, each half in columns of its own
+    (Ip: its width up to a multiple of 128)."""
+    g8, sg = fp8.fp8_quant_1x128_fmt(dy.float(), "e5m2")
+    dGU = torch.empty_like(GU)
+    d8, sd = fp8.fp8gemm_gated_backward(g8, sg, *w2t, GU, dGU=dGU)
+    return fp8.fp8gemm_dense_fmt(d8, sd, "e5m2", *w1t, "e4m3"), dGU
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--hidden", type=int, default=2048)
     ap.add_argument("--prompts", type=int, nargs="+", default=[37, 5, 130, 64])
     ap.add_argument("--steps", type=int, default=4)
     a = ap.parse_args()
-    layer = Layer(a.hidden, heads=4, group=4, dim=128, experts=16, expert_hidden=1024, top_k=2)
+    layer = Layer(a.hidden, heads=4, group=4, dim=128, experts=16, expert_hidden=1024, top_k=2,
+                  positions=rotary.frequencies(128, scaling="parts", factor=4.0, trained=8192))
     B = len(a.prompts)
     cache = Cache(64, 4, 64, 128, B, 16)
     T = sum(a.prompts)
@@ -140,6 +169,13 @@ def main():
     dx, dgain = norm_linear_backward(dy, dh, saved, layer.gain1, *fp8.fp8_quant_128x128(w.t().contiguous()))
     print(f"training step: output {tuple(out.shape)}, input gradient {tuple(dx.shape)}, gain gradient "
           f"rms {dgain.square().mean().sqrt():.3f}")
+    up = torch.randn((2 * 640, a.hidden), device="cuda") / math.sqrt(a.hidden)
+    down = torch.randn((a.hidden, 640), device="cuda") / math.sqrt(640)
+    w1, w2, w1t, w2t = (fp8.fp8_quant_128x128(w.contiguous()) for w in (up, down, up.t(), down.t()))
+    y, GU = gated_ffn(*fp8.fp8_quant_1x128(x.float()), w1, w2)
+    dx, dGU = gated_ffn_backward(dh, GU, w1t, w2t)
+    print(f"feed-forward block: output {tuple(y.shape)}, input gradient {tuple(dx.shape)}, gate and up gradients rms "
+          f"{dGU.float().square().mean().sqrt():.3f}")
     assert fp8.fp8gemm_get_device_status() == fp8.OK
 
 
