@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (unset && top > -INFINITY) {
-              ref = ceilf(top - kLift);
+              ref = top - kLift;  // the largest P a power of two, which FP16 holds exactly
               unset = false;
             }
           }
@@ -580,8 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             float up = 0.f;
             if (most > kMostP) up = float(int(__float_as_uint(most) >> 23) - 127) - kLift;
             const float to = ref + up;
-            plain = !__any_sync(0xffffffffu, most == INFINITY || to - ref != up);
+            plain = !__any_sync(0xffffffffu, most == INFINITY || !(to - ref > up - 1.f));
             if (plain) {
+              up = to - ref;
               ref = to;
               if (!(ok = rescale(exp2_fast(-up)))) break;
             }
@@ -639,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               // by how much the reference rises; the first score that is there sets it
               float up = 0.f, shrink = 1.f;
               if (!unset) {
-                const float to = ref + fmaxf(ceilf(top - kLift), 0.f);
+                const float to = ref + fmaxf(top - kLift, 0.f);
                 up = to - ref;
                 shrink = exp2_fast(-up);
                 ref = to;
               } else if (top > -INFINITY) {
-                ref = ceilf(top - kLift);
+                ref = top - kLift;
                 unset = false;
               }
               if (h > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {  // P of the tile's tokens before these
