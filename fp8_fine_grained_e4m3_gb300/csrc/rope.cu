@@ -10,7 +10,12 @@
 // [-1, 1] there; its sine and cosine are FP32's (sincospi, 1 to 2 ulp).  That is ten FP64
 // operations for a pair of a token, shared by all heads of the token through shared memory.
 //
-// Bound by memory: every element is read and written once, 16 bytes a lane.
+// Bound by memory: every element is read and written once, 16 bytes a lane.  9700 tokens of 64 + 8
+// BF16 heads of 128 take 62 us, 86 % of what a plain copy reaches; the gradient of 7800 tokens of
+// 32 + 8 such heads, 64 elements of each in neighbouring pairs, 29 us (82 %).  CTAs of 128
+// threads and two tokens, the first loads under way before the position is looked up: CTAs of 256
+// threads and eight tokens took 64 and 32 us, two units in flight a thread 64 and 31 (more registers,
+// fewer threads).  A step of 64 tokens is one chain of latencies, 3.7 us.
 #include "common.cuh"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
@@ -19,9 +24,9 @@
 namespace fp8gemm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTokens = 8;  // of a CTA: a warp looks up each one's position
+constexpr int kMaxTokens = 2;  // of a CTA: a warp looks up each one's position
 constexpr int kMaxPairs = kMaxRopeDim / 2;
 
 // A token's position; false where it has none (its rows are then left as they are).
@@ -62,8 +67,9 @@ template <class T>
 struct Unit {  // 16 elements of a head: the two halves of 8 pairs, or 8 pairs (or none) in a row
   const T* x;
   T* y;
-  int gap;   // from the first eight elements to the second eight
-  int pair;  // first pair in the CTA's table, -1: to be copied, -2: nothing to do
+  int gap;    // from the first eight elements to the second eight
+  int pair;   // first pair in the CTA's table, -1: to be copied, -2: nothing to do
+  int token;  // of the CTA
 };
 
 template <class T, bool kInterleaved>
@@ -98,7 +104,7 @@ __device__ __forceinline__ void turn(const Raw8<T>& r0, const Raw8<T>& r1, const
 // CTA (x, y): tokens x tokens .. + tokens - 1, the y-th of gridDim.y shares of their heads' units.
 template <class T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tokens, int* status) {
-  __shared__ float2 cs[kMaxTokens * 32 > kMaxPairs ? kMaxTokens * 32 : kMaxPairs];
+  __shared__ float2 cs[kThreads > kMaxPairs ? kThreads : kMaxPairs];
   __shared__ int pos[kMaxTokens];
   __shared__ bool has[kMaxTokens];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -106,6 +112,45 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
   const int pairs = a.rot / 2;
   griddep_launch_dependents();
   griddep_wait();
+  const int U = a.dim / 16, per_token = (a.heads_q + a.heads_k) * U;
+  const int end = n_tok * per_token, step = gridDim.y * kThreads;
+  auto unit = [&](int u) {
+    Unit<T> r = {nullptr, nullptr, 0, -2, 0};
+    if (u >= end) return r;
+    const int k = u / per_token;
+    u -= k * per_token;
+    int h = u / U;
+    const int c = u - h * U;
+    const bool key = h >= a.heads_q;
+    if (key) h -= a.heads_q;
+    const long long t = t_first + k;
+    const T* x = static_cast<const T*>(key ? a.K : a.Q) + t * (key ? a.ld_k : a.ld_q) + h * a.dim;
+    T* y = static_cast<T*>(key ? a.Ko : a.Qo) + t * (key ? a.ld_ko : a.ld_qo) + h * a.dim;
+    const bool turned = 16 * c < a.rot;
+    if (!turned && x == y) return r;
+    const bool half = turned && !kInterleaved;
+    r.x = x + (half ? 8 : 16) * c;
+    r.y = y + (half ? 8 : 16) * c;
+    r.gap = half ? pairs : 8;
+    r.pair = turned ? k * pairs + 8 * c : -1;
+    r.token = k;
+    return r;
+  };
+  // The next unit's elements are asked for before this one's are stored; the first unit's do not
+  // wait for the positions and the angles.
+  Unit<T> next;
+  Raw8<T> r0, r1;
+  auto ask = [&](int u) {
+    next = unit(u);
+    zero8(r0);
+    zero8(r1);
+    if (next.pair != -2) {
+      r0 = load8(next.x);
+      r1 = load8(next.x + next.gap);
+    }
+  };
+  int u = blockIdx.y * kThreads + threadIdx.x;
+  ask(u);
   if (warp < n_tok) {
     int p = 0;
     const bool ok = token_position(a, t_first + warp, lane, status, &p);
@@ -127,64 +172,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
     cs[i] = make_float2(a.amplitude * c, a.backward ? -a.amplitude * s : a.amplitude * s);
   }
   __syncthreads();
-  const int U = a.dim / 16, per_token = (a.heads_q + a.heads_k) * U;
-  auto unit = [&](int u) {
-    Unit<T> r = {nullptr, nullptr, 0, -2};
-    const int k = u / per_token;
-    if (k >= n_tok || !has[k]) return r;
-    u -= k * per_token;
-    int h = u / U;
-    const int c = u - h * U;
-    const bool key = h >= a.heads_q;
-    if (key) h -= a.heads_q;
-    const long long t = t_first + k;
-    const T* x = static_cast<const T*>(key ? a.K : a.Q) + t * (key ? a.ld_k : a.ld_q) + h * a.dim;
-    T* y = static_cast<T*>(key ? a.Ko : a.Qo) + t * (key ? a.ld_ko : a.ld_qo) + h * a.dim;
-    const bool turned = 16 * c < a.rot;
-    if (!turned && x == y) return r;
-    const bool half = turned && !kInterleaved;
-    r.x = x + (half ? 8 : 16) * c;
-    r.y = y + (half ? 8 : 16) * c;
-    r.gap = half ? pairs : 8;
-    r.pair = turned ? k * pairs + 8 * c : -1;
-    return r;
-  };
-  const int end = n_tok * per_token;
-  constexpr int kAhead = 2;  // units whose loads a thread has in flight
-  for (int u = blockIdx.y * kThreads + threadIdx.x; u < end; u += kAhead * gridDim.y * kThreads) {
-    Unit<T> w[kAhead];
-    Raw8<T> r0[kAhead], r1[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      w[j] = unit(u + j * int(gridDim.y) * kThreads);
-      zero8(r0[j]);
-      zero8(r1[j]);
-      if (w[j].pair != -2) {
-        r0[j] = load8(w[j].x);
-        r1[j] = load8(w[j].x + w[j].gap);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (w[j].pair == -2) continue;
-      if (w[j].pair >= 0) turn<T, kInterleaved>(r0[j], r1[j], cs + w[j].pair, r0[j], r1[j]);
-      store8(w[j].y, r0[j]);
-      store8(w[j].y + w[j].gap, r1[j]);
-    }
+  for (; u < end; u += step) {
+    const Unit<T> v = next;
+    Raw8<T> x0 = r0, x1 = r1;
+    ask(u + step);
+    if (v.pair == -2 || !has[v.token]) continue;
+    if (v.pair >= 0) turn<T, kInterleaved>(x0, x1, cs + v.pair, x0, x1);
+    store8(v.y, x0);
+    store8(v.y + v.gap, x1);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const LaunchCtx& c, const RopeArgs& a) {
-  // As many tokens as give each thread an angle, where that still leaves a CTA or more an SM; with
-  // few tokens one each, its heads shared by several CTAs.
+  // Two tokens a CTA where that leaves two CTAs or more an SM; with few tokens one each, its heads
+  // shared by as many CTAs as give an SM two (one: 3.9 us for a step of 64 tokens, two: 3.7).
   int tokens = min(kMaxTokens, max(1, kThreads / (a.rot / 2)));
   while (tokens > 1 && ceil_div(a.T, tokens) < 2 * c.num_sms) tokens /= 2;
   const int grid_x = ceil_div(a.T, tokens);
   const long long units = (long long)tokens * (a.heads_q + a.heads_k) * (a.dim / 16);
   const long long most = (units + kThreads - 1) / kThreads;
-  const int grid_y = int(max(1LL, min(most, (long long)c.num_sms / grid_x)));
+  const int grid_y = int(max(1LL, min(most, 2LL * c.num_sms / grid_x)));
   auto fn = a.f32 ? (a.interleaved ? rope_kernel<float, true> : rope_kernel<float, false>)
                   : (a.interleaved ? rope_kernel<__nv_bfloat16, true> : rope_kernel<__nv_bfloat16, false>);
   return launch_dependent(c, fn, dim3(grid_x, grid_y), kThreads, 0, a, tokens, c.status);
