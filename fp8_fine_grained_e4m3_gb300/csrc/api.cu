@@ -690,10 +690,13 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
   return finish(launch_kv_attention(c, a, ws), 1);
 }
 
+// Counts that are rounded up to tiles in 32 bits.
+constexpr int kMostIndex = 0x7fffff00;
+
 // What the gated products' two calls have in common (rows of B: 2 I or I).
 static int check_gated(int M, int I, int K, int a_fmt, int b_fmt, int q_fmt) {
   if (int r = check_common(M, I, K)) return r;
-  if (I == 0 || I % kKAlign != 0 || I > (1 << 29)) return FP8GEMM_ERR_SHAPE;
+  if (I == 0 || I % kKAlign != 0 || I > (1 << 29) || M > kMostIndex) return FP8GEMM_ERR_SHAPE;
   if ((long long)ceil_div(M, kBlockM) * ceil_div(I, kBlockK) > 0x3fffffffLL) return FP8GEMM_ERR_SHAPE;
   if (!valid_fmt(a_fmt) || !valid_fmt(b_fmt) || !valid_fmt(q_fmt)) return FP8GEMM_ERR_FORMAT;
   return FP8GEMM_OK;
@@ -735,7 +738,8 @@ int fp8_rope(const void* Q, int64_t ld_q, const void* K, int64_t ld_k, int x_typ
              int64_t ld_qo, void* Ko, int64_t ld_ko, const float* freq, const int32_t* positions,
              const int32_t* seq_lens, const int32_t* cu, float amplitude, int T, int B, int heads_q,
              int heads_k, int dim, int rot, int interleaved, int backward, fp8gemm_stream_t stream) {
-  if (T < 0 || B < 0 || heads_q < 0 || heads_k < 0 || heads_q > 65535 || heads_k > 65535)
+  if (T < 0 || T > kMostIndex || B < 0 || B > (1 << 30) || heads_q < 0 || heads_k < 0 || heads_q > 65535 ||
+      heads_k > 65535)
     return FP8GEMM_ERR_SHAPE;
   if (dim <= 0 || dim % 16 != 0 || dim > kMaxRopeDim || rot <= 0 || rot % 16 != 0 || rot > dim)
     return FP8GEMM_ERR_SHAPE;
@@ -746,6 +750,8 @@ int fp8_rope(const void* Q, int64_t ld_q, const void* K, int64_t ld_k, int x_typ
     if (ld % 8 != 0 || ld < int64_t(heads_q) * dim) return FP8GEMM_ERR_SHAPE;
   for (int64_t ld : {heads_k ? ld_k : int64_t(0), heads_k ? ld_ko : int64_t(0)})
     if (ld % 8 != 0 || ld < int64_t(heads_k) * dim) return FP8GEMM_ERR_SHAPE;
+  if (T > 1 && ((heads_q && Q == Qo && ld_q != ld_qo) || (heads_k && K == Ko && ld_k != ld_ko)))
+    return FP8GEMM_ERR_SHAPE;
   if (!freq || (heads_q && (!Q || !Qo)) || (heads_k && (!K || !Ko)) || (!positions && !seq_lens))
     return FP8GEMM_ERR_NULL;
   if ((heads_q && (!aligned16(Q) || !aligned16(Qo))) || (heads_k && (!aligned16(K) || !aligned16(Ko))) ||
@@ -767,8 +773,8 @@ int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, 
                            fp8gemm_stream_t stream) {
   if (int r = check_cache(T, B, heads, dim, block, table_width, num_blocks, max_q, cu_q, fmt))
     return r;
-  if (group < 0 || (long long)heads * group > 65535 || (long long)max_q * group > 0x7fffffffLL ||
-      (long long)T * group > 0x7fffffffLL || (long long)table_width * block > 0x7fffffffLL)
+  if (group < 0 || (long long)heads * group > 65535 || (long long)max_q * group > kMostIndex ||
+      (long long)T * group > kMostIndex || (long long)table_width * block > kMostIndex)
     return FP8GEMM_ERR_SHAPE;
   if (T == 0 || B == 0 || heads == 0 || group == 0 || max_q == 0) return FP8GEMM_OK;
   if (ld_q < int64_t(heads) * group * dim || ld_q % 8 != 0) return FP8GEMM_ERR_SHAPE;

@@ -943,13 +943,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (un >= units_of(a, s.n)) break;  // (cannot be: the offset lies in the sequence)
         }
         while (at < hi && ok) {
-          while (un >= units_of(a, s.n)) {  // on to the next sequence, or the next head's list
+          while (un >= units_of(a, s.n)) {  // on to the next sequence that has tokens, or the next head's list
             un = 0;
-            if (++b == a.B) {
-              b = 0;
+            const Seq next = sequence(a, b + 1 + lane, status);  // (none behind the last)
+            const uint32_t some = __ballot_sync(0xffffffffu, next.n > 0);
+            const int l = some ? __ffs(some) - 1 : 31;
+            s.t0 = __shfl_sync(0xffffffffu, next.t0, l);
+            s.n = __shfl_sync(0xffffffffu, next.n, l);
+            s.len = __shfl_sync(0xffffffffu, next.len, l);
+            b += 1 + l;
+            if (b >= a.B) {
+              b = -1;
+              s.n = 0;
               ++head;
             }
-            s = sequence(a, b, status);
           }
           const int tiles = unit_tiles(a, s.len, s.n, un);
           const long long cost = tiles + kUnitCost, begin = at - off;

@@ -54,12 +54,12 @@ __device__ __forceinline__ bool token_position(const RopeArgs& a, int t, int lan
     b = t / n;
     t0 = b * n;
   }
-  const int start = a.lens[b] - n;
-  if (start < 0) {
+  const int len = a.lens[b];
+  if (len < n) {
     if (lane == 0) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
     return false;
   }
-  *pos = start + t - t0;
+  *pos = len - n + t - t0;
   return true;
 }
 

@@ -52,7 +52,9 @@
  *    counters (and order) in small per-stream buffers; fp8_rmsnorm_backward
  *    (10 MB), fp8_kv_attention (8 MB), fp8_kv_attention_chunk (42 MB) and
  *    fp8_moe_few (60 MB + 1 KB for each element of I) keep theirs the same way.
- *    Such a first call must therefore not happen during CUDA graph capture.
+ *    Such a first call must therefore not happen during CUDA graph capture, and
+ *    graphs that captured such calls on one stream share its workspace: their
+ *    replays follow one another.
  *    Calls on different streams never share a workspace.  Host threads may
  *    call at the same time, on one stream too: a call that needs a workspace
  *    holds a lock of its stream until its last kernel is enqueued.  The reduction
@@ -589,11 +591,20 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  *
  * Layouts, cache, index arrays, refusals and what the status word says are those of
  * fp8_kv_attention; a query that sees no token gives zeros.  Rows of O that belong to no
- * sequence are left as they were.  T * group, max_q * group and table_width * block below 2^31.
+ * sequence are left as they were.  T * group, max_q * group and table_width * block at most
+ * 2^31 - 256.
  *
  * Work is shared out evenly over the SMs whatever the lengths; parts of a sequence's rows are
  * joined through a per-(device, stream) workspace of one size for all calls.  Results are
  * deterministic for given host sizes, lengths and offsets.
+ *
+ * Arithmetic: products of FP16 operands (codes and queries are exact in it, the queries after a shift
+ * of each by a power of two) and FP32 sums.  A key block's scale acts on the product of query and
+ * codes.  A softmax weight times its value block's |scale| has FP16's 11 bits down to 2^-19 of the
+ * row's largest such term, fewer bits below, and counts as 0 below 2^-30 of it; the weights' sum
+ * is exact to FP32 as long as the scales of the blocks that a row sees lie within a factor
+ * of 2^64 of each other.  Value scales below 2^-126 count as 0.  An infinity among values or value
+ * scales counts as NaN, and what is not finite reaches the queries that see its token, and no others.
  */
 int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
                            const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
@@ -616,7 +627,7 @@ int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, 
  *   s1  f32 [ceil(2 I/128), ceil(K/128)]
  *   Q   u8 [M, I] of q_fmt, sQ f32 [M, ceil(I/128)] (outputs)
  *   GU  bf16 [M, 2 I]: u, rounded, for fp8gemm_gated_backward; or NULL: not wanted
- *   I and K positive multiples of 16, I at most 2^29; alignment 16 bytes.
+ *   I and K positive multiples of 16, I at most 2^29, M at most 2^31 - 256; alignment 16 bytes.
  */
 int fp8gemm_gated(const uint8_t* A, const float* sA, int a_fmt, const uint8_t* W1, const float* s1,
                   int b_fmt, uint8_t* Q, float* sQ, int q_fmt, void* GU, int M, int I, int K,
@@ -668,7 +679,8 @@ int fp8gemm_gated_backward(const uint8_t* dY, const float* sdY, int a_fmt, const
  *          Rows that belong to no sequence are left as they were.  Offsets that fall or leave
  *          0 .. T and lengths below a sequence's new tokens set FP8GEMM_ERR_DEVICE_STATUS; the
  *          rows concerned are left as they were.
- *   dim a multiple of 16 up to 512, rot a multiple of 16 up to dim, heads up to 65535.
+ *   dim a multiple of 16 up to 512, rot a multiple of 16 up to dim, heads up to 65535, T up to
+ *   2^31 - 256, B up to 2^30.
  *   Alignment: 16 bytes (freq, positions, seq_lens, cu 4).
  */
 int fp8_rope(const void* Q, int64_t ld_q, const void* K, int64_t ld_k, int x_type, void* Qo,

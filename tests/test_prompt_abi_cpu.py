@@ -231,3 +231,21 @@ def test_frequencies_refuses():
                dict(rot=2, scaling="base"), dict(rot=8, scaling="parts"), dict(rot=8, scaling="parts", trained=9, fast=1.0)):
         with pytest.raises(ValueError):
             rotary.frequencies(device="cpu", **kw)
+
+
+MOST = 0x7fffff00
+
+
+@pytest.mark.parametrize("call,kw,code", [
+    # counts that would pass 2^31 when they are rounded up to tiles
+    (_rope, dict(T=MOST + 1, pos=GOOD), "SHAPE"), (_rope, dict(B=(1 << 30) + 1), "SHAPE"),
+    (_gated, dict(M=MOST + 1, I=16, K=16), "SHAPE"), (_back, dict(M=MOST + 1, I=16, K=16), "SHAPE"),
+    (_chunk, dict(T=MOST // 4 + 1), "SHAPE"), (_chunk, dict(most=MOST // 4 + 1), "SHAPE"),
+    (_chunk, dict(width=MOST // 64 + 1), "SHAPE"),
+    # in place, but rows of the output elsewhere than the input's
+    (_rope, dict(ld_qo=264), "SHAPE"), (_rope, dict(ld_k=136), "SHAPE"),
+    (_rope, dict(ld_k=136, hk=0, T=0), "OK"),
+])
+def test_limits_of_counts_and_turning_in_place(lib, call, kw, code):
+    from fp8_fine_grained_e4m3_gb300 import binding
+    assert call(lib, **kw) == getattr(binding, "OK" if code == "OK" else f"ERR_{code}")
