@@ -275,7 +275,7 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* tile, int row, int c) {
 template <int kDim>
 __device__ __forceinline__ void request_queries(uint8_t* tile, int row, int lane, const __nv_bfloat16* Q, long long at) {
   constexpr int kChunks = kDim / 8, kRowsAtOnce = 32 / kChunks;
-#pragma unroll 4
+#pragma unroll 2
   for (int y = 0; y < 32; y += kRowsAtOnce) {
     const int from = y + lane / kChunks;
     const long long q = __shfl_sync(0xffffffffu, at, from);
@@ -289,7 +289,7 @@ __device__ __forceinline__ float stage_queries(uint8_t* tile, int row) {
   cp_async_wait_all();
   __syncwarp();
   uint32_t top2 = 0u;  // of the even elements and of the odd ones: magnitudes of BF16 order as whole numbers do
-#pragma unroll 4
+#pragma unroll 2
   for (int c = 0; c < kChunks; ++c) {
     const uint4 v = *reinterpret_cast<const uint4*>(chunk_at<kDim>(tile, row, c));
     top2 = __vmaxu2(__vmaxu2(__vmaxu2(top2, v.x & 0x7fff7fffu), __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu)),
@@ -299,7 +299,7 @@ __device__ __forceinline__ float stage_queries(uint8_t* tile, int row) {
   // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
   const int exp = max(int(top >> 7), 10);
   const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
-#pragma unroll 4
+#pragma unroll 2
   for (int c = 0; c < kChunks; ++c) {
     uint4* p = reinterpret_cast<uint4*>(chunk_at<kDim>(tile, row, c));
     float f[8];
@@ -308,6 +308,26 @@ __device__ __forceinline__ float stage_queries(uint8_t* tile, int row) {
                     f16x2_bits(f[4] * up, f[5] * up), f16x2_bits(f[6] * up, f[7] * up));
   }
   return __uint_as_float(uint32_t(exp - 10) << 23);
+}
+
+// Piece y of lane x of four becomes piece x of lane y, after kBit = 1 and 2.
+template <int kBit>
+__device__ __forceinline__ void exchange(uint4 (&w)[4], int lane) {
+  const bool high = lane & kBit;
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    uint4& lo = w[kBit == 1 ? 2 * p : p];
+    uint4& hi = w[kBit == 1 ? 2 * p + 1 : p + 2];
+    uint4 send = high ? lo : hi;
+    send.x = __shfl_xor_sync(0xffffffffu, send.x, kBit);
+    send.y = __shfl_xor_sync(0xffffffffu, send.y, kBit);
+    send.z = __shfl_xor_sync(0xffffffffu, send.z, kBit);
+    send.w = __shfl_xor_sync(0xffffffffu, send.w, kBit);
+    if (high)
+      lo = send;
+    else
+      hi = send;
+  }
 }
 
 // Bits of the bytes of a word that are no finite number (0xff in each).
@@ -462,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seq_row = u->row0 + r;
       const int limit = row_ok ? row_limit(a, u->len, u->n, seq_row) : 0x7fffffff;
       const int least = __shfl_sync(0xffffffffu, limit, 0);  // rows see more and more
-      const int most_seen = u->vis;
+      const int most_seen = __reduce_max_sync(0xffffffffu, row_ok ? limit : 0);  // by a row of the warp
       float ref = 0.f, sum = 0.f, vref = 1.f;  // sum: of p over vref's share of |v_scale|
       bool unset = true;
       if (j1 > j0) {
@@ -701,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
       }
       const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
-      __nv_bfloat16* out = a.O + ((long long)(u->t0 + seq_row / a.group) * a.heads * a.group + u->head * a.group +
-                                  seq_row % a.group) * kDim;
+      const long long out = !row_ok ? -1 : ((long long)(u->t0 + seq_row / a.group) * a.heads * a.group +
+                                      u->head * a.group + seq_row % a.group) * kDim;
       // parts: [kDim / 4][rows][4], then [rows][4], so that neighbouring lanes write neighbouring places
       float4* part = reinterpret_cast<float4*>(parts) +
                      (size_t(blockIdx.x) * 2 + (kind == kFirst)) * (kUnitRows * (kDim / 4 + 1)) + r;
@@ -713,18 +733,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(o_at + d, o);
           tmem_ld_wait_tied(o);
         }
-        if (!row_ok) {
-        } else if (kind == kWhole) {
+        if (kind == kWhole) {
+          // four lanes exchange their rows' pieces so that they write 64 bytes of a row together (16 bytes a
+          // row from each lane took as long as the rest of a unit's end)
+          uint4 w[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
+          for (int e = 0; e < 4; ++e) {
             float v[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(o[e + y]) * f * vref;
-            Raw8<__nv_bfloat16> w;
-            pack8(v, w);
-            store8(out + d + e, w);
+            for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(o[8 * e + y]) * f * vref;
+            w[e] = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
           }
-        } else {
+          exchange<1>(w, lane);
+          exchange<2>(w, lane);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const long long at = __shfl_sync(0xffffffffu, out, (lane & ~3) + y);
+            if (at >= 0) *reinterpret_cast<uint4*>(a.O + at + d + 8 * (lane & 3)) = w[y];
+          }
+        } else if (row_ok) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             part[size_t(d + e) / 4 * kUnitRows] =
@@ -796,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (bad) ring(tab.slot)->bad = 1;
         }
         uint8_t* tile = smem + (v ? S::kV : S::kK) + st * S::kTileBytes;
-#pragma unroll
+#pragma unroll 1
         for (int l0 = 0; l0 < kLoads; l0 += 4) {
           uint4 x[4];
 #pragma unroll
@@ -1141,7 +1168,7 @@ __global__ void __launch_bounds__(kUnitRows) kv_chunk_join_kernel(const __grid_c
   auto part = [&](int p) { return parts + (size_t(blockIdx.x + p) * 2 + (p == 0)) * kSlot + r; };
   auto stat = [&](int p) { return part(p)[size_t(kUnitRows) * (kDim / 4)]; };
   float top = -INFINITY;
-#pragma unroll 4
+#pragma unroll 2
   for (int p = 0; p < s.parts; ++p) top = max_nan(top, stat(p).x);
   const float vref = stat(0).z;
   float4 o[kJoinDims / 4] = {};

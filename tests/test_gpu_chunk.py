@@ -286,3 +286,14 @@ def test_same_bits_on_every_run_in_a_graph_and_after_larger_calls():
         assert torch.equal(got, b.fp8_kv_attention_chunk(qs, *ts))
     b.fp8gemm_release_workspaces(s)
     assert b.fp8gemm_get_device_status() == b.OK
+
+
+def test_padded_batch_and_rows_of_one_warp():
+    # empty sequences before, between and behind the others, in runs longer than a warp; causal rows whose warps see
+    # ever more of a tile, one of them with a single row
+    counts = [0] * 40 + [1] + [0] * 33 + [130] + [0] * 64 + [33, 0, 257] + [0] * 35
+    lens = [0 if n == 0 else n + 3 * n % 50 for n in counts]
+    c = Cache(lens, 3, 64, 32, "e4m3", seed=12).stale()
+    for group in (1, 3):
+        O, Q, cu = _run(c, _queries(sum(counts), 3 * group, 64, group), counts)
+        _check(O, c, Q, cu)

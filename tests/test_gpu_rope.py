@@ -143,3 +143,18 @@ def test_bad_offsets_and_lengths_set_the_status():
     b.fp8_rope(q[:0], None, f, seq_lens=i32())
     b.fp8_rope(q, None, f, seq_lens=i32(1, 1), cu=i32(0, 0, 0))  # no sequence has a token
     assert b.fp8gemm_get_device_status() == b.OK
+
+
+def test_lengths_at_the_types_end():
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    q = torch.ones((6, 1, 32), device="cuda")
+    f = dev(_freq(32))
+    lens = dev(np.array([-2 ** 31, 2 ** 31 - 1], np.int32))
+    cu = dev(np.array([0, 3, 6], np.int32))
+    out = torch.full_like(q, 5.0)
+    b.fp8_rope(q, None, f, seq_lens=lens, cu=cu, Qo=out)  # the first has fewer tokens than new ones
+    assert b.fp8gemm_get_device_status() == b.ERR_DEVICE_STATUS
+    assert bool((out[:3] == 5).all())
+    same = b.fp8_rope(q[3:], None, f, positions=dev(np.array([2 ** 31 - 4, 2 ** 31 - 3, 2 ** 31 - 2], np.int32)))[0]
+    assert torch.equal(out[3:], same)
