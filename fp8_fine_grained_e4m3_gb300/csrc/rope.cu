@@ -11,11 +11,11 @@
 // operations for a pair of a token, shared by all heads of the token through shared memory.
 //
 // Bound by memory: every element is read and written once, 16 bytes a lane.  9700 tokens of 64 + 8
-// BF16 heads of 128 take 62 us, 86 % of what a plain copy reaches; the gradient of 7800 tokens of
+// BF16 heads of 128 take 61 us, 87 % of what a plain copy reaches; the gradient of 7800 tokens of
 // 32 + 8 such heads, 64 elements of each in neighbouring pairs, 29 us (82 %).  CTAs of 128
 // threads and two tokens, the first loads under way before the position is looked up: CTAs of 256
 // threads and eight tokens took 64 and 32 us, two units in flight a thread 64 and 31 (more registers,
-// fewer threads).  A step of 64 tokens is one chain of latencies, 3.7 us.
+// fewer threads).  A step of 64 tokens is one chain of latencies, 3.6 us.
 #include "common.cuh"
 #include "kv_cache.cuh"
 #include "ptx.cuh"
@@ -68,20 +68,27 @@ struct Unit {  // 16 elements of a head: the two halves of 8 pairs, or 8 pairs (
   const T* x;
   T* y;
   int gap;    // from the first eight elements to the second eight
-  int pair;   // first pair in the CTA's table, -1: to be copied, -2: nothing to do
+  int pair;   // first two pairs in the CTA's table, -1: to be copied, -2: nothing to do
   int token;  // of the CTA
 };
 
 template <class T, bool kInterleaved>
-__device__ __forceinline__ void turn(const Raw8<T>& r0, const Raw8<T>& r1, const float2* cs, Raw8<T>& o0,
+__device__ __forceinline__ void turn(const Raw8<T>& r0, const Raw8<T>& r1, const float4* cs, int gap, Raw8<T>& o0,
                                      Raw8<T>& o1) {
+  float2 t[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = cs[i * gap];
+    t[2 * i] = make_float2(v.x, v.y);
+    t[2 * i + 1] = make_float2(v.z, v.w);
+  }
   float a[8], b[8];
   unpack8(r0, a);
   unpack8(r1, b);
   if constexpr (kInterleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 p = cs[i], q = cs[i + 4];
+      const float2 p = t[i], q = t[i + 4];
       const float u = a[2 * i], v = b[2 * i];
       a[2 * i] = fmaf(u, p.x, -(a[2 * i + 1] * p.y));
       a[2 * i + 1] = fmaf(a[2 * i + 1], p.x, u * p.y);
@@ -91,7 +98,7 @@ __device__ __forceinline__ void turn(const Raw8<T>& r0, const Raw8<T>& r1, const
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 p = cs[i];
+      const float2 p = t[i];
       const float u = a[i];
       a[i] = fmaf(u, p.x, -(b[i] * p.y));
       b[i] = fmaf(b[i], p.x, u * p.y);
@@ -104,7 +111,9 @@ __device__ __forceinline__ void turn(const Raw8<T>& r0, const Raw8<T>& r1, const
 // CTA (x, y): tokens x tokens .. + tokens - 1, the y-th of gridDim.y shares of their heads' units.
 template <class T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int tokens, int* status) {
-  __shared__ float2 cs[kThreads > kMaxPairs ? kThreads : kMaxPairs];
+  // cos and sin, two pairs an entry: entries j of all of a token's units of 8 pairs lie in a row, so that
+  // neighbouring lanes' units meet all banks
+  __shared__ float4 cs[(kThreads > kMaxPairs ? kThreads : kMaxPairs) / 2];
   __shared__ int pos[kMaxTokens];
   __shared__ bool has[kMaxTokens];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -132,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
     r.x = x + (half ? 8 : 16) * c;
     r.y = y + (half ? 8 : 16) * c;
     r.gap = half ? pairs : 8;
-    r.pair = turned ? k * pairs + 8 * c : -1;
+    r.pair = turned ? k * (pairs / 2) + c : -1;
     r.token = k;
     return r;
   };
@@ -161,15 +170,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_tok * pairs; i += kThreads) {
-    const int k = i / pairs;
+    const int k = i / pairs, p = i - k * pairs;
     // 1 / pi in two parts: a position of 2^31 would lose 2^-21 of a turn in one
     constexpr double kInvPi = 0.31830988618379067154, kInvPiLow = -1.9678676675182486e-17;
-    const double x = double(pos[k]) * double(a.freq[i - k * pairs]);  // radians
+    const double x = double(pos[k]) * double(a.freq[p]);         // radians
     const double t = x * kInvPi;                                      // half turns
     const double low = fma(x, kInvPi, -t) + x * kInvPiLow;
     float s, c;
     sincospif(float(fma(-2.0, rint(0.5 * t), t) + low), &s, &c);
-    cs[i] = make_float2(a.amplitude * c, a.backward ? -a.amplitude * s : a.amplitude * s);
+    reinterpret_cast<float2*>(cs)[k * pairs + (p % 8 / 2 * (pairs / 8) + p / 8) * 2 + p % 2] =
+        make_float2(a.amplitude * c, a.backward ? -a.amplitude * s : a.amplitude * s);
   }
   __syncthreads();
   for (; u < end; u += step) {
@@ -177,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a, int to
     Raw8<T> x0 = r0, x1 = r1;
     ask(u + step);
     if (v.pair == -2 || !has[v.token]) continue;
-    if (v.pair >= 0) turn<T, kInterleaved>(x0, x1, cs + v.pair, x0, x1);
+    if (v.pair >= 0) turn<T, kInterleaved>(x0, x1, cs + v.pair, pairs / 8, x0, x1);
     store8(v.y, x0);
     store8(v.y + v.gap, x1);
   }
