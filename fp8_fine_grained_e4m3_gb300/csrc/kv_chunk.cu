@@ -61,7 +61,8 @@ constexpr int kGroups = 8;  // of 16 tokens: the smallest block, and the K of on
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kScoutWarp = 14, kLoadWarp = 15;
 // 512 threads are launched with 128 registers each: 512 for the four warps of a sub-partition
-constexpr uint32_t kSoftRegs = 184, kConvRegs = 64, kLowRegs = 80;
+// (184, 64 and 80 left values of the softmax's loop in local memory: 3 % slower)
+constexpr uint32_t kSoftRegs = 208, kConvRegs = 48, kLowRegs = 48;
 static_assert(2 * kSoftRegs + kConvRegs + kLowRegs <= 512, "register split");
 constexpr int kStages = 2;  // of keys and of values
 constexpr int kTabs = 8;    // tiles of which it is known where they lie
