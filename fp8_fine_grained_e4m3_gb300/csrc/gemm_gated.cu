@@ -718,17 +718,16 @@ int max_clusters(int dev, int s) {
   return k > 0 ? int(k) : 0;
 }
 
-// Parts per tile when all tiles fit in one wave: as many as leave every tile's cluster resident, of a K block
-// or more each, where that saves a CTA kMinSaved K blocks (half a microsecond each; the cluster's
-// barriers and exchange cost 2 to 3 us, but its CTAs share the epilogue: 77 rows of 1040 x 400 take 9 us in 8
-// parts, 12 whole; gradient of 130 rows of 400 x 272 14 us in 4 parts, 15 whole, 23 in 2).
+// Parts per tile when all tiles fit in one wave: as many as leave every tile's cluster resident, where that
+// saves a CTA kMinSaved K blocks (half a microsecond each; the cluster's barriers and exchange cost 2 to 3 us, but its
+// CTAs share the epilogue, those that are left without a K block too: 77 rows of 1040 x 400 take 9 us in 8
+// parts, 12 whole; gradient of 130 rows of 400 x 272, four K blocks, 11 us in 8 parts, 14 in 4, 15 whole, 23 in 2).
 constexpr int kMinSaved = 3;
 
 template <bool kGrad>
 int choose_split(const LaunchCtx& c, long long tiles, int Kb) {
   if (tiles >= c.num_sms) return 1;
   long long s = c.num_sms / tiles;
-  if (s > Kb) s = Kb;
   if (s > kMaxSplit) s = kMaxSplit;
   for (; s >= 2 && Kb - ceil_div(Kb, int(s)) >= kMinSaved; --s)
     if (max_clusters<kGrad>(c.dev, int(s)) >= tiles) return int(s);
