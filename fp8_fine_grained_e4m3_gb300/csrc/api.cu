@@ -793,7 +793,9 @@ int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, 
   void* ws = nullptr;
   const StreamLock lk = lock_stream(c.dev, stream);
   if (int r = workspace_on(c.dev, c.ctx, stream, kv_chunk_workspace_bytes(c), &ws, kWsChunk)) return r;
-  return finish(launch_kv_chunk(c, a, ws), 2);
+  int launches = 0;
+  const cudaError_t e = launch_kv_chunk(c, a, ws, &launches);
+  return finish(e, launches);
 }
 
 int fp8_moe_few(const uint8_t* A, const float* sA, const float* logits, const uint8_t* W1,

@@ -198,9 +198,10 @@ struct KvChunkArgs {
   int log_block;
   bool causal;
   unsigned long long wait_ns;  // limit of each wait
+  bool whole = false;          // no unit of work is split
 };
 size_t kv_chunk_workspace_bytes(const LaunchCtx& c);
-cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws);
+cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws, int* launches);
 
 // The gated feed-forward products (gemm_gated.cu).
 struct GatedArgs {

@@ -43,7 +43,8 @@
 //
 // Units are shared out evenly over the CTAs by their tiles of 128 tokens (a unit's start and end
 // count as kUnitCost more), whatever the lengths: a CTA's share may begin and end inside a unit, whose
-// parts are then joined, in CTA order, by a second kernel.
+// parts are then joined, in CTA order, by a second kernel.  Where few units of few tiles can have a CTA each, they
+// get one, and there is nothing to join.
 #include <cfloat>
 
 #include "common.cuh"
@@ -120,6 +121,11 @@ __device__ __forceinline__ int unit_tiles(const KvChunkArgs& a, int len, int n, 
   return (row_limit(a, len, n, last) + kTok - 1) / kTok;
 }
 
+// What unit u of a sequence counts for in the shares.
+__device__ __forceinline__ int unit_cost(const KvChunkArgs& a, int len, int n, int u) {
+  return a.whole ? 1 : unit_tiles(a, len, n, u) + kUnitCost;
+}
+
 struct Seq {
   int t0, n, len;
 };
@@ -148,14 +154,14 @@ __device__ __forceinline__ long long sequence_cost(const KvChunkArgs& a, const S
   const int units = units_of(a, s.n);
   long long w = 0;
   if (units <= 4)
-    for (int u = 0; u < units; ++u) w += unit_tiles(a, s.len, s.n, u) + kUnitCost;
+    for (int u = 0; u < units; ++u) w += unit_cost(a, s.len, s.n, u);
   uint32_t many = __ballot_sync(0xffffffffu, units > 4);
   while (many) {  // the lanes share a long sequence's
     const int l = __ffs(many) - 1;
     many &= many - 1;
     const int n = __shfl_sync(0xffffffffu, s.n, l), len = __shfl_sync(0xffffffffu, s.len, l);
     long long sum = 0;
-    for (int u = lane; u < units_of(a, n); u += 32) sum += unit_tiles(a, len, n, u) + kUnitCost;
+    for (int u = lane; u < units_of(a, n); u += 32) sum += unit_cost(a, len, n, u);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == l) w = sum;
   }
@@ -198,7 +204,7 @@ __device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, in
   for (base = 0; base < a.B; base += kThreads) list += round();
   Share sh;
   sh.total = list * a.heads;
-  sh.each = max((long long)kMinShare, (long long)((unsigned long long)(sh.total + gridDim.x - 1) / gridDim.x));
+  sh.each = max(a.whole ? 1LL : (long long)kMinShare, (long long)((unsigned long long)(sh.total + gridDim.x - 1) / gridDim.x));
   sh.lo = min(sh.total, sh.each * blockIdx.x);
   sh.hi = min(sh.total, sh.lo + sh.each);
   sh.head = list > 0 ? int((unsigned long long)sh.lo / (unsigned long long)list) : 0;
@@ -962,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the unit that holds the offset, 32 at a time
         while (true) {
           const int u = un + lane;
-          const int w = u < units_of(a, s.n) ? unit_tiles(a, s.len, s.n, u) + kUnitCost : 0;
+          const int w = u < units_of(a, s.n) ? unit_cost(a, s.len, s.n, u) : 0;
           int upto = w;
           for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -996,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const int tiles = unit_tiles(a, s.len, s.n, un);
-          const long long cost = tiles + kUnitCost, begin = at - off;
+          const long long cost = unit_cost(a, s.len, s.n, un), begin = at - off;
           const long long x1 = min(cost, off + (hi - at));
           Unit unit;
           unit.head = head;
@@ -1007,7 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unit.row0 = un * kUnitRows;
           unit.rows = min(kUnitRows, s.n * a.group - unit.row0);
           unit.j0 = int(max(0LL, off - kUnitCost));
-          unit.j1 = int(max(0LL, x1 - kUnitCost));
+          unit.j1 = a.whole ? tiles : int(max(0LL, x1 - kUnitCost));
           unit.first = row_limit(a, s.len, s.n, unit.row0);
           unit.vis = row_limit(a, s.len, s.n, unit.row0 + unit.rows - 1);
           unit.bad = 0;
@@ -1210,18 +1216,26 @@ __global__ void __launch_bounds__(kUnitRows) kv_chunk_join_kernel(const __grid_c
 }
 
 template <int kDim, bool kE5M2>
-cudaError_t run(const LaunchCtx& c, const KvChunkArgs& a, void* ws) {
+cudaError_t run(const LaunchCtx& c, KvChunkArgs a, void* ws, int* launches) {
   static SmemLimit limit;
   auto fn = kv_chunk_kernel<kDim, kE5M2>;
   if (cudaError_t e = limit.raise(c, reinterpret_cast<const void*>(fn), Smem<kDim>::kBytes)) return e;
   // no more CTAs than there can be work for
   const long long units = (long long)a.heads * ((long long)a.T * a.group / kUnitRows + a.B);
-  const long long tiles = ((long long)a.width * a.block + kTok - 1) / kTok + kUnitCost;
-  const long long most = units > c.num_sms ? c.num_sms : max(1LL, units * tiles / kMinShare);
-  const int grid = int(min((long long)c.num_sms, most));
+  const long long tiles = ((long long)a.width * a.block + kTok - 1) / kTok;
+  // Whole units, a CTA each, where sharing their tiles out cannot win what the join costs: tables of up to 4 tiles
+  // (17 tokens behind 37: 10.4 us, shared out 11.7; 512 x 64 heads 20.8 and 28.7), of up to 8 where units for half of
+  // the CTAs and more leave little to share out (1024 x 32 heads: 26.0 and 32.6; but 1024 x 2 heads 26.7 and 25.2, and
+  // 1964 tokens for 128 units 40 and 35).
+  a.whole = units <= c.num_sms && tiles <= (2 * units >= c.num_sms ? 8 : 4);
+  const long long most = units > c.num_sms ? c.num_sms : a.whole ? units : units * (tiles + kUnitCost) / kMinShare;
+  const int grid = int(min((long long)c.num_sms, max(1LL, most)));
   Split* splits = static_cast<Split*>(ws);
   float* parts = reinterpret_cast<float*>(static_cast<char*>(ws) + size_t(c.num_sms) * 64);
   if (cudaError_t e = launch_dependent(c, fn, grid, kThreads, Smem<kDim>::kBytes, a, parts, splits, c.status)) return e;
+  *launches = 1;
+  if (a.whole) return cudaSuccess;
+  *launches = 2;
   return launch_dependent(c, kv_chunk_join_kernel<kDim>, dim3(grid, kDim / kJoinDims), kUnitRows, 0, a,
                           reinterpret_cast<const float4*>(parts), splits);
 }
@@ -1235,10 +1249,10 @@ size_t kv_chunk_workspace_bytes(const LaunchCtx& c) {
   return size_t(c.num_sms) * (64 + 2 * size_t(kUnitRows) * (128 + 4) * 4);
 }
 
-cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws) {
+cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws, int* launches) {
   const bool e5 = a.fmt == FP8GEMM_FMT_E5M2;
-  if (a.dim == 128) return e5 ? run<128, true>(c, a, ws) : run<128, false>(c, a, ws);
-  return e5 ? run<64, true>(c, a, ws) : run<64, false>(c, a, ws);
+  if (a.dim == 128) return e5 ? run<128, true>(c, a, ws, launches) : run<128, false>(c, a, ws, launches);
+  return e5 ? run<64, true>(c, a, ws, launches) : run<64, false>(c, a, ws, launches);
 }
 
 }  // namespace fp8gemm

@@ -288,6 +288,19 @@ def test_same_bits_on_every_run_in_a_graph_and_after_larger_calls():
     assert b.fp8gemm_get_device_status() == b.OK
 
 
+@pytest.mark.parametrize("n,heads,tiles,launches", [(100, 2, 4, 1), (100, 2, 5, 2), (700, 32, 8, 1), (700, 32, 9, 2), (700, 8, 8, 2)])
+def test_units_whole_or_split(n, heads, tiles, launches):
+    """By the table's width and the units: the same results."""
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    c = Cache([n], heads, 64, 128, "e4m3", seed=tiles).stale()
+    c.table = np.concatenate([c.table, np.zeros((1, tiles), c.table.dtype)], 1)[:, :tiles]
+    c.width = tiles
+    before = b.num_kernel_launches()
+    O, Q, cu = _run(c, _queries(n, heads, 64, 3), [n])
+    assert b.num_kernel_launches() - before == launches
+    _check(O, c, Q, cu)
+
+
 def test_padded_batch_and_rows_of_one_warp():
     # empty sequences before, between and behind the others, in runs longer than a warp; causal rows whose warps see
     # ever more of a tile, one of them with a single row
