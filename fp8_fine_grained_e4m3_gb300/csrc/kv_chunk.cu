@@ -1183,24 +1183,33 @@ __global__ void __launch_bounds__(kUnitRows) kv_chunk_join_kernel(const __grid_c
   constexpr size_t kSlot = size_t(kUnitRows) * (kDim / 4 + 1);
   auto part = [&](int p) { return parts + (size_t(blockIdx.x + p) * 2 + (p == 0)) * kSlot + r; };
   auto stat = [&](int p) { return part(p)[size_t(kUnitRows) * (kDim / 4)]; };
-  float top = -INFINITY;
-#pragma unroll 2
-  for (int p = 0; p < s.parts; ++p) top = max_nan(top, stat(p).x);
-  const float vref = stat(0).z;
+  // two parts at a time, statistics and rows asked for together
+  float top = -INFINITY, sum = 0.f, vref = 1.f;
   float4 o[kJoinDims / 4] = {};
-  float sum = 0.f;
-#pragma unroll 2
-  for (int p = 0; p < s.parts; ++p) {
-    const float4 t = stat(p);
-    const float f = t.x == -INFINITY ? 0.f : exp2_fast(t.x - top);
-    sum = fmaf(t.y, f * __fdiv_rn(vref, t.z), sum);
+#pragma unroll 1
+  for (int p = 0; p < s.parts; p += 2) {
+    const bool two = p + 1 < s.parts;
+    const int q = two ? p + 1 : p;
+    const float4 t0 = stat(p), t1 = stat(q);
+    float4 v0[kJoinDims / 4], v1[kJoinDims / 4];
 #pragma unroll
     for (int i = 0; i < kJoinDims / 4; ++i) {
-      const float4 v = part(p)[size_t(d / 4 + i) * kUnitRows];
-      o[i].x = fmaf(v.x, f, o[i].x);
-      o[i].y = fmaf(v.y, f, o[i].y);
-      o[i].z = fmaf(v.z, f, o[i].z);
-      o[i].w = fmaf(v.w, f, o[i].w);
+      v0[i] = part(p)[size_t(d / 4 + i) * kUnitRows];
+      v1[i] = part(q)[size_t(d / 4 + i) * kUnitRows];
+    }
+    if (p == 0) vref = t0.z;
+    const float up = max_nan(top, max_nan(t0.x, t1.x));
+    const float shrink = top == -INFINITY ? 1.f : exp2_fast(top - up);  // (of nothing yet)
+    const float w0 = t0.x == -INFINITY ? 0.f : exp2_fast(t0.x - up);
+    const float w1 = !two || t1.x == -INFINITY ? 0.f : exp2_fast(t1.x - up);
+    top = up;
+    sum = fmaf(t1.y, w1 * __fdiv_rn(vref, t1.z), fmaf(t0.y, w0 * __fdiv_rn(vref, t0.z), sum * shrink));
+#pragma unroll
+    for (int i = 0; i < kJoinDims / 4; ++i) {
+      o[i].x = fmaf(v1[i].x, w1, fmaf(v0[i].x, w0, o[i].x * shrink));
+      o[i].y = fmaf(v1[i].y, w1, fmaf(v0[i].y, w0, o[i].y * shrink));
+      o[i].z = fmaf(v1[i].z, w1, fmaf(v0[i].z, w0, o[i].z * shrink));
+      o[i].w = fmaf(v1[i].w, w1, fmaf(v0[i].w, w0, o[i].w * shrink));
     }
   }
   const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
