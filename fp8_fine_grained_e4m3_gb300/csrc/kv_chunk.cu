@@ -175,6 +175,49 @@ struct Share {
   long long off;
 };
 
+// a / b of numbers that are not negative; in 32 bits where they fit (code that runs once is slow by its length).
+__device__ __forceinline__ long long quotient_ll(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
+  return (unsigned long long)a / (unsigned long long)b;
+}
+
+// Share of a CTA when all heads' lists together cost heads * list.
+__device__ __forceinline__ Share share_of(const KvChunkArgs& a, long long list) {
+  Share sh;
+  sh.total = list * a.heads;
+  sh.each = max(a.whole ? 1LL : (long long)kMinShare, quotient_ll(sh.total + gridDim.x - 1, gridDim.x));
+  sh.lo = min(sh.total, sh.each * blockIdx.x);
+  sh.hi = min(sh.total, sh.lo + sh.each);
+  sh.head = list > 0 ? int(quotient_ll(sh.lo, list)) : 0;
+  sh.b = 0;
+  sh.off = 0;
+  return sh;
+}
+
+// Up to 32 sequences: one warp finds the share, and the sequence that it begins in, by itself, a lane each (the
+// block's way took 1 us longer).
+constexpr int kFew = 32;
+__device__ __forceinline__ void find_share_few(const KvChunkArgs& a, int lane, Share* out, Seq* s, int* status) {
+  const Seq mine = sequence(a, lane, status);
+  const long long w = sequence_cost(a, mine, lane);
+  long long upto = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = shfl_up_ll(upto, o);
+    if (lane >= o) upto += v;
+  }
+  const long long list = __shfl_sync(0xffffffffu, upto, 31);
+  Share sh = share_of(a, list);
+  const long long at = sh.lo - sh.head * list;
+  const uint32_t in = __ballot_sync(0xffffffffu, at >= upto - w && at < upto);
+  if (lane == (in ? __ffs(in) - 1 : 0)) {
+    sh.b = lane;
+    sh.off = at - (upto - w);
+    *out = sh;
+    *s = mine;
+  }
+  __syncwarp();
+}
+
 __device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, int* status) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   long long list = 0;
@@ -202,14 +245,7 @@ __device__ void find_share(const KvChunkArgs& a, Share* out, long long* sums, in
     return all;
   };
   for (base = 0; base < a.B; base += kThreads) list += round();
-  Share sh;
-  sh.total = list * a.heads;
-  sh.each = max(a.whole ? 1LL : (long long)kMinShare, (long long)((unsigned long long)(sh.total + gridDim.x - 1) / gridDim.x));
-  sh.lo = min(sh.total, sh.each * blockIdx.x);
-  sh.hi = min(sh.total, sh.lo + sh.each);
-  sh.head = list > 0 ? int((unsigned long long)sh.lo / (unsigned long long)list) : 0;
-  sh.b = 0;
-  sh.off = 0;
+  const Share sh = share_of(a, list);
   if (tid == 0) *out = sh;
   __syncthreads();
   if (sh.lo >= sh.hi) return;
@@ -253,6 +289,7 @@ struct Bars {
   uint32_t tmem;
   int abort;
   Share share;
+  Seq seq;  // that it begins in
 };
 static_assert(sizeof(Bars) <= 512, "barrier area");
 
@@ -439,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  find_share(a, &share, reinterpret_cast<long long*>(smem), status);
+  if (a.B > kFew) find_share(a, &share, reinterpret_cast<long long*>(smem), status);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -960,11 +997,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++given;
         return true;
       };
+      if (a.B <= kFew) find_share_few(a, lane, &share, &bar.seq, status);
+      Seq s = bar.seq;
+      if (a.B > kFew) s = sequence(a, share.b, status);
       const long long lo = share.lo, hi = share.hi;
       if (lo < hi) {
         long long at = lo, off = share.off;  // off: cost before `at` within the sequence, then the unit
         int head = share.head, b = share.b, un = 0;
-        Seq s = sequence(a, b, status);
         // the unit that holds the offset, 32 at a time
         while (true) {
           const int u = un + lane;
