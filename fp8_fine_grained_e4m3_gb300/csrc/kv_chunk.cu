@@ -33,9 +33,9 @@
 // tokens there are 2^-13 of the sum; the output is BF16).
 //
 // Bound by the softmax and the chain S -> P -> O of a tile: 512 tokens x 32 heads of 128 behind 131077 take
-// 0.90 ms, 1.22 PFLOP/s or 64 % of what cuBLAS reaches; a pair of tiles of rows takes 3500 cycles a tile of
+// 0.88 ms, 1.25 PFLOP/s or 65 % of what cuBLAS reaches; a pair of tiles of rows takes 3400 cycles a tile of
 // tokens, of which the tensor cores work 2200 and each softmax warp 1900 (512 of them exponentials, beside those of the
-// other warp of its scheduler).  Prompts from empty caches (9 sequences, 14600 tokens x 64 heads) take 0.78 ms, 0.70
+// other warp of its scheduler).  Prompts from empty caches (9 sequences, 14600 tokens x 64 heads) take 0.75 ms, 0.73
 // PFLOP/s: their units are nine tiles long, and a unit's start and end cost as much as three; scores that keep rising
 // cost a second pass over a tile's scores in one of four.  What the warps run together has to fit in the
 // instruction cache: loops are rolled and hold one copy of their body, without which it took two to three times
