@@ -790,9 +790,15 @@ int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, 
                       block_table, seq_lens, cu_q, static_cast<__nv_bfloat16*>(O), scale, T, B, heads,
                       group, dim, block, table_width, num_blocks, max_q, fmt, log2_block(block),
                       causal != 0, wait_limit_ns()};
-  void* ws = nullptr;
+  void *ws = nullptr, *few = nullptr;
   const StreamLock lk = lock_stream(c.dev, stream);
+  // (both whatever the rows, so that any first call on a stream prepares those that are captured there)
   if (int r = workspace_on(c.dev, c.ctx, stream, kv_chunk_workspace_bytes(c), &ws, kWsChunk)) return r;
+  if (int r = workspace_on(c.dev, c.ctx, stream, kv_attention_workspace_bytes(c), &few, kWsAttention)) return r;
+  if (kv_chunk_few_rows(c, a))
+    return finish(launch_kv_attention(c, KvAttentionArgs{a.Q, ld_q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
+                                                         cu_q, a.O, scale, T, B, heads, group, dim, block, table_width,
+                                                         num_blocks, max_q, fmt, a.log_block, a.wait_ns}, few), 1);
   int launches = 0;
   const cudaError_t e = launch_kv_chunk(c, a, ws, &launches);
   return finish(e, launches);

@@ -201,6 +201,8 @@ struct KvChunkArgs {
   bool whole = false;          // no unit of work is split
 };
 size_t kv_chunk_workspace_bytes(const LaunchCtx& c);
+// Whether launch_kv_attention is the kernel for a call's rows.
+bool kv_chunk_few_rows(const LaunchCtx& c, const KvChunkArgs& a);
 cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws, int* launches);
 
 // The gated feed-forward products (gemm_gated.cu).

@@ -1263,19 +1263,27 @@ __global__ void __launch_bounds__(kUnitRows) kv_chunk_join_kernel(const __grid_c
                    bf16x2_bits(scaled(o[i + 1].x), scaled(o[i + 1].y)), bf16x2_bits(scaled(o[i + 1].z), scaled(o[i + 1].w)));
 }
 
+// Units and tiles of a unit that a call has at most.
+long long most_units(const KvChunkArgs& a) { return (long long)a.heads * ((long long)a.T * a.group / kUnitRows + a.B); }
+long long most_tiles(const KvChunkArgs& a) { return ((long long)a.width * a.block + kTok - 1) / kTok; }
+
+// Whole units, a CTA each, where sharing their tiles out cannot win what the join costs: tables of up to 4 tiles
+// (17 tokens behind 37: 9.5 us, shared out 10.6; 512 x 64 heads 19.9 and 26.4), of up to 8 where units for half of
+// the CTAs and more leave little to share out (1024 x 32 heads: 26.0 and 32.6; but 1024 x 2 heads 26.7 and 25.2, and
+// 1964 tokens for 128 units 40 and 35).
+bool whole_units(const LaunchCtx& c, const KvChunkArgs& a) {
+  const long long units = most_units(a);
+  return units <= c.num_sms && most_tiles(a) <= (2 * units >= c.num_sms ? 8 : 4);
+}
+
 template <int kDim, bool kE5M2>
 cudaError_t run(const LaunchCtx& c, KvChunkArgs a, void* ws, int* launches) {
   static SmemLimit limit;
   auto fn = kv_chunk_kernel<kDim, kE5M2>;
   if (cudaError_t e = limit.raise(c, reinterpret_cast<const void*>(fn), Smem<kDim>::kBytes)) return e;
   // no more CTAs than there can be work for
-  const long long units = (long long)a.heads * ((long long)a.T * a.group / kUnitRows + a.B);
-  const long long tiles = ((long long)a.width * a.block + kTok - 1) / kTok;
-  // Whole units, a CTA each, where sharing their tiles out cannot win what the join costs: tables of up to 4 tiles
-  // (17 tokens behind 37: 10.4 us, shared out 11.7; 512 x 64 heads 20.8 and 28.7), of up to 8 where units for half of
-  // the CTAs and more leave little to share out (1024 x 32 heads: 26.0 and 32.6; but 1024 x 2 heads 26.7 and 25.2, and
-  // 1964 tokens for 128 units 40 and 35).
-  a.whole = units <= c.num_sms && tiles <= (2 * units >= c.num_sms ? 8 : 4);
+  const long long units = most_units(a), tiles = most_tiles(a);
+  a.whole = whole_units(c, a);
   const long long most = units > c.num_sms ? c.num_sms : a.whole ? units : units * (tiles + kUnitCost) / kMinShare;
   const int grid = int(min((long long)c.num_sms, max(1LL, most)));
   Split* splits = static_cast<Split*>(ws);
@@ -1295,6 +1303,16 @@ cudaError_t run(const LaunchCtx& c, KvChunkArgs a, void* ws, int* launches) {
 size_t kv_chunk_workspace_bytes(const LaunchCtx& c) {
   static_assert(sizeof(Split) <= 64, "split record");
   return size_t(c.num_sms) * (64 + 2 * size_t(kUnitRows) * (128 + 4) * 4);
+}
+
+// The cache attention for single tokens (16 rows of a cached head a pass, at the memory's rate) takes up to 32 rows
+// faster (128 dimensions, 8 cached heads; us there / here: 8 rows over 100000 tokens 41 / 80, 64 sequences of 300 tokens with
+// 16 rows 25 / 48, with 32 rows 38 / 48, 16 of 16000 with 32 rows 184 / 177, with 64 rows 339 / 178), but for 9 rows
+// and more of many short sequences (64 of 40 with 2 heads: 14.4 / 13.0).  It is causal; of one token that is no matter.
+bool kv_chunk_few_rows(const LaunchCtx& c, const KvChunkArgs& a) {
+  const long long rows = (long long)a.max_q * a.group;
+  if (!(a.causal || a.max_q == 1) || rows > 32) return false;
+  return rows <= 8 || !(whole_units(c, a) && 2 * most_units(a) >= c.num_sms);
 }
 
 cudaError_t launch_kv_chunk(const LaunchCtx& c, const KvChunkArgs& a, void* ws, int* launches) {

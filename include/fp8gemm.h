@@ -594,9 +594,12 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  * sequence are left as they were.  T * group, max_q * group and table_width * block at most
  * 2^31 - 256.
  *
+ * Calls of few rows (causal, max_q * group up to 32) are those of fp8_kv_attention but for many
+ * short sequences: max_q as small as it is known to be helps.
+ *
  * Work is shared out evenly over the SMs whatever the lengths; parts of a sequence's rows are
- * joined through a per-(device, stream) workspace of one size for all calls.  Results are
- * deterministic for given host sizes, lengths and offsets.
+ * joined through a per-(device, stream) workspace of one size for all calls (fp8_kv_attention's
+ * is taken too).  Results are deterministic for given host sizes, lengths and offsets.
  *
  * Arithmetic: products of FP16 operands (codes and queries are exact in it, the queries after a shift
  * of each by a power of two) and FP32 sums.  A key block's scale acts on the product of query and
@@ -604,7 +607,8 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  * row's largest such term, fewer bits below, and counts as 0 below 2^-30 of it; the weights' sum
  * is exact to FP32 as long as the scales of the blocks that a row sees lie within a factor
  * of 2^64 of each other.  Value scales below 2^-126 count as 0.  An infinity among values or value
- * scales counts as NaN, and what is not finite reaches the queries that see its token, and no others.
+ * scales counts as NaN (calls of few rows: as in fp8_kv_attention), and what is not finite reaches the
+ * queries that see its token, and no others.
  */
 int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
                            const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,

@@ -301,6 +301,20 @@ def test_units_whole_or_split(n, heads, tiles, launches):
     _check(O, c, Q, cu)
 
 
+@pytest.mark.parametrize("lens,counts,heads,group,causal", [
+    ([300], [4], 2, 8, True), ([300], [11], 2, 3, True),  # 32 rows and 33
+    ([300, 2000], [1, 1], 2, 8, False), ([300, 2000], [2, 1], 2, 8, False),
+    ([40 + i for i in range(64)], [1 + i % 2 for i in range(64)], 2, 8, True), ([9] * 64, [1] * 64, 2, 8, True)])
+def test_few_rows(lens, counts, heads, group, causal):
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    c = Cache(lens, heads, 128, 16, "e4m3", seed=21).stale()
+    O, Q, cu = _run(c, _queries(sum(counts), heads * group, 128, 22), counts, causal=causal)
+    _check(O, c, Q, cu, causal=causal)
+    wide, _, _ = _run(c, _queries(sum(counts), heads * group, 128, 22), counts, causal=causal, max_q=sum(counts) + 40)
+    _check(wide, c, Q, cu, causal=causal)
+    assert b.fp8gemm_get_device_status() == b.OK
+
+
 def test_padded_batch_and_rows_of_one_warp():
     # empty sequences before, between and behind the others, in runs longer than a warp; causal rows whose warps see
     # ever more of a tile, one of them with a single row
