@@ -26,7 +26,7 @@
 // the plain product of that size takes 106 (four waves, the last one of 56 tiles: splitting that one along K as
 // a launch of its own won 1 us here and lost 9 in the gradient), the gradient of 8192 rows 149 us where
 // the product takes 107; its epilogue is 10 us a tile.  By latency and the weights' bytes for a few tokens
-// (29 MB in 12.7 us): then all tiles fit in one wave, and each is split along K over a cluster (as in
+// (29 MB in 12.1 us): then all tiles fit in one wave, and each is split along K over a cluster (as in
 // gemm_tc.cu), whose CTAs share the rows of the epilogue.
 #include <cstring>
 
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kSplit) {
         float4* srow = reinterpret_cast<float4*>(smem) + (row * kPitch + wg * kCols) / 4;
 #pragma unroll
-        for (int j = 0; j < kCols / 4; ++j)
+        for (int j = 0; j < kCols / 4 && row_ok; ++j)  // (rows that do not exist would meet the others' banks)
           srow[j] = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
         continue;
       }
