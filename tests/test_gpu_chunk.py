@@ -324,3 +324,31 @@ def test_padded_batch_and_rows_of_one_warp():
     for group in (1, 3):
         O, Q, cu = _run(c, _queries(sum(counts), 3 * group, 64, group), counts)
         _check(O, c, Q, cu)
+
+
+@pytest.mark.parametrize("first", [(300, 1), (1, 300)])
+def test_any_first_call_prepares_a_capture_of_few_or_many_rows(first):
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    s = torch.cuda.Stream()
+    for i, n in enumerate(first):
+        c = Cache([400], 2, 128, 64, "e4m3", seed=n).stale()
+        cache = c.on_gpu()
+        Q = dev(_queries(n, 2, 128, n)).to(torch.bfloat16)
+        O = torch.zeros_like(Q)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            if i == 0:
+                b.fp8_kv_attention_chunk(Q, *cache, O=O)
+                continue
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                b.fp8_kv_attention_chunk(Q, *cache, O=O)
+            for _ in range(2):
+                O.zero_()
+                graph.replay()
+            s.synchronize()
+        _check(O, c, Q.double().cpu().numpy(), _offsets([n]))
+    with torch.cuda.stream(s):
+        assert b.fp8gemm_get_device_status() == b.OK
+        b.fp8gemm_release_workspaces()

@@ -4,7 +4,7 @@ Bound, derived before the first run: the angle in half turns is rounded to FP32
 once it lies in [-1, 1] (2^-25; 2^-23 radians at most), sine and cosine add 2 ulp (2^-23), the
 amplitude, the products and the sum a rounding each (4 x 2^-24 of the terms), the type half a step:
   |got - ref| <= eps / 2 |ref| + amplitude (|x1| + |x2|) 2^-21
-(eps / 2 = 2^-9 ... finfo(t).eps / 2: bf16 2^-8, f32 2^-24)
+(finfo(t).eps / 2: bf16 2^-8, f32 2^-24)
 """
 
 import numpy as np
