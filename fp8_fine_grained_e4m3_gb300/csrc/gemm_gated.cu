@@ -273,6 +273,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 1;
     raise_status(status, FP8GEMM_ERR_TIMEOUT);
   };
+  // A whole warp's wait, with one outcome: the TMEM loads behind it are the warp's.
+  auto warp_wait = [&](uint64_t* b, uint32_t parity) {
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(b, parity))) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t0 > args.wait_ns)) return false;
+    }
+    return true;
+  };
 
   if (warp == kTmaWarp) {
     regs_decrease<kLowRegs>();
@@ -414,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int buf = n_mma & 1;
-        if (!mbar_wait(&tfull_bar[buf], (n_mma / 2) & 1, abort_flag, args.wait_ns)) {
+        if (!warp_wait(&tfull_bar[buf], (n_mma / 2) & 1)) {
           fail();
           ok = false;
           break;

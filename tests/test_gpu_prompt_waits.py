@@ -59,3 +59,26 @@ def test_calls_beside_and_behind_one_that_gave_up(gives_up):
     assert b.fp8gemm_get_device_status() in (b.OK, b.ERR_TIMEOUT)
     assert all(torch.equal(x, want) for x in behind)
     assert torch.equal(good(), want) and b.fp8gemm_get_device_status() == b.OK
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if not n.startswith("chunk")])
+def test_limits_that_run_out_somewhere_in_a_product(name):
+    """Limits in small steps, so that waits run out at the first K block, in the middle and behind the last one: every
+    warp goes on to its matrix instructions and shuffles as a whole."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    call = CALLS[name](1)
+    want = call()
+    torch.cuda.synchronize()
+    for i in range(60):
+        b.set_wait_limit_ns(int(1.2 ** i))
+        try:
+            got = call()
+            status = b.fp8gemm_get_device_status()
+        finally:
+            b.set_wait_limit_ns(0)
+        assert status in (b.OK, b.ERR_TIMEOUT)
+        if status == b.OK:
+            assert torch.equal(got, want)
+    assert torch.equal(call(), want)
+    assert b.fp8gemm_get_device_status() == b.OK
