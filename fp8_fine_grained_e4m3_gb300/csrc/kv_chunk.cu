@@ -709,20 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sums[g] = sum_a + sum_b;
               }
               const float top = fmaxf(top0, top1);
-              if (again || !__any_sync(0xffffffffu, unset ? top > -INFINITY : top > kMost)) break;
-              // by how much the reference rises; the first score that is there sets it
-              float up = 0.f, shrink = 1.f;
-              if (!unset) {
-                const float to = ref + fmaxf(top - kLift, 0.f);
-                up = to - ref;
-                shrink = exp2_fast(-up);
-                ref = to;
-              } else if (top > -INFINITY) {
-                ref = top - kLift;
-                unset = false;
-              }
-              if (h > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {  // P of the tile's tokens before these
-                const __half2 f = __float2half2_rn(shrink);
+              if (again || !__any_sync(0xffffffffu, top > kMost)) break;
+              // by how much the reference rises: a whole number, for what is there to be multiplied by a power of two
+              const float to = ref + floorf(fmaxf(top - kLift, 0.f));
+              const float shrink = exp2_fast(ref - to);
+              ref = to;
+              // P of the tile's tokens before these, in FP32: exact but for what FP16 then holds with fewer bits
+              if (h > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {
                 tmem_st_wait();
 #pragma unroll 1
                 for (int d = 0; d < 16 * h; d += 16) {
@@ -731,8 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_ld_wait_tied16(o);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) {
-                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f);
-                    o[e] = *reinterpret_cast<const uint32_t*>(&v);
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&o[e]));
+                    o[e] = f16x2_bits(v.x * shrink, v.y * shrink);
                   }
                   tmem_st_32x32b_x16(s_at + d, o);
                 }
