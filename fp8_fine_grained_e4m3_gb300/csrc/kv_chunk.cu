@@ -95,7 +95,7 @@ struct Split {
 // What the roles need of a tile of tokens, found ahead of them.
 struct Scales {   // of 16 tokens
   float k;        // of the keys
-  float add;      // log2 |v_scale| (of 1 for scales of 0 and such as are not finite), -infinity without a block
+  float add;      // log2 |v_scale| (or of kNoScale), -infinity without a block
   float inv;      // 1 / |v_scale|
   uint32_t mode;  // what becomes of the values' codes: see kZero, kNegate, kNotFinite
 };
@@ -109,6 +109,10 @@ struct Tab {
   float v0;          // |v_scale| of its first tokens
   int pad[2];
 };
+// What stands for the |v_scale| of a block whose own is 0, below FP32's normal numbers or not finite: its tokens count in the
+// weights' sum alone, so it is small, for the reference to be that of the blocks that reach the output (scales that
+// fp8_kv_append makes of values down to 10^-15 are larger), and far enough from FP32's least for the sum to keep them.
+constexpr float kNoScale = 0x1p-60f;
 static_assert(sizeof(Tab) == 192, "tile record");
 enum : uint32_t { kZero = 1, kNegate = 2, kNotFinite = 4 };
 
@@ -766,7 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
       }
-      const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
+      // (times vref first, whose share is in the sum: the product is about a value scale)
+      const float f = (sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f) * vref;
       const long long out = !row_ok ? -1 : ((long long)(u->t0 + seq_row / a.group) * a.heads * a.group +
                                       u->head * a.group + seq_row % a.group) * kDim;
       // parts: [kDim / 4][rows][4], then [rows][4], so that neighbouring lanes write neighbouring places
@@ -787,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             float v[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(o[8 * e + y]) * f * vref;
+            for (int y = 0; y < 8; ++y) v[y] = __uint_as_float(o[8 * e + y]) * f;
             w[e] = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
           }
           exchange<1>(w, lane);
@@ -1159,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           prefetch_l2(a.vc + (long long)row * kDim, 16 * kDim);
         }
         const bool fin = fabsf(vs) <= FLT_MAX, used = fin && fabsf(vs) >= FLT_MIN;
-        const float av = used ? fabsf(vs) : 1.f;
+        const float av = used ? fabsf(vs) : kNoScale;
         Scales x;
         x.k = ks;
         // (its error is one of the weight of these tokens: 2^-15 at most)
@@ -1244,11 +1249,11 @@ __global__ void __launch_bounds__(kUnitRows) kv_chunk_join_kernel(const __grid_c
       o[i].w = fmaf(v1[i].w, w1, fmaf(v0[i].w, w0, o[i].w * shrink));
     }
   }
-  const float f = sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f;
+  const float f = (sum > 0.f || isnan(sum) ? __fdividef(1.f, sum) : 0.f) * vref;
   const int row = s.row0 + r;
   __nv_bfloat16* out =
       a.O + (((long long)s.t0 + row / a.group) * a.heads * a.group + s.head * a.group + row % a.group) * kDim + d;
-  auto scaled = [&](float v) { return v * f * vref; };
+  auto scaled = [&](float v) { return v * f; };
 #pragma unroll
   for (int i = 0; i < kJoinDims / 4; i += 2)
     *reinterpret_cast<uint4*>(out + 4 * i) =

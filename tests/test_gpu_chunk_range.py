@@ -102,3 +102,31 @@ def test_sixteen_equal_peaks_in_a_tile_that_all_rows_see(rise, causal):
     c.v[c.table[0, 8], 0, :, :32] = 0
     O, Q, cu = _run(c, _queries_of([1.0] * 40), [40], scale=math.log(2), causal=causal)
     _within(O, c, Q, cu, causal)
+
+
+@pytest.mark.parametrize("power", [-9, -25, -32, -40])
+@pytest.mark.parametrize("causal", [True, False])
+def test_blocks_of_zero_scale_beside_small_values(power, causal):
+    """Blocks of zeros have the scale 0: they are in the sum of the weights and do not cost the others bits."""
+    dim, n, new = 128, 700, 150
+    c = Cache([n], 1, dim, 16, "e4m3", seed=70)
+    c.vs[:] = 2.0 ** power
+    c.vs[c.table[0, ::3]] = 0
+    O, Q, cu = _run(c, _queries(new, 1, dim, 71), [new], causal=causal)
+    _within(O, c, Q, cu, causal, scale=dim ** -0.5)
+    c.vs[:] = 0
+    O, Q, cu = _run(c, _queries(new, 1, dim, 71), [new], causal=causal)
+    assert not host(O).any()
+
+
+@pytest.mark.parametrize("rise", [12.0, 20.3, 25.0, 33.0])
+@pytest.mark.parametrize("at", [0, 9, 17])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_block_of_zero_scale_that_dominates(rise, at, causal):
+    """Zeros that the scores point to leave the rest of the output small, not rough: the bound is of the rest alone."""
+    scores = [0] * 20
+    scores[at] = rise
+    c = _cache(scores, n=310)
+    c.vs[c.table[0, at]] = 0
+    O, Q, cu = _run(c, _queries_of([1.0] * 33), [33], scale=math.log(2), causal=causal)
+    _within(O, c, Q, cu, causal)
