@@ -860,12 +860,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              uint32_t lost = mode & kNotFinite ? 0xffffffffu : mixed && v == 1 ? not_finite4<kE5M2>(w[e]) : 0u;
-              if (tab.row[r / 16] < 0 || r >= tab.there || (mode & kZero)) {
-                w[e] = lost = 0u;
-              } else if (mode & kNegate) {
-                w[e] ^= 0x80808080u;
+              if (tab.row[r / 16] < 0 || r >= tab.there) {
+                w[e] = 0u;
+                continue;
               }
+              // (0 times what is not finite is NaN)
+              const uint32_t lost = mode & kNotFinite                             ? 0xffffffffu
+                                    : (mode & kZero) || (mixed && v == 1) ? not_finite4<kE5M2>(w[e])
+                                                                          : 0u;
+              if (mode & kZero) w[e] = 0u;
+              if (mode & kNegate) w[e] ^= 0x80808080u;
               bad |= mixed && lost != 0u;
               w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
             }

@@ -130,3 +130,25 @@ def test_a_block_of_zero_scale_that_dominates(rise, at, causal):
     c.vs[c.table[0, at]] = 0
     O, Q, cu = _run(c, _queries_of([1.0] * 33), [33], scale=math.log(2), causal=causal)
     _within(O, c, Q, cu, causal)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -130])
+@pytest.mark.parametrize("at", [40, 433])
+@pytest.mark.parametrize("second", [False, True])
+def test_what_is_not_finite_under_a_scale_of_zero(fmt, size, at, second):
+    """0 times NaN is NaN, in a tile that all rows see and in one that some do not, whatever other tokens hold."""
+    dim, n, new = 64, 600, 300
+    c = Cache([n], 1, dim, 16, fmt, seed=80)
+    c.vs[c.table[0, at // 16]] = size
+    clean, Q, cu = _run(c, _queries(new, 2, dim, 81), [new])
+    c.v[c.table[0, at // 16], 0, at % 16, 5] = 0x7F
+    if second:
+        c.v[c.table[0, 520 // 16], 0, 520 % 16, 9] = 0x7F
+    O, _, _ = _run(c, _queries(new, 2, dim, 81), [new])
+    sees = n - new + 1 + np.arange(new)
+    want = host(clean).copy()
+    want[sees > at, :, 5] = np.nan
+    if second:
+        want[sees > 520, :, 9] = np.nan
+    assert np.array_equal(host(O), want, equal_nan=True)
