@@ -353,8 +353,9 @@ __device__ __forceinline__ float stage_queries(uint8_t* tile, int row) {
                     v.w & 0x7fff7fffu);
   }
   const uint32_t top = max(top2 >> 16, top2 & 0xffffu);
-  // rows below 2^-117 (zeros among them) take the largest shift that is a normal number
-  const int exp = max(int(top >> 7), 10);
+  // rows below 2^-115 (zeros among them) take the largest shift whose reciprocal is a normal number: theirs and BF16's
+  // subnormal numbers become normal ones
+  const int exp = max(int(top >> 7), 11);
   const float up = __uint_as_float(uint32_t(264 - exp) << 23);  // 2^(10 - (exp - 127))
 #pragma unroll 2
   for (int c = 0; c < kChunks; ++c) {

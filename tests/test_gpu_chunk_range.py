@@ -152,3 +152,14 @@ def test_what_is_not_finite_under_a_scale_of_zero(fmt, size, at, second):
     if second:
         want[sees > 520, :, 9] = np.nan
     assert np.array_equal(host(O), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("power", [-114, -116, -117, -120, -128])
+def test_queries_near_the_least_of_their_type(power):
+    """Queries of BF16's last normal numbers and below them, under key scales that make ordinary scores of them."""
+    dim, n, new = 64, 300, 60
+    c = Cache([n], 1, dim, 16, "e4m3", seed=90)
+    c.ks = (c.ks * 2.0 ** 110).astype(np.float32)
+    Q = _queries(new, 1, dim, 91) * np.float32(2.0 ** power)
+    O, Qr, cu = _run(c, Q, [new], scale=dim ** -0.5 * 2.0 ** (-power - 110))
+    _check(O, c, Qr, cu, dim ** -0.5 * 2.0 ** (-power - 110))
