@@ -493,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // A whole warp's wait, with one outcome.  (Short: the roles' loops have to fit in the instruction
   // cache together.)
-  auto warp_wait = [&](uint64_t* b, uint32_t parity) {
+  auto warp_wait = [&](uint64_t* b, uint32_t parity, bool poll = false) {
     uint64_t t0 = 0;
-    while (!__all_sync(0xffffffffu, mbar_try_wait(b, parity))) {
+    while (!__all_sync(0xffffffffu, poll ? mbar_test(b, parity) : mbar_try_wait(b, parity))) {
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
       if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t0 > a.wait_ns)) {
@@ -1084,16 +1084,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kLoadWarp) {
       // ------------------------------------------- codes into shared memory, 16 tokens a copy
       constexpr uint32_t kBytes = 16 * kDim;
+      // One try of a wait may sleep for many microseconds: limits under 100 us are kept by this warp, which polls for
+      // them (all roles doing so took 0.5 % of the call's time).
+      const bool poll = a.wait_ns < 100000;
       bool ok = true;
       uint32_t asked = 0;  // copies, keys' and values' in turn
       for (uint32_t it = 0; ok; ++it) {
         const Tab& tab = tabs[it % kTabs];
-        if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1)) || tab.slot < 0) break;
+        if (!(ok = warp_wait(&bar.tab_full[it % kTabs], (it / kTabs) & 1, poll)) || tab.slot < 0) break;
         const int row = lane < kGroups ? tab.row[lane] : -1;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, row >= 0));
 #pragma unroll 1
         for (int v = 0; v < 2; ++v) {
-          if (!(ok = warp_wait(&bar.codes_empty[v], (it & 1) ^ 1))) break;
+          if (!(ok = warp_wait(&bar.codes_empty[v], (it & 1) ^ 1, poll))) break;
           ++asked;
           if (lane == 0) mbar_arrive_expect_tx(&bar.codes_full[v], n * kBytes);
           __syncwarp();

@@ -82,3 +82,22 @@ def test_limits_that_run_out_somewhere_in_a_product(name):
             assert torch.equal(got, want)
     assert torch.equal(call(), want)
     assert b.fp8gemm_get_device_status() == b.OK
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_no_time_is_not_enough(name):
+    """A limit of 1 ns runs out, and the status says so: in one of a few calls at the least, since a wait may find that
+    what it waits for is there."""
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    call = CALLS[name](1)
+    call()
+    assert b.fp8gemm_get_device_status() == b.OK
+    seen = set()
+    for _ in range(4):
+        b.set_wait_limit_ns(1)
+        try:
+            call()
+            seen.add(b.fp8gemm_get_device_status())
+        finally:
+            b.set_wait_limit_ns(0)
+    assert b.ERR_TIMEOUT in seen and seen <= {b.OK, b.ERR_TIMEOUT}
