@@ -158,3 +158,16 @@ def test_lengths_at_the_types_end():
     assert bool((out[:3] == 5).all())
     same = b.fp8_rope(q[3:], None, f, positions=dev(np.array([2 ** 31 - 4, 2 ** 31 - 3, 2 ** 31 - 2], np.int32)))[0]
     assert torch.equal(out[3:], same)
+
+
+@pytest.mark.parametrize("lens,cu", [
+    ((9, 9, 9), (0, 4, 2, 6)), ((9, 9, 9), (0, 6, 3, 3)), ((9, 9), (-3, 0, 6)), ((9, 9), (0, 6, 9)), ((9, -1, 9), (0, 3, 3, 6)),
+    ((9,) * 400 + (-7,), (0,) * 400 + (6, 6)), ((9,) * 300, (0,) * 150 + (-1,) * 150 + (6,))])
+def test_every_sequence_is_looked_at(lens, cu):
+    """Offsets that fall or leave the tokens, and lengths below 0, of sequences that no token finds."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    q = torch.ones((6, 1, 32), device="cuda")
+    b.fp8_rope(q, None, dev(_freq(32)), seq_lens=dev(np.array(lens, np.int32)), cu=dev(np.array(cu, np.int32)))
+    assert b.fp8gemm_get_device_status() == b.ERR_DEVICE_STATUS
+    assert b.fp8gemm_get_device_status() == b.OK
