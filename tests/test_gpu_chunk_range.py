@@ -104,7 +104,7 @@ def test_sixteen_equal_peaks_in_a_tile_that_all_rows_see(rise, causal):
     _within(O, c, Q, cu, causal)
 
 
-@pytest.mark.parametrize("power", [-9, -25, -32, -40])
+@pytest.mark.parametrize("power", [50, 20, -9, -25, -32, -40])
 @pytest.mark.parametrize("causal", [True, False])
 def test_blocks_of_zero_scale_beside_small_values(power, causal):
     """Blocks of zeros have the scale 0: they are in the sum of the weights and do not cost the others bits."""
