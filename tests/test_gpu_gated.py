@@ -165,6 +165,25 @@ def test_saturated_gates(gate):
     assert bool(((got - float(h)).abs() <= 2.0 ** -4 * float(h) + 1e-30).all())
 
 
+@pytest.mark.parametrize("M,I", [(5, 144), (2700, 2064)])
+@pytest.mark.parametrize("gate,up", [(-1e30, 1e10), (-3e38, -3e38), (1e30, 1e7), (-1e20, 3e38)])
+def test_gates_and_up_values_whose_product_leaves_fp32(M, I, gate, up):
+    """The sigmoid's 0 takes the gradients with it, its 1 leaves dh u and dh g, whatever the product of gate and up value
+    (dh = 2^-20 times 16 products of ones: exact)."""
+    import torch
+    from fp8_fine_grained_e4m3_gb300 import binding as b
+    GU = torch.full((M, 2 * I), gate, dtype=torch.bfloat16, device="cuda")
+    GU[:, I:] = up
+    A, W = torch.full((M, 16), 0x38, dtype=torch.uint8, device="cuda"), torch.full((I, 16), 0x38, dtype=torch.uint8, device="cuda")
+    dGU = torch.empty_like(GU)
+    Q, sQ = b.fp8gemm_gated_backward(A, torch.full((M, 1), 2.0 ** -20, device="cuda"), W, torch.ones((-(-I // 128), 1), device="cuda"),
+                                     GU, a_fmt="e4m3", dGU=dGU)
+    want = torch.zeros_like(GU) if gate < 0 else torch.cat((GU[:, I:], GU[:, :I]), 1) * 2.0 ** -16
+    assert torch.equal(dGU, want)
+    if gate < 0:
+        assert not bool(sQ.any()) and not bool(Q.any())
+
+
 def test_rows_of_zeros_and_nan():
     """A row of zeros has scale 0 and zero codes; a NaN scale makes its row's scales NaN, no other's."""
     import torch
