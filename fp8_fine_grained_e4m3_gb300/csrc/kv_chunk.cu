@@ -1069,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ok = give(unit);
             const int t0 = unit.t0 + unit.row0 / a.group, t1 = unit.t0 + (unit.row0 + unit.rows - 1) / a.group;
-            for (int t = t0 + lane; t <= t1; t += 32)  // its queries
+            for (int t = t0 + lane; t <= t1 && a.group <= kUnitRows; t += 32)  // its queries (not all of a wider group's)
               prefetch_l2(a.Q + (long long)t * a.ld_q + (long long)head * a.group * kDim, a.group * kDim * 2);
           }
           at += x1 - off;

@@ -93,6 +93,13 @@ def test_few_rows_leave_the_rows_behind_the_last_sequence():
     assert np.isnan(host(O)[4:]).all()
 
 
+@pytest.mark.parametrize("heads,group,counts,causal", [(1, 300, [3, 1], True), (2, 257, [2, 5], False), (1, 1000, [1, 1], True)])
+def test_groups_wider_than_a_unit_of_rows(heads, group, counts, causal):
+    c = Cache([140, 77], heads, 64, 32, "e4m3", seed=97).stale()
+    O, Q, cu = _run(c, _queries(sum(counts), heads * group, 64, 98), counts, causal=causal)
+    _check(O, c, Q, cu, causal=causal)
+
+
 @pytest.mark.parametrize("rise", [11.3, 17.9, 21.7, 24.9])
 @pytest.mark.parametrize("causal", [True, False])
 def test_sixteen_equal_peaks_in_a_tile_that_all_rows_see(rise, causal):
