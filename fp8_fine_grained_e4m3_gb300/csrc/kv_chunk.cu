@@ -851,32 +851,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           // finite, or some row does not see the whole tile.  There 0 times what is not finite would
           // reach rows that do not see it: such values become 0, and the rows that do see them are
           // marked when the unit ends.
-          bool bad = false;
-#pragma unroll 1
+          uint32_t bad = 0u;
+#pragma unroll 2
           for (int l = 0; l < kLoads; ++l) {
             const int r = row0 + kRowsAtOnce * l;
             const uint32_t mode = v == 1 ? tab.g[r / 16].mode : 0u;
             uint4* at = reinterpret_cast<uint4*>(codes + l * kRowsAtOnce * kDim);
             const uint4 x = *at;
             uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            // Bits of a code: those that are there, those whose value a scale of 0 leaves, those to be looked at, all of
+            // a scale that is not finite.
+            const uint32_t there = tab.row[r / 16] < 0 || r >= tab.there ? 0u : 0xffffffffu;
+            const uint32_t kept = mode & kZero ? 0u : there;
+            const uint32_t seen = (mixed && v == 1) || mode & kZero ? there : 0u;
+            const uint32_t all = mode & kNotFinite ? there : 0u;
+            const uint32_t sign = mode & kNegate ? 0x80808080u : 0u;
+            const uint32_t nan = mixed ? 0u : 0x7f7f7f7fu;  // in either format
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (tab.row[r / 16] < 0 || r >= tab.there) {
-                w[e] = 0u;
-                continue;
-              }
-              // (0 times what is not finite is NaN)
-              const uint32_t lost = mode & kNotFinite                             ? 0xffffffffu
-                                    : (mode & kZero) || (mixed && v == 1) ? not_finite4<kE5M2>(w[e])
-                                                                          : 0u;
-              if (mode & kZero) w[e] = 0u;
-              if (mode & kNegate) w[e] ^= 0x80808080u;
-              bad |= mixed && lost != 0u;
-              w[e] = (w[e] & ~lost) | (mixed ? 0u : lost & 0x7f7f7f7fu);  // 0, or NaN in either format
+              const uint32_t lost = (not_finite4<kE5M2>(w[e]) & seen) | all;  // (0 times what is not finite is NaN)
+              bad |= lost;
+              w[e] = (((w[e] ^ sign) & kept) & ~lost) | (lost & nan);
             }
             *at = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (bad) ring(tab.slot)->bad = 1;
+          if (mixed && bad) ring(tab.slot)->bad = 1;
         }
         uint8_t* tile = smem + (v ? S::kV : S::kK) + st * S::kTileBytes;
 #pragma unroll 1
