@@ -425,7 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int buf = n_mma & 1;
-        if (!warp_wait(&tfull_bar[buf], (n_mma / 2) & 1)) {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&tfull_bar[buf], (n_mma / 2) & 1)) &&  // (most find it there)
+            !warp_wait(&tfull_bar[buf], (n_mma / 2) & 1)) {
           fail();
           ok = false;
           break;
