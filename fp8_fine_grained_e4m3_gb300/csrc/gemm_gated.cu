@@ -26,7 +26,7 @@
 // the plain product of that size takes 106 (four waves, the last one of 56 tiles: splitting that one along K as
 // a launch of its own won 1 us here and lost 9 in the gradient), the gradient of 8192 rows 149 us where
 // the product takes 107; its epilogue is 10 us a tile.  By latency and the weights' bytes for a few tokens
-// (29 MB in 12.1 us): then all tiles fit in one wave, and each is split along K over a cluster (as in
+// (29 MB in 10.8 us): then all tiles fit in one wave, and each is split along K over a cluster (as in
 // gemm_tc.cu), whose CTAs share the rows of the epilogue.
 #include <cstring>
 
@@ -88,7 +88,7 @@ __device__ __forceinline__ float exp_minus(float x) {
   return r;
 }
 
-// 1 / (1 + e^-g), to a few units in FP32's last place; 0 where e^-g is past FP32's range.
+// 1 / (1 + e^-g), to a few units in FP32's last place; 0 where it is below FP32's normal numbers (g below -87.3).
 __device__ __forceinline__ float sigmoid(float g) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp_minus(g)));

@@ -9,8 +9,9 @@
 // row sees, 128 at a time:
 //   S [128, 128] = Q K^T, P = 2^(S - reference), O [128, dim] += P V
 // both products by tcgen05 on FP16 operands (FP8 codes are exact in FP16; q is shifted by a power
-// of two per row into its range, as BF16 has fewer bits; P has 11).  S and O live in TMEM -- the
-// two tiles' S and O fill its 512 columns -- and P takes the place of S there.
+// of two per row into its range, as BF16 has fewer bits: exact down to 2^-27 of the row's largest
+// element; P has 11).  S and O live in TMEM -- the two tiles' S and O fill its 512 columns -- and P
+// takes the place of S there.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and of tile 1: thread = row = TMEM lane
 //   warps 8-11       keys and values: codes to FP16, into a two-stage ring in shared memory
@@ -27,10 +28,12 @@
 // reference the running maximum of that sum, which is what the terms p v_scale are relative to
 // the largest.  The sum of p itself is formed per block from P / |v_scale|.
 //
-// The reference lags behind the maximum until a P passes 2^15: a first tile sets it so that its largest
-// P is 2^kLift, and O is multiplied up (in TMEM) when later ones have risen by 2^10.  P keeps its
-// 11 bits down to 2^-(14 + kLift) of the largest term and is lost below 2^-(25 + kLift) (131072
-// tokens there are 2^-13 of the sum; the output is BF16).
+// The reference lags behind the maximum: a first tile sets it so that its largest P is 2^kLift, and it rises (O
+// is multiplied in TMEM) when 16 neighbouring P of a tile that all rows see pass 2^15 together, or one P of another
+// tile.  16 such P are 2^kLift together at the least: of that sum, the row's largest, P keeps its 11 bits
+// down to 2^-(14 + kLift) and is lost below 2^-(25 + kLift) (131072 tokens there are 2^-13 of the sum; the
+// output is BF16).  Where a tile that some row does not see whole makes the reference rise half-way, P of its first
+// tokens is multiplied by a power of two in FP32: exact, but for what FP16 then holds with fewer bits.
 //
 // Bound by the softmax and the chain S -> P -> O of a tile: 512 tokens x 32 heads of 128 behind 131077 take
 // 0.88 ms, 1.25 PFLOP/s or 65 % of what cuBLAS reaches; a pair of tiles of rows takes 3400 cycles a tile of

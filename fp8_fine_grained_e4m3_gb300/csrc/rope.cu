@@ -12,10 +12,10 @@
 //
 // Bound by memory: every element is read and written once, 16 bytes a lane.  9700 tokens of 64 + 8
 // BF16 heads of 128 take 61 us, 87 % of what a plain copy reaches; the gradient of 7800 tokens of
-// 32 + 8 such heads, 64 elements of each in neighbouring pairs, 29 us (82 %).  CTAs of 128
+// 32 + 8 such heads, 64 elements of each in neighbouring pairs, 29 us (80 %).  CTAs of 128
 // threads and two tokens, the first loads under way before the position is looked up: CTAs of 256
 // threads and eight tokens took 64 and 32 us, two units in flight a thread 64 and 31 (more registers,
-// fewer threads).  A step of 64 tokens is one chain of latencies, 3.6 us.
+// fewer threads).  A step of 64 tokens is one chain of latencies, 3.5 us.
 #include "common.cuh"
 #include "kv_cache.cuh"
 #include "ptx.cuh"

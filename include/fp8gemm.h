@@ -595,20 +595,25 @@ int fp8_kv_attention(const void* Q, int64_t ld_q, const uint8_t* k_cache, const 
  * 2^31 - 256.
  *
  * Calls of few rows (causal, max_q * group up to 32) are those of fp8_kv_attention but for many
- * short sequences: max_q as small as it is known to be helps.
+ * short sequences: max_q as small as it is known to be helps.  So does a table no wider than the longest
+ * sequence: whether units (256 rows of a cached head of a sequence) are split and joined, or have a CTA each,
+ * depends on host sizes alone.  They are not split where there are no more of them than SMs and
+ * table_width * block is at most 512 (1024 with units for half of the SMs and more): 512 tokens x 64
+ * heads take 19 us so, 25 split.
  *
  * Work is shared out evenly over the SMs whatever the lengths; parts of a sequence's rows are
  * joined through a per-(device, stream) workspace of one size for all calls (fp8_kv_attention's
  * is taken too).  Results are deterministic for given host sizes, lengths and offsets.
  *
- * Arithmetic: products of FP16 operands (codes and queries are exact in it, the queries after a shift
- * of each by a power of two) and FP32 sums.  A key block's scale acts on the product of query and
- * codes.  A softmax weight times its value block's |scale| has FP16's 11 bits down to 2^-19 of the
- * row's largest such term, fewer bits below, and counts as 0 below 2^-30 of it; the weights' sum
- * is exact to FP32 as long as the scales of the blocks that a row sees lie within a factor
- * of 2^64 of each other.  Value scales below 2^-126 count as 0.  An infinity among values or value
- * scales counts as NaN (calls of few rows: as in fp8_kv_attention), and what is not finite reaches the
- * queries that see its token, and no others.
+ * Arithmetic: products of FP16 operands and FP32 sums.  Codes are exact in FP16, and so are queries, after
+ * a shift of each row by a power of two, but for elements below 2^-27 of the row's largest.  A key block's
+ * scale acts on the product of query and codes.  A softmax weight times its value block's |scale| has FP16's 11
+ * bits down to 2^-19 of the row's largest sum of 16 neighbouring such terms, fewer bits below, and counts as 0
+ * below 2^-30 of it; the weights' sum is exact to FP32 as long as the scales of the blocks that a row
+ * sees lie within a factor of 2^64 of each other.  Value scales below 2^-126 count as 0; a block whose scale
+ * counts as 0 stands in all this for one of 2^-60.  What is not finite reaches the queries that see its
+ * token, and no others: as NaN, an infinity among values (under a scale that is neither 0 nor
+ * infinite) as an infinity or NaN; in calls of few rows as in fp8_kv_attention.
  */
 int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, const float* k_scale,
                            const uint8_t* v_cache, const float* v_scale, const int32_t* block_table,
@@ -622,7 +627,8 @@ int fp8_kv_attention_chunk(const void* Q, int64_t ld_q, const uint8_t* k_cache, 
  * projections, the activation, their product and the quantiser of the second half's A.
  *
  *   u = A W1^T (block scales and promotion as fp8gemm_dense; FP32)
- *   h = silu(u[:, :I]) u[:, I:] in FP32;  sQ, Q = fp8_quant_1x128's rule on h (limit of
+ *   h = silu(u[:, :I]) u[:, I:] in FP32 (the sigmoid counts as 0 where it is below 2^-126, for gates
+ *       below -87.3);  sQ, Q = fp8_quant_1x128's rule on h (limit of
  *       q_fmt; zeros where a block's scale underflows to 0).  A NaN in a block makes its scale
  *       NaN.
  *
@@ -642,7 +648,7 @@ int fp8gemm_gated(const uint8_t* A, const float* sA, int a_fmt, const uint8_t* W
  * straight through, from the gradient dY of the block's output y = h W2^T:
  *
  *   dh = dY W2 (block scales and promotion as fp8gemm_dense; FP32)
- *   with g = GU[:, :I], u = GU[:, I:], s = 1 / (1 + exp(-g)), all in FP32:
+ *   with g = GU[:, :I], u = GU[:, I:], s = 1 / (1 + exp(-g)) (as above), all in FP32:
  *   dg = dh u s (1 + g (1 - s)),   du = dh g s
  *   Q, sQ: 1x128 codes and scales of dg and du (rule as above), the A operand of
  *   dX = [dg, du] W1.  Each half begins at a scale block: with Ip = 128 ceil(I/128), columns
