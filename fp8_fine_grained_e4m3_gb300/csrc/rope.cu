@@ -52,12 +52,16 @@ __device__ __forceinline__ bool token_position(const RopeArgs& a, int t, int lan
 
 // Offsets and length of every sequence, whether a token finds it or not: by the warps without a token of the first CTAs.
 constexpr int kFree = kThreads - 32 * kMaxTokens;
-__device__ __forceinline__ void check_sequences(const RopeArgs& a, int* status) {
-  for (long long b = (long long)blockIdx.x * kFree + threadIdx.x - 32 * kMaxTokens; b < a.B; b += (long long)gridDim.x * kFree) {
+__device__ __forceinline__ void check_sequences(const RopeArgs& a, unsigned cta, int* status) {
+  bool bad = false;
+#pragma unroll 1
+  for (long long b = (long long)cta * kFree + threadIdx.x - 32 * kMaxTokens; b < a.B;
+       b += (long long)gridDim.x * gridDim.y * kFree) {
     int t0, n;
-    if (!sequence_tokens(a.cu, int(b), a.B, a.T, a.T, &t0, &n) || a.lens[b] < n)
-      raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
+    const int len = a.lens[b];
+    bad |= !sequence_tokens(a.cu, int(b), a.B, a.T, a.T, &t0, &n) | (len < n);
   }
+  if (bad) raise_status(status, FP8GEMM_ERR_DEVICE_STATUS);
 }
 
 template <class T>
@@ -166,8 +170,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 10 : 8) rope_kernel
       pos[warp] = p;
       has[warp] = ok;
     }
-  } else if (warp >= kMaxTokens && blockIdx.y == 0 && blockIdx.x <= unsigned(a.B) / kFree && !a.positions) {  // meanwhile
-    check_sequences(a, status);
+  } else if (const unsigned cta = blockIdx.y * gridDim.x + blockIdx.x;
+             warp >= kMaxTokens && cta <= unsigned(a.B) / kFree && !a.positions) {  // meanwhile
+    check_sequences(a, cta, status);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_tok * pairs; i += kThreads) {
